@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "fxtx.h"
+#include "host.h"
 #include "kernels.h"
 #include "multi.h"
 #include "plan.h"
@@ -20,6 +21,14 @@ namespace {
 constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::once_flag g_dev_once[kMaxDevices];
+
+// Test hook: FXTX_FAIL_ALLOC=1 makes every workspace allocation fail (host side).
+bool fail_alloc() {
+  const char* s = getenv("FXTX_FAIL_ALLOC");
+  return s && s[0] == '1';
+}
+
+}  // namespace
 
 // Properties of the current device, queried once per device.
 fxtx_status_t current_device(const DeviceInfo** out) {
@@ -52,12 +61,6 @@ bool log_enabled() {
   return on;
 }
 
-// Test hook: FXTX_FAIL_ALLOC=1 makes every workspace allocation fail (host side).
-bool fail_alloc() {
-  const char* s = getenv("FXTX_FAIL_ALLOC");
-  return s && s[0] == '1';
-}
-
 fxtx_status_t alloc_ws(void** p, size_t bytes, cudaStream_t st) {
   *p = nullptr;
   if (bytes == 0) return FXTX_OK;
@@ -69,6 +72,8 @@ fxtx_status_t alloc_ws(void** p, size_t bytes, cudaStream_t st) {
   }
   return FXTX_OK;
 }
+
+namespace {
 
 // Sampled statistics of analysed CSR matrices (fxtx_csr_analyze), keyed by device,
 // structure pointers and sizes. They steer launch parameters only, never results.

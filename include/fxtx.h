@@ -322,6 +322,68 @@ fxtx_status_t fxtx_autotune_candidates(int is_csr, int is_f64, int64_t m, int64_
 fxtx_status_t fxtx_multi_plan_describe(int is_f64, int64_t m, int64_t n, int64_t k, int64_t ld, int v_mode, char* buf,
                                        int64_t cap);
 
+/*
+ * The layer operators: a linear layer with its bias, activation and residual in one
+ * pass, its gradient, and the AdamW step that uses it. Each takes the element type of
+ * its tensors as an argument; sums are held in fp32 and results are rounded once, on
+ * storing. Streams, ownership and errors are those of the entry points above.
+ */
+typedef enum { FXTX_F32 = 0, FXTX_BF16 = 1, FXTX_F16 = 2 } fxtx_type_t;
+
+/* gelu is z Phi(z); gelu_tanh its tanh form, 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))). */
+typedef enum {
+  FXTX_ACT_NONE = 0,
+  FXTX_ACT_RELU = 1,
+  FXTX_ACT_GELU = 2,
+  FXTX_ACT_GELU_TANH = 3,
+  FXTX_ACT_SILU = 4,
+  FXTX_ACT_SIGMOID = 5
+} fxtx_act_t;
+
+/*
+ * One AdamW step over `count` tensors, step number `step` (1 for the first):
+ *
+ *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *
+ * in fp32, each operation rounded on its own; p is rounded to its type on storing.
+ * `tensors` is a HOST array, read before the call returns; its pointers are device
+ * pointers. p, g and copy hold n elements of p_type, g_type and copy_type. copy
+ * (NULL: none) receives the new p before its rounding to p_type, rounded to copy_type: the
+ * working copy of full-precision weights. A tensor with n = 0 is left out.
+ *
+ * state_bits = 32: m and v are fp32 arrays of n elements. state_bits = 8: blocks of
+ * FXTX_ADAMW_BLOCK elements (the last one short) share a scale; m is int8_t codes with
+ * value m_scale c |c|, v is uint8_t codes of its ROOT, v = (v_scale c^2)^2, and m_scale,
+ * v_scale hold ceil(n / FXTX_ADAMW_BLOCK) floats. New codes are rounded to nearest; a
+ * root above zero is held as 1 at least. A block with an infinity or a NaN in it reads
+ * back as NaN. All-zero codes and scales are the initial state.
+ *
+ * Any alignment is taken; 16-byte aligned arrays (8-byte for codes) move in wide
+ * accesses. Tensors must not overlap. The call allocates nothing and launches one kernel
+ * for each 448 tensors. The result is bitwise reproducible.
+ * FXTX_ERR_INVALID_ARG: sizes, step < 1, a beta outside [0, 1), negative or non-finite
+ * lr, eps or weight_decay, a missing pointer, n over 2^39.
+ */
+#define FXTX_ADAMW_BLOCK 256
+typedef struct {
+  int64_t n;
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+} fxtx_adamw_tensor_t;
+fxtx_status_t fxtx_adamw(int64_t count, const fxtx_adamw_tensor_t* tensors, fxtx_type_t p_type, fxtx_type_t g_type,
+                         fxtx_type_t copy_type, int state_bits, int64_t step, double lr, double beta1, double beta2,
+                         double eps, double weight_decay, void* stream);
+
+/* The fp32 moments that n elements of 8-bit states stand for, from the start of a block. */
+fxtx_status_t fxtx_adamw_moments(int64_t n, const int8_t* m, const float* m_scale, const uint8_t* v,
+                                 const float* v_scale, float* m_out, float* v_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
