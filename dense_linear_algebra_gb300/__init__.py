@@ -11,12 +11,13 @@ Raw C-ABI calls (pointers as ints, stream as a cudaStream_t int) carry the C nam
 ``fxtx_dense_multi_f32``, ``fxtx_dense_multi_f64``, ``fxtx_csr_f32``, ``fxtx_csr_f64``,
 ``fxtx_csr_validate``, ``fxtx_csr_analyze``, ``fxtx_csr_analysis_clear``,
 ``fxtx_csr_plan_describe_host``, ``fxtx_epilogue_f32``, ``fxtx_epilogue_f64``, ``fxtx_device_error``,
-``fxtx_status_string``, ``fxtx_adamw``, ``fxtx_adamw_moments``,
+``fxtx_status_string``, ``fxtx_linear``, ``fxtx_linear_grad``, ``fxtx_adamw``, ``fxtx_adamw_moments``,
 ``fxtx_plan_describe``, ``fxtx_multi_plan_describe`` and the ``fxtx_autotune_*`` calls. ``dense``, ``dense_multi`` and
 ``csr`` take torch CUDA tensors; ``epilogue`` applies alpha * w + beta * z. The module
 ``distributed`` runs one call across ranks, each holding a block of X's rows.
 
-The layer operators train and serve a model of more than one layer: ``AdamW`` updates a list of tensors in one launch,
+The layer operators train and serve a model of more than one layer: ``linear`` is act(X W + b) + residual in one pass,
+``linear_grad`` its gradient, and ``AdamW`` updates a list of tensors in one launch,
 with its states in 32 bits or in 8.
 """
 from ._lib import (  # noqa: F401
@@ -70,6 +71,8 @@ from ._lib import (  # noqa: F401
     fxtx_device_error,
     fxtx_epilogue_f32,
     fxtx_epilogue_f64,
+    fxtx_linear,
+    fxtx_linear_grad,
     fxtx_multi_plan_describe,
     fxtx_plan_describe,
     fxtx_status_string,
@@ -81,7 +84,7 @@ from ._lib import (  # noqa: F401
 
 def __getattr__(name):
     """The layer operators need torch at import; the raw calls above do not."""
-    if name in ("AdamW",):
+    if name in ("AdamW", "linear", "linear_grad"):
         from . import layers
 
         return getattr(layers, name)

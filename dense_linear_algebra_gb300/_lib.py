@@ -57,6 +57,9 @@ def _load() -> ctypes.CDLL:
                                                 ctypes.c_char_p, i64]
     lib.fxtx_epilogue_f32.argtypes = [i64, vp, f32, f32, vp, vp, vp]
     lib.fxtx_epilogue_f64.argtypes = [i64, vp, f64, f64, vp, vp, vp]
+    lib.fxtx_linear.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, i32, vp, i64, vp, i64, vp, i64, vp]
+    lib.fxtx_linear_grad.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64,
+                                     vp, vp]
     lib.fxtx_adamw.argtypes = [i64, vp, i32, i32, i32, i32, i64, f64, f64, f64, f64, f64, vp]
     lib.fxtx_adamw_moments.argtypes = [i64, vp, vp, vp, vp, vp, vp, vp]
     lib.fxtx_device_error.argtypes = [vp]
@@ -75,7 +78,7 @@ def _load() -> ctypes.CDLL:
     for name in ("fxtx_dense_f32", "fxtx_dense_f64", "fxtx_dense_f32_noalloc", "fxtx_dense_bf16", "fxtx_dense_multi_f32",
                  "fxtx_dense_multi_f64", "fxtx_csr_f32", "fxtx_csr_f64", "fxtx_csr_validate", "fxtx_device_error",
                  "fxtx_epilogue_f32", "fxtx_epilogue_f64", "fxtx_csr_analyze", "fxtx_csr_analysis_clear",
-                 "fxtx_csr_plan_describe_host", "fxtx_adamw", "fxtx_adamw_moments",
+                 "fxtx_csr_plan_describe_host", "fxtx_linear", "fxtx_linear_grad", "fxtx_adamw", "fxtx_adamw_moments",
                  "fxtx_plan_describe", "fxtx_multi_plan_describe", "fxtx_autotune_set", "fxtx_autotune_get",
                  "fxtx_autotune_clear", "fxtx_autotune_save", "fxtx_autotune_load", "fxtx_autotune_candidates"):
         getattr(lib, name).restype = i32
@@ -99,6 +102,8 @@ fxtx_csr_analysis_clear = _lib.fxtx_csr_analysis_clear
 fxtx_csr_plan_describe_host = _lib.fxtx_csr_plan_describe_host
 fxtx_epilogue_f32 = _lib.fxtx_epilogue_f32
 fxtx_epilogue_f64 = _lib.fxtx_epilogue_f64
+fxtx_linear = _lib.fxtx_linear
+fxtx_linear_grad = _lib.fxtx_linear_grad
 fxtx_adamw = _lib.fxtx_adamw
 fxtx_adamw_moments = _lib.fxtx_adamw_moments
 fxtx_device_error = _lib.fxtx_device_error

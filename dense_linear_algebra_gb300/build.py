@@ -18,8 +18,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfusedxtx.so")
 SOURCES = ["api.cu", "dense.cu", "csr.cu", "multi.cu", "multi_tc.cu", "split.cu", "plan.cpp", "tmap.cpp",
-           "tune.cpp", "noalloc.cu", "layers_api.cu", "adamw.cu"]
-HEADERS = ["common.cuh", "host.h", "kernels.h", "layers.h", "multi.h", "plan.h", "tmap.h", "tune.h"]
+           "tune.cpp", "noalloc.cu", "layers_api.cu", "adamw.cu",
+           "linear.cu", "slope.cu"]
+HEADERS = ["act.cuh", "common.cuh", "host.h", "kernels.h", "layers.h", "linear.h", "multi.h", "plan.h", "tmap.h", "tune.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

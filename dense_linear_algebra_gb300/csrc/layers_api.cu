@@ -4,6 +4,7 @@
 
 #include "host.h"
 #include "layers.h"
+#include "linear.h"
 
 using namespace fxtx;
 
@@ -15,9 +16,106 @@ fxtx_status_t status_of(cudaError_t e) {
   return FXTX_ERR_CUDA;
 }
 
+// A matrix argument with `rows` rows of `cols` entries: its pitch, and its pointer where it has entries.
+bool rows_ok(const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return ld >= cols && (p != nullptr || rows == 0 || cols == 0);
+}
+
+// Sizes the kernels index: every matrix within 2^46 entries, each size within 2^31.
+bool sizes_ok(int64_t m, int64_t n, int64_t k) {
+  const int64_t top = (int64_t)1 << 31;
+  return m >= 0 && n >= 0 && k >= 0 && m < top && n < top && k < top;
+}
+
 }  // namespace
 
 extern "C" {
+
+fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                          int64_t ldw, int w_trans, const void* b, fxtx_act_t act, const void* R, int64_t ldr, void* Z,
+                          int64_t ldz, void* OUT, int64_t ldo, void* stream) {
+  if (!type_ok(type) || !act_ok(act) || !sizes_ok(m, n, k) || (w_trans != 0 && w_trans != 1)) return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(X, m, n, ldx) || !rows_ok(W, w_trans ? k : n, w_trans ? n : k, ldw) || !rows_ok(OUT, m, k, ldo))
+    return FXTX_ERR_INVALID_ARG;
+  if ((R != nullptr && ldr < k) || (Z != nullptr && ldz < k)) return FXTX_ERR_INVALID_ARG;
+  if (m == 0 || k == 0) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  Product p;
+  p.type = type;
+  p.M = m; p.N = k; p.K = n;
+  p.A.p = X; p.A.ld = ldx;
+  p.B.p = W; p.B.ld = ldw; p.B.mn_major = !w_trans;
+  p.e.bias = b; p.e.act = act;
+  p.e.R = R; p.e.ldr = ldr;
+  p.e.Z = Z; p.e.ldz = ldz;
+  p.e.out = OUT; p.e.ldo = ldo;
+  return run_product(p, *dev, static_cast<cudaStream_t>(stream));
+}
+
+fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* G, int64_t ldg,
+                               const void* X, int64_t ldx, const void* W, int64_t ldw, int w_trans, const void* Z,
+                               int64_t ldz, fxtx_act_t act, void* DX, int64_t lddx, void* DW, int64_t lddw, void* DB,
+                               void* stream) {
+  if (!type_ok(type) || !act_ok(act) || !sizes_ok(m, n, k) || (w_trans != 0 && w_trans != 1)) return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(G, m, k, ldg)) return FXTX_ERR_INVALID_ARG;
+  if (act != FXTX_ACT_NONE && !rows_ok(Z, m, k, ldz)) return FXTX_ERR_INVALID_ARG;
+  if (DX && (!rows_ok(W, w_trans ? k : n, w_trans ? n : k, ldw) || lddx < n)) return FXTX_ERR_INVALID_ARG;
+  if (DW && (!rows_ok(X, m, n, ldx) || lddw < (w_trans ? n : k))) return FXTX_ERR_INVALID_ARG;
+  if ((n == 0 || (!DX && !DW)) && (!DB || k == 0)) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  const bool products = n > 0 && (DX || DW) && m > 0 && k > 0;
+  SlopeArgs a;
+  a.type = type;
+  a.m = m; a.k = k;
+  a.G = G; a.ldg = ldg;
+  a.Z = Z; a.ldz = ldz;
+  a.act = act;
+  a.db = k > 0 ? DB : nullptr;
+  void* ws = nullptr;
+  const size_t d_bytes = products && act != FXTX_ACT_NONE ? ((size_t)m * k * type_size(type) + 255) / 256 * 256 : 0;
+  const size_t sum_bytes = a.db ? slope_ws_bytes(m, k, dev->sm_count) : 0;
+  s = alloc_ws(&ws, d_bytes + sum_bytes, st);
+  if (s != FXTX_OK) return s;
+  a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + d_bytes);
+  if (d_bytes) {
+    a.D = ws;
+    a.ldd = k;
+  }
+  if (a.D || a.db) s = status_of(launch_slope(a, dev->sm_count, st));
+
+  Operand D;
+  D.p = a.D ? a.D : G;
+  D.ld = a.D ? a.ldd : ldg;
+  if (s == FXTX_OK && DX && m > 0 && n > 0) {
+    Product p;
+    p.type = type;
+    p.M = m; p.N = n; p.K = k;
+    p.A = D;
+    p.B.p = W; p.B.ld = ldw; p.B.mn_major = w_trans;
+    p.e.out = DX; p.e.ldo = lddx;
+    s = run_product(p, *dev, st);
+  }
+  if (s == FXTX_OK && DW && n > 0 && k > 0) {
+    Operand x;
+    x.p = X; x.ld = ldx; x.mn_major = true;
+    D.mn_major = true;
+    Product p;
+    p.type = type;
+    p.M = w_trans ? k : n; p.N = w_trans ? n : k; p.K = m;
+    p.A = w_trans ? D : x;
+    p.B = w_trans ? x : D;
+    p.e.out = DW; p.e.ldo = lddw;
+    s = run_product(p, *dev, st);
+  }
+  if (ws) cudaFreeAsync(ws, st);
+  return s;
+}
 
 fxtx_status_t fxtx_adamw(int64_t count, const fxtx_adamw_tensor_t* tensors, fxtx_type_t p_type, fxtx_type_t g_type,
                          fxtx_type_t copy_type, int state_bits, int64_t step, double lr, double beta1, double beta2,

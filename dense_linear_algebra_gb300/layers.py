@@ -1,5 +1,6 @@
-"""Layer operators on CUDA tensors: the AdamW step (``AdamW``) over the C entries ``fxtx_adamw`` and
-``fxtx_adamw_moments``. The package only marshals arguments: every step runs in the kernels of ``libfusedxtx.so``.
+"""Layer operators on CUDA tensors: the fused linear layer (``linear``), its gradient (``linear_grad``) and the AdamW
+step (``AdamW``), over the C entries ``fxtx_linear``, ``fxtx_linear_grad``, ``fxtx_adamw`` and ``fxtx_adamw_moments``.
+The package only marshals arguments: every step runs in the kernels of ``libfusedxtx.so``.
 """
 from __future__ import annotations
 
@@ -19,6 +20,122 @@ def _type(t, name):
     if code is None:
         raise TypeError(f"{name}: unsupported dtype {t.dtype} (float32, bfloat16 or float16)")
     return code
+
+
+# fxtx_act_t
+ACTS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
+
+
+def _act(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act: expected one of {[a for a in ACTS if a]} or None, got {act!r}")
+    return code
+
+
+def _matrix(t, dtype, m, n, name, index):
+    """The row pitch of a row-major (m, n) CUDA tensor."""
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
+        raise ValueError(f"{name}: expected a {dtype} matrix on cuda:{index}")
+    if t.shape[0] != m or t.shape[1] != n:
+        raise ValueError(f"{name}: expected shape {(m, n)}, got {tuple(t.shape)}")
+    ld, unit = t.stride()
+    if m <= 1:
+        ld = n
+    if (unit != 1 and n > 1) or ld < n:
+        raise ValueError(f"{name}: expected a row-major tensor with unit column stride")
+    return ld
+
+
+def _weights(W, dtype, n, index):
+    """W (n, k): its columns' count, its pitch and whether it is stored by its columns."""
+    if W.dtype is not dtype or W.get_device() != index or W.dim() != 2:
+        raise ValueError(f"W: expected a {dtype} matrix on cuda:{index}")
+    k = W.shape[1]
+    if W.shape[0] != n:
+        raise ValueError(f"W: expected {n} rows, got {W.shape[0]}")
+    s0, s1 = W.stride()
+    if (s1 == 1 or k <= 1) and (s0 >= k or n <= 1):
+        return k, s0 if n > 1 else k, 0
+    if (s0 == 1 or n <= 1) and (s1 >= n or k <= 1):
+        return k, s1 if k > 1 else n, 1
+    raise ValueError("W: expected unit stride along its rows or its columns")
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that writes it (the current one unless `stream` is given)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=None):
+    """act(X W + b) + residual in one pass: X (m, n), W (n, k), b (k), residual and the result (m, k).
+
+    All tensors have one dtype (bfloat16, float16 or float32); sums are fp32 and rounded once. ``W`` may be a
+    row-major (n, k) tensor or the transposed view of a row-major (k, n) one; the others are row-major, column slices
+    of wider matrices included. ``act``: None, "relu", "gelu", "gelu_tanh", "silu" or "sigmoid". ``pre=True`` also
+    returns Z = X W + b for ``linear_grad`` (or give the (m, k) tensor to keep it in). ``out`` may be ``residual``.
+    Runs on the current stream, or on ``stream``, which then owns the new tensors.
+    """
+    if not X.is_cuda or X.dim() != 2:
+        raise ValueError("X: expected a 2-D CUDA tensor")
+    dt, di = X.dtype, X.get_device()
+    code = _type(X, "X")
+    m, n = X.shape
+    ldx = _matrix(X, dt, m, n, "X", di)
+    k, ldw, trans = _weights(W, dt, n, di)
+    if b is not None:
+        _lib._vec(b, dt, k, "b", di)
+    ldr = 0 if residual is None else _matrix(residual, dt, m, k, "residual", di)
+    keep = None if pre is False or pre is None else (_empty((m, k), dt, X.device, stream) if pre is True else pre)
+    ldz = 0 if keep is None else _matrix(keep, dt, m, k, "pre", di)
+    if out is None:
+        out, ldo = _empty((m, k), dt, X.device, stream), k
+    else:
+        ldo = _matrix(out, dt, m, k, "out", di)
+    with _on(di):
+        rc = _lib.fxtx_linear(code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans,
+                              None if b is None else b.data_ptr(), _act(act),
+                              None if residual is None else residual.data_ptr(), ldr,
+                              None if keep is None else keep.data_ptr(), ldz, out.data_ptr(), ldo,
+                              _stream(stream, X.device))
+    _check(rc, "fxtx_linear")
+    return out if keep is None else (out, keep)
+
+
+def linear_grad(G, X, W, pre=None, act=None, need=(True, True, True), stream=None):
+    """The gradient of ``linear``: with D = G * act'(pre), (dX, dW, db) = (D W^T, X^T D, the column sums of D).
+
+    ``G`` (m, k) is the gradient at the result (and the gradient at the residual), ``pre`` the Z that ``linear`` kept
+    (not needed without an activation). ``need`` says which of the three are computed; the others come back as None.
+    dW is stored as W is. Types, layouts and streams are those of ``linear``.
+    """
+    if not X.is_cuda or X.dim() != 2:
+        raise ValueError("X: expected a 2-D CUDA tensor")
+    dt, di = X.dtype, X.get_device()
+    code, kind = _type(X, "X"), _act(act)
+    m, n = X.shape
+    ldx = _matrix(X, dt, m, n, "X", di)
+    k, ldw, trans = _weights(W, dt, n, di)
+    ldg = _matrix(G, dt, m, k, "G", di)
+    if kind and pre is None:
+        raise ValueError("pre: the gradient of an activation needs the Z that linear kept")
+    ldz = 0 if not kind else _matrix(pre, dt, m, k, "pre", di)
+    dX = _empty((m, n), dt, X.device, stream) if need[0] else None
+    dW = _empty((k, n) if trans else (n, k), dt, X.device, stream) if need[1] else None
+    db = _empty((k,), dt, X.device, stream) if need[2] else None
+    with _on(di):
+        rc = _lib.fxtx_linear_grad(code, m, n, k, G.data_ptr(), ldg, X.data_ptr(), ldx, W.data_ptr(), ldw, trans,
+                                   pre.data_ptr() if kind else None, ldz, kind,
+                                   None if dX is None else dX.data_ptr(), n,
+                                   None if dW is None else dW.data_ptr(), n if trans else k,
+                                   None if db is None else db.data_ptr(), _stream(stream, X.device))
+    _check(rc, "fxtx_linear_grad")
+    return dX, dW.t() if dW is not None and trans else dW, db
 
 
 class AdamW:

@@ -341,6 +341,43 @@ typedef enum {
 } fxtx_act_t;
 
 /*
+ * A linear layer: OUT = act(Z) + R,  Z = X W + b.
+ *
+ * X is m x n (rows, features), W n x k, b a k-vector or NULL, R (the residual) m x k or
+ * NULL, OUT m x k, all of `type` and row-major: entry (i, j) of X at X[i * ldx + j]. With
+ * w_trans = 1 W is stored by its columns: entry (j, c) at W[c * ldw + j], ldw >= n; with 0
+ * at W[j * ldw + c], ldw >= k. Z (NULL: not kept) receives the pre-activations, rounded to
+ * `type`, as fxtx_linear_grad takes them. n = 0 gives Z = b; m = 0 or k = 0 does nothing.
+ *
+ * OUT may equal R with ldo == ldr (in place); other overlaps of OUT or Z with anything
+ * else are undefined. Any alignment and pitch is taken.
+ *
+ * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32. The result is
+ * bitwise reproducible. FXTX_ERR_INVALID_ARG: an unknown type or activation, a size that is
+ * negative or not below 2^31, a pitch below its row, a missing pointer.
+ */
+fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                          int64_t ldw, int w_trans, const void* b, fxtx_act_t act, const void* R, int64_t ldr, void* Z,
+                          int64_t ldz, void* OUT, int64_t ldo, void* stream);
+
+/*
+ * The gradient of fxtx_linear. G (m x k) is the gradient at OUT; with D = G * act'(Z):
+ *
+ *     DX = D W^T (m x n)      DW = X^T D (n x k)      DB = the column sums of D (k)
+ *
+ * and the gradient at R is G itself. Each of DX, DW, DB may be NULL (not computed; W is
+ * read only for DX, X only for DW). DW is stored as W is (w_trans, pitch lddw). Z is
+ * what fxtx_linear kept, and not read when act is FXTX_ACT_NONE. The slope of relu is
+ * 0 at z <= 0. D is rounded to `type` before the products; DB is summed from the
+ * unrounded values. m = 0 gives DW = 0 and DB = 0. Outputs must not overlap anything
+ * else. Types, layouts, precision and errors are those of fxtx_linear.
+ */
+fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* G, int64_t ldg,
+                               const void* X, int64_t ldx, const void* W, int64_t ldw, int w_trans, const void* Z,
+                               int64_t ldz, fxtx_act_t act, void* DX, int64_t lddx, void* DW, int64_t lddw, void* DB,
+                               void* stream);
+
+/*
  * One AdamW step over `count` tensors, step number `step` (1 for the first):
  *
  *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
