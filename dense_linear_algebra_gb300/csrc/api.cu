@@ -11,6 +11,7 @@
 #include "fxtx.h"
 #include "host.h"
 #include "kernels.h"
+#include "linear.h"
 #include "multi.h"
 #include "plan.h"
 #include "tune.h"
@@ -582,11 +583,12 @@ fxtx_status_t fxtx_device_error(void* stream) {
   const int a = take_dense_device_error();
   const int b = take_csr_device_error();
   const int c = take_multi_device_error();
-  if (a < 0 || b < 0 || c < 0) {
+  const int d = take_product_device_error();
+  if (a < 0 || b < 0 || c < 0 || d < 0) {
     cudaGetLastError();
     return FXTX_ERR_CUDA;
   }
-  return (a || b || c) ? FXTX_ERR_TIMEOUT : FXTX_OK;
+  return (a || b || c || d) ? FXTX_ERR_TIMEOUT : FXTX_OK;
 }
 
 const char* fxtx_status_string(fxtx_status_t status) {

@@ -78,20 +78,25 @@ fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k
   a.act = act;
   a.db = k > 0 ? DB : nullptr;
   void* ws = nullptr;
-  const size_t d_bytes = products && act != FXTX_ACT_NONE ? ((size_t)m * k * type_size(type) + 255) / 256 * 256 : 0;
+  // D is G itself where there is nothing to multiply and the products can read G where it lies
+  const bool as_is = act == FXTX_ACT_NONE && type != FXTX_F32 && ((uintptr_t)G & 15u) == 0 && ldg % 8 == 0;
+  const int64_t pitch = (k + 7) / 8 * 8, planes = type == FXTX_F32 ? 3 : 1;
+  const size_t d_bytes = products && !as_is ? ((size_t)planes * m * pitch * 2 + 255) / 256 * 256 : 0;
   const size_t sum_bytes = a.db ? slope_ws_bytes(m, k, dev->sm_count) : 0;
   s = alloc_ws(&ws, d_bytes + sum_bytes, st);
   if (s != FXTX_OK) return s;
   a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + d_bytes);
   if (d_bytes) {
     a.D = ws;
-    a.ldd = k;
+    a.ldd = pitch;
+    a.d_planes = m * pitch;
   }
   if (a.D || a.db) s = status_of(launch_slope(a, dev->sm_count, st));
 
   Operand D;
   D.p = a.D ? a.D : G;
   D.ld = a.D ? a.ldd : ldg;
+  D.plane_stride = a.D && type == FXTX_F32 ? a.d_planes : 0;
   if (s == FXTX_OK && DX && m > 0 && n > 0) {
     Product p;
     p.type = type;

@@ -1,124 +1,149 @@
 // linear.cu — the product behind the linear layer and its gradient,
-//     C_ij = sum_kk A(i, kk) B(j, kk),   out = act(C + bias_j) + R_ij,
-// on the CUDA cores: 64 x 64 tiles, 4 x 4 entries a thread, operands staged in shared memory
-// 16 of kk at a time, fp32 sums. Long sums are split over the grid's third dimension into
-// fp32 partials of at most 4,096 terms that a second kernel adds in order.
+//     C_ij = sum_kk A(i, kk) B(j, kk),   out = act(C + bias_j) + R_ij:
+// its operands brought into the form that the tensor copies read, and its layout over the
+// tensor cores (plan_product).
 #include <algorithm>
-#include <type_traits>
+#include <cmath>
 
-#include "act.cuh"
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
 #include "linear.h"
+#include "product.cuh"
 
 namespace fxtx {
 namespace {
 
-constexpr int TM = 64, TK = 16;
-
+// A sum of no terms: out = act(bias_j) + R_ij.
 template <typename T>
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t i, int64_t j, float c) {
-  if (e.bias) c += to_f32(static_cast<const T*>(e.bias)[j]);
-  if (e.Z) static_cast<T*>(e.Z)[i * e.ldz + j] = from_f32<T>(c);
-  with_act(e.act, [&](auto act) { c = act_of<decltype(act)::value>(c); });
-  if (e.R) c += to_f32(static_cast<const T*>(e.R)[i * e.ldr + j]);
-  static_cast<T*>(e.out)[i * e.ldo + j] = from_f32<T>(c);
+__global__ void __launch_bounds__(256) empty_sum_kernel(const Epilogue e, int64_t rows, int64_t cols) {
+  const Finish<T> fin(e, rows, cols);
+  const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
+  const float zero[16] = {};
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride)
+    fin.row16(x / groups, x % groups * 16, zero);
 }
 
-template <typename T>
-__device__ __forceinline__ void stage(float (*s)[TM + 1], const Operand& o, int64_t i0, int64_t rows, int64_t k0,
-                                      int64_t k1) {
-  for (int e = threadIdx.x; e < TM * TK; e += 256) {
-    const int i = o.mn_major ? e % TM : e / TK, kk = o.mn_major ? e / TM : e % TK;
-    const int64_t r = i0 + i, c = k0 + kk;
-    float x = 0.f;
-    if (r < rows && c < k1) x = to_f32(static_cast<const T*>(o.p)[o.mn_major ? c * o.ld + r : r * o.ld + c]);
-    s[kk][i] = x;
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) product_kernel(const Product p, const int64_t per_split, float* part) {
-  __shared__ float as[TK][TM + 1], bs[TK][TM + 1];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t i0 = (int64_t)blockIdx.x * TM, j0 = (int64_t)blockIdx.y * TM;
-  const int64_t k0 = (int64_t)blockIdx.z * per_split, k1 = min(p.K, k0 + per_split);
-  float c[4][4] = {};
-  for (int64_t k = k0; k < k1; k += TK) {
-    stage<T>(as, p.A, i0, p.M, k, k1);
-    stage<T>(bs, p.B, j0, p.N, k, k1);
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < TK; ++kk) {
-      float x[4], y[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        x[q] = as[kk][ty + 16 * q];
-        y[q] = bs[kk][tx + 16 * q];
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) c[u][v] = fmaf(x[u], y[v], c[u][v]);
-    }
-    __syncthreads();
-  }
-  for (int u = 0; u < 4; ++u)
-    for (int v = 0; v < 4; ++v) {
-      const int64_t i = i0 + ty + 16 * u, j = j0 + tx + 16 * v;
-      if (i >= p.M || j >= p.N) continue;
-      if (part) part[((int64_t)blockIdx.z * p.M + i) * p.N + j] = c[u][v];
-      else finish<T>(p.e, i, j, c[u][v]);
-    }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t M, int64_t N, int splits, const float* part) {
-  const int64_t stride = (int64_t)gridDim.x * 256;
-  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < M * N; x += stride) {
-    float c = 0.f;
-    for (int s = 0; s < splits; ++s) c += part[(int64_t)s * M * N + x];
-    finish<T>(e, x / N, x % N, c);
-  }
-}
-
-template <typename T>
-fxtx_status_t run_t(const Product& p, const DeviceInfo& dev, cudaStream_t st) {
-  const int64_t tm = (p.M + TM - 1) / TM, tn = (p.N + TM - 1) / TM;
-  if (tn > 65535) return FXTX_ERR_UNSUPPORTED;
-  int64_t splits = 1;
-  if (p.K > 4096) splits = std::max<int64_t>(1, std::min<int64_t>((p.K + 4095) / 4096, (int64_t)dev.sm_count * 8 / (tm * tn)));
-  int64_t per = ((p.K + splits - 1) / splits + TK - 1) / TK * TK;
-  splits = p.K > 0 ? (p.K + per - 1) / per : 1;
-  float* part = nullptr;
-  if (splits > 1) {
-    const fxtx_status_t s = alloc_ws(reinterpret_cast<void**>(&part), (size_t)splits * p.M * p.N * 4, st);
-    if (s != FXTX_OK) return s;
-  }
-  product_kernel<T><<<dim3((unsigned)tm, (unsigned)tn, (unsigned)splits), 256, 0, st>>>(p, per, part);
-  cudaError_t e = cudaGetLastError();
-  if (part) {
-    if (e == cudaSuccess) {
-      const int64_t blocks = std::min<int64_t>((p.M * p.N + 255) / 256, (int64_t)dev.sm_count * 8);
-      join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(p.e, p.M, p.N, (int)splits, part);
-      e = cudaGetLastError();
-    }
-    cudaFreeAsync(part, st);
-  }
+fxtx_status_t status_of(cudaError_t e) {
   if (e == cudaSuccess) return FXTX_OK;
   cudaGetLastError();
   return FXTX_ERR_CUDA;
 }
 
+// Whether the tensor copies can read a 16-bit operand where it lies.
+bool copyable(const Operand& o) { return ((uintptr_t)o.p & 15u) == 0 && o.ld % 8 == 0; }
+
+// The operand's planes (rows x cols in memory), where they will lie in `at` if it has to be packed.
+Planes planes_of(const Operand& o, fxtx_type_t type, int64_t mn, int64_t k, char* at, size_t* bytes) {
+  Planes x;
+  x.rows = o.mn_major ? k : mn;
+  x.cols = o.mn_major ? mn : k;
+  x.mn_major = o.mn_major;
+  x.planes = type == FXTX_F32 ? 3 : 1;
+  *bytes = 0;
+  if (o.plane_stride > 0 || (type != FXTX_F32 && copyable(o))) {
+    x.p = o.p;
+    x.pitch = o.ld;
+    x.plane_stride = o.plane_stride > 0 ? o.plane_stride : x.rows * x.pitch;
+  } else {
+    x.p = at;
+    x.pitch = (x.cols + 7) / 8 * 8;
+    x.plane_stride = x.rows * x.pitch;
+    *bytes = ((size_t)x.planes * x.plane_stride * 2 + 255) / 256 * 256;
+  }
+  return x;
+}
+
+fxtx_status_t pack(const Operand& o, fxtx_type_t type, const Planes& x, const DeviceInfo& dev, cudaStream_t st) {
+  PackArgs a;
+  a.type = type;
+  a.src = o.p;
+  a.rows = x.rows;
+  a.cols = x.cols;
+  a.ld = o.ld;
+  a.dst = const_cast<void*>(x.p);
+  a.pitch = x.pitch;
+  a.plane_stride = x.plane_stride;
+  return status_of(launch_pack(a, dev.sm_count, st));
+}
+
+template <typename T>
+fxtx_status_t run_empty(const Product& p, const DeviceInfo& dev, cudaStream_t st) {
+  const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 15) / 16) + 255) / 256, (int64_t)dev.sm_count * 8);
+  empty_sum_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(p.e, p.M, p.N);
+  return status_of(cudaGetLastError());
+}
+
 }  // namespace
 
+// The layout with the least estimated time. Cycles of a stage (64 of kk): its products (an
+// M = 128, K = 16 product holds the pipe for 64 cycles up to N = 128), or its bytes at an SM's
+// share of L2; a CTA's pieces of work one after the other, and a fixed cost for filling the pipeline and for
+// the last epilogue; partial sums written and read once more.
+TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count) {
+  const int64_t kb = std::max<int64_t>(1, (K + 63) / 64);
+  TcPlan best;
+  double best_t = 1e300;
+  auto consider = [&](bool swap, int cg, int bn) {
+    const int64_t L = swap ? N : M, Cn = swap ? M : N;
+    if ((swap ? a_mn : b_mn) && bn / cg < 64) return;  // an MN-major box is 64 wide
+    const int64_t tiles = ((L + 128 * cg - 1) / (128 * cg)) * ((Cn + bn - 1) / bn), units = sm_count / cg;
+    const double mma = 4.0 * (planes == 3 ? 6 : 1) * std::max(64.0, bn / 2.0);
+    const double bytes = planes * (16384.0 + bn / cg * 128.0);
+    const double stage = std::max(mma, bytes / 40.0);
+    for (int64_t s = 1; s <= std::min<int64_t>(kb, 4 * units); s = s < 8 ? s + 1 : s + s / 4) {
+      const int64_t per = (kb + s - 1) / s, waves = (tiles * s + units - 1) / units;
+      double t = waves * (per * stage + 400.0) + 2500.0 + 6.0 * bn;
+      if (s > 1) t += 5000.0 + (double)s * M * N * 8.0 / 2500.0;
+      if (t < best_t) {
+        best_t = t;
+        best.swap = swap;
+        best.cg = cg;
+        best.bn = bn;
+        best.splits = (int)s;
+      }
+    }
+  };
+  if (M <= 128)
+    for (int bn : {16, 32, 64, 128})
+      if (bn >= M || bn == 128) consider(true, 1, bn);
+  consider(false, 1, 64);
+  consider(false, 1, 128);
+  if (planes == 1) consider(false, 2, 256);
+  return best;
+}
+
 fxtx_status_t run_product(const Product& p, const DeviceInfo& dev, cudaStream_t st) {
-  switch (p.type) {
-    case FXTX_F32: return run_t<float>(p, dev, st);
-    case FXTX_BF16: return run_t<__nv_bfloat16>(p, dev, st);
-    default: return run_t<__half>(p, dev, st);
+  if (p.K == 0) {
+    switch (p.type) {
+      case FXTX_F32: return run_empty<float>(p, dev, st);
+      case FXTX_BF16: return run_empty<__nv_bfloat16>(p, dev, st);
+      default: return run_empty<__half>(p, dev, st);
+    }
   }
+  PlanesProduct q;
+  q.M = p.M;
+  q.N = p.N;
+  q.K = p.K;
+  q.e = p.e;
+  size_t ab = 0, bb = 0;
+  planes_of(p.A, p.type, p.M, p.K, nullptr, &ab);
+  planes_of(p.B, p.type, p.N, p.K, nullptr, &bb);
+  char* ws = nullptr;
+  fxtx_status_t s = alloc_ws(reinterpret_cast<void**>(&ws), ab + bb, st);
+  if (s != FXTX_OK) return s;
+  size_t used = 0;
+  q.A = planes_of(p.A, p.type, p.M, p.K, ws, &used);
+  q.B = planes_of(p.B, p.type, p.N, p.K, ws + ab, &used);
+  if (ab) s = pack(p.A, p.type, q.A, dev, st);
+  if (s == FXTX_OK && bb) s = pack(p.B, p.type, q.B, dev, st);
+  if (s == FXTX_OK) switch (p.type) {
+      case FXTX_F32: s = run_planes<float>(q, dev, st); break;
+      case FXTX_BF16: s = run_planes<__nv_bfloat16>(q, dev, st); break;
+      default: s = run_planes<__half>(q, dev, st); break;
+    }
+  if (ws) cudaFreeAsync(ws, st);
+  return s;
 }
 
 }  // namespace fxtx

@@ -9,11 +9,13 @@
 namespace fxtx {
 
 // A matrix operand of a product over an index kk: entry (i, kk) at p[i * ld + kk], or with
-// mn_major at p[kk * ld + i].
+// mn_major at p[kk * ld + i]. plane_stride > 0: not float32 entries but their three bfloat16
+// planes, plane_stride elements apart, 16-byte aligned.
 struct Operand {
   const void* p = nullptr;
   int64_t ld = 0;
   bool mn_major = false;
+  int64_t plane_stride = 0;
 };
 
 // What is done with a product's entry (i, j) before it is stored: out = act(acc + bias_j) + R_ij,
@@ -38,7 +40,45 @@ struct Product {
 };
 fxtx_status_t run_product(const Product& p, const DeviceInfo& dev, cudaStream_t st);
 
-// D = G * act'(Z) and its column sums. D is written with row pitch ldd unless it is NULL; db unless it is NULL.
+// A 16-bit operand as the tensor copies read it: `planes` matrices of rows x cols in memory,
+// `pitch` elements from row to row and `plane_stride` from plane to plane, 16-byte aligned.
+// mn_major: the rows run over kk (entry (i, kk) at row kk, column i), else over i.
+struct Planes {
+  const void* p = nullptr;
+  int64_t rows = 0, cols = 0, pitch = 0, plane_stride = 0;
+  int planes = 1;
+  bool mn_major = false;
+};
+
+// The same product from planes: one of bfloat16 or float16, three bfloat16 ones of a float32 operand.
+struct PlanesProduct {
+  int64_t M = 0, N = 0, K = 0;
+  Planes A, B;
+  Epilogue e;
+};
+template <typename T>
+fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStream_t st);
+int take_product_device_error();
+
+// How a product is laid over the tensor cores.
+struct TcPlan {
+  bool swap = false;  // tiles of 128 columns x bn rows of the result instead of 128 cg rows x bn columns
+  int cg = 1, bn = 128, splits = 1;
+};
+TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count);
+
+// A copy of a matrix with an aligned pitch: 16-bit as it is, float32 as three bfloat16 planes.
+struct PackArgs {
+  fxtx_type_t type = FXTX_F32;
+  const void* src = nullptr;
+  int64_t rows = 0, cols = 0, ld = 0;
+  void* dst = nullptr;
+  int64_t pitch = 0, plane_stride = 0;
+};
+cudaError_t launch_pack(const PackArgs& a, int sm_count, cudaStream_t st);
+
+// D = G * act'(Z) and its column sums. D is written with row pitch ldd unless it is NULL (of
+// float32 as three bfloat16 planes, d_planes elements apart); db unless it is NULL.
 struct SlopeArgs {
   fxtx_type_t type = FXTX_F32;
   int64_t m = 0, k = 0;
@@ -48,7 +88,7 @@ struct SlopeArgs {
   int64_t ldz = 0;
   int act = FXTX_ACT_NONE;
   void* D = nullptr;
-  int64_t ldd = 0;
+  int64_t ldd = 0, d_planes = 0;
   void* db = nullptr;
   float* ws = nullptr;  // slope_ws_bytes
 };

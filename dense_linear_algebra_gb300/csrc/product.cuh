@@ -1,0 +1,128 @@
+// product.cuh — the epilogue of a product's entries: out = act(c + bias_j) + R_ij, c + bias_j to Z.
+#pragma once
+
+#include <type_traits>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "linear.h"
+
+namespace fxtx {
+
+template <typename T>
+struct Finish {
+  const Epilogue e;
+  const int64_t rows, cols;
+  bool wide_out, wide_z, wide_r, wide_b;
+
+  __device__ static bool wide(const void* p, int64_t ld) {
+    return p != nullptr && ((uintptr_t)p & 15u) == 0 && (ld * (int64_t)sizeof(T)) % 16 == 0;
+  }
+  __device__ Finish(const Epilogue& ep, int64_t m, int64_t n) : e(ep), rows(m), cols(n) {
+    wide_out = wide(e.out, e.ldo);
+    wide_z = wide(e.Z, e.ldz);
+    wide_r = wide(e.R, e.ldr);
+    wide_b = wide(e.bias, 0);
+  }
+
+  __device__ __forceinline__ static void load16(const T* p, int n, bool w, float* x) {
+    if (w && n == 16) {
+      uint4 v[sizeof(T)];
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+      const T* t = reinterpret_cast<const T*>(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = to_f32(t[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ static void store16(T* p, int n, bool w, const float* x) {
+    if (w && n == 16) {
+      uint4 v[sizeof(T)];
+      T* t = reinterpret_cast<T*>(v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) t[i] = from_f32<T>(x[i]);
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) p[i] = from_f32<T>(x[i]);
+    }
+  }
+
+  // 16 entries of row i from column j on.
+  __device__ __forceinline__ void row16(int64_t i, int64_t j, const float* acc) const {
+    if (i >= rows || j >= cols) return;
+    const int n = cols - j >= 16 ? 16 : (int)(cols - j);
+    float c[16], x[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) c[q] = acc[q];
+    if (e.bias) {
+      load16(static_cast<const T*>(e.bias) + j, n, wide_b, x);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) c[q] += x[q];
+    }
+    if (e.Z) store16(static_cast<T*>(e.Z) + i * e.ldz + j, n, wide_z, c);
+    with_act(e.act, [&](auto act) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) c[q] = act_of<decltype(act)::value>(c[q]);
+    });
+    if (e.R) {
+      load16(static_cast<const T*>(e.R) + i * e.ldr + j, n, wide_r, x);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) c[q] += x[q];
+    }
+    store16(static_cast<T*>(e.out) + i * e.ldo + j, n, wide_out, c);
+  }
+
+  // 16 entries of column j from row i on: the warp's lanes hold neighbouring columns.
+  __device__ __forceinline__ void column16(int64_t j, int64_t i, const float* acc) const {
+    if (j >= cols) return;
+    const float b = e.bias ? to_f32(static_cast<const T*>(e.bias)[j]) : 0.f;
+    float c[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) c[q] = acc[q] + b;
+    if (e.Z) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (i + q < rows) static_cast<T*>(e.Z)[(i + q) * e.ldz + j] = from_f32<T>(c[q]);
+    }
+    with_act(e.act, [&](auto act) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) c[q] = act_of<decltype(act)::value>(c[q]);
+    });
+    if (e.R) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (i + q < rows) c[q] += to_f32(static_cast<const T*>(e.R)[(i + q) * e.ldr + j]);
+    }
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      if (i + q < rows) static_cast<T*>(e.out)[(i + q) * e.ldo + j] = from_f32<T>(c[q]);
+  }
+};
+
+// The same entries as partial sums.
+__device__ __forceinline__ void part_row(float* part, int64_t rows, int64_t cols, int64_t i, int64_t j, const float* c) {
+  if (i >= rows) return;
+  float* p = part + i * cols + j;
+  if (cols % 4 == 0 && j + 16 <= cols) {
+#pragma unroll
+    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(p + q) = make_float4(c[q], c[q + 1], c[q + 2], c[q + 3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      if (j + q < cols) p[q] = c[q];
+  }
+}
+__device__ __forceinline__ void part_column(float* part, int64_t rows, int64_t cols, int64_t j, int64_t i, const float* c) {
+  if (j >= cols) return;
+#pragma unroll
+  for (int q = 0; q < 16; ++q)
+    if (i + q < rows) part[(i + q) * cols + j] = c[q];
+}
+
+}  // namespace fxtx

@@ -1,0 +1,412 @@
+// product_tc.cu — the products of the linear layer and its gradient on the tensor cores:
+//     C_ij = sum_kk A(i, kk) B(j, kk),   out = act(C + bias_j) + R_ij.
+//
+// One persistent CTA a SM, or a pair of CTAs over two SMs (CG = 2), takes tiles of
+// 128 CG x BN entries of C in turn. Roles, linked by mbarriers only:
+//   warp 0      one lane: tensor copies of A and B, 64 of kk a stage, 128-byte swizzle;
+//   warp 1      the products (tcgen05.mma, K = 16), one elected lane issuing; in a pair the
+//               first CTA issues for both, each holding its 128 rows of A and half of B;
+//   warps 4-11  the epilogue: a tile's sums from tensor memory (lane = row of the tile),
+//               two warps a quarter of the lanes, each half of the columns.
+// Sums live in two tensor-memory accumulators, so that the epilogue of one tile overlaps the
+// products of the next.
+//
+// Operands may be K-major (kk contiguous) or MN-major: the box of a tensor copy, the descriptor
+// and the instruction's major bits change, nothing is transposed. Rows, columns and kk beyond
+// the matrices read as zero.
+//
+// SWAP: the tile's lanes run over the result's columns and its columns over the result's rows,
+// for results of few rows: a tile is then 128 columns x BN rows, and the weights are read once
+// with no row of the tile wasted.
+//
+// float32 (PL = 3): each operand comes as three bfloat16 planes (x = hi + mid + lo, exactly),
+// and the six products of planes whose order is within 2^-18 of the first are summed; the rest
+// is at most 2^-26 of a term. The tensor cores' sums are taken out every 256 of kk and added in
+// fp32 registers, rounded to nearest, so that a long sum's error does not grow with its length.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+#include "linear.h"
+#include "product.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+namespace fxtx {
+namespace {
+
+constexpr int BK = 64;                 // kk a stage
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 32 * (4 + EPI_WARPS);
+constexpr int A_BYTES = 128 * BK * 2;  // one plane of A in a stage
+constexpr int CHUNK = 4;               // stages a sum stays in tensor memory (float32)
+
+template <int CG, int BN, int PL>
+struct Cfg {
+  static constexpr int BROWS = BN / CG;  // B's entries a CTA holds
+  static constexpr int B_BYTES = BROWS * BK * 2;
+  static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
+  static constexpr int S = std::min(8, 208 * 1024 / STAGE);
+  static constexpr size_t BYTES = (size_t)S * STAGE + 1024;
+  static constexpr int TMEM_COLS = std::max(32, 2 * BN);
+  static constexpr int COLS = BN / 2 >= 16 ? BN / 2 : 16;  // columns an epilogue thread takes
+  static_assert(S >= 2 && BYTES <= 227 * 1024 && TMEM_COLS <= 512, "shared and tensor memory");
+};
+
+struct TcArgs {
+  int64_t rows = 0, cols = 0;   // the result's
+  int tiles_l = 0, tiles_c = 0;  // tiles along the lanes (A) and the columns (B) of a tile
+  int kblocks = 0, splits = 1, per_split = 0;
+  bool a_mn = false, b_mn = false;
+  uint32_t idesc = 0;
+  Epilogue e;
+  float* part = nullptr;  // [splits][rows][cols] when splits > 1
+};
+
+// Tile `t`'s place: 8 tiles along the lanes at a time, then along the columns, so that the
+// tiles in flight share their operands in L2.
+__device__ __forceinline__ void place(int t, int tl, int tc, int& l, int& c) {
+  const int group = 8 * tc, g = t / group, first = g * 8, size = min(8, tl - first), r = t - g * group;
+  l = first + r % size;
+  c = r / size;
+}
+
+template <typename T, int CG, int BN, int PL, bool SWAP>
+__global__ void __launch_bounds__(THREADS, 1)
+    product_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                      const __grid_constant__ TcArgs a) {
+  using C = Cfg<CG, BN, PL>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  volatile int* abort_word = &s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < C::S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], EPI_WARPS * CG);
+    }
+    mbar_init(&fin_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc<CG>(&s_tmem, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  const int tiles = a.tiles_l * a.tiles_c, work = tiles * a.splits;
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  // the stages of kk a piece of work covers
+  auto range = [&](int w, int& k0, int& k1) {
+    const int s = w % a.splits;
+    k0 = s * a.per_split;
+    k1 = min(a.kblocks, k0 + a.per_split);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int w = first; w < work && ok; w += step) {
+        int l, c, k0, k1;
+        place(w / a.splits, a.tiles_l, a.tiles_c, l, c);
+        range(w, k0, k1);
+        const int ar = l * 128 * CG + (int)rank * 128, br = c * BN + (int)rank * C::BROWS;
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const int s = it % C::S;
+          if (it >= C::S && !(ok = tc_wait(&empty[s], (uint32_t)((it / C::S - 1) & 1), abort_word))) break;
+          // a pair's copies all complete on its first CTA's barrier
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(CG * C::STAGE));
+          const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_addr(&full[s]);
+          unsigned char* st = smem + (size_t)s * C::STAGE;
+#pragma unroll
+          for (int p = 0; p < PL; ++p) {
+            unsigned char* d = st + p * A_BYTES;
+            if (a.a_mn) {
+              tma_load_3d<CG>(d, &amap, ar, kb * BK, p, bar);
+              tma_load_3d<CG>(d + BK * 128, &amap, ar + 64, kb * BK, p, bar);
+            } else {
+              tma_load_3d<CG>(d, &amap, kb * BK, ar, p, bar);
+            }
+            d = st + PL * A_BYTES + p * C::B_BYTES;
+            if (a.b_mn) {
+#pragma unroll
+              for (int x = 0; x < C::BROWS / 64; ++x)
+                tma_load_3d<CG>(d + x * BK * 128, &bmap, br + 64 * x, kb * BK, p, bar);
+            } else {
+              tma_load_3d<CG>(d, &bmap, kb * BK, br, p, bar);
+            }
+          }
+        }
+      }
+      // copies still in flight after an abort land before the CTA leaves
+      if (!ok && rank == 0)
+        for (int j = it > C::S ? it - C::S : 0; j < it; ++j) mbar_wait_bounded(&full[j % C::S], (uint32_t)((j / C::S) & 1));
+    }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const bool leader = elect_one();
+      const uint64_t ad0 = swizzled_desc(smem_addr(smem), BK * 128, 1024);
+      const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * A_BYTES), BK * 128, 1024);
+      // K = 16 further: 32 bytes along a K-major row, 16 rows of an MN-major operand (16-byte units)
+      const uint64_t as = a.a_mn ? 128 : 2, bs = a.b_mn ? 128 : 2;
+      int it = 0, acc = 0;
+      bool ok = true;
+      for (int w = first; w < work && ok; w += step) {
+        int k0, k1;
+        range(w, k0, k1);
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const bool fresh = PL == 3 ? (kb - k0) % CHUNK == 0 : kb == k0;
+          const bool last = kb == k1 - 1 || (PL == 3 && (kb - k0) % CHUNK == CHUNK - 1);
+          if (fresh && acc >= 2 && !(ok = warp_wait(&tempty[acc & 1], (uint32_t)(((acc >> 1) - 1) & 1), abort_word))) break;
+          const int s = it % C::S;
+          if (!(ok = warp_wait(&full[s], (uint32_t)((it / C::S) & 1), abort_word))) break;
+          tc_fence_after();
+          if (leader) {
+            const uint32_t d = tmem + (uint32_t)((acc & 1) * BN);
+            const uint64_t ad = ad0 + (uint64_t)(s * (C::STAGE >> 4)), bd = bd0 + (uint64_t)(s * (C::STAGE >> 4));
+            if constexpr (PL == 1) {
+#pragma unroll
+              for (int q = 0; q < BK / 16; ++q)
+                mma_f16<CG>(d, ad + q * as, bd + q * bs, a.idesc, !fresh || q > 0);
+            } else {
+              // the planes' products, the smallest first
+              constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+              for (int x = 0; x < 6; ++x)
+#pragma unroll
+                for (int q = 0; q < BK / 16; ++q)
+                  mma_f16<CG>(d, ad + PA[x] * (A_BYTES >> 4) + q * as, bd + PB[x] * (C::B_BYTES >> 4) + q * bs, a.idesc,
+                              !fresh || x > 0 || q > 0);
+            }
+            mma_commit<CG>(&empty[s]);
+            if (last) mma_commit<CG>(&tfull[acc & 1]);
+          }
+          __syncwarp();
+          if (last) ++acc;
+        }
+      }
+      // every product has completed before the CTA leaves, after an abort too
+      if (leader) mma_commit<CG>(&fin_bar);
+      __syncwarp();
+      mbar_wait_bounded(&fin_bar, 0);
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t te0 = CG == 2 ? cluster_addr(&tempty[0], 0) : smem_addr(&tempty[0]);
+    const Finish<T> fin(a.e, a.rows, a.cols);
+    int acc = 0;
+    bool ok = true;
+    for (int w = first; w < work && ok; w += step) {
+      int l, c, k0, k1;
+      place(w / a.splits, a.tiles_l, a.tiles_c, l, c);
+      range(w, k0, k1);
+      const int64_t li = (int64_t)l * 128 * CG + rank * 128 + 32 * q + lane;  // the lane's row (column) of the result
+      const int64_t ci = (int64_t)c * BN + half * C::COLS;                   // its first column (row)
+      const bool mine = half * C::COLS < BN;
+      float* part = a.splits > 1 ? a.part + (int64_t)(w % a.splits) * a.rows * a.cols : nullptr;
+      auto store = [&](int64_t col, const float* x) {
+        if constexpr (SWAP) {
+          if (part) part_column(part, a.rows, a.cols, li, col, x);
+          else fin.column16(li, col, x);
+        } else {
+          if (part) part_row(part, a.rows, a.cols, li, col, x);
+          else fin.row16(li, col, x);
+        }
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(te0 + (uint32_t)((acc & 1) * 8));
+        ++acc;
+      };
+      if constexpr (PL == 1) {
+        if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
+        tc_fence_after();
+        if (mine) {
+          const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN + half * C::COLS);
+#pragma unroll 1
+          for (int x = 0; x < C::COLS; x += 16) {
+            float r[16];
+            tc_load16(t + (uint32_t)x, r);
+            tc_wait_ld();
+            store(ci + x, r);
+          }
+        }
+        release();
+      } else {
+        float sum[C::COLS];
+#pragma unroll
+        for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
+        for (int kb = k0; kb < k1; kb += CHUNK) {
+          if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
+          tc_fence_after();
+          if (mine) {
+            const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN + half * C::COLS);
+#pragma unroll
+            for (int x = 0; x < C::COLS; x += 16) {
+              float r[16];
+              tc_load16(t + (uint32_t)x, r);
+              tc_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[x + i] += r[i];
+            }
+          }
+          release();
+        }
+        if (!ok) break;
+        if (mine) {
+#pragma unroll
+          for (int x = 0; x < C::COLS; x += 16) store(ci + x, sum + x);
+        }
+      }
+    }
+  }
+
+  // tensor memory is released, and a pair's shared memory given up, when all roles are done
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) {
+    // the pair's second CTA receives the first one's commits too: the last of them has landed
+    if (rank == 1 && warp == 1) mbar_wait_bounded(&fin_bar, 0);
+    __syncthreads();
+    cluster_sync();
+  }
+  tc_fence_after();
+  if (warp == 2) tmem_free<CG>(tmem, C::TMEM_COLS);
+}
+
+// out = the epilogue of the splits' sums, added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t rows, int64_t cols, int splits,
+                                                   const float* part) {
+  const Finish<T> fin(e, rows, cols);
+  const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride) {
+    const int64_t i = x / groups, j = x % groups * 16;
+    float c[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) c[q] = 0.f;
+    for (int s = 0; s < splits; ++s) {
+      const float* p = part + ((int64_t)s * rows + i) * cols + j;
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        if (j + q < cols) c[q] += p[q];
+    }
+    fin.row16(i, j, c);
+  }
+}
+
+template <typename T, int CG, int BN, int PL, bool SWAP>
+cudaError_t launch(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, int sm_count, cudaStream_t st) {
+  using C = Cfg<CG, BN, PL>;
+  const void* k = (const void*)product_tc_kernel<T, CG, BN, PL, SWAP>;
+  cudaError_t e = ensure_smem(k, C::BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t work = (int64_t)a.tiles_l * a.tiles_c * a.splits;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(work, sm_count / CG) * CG));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  if (CG > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, product_tc_kernel<T, CG, BN, PL, SWAP>, am, bm, a);
+}
+
+// The map of an operand for boxes of 128 bytes x its tile's rows (or BK of them, MN-major).
+bool operand_map(CUtensorMap* map, const Planes& o, bool bf16, int box_rows) {
+  return encode_planes_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, o.p, o.planes,
+                           o.rows, o.cols, o.pitch * 2, o.plane_stride * 2, o.mn_major ? BK : box_rows);
+}
+
+}  // namespace
+
+int take_product_device_error() { return take_device_error(); }
+
+template <typename T>
+fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr bool F32 = std::is_same<T, float>::value;
+  constexpr int PL = F32 ? 3 : 1;
+  const bool bf16 = !std::is_same<T, __half>::value;
+  const TcPlan plan = plan_product(p.M, p.N, p.K, PL, p.A.mn_major, p.B.mn_major, dev.sm_count);
+  const Planes &A = plan.swap ? p.B : p.A, &B = plan.swap ? p.A : p.B;
+  TcArgs a;
+  a.rows = p.M;
+  a.cols = p.N;
+  const int64_t L = plan.swap ? p.N : p.M, Cn = plan.swap ? p.M : p.N;
+  a.tiles_l = (int)((L + 128 * plan.cg - 1) / (128 * plan.cg));
+  a.tiles_c = (int)((Cn + plan.bn - 1) / plan.bn);
+  a.kblocks = (int)((p.K + BK - 1) / BK);
+  a.per_split = (a.kblocks + plan.splits - 1) / plan.splits;
+  a.splits = (a.kblocks + a.per_split - 1) / a.per_split;  // none of them empty
+  a.a_mn = A.mn_major;
+  a.b_mn = B.mn_major;
+  a.idesc = mma_desc(bf16, A.mn_major, B.mn_major, 128 * plan.cg, plan.bn);
+  a.e = p.e;
+  CUtensorMap am, bm;
+  memset(&am, 0, sizeof am);
+  memset(&bm, 0, sizeof bm);
+  if (!operand_map(&am, A, bf16, 128) || !operand_map(&bm, B, bf16, plan.bn / plan.cg)) return FXTX_ERR_CUDA;
+  if (a.splits > 1) {
+    const fxtx_status_t s = alloc_ws(reinterpret_cast<void**>(&a.part), (size_t)a.splits * p.M * p.N * 4, st);
+    if (s != FXTX_OK) return s;
+  }
+  cudaError_t e = cudaErrorInvalidConfiguration;
+  if (plan.swap) {
+    switch (plan.bn) {
+      case 16: e = launch<T, 1, 16, PL, true>(am, bm, a, dev.sm_count, st); break;
+      case 32: e = launch<T, 1, 32, PL, true>(am, bm, a, dev.sm_count, st); break;
+      case 64: e = launch<T, 1, 64, PL, true>(am, bm, a, dev.sm_count, st); break;
+      case 128: e = launch<T, 1, 128, PL, true>(am, bm, a, dev.sm_count, st); break;
+    }
+  } else if (plan.cg == 2) {
+    if constexpr (!F32) e = launch<T, 2, 256, PL, false>(am, bm, a, dev.sm_count, st);
+  } else {
+    switch (plan.bn) {
+      case 64: e = launch<T, 1, 64, PL, false>(am, bm, a, dev.sm_count, st); break;
+      case 128: e = launch<T, 1, 128, PL, false>(am, bm, a, dev.sm_count, st); break;
+    }
+  }
+  if (a.part) {
+    if (e == cudaSuccess) {
+      const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 15) / 16) + 255) / 256, (int64_t)dev.sm_count * 8);
+      join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(a.e, p.M, p.N, a.splits, a.part);
+      e = cudaGetLastError();
+    }
+    cudaFreeAsync(a.part, st);
+  }
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+template fxtx_status_t run_planes<float>(const PlanesProduct&, const DeviceInfo&, cudaStream_t);
+template fxtx_status_t run_planes<__nv_bfloat16>(const PlanesProduct&, const DeviceInfo&, cudaStream_t);
+template fxtx_status_t run_planes<__half>(const PlanesProduct&, const DeviceInfo&, cudaStream_t);
+
+}  // namespace fxtx

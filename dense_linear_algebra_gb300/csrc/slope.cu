@@ -5,7 +5,8 @@
 // CTA 256 / CX rows at a time of CX such column groups; each CTA's column sums go to a
 // workspace and a second kernel adds them in order, so db is the same on every call. D is
 // rounded to the layer's type (the products that follow take it as an operand); db is summed
-// from the unrounded values.
+// from the unrounded values. Of float32, D is written as the three bfloat16 planes that the
+// products take. The same stores serve a plain copy into an aligned pitch (launch_pack).
 #include <algorithm>
 #include <type_traits>
 
@@ -35,23 +36,30 @@ __device__ __forceinline__ void load8(const T* p, int n, bool wide, float* x) {
   }
 }
 
+// 8 values as T, or of float32 as their three bfloat16 planes.
 template <typename T>
-__device__ __forceinline__ void store8(T* p, int n, bool wide, const float* x) {
-  if (wide) {
-    if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-    } else {
-      uint4 a;
-      T* e = reinterpret_cast<T*>(&a);
+__device__ __forceinline__ void store8(void* dst, int64_t at, int64_t plane_stride, int n, bool wide, const float* x) {
+  using S = typename std::conditional<sizeof(T) == 4, __nv_bfloat16, T>::type;
+  float r[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = from_f32<T>(x[i]);
-      *reinterpret_cast<uint4*>(p) = a;
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int plane = 0; plane < (sizeof(T) == 4 ? 3 : 1); ++plane) {
+    S* p = static_cast<S*>(dst) + plane * plane_stride + at;
+    uint4 a;
+    S* e = reinterpret_cast<S*>(&a);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = from_f32<S>(r[i]);
+      if constexpr (sizeof(T) == 4) r[i] -= to_f32(e[i]);  // exact
     }
-  } else {
+    if (wide) {
+      *reinterpret_cast<uint4*>(p) = a;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = from_f32<T>(x[i]);
+      for (int i = 0; i < 8; ++i)
+        if (i < n) p[i] = e[i];
+    }
   }
 }
 
@@ -68,9 +76,8 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, const int
   const int n = a.k - col >= 8 ? 8 : (a.k > col ? (int)(a.k - col) : 0);
   const bool wg = n == 8 && rows_aligned(a.G, a.ldg, sizeof(T));
   const bool wz = n == 8 && rows_aligned(a.Z, a.ldz, sizeof(T));
-  const bool wd = n == 8 && rows_aligned(a.D, a.ldd, sizeof(T));
+  const bool wd = n == 8 && rows_aligned(a.D, a.ldd, 2) && a.d_planes % 8 == 0;
   const T *G = static_cast<const T*>(a.G) + col, *Z = static_cast<const T*>(a.Z) + col;
-  T* D = static_cast<T*>(a.D) + col;
   float sum[8] = {};
   if (n > 0)
     with_act(a.act, [&](auto act) {
@@ -84,7 +91,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, const int
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] *= slope_of<ACT>(z[i]);
         }
-        if (a.D != nullptr) store8(D + r * a.ldd, n, wd, g);
+        if (a.D != nullptr) store8<T>(a.D, r * a.ldd + col, a.d_planes, n, wd, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[i] += g[i];
       }
@@ -117,6 +124,19 @@ __global__ void __launch_bounds__(256) sums_kernel(const float* ws, int64_t part
   if (y == 0 && j < k) {
     for (int i = 1; i < 8; ++i) s += part[i][x];
     db[j] = from_f32<T>(s);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
+  const int64_t groups = (a.cols + 7) / 8, stride = (int64_t)gridDim.x * 256;
+  const bool aligned = rows_aligned(a.src, a.ld, sizeof(T));
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < a.rows * groups; x += stride) {
+    const int64_t i = x / groups, j = x % groups * 8;
+    const int n = a.cols - j >= 8 ? 8 : (int)(a.cols - j);
+    float v[8];
+    load8(static_cast<const T*>(a.src) + i * a.ld + j, n, aligned && n == 8, v);
+    store8<T>(a.dst, i * a.pitch + j, a.plane_stride, n, n == 8, v);
   }
 }
 
@@ -154,6 +174,17 @@ cudaError_t launch_t(const SlopeArgs& a, int sm_count, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_pack(const PackArgs& a, int sm_count, cudaStream_t st) {
+  const int64_t blocks = std::min<int64_t>((a.rows * ((a.cols + 7) / 8) + 255) / 256, (int64_t)sm_count * 16);
+  if (blocks == 0) return cudaSuccess;
+  switch (a.type) {
+    case FXTX_F32: pack_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(a); break;
+    case FXTX_BF16: pack_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(a); break;
+    default: pack_kernel<__half><<<(unsigned)blocks, 256, 0, st>>>(a); break;
+  }
+  return cudaGetLastError();
+}
 
 size_t slope_ws_bytes(int64_t m, int64_t k, int sm_count) {
   return (size_t)slope_grid(m, k, sm_count).gy * (size_t)k * 4;

@@ -47,4 +47,17 @@ bool encode_rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* bas
   return r == CUDA_SUCCESS;
 }
 
+bool encode_planes_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int planes, int64_t rows,
+                       int64_t cols, int64_t pitch_bytes, int64_t plane_bytes, int box_rows) {
+  EncodeFn fn = encode_fn();
+  if (!fn || box_rows < 1 || box_rows > 256) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)pitch_bytes, (cuuint64_t)plane_bytes};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace fxtx

@@ -1,4 +1,4 @@
-// tmap.h — 2-D tensor maps of row-major matrices for the tensor copies
+// tmap.h — tensor maps of row-major matrices for the tensor copies
 // (cp.async.bulk.tensor), encoded by the driver's cuTensorMapEncodeTiled, which is
 // fetched once through the runtime (no link against libcuda).
 #pragma once
@@ -15,5 +15,10 @@ namespace fxtx {
 // False if the driver entry point is missing or refuses the arguments.
 bool encode_rows_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
                      int64_t pitch_bytes, int elem, int box_rows, int box_bytes, int swizzle);
+
+// Map of `planes` such matrices of 16-bit elements, plane_bytes apart, read in boxes of
+// box_rows x 128 bytes of one plane with the 128-byte swizzle.
+bool encode_planes_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int planes, int64_t rows,
+                       int64_t cols, int64_t pitch_bytes, int64_t plane_bytes, int box_rows);
 
 }  // namespace fxtx
