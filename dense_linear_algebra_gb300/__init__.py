@@ -87,5 +87,6 @@ def __getattr__(name):
     if name in ("AdamW", "linear", "linear_grad"):
         from . import layers
 
-        return getattr(layers, name)
+        value = globals()[name] = getattr(layers, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -74,6 +74,35 @@ fxtx_status_t alloc_ws(void** p, size_t bytes, cudaStream_t st) {
   return FXTX_OK;
 }
 
+fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st) {
+  static cudaMemPool_t pools[kMaxDevices];
+  static std::once_flag once[kMaxDevices];
+  *p = nullptr;
+  if (bytes == 0) return FXTX_OK;
+  if (fail_alloc()) return FXTX_ERR_ALLOC;
+  int d = -1;
+  if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
+    cudaGetLastError();
+    return FXTX_ERR_ALLOC;
+  }
+  std::call_once(once[d], [d] {
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = d;
+    uint64_t keep = 256u << 20;
+    if (cudaMemPoolCreate(&pools[d], &props) != cudaSuccess) pools[d] = nullptr;
+    else cudaMemPoolSetAttribute(pools[d], cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaGetLastError();
+  });
+  if (!pools[d] || cudaMallocFromPoolAsync(p, bytes, pools[d], st) != cudaSuccess) {
+    cudaGetLastError();
+    *p = nullptr;
+    return FXTX_ERR_ALLOC;
+  }
+  return FXTX_OK;
+}
+
 namespace {
 
 // Sampled statistics of analysed CSR matrices (fxtx_csr_analyze), keyed by device,

@@ -83,7 +83,7 @@ fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k
   const int64_t pitch = (k + 7) / 8 * 8, planes = type == FXTX_F32 ? 3 : 1;
   const size_t d_bytes = products && !as_is ? ((size_t)planes * m * pitch * 2 + 255) / 256 * 256 : 0;
   const size_t sum_bytes = a.db ? slope_ws_bytes(m, k, dev->sm_count) : 0;
-  s = alloc_ws(&ws, d_bytes + sum_bytes, st);
+  s = alloc_pooled(&ws, d_bytes + sum_bytes, st);
   if (s != FXTX_OK) return s;
   a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + d_bytes);
   if (d_bytes) {

@@ -21,7 +21,7 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(const Epilogue e, int64_
   const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
   const float zero[16] = {};
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride)
-    fin.row16(x / groups, x % groups * 16, zero);
+    fin.template row<16>(x / groups, x % groups * 16, zero);
 }
 
 fxtx_status_t status_of(cudaError_t e) {
@@ -76,40 +76,53 @@ fxtx_status_t run_empty(const Product& p, const DeviceInfo& dev, cudaStream_t st
 
 }  // namespace
 
-// The layout with the least estimated time. Cycles of a stage (64 of kk): its products (an
-// M = 128, K = 16 product holds the pipe for 64 cycles up to N = 128), or its bytes at an SM's
-// share of L2; a CTA's pieces of work one after the other, and a fixed cost for filling the pipeline and for
-// the last epilogue; partial sums written and read once more.
+// The layout with the least estimated time, in cycles. A stage (64 of kk) takes its products (an
+// M = 128, K = 16 product holds the pipe for 64 cycles up to N = 128) or its bytes at an SM's
+// share of L2; the stages that the busiest SM gets follow one another, and no layout beats the
+// operands' stream from HBM. On top come a fixed cost for filling the pipeline, and the
+// exchange of partial sums: between the CTAs of a cluster, or through memory and a second kernel.
 TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count) {
   const int64_t kb = std::max<int64_t>(1, (K + 63) / 64);
   TcPlan best;
   double best_t = 1e300;
-  auto consider = [&](bool swap, int cg, int bn) {
+  const double floor = planes * 2.0 * K * (double)(M + N) / 3400.0;
+  auto consider = [&](bool swap, bool cluster, int cg, int bn) {
     const int64_t L = swap ? N : M, Cn = swap ? M : N;
     if ((swap ? a_mn : b_mn) && bn / cg < 64) return;  // an MN-major box is 64 wide
     const int64_t tiles = ((L + 128 * cg - 1) / (128 * cg)) * ((Cn + bn - 1) / bn), units = sm_count / cg;
     const double mma = 4.0 * (planes == 3 ? 6 : 1) * std::max(64.0, bn / 2.0);
     const double bytes = planes * (16384.0 + bn / cg * 128.0);
     const double stage = std::max(mma, bytes / 40.0);
-    for (int64_t s = 1; s <= std::min<int64_t>(kb, 4 * units); s = s < 8 ? s + 1 : s + s / 4) {
-      const int64_t per = (kb + s - 1) / s, waves = (tiles * s + units - 1) / units;
-      double t = waves * (per * stage + 400.0) + 2500.0 + 6.0 * bn;
-      if (s > 1) t += 5000.0 + (double)s * M * N * 8.0 / 2500.0;
+    auto price = [&](int64_t s) {
+      const int64_t per = (kb + s - 1) / s;
+      if (cluster && (s - 1) * per >= kb) return;  // a CTA without work
+      const int64_t waves = (tiles * s + units - 1) / units;
+      double t = std::max(floor, waves * (per * stage + 400.0)) + 2500.0 + 6.0 * bn;
+      if (cluster) t += (s > 1 ? 1000.0 : 0.0) + (waves - 1) * 1500.0;
+      else if (s > 1) t += 5000.0 + (double)s * M * N * 8.0 / 2500.0;
       if (t < best_t) {
         best_t = t;
         best.swap = swap;
+        best.cluster = cluster;
         best.cg = cg;
         best.bn = bn;
         best.splits = (int)s;
       }
-    }
+    };
+    if (cluster)
+      for (int s = 1; s <= 8; s *= 2) price(s);
+    else
+      for (int64_t s = 1; s <= std::min<int64_t>(kb, 4 * units); s = s < 8 ? s + 1 : s + s / 4) price(s);
   };
-  if (M <= 128)
+  const int top = planes == 3 ? 64 : 128;  // the widest tile of the split kernel
+  if (M <= top)
     for (int bn : {16, 32, 64, 128})
-      if (bn >= M || bn == 128) consider(true, 1, bn);
-  consider(false, 1, 64);
-  consider(false, 1, 128);
-  if (planes == 1) consider(false, 2, 256);
+      if (bn >= M && bn <= top) consider(true, true, 1, bn);
+  consider(false, true, 1, 64);
+  if (planes == 1) consider(false, true, 1, 128);
+  consider(false, false, 1, 64);
+  consider(false, false, 1, 128);
+  if (planes == 1) consider(false, false, 2, 256);
   return best;
 }
 
@@ -130,7 +143,7 @@ fxtx_status_t run_product(const Product& p, const DeviceInfo& dev, cudaStream_t 
   planes_of(p.A, p.type, p.M, p.K, nullptr, &ab);
   planes_of(p.B, p.type, p.N, p.K, nullptr, &bb);
   char* ws = nullptr;
-  fxtx_status_t s = alloc_ws(reinterpret_cast<void**>(&ws), ab + bb, st);
+  fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), ab + bb, st);
   if (s != FXTX_OK) return s;
   size_t used = 0;
   q.A = planes_of(p.A, p.type, p.M, p.K, ws, &used);

@@ -63,6 +63,7 @@ int take_product_device_error();
 // How a product is laid over the tensor cores.
 struct TcPlan {
   bool swap = false;  // tiles of 128 columns x bn rows of the result instead of 128 cg rows x bn columns
+  bool cluster = false;  // one tile a cluster of `splits` CTAs (a power of two up to 8), each taking a part of kk
   int cg = 1, bn = 128, splits = 1;
 };
 TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count);

@@ -25,83 +25,65 @@ struct Finish {
     wide_b = wide(e.bias, 0);
   }
 
-  __device__ __forceinline__ static void load16(const T* p, int n, bool w, float* x) {
-    if (w && n == 16) {
-      uint4 v[sizeof(T)];
+  // NV entries in accesses of 16 bytes, or of 8 (NV = 4 of a 16-bit type).
+  template <int NV>
+  using Word = typename std::conditional<NV * sizeof(T) % 16 == 0, uint4, uint2>::type;
+  template <int NV>
+  __device__ __forceinline__ static void load(const T* p, int n, bool w, float* x) {
+    if (w && n == NV) {
+      constexpr int V = NV * sizeof(T) / sizeof(Word<NV>);
+      Word<NV> v[V];
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+      for (int i = 0; i < V; ++i) v[i] = reinterpret_cast<const Word<NV>*>(p)[i];
       const T* t = reinterpret_cast<const T*>(v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = to_f32(t[i]);
+      for (int i = 0; i < NV; ++i) x[i] = to_f32(t[i]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = i < n ? to_f32(p[i]) : 0.f;
+      for (int i = 0; i < NV; ++i) x[i] = i < n ? to_f32(p[i]) : 0.f;
     }
   }
-  __device__ __forceinline__ static void store16(T* p, int n, bool w, const float* x) {
-    if (w && n == 16) {
-      uint4 v[sizeof(T)];
+  template <int NV>
+  __device__ __forceinline__ static void store(T* p, int n, bool w, const float* x) {
+    if (w && n == NV) {
+      constexpr int V = NV * sizeof(T) / sizeof(Word<NV>);
+      Word<NV> v[V];
       T* t = reinterpret_cast<T*>(v);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) t[i] = from_f32<T>(x[i]);
+      for (int i = 0; i < NV; ++i) t[i] = from_f32<T>(x[i]);
 #pragma unroll
-      for (int i = 0; i < (int)sizeof(T); ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+      for (int i = 0; i < V; ++i) reinterpret_cast<Word<NV>*>(p)[i] = v[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < NV; ++i)
         if (i < n) p[i] = from_f32<T>(x[i]);
     }
   }
 
-  // 16 entries of row i from column j on.
-  __device__ __forceinline__ void row16(int64_t i, int64_t j, const float* acc) const {
+  // NV (4 or 16) entries of row i from column j on, j a multiple of NV.
+  template <int NV>
+  __device__ __forceinline__ void row(int64_t i, int64_t j, const float* acc) const {
     if (i >= rows || j >= cols) return;
-    const int n = cols - j >= 16 ? 16 : (int)(cols - j);
-    float c[16], x[16];
+    const int n = cols - j >= NV ? NV : (int)(cols - j);
+    float c[NV], x[NV];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) c[q] = acc[q];
+    for (int q = 0; q < NV; ++q) c[q] = acc[q];
     if (e.bias) {
-      load16(static_cast<const T*>(e.bias) + j, n, wide_b, x);
+      load<NV>(static_cast<const T*>(e.bias) + j, n, wide_b, x);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) c[q] += x[q];
+      for (int q = 0; q < NV; ++q) c[q] += x[q];
     }
-    if (e.Z) store16(static_cast<T*>(e.Z) + i * e.ldz + j, n, wide_z, c);
+    if (e.Z) store<NV>(static_cast<T*>(e.Z) + i * e.ldz + j, n, wide_z, c);
     with_act(e.act, [&](auto act) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) c[q] = act_of<decltype(act)::value>(c[q]);
+      for (int q = 0; q < NV; ++q) c[q] = act_of<decltype(act)::value>(c[q]);
     });
     if (e.R) {
-      load16(static_cast<const T*>(e.R) + i * e.ldr + j, n, wide_r, x);
+      load<NV>(static_cast<const T*>(e.R) + i * e.ldr + j, n, wide_r, x);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) c[q] += x[q];
+      for (int q = 0; q < NV; ++q) c[q] += x[q];
     }
-    store16(static_cast<T*>(e.out) + i * e.ldo + j, n, wide_out, c);
-  }
-
-  // 16 entries of column j from row i on: the warp's lanes hold neighbouring columns.
-  __device__ __forceinline__ void column16(int64_t j, int64_t i, const float* acc) const {
-    if (j >= cols) return;
-    const float b = e.bias ? to_f32(static_cast<const T*>(e.bias)[j]) : 0.f;
-    float c[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) c[q] = acc[q] + b;
-    if (e.Z) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (i + q < rows) static_cast<T*>(e.Z)[(i + q) * e.ldz + j] = from_f32<T>(c[q]);
-    }
-    with_act(e.act, [&](auto act) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) c[q] = act_of<decltype(act)::value>(c[q]);
-    });
-    if (e.R) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (i + q < rows) c[q] += to_f32(static_cast<const T*>(e.R)[(i + q) * e.ldr + j]);
-    }
-#pragma unroll
-    for (int q = 0; q < 16; ++q)
-      if (i + q < rows) static_cast<T*>(e.out)[(i + q) * e.ldo + j] = from_f32<T>(c[q]);
+    store<NV>(static_cast<T*>(e.out) + i * e.ldo + j, n, wide_out, c);
   }
 };
 
@@ -117,12 +99,6 @@ __device__ __forceinline__ void part_row(float* part, int64_t rows, int64_t cols
     for (int q = 0; q < 16; ++q)
       if (j + q < cols) p[q] = c[q];
   }
-}
-__device__ __forceinline__ void part_column(float* part, int64_t rows, int64_t cols, int64_t j, int64_t i, const float* c) {
-  if (j >= cols) return;
-#pragma unroll
-  for (int q = 0; q < 16; ++q)
-    if (i + q < rows) part[(i + q) * cols + j] = c[q];
 }
 
 }  // namespace fxtx

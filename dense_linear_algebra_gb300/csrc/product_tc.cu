@@ -1,15 +1,24 @@
 // product_tc.cu — the products of the linear layer and its gradient on the tensor cores:
 //     C_ij = sum_kk A(i, kk) B(j, kk),   out = act(C + bias_j) + R_ij.
 //
-// One persistent CTA a SM, or a pair of CTAs over two SMs (CG = 2), takes tiles of
-// 128 CG x BN entries of C in turn. Roles, linked by mbarriers only:
+// Roles of a CTA, linked by mbarriers only:
 //   warp 0      one lane: tensor copies of A and B, 64 of kk a stage, 128-byte swizzle;
 //   warp 1      the products (tcgen05.mma, K = 16), one elected lane issuing; in a pair the
 //               first CTA issues for both, each holding its 128 rows of A and half of B;
 //   warps 4-11  the epilogue: a tile's sums from tensor memory (lane = row of the tile),
 //               two warps a quarter of the lanes, each half of the columns.
-// Sums live in two tensor-memory accumulators, so that the epilogue of one tile overlaps the
-// products of the next.
+//
+// Two kernels share them.
+//   product_tc_kernel     many tiles: one persistent CTA a SM, or a pair of CTAs over two SMs
+//                         (CG = 2, 256 x 256 tiles), takes tiles in turn; the sums live in two
+//                         tensor-memory accumulators, so that the epilogue of one tile overlaps
+//                         the products of the next. Few tiles with long sums: the sums are split
+//                         and fp32 partials go to a workspace, which join_kernel adds in order.
+//   product_split_kernel  few tiles: a cluster of up to 8 CTAs takes one tile, each a part of
+//                         kk; every CTA sends each of the others its share of the partial sums
+//                         (distributed shared memory) and finishes its own, adding in order: one
+//                         launch, no workspace. Stages are few, so that two or more CTAs share a
+//                         SM and all of the weights' stream is in flight at once.
 //
 // Operands may be K-major (kk contiguous) or MN-major: the box of a tensor copy, the descriptor
 // and the instruction's major bits change, nothing is transposed. Rows, columns and kk beyond
@@ -47,17 +56,40 @@ constexpr int THREADS = 32 * (4 + EPI_WARPS);
 constexpr int A_BYTES = 128 * BK * 2;  // one plane of A in a stage
 constexpr int CHUNK = 4;               // stages a sum stays in tensor memory (float32)
 
-template <int CG, int BN, int PL>
-struct Cfg {
+template <int CG, int BN, int PL, int KB>
+struct Cfg {  // stages in at most KB kilobytes
   static constexpr int BROWS = BN / CG;  // B's entries a CTA holds
   static constexpr int B_BYTES = BROWS * BK * 2;
   static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
-  static constexpr int S = std::min(8, 208 * 1024 / STAGE);
+  static constexpr int S = std::min(8, KB * 1024 / STAGE);
   static constexpr size_t BYTES = (size_t)S * STAGE + 1024;
   static constexpr int TMEM_COLS = std::max(32, 2 * BN);
   static constexpr int COLS = BN / 2 >= 16 ? BN / 2 : 16;  // columns an epilogue thread takes
   static_assert(S >= 2 && BYTES <= 227 * 1024 && TMEM_COLS <= 512, "shared and tensor memory");
 };
+
+// The split kernel's stages, and room for a tile's partial sums: two CTAs a SM for tiles of
+// up to 64 columns of 16 bits, one of the others.
+template <int BN, int PL>
+struct SplitCfg : Cfg<1, BN, PL, PL == 3 ? 150 : (BN == 128 ? 128 : 80)> {
+  static constexpr int CTAS = PL == 1 && BN <= 64 ? 2 : 1;
+  static constexpr int RED = 128 * (BN + 4) * 4;
+  static constexpr size_t BYTES = SplitCfg::Cfg::BYTES + RED;
+  static_assert(CTAS * (BYTES + 2048) <= 228 * 1024, "shared memory");
+};
+
+// A warp's 32 lanes of COLS tensor-memory columns added to `sum`.
+template <int COLS>
+__device__ __forceinline__ void add_columns(uint32_t t, float* sum) {
+#pragma unroll
+  for (int x = 0; x < COLS; x += 16) {
+    float r[16];
+    tc_load16(t + (uint32_t)x, r);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[x + i] += r[i];
+  }
+}
 
 struct TcArgs {
   int64_t rows = 0, cols = 0;   // the result's
@@ -77,11 +109,54 @@ __device__ __forceinline__ void place(int t, int tl, int tc, int& l, int& c) {
   c = r / size;
 }
 
-template <typename T, int CG, int BN, int PL, bool SWAP>
+// The tensor copies of stage `s`: kk from kb * BK on of the tile's rows of A (from ar) and B (from br).
+template <int CG, class C, int PL>
+__device__ __forceinline__ void load_stage(const CUtensorMap* amap, const CUtensorMap* bmap, const TcArgs& a,
+                                           unsigned char* st, int ar, int br, int kb, uint32_t bar) {
+#pragma unroll
+  for (int p = 0; p < PL; ++p) {
+    unsigned char* d = st + p * A_BYTES;
+    if (a.a_mn) {
+      tma_load_3d<CG>(d, amap, ar, kb * BK, p, bar);
+      tma_load_3d<CG>(d + BK * 128, amap, ar + 64, kb * BK, p, bar);
+    } else {
+      tma_load_3d<CG>(d, amap, kb * BK, ar, p, bar);
+    }
+    d = st + PL * A_BYTES + p * C::B_BYTES;
+    if (a.b_mn) {
+#pragma unroll
+      for (int x = 0; x < C::BROWS / 64; ++x) tma_load_3d<CG>(d + x * BK * 128, bmap, br + 64 * x, kb * BK, p, bar);
+    } else {
+      tma_load_3d<CG>(d, bmap, kb * BK, br, p, bar);
+    }
+  }
+}
+
+// The products of one stage into the accumulator at `d`; `fresh`: the first of a sum.
+template <int CG, class C, int PL>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, const TcArgs& a, bool fresh) {
+  // K = 16 further: 32 bytes along a K-major row, 16 rows of an MN-major operand (16-byte units)
+  const uint64_t as = a.a_mn ? 128 : 2, bs = a.b_mn ? 128 : 2;
+  if constexpr (PL == 1) {
+#pragma unroll
+    for (int q = 0; q < BK / 16; ++q) mma_f16<CG>(d, ad + q * as, bd + q * bs, a.idesc, !fresh || q > 0);
+  } else {
+    // the planes' products, the smallest first
+    constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+    for (int x = 0; x < 6; ++x)
+#pragma unroll
+      for (int q = 0; q < BK / 16; ++q)
+        mma_f16<CG>(d, ad + PA[x] * (A_BYTES >> 4) + q * as, bd + PB[x] * (C::B_BYTES >> 4) + q * bs, a.idesc,
+                    !fresh || x > 0 || q > 0);
+  }
+}
+
+template <typename T, int CG, int BN, int PL>
 __global__ void __launch_bounds__(THREADS, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                       const __grid_constant__ TcArgs a) {
-  using C = Cfg<CG, BN, PL>;
+  using C = Cfg<CG, BN, PL, 208>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
@@ -134,26 +209,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (it >= C::S && !(ok = tc_wait(&empty[s], (uint32_t)((it / C::S - 1) & 1), abort_word))) break;
           // a pair's copies all complete on its first CTA's barrier
           if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(CG * C::STAGE));
-          const uint32_t bar = CG == 2 ? cluster_addr(&full[s], 0) : smem_addr(&full[s]);
-          unsigned char* st = smem + (size_t)s * C::STAGE;
-#pragma unroll
-          for (int p = 0; p < PL; ++p) {
-            unsigned char* d = st + p * A_BYTES;
-            if (a.a_mn) {
-              tma_load_3d<CG>(d, &amap, ar, kb * BK, p, bar);
-              tma_load_3d<CG>(d + BK * 128, &amap, ar + 64, kb * BK, p, bar);
-            } else {
-              tma_load_3d<CG>(d, &amap, kb * BK, ar, p, bar);
-            }
-            d = st + PL * A_BYTES + p * C::B_BYTES;
-            if (a.b_mn) {
-#pragma unroll
-              for (int x = 0; x < C::BROWS / 64; ++x)
-                tma_load_3d<CG>(d + x * BK * 128, &bmap, br + 64 * x, kb * BK, p, bar);
-            } else {
-              tma_load_3d<CG>(d, &bmap, kb * BK, br, p, bar);
-            }
-          }
+          load_stage<CG, C, PL>(&amap, &bmap, a, smem + (size_t)s * C::STAGE, ar, br, kb,
+                                CG == 2 ? cluster_addr(&full[s], 0) : smem_addr(&full[s]));
         }
       }
       // copies still in flight after an abort land before the CTA leaves
@@ -165,8 +222,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool leader = elect_one();
       const uint64_t ad0 = swizzled_desc(smem_addr(smem), BK * 128, 1024);
       const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * A_BYTES), BK * 128, 1024);
-      // K = 16 further: 32 bytes along a K-major row, 16 rows of an MN-major operand (16-byte units)
-      const uint64_t as = a.a_mn ? 128 : 2, bs = a.b_mn ? 128 : 2;
       int it = 0, acc = 0;
       bool ok = true;
       for (int w = first; w < work && ok; w += step) {
@@ -180,22 +235,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!(ok = warp_wait(&full[s], (uint32_t)((it / C::S) & 1), abort_word))) break;
           tc_fence_after();
           if (leader) {
-            const uint32_t d = tmem + (uint32_t)((acc & 1) * BN);
-            const uint64_t ad = ad0 + (uint64_t)(s * (C::STAGE >> 4)), bd = bd0 + (uint64_t)(s * (C::STAGE >> 4));
-            if constexpr (PL == 1) {
-#pragma unroll
-              for (int q = 0; q < BK / 16; ++q)
-                mma_f16<CG>(d, ad + q * as, bd + q * bs, a.idesc, !fresh || q > 0);
-            } else {
-              // the planes' products, the smallest first
-              constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
-#pragma unroll
-              for (int x = 0; x < 6; ++x)
-#pragma unroll
-                for (int q = 0; q < BK / 16; ++q)
-                  mma_f16<CG>(d, ad + PA[x] * (A_BYTES >> 4) + q * as, bd + PB[x] * (C::B_BYTES >> 4) + q * bs, a.idesc,
-                              !fresh || x > 0 || q > 0);
-            }
+            mma_stage<CG, C, PL>(tmem + (uint32_t)((acc & 1) * BN), ad0 + (uint64_t)(s * (C::STAGE >> 4)),
+                                 bd0 + (uint64_t)(s * (C::STAGE >> 4)), a, fresh);
             mma_commit<CG>(&empty[s]);
             if (last) mma_commit<CG>(&tfull[acc & 1]);
           }
@@ -210,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
     const uint32_t te0 = CG == 2 ? cluster_addr(&tempty[0], 0) : smem_addr(&tempty[0]);
     const Finish<T> fin(a.e, a.rows, a.cols);
     int acc = 0;
@@ -219,18 +260,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       int l, c, k0, k1;
       place(w / a.splits, a.tiles_l, a.tiles_c, l, c);
       range(w, k0, k1);
-      const int64_t li = (int64_t)l * 128 * CG + rank * 128 + 32 * q + lane;  // the lane's row (column) of the result
-      const int64_t ci = (int64_t)c * BN + half * C::COLS;                   // its first column (row)
-      const bool mine = half * C::COLS < BN;
+      const int64_t li = (int64_t)l * 128 * CG + rank * 128 + 32 * q + lane;  // the lane's row of the result
+      const int64_t ci = (int64_t)c * BN + half * C::COLS;                   // its first column
       float* part = a.splits > 1 ? a.part + (int64_t)(w % a.splits) * a.rows * a.cols : nullptr;
       auto store = [&](int64_t col, const float* x) {
-        if constexpr (SWAP) {
-          if (part) part_column(part, a.rows, a.cols, li, col, x);
-          else fin.column16(li, col, x);
-        } else {
-          if (part) part_row(part, a.rows, a.cols, li, col, x);
-          else fin.row16(li, col, x);
-        }
+        if (part) part_row(part, a.rows, a.cols, li, col, x);
+        else fin.template row<16>(li, col, x);
       };
       auto release = [&]() {
         tc_fence_before();
@@ -241,15 +276,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       if constexpr (PL == 1) {
         if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
         tc_fence_after();
-        if (mine) {
-          const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN + half * C::COLS);
+        const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN);
 #pragma unroll 1
-          for (int x = 0; x < C::COLS; x += 16) {
-            float r[16];
-            tc_load16(t + (uint32_t)x, r);
-            tc_wait_ld();
-            store(ci + x, r);
-          }
+        for (int x = 0; x < C::COLS; x += 16) {
+          float r[16];
+          tc_load16(t + (uint32_t)x, r);
+          tc_wait_ld();
+          store(ci + x, r);
         }
         release();
       } else {
@@ -259,24 +292,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int kb = k0; kb < k1; kb += CHUNK) {
           if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
           tc_fence_after();
-          if (mine) {
-            const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN + half * C::COLS);
-#pragma unroll
-            for (int x = 0; x < C::COLS; x += 16) {
-              float r[16];
-              tc_load16(t + (uint32_t)x, r);
-              tc_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) sum[x + i] += r[i];
-            }
-          }
+          add_columns<C::COLS>(lane_base + (uint32_t)((acc & 1) * BN), sum);
           release();
         }
         if (!ok) break;
-        if (mine) {
 #pragma unroll
-          for (int x = 0; x < C::COLS; x += 16) store(ci + x, sum + x);
-        }
+        for (int x = 0; x < C::COLS; x += 16) store(ci + x, sum + x);
       }
     }
   }
@@ -292,6 +313,167 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
   tc_fence_after();
   if (warp == 2) tmem_free<CG>(tmem, C::TMEM_COLS);
+}
+
+// One tile a cluster. The CTA of rank r of R finishes lanes r * 128 / R .. of the tile: every
+// CTA stores its partial sums of those lanes to r's shared memory (after the stages, which r
+// may still be reading), one cluster barrier, and r adds the R parts in order.
+template <typename T, int BN, int PL, bool SWAP>
+__global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
+    product_split_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+                         const __grid_constant__ TcArgs a) {
+  using C = SplitCfg<BN, PL>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  volatile int* abort_word = &s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int R = a.splits;
+
+  if (tid == 0) {
+    s_abort = 0;
+    for (int s = 0; s < C::S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&tfull[s], 1);
+      mbar_init(&tempty[s], EPI_WARPS);
+    }
+    mbar_init(&fin_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 2) tmem_alloc<1>(&s_tmem, C::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  cluster_arrive();  // waited for before the first store to another CTA
+  const uint32_t tmem = s_tmem;
+
+  int l, c;
+  place((int)(blockIdx.x / (unsigned)R), a.tiles_l, a.tiles_c, l, c);
+  const int k0 = (int)rank * a.per_split, k1 = min(a.kblocks, k0 + a.per_split);
+  bool ok = true;
+  float sum[PL == 3 ? C::COLS : 1];
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      for (int kb = k0; kb < k1; ++kb, ++it) {
+        const int s = it % C::S;
+        if (it >= C::S && !(ok = tc_wait(&empty[s], (uint32_t)((it / C::S - 1) & 1), abort_word))) break;
+        mbar_arrive_expect_tx(&full[s], (uint32_t)C::STAGE);
+        load_stage<1, C, PL>(&amap, &bmap, a, smem + (size_t)s * C::STAGE, l * 128, c * BN, kb, smem_addr(&full[s]));
+      }
+      if (!ok)
+        for (int j = it > C::S ? it - C::S : 0; j < it; ++j) mbar_wait_bounded(&full[j % C::S], (uint32_t)((j / C::S) & 1));
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool leader = elect_one();
+    const uint64_t ad0 = swizzled_desc(smem_addr(smem), BK * 128, 1024);
+    const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * A_BYTES), BK * 128, 1024);
+    int acc = 0, it = 0;
+    for (int kb = k0; kb < k1; ++kb, ++it) {
+      const bool fresh = PL == 3 ? it % CHUNK == 0 : it == 0;
+      const bool last = kb == k1 - 1 || (PL == 3 && it % CHUNK == CHUNK - 1);
+      if (fresh && acc >= 2 && !(ok = warp_wait(&tempty[acc & 1], (uint32_t)(((acc >> 1) - 1) & 1), abort_word))) break;
+      const int s = it % C::S;
+      if (!(ok = warp_wait(&full[s], (uint32_t)((it / C::S) & 1), abort_word))) break;
+      tc_fence_after();
+      if (leader) {
+        mma_stage<1, C, PL>(tmem + (uint32_t)((acc & 1) * BN), ad0 + (uint64_t)(s * (C::STAGE >> 4)),
+                            bd0 + (uint64_t)(s * (C::STAGE >> 4)), a, fresh);
+        mma_commit<1>(&empty[s]);
+        if (last) mma_commit<1>(&tfull[acc & 1]);
+      }
+      __syncwarp();
+      if (last) ++acc;
+    }
+    if (leader) mma_commit<1>(&fin_bar);
+    __syncwarp();
+    mbar_wait_bounded(&fin_bar, 0);
+  } else if (warp >= 4) {
+    // the sums into registers (float32), or up to their last product (16 bits)
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const bool mine = half * C::COLS < BN;
+    if constexpr (PL == 3) {
+      const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
+#pragma unroll
+      for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
+      int acc = 0;
+      for (int kb = k0; kb < k1; kb += CHUNK, ++acc) {
+        if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
+        tc_fence_after();
+        if (mine) add_columns<C::COLS>(t + (uint32_t)((acc & 1) * BN), sum);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(smem_addr(&tempty[acc & 1]));
+      }
+    } else {
+      ok = warp_wait(&tfull[0], 0, abort_word);
+      tc_fence_after();
+    }
+  }
+
+  // the partial sums to the CTAs that finish them: [from][lane of R-th][column] (rows of the result
+  // are lanes), or with SWAP [from][column][lane]
+  __syncwarp();
+  cluster_wait();
+  const int share = 128 / R;  // lanes a CTA finishes
+  const int pitch = SWAP ? share : BN + 4, block = SWAP ? BN * share : share * pitch;
+  float* red = reinterpret_cast<float*>(smem + (size_t)C::S * C::STAGE);
+  if (warp >= 4 && ok) {
+    const int q = warp & 3, half = (warp - 4) >> 2, L = 32 * q + lane;
+    if (half * C::COLS < BN) {
+      const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
+      const uint32_t to = cluster_addr(red, (uint32_t)(L / share)) + (uint32_t)((rank * block) * 4);
+#pragma unroll
+      for (int x = 0; x < C::COLS; x += 16) {
+        float r[16];
+        if constexpr (PL == 3) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) r[i] = sum[x + i];
+        } else {
+          tc_load16(t + (uint32_t)x, r);
+          tc_wait_ld();
+        }
+        const int col = half * C::COLS + x;
+        if constexpr (SWAP) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) st_cluster(to + (uint32_t)(((col + i) * share + L % share) * 4), r[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            st_cluster4(to + (uint32_t)(((L % share) * pitch + col + i) * 4), r[i], r[i + 1], r[i + 2], r[i + 3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  const bool failed = __syncthreads_or(!ok);
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 2) tmem_free<1>(tmem, C::TMEM_COLS);
+  if (failed) return;  // FXTX_ERR_TIMEOUT is raised
+
+  const Finish<T> fin(a.e, a.rows, a.cols);
+  const int groups = SWAP ? share / 4 : BN / 4, units = SWAP ? BN * groups : share * groups;
+  for (int u = tid; u < units; u += THREADS) {
+    const int y = u / groups, x = u % groups * 4;
+    const int64_t i = SWAP ? (int64_t)c * BN + y : (int64_t)l * 128 + rank * share + y;
+    const int64_t j = SWAP ? (int64_t)l * 128 + rank * share + x : (int64_t)c * BN + x;
+    if (i >= a.rows || j >= a.cols) continue;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < R; ++s) {
+      const float4 p = *reinterpret_cast<const float4*>(red + s * block + y * pitch + x);
+      v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+    }
+    fin.template row<4>(i, j, v);
+  }
 }
 
 // out = the epilogue of the splits' sums, added in order.
@@ -311,31 +493,42 @@ __global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t row
       for (int q = 0; q < 16; ++q)
         if (j + q < cols) c[q] += p[q];
     }
-    fin.row16(i, j, c);
+    fin.template row<16>(i, j, c);
   }
 }
 
-template <typename T, int CG, int BN, int PL, bool SWAP>
-cudaError_t launch(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, int sm_count, cudaStream_t st) {
-  using C = Cfg<CG, BN, PL>;
-  const void* k = (const void*)product_tc_kernel<T, CG, BN, PL, SWAP>;
-  cudaError_t e = ensure_smem(k, C::BYTES);
+cudaError_t launch_clustered(const void* k, size_t smem, unsigned grid, int cluster, const CUtensorMap& am,
+                             const CUtensorMap& bm, const TcArgs& a, cudaStream_t st) {
+  cudaError_t e = ensure_smem(k, smem);
   if (e != cudaSuccess) return e;
-  const int64_t work = (int64_t)a.tiles_l * a.tiles_c * a.splits;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(work, sm_count / CG) * CG));
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
-  if (CG > 1) {
+  if (cluster > 1) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
   }
-  return cudaLaunchKernelEx(&cfg, product_tc_kernel<T, CG, BN, PL, SWAP>, am, bm, a);
+  void* args[] = {const_cast<CUtensorMap*>(&am), const_cast<CUtensorMap*>(&bm), const_cast<TcArgs*>(&a)};
+  return cudaLaunchKernelExC(&cfg, k, args);
+}
+
+template <typename T, int CG, int BN, int PL>
+cudaError_t launch(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, int sm_count, cudaStream_t st) {
+  const int64_t work = (int64_t)a.tiles_l * a.tiles_c * a.splits;
+  return launch_clustered((const void*)product_tc_kernel<T, CG, BN, PL>, Cfg<CG, BN, PL, 208>::BYTES,
+                          (unsigned)(std::min<int64_t>(work, sm_count / CG) * CG), CG, am, bm, a, st);
+}
+
+template <typename T, int BN, int PL, bool SWAP>
+cudaError_t launch_split(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, cudaStream_t st) {
+  return launch_clustered((const void*)product_split_kernel<T, BN, PL, SWAP>, SplitCfg<BN, PL>::BYTES,
+                          (unsigned)(a.tiles_l * a.tiles_c * a.splits), a.splits, am, bm, a, st);
 }
 
 // The map of an operand for boxes of 128 bytes x its tile's rows (or BK of them, MN-major).
@@ -372,24 +565,33 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   memset(&am, 0, sizeof am);
   memset(&bm, 0, sizeof bm);
   if (!operand_map(&am, A, bf16, 128) || !operand_map(&bm, B, bf16, plan.bn / plan.cg)) return FXTX_ERR_CUDA;
-  if (a.splits > 1) {
-    const fxtx_status_t s = alloc_ws(reinterpret_cast<void**>(&a.part), (size_t)a.splits * p.M * p.N * 4, st);
+  if (!plan.cluster && a.splits > 1) {
+    const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)a.splits * p.M * p.N * 4, st);
     if (s != FXTX_OK) return s;
   }
   cudaError_t e = cudaErrorInvalidConfiguration;
   if (plan.swap) {
     switch (plan.bn) {
-      case 16: e = launch<T, 1, 16, PL, true>(am, bm, a, dev.sm_count, st); break;
-      case 32: e = launch<T, 1, 32, PL, true>(am, bm, a, dev.sm_count, st); break;
-      case 64: e = launch<T, 1, 64, PL, true>(am, bm, a, dev.sm_count, st); break;
-      case 128: e = launch<T, 1, 128, PL, true>(am, bm, a, dev.sm_count, st); break;
+      case 16: e = launch_split<T, 16, PL, true>(am, bm, a, st); break;
+      case 32: e = launch_split<T, 32, PL, true>(am, bm, a, st); break;
+      case 64: e = launch_split<T, 64, PL, true>(am, bm, a, st); break;
+      case 128:
+        if constexpr (!F32) e = launch_split<T, 128, PL, true>(am, bm, a, st);
+        break;
+    }
+  } else if (plan.cluster) {
+    switch (plan.bn) {
+      case 64: e = launch_split<T, 64, PL, false>(am, bm, a, st); break;
+      case 128:
+        if constexpr (!F32) e = launch_split<T, 128, PL, false>(am, bm, a, st);
+        break;
     }
   } else if (plan.cg == 2) {
-    if constexpr (!F32) e = launch<T, 2, 256, PL, false>(am, bm, a, dev.sm_count, st);
+    if constexpr (!F32) e = launch<T, 2, 256, PL>(am, bm, a, dev.sm_count, st);
   } else {
     switch (plan.bn) {
-      case 64: e = launch<T, 1, 64, PL, false>(am, bm, a, dev.sm_count, st); break;
-      case 128: e = launch<T, 1, 128, PL, false>(am, bm, a, dev.sm_count, st); break;
+      case 64: e = launch<T, 1, 64, PL>(am, bm, a, dev.sm_count, st); break;
+      case 128: e = launch<T, 1, 128, PL>(am, bm, a, dev.sm_count, st); break;
     }
   }
   if (a.part) {

@@ -8,7 +8,10 @@ import numpy as np
 import torch
 
 from . import _lib
-from ._lib import _check, _on, _stream
+from ._lib import _check, fxtx_adamw, fxtx_adamw_moments, fxtx_linear, fxtx_linear_grad
+
+_current_device = torch.cuda.current_device
+_current_stream = torch._C._cuda_getCurrentRawStream  # of a device, as the integer that the C entries take
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # fxtx_type_t
 
@@ -35,10 +38,8 @@ def _act(act):
 
 def _matrix(t, dtype, m, n, name, index):
     """The row pitch of a row-major (m, n) CUDA tensor."""
-    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
-        raise ValueError(f"{name}: expected a {dtype} matrix on cuda:{index}")
-    if t.shape[0] != m or t.shape[1] != n:
-        raise ValueError(f"{name}: expected shape {(m, n)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype or t.get_device() != index or t.shape != (m, n):
+        raise ValueError(f"{name}: expected a {dtype} matrix of shape {(m, n)} on cuda:{index}")
     ld, unit = t.stride()
     if m <= 1:
         ld = n
@@ -49,11 +50,9 @@ def _matrix(t, dtype, m, n, name, index):
 
 def _weights(W, dtype, n, index):
     """W (n, k): its columns' count, its pitch and whether it is stored by its columns."""
-    if W.dtype is not dtype or W.get_device() != index or W.dim() != 2:
-        raise ValueError(f"W: expected a {dtype} matrix on cuda:{index}")
+    if W.dtype is not dtype or W.get_device() != index or W.dim() != 2 or W.shape[0] != n:
+        raise ValueError(f"W: expected a {dtype} matrix of {n} rows on cuda:{index}")
     k = W.shape[1]
-    if W.shape[0] != n:
-        raise ValueError(f"W: expected {n} rows, got {W.shape[0]}")
     s0, s1 = W.stride()
     if (s1 == 1 or k <= 1) and (s0 >= k or n <= 1):
         return k, s0 if n > 1 else k, 0
@@ -62,14 +61,41 @@ def _weights(W, dtype, n, index):
     raise ValueError("W: expected unit stride along its rows or its columns")
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, like, stream):
     """A new tensor of the stream that writes it (the current one unless `stream` is given)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _raw(stream, index):
+    """`stream`, or the current one, as the C entries take it."""
+    if stream is None:
+        return _current_stream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _call(fn, index, *args):
+    """A C entry with the tensors' device current."""
+    if _current_device() == index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args)
+    if rc:
+        _check(rc, fn.__name__)
+
+
+def _features(X):
+    """The type code, device, rows, features and row pitch of X."""
+    index = X.get_device()
+    if index < 0 or X.dim() != 2:
+        raise ValueError("X: expected a 2-D CUDA tensor")
+    m, n = X.shape
+    return _type(X, "X"), index, m, n, _matrix(X, X.dtype, m, n, "X", index)
 
 
 def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=None):
@@ -81,30 +107,29 @@ def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=No
     returns Z = X W + b for ``linear_grad`` (or give the (m, k) tensor to keep it in). ``out`` may be ``residual``.
     Runs on the current stream, or on ``stream``, which then owns the new tensors.
     """
-    if not X.is_cuda or X.dim() != 2:
-        raise ValueError("X: expected a 2-D CUDA tensor")
-    dt, di = X.dtype, X.get_device()
-    code = _type(X, "X")
-    m, n = X.shape
-    ldx = _matrix(X, dt, m, n, "X", di)
+    code, di, m, n, ldx = _features(X)
+    dt = X.dtype
     k, ldw, trans = _weights(W, dt, n, di)
+    pb = pr = pz = None
+    ldr = ldz = 0
     if b is not None:
         _lib._vec(b, dt, k, "b", di)
-    ldr = 0 if residual is None else _matrix(residual, dt, m, k, "residual", di)
-    keep = None if pre is False or pre is None else (_empty((m, k), dt, X.device, stream) if pre is True else pre)
-    ldz = 0 if keep is None else _matrix(keep, dt, m, k, "pre", di)
+        pb = b.data_ptr()
+    if residual is not None:
+        ldr, pr = _matrix(residual, dt, m, k, "residual", di), residual.data_ptr()
+    if pre is False:
+        pre = None
+    elif pre is True:
+        pre = _empty((m, k), X, stream)
+    if pre is not None:
+        ldz, pz = _matrix(pre, dt, m, k, "pre", di), pre.data_ptr()
     if out is None:
-        out, ldo = _empty((m, k), dt, X.device, stream), k
+        out, ldo = _empty((m, k), X, stream), k
     else:
         ldo = _matrix(out, dt, m, k, "out", di)
-    with _on(di):
-        rc = _lib.fxtx_linear(code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans,
-                              None if b is None else b.data_ptr(), _act(act),
-                              None if residual is None else residual.data_ptr(), ldr,
-                              None if keep is None else keep.data_ptr(), ldz, out.data_ptr(), ldo,
-                              _stream(stream, X.device))
-    _check(rc, "fxtx_linear")
-    return out if keep is None else (out, keep)
+    _call(fxtx_linear, di, code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans, pb, _act(act), pr, ldr, pz, ldz,
+          out.data_ptr(), ldo, _raw(stream, di))
+    return out if pre is None else (out, pre)
 
 
 def linear_grad(G, X, W, pre=None, act=None, need=(True, True, True), stream=None):
@@ -114,27 +139,20 @@ def linear_grad(G, X, W, pre=None, act=None, need=(True, True, True), stream=Non
     (not needed without an activation). ``need`` says which of the three are computed; the others come back as None.
     dW is stored as W is. Types, layouts and streams are those of ``linear``.
     """
-    if not X.is_cuda or X.dim() != 2:
-        raise ValueError("X: expected a 2-D CUDA tensor")
-    dt, di = X.dtype, X.get_device()
-    code, kind = _type(X, "X"), _act(act)
-    m, n = X.shape
-    ldx = _matrix(X, dt, m, n, "X", di)
+    code, di, m, n, ldx = _features(X)
+    dt, kind = X.dtype, _act(act)
     k, ldw, trans = _weights(W, dt, n, di)
     ldg = _matrix(G, dt, m, k, "G", di)
     if kind and pre is None:
         raise ValueError("pre: the gradient of an activation needs the Z that linear kept")
-    ldz = 0 if not kind else _matrix(pre, dt, m, k, "pre", di)
-    dX = _empty((m, n), dt, X.device, stream) if need[0] else None
-    dW = _empty((k, n) if trans else (n, k), dt, X.device, stream) if need[1] else None
-    db = _empty((k,), dt, X.device, stream) if need[2] else None
-    with _on(di):
-        rc = _lib.fxtx_linear_grad(code, m, n, k, G.data_ptr(), ldg, X.data_ptr(), ldx, W.data_ptr(), ldw, trans,
-                                   pre.data_ptr() if kind else None, ldz, kind,
-                                   None if dX is None else dX.data_ptr(), n,
-                                   None if dW is None else dW.data_ptr(), n if trans else k,
-                                   None if db is None else db.data_ptr(), _stream(stream, X.device))
-    _check(rc, "fxtx_linear_grad")
+    ldz = _matrix(pre, dt, m, k, "pre", di) if kind else 0
+    dX = _empty((m, n), X, stream) if need[0] else None
+    dW = _empty((k, n) if trans else (n, k), X, stream) if need[1] else None
+    db = _empty((k,), X, stream) if need[2] else None
+    _call(fxtx_linear_grad, di, code, m, n, k, G.data_ptr(), ldg, X.data_ptr(), ldx, W.data_ptr(), ldw, trans,
+          pre.data_ptr() if kind else None, ldz, kind, None if dX is None else dX.data_ptr(), n,
+          None if dW is None else dW.data_ptr(), n if trans else k, None if db is None else db.data_ptr(),
+          _raw(stream, di))
     return dX, dW.t() if dW is not None and trans else dW, db
 
 
@@ -231,11 +249,9 @@ class AdamW:
             table[:, 7] = self._pointers(self.copies, self._copy_dtype, "copies")
         # an entry of no elements is left out
         table[:, 0] = [0 if g is None else n for g, n in zip(grads, self._sizes)]
-        with _on(self._index):
-            rc = _lib.fxtx_adamw(len(self._sizes), table.ctypes.data, self._type, g_type, self._copy_type,
-                                 self.state_bits, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps,
-                                 self.weight_decay, _stream(stream, self._device))
-        _check(rc, "fxtx_adamw")
+        _call(fxtx_adamw, self._index, len(self._sizes), table.ctypes.data, self._type, g_type, self._copy_type,
+              self.state_bits, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
+              _raw(stream, self._index))
         self.steps += 1
 
     def moments(self, stream=None):
@@ -243,13 +259,11 @@ class AdamW:
         bits, for 8 the values that they stand for."""
         if self.state_bits == 32:
             return self.exp_avg, self.exp_avg_sq
-        m = torch.empty(self._total, dtype=torch.float32, device=self._device)
-        v = torch.empty(self._total, dtype=torch.float32, device=self._device)
-        with _on(self._index):
-            rc = _lib.fxtx_adamw_moments(self._total, self.exp_avg.data_ptr(), self.exp_avg_scale.data_ptr(),
-                                         self.exp_avg_sq.data_ptr(), self.exp_avg_sq_scale.data_ptr(), m.data_ptr(),
-                                         v.data_ptr(), _stream(stream, self._device))
-        _check(rc, "fxtx_adamw_moments")
+        m = _empty((self._total,), self.exp_avg_scale, stream)
+        v = _empty((self._total,), self.exp_avg_scale, stream)
+        _call(fxtx_adamw_moments, self._index, self._total, self.exp_avg.data_ptr(), self.exp_avg_scale.data_ptr(),
+              self.exp_avg_sq.data_ptr(), self.exp_avg_sq_scale.data_ptr(), m.data_ptr(), v.data_ptr(),
+              _raw(stream, self._index))
         return m, v
 
     def _state(self):
