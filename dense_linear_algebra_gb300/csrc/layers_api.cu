@@ -42,15 +42,22 @@ fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, con
   const DeviceInfo* dev = nullptr;
   const fxtx_status_t s = current_device(&dev);
   if (s != FXTX_OK) return s;
+  LayerArgs l;
+  l.type = type;
+  l.m = m; l.n = n; l.k = k;
+  l.X = X; l.ldx = ldx;
+  l.W = W; l.ldw = ldw; l.w_trans = w_trans != 0;
+  l.e.bias = b; l.e.act = act;
+  l.e.R = R; l.e.ldr = ldr;
+  l.e.Z = Z; l.e.ldz = ldz;
+  l.e.out = OUT; l.e.ldo = ldo;
+  if (thin_shape(n, k)) return run_thin_linear(l, *dev, static_cast<cudaStream_t>(stream));
   Product p;
   p.type = type;
   p.M = m; p.N = k; p.K = n;
   p.A.p = X; p.A.ld = ldx;
   p.B.p = W; p.B.ld = ldw; p.B.mn_major = !w_trans;
-  p.e.bias = b; p.e.act = act;
-  p.e.R = R; p.e.ldr = ldr;
-  p.e.Z = Z; p.e.ldz = ldz;
-  p.e.out = OUT; p.e.ldo = ldo;
+  p.e = l.e;
   return run_product(p, *dev, static_cast<cudaStream_t>(stream));
 }
 
@@ -69,6 +76,21 @@ fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k
   if (s != FXTX_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
 
+  if (m > 0 && thin_shape(n, k)) {
+    LayerArgs l;
+    l.type = type;
+    l.m = m; l.n = n; l.k = k;
+    l.X = X; l.ldx = ldx;
+    l.W = W; l.ldw = ldw; l.w_trans = w_trans != 0;
+    GradArgs g;
+    g.G = G; g.ldg = ldg;
+    g.Z = Z; g.ldz = ldz;
+    g.act = act;
+    g.DX = DX; g.lddx = lddx;
+    g.DW = DW; g.lddw = lddw;
+    g.DB = DB;
+    return run_thin_grad(l, g, *dev, st);
+  }
   const bool products = n > 0 && (DX || DW) && m > 0 && k > 0;
   SlopeArgs a;
   a.type = type;

@@ -78,6 +78,36 @@ struct PackArgs {
 };
 cudaError_t launch_pack(const PackArgs& a, int sm_count, cudaStream_t st);
 
+// A layer's arguments, and its gradient's.
+struct LayerArgs {
+  fxtx_type_t type = FXTX_F32;
+  int64_t m = 0, n = 0, k = 0;
+  const void* X = nullptr;
+  int64_t ldx = 0;
+  const void* W = nullptr;
+  int64_t ldw = 0;
+  bool w_trans = false;
+  Epilogue e;
+};
+struct GradArgs {
+  const void* G = nullptr;
+  int64_t ldg = 0;
+  const void* Z = nullptr;
+  int64_t ldz = 0;
+  int act = FXTX_ACT_NONE;
+  void* DX = nullptr;
+  int64_t lddx = 0;
+  void* DW = nullptr;
+  int64_t lddw = 0;
+  void* DB = nullptr;
+};
+
+// Layers of 1 to kThin features and outputs, on the CUDA cores.
+constexpr int kThin = 64;
+bool thin_shape(int64_t n, int64_t k);
+fxtx_status_t run_thin_linear(const LayerArgs& l, const DeviceInfo& dev, cudaStream_t st);
+fxtx_status_t run_thin_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& dev, cudaStream_t st);
+
 // D = G * act'(Z) and its column sums. D is written with row pitch ldd unless it is NULL (of
 // float32 as three bfloat16 planes, d_planes elements apart); db unless it is NULL.
 struct SlopeArgs {

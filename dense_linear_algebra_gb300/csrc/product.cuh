@@ -60,7 +60,7 @@ struct Finish {
     }
   }
 
-  // NV (4 or 16) entries of row i from column j on, j a multiple of NV.
+  // NV (4, 8 or 16) entries of row i from column j on, j a multiple of NV.
   template <int NV>
   __device__ __forceinline__ void row(int64_t i, int64_t j, const float* acc) const {
     if (i >= rows || j >= cols) return;

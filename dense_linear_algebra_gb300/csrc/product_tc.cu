@@ -35,6 +35,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstdio>
 #include <cstring>
 #include <type_traits>
 
@@ -547,6 +548,10 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   constexpr int PL = F32 ? 3 : 1;
   const bool bf16 = !std::is_same<T, __half>::value;
   const TcPlan plan = plan_product(p.M, p.N, p.K, PL, p.A.mn_major, p.B.mn_major, dev.sm_count);
+  if (log_enabled())
+    fprintf(stderr, "[fxtx] product M=%lld N=%lld K=%lld planes=%d %s%s cg=%d bn=%d splits=%d\n", (long long)p.M,
+            (long long)p.N, (long long)p.K, PL, plan.swap ? "swap " : "", plan.cluster ? "cluster" : "persistent", plan.cg,
+            plan.bn, plan.splits);
   const Planes &A = plan.swap ? p.B : p.A, &B = plan.swap ? p.A : p.B;
   TcArgs a;
   a.rows = p.M;
