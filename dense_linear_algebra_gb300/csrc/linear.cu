@@ -76,11 +76,13 @@ fxtx_status_t run_empty(const Product& p, const DeviceInfo& dev, cudaStream_t st
 
 }  // namespace
 
-// The layout with the least estimated time, in cycles. A stage (64 of kk) takes its products (an
-// M = 128, K = 16 product holds the pipe for 64 cycles up to N = 128) or its bytes at an SM's
-// share of L2; the stages that the busiest SM gets follow one another, and no layout beats the
-// operands' stream from HBM. On top come a fixed cost for filling the pipeline, and the
-// exchange of partial sums: between the CTAs of a cluster, or through memory and a second kernel.
+// The layout with the least estimated time, in cycles of an SM (figures measured on GB300). A stage
+// (64 of kk) takes its products (an M = 128, K = 16 product of a CTA holds the pipe for 64 cycles up
+// to N = 128) or its bytes, of which an SM gets about 55 a cycle from L2 with the deep pipelines of the
+// persistent kernel and a CTA of the split kernel about 32; no layout beats the operands' stream from
+// HBM. A persistent CTA's tiles follow one another, each for as long as its products or its epilogue
+// take. On top come a fixed cost (launch, filling the pipeline, the last epilogue) and the exchange of
+// partial sums: between the CTAs of a cluster, or through memory and a second kernel.
 TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count) {
   const int64_t kb = std::max<int64_t>(1, (K + 63) / 64);
   TcPlan best;
@@ -89,17 +91,23 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
   auto consider = [&](bool swap, bool cluster, int cg, int bn) {
     const int64_t L = swap ? N : M, Cn = swap ? M : N;
     if ((swap ? a_mn : b_mn) && bn / cg < 64) return;  // an MN-major box is 64 wide
-    const int64_t tiles = ((L + 128 * cg - 1) / (128 * cg)) * ((Cn + bn - 1) / bn), units = sm_count / cg;
+    const int64_t tiles = ((L + 128 * cg - 1) / (128 * cg)) * ((Cn + bn - 1) / bn);
+    // CTAs (or pairs) at a time: two of the split kernel's narrow ones share an SM
+    const int64_t units = cluster && planes == 1 && bn <= 64 ? 2 * sm_count : sm_count / cg;
     const double mma = 4.0 * (planes == 3 ? 6 : 1) * std::max(64.0, bn / 2.0);
     const double bytes = planes * (16384.0 + bn / cg * 128.0);
-    const double stage = std::max(mma, bytes / 40.0);
+    const double stage = std::max(mma, bytes / (cluster ? 32.0 : 55.0)), epilogue = 400.0 + 12.0 * bn;
     auto price = [&](int64_t s) {
       const int64_t per = (kb + s - 1) / s;
       if (cluster && (s - 1) * per >= kb) return;  // a CTA without work
       const int64_t waves = (tiles * s + units - 1) / units;
-      double t = std::max(floor, waves * (per * stage + 400.0)) + 2500.0 + 6.0 * bn;
-      if (cluster) t += (s > 1 ? 1000.0 : 0.0) + (waves - 1) * 1500.0;
-      else if (s > 1) t += 5000.0 + (double)s * M * N * 8.0 / 2500.0;
+      double t;
+      if (cluster) {
+        t = std::max(floor, waves * (per * stage)) + waves * (3000.0 + 15.0 * bn) + (s > 1 ? 800.0 : 0.0);
+      } else {
+        t = std::max(floor, waves * std::max(per * stage, epilogue)) + 4500.0 + epilogue;
+        if (s > 1) t += 4500.0 + (double)s * M * N * 8.0 / 3000.0;
+      }
       if (t < best_t) {
         best_t = t;
         best.swap = swap;
@@ -122,6 +130,7 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
   if (planes == 1) consider(false, true, 1, 128);
   consider(false, false, 1, 64);
   consider(false, false, 1, 128);
+  consider(false, false, 2, 128);
   if (planes == 1) consider(false, false, 2, 256);
   return best;
 }

@@ -87,18 +87,64 @@ struct Finish {
   }
 };
 
-// The same entries as partial sums.
-__device__ __forceinline__ void part_row(float* part, int64_t rows, int64_t cols, int64_t i, int64_t j, const float* c) {
-  if (i >= rows) return;
-  float* p = part + i * cols + j;
-  if (cols % 4 == 0 && j + 16 <= cols) {
-#pragma unroll
-    for (int q = 0; q < 16; q += 4) *reinterpret_cast<float4*>(p + q) = make_float4(c[q], c[q + 1], c[q + 2], c[q + 3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 16; ++q)
-      if (j + q < cols) p[q] = c[q];
+// A warp's 32 rows x up to 128 bytes on their way between the lanes, a row each, and memory, where
+// 16-byte accesses of neighbouring lanes cover neighbouring bytes: row r's 16-byte chunk c lies at chunk
+// c ^ (r % 8) of its 128 bytes, so that both sides' accesses fall into distinct banks.
+template <typename T, int W>
+struct Tile32 {
+  static constexpr int EPC = 16 / sizeof(T), CH = W / EPC, ROWS = 32 / CH;  // entries a chunk, chunks a row, rows an access
+  static_assert(W * sizeof(T) <= 128 && W % 16 == 0, "a row is 32 to 128 bytes");
+  __device__ __forceinline__ static uint4* at(unsigned char* buf, int r, int c) {
+    return reinterpret_cast<uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
   }
-}
+  // 16 entries of the lane's own row from column x on
+  __device__ __forceinline__ static void put(unsigned char* buf, int x, const float* v) {
+    const int r = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 16 / EPC; ++c) {
+      uint4 w;
+      T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+      for (int q = 0; q < EPC; ++q) t[q] = from_f32<T>(v[c * EPC + q]);
+      *at(buf, r, x / EPC + c) = w;
+    }
+  }
+  __device__ __forceinline__ static void add(unsigned char* buf, int x, float* v) {
+    const int r = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 16 / EPC; ++c) {
+      const uint4 w = *at(buf, r, x / EPC + c);
+      const T* t = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int q = 0; q < EPC; ++q) v[c * EPC + q] += to_f32(t[q]);
+    }
+  }
+  // rows i0 .. i0 + 31 and columns j0 .. j0 + W - 1 of a matrix of rows x cols to memory, or from it
+  template <bool STORE>
+  __device__ __forceinline__ static void move(unsigned char* buf, T* p, int64_t ld, bool wide, int64_t i0, int64_t rows,
+                                              int64_t j0, int64_t cols) {
+    const int lane = threadIdx.x & 31;
+    if (wide && j0 + W <= cols) {
+#pragma unroll
+      for (int k = 0; k < CH; ++k) {
+        const int r = k * ROWS + lane / CH, c = lane % CH;
+        if (i0 + r < rows) {
+          uint4* g = reinterpret_cast<uint4*>(p + (i0 + r) * ld + j0 + c * EPC);
+          if constexpr (STORE) *g = *at(buf, r, c);
+          else *at(buf, r, c) = *g;
+        }
+      }
+    } else {
+      const int n = cols - j0 < W ? (int)(cols - j0) : W, m = rows - i0 < 32 ? (int)(rows - i0) : 32;
+      for (int r = 0; r < m; ++r)
+        for (int e = lane; e < n; e += 32) {
+          T* t = reinterpret_cast<T*>(at(buf, r, e / EPC)) + e % EPC;
+          T* g = p + (i0 + r) * ld + j0 + e;
+          if constexpr (STORE) *g = *t;
+          else *t = *g;
+        }
+    }
+  }
+};
 
 }  // namespace fxtx

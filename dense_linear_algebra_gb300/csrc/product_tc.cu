@@ -56,6 +56,7 @@ constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
 constexpr int A_BYTES = 128 * BK * 2;  // one plane of A in a stage
 constexpr int CHUNK = 4;               // stages a sum stays in tensor memory (float32)
+constexpr int TILE_BYTES = 4096;       // an epilogue warp's 32 rows x 128 bytes
 
 template <int CG, int BN, int PL, int KB>
 struct Cfg {  // stages in at most KB kilobytes
@@ -67,6 +68,13 @@ struct Cfg {  // stages in at most KB kilobytes
   static constexpr int TMEM_COLS = std::max(32, 2 * BN);
   static constexpr int COLS = BN / 2 >= 16 ? BN / 2 : 16;  // columns an epilogue thread takes
   static_assert(S >= 2 && BYTES <= 227 * 1024 && TMEM_COLS <= 512, "shared and tensor memory");
+};
+
+// The persistent kernel's stages, and the epilogue warps' rows.
+template <int CG, int BN, int PL>
+struct TileCfg : Cfg<CG, BN, PL, BN == 256 ? 191 : 192> {
+  static constexpr size_t BYTES = TileCfg::Cfg::BYTES + EPI_WARPS * TILE_BYTES;
+  static_assert(BYTES + 2 * BN * 4 + 512 <= 227 * 1024, "shared memory");
 };
 
 // The split kernel's stages, and room for a tile's partial sums: two CTAs a SM for tiles of
@@ -157,10 +165,11 @@ template <typename T, int CG, int BN, int PL>
 __global__ void __launch_bounds__(THREADS, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                       const __grid_constant__ TcArgs a) {
-  using C = Cfg<CG, BN, PL, 208>;
+  using C = TileCfg<CG, BN, PL>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
+  __shared__ float s_bias[2][BN];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   volatile int* abort_word = &s_abort;
@@ -254,37 +263,100 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
     const uint32_t te0 = CG == 2 ? cluster_addr(&tempty[0], 0) : smem_addr(&tempty[0]);
-    const Finish<T> fin(a.e, a.rows, a.cols);
-    int acc = 0;
+    unsigned char* buf = smem + (size_t)C::S * C::STAGE + (warp - 4) * TILE_BYTES;
+    const bool wide_out = Finish<T>::wide(a.e.out, a.e.ldo), wide_z = Finish<T>::wide(a.e.Z, a.e.ldz),
+               wide_r = Finish<T>::wide(a.e.R, a.e.ldr);
+    int acc = 0, turn = 0;
     bool ok = true;
-    for (int w = first; w < work && ok; w += step) {
+    // (after an abort a warp goes on to meet the others at each tile's barrier, and does nothing else)
+    for (int w = first; w < work; w += step, ++turn) {
       int l, c, k0, k1;
       place(w / a.splits, a.tiles_l, a.tiles_c, l, c);
       range(w, k0, k1);
-      const int64_t li = (int64_t)l * 128 * CG + rank * 128 + 32 * q + lane;  // the lane's row of the result
-      const int64_t ci = (int64_t)c * BN + half * C::COLS;                   // its first column
+      const int64_t i0 = (int64_t)l * 128 * CG + rank * 128 + 32 * q;  // the warp's first row of the result
+      const int64_t j0 = (int64_t)c * BN + half * C::COLS;            // and its first column
       float* part = a.splits > 1 ? a.part + (int64_t)(w % a.splits) * a.rows * a.cols : nullptr;
-      auto store = [&](int64_t col, const float* x) {
-        if (part) part_row(part, a.rows, a.cols, li, col, x);
-        else fin.template row<16>(li, col, x);
-      };
+      // the tile's biases, read while its products run (the buffers alternate, and all epilogue warps
+      // meet here once a tile)
+      float* bias = s_bias[turn & 1];
+      for (int e = tid - 128; e < BN; e += 32 * EPI_WARPS)
+        bias[e] = a.e.bias && !part && (int64_t)c * BN + e < a.cols ? to_f32(static_cast<const T*>(a.e.bias)[c * (int64_t)BN + e]) : 0.f;
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+      if (!ok) continue;
+      bias += half * C::COLS;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(te0 + (uint32_t)((acc & 1) * 8));
         ++acc;
       };
+      // the tile, W columns at a time: get(x, v) gives the lane's row's sums of columns x .. x + 15
+      auto finish = [&](auto get) {
+        if (part) {
+          constexpr int W = C::COLS < 32 ? C::COLS : 32;
+          const bool wide = a.cols % 4 == 0;
+#pragma unroll
+          for (int x = 0; x < C::COLS; x += W) {
+#pragma unroll
+            for (int y = 0; y < W; y += 16) {
+              float v[16];
+              get(x + y, v);
+              Tile32<float, W>::put(buf, y, v);
+            }
+            __syncwarp();
+            Tile32<float, W>::template move<true>(buf, part, a.cols, wide, i0, a.rows, j0 + x, a.cols);
+            __syncwarp();
+          }
+          return;
+        }
+        constexpr int W = C::COLS < 128 / (int)sizeof(T) ? C::COLS : 128 / (int)sizeof(T);
+        using Tile = Tile32<T, W>;
+#pragma unroll
+        for (int x = 0; x < C::COLS; x += W) {
+          if (a.e.Z) {
+#pragma unroll
+            for (int y = 0; y < W; y += 16) {
+              float v[16];
+              get(x + y, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] += bias[x + y + i];
+              Tile::put(buf, y, v);
+            }
+            __syncwarp();
+            Tile::template move<true>(buf, static_cast<T*>(a.e.Z), a.e.ldz, wide_z, i0, a.rows, j0 + x, a.cols);
+            __syncwarp();
+          }
+          if (a.e.R) {
+            Tile::template move<false>(buf, static_cast<T*>(const_cast<void*>(a.e.R)), a.e.ldr, wide_r, i0, a.rows, j0 + x,
+                                       a.cols);
+            __syncwarp();
+          }
+#pragma unroll
+          for (int y = 0; y < W; y += 16) {
+            float v[16];
+            get(x + y, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += bias[x + y + i];
+            with_act(a.e.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = act_of<decltype(act)::value>(v[i]);
+            });
+            if (a.e.R) Tile::add(buf, y, v);
+            Tile::put(buf, y, v);
+          }
+          __syncwarp();
+          Tile::template move<true>(buf, static_cast<T*>(a.e.out), a.e.ldo, wide_out, i0, a.rows, j0 + x, a.cols);
+          __syncwarp();
+        }
+      };
       if constexpr (PL == 1) {
-        if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
+        if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) continue;
         tc_fence_after();
         const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN);
-#pragma unroll 1
-        for (int x = 0; x < C::COLS; x += 16) {
-          float r[16];
-          tc_load16(t + (uint32_t)x, r);
+        finish([&](int x, float* v) {
+          tc_load16(t + (uint32_t)x, v);
           tc_wait_ld();
-          store(ci + x, r);
-        }
+        });
         release();
       } else {
         float sum[C::COLS];
@@ -296,9 +368,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           add_columns<C::COLS>(lane_base + (uint32_t)((acc & 1) * BN), sum);
           release();
         }
-        if (!ok) break;
+        if (ok)
+          finish([&](int x, float* v) {
 #pragma unroll
-        for (int x = 0; x < C::COLS; x += 16) store(ci + x, sum + x);
+            for (int i = 0; i < 16; ++i) v[i] = sum[x + i];
+          });
       }
     }
   }
@@ -477,24 +551,29 @@ __global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
   }
 }
 
-// out = the epilogue of the splits' sums, added in order.
+// out = the epilogue of the splits' sums, added in order: 4 neighbouring entries a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t rows, int64_t cols, int splits,
                                                    const float* part) {
   const Finish<T> fin(e, rows, cols);
-  const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
+  const int64_t groups = (cols + 3) / 4, stride = (int64_t)gridDim.x * 256;
+  const bool wide = cols % 4 == 0;
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride) {
-    const int64_t i = x / groups, j = x % groups * 16;
-    float c[16];
+    const int64_t i = x / groups, j = (x - i * groups) * 4;
+    const float* p = part + i * cols + j;
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s, p += rows * cols) {
+      if (wide) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        c[0] += v.x; c[1] += v.y; c[2] += v.z; c[3] += v.w;
+      } else {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) c[q] = 0.f;
-    for (int s = 0; s < splits; ++s) {
-      const float* p = part + ((int64_t)s * rows + i) * cols + j;
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        if (j + q < cols) c[q] += p[q];
+        for (int q = 0; q < 4; ++q)
+          if (j + q < cols) c[q] += p[q];
+      }
     }
-    fin.template row<16>(i, j, c);
+    fin.template row<4>(i, j, c);
   }
 }
 
@@ -522,7 +601,7 @@ cudaError_t launch_clustered(const void* k, size_t smem, unsigned grid, int clus
 template <typename T, int CG, int BN, int PL>
 cudaError_t launch(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, int sm_count, cudaStream_t st) {
   const int64_t work = (int64_t)a.tiles_l * a.tiles_c * a.splits;
-  return launch_clustered((const void*)product_tc_kernel<T, CG, BN, PL>, Cfg<CG, BN, PL, 208>::BYTES,
+  return launch_clustered((const void*)product_tc_kernel<T, CG, BN, PL>, TileCfg<CG, BN, PL>::BYTES,
                           (unsigned)(std::min<int64_t>(work, sm_count / CG) * CG), CG, am, bm, a, st);
 }
 
@@ -562,6 +641,8 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   a.kblocks = (int)((p.K + BK - 1) / BK);
   a.per_split = (a.kblocks + plan.splits - 1) / plan.splits;
   a.splits = (a.kblocks + a.per_split - 1) / a.per_split;  // none of them empty
+  // a cluster's CTAs share the tile's 128 lanes out evenly, and each has work
+  if (plan.cluster && (a.splits != plan.splits || 128 % a.splits != 0 || a.splits > 8)) return FXTX_ERR_UNSUPPORTED;
   a.a_mn = A.mn_major;
   a.b_mn = B.mn_major;
   a.idesc = mma_desc(bf16, A.mn_major, B.mn_major, 128 * plan.cg, plan.bn);
@@ -592,7 +673,12 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
         break;
     }
   } else if (plan.cg == 2) {
-    if constexpr (!F32) e = launch<T, 2, 256, PL>(am, bm, a, dev.sm_count, st);
+    switch (plan.bn) {
+      case 128: e = launch<T, 2, 128, PL>(am, bm, a, dev.sm_count, st); break;
+      case 256:
+        if constexpr (!F32) e = launch<T, 2, 256, PL>(am, bm, a, dev.sm_count, st);
+        break;
+    }
   } else {
     switch (plan.bn) {
       case 64: e = launch<T, 1, 64, PL>(am, bm, a, dev.sm_count, st); break;
@@ -601,7 +687,7 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   }
   if (a.part) {
     if (e == cudaSuccess) {
-      const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 15) / 16) + 255) / 256, (int64_t)dev.sm_count * 8);
+      const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 3) / 4) + 255) / 256, (int64_t)dev.sm_count * 8);
       join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(a.e, p.M, p.N, a.splits, a.part);
       e = cudaGetLastError();
     }

@@ -57,7 +57,7 @@ struct ThinArgs {
   void* DW;
   int64_t dws0, dws1;
   void* DB;
-  float* part;  // [ctas][n * k + k]
+  float* part;  // the CTAs' sums of dW and db, as their lanes hold them
 };
 
 template <typename T>
@@ -156,7 +156,15 @@ __device__ __forceinline__ bool chunk_wide(const T* p, int64_t ld) {
   return ((uintptr_t)p & (B - 1)) == 0 && ld * (int64_t)sizeof(T) % B == 0;
 }
 
-// A warp's 16 rows of a matrix, 4 KS entries of rows g and g + 8 a lane.
+// 4 KS neighbouring entries of rows g and g + 8 of a warp's 16: float32 as such, 16-bit types as the
+// pairs that the products take.
+template <typename T, int KS>
+struct Chunk {
+  static constexpr int W = sizeof(T) == 4 ? 4 * KS : 2 * KS;
+  using type = typename std::conditional<sizeof(T) == 4, float, uint32_t>::type;
+  type v[2][W];
+};
+
 template <typename T, int KS>
 struct Rows {
   const T* p;
@@ -167,12 +175,42 @@ struct Rows {
     const int t = threadIdx.x & 3;
     p = static_cast<const T*>(base) + 4 * KS * t;
     n = cols - 4 * KS * t;
-    wide = chunk_wide<T, 4 * KS>(static_cast<const T*>(base), pitch);
+    wide = n >= 4 * KS && chunk_wide<T, 4 * KS>(static_cast<const T*>(base), pitch);
   }
   __device__ __forceinline__ void load(int64_t r0, int64_t m, float (&x)[2][4 * KS]) const {
     const int64_t r = r0 + ((threadIdx.x & 31) >> 2);
     load_chunk<T, 4 * KS>(p + r * ld, r < m ? n : 0, wide, x[0]);
     load_chunk<T, 4 * KS>(p + (r + 8) * ld, r + 8 < m ? n : 0, wide, x[1]);
+  }
+  __device__ __forceinline__ void load(int64_t r0, int64_t m, Chunk<T, KS>& c) const {
+    if constexpr (sizeof(T) == 4) {
+      load(r0, m, c.v);
+    } else {
+      const int64_t r1 = r0 + ((threadIdx.x & 31) >> 2);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t r = r1 + 8 * h;
+        const T* q = p + r * ld;
+        const int k = r < m ? n : 0;
+        if (wide && k > 0) {
+          if constexpr (KS == 1) {
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(q));
+            c.v[h][0] = v.x; c.v[h][1] = v.y;
+          } else {
+#pragma unroll
+            for (int i = 0; i < KS / 2; ++i) {
+              const uint4 v = __ldcs(reinterpret_cast<const uint4*>(q) + i);
+              c.v[h][4 * i] = v.x; c.v[h][4 * i + 1] = v.y; c.v[h][4 * i + 2] = v.z; c.v[h][4 * i + 3] = v.w;
+            }
+          }
+        } else {
+          const uint16_t* u = reinterpret_cast<const uint16_t*>(q);
+#pragma unroll
+          for (int i = 0; i < 2 * KS; ++i)
+            c.v[h][i] = (2 * i < k ? (uint32_t)u[2 * i] : 0u) | (2 * i + 1 < k ? (uint32_t)u[2 * i + 1] << 16 : 0u);
+        }
+      }
+    }
   }
 };
 
@@ -188,6 +226,17 @@ __device__ __forceinline__ void fragments(const float (&x)[2][4 * KS], int s, ui
 #pragma unroll
       for (int q = 0; q < Term<T>::P; ++q) a[q][h + 2 * p] = r[q];
     }
+}
+template <typename T, int KS>
+__device__ __forceinline__ void fragments(const Chunk<T, KS>& x, int s, uint32_t (&a)[Term<T>::P][4]) {
+  if constexpr (sizeof(T) == 4) {
+    fragments<T, KS>(x.v, s, a);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) a[0][h + 2 * p] = x.v[h][2 * s + p];
+  }
 }
 
 // A matrix (16 KS rows of kk, 8 NT columns, entry (i, j) at p[i * s0 + j * s1], zero beyond rows x cols) as the
@@ -211,8 +260,8 @@ __device__ __forceinline__ void stage_operand(uint2* ws, const T* p, int64_t s0,
 }
 
 // 16 rows times the staged operand: 2 NT neighbouring results of rows g and g + 8 a lane.
-template <typename T, int KS, int NT>
-__device__ __forceinline__ void rows_times(const float (&x)[2][4 * KS], const uint2* ws, float (&out)[2][2 * NT]) {
+template <typename T, int KS, int NT, typename X>
+__device__ __forceinline__ void rows_times(const X& x, const uint2* ws, float (&out)[2][2 * NT]) {
   using S = typename Term<T>::type;
   using PR = Pairs<Term<T>::P>;
   constexpr int P = Term<T>::P;
@@ -249,15 +298,12 @@ __global__ void __launch_bounds__(THREADS) thin_kernel(const ThinArgs a) {
   const Rows<T, KS> rows(a.X, a.ldx, a.n);
   const Finish<T> fin(a.e, a.m, a.k);
   int64_t w = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-  float next[2][4 * KS];
+  Chunk<T, KS> next;
   rows.load(w * 16, a.m, next);
   __syncthreads();
   for (; w < tiles; w += step) {
-    float x[2][4 * KS], c[2][2 * NT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4 * KS; ++i) x[h][i] = next[h][i];
+    const Chunk<T, KS> x = next;
+    float c[2][2 * NT];
     rows.load((w + step) * 16, a.m, next);
     rows_times<T, KS, NT>(x, ws, c);
 #pragma unroll
@@ -272,7 +318,7 @@ __global__ void __launch_bounds__(THREADS) thin_grad_kernel(const ThinArgs a) {
   using PR = Pairs<Term<T>::P>;
   constexpr int P = Term<T>::P;
   __shared__ uint2 ws[DX ? KC * (2 * KN) * P * 32 : 1];
-  __shared__ float sums[DW ? 16 * KN * 16 * KC + 16 * KC : 1];
+  __shared__ float sums[DW ? WARPS / 2 * (KN * KC * 256 + 32 * 4 * KC) : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if constexpr (DX) stage_operand<T, KC, 2 * KN>(ws, static_cast<const T*>(a.W), a.ws1, a.ws0, a.k, a.n);
   __syncthreads();
@@ -287,7 +333,8 @@ __global__ void __launch_bounds__(THREADS) thin_grad_kernel(const ThinArgs a) {
 
   for (int64_t w = (int64_t)blockIdx.x * WARPS + warp; w < tiles; w += step) {
     const int64_t r = w * 16 + g;
-    float d[2][4 * KC], x[2][4 * KN];
+    float d[2][4 * KC];
+    Chunk<T, KN> x;
     gr.load(w * 16, a.m, d);
     if (DW && a.DW) xr.load(w * 16, a.m, x);
     with_act(a.act, [&](auto act) {
@@ -358,57 +405,66 @@ __global__ void __launch_bounds__(THREADS) thin_grad_kernel(const ThinArgs a) {
   }
 
   if constexpr (DW) {
-    // the warps' sums, in order, to this CTA's place
-    for (int y = 0; y < WARPS; ++y) {
-      __syncthreads();
-      if (warp != y) continue;
+    // the warps' sums to this CTA's place: the upper half of the warps added to the lower, in turn, as
+    // the lanes hold them ([register][lane])
+    constexpr int SIZE = KN * KC * 256 + 32 * 4 * KC;
+    float* part = a.part + (int64_t)blockIdx.x * SIZE;
 #pragma unroll
-      for (int s = 0; s < KN; ++s)
+    for (int half = WARPS / 2; half >= 0; half /= 2) {
+      if (half > 0 && warp >= half && warp < 2 * half) {
+        float* at = sums + (warp - half) * SIZE + lane;
 #pragma unroll
-        for (int c = 0; c < 2 * KC; ++c)
+        for (int e = 0; e < KN * KC * 8; ++e) at[e * 32] = acc[e / (8 * KC)][e / 4 % (2 * KC)][e % 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // row g (i < 2) or g + 8 of the block: entry 2 (i / 2) + g % 2 of lane g / 2's chunk, step s
-            const int j = 4 * KN * (g >> 1) + 4 * s + 2 * (i >> 1) + (g & 1);
-            const int o = 4 * KC * t + 4 * (c >> 1) + 2 * (c & 1) + (i & 1);
-            float* at = sums + j * 16 * KC + o;
-            *at = y == 0 ? acc[s][c][i] : *at + acc[s][c][i];
-          }
-#pragma unroll
-      for (int i = 0; i < 4 * KC; ++i) {
-        float v = db[i];
-        v += __shfl_xor_sync(FULL_MASK, v, 4);
-        v += __shfl_xor_sync(FULL_MASK, v, 8);
-        v += __shfl_xor_sync(FULL_MASK, v, 16);
-        float* at = sums + 16 * KN * 16 * KC + 4 * KC * t + i;
-        if (g == 0) *at = y == 0 ? v : *at + v;
+        for (int i = 0; i < 4 * KC; ++i) at[(KN * KC * 8 + i) * 32] = db[i];
       }
+      __syncthreads();
+      if (half > 0 ? warp < half : warp == 0) {
+        const float* at = sums + warp * SIZE + lane;
+#pragma unroll
+        for (int e = 0; e < KN * KC * 8; ++e) {
+          float& v = acc[e / (8 * KC)][e / 4 % (2 * KC)][e % 4];
+          if (half > 0) v += at[e * 32];
+          else part[e * 32 + lane] = v;
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * KC; ++i) {
+          if (half > 0) db[i] += at[(KN * KC * 8 + i) * 32];
+          else part[(KN * KC * 8 + i) * 32 + lane] = db[i];
+        }
+      }
+      if (half == 0) break;
+      __syncthreads();
     }
-    __syncthreads();
-    float* part = a.part + (int64_t)blockIdx.x * (a.n * a.k + a.k);
-    for (int e = threadIdx.x; e < a.n * a.k; e += THREADS) part[e] = sums[e / a.k * 16 * KC + e % a.k];
-    for (int e = threadIdx.x; e < a.k; e += THREADS) part[a.n * a.k + e] = sums[16 * KN * 16 * KC + e];
   }
 }
 
-// dW and db from the CTAs' sums: 8 entries a CTA, 32 threads an entry.
-template <typename T>
+// dW and db from the CTAs' sums: a CTA takes 32 registers' worth of one ([register][lane]), 8 threads a place.
+template <typename T, int KN, int KC>
 __global__ void __launch_bounds__(256) thin_join_kernel(const ThinArgs a, int parts) {
-  const int size = a.n * a.k + a.k;
-  const int e = blockIdx.x * 8 + (threadIdx.x & 7), y = threadIdx.x >> 3;
-  __shared__ float sum[32][9];
+  constexpr int SIZE = KN * KC * 256 + 32 * 4 * KC;
+  const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, reg = blockIdx.x;
+  __shared__ float sum[8][32];
   float s = 0.f;
-  if (e < size)
-#pragma unroll 4
-    for (int p = y; p < parts; p += 32) s += a.part[(int64_t)p * size + e];
-  sum[y][threadIdx.x & 7] = s;
+#pragma unroll 8
+  for (int p = y; p < parts; p += 8) s += a.part[(int64_t)p * SIZE + reg * 32 + lane];
+  sum[y][lane] = s;
   __syncthreads();
-  if (y != 0 || e >= size) return;
-  for (int q = 1; q < 32; ++q) s += sum[q][threadIdx.x & 7];
-  if (e < a.n * a.k) {
-    if (a.DW) static_cast<T*>(a.DW)[e / a.k * a.dws0 + e % a.k * a.dws1] = from_f32<T>(s);
-  } else if (a.DB) {
-    static_cast<T*>(a.DB)[e - a.n * a.k] = from_f32<T>(s);
+  if (y != 0) return;
+  for (int q = 1; q < 8; ++q) s += sum[q][lane];
+  const int g = lane >> 2, t = lane & 3;
+  if (reg < KN * KC * 8) {
+    // row g (i < 2) or g + 8 of block (st, c): entry 2 (i / 2) + g % 2 of lane g / 2's chunk, step st
+    const int st = reg / (8 * KC), c = reg / 4 % (2 * KC), i = reg % 4;
+    const int j = 4 * KN * (g >> 1) + 4 * st + 2 * (i >> 1) + (g & 1);
+    const int o = 4 * KC * t + 4 * (c >> 1) + 2 * (c & 1) + (i & 1);
+    if (a.DW && j < a.n && o < a.k) static_cast<T*>(a.DW)[j * a.dws0 + o * a.dws1] = from_f32<T>(s);
+  } else {
+    s += __shfl_xor_sync(FULL_MASK, s, 4);
+    s += __shfl_xor_sync(FULL_MASK, s, 8);
+    s += __shfl_xor_sync(FULL_MASK, s, 16);
+    const int o = 4 * KC * t + reg - KN * KC * 8;
+    if (a.DB && g == 0 && o < a.k) static_cast<T*>(a.DB)[o] = from_f32<T>(s);
   }
 }
 
@@ -432,16 +488,16 @@ cudaError_t launch_layer(const ThinArgs& a, int sm_count, cudaStream_t st) {
 template <typename T, int KN, int KC, bool DX, bool DW>
 fxtx_status_t launch_grad(ThinArgs a, int sm_count, cudaStream_t st) {
   const unsigned ctas = grid_of(thin_grad_kernel<T, KN, KC, DX, DW>, a.m, sm_count);
-  const int size = a.n * a.k + a.k;
+  constexpr int SIZE = KN * KC * 256 + 32 * 4 * KC;
   if (DW) {
-    const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)ctas * size * 4, st);
+    const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)ctas * SIZE * 4, st);
     if (s != FXTX_OK) return s;
   }
   thin_grad_kernel<T, KN, KC, DX, DW><<<ctas, THREADS, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (DW) {
     if (e == cudaSuccess) {
-      thin_join_kernel<T><<<(unsigned)((size + 7) / 8), 256, 0, st>>>(a, (int)ctas);
+      thin_join_kernel<T, KN, KC><<<SIZE / 32, 256, 0, st>>>(a, (int)ctas);
       e = cudaGetLastError();
     }
     cudaFreeAsync(a.part, st);
