@@ -84,7 +84,6 @@ fxtx_status_t run_empty(const Product& p, const DeviceInfo& dev, cudaStream_t st
 // take. On top come a fixed cost (launch, filling the pipeline, the last epilogue) and the exchange of
 // partial sums: between the CTAs of a cluster, or through memory and a second kernel.
 TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count) {
-  const int64_t kb = std::max<int64_t>(1, (K + 63) / 64);
   TcPlan best;
   double best_t = 1e300;
   const double floor = planes * 2.0 * K * (double)(M + N) / 3400.0;
@@ -94,8 +93,10 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
     const int64_t tiles = ((L + 128 * cg - 1) / (128 * cg)) * ((Cn + bn - 1) / bn);
     // CTAs (or pairs) at a time: two of the split kernel's narrow ones share an SM
     const int64_t units = cluster && planes == 1 && bn <= 64 ? 2 * sm_count : sm_count / cg;
-    const double mma = 4.0 * (planes == 3 ? 6 : 1) * std::max(64.0, bn / 2.0);
-    const double bytes = planes * (16384.0 + bn / cg * 128.0);
+    const int bk = planes == 1 && !cluster ? 128 : 64;  // kk a stage
+    const int64_t kb = std::max<int64_t>(1, (K + bk - 1) / bk);
+    const double mma = bk / 16 * (planes == 3 ? 6 : 1) * std::max(64.0, bn / 2.0);
+    const double bytes = planes * 2.0 * bk * (128.0 + bn / cg);
     const double stage = std::max(mma, bytes / (cluster ? 32.0 : 55.0)), epilogue = 400.0 + 12.0 * bn;
     auto price = [&](int64_t s) {
       const int64_t per = (kb + s - 1) / s;

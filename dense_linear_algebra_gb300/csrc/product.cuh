@@ -87,15 +87,15 @@ struct Finish {
   }
 };
 
-// A warp's 32 rows x up to 128 bytes on their way between the lanes, a row each, and memory, where
+// A warp's 32 rows x 64 bytes (2 KB) on their way between the lanes, a row each, and memory, where
 // 16-byte accesses of neighbouring lanes cover neighbouring bytes: row r's 16-byte chunk c lies at chunk
-// c ^ (r % 8) of its 128 bytes, so that both sides' accesses fall into distinct banks.
-template <typename T, int W>
+// c ^ (r / 2 % 4) of its 64 bytes, so that both sides' accesses fall into distinct banks.
+template <typename T>
 struct Tile32 {
-  static constexpr int EPC = 16 / sizeof(T), CH = W / EPC, ROWS = 32 / CH;  // entries a chunk, chunks a row, rows an access
-  static_assert(W * sizeof(T) <= 128 && W % 16 == 0, "a row is 32 to 128 bytes");
+  static constexpr int BYTES = 32 * 64;
+  static constexpr int W = 64 / sizeof(T), EPC = 16 / sizeof(T), CH = 4, ROWS = 8;  // entries a row and a chunk, chunks a row, rows an access
   __device__ __forceinline__ static uint4* at(unsigned char* buf, int r, int c) {
-    return reinterpret_cast<uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
+    return reinterpret_cast<uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
   }
   // 16 entries of the lane's own row from column x on
   __device__ __forceinline__ static void put(unsigned char* buf, int x, const float* v) {

@@ -2,7 +2,8 @@
 //     C_ij = sum_kk A(i, kk) B(j, kk),   out = act(C + bias_j) + R_ij.
 //
 // Roles of a CTA, linked by mbarriers only:
-//   warp 0      one lane: tensor copies of A and B, 64 of kk a stage, 128-byte swizzle;
+//   warp 0      one lane: tensor copies of A, 64 or 128 of kk a stage, 128-byte swizzle;
+//   warp 3      the same of B;
 //   warp 1      the products (tcgen05.mma, K = 16), one elected lane issuing; in a pair the
 //               first CTA issues for both, each holding its 128 rows of A and half of B;
 //   warps 4-11  the epilogue: a tile's sums from tensor memory (lane = row of the tile),
@@ -51,16 +52,17 @@
 namespace fxtx {
 namespace {
 
-constexpr int BK = 64;                 // kk a stage
+constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 32 * (4 + EPI_WARPS);
-constexpr int A_BYTES = 128 * BK * 2;  // one plane of A in a stage
-constexpr int CHUNK = 4;               // stages a sum stays in tensor memory (float32)
-constexpr int TILE_BYTES = 4096;       // an epilogue warp's 32 rows x 128 bytes
+constexpr int CHUNK = 4;          // stages a sum stays in tensor memory (float32)
 
-template <int CG, int BN, int PL, int KB>
-struct Cfg {  // stages in at most KB kilobytes
-  static constexpr int BROWS = BN / CG;  // B's entries a CTA holds
+// BK: kk a stage; KB: kilobytes the stages may take.
+template <int CG, int BN, int PL, int BK_, int KB>
+struct Cfg {
+  static constexpr int BK = BK_;
+  static constexpr int BROWS = BN / CG;            // B's entries a CTA holds
+  static constexpr int A_BYTES = 128 * BK * 2;     // one plane of A in a stage
   static constexpr int B_BYTES = BROWS * BK * 2;
   static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
   static constexpr int S = std::min(8, KB * 1024 / STAGE);
@@ -70,17 +72,19 @@ struct Cfg {  // stages in at most KB kilobytes
   static_assert(S >= 2 && BYTES <= 227 * 1024 && TMEM_COLS <= 512, "shared and tensor memory");
 };
 
-// The persistent kernel's stages, and the epilogue warps' rows.
+// The persistent kernel's stages, and the epilogue warps' rows. A 16-bit stage is 128 of kk: a turn
+// of the copying and of the issuing thread costs 300 to 400 cycles whatever it moves, more
+// than the 256 of a 64-wide stage's products.
 template <int CG, int BN, int PL>
-struct TileCfg : Cfg<CG, BN, PL, BN == 256 ? 191 : 192> {
-  static constexpr size_t BYTES = TileCfg::Cfg::BYTES + EPI_WARPS * TILE_BYTES;
+struct TileCfg : Cfg<CG, BN, PL, PL == 3 ? 64 : 128, 192> {
+  static constexpr size_t BYTES = TileCfg::Cfg::BYTES + EPI_WARPS * Tile32<float>::BYTES;
   static_assert(BYTES + 2 * BN * 4 + 512 <= 227 * 1024, "shared memory");
 };
 
 // The split kernel's stages, and room for a tile's partial sums: two CTAs a SM for tiles of
 // up to 64 columns of 16 bits, one of the others.
 template <int BN, int PL>
-struct SplitCfg : Cfg<1, BN, PL, PL == 3 ? 150 : (BN == 128 ? 128 : 80)> {
+struct SplitCfg : Cfg<1, BN, PL, 64, PL == 3 ? 150 : (BN == 128 ? 128 : 80)> {
   static constexpr int CTAS = PL == 1 && BN <= 64 ? 2 : 1;
   static constexpr int RED = 128 * (BN + 4) * 4;
   static constexpr size_t BYTES = SplitCfg::Cfg::BYTES + RED;
@@ -103,7 +107,8 @@ __device__ __forceinline__ void add_columns(uint32_t t, float* sum) {
 struct TcArgs {
   int64_t rows = 0, cols = 0;   // the result's
   int tiles_l = 0, tiles_c = 0;  // tiles along the lanes (A) and the columns (B) of a tile
-  int kblocks = 0, splits = 1, per_split = 0;
+  int kblocks = 0, splits = 1, per_split = 0;  // stages of kk
+  int ksteps = 0;                              // 16 of kk
   bool a_mn = false, b_mn = false;
   uint32_t idesc = 0;
   Epilogue e;
@@ -118,47 +123,83 @@ __device__ __forceinline__ void place(int t, int tl, int tc, int& l, int& c) {
   c = r / size;
 }
 
-// The tensor copies of stage `s`: kk from kb * BK on of the tile's rows of A (from ar) and B (from br).
-template <int CG, class C, int PL>
-__device__ __forceinline__ void load_stage(const CUtensorMap* amap, const CUtensorMap* bmap, const TcArgs& a,
-                                           unsigned char* st, int ar, int br, int kb, uint32_t bar) {
+// The tensor copies of one operand of a stage at `d`: kk from k on of its ROWS entries from r on. A
+// K-major operand lies in boxes of 64 of kk (ROWS rows of 128 bytes), an MN-major one in boxes of 64
+// entries (BK rows of 128 bytes).
+template <int CG, int PL, int BK, int ROWS>
+__device__ __forceinline__ void load_operand(const CUtensorMap* map, bool mn, uint32_t d, int r, int k, uint32_t bar) {
 #pragma unroll
-  for (int p = 0; p < PL; ++p) {
-    unsigned char* d = st + p * A_BYTES;
-    if (a.a_mn) {
-      tma_load_3d<CG>(d, amap, ar, kb * BK, p, bar);
-      tma_load_3d<CG>(d + BK * 128, amap, ar + 64, kb * BK, p, bar);
-    } else {
-      tma_load_3d<CG>(d, amap, kb * BK, ar, p, bar);
-    }
-    d = st + PL * A_BYTES + p * C::B_BYTES;
-    if (a.b_mn) {
+  for (int p = 0; p < PL; ++p, d += ROWS * BK * 2) {
+    if (mn) {
 #pragma unroll
-      for (int x = 0; x < C::BROWS / 64; ++x) tma_load_3d<CG>(d + x * BK * 128, bmap, br + 64 * x, kb * BK, p, bar);
+      for (int x = 0; x < ROWS / 64; ++x) tma_load_3d<CG>(d + x * BK * 128, map, r + 64 * x, k, p, bar);
     } else {
-      tma_load_3d<CG>(d, bmap, kb * BK, br, p, bar);
+#pragma unroll
+      for (int x = 0; x < BK / BX; ++x) tma_load_3d<CG>(d + x * ROWS * 128, map, k + BX * x, r, p, bar);
     }
   }
 }
 
-// The products of one stage into the accumulator at `d`; `fresh`: the first of a sum.
+// The products of one stage into the accumulator at `d`; `fresh`: the first of a sum; STEPS: the 16 of kk
+// that are inside the matrices, up to all of the stage's.
+template <int CG, class C, int PL, int STEPS>
+__device__ __forceinline__ void mma_steps(uint32_t d, uint64_t ad, uint64_t bd, const TcArgs& a, bool fresh) {
+  // K = 16 further: 32 bytes along a K-major row and the next box after 64, 16 rows of an MN-major
+  // operand (in 16-byte units)
+  const uint32_t as = a.a_mn ? 128 : 2, bs = a.b_mn ? 128 : 2;
+  const uint32_t ax = a.a_mn ? 512 : 128 * 8, bx = a.b_mn ? 512 : C::BROWS * 8;
+  // the planes' products, the smallest first
+  constexpr int N = PL == 3 ? 6 : 1, PA[6] = {PL == 3 ? 2 : 0, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+  for (int x = 0; x < N; ++x)
+#pragma unroll
+    for (int q = 0; q < STEPS; ++q)
+      mma_f16<CG>(d, ad + PA[x] * (C::A_BYTES >> 4) + (q % 4) * as + (q / 4) * ax,
+                  bd + PB[x] * (C::B_BYTES >> 4) + (q % 4) * bs + (q / 4) * bx, a.idesc, !fresh || x > 0 || q > 0);
+}
 template <int CG, class C, int PL>
-__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, const TcArgs& a, bool fresh) {
-  // K = 16 further: 32 bytes along a K-major row, 16 rows of an MN-major operand (16-byte units)
-  const uint64_t as = a.a_mn ? 128 : 2, bs = a.b_mn ? 128 : 2;
-  if constexpr (PL == 1) {
-#pragma unroll
-    for (int q = 0; q < BK / 16; ++q) mma_f16<CG>(d, ad + q * as, bd + q * bs, a.idesc, !fresh || q > 0);
-  } else {
-    // the planes' products, the smallest first
-    constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
-#pragma unroll
-    for (int x = 0; x < 6; ++x)
-#pragma unroll
-      for (int q = 0; q < BK / 16; ++q)
-        mma_f16<CG>(d, ad + PA[x] * (A_BYTES >> 4) + q * as, bd + PB[x] * (C::B_BYTES >> 4) + q * bs, a.idesc,
-                    !fresh || x > 0 || q > 0);
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, const TcArgs& a, bool fresh, int steps) {
+  constexpr int Q = C::BK / 16;
+  if (steps > Q / 2) mma_steps<CG, C, PL, Q>(d, ad, bd, a, fresh);
+  else if (steps > Q / 4) mma_steps<CG, C, PL, Q / 2>(d, ad, bd, a, fresh);
+  else mma_steps<CG, C, PL, Q / 4>(d, ad, bd, a, fresh);
+}
+
+// The loop of a CTA's products over a ring of stages: one lane's. `tile(k0, k1)` gives the next range of
+// stages of kk, false after the last.
+template <int CG, class C, int PL, typename F>
+__device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* smem, uint64_t* full, uint64_t* empty,
+                                               uint64_t* tfull, uint64_t* tempty, uint32_t tmem, int bn,
+                                               volatile int* abort_word, F tile) {
+  const uint64_t ad0 = swizzled_desc(smem_addr(smem), C::BK * 128, 1024);
+  const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * C::A_BYTES), C::BK * 128, 1024);
+  Ring<C::S> ring;
+  Ring<2> acc;
+  bool ready = false;  // the stage in turn was seen full while the last one's products were issued
+  int k0, k1;
+  while (tile(k0, k1)) {
+    int left = 0;  // stages of the sum in hand
+    for (int kb = k0; kb < k1; ++kb) {
+      const bool fresh = left == 0;
+      if (fresh) {
+        left = PL == 3 ? min(CHUNK, k1 - kb) : k1 - kb;
+        if (!tc_wait(&tempty[acc.s], acc.phase ^ 1u, abort_word)) return false;
+      }
+      if (!tc_wait(&full[ring.s], ring.phase, abort_word, ready)) return false;
+      const uint32_t s = ring.s;
+      ring.next();
+      ready = mbar_test(&full[ring.s], ring.phase);
+      tc_fence_after();
+      mma_stage<CG, C, PL>(tmem + acc.s * bn, ad0 + s * (uint32_t)(C::STAGE >> 4), bd0 + s * (uint32_t)(C::STAGE >> 4), a,
+                           fresh, a.ksteps - kb * (C::BK / 16));
+      mma_commit<CG>(&empty[s]);
+      if (--left == 0) {
+        mma_commit<CG>(&tfull[acc.s]);
+        acc.next();
+      }
+    }
   }
+  return true;
 }
 
 template <typename T, int CG, int BN, int PL>
@@ -205,65 +246,56 @@ __global__ void __launch_bounds__(THREADS, 1)
     k1 = min(a.kblocks, k0 + a.per_split);
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp == 0 || warp == 3) {
+    // warp 0 copies A, warp 3 B: one lane's turn takes longer than a narrow tile's products
+    if (elect_one()) {
+      Ring<C::S> ring;
       int it = 0;
       bool ok = true;
+      // a pair's copies all complete on its first CTA's barriers
+      const uint32_t full0 = CG == 2 ? cluster_addr(&full[0], 0) : smem_addr(&full[0]);
+      const uint32_t st0 = smem_addr(smem);
       for (int w = first; w < work && ok; w += step) {
         int l, c, k0, k1;
         place(w / a.splits, a.tiles_l, a.tiles_c, l, c);
         range(w, k0, k1);
         const int ar = l * 128 * CG + (int)rank * 128, br = c * BN + (int)rank * C::BROWS;
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const int s = it % C::S;
-          if (it >= C::S && !(ok = tc_wait(&empty[s], (uint32_t)((it / C::S - 1) & 1), abort_word))) break;
-          // a pair's copies all complete on its first CTA's barrier
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(CG * C::STAGE));
-          load_stage<CG, C, PL>(&amap, &bmap, a, smem + (size_t)s * C::STAGE, ar, br, kb,
-                                CG == 2 ? cluster_addr(&full[s], 0) : smem_addr(&full[s]));
+        for (int kb = k0; kb < k1; ++kb, ++it, ring.next()) {
+          // (the barriers start as if the stages had been emptied once)
+          if (!(ok = tc_wait(&empty[ring.s], ring.phase ^ 1u, abort_word))) break;
+          const uint32_t st = st0 + ring.s * C::STAGE;
+          if (warp == 0) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[ring.s], (uint32_t)(CG * C::STAGE));
+            load_operand<CG, PL, C::BK, 128>(&amap, a.a_mn, st, ar, kb * C::BK, full0 + ring.s * 8);
+          } else {
+            load_operand<CG, PL, C::BK, C::BROWS>(&bmap, a.b_mn, st + PL * C::A_BYTES, br, kb * C::BK, full0 + ring.s * 8);
+          }
         }
       }
       // copies still in flight after an abort land before the CTA leaves
       if (!ok && rank == 0)
         for (int j = it > C::S ? it - C::S : 0; j < it; ++j) mbar_wait_bounded(&full[j % C::S], (uint32_t)((j / C::S) & 1));
     }
+    __syncwarp();
   } else if (warp == 1) {
-    if (rank == 0) {
-      const bool leader = elect_one();
-      const uint64_t ad0 = swizzled_desc(smem_addr(smem), BK * 128, 1024);
-      const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * A_BYTES), BK * 128, 1024);
-      int it = 0, acc = 0;
-      bool ok = true;
-      for (int w = first; w < work && ok; w += step) {
-        int k0, k1;
+    if (rank == 0 && elect_one()) {
+      int w = first;
+      issue_products<CG, C, PL>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
+        if (w >= work) return false;
         range(w, k0, k1);
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const bool fresh = PL == 3 ? (kb - k0) % CHUNK == 0 : kb == k0;
-          const bool last = kb == k1 - 1 || (PL == 3 && (kb - k0) % CHUNK == CHUNK - 1);
-          if (fresh && acc >= 2 && !(ok = warp_wait(&tempty[acc & 1], (uint32_t)(((acc >> 1) - 1) & 1), abort_word))) break;
-          const int s = it % C::S;
-          if (!(ok = warp_wait(&full[s], (uint32_t)((it / C::S) & 1), abort_word))) break;
-          tc_fence_after();
-          if (leader) {
-            mma_stage<CG, C, PL>(tmem + (uint32_t)((acc & 1) * BN), ad0 + (uint64_t)(s * (C::STAGE >> 4)),
-                                 bd0 + (uint64_t)(s * (C::STAGE >> 4)), a, fresh);
-            mma_commit<CG>(&empty[s]);
-            if (last) mma_commit<CG>(&tfull[acc & 1]);
-          }
-          __syncwarp();
-          if (last) ++acc;
-        }
-      }
+        w += step;
+        return true;
+      });
       // every product has completed before the CTA leaves, after an abort too
-      if (leader) mma_commit<CG>(&fin_bar);
-      __syncwarp();
+      mma_commit<CG>(&fin_bar);
       mbar_wait_bounded(&fin_bar, 0);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
     const uint32_t te0 = CG == 2 ? cluster_addr(&tempty[0], 0) : smem_addr(&tempty[0]);
-    unsigned char* buf = smem + (size_t)C::S * C::STAGE + (warp - 4) * TILE_BYTES;
+    unsigned char* buf = smem + (size_t)C::S * C::STAGE + (warp - 4) * Tile32<T>::BYTES;
     const bool wide_out = Finish<T>::wide(a.e.out, a.e.ldo), wide_z = Finish<T>::wide(a.e.Z, a.e.ldz),
                wide_r = Finish<T>::wide(a.e.R, a.e.ldr);
     int acc = 0, turn = 0;
@@ -293,7 +325,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // the tile, W columns at a time: get(x, v) gives the lane's row's sums of columns x .. x + 15
       auto finish = [&](auto get) {
         if (part) {
-          constexpr int W = C::COLS < 32 ? C::COLS : 32;
+          constexpr int W = Tile32<float>::W;
           const bool wide = a.cols % 4 == 0;
 #pragma unroll
           for (int x = 0; x < C::COLS; x += W) {
@@ -301,16 +333,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int y = 0; y < W; y += 16) {
               float v[16];
               get(x + y, v);
-              Tile32<float, W>::put(buf, y, v);
+              Tile32<float>::put(buf, y, v);
             }
             __syncwarp();
-            Tile32<float, W>::template move<true>(buf, part, a.cols, wide, i0, a.rows, j0 + x, a.cols);
+            Tile32<float>::template move<true>(buf, part, a.cols, wide, i0, a.rows, j0 + x, a.cols);
             __syncwarp();
           }
           return;
         }
-        constexpr int W = C::COLS < 128 / (int)sizeof(T) ? C::COLS : 128 / (int)sizeof(T);
-        using Tile = Tile32<T, W>;
+        using Tile = Tile32<T>;
+        constexpr int W = Tile::W;
 #pragma unroll
         for (int x = 0; x < C::COLS; x += W) {
           if (a.e.Z) {
@@ -434,43 +466,40 @@ __global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
   bool ok = true;
   float sum[PL == 3 ? C::COLS : 1];
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp == 0 || warp == 3) {
+    if (elect_one()) {
+      const uint32_t st0 = smem_addr(smem);
+      Ring<C::S> ring;
       int it = 0;
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = it % C::S;
-        if (it >= C::S && !(ok = tc_wait(&empty[s], (uint32_t)((it / C::S - 1) & 1), abort_word))) break;
-        mbar_arrive_expect_tx(&full[s], (uint32_t)C::STAGE);
-        load_stage<1, C, PL>(&amap, &bmap, a, smem + (size_t)s * C::STAGE, l * 128, c * BN, kb, smem_addr(&full[s]));
+      for (int kb = k0; kb < k1; ++kb, ++it, ring.next()) {
+        if (!(ok = tc_wait(&empty[ring.s], ring.phase ^ 1u, abort_word))) break;
+        const uint32_t st = st0 + ring.s * C::STAGE;
+        if (warp == 0) {
+          mbar_arrive_expect_tx(&full[ring.s], (uint32_t)C::STAGE);
+          load_operand<1, PL, C::BK, 128>(&amap, a.a_mn, st, l * 128, kb * C::BK, smem_addr(&full[ring.s]));
+        } else {
+          load_operand<1, PL, C::BK, C::BROWS>(&bmap, a.b_mn, st + PL * C::A_BYTES, c * BN, kb * C::BK,
+                                               smem_addr(&full[ring.s]));
+        }
       }
       if (!ok)
         for (int j = it > C::S ? it - C::S : 0; j < it; ++j) mbar_wait_bounded(&full[j % C::S], (uint32_t)((j / C::S) & 1));
     }
     __syncwarp();
   } else if (warp == 1) {
-    const bool leader = elect_one();
-    const uint64_t ad0 = swizzled_desc(smem_addr(smem), BK * 128, 1024);
-    const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * A_BYTES), BK * 128, 1024);
-    int acc = 0, it = 0;
-    for (int kb = k0; kb < k1; ++kb, ++it) {
-      const bool fresh = PL == 3 ? it % CHUNK == 0 : it == 0;
-      const bool last = kb == k1 - 1 || (PL == 3 && it % CHUNK == CHUNK - 1);
-      if (fresh && acc >= 2 && !(ok = warp_wait(&tempty[acc & 1], (uint32_t)(((acc >> 1) - 1) & 1), abort_word))) break;
-      const int s = it % C::S;
-      if (!(ok = warp_wait(&full[s], (uint32_t)((it / C::S) & 1), abort_word))) break;
-      tc_fence_after();
-      if (leader) {
-        mma_stage<1, C, PL>(tmem + (uint32_t)((acc & 1) * BN), ad0 + (uint64_t)(s * (C::STAGE >> 4)),
-                            bd0 + (uint64_t)(s * (C::STAGE >> 4)), a, fresh);
-        mma_commit<1>(&empty[s]);
-        if (last) mma_commit<1>(&tfull[acc & 1]);
-      }
-      __syncwarp();
-      if (last) ++acc;
+    if (elect_one()) {
+      bool more = true;
+      ok = issue_products<1, C, PL>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
+        f0 = k0;
+        f1 = k1;
+        const bool m = more;
+        more = false;
+        return m;
+      });
+      mma_commit<1>(&fin_bar);
+      mbar_wait_bounded(&fin_bar, 0);
     }
-    if (leader) mma_commit<1>(&fin_bar);
     __syncwarp();
-    mbar_wait_bounded(&fin_bar, 0);
   } else if (warp >= 4) {
     // the sums into registers (float32), or up to their last product (16 bits)
     const int q = warp & 3, half = (warp - 4) >> 2;
@@ -611,11 +640,13 @@ cudaError_t launch_split(const CUtensorMap& am, const CUtensorMap& bm, const TcA
                           (unsigned)(a.tiles_l * a.tiles_c * a.splits), a.splits, am, bm, a, st);
 }
 
-// The map of an operand for boxes of 128 bytes x its tile's rows (or BK of them, MN-major).
-bool operand_map(CUtensorMap* map, const Planes& o, bool bf16, int box_rows) {
+// The map of an operand for boxes of 128 bytes x its tile's rows (or a stage's kk of them, MN-major).
+bool operand_map(CUtensorMap* map, const Planes& o, bool bf16, int box_rows, int bk) {
   return encode_planes_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, o.p, o.planes,
-                           o.rows, o.cols, o.pitch * 2, o.plane_stride * 2, o.mn_major ? BK : box_rows);
+                           o.rows, o.cols, o.pitch * 2, o.plane_stride * 2, o.mn_major ? bk : box_rows);
 }
+
+int stage_of(const TcPlan& plan, int planes) { return planes == 1 && !plan.cluster ? 128 : 64; }
 
 }  // namespace
 
@@ -638,7 +669,9 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   const int64_t L = plan.swap ? p.N : p.M, Cn = plan.swap ? p.M : p.N;
   a.tiles_l = (int)((L + 128 * plan.cg - 1) / (128 * plan.cg));
   a.tiles_c = (int)((Cn + plan.bn - 1) / plan.bn);
-  a.kblocks = (int)((p.K + BK - 1) / BK);
+  const int bk = stage_of(plan, PL);
+  a.kblocks = (int)((p.K + bk - 1) / bk);
+  a.ksteps = (int)((p.K + 15) / 16);
   a.per_split = (a.kblocks + plan.splits - 1) / plan.splits;
   a.splits = (a.kblocks + a.per_split - 1) / a.per_split;  // none of them empty
   // a cluster's CTAs share the tile's 128 lanes out evenly, and each has work
@@ -650,7 +683,7 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   CUtensorMap am, bm;
   memset(&am, 0, sizeof am);
   memset(&bm, 0, sizeof bm);
-  if (!operand_map(&am, A, bf16, 128) || !operand_map(&bm, B, bf16, plan.bn / plan.cg)) return FXTX_ERR_CUDA;
+  if (!operand_map(&am, A, bf16, 128, bk) || !operand_map(&bm, B, bf16, plan.bn / plan.cg, bk)) return FXTX_ERR_CUDA;
   if (!plan.cluster && a.splits > 1) {
     const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)a.splits * p.M * p.N * 4, st);
     if (s != FXTX_OK) return s;

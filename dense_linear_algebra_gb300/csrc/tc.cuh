@@ -92,17 +92,17 @@ __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sy
 // completing its box bytes on `bar`: a shared::cluster address, which for CG = 2 may lie in the
 // pair's other CTA. x * sizeof(element) must be a multiple of 16 bytes.
 template <int CG>
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
   if constexpr (CG == 1)
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
   else
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
@@ -134,9 +134,21 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// A ring of N stages: the stage in turn and the parity of its barriers' phase.
+template <int N>
+struct Ring {
+  uint32_t s = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 // Waits for phase `parity` of `bar`; gives up when another role has given up (the CTA's abort
 // word) or after WAIT_LIMIT polls (raising FXTX_ERR_TIMEOUT and setting the word).
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word) {
+__device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_word) {
   for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 63u && *abort_word) return false;
@@ -144,6 +156,22 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
   raise_error(FXTX_ERR_TIMEOUT);
   *abort_word = 1;
   return false;
+}
+// Whether phase `parity` of `bar` is over, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// `ready`: the outcome of an earlier poll.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word, bool ready = false) {
+  return ready || mbar_try_wait(bar, parity) || tc_wait_long(bar, parity, abort_word);
 }
 // A whole warp's wait: every lane waits, and all take the same branch after it.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_word) {
