@@ -104,6 +104,7 @@ template <typename P, typename G, int BITS, int N>
 __global__ void __launch_bounds__(WARPS * 32) adamw_kernel(const __grid_constant__ Table<N> tab, const AdamwConst c,
                                                            const int copy_type, const int per_warp) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  after_previous();
   int ti = -1;
   uint32_t lo = 0, hi = 0;  // the blocks of tensor ti
   for (int it = 0; it < per_warp; ++it) {
@@ -264,8 +265,7 @@ cudaError_t launch_n(int64_t count, const fxtx_adamw_tensor_t* t, int copy_type,
     const int64_t units = ((int64_t)blocks + WARPS - 1) / WARPS;
     const int per_warp = (int)std::min<int64_t>(4, std::max<int64_t>(1, units / ((int64_t)sm_count * 8)));
     const unsigned grid = (unsigned)((units + per_warp - 1) / per_warp);
-    adamw_kernel<P, G, BITS, N><<<grid, WARPS * 32, 0, st>>>(tab, c, copy_type, per_warp);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_kernel(adamw_kernel<P, G, BITS, N>, dim3(grid), WARPS * 32, 0, st, tab, c, copy_type, per_warp);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -300,6 +300,7 @@ cudaError_t launch_param(int64_t count, const fxtx_adamw_tensor_t* t, int g_type
 __global__ void __launch_bounds__(256) moments_kernel(int64_t n, const int8_t* m, const float* ms, const uint8_t* r,
                                                       const float* rs, float* m_out, float* v_out) {
   const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * PER;
+  after_previous();
   if (at >= n) return;
   const float a = ms[at / BLOCK], b = rs[at / BLOCK];
   const bool wide = at + PER <= n && (((uintptr_t)m | (uintptr_t)r) & 7u) == 0 &&
@@ -347,8 +348,7 @@ cudaError_t launch_adamw(int64_t count, const fxtx_adamw_tensor_t* t, int p_type
 cudaError_t launch_adamw_moments(int64_t n, const int8_t* m, const float* ms, const uint8_t* r, const float* rs,
                                  float* m_out, float* v_out, cudaStream_t st) {
   if (n <= 0) return cudaSuccess;
-  moments_kernel<<<(unsigned)((n + 2047) / 2048), 256, 0, st>>>(n, m, ms, r, rs, m_out, v_out);
-  return cudaGetLastError();
+  return launch_kernel(moments_kernel, dim3((unsigned)((n + 2047) / 2048)), 256, 0, st, n, m, ms, r, rs, m_out, v_out);
 }
 
 }  // namespace fxtx

@@ -16,6 +16,31 @@ inline int type_size(fxtx_type_t t) { return t == FXTX_F32 ? 4 : 2; }
 inline bool type_ok(int t) { return t >= FXTX_F32 && t <= FXTX_F16; }
 inline bool act_ok(int a) { return a >= FXTX_ACT_NONE && a <= FXTX_ACT_SIGMOID; }
 
+// The layer operators' kernels are launched so that each may start while the one before it on
+// the stream drains: its CTAs are set up as SMs come free, and wait in after_previous() until that
+// kernel has completed and its writes are seen. Every such kernel calls it, in all threads, before
+// its first access to global memory. A launch then costs what its work does, not also the two
+// microseconds between kernels (measured on calls of a few microseconds).
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // Widening is exact; narrowing rounds to nearest even, once.
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(const Epilogue e, int64_
   const Finish<T> fin(e, rows, cols);
   const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
   const float zero[16] = {};
+  after_previous();
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride)
     fin.template row<16>(x / groups, x % groups * 16, zero);
 }
@@ -70,8 +71,7 @@ fxtx_status_t pack(const Operand& o, fxtx_type_t type, const Planes& x, const De
 template <typename T>
 fxtx_status_t run_empty(const Product& p, const DeviceInfo& dev, cudaStream_t st) {
   const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 15) / 16) + 255) / 256, (int64_t)dev.sm_count * 8);
-  empty_sum_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(p.e, p.M, p.N);
-  return status_of(cudaGetLastError());
+  return status_of(launch_kernel(empty_sum_kernel<T>, dim3((unsigned)blocks), 256, 0, st, p.e, p.M, p.N));
 }
 
 }  // namespace

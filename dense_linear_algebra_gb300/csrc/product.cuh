@@ -119,6 +119,20 @@ struct Tile32 {
       for (int q = 0; q < EPC; ++q) v[c * EPC + q] += to_f32(t[q]);
     }
   }
+  // what move<false> would bring, held by the lanes on its way (wide rows only), and put down
+  __device__ __forceinline__ static void fetch(uint4 (&v)[CH], const T* p, int64_t ld, int64_t i0, int64_t rows, int64_t j0) {
+    const int lane = threadIdx.x & 31, c = lane % CH;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t r = i0 + k * ROWS + lane / CH;
+      v[k] = r < rows ? *reinterpret_cast<const uint4*>(p + r * ld + j0 + c * EPC) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ static void place(unsigned char* buf, const uint4 (&v)[CH]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) *at(buf, k * ROWS + lane / CH, lane % CH) = v[k];
+  }
   // rows i0 .. i0 + 31 and columns j0 .. j0 + W - 1 of a matrix of rows x cols to memory, or from it
   template <bool STORE>
   __device__ __forceinline__ static void move(unsigned char* buf, T* p, int64_t ld, bool wide, int64_t i0, int64_t rows,

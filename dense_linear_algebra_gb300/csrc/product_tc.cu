@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
-  __shared__ float s_bias[2][BN];
+  __shared__ __align__(16) float s_bias[2][BN];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   volatile int* abort_word = &s_abort;
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (CG == 2) cluster_sync();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
+  after_previous();
 
   const int tiles = a.tiles_l * a.tiles_c, work = tiles * a.splits;
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
@@ -322,90 +323,94 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(te0 + (uint32_t)((acc & 1) * 8));
         ++acc;
       };
-      // the tile, W columns at a time: get(x, v) gives the lane's row's sums of columns x .. x + 15
-      auto finish = [&](auto get) {
-        if (part) {
-          constexpr int W = Tile32<float>::W;
-          const bool wide = a.cols % 4 == 0;
-#pragma unroll
-          for (int x = 0; x < C::COLS; x += W) {
-#pragma unroll
-            for (int y = 0; y < W; y += 16) {
-              float v[16];
-              get(x + y, v);
-              Tile32<float>::put(buf, y, v);
-            }
-            __syncwarp();
-            Tile32<float>::template move<true>(buf, part, a.cols, wide, i0, a.rows, j0 + x, a.cols);
-            __syncwarp();
-          }
-          return;
-        }
-        using Tile = Tile32<T>;
-        constexpr int W = Tile::W;
-#pragma unroll
-        for (int x = 0; x < C::COLS; x += W) {
-          if (a.e.Z) {
-#pragma unroll
-            for (int y = 0; y < W; y += 16) {
-              float v[16];
-              get(x + y, v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] += bias[x + y + i];
-              Tile::put(buf, y, v);
-            }
-            __syncwarp();
-            Tile::template move<true>(buf, static_cast<T*>(a.e.Z), a.e.ldz, wide_z, i0, a.rows, j0 + x, a.cols);
-            __syncwarp();
-          }
-          if (a.e.R) {
-            Tile::template move<false>(buf, static_cast<T*>(const_cast<void*>(a.e.R)), a.e.ldr, wide_r, i0, a.rows, j0 + x,
-                                       a.cols);
-            __syncwarp();
-          }
-#pragma unroll
-          for (int y = 0; y < W; y += 16) {
-            float v[16];
-            get(x + y, v);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += bias[x + y + i];
-            with_act(a.e.act, [&](auto act) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = act_of<decltype(act)::value>(v[i]);
-            });
-            if (a.e.R) Tile::add(buf, y, v);
-            Tile::put(buf, y, v);
-          }
-          __syncwarp();
-          Tile::template move<true>(buf, static_cast<T*>(a.e.out), a.e.ldo, wide_out, i0, a.rows, j0 + x, a.cols);
-          __syncwarp();
-        }
-      };
+      using Tile = Tile32<T>;
+      const T* R = static_cast<const T*>(a.e.R);
+      // the residual's first rows are on their way while the products run
+      const bool ahead = R != nullptr && !part && wide_r && j0 + C::COLS <= a.cols;
+      uint4 next[Tile::CH];
+      if (ahead) Tile::fetch(next, R, a.e.ldr, i0, a.rows, j0);
+
+      uint32_t t = lane_base + (uint32_t)((acc & 1) * BN);
       if constexpr (PL == 1) {
         if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) continue;
         tc_fence_after();
-        const uint32_t t = lane_base + (uint32_t)((acc & 1) * BN);
-        finish([&](int x, float* v) {
-          tc_load16(t + (uint32_t)x, v);
-          tc_wait_ld();
-        });
-        release();
       } else {
         float sum[C::COLS];
 #pragma unroll
         for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
         for (int kb = k0; kb < k1; kb += CHUNK) {
+          if (kb > k0) release();
+          t = lane_base + (uint32_t)((acc & 1) * BN);
           if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
           tc_fence_after();
-          add_columns<C::COLS>(lane_base + (uint32_t)((acc & 1) * BN), sum);
-          release();
+          add_columns<C::COLS>(t, sum);
         }
-        if (ok)
-          finish([&](int x, float* v) {
+        if (!ok) continue;
+        // the sums go back to where the last of them came from: what follows reads them 16 columns at a time
+        // in a loop (unrolled over registers its code would not fit the instruction cache)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = sum[x + i];
-          });
+        for (int x = 0; x < C::COLS; x += 16) tc_store16(t + (uint32_t)x, sum + x);
+        tc_wait_st();
       }
+      // 16 sums of the lane's row from column x on, with their biases
+      auto get = [&](int x, float* v) {
+        tc_load16(t + (uint32_t)x, v);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(bias + x + i);
+          v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
+        }
+      };
+      if (part) {
+#pragma unroll 1
+        for (int x = 0; x < C::COLS; x += 16) {
+          float v[16];
+          get(x, v);
+          Tile32<float>::put(buf, 0, v);
+          __syncwarp();
+          Tile32<float>::template move<true>(buf, part, a.cols, a.cols % 4 == 0, i0, a.rows, j0 + x, a.cols);
+          __syncwarp();
+        }
+        release();
+        continue;
+      }
+#pragma unroll 1
+      for (int x = 0; x < C::COLS; x += Tile::W) {
+        if (a.e.Z) {
+#pragma unroll 1
+          for (int y = 0; y < Tile::W; y += 16) {
+            float v[16];
+            get(x + y, v);
+            Tile::put(buf, y, v);
+          }
+          __syncwarp();
+          Tile::template move<true>(buf, static_cast<T*>(a.e.Z), a.e.ldz, wide_z, i0, a.rows, j0 + x, a.cols);
+          __syncwarp();
+        }
+        if (ahead) {
+          Tile::place(buf, next);
+          if (x + Tile::W < C::COLS) Tile::fetch(next, R, a.e.ldr, i0, a.rows, j0 + x + Tile::W);
+        } else if (R) {
+          Tile::template move<false>(buf, const_cast<T*>(R), a.e.ldr, wide_r, i0, a.rows, j0 + x, a.cols);
+        }
+        if (R) __syncwarp();
+#pragma unroll 1
+        for (int y = 0; y < Tile::W; y += 16) {
+          float v[16];
+          get(x + y, v);
+          with_act(a.e.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = act_of<decltype(act)::value>(v[i]);
+          });
+          if (R) Tile::add(buf, y, v);
+          Tile::put(buf, y, v);
+        }
+        __syncwarp();
+        Tile::template move<true>(buf, static_cast<T*>(a.e.out), a.e.ldo, wide_out, i0, a.rows, j0 + x, a.cols);
+        __syncwarp();
+      }
+      release();
     }
   }
 
@@ -459,6 +464,7 @@ __global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
   tc_fence_after();
   cluster_arrive();  // waited for before the first store to another CTA
   const uint32_t tmem = s_tmem;
+  after_previous();
 
   int l, c;
   place((int)(blockIdx.x / (unsigned)R), a.tiles_l, a.tiles_c, l, c);
@@ -587,6 +593,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t row
   const Finish<T> fin(e, rows, cols);
   const int64_t groups = (cols + 3) / 4, stride = (int64_t)gridDim.x * 256;
   const bool wide = cols % 4 == 0;
+  after_previous();
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride) {
     const int64_t i = x / groups, j = (x - i * groups) * 4;
     const float* p = part + i * cols + j;
@@ -615,14 +622,14 @@ cudaError_t launch_clustered(const void* k, size_t smem, unsigned grid, int clus
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  if (cluster > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (see after_previous)
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   void* args[] = {const_cast<CUtensorMap*>(&am), const_cast<CUtensorMap*>(&bm), const_cast<TcArgs*>(&a)};
   return cudaLaunchKernelExC(&cfg, k, args);
 }
@@ -721,8 +728,7 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   if (a.part) {
     if (e == cudaSuccess) {
       const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 3) / 4) + 255) / 256, (int64_t)dev.sm_count * 8);
-      join_kernel<T><<<(unsigned)blocks, 256, 0, st>>>(a.e, p.M, p.N, a.splits, a.part);
-      e = cudaGetLastError();
+      e = launch_kernel(join_kernel<T>, dim3((unsigned)blocks), 256, 0, st, a.e, p.M, p.N, a.splits, a.part);
     }
     cudaFreeAsync(a.part, st);
   }

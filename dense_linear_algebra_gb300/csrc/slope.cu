@@ -70,6 +70,7 @@ __host__ __device__ inline bool rows_aligned(const void* p, int64_t ld, int size
 // cx: column groups of 8 a CTA takes, a power of two up to 32
 template <typename T>
 __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, const int cx, const int64_t rows_per_cta) {
+  after_previous();
   const int gx = threadIdx.x & (cx - 1), gy = threadIdx.x / cx, step = 256 / cx;
   const int64_t col = ((int64_t)blockIdx.x * cx + gx) * 8;
   const int64_t r1 = min(a.m, (int64_t)(blockIdx.y + 1) * rows_per_cta);
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(256) sums_kernel(const float* ws, int64_t part
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t j = (int64_t)blockIdx.x * 32 + x;
   float s = 0.f;
+  after_previous();
   if (j < k)
     for (int64_t r = y; r < parts; r += 8) s += ws[r * k + j];
   part[y][x] = s;
@@ -130,6 +132,7 @@ __global__ void __launch_bounds__(256) sums_kernel(const float* ws, int64_t part
 template <typename T>
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
   const int64_t groups = (a.cols + 7) / 8, stride = (int64_t)gridDim.x * 256;
+  after_previous();
   const bool aligned = rows_aligned(a.src, a.ld, sizeof(T));
   for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < a.rows * groups; x += stride) {
     const int64_t i = x / groups, j = x % groups * 8;
@@ -166,11 +169,9 @@ SlopeGrid slope_grid(int64_t m, int64_t k, int sm_count) {
 template <typename T>
 cudaError_t launch_t(const SlopeArgs& a, int sm_count, cudaStream_t st) {
   const SlopeGrid g = slope_grid(a.m, a.k, sm_count);
-  slope_kernel<T><<<dim3((unsigned)g.gx, (unsigned)g.gy), 256, 0, st>>>(a, g.cx, g.rows);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_kernel(slope_kernel<T>, dim3((unsigned)g.gx, (unsigned)g.gy), 256, 0, st, a, g.cx, g.rows);
   if (e != cudaSuccess || a.db == nullptr) return e;
-  sums_kernel<T><<<(unsigned)((a.k + 31) / 32), 256, 0, st>>>(a.ws, g.gy, a.k, static_cast<T*>(a.db));
-  return cudaGetLastError();
+  return launch_kernel(sums_kernel<T>, dim3((unsigned)((a.k + 31) / 32)), 256, 0, st, a.ws, g.gy, a.k, static_cast<T*>(a.db));
 }
 
 }  // namespace
@@ -179,11 +180,10 @@ cudaError_t launch_pack(const PackArgs& a, int sm_count, cudaStream_t st) {
   const int64_t blocks = std::min<int64_t>((a.rows * ((a.cols + 7) / 8) + 255) / 256, (int64_t)sm_count * 16);
   if (blocks == 0) return cudaSuccess;
   switch (a.type) {
-    case FXTX_F32: pack_kernel<float><<<(unsigned)blocks, 256, 0, st>>>(a); break;
-    case FXTX_BF16: pack_kernel<__nv_bfloat16><<<(unsigned)blocks, 256, 0, st>>>(a); break;
-    default: pack_kernel<__half><<<(unsigned)blocks, 256, 0, st>>>(a); break;
+    case FXTX_F32: return launch_kernel(pack_kernel<float>, dim3((unsigned)blocks), 256, 0, st, a);
+    case FXTX_BF16: return launch_kernel(pack_kernel<__nv_bfloat16>, dim3((unsigned)blocks), 256, 0, st, a);
+    default: return launch_kernel(pack_kernel<__half>, dim3((unsigned)blocks), 256, 0, st, a);
   }
-  return cudaGetLastError();
 }
 
 size_t slope_ws_bytes(int64_t m, int64_t k, int sm_count) {

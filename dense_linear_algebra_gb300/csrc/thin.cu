@@ -292,6 +292,7 @@ __device__ __forceinline__ void rows_times(const X& x, const uint2* ws, float (&
 template <typename T, int KS, int NT>
 __global__ void __launch_bounds__(THREADS) thin_kernel(const ThinArgs a) {
   __shared__ uint2 ws[KS * NT * Term<T>::P * 32];
+  after_previous();
   stage_operand<T, KS, NT>(ws, static_cast<const T*>(a.W), a.ws0, a.ws1, a.n, a.k);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int64_t tiles = (a.m + 15) / 16, step = (int64_t)gridDim.x * WARPS;
@@ -320,6 +321,7 @@ __global__ void __launch_bounds__(THREADS) thin_grad_kernel(const ThinArgs a) {
   __shared__ uint2 ws[DX ? KC * (2 * KN) * P * 32 : 1];
   __shared__ float sums[DW ? WARPS / 2 * (KN * KC * 256 + 32 * 4 * KC) : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  after_previous();
   if constexpr (DX) stage_operand<T, KC, 2 * KN>(ws, static_cast<const T*>(a.W), a.ws1, a.ws0, a.k, a.n);
   __syncthreads();
   const int64_t tiles = (a.m + 15) / 16, step = (int64_t)gridDim.x * WARPS;
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(256) thin_join_kernel(const ThinArgs a, int pa
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5, reg = blockIdx.x;
   __shared__ float sum[8][32];
   float s = 0.f;
+  after_previous();
 #pragma unroll 8
   for (int p = y; p < parts; p += 8) s += a.part[(int64_t)p * SIZE + reg * 32 + lane];
   sum[y][lane] = s;
@@ -481,8 +484,7 @@ unsigned grid_of(K* kernel, int64_t m, int sm_count) {
 
 template <typename T, int KS, int NT>
 cudaError_t launch_layer(const ThinArgs& a, int sm_count, cudaStream_t st) {
-  thin_kernel<T, KS, NT><<<grid_of(thin_kernel<T, KS, NT>, a.m, sm_count), THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_kernel(thin_kernel<T, KS, NT>, dim3(grid_of(thin_kernel<T, KS, NT>, a.m, sm_count)), THREADS, 0, st, a);
 }
 
 template <typename T, int KN, int KC, bool DX, bool DW>
@@ -493,12 +495,10 @@ fxtx_status_t launch_grad(ThinArgs a, int sm_count, cudaStream_t st) {
     const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)ctas * SIZE * 4, st);
     if (s != FXTX_OK) return s;
   }
-  thin_grad_kernel<T, KN, KC, DX, DW><<<ctas, THREADS, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_kernel(thin_grad_kernel<T, KN, KC, DX, DW>, dim3(ctas), THREADS, 0, st, a);
   if (DW) {
     if (e == cudaSuccess) {
-      thin_join_kernel<T, KN, KC><<<SIZE / 32, 256, 0, st>>>(a, (int)ctas);
-      e = cudaGetLastError();
+      e = launch_kernel(thin_join_kernel<T, KN, KC>, dim3(SIZE / 32), 256, 0, st, a, (int)ctas);
     }
     cudaFreeAsync(a.part, st);
   }
