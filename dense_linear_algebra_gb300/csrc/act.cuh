@@ -1,10 +1,10 @@
 // act.cuh — the activations and their slopes, in fp32.
 //
 // They are evaluated for every entry of a result, in epilogues that have few warps to hide
-// them, so the forms are the cheapest that keep fp32 accuracy: exp by __expf, whose error is
-// about 1.2 |x| + 2 units in the last place of the exponential, one approximate reciprocal (2
-// units), and no difference of nearly equal terms. With expf, erff, tanhf and IEEE division
-// a tall layer (1,000,000 x 32, 32 outputs, silu) spent half of its time here.
+// them, so the forms are the cheapest that keep fp32 accuracy: one ex2.approx (the exponential is
+// then off by about 1.2 |x| + 2 units in its last place), one rcp.approx (1 unit), both with
+// subnormal numbers taken as zero, and no difference of nearly equal terms. With expf, erff, tanhf
+// and IEEE division a tall layer (1,000,000 x 32, 32 outputs, silu) spent half of its time here.
 //   gelu       the complementary error function q of |z| / sqrt(2) by Abramowitz and Stegun 7.1.26
 //              (absolute error 1.5e-7): z (1 - q / 2) for z >= 0, z q / 2 below; its
 //              exponential exp(-z^2 / 2) is the slope's too
@@ -23,12 +23,24 @@ constexpr float kRootTwoPi = 0.39894228040143267794f;  // 1 / sqrt(2 pi)
 constexpr float kTanh0 = 1.59576912160573071176f;      // 2 sqrt(2 / pi)
 constexpr float kTanh1 = 0.044715f;
 
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-kLog2e * z)); }
 
 // erfc(|z| / sqrt(2)) and exp(-z^2 / 2).
 __device__ __forceinline__ float erfc_half(float z, float& gauss) {
-  const float t = __fdividef(1.f, fmaf(0.3275911f * kRootHalf, fabsf(z), 1.f));
-  gauss = __expf(-0.5f * z * z);
+  const float t = rcp(fmaf(0.3275911f * kRootHalf, fabsf(z), 1.f));
+  gauss = ex2(-0.5f * kLog2e * z * z);
   float p = fmaf(1.061405429f, t, -1.453152027f);
   p = fmaf(p, t, 1.421413741f);
   p = fmaf(p, t, -0.284496736f);

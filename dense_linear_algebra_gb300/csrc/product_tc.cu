@@ -6,8 +6,8 @@
 //   warp 3      the same of B;
 //   warp 1      the products (tcgen05.mma, K = 16), one elected lane issuing; in a pair the
 //               first CTA issues for both, each holding its 128 rows of A and half of B;
-//   warps 4-11  the epilogue: a tile's sums from tensor memory (lane = row of the tile),
-//               two warps a quarter of the lanes, each half of the columns.
+//   warps 4 on  the epilogue: a tile's sums from tensor memory (lane = row of the tile), two
+//               or four warps a quarter of the lanes, each a part of the columns.
 //
 // Two kernels share them.
 //   product_tc_kernel     many tiles: one persistent CTA a SM, or a pair of CTAs over two SMs
@@ -53,8 +53,8 @@ namespace fxtx {
 namespace {
 
 constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 32 * (4 + EPI_WARPS);
+constexpr int SPLIT_EPI = 8;      // epilogue warps of the split kernel
+constexpr int SPLIT_THREADS = 32 * (4 + SPLIT_EPI);
 constexpr int CHUNK = 4;          // stages a sum stays in tensor memory (float32)
 
 // BK: kk a stage; KB: kilobytes the stages may take.
@@ -68,7 +68,7 @@ struct Cfg {
   static constexpr int S = std::min(8, KB * 1024 / STAGE);
   static constexpr size_t BYTES = (size_t)S * STAGE + 1024;
   static constexpr int TMEM_COLS = std::max(32, 2 * BN);
-  static constexpr int COLS = BN / 2 >= 16 ? BN / 2 : 16;  // columns an epilogue thread takes
+  static constexpr int COLS = BN / 2 >= 16 ? BN / 2 : 16;  // columns an epilogue thread of the split kernel takes
   static_assert(S >= 2 && BYTES <= 227 * 1024 && TMEM_COLS <= 512, "shared and tensor memory");
 };
 
@@ -77,7 +77,11 @@ struct Cfg {
 // than the 256 of a 64-wide stage's products.
 template <int CG, int BN, int PL>
 struct TileCfg : Cfg<CG, BN, PL, PL == 3 ? 64 : 128, 192> {
-  static constexpr size_t BYTES = TileCfg::Cfg::BYTES + EPI_WARPS * Tile32<float>::BYTES;
+  // Epilogue warps: few are slow to finish a tile, for the latencies of the exponentials and of the stores (a
+  // 128 x 128 tile with silu took 7,600 cycles with eight); 256 columns leave the memory for eight.
+  static constexpr int EPI = BN == 256 ? 8 : 16, THREADS = 32 * (4 + EPI);
+  static constexpr int COLS = std::max(32, BN / (EPI / 4));  // columns a thread takes
+  static constexpr size_t BYTES = TileCfg::Cfg::BYTES + EPI * Tile32<float>::BYTES;
   static_assert(BYTES + 2 * BN * 4 + 512 <= 227 * 1024, "shared memory");
 };
 
@@ -203,7 +207,7 @@ __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* s
 }
 
 template <typename T, int CG, int BN, int PL>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                       const __grid_constant__ TcArgs a) {
   using C = TileCfg<CG, BN, PL>;
@@ -225,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], EPI_WARPS * CG);
+      mbar_init(&tempty[s], C::EPI * CG);
     }
     mbar_init(&fin_bar, 1);
     fence_mbar_init();
@@ -293,8 +297,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
+    const int q = warp & 3, group = (warp - 4) >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(group * C::COLS);
     const uint32_t te0 = CG == 2 ? cluster_addr(&tempty[0], 0) : smem_addr(&tempty[0]);
     unsigned char* buf = smem + (size_t)C::S * C::STAGE + (warp - 4) * Tile32<T>::BYTES;
     const bool wide_out = Finish<T>::wide(a.e.out, a.e.ldo), wide_z = Finish<T>::wide(a.e.Z, a.e.ldz),
@@ -307,16 +311,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       place(w / a.splits, a.tiles_l, a.tiles_c, l, c);
       range(w, k0, k1);
       const int64_t i0 = (int64_t)l * 128 * CG + rank * 128 + 32 * q;  // the warp's first row of the result
-      const int64_t j0 = (int64_t)c * BN + half * C::COLS;            // and its first column
+      const int64_t j0 = (int64_t)c * BN + group * C::COLS;            // and its first column
       float* part = a.splits > 1 ? a.part + (int64_t)(w % a.splits) * a.rows * a.cols : nullptr;
       // the tile's biases, read while its products run (the buffers alternate, and all epilogue warps
       // meet here once a tile)
       float* bias = s_bias[turn & 1];
-      for (int e = tid - 128; e < BN; e += 32 * EPI_WARPS)
+      for (int e = tid - 128; e < BN; e += 32 * C::EPI)
         bias[e] = a.e.bias && !part && (int64_t)c * BN + e < a.cols ? to_f32(static_cast<const T*>(a.e.bias)[c * (int64_t)BN + e]) : 0.f;
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * C::EPI) : "memory");
       if (!ok) continue;
-      bias += half * C::COLS;
+      if (group * C::COLS >= BN) {  // a narrow tile's spare warps only give its accumulators back
+        for (int kb = k0; kb < k1; kb += PL == 3 ? CHUNK : k1 - k0) {
+          if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(te0 + (uint32_t)((acc & 1) * 8));
+          ++acc;
+        }
+        continue;
+      }
+      bias += group * C::COLS;
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -431,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // CTA stores its partial sums of those lanes to r's shared memory (after the stages, which r
 // may still be reading), one cluster barrier, and r adds the R parts in order.
 template <typename T, int BN, int PL, bool SWAP>
-__global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
+__global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
     product_split_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                          const __grid_constant__ TcArgs a) {
   using C = SplitCfg<BN, PL>;
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
-      mbar_init(&tempty[s], EPI_WARPS);
+      mbar_init(&tempty[s], SPLIT_EPI);
     }
     mbar_init(&fin_bar, 1);
     fence_mbar_init();
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, SplitCfg<BN, PL>::CTAS)
 
   const Finish<T> fin(a.e, a.rows, a.cols);
   const int groups = SWAP ? share / 4 : BN / 4, units = SWAP ? BN * groups : share * groups;
-  for (int u = tid; u < units; u += THREADS) {
+  for (int u = tid; u < units; u += SPLIT_THREADS) {
     const int y = u / groups, x = u % groups * 4;
     const int64_t i = SWAP ? (int64_t)c * BN + y : (int64_t)l * 128 + rank * share + y;
     const int64_t j = SWAP ? (int64_t)l * 128 + rank * share + x : (int64_t)c * BN + x;
@@ -613,13 +626,13 @@ __global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t row
   }
 }
 
-cudaError_t launch_clustered(const void* k, size_t smem, unsigned grid, int cluster, const CUtensorMap& am,
+cudaError_t launch_clustered(const void* k, size_t smem, unsigned grid, int threads, int cluster, const CUtensorMap& am,
                              const CUtensorMap& bm, const TcArgs& a, cudaStream_t st) {
   cudaError_t e = ensure_smem(k, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -638,13 +651,13 @@ template <typename T, int CG, int BN, int PL>
 cudaError_t launch(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, int sm_count, cudaStream_t st) {
   const int64_t work = (int64_t)a.tiles_l * a.tiles_c * a.splits;
   return launch_clustered((const void*)product_tc_kernel<T, CG, BN, PL>, TileCfg<CG, BN, PL>::BYTES,
-                          (unsigned)(std::min<int64_t>(work, sm_count / CG) * CG), CG, am, bm, a, st);
+                          (unsigned)(std::min<int64_t>(work, sm_count / CG) * CG), TileCfg<CG, BN, PL>::THREADS, CG, am, bm, a, st);
 }
 
 template <typename T, int BN, int PL, bool SWAP>
 cudaError_t launch_split(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, cudaStream_t st) {
   return launch_clustered((const void*)product_split_kernel<T, BN, PL, SWAP>, SplitCfg<BN, PL>::BYTES,
-                          (unsigned)(a.tiles_l * a.tiles_c * a.splits), a.splits, am, bm, a, st);
+                          (unsigned)(a.tiles_l * a.tiles_c * a.splits), SPLIT_THREADS, a.splits, am, bm, a, st);
 }
 
 // The map of an operand for boxes of 128 bytes x its tile's rows (or a stage's kk of them, MN-major).
