@@ -51,14 +51,8 @@ fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, con
   l.e.R = R; l.e.ldr = ldr;
   l.e.Z = Z; l.e.ldz = ldz;
   l.e.out = OUT; l.e.ldo = ldo;
-  if (thin_shape(n, k)) return run_thin_linear(l, *dev, static_cast<cudaStream_t>(stream));
-  Product p;
-  p.type = type;
-  p.M = m; p.N = k; p.K = n;
-  p.A.p = X; p.A.ld = ldx;
-  p.B.p = W; p.B.ld = ldw; p.B.mn_major = !w_trans;
-  p.e = l.e;
-  return run_product(p, *dev, static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return thin_shape(n, k) ? run_thin_linear(l, *dev, st) : run_linear(l, *dev, st);
 }
 
 fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* G, int64_t ldg,
@@ -72,76 +66,22 @@ fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k
   if (DW && (!rows_ok(X, m, n, ldx) || lddw < (w_trans ? n : k))) return FXTX_ERR_INVALID_ARG;
   if ((n == 0 || (!DX && !DW)) && (!DB || k == 0)) return FXTX_OK;
   const DeviceInfo* dev = nullptr;
-  fxtx_status_t s = current_device(&dev);
+  const fxtx_status_t s = current_device(&dev);
   if (s != FXTX_OK) return s;
+  LayerArgs l;
+  l.type = type;
+  l.m = m; l.n = n; l.k = k;
+  l.X = X; l.ldx = ldx;
+  l.W = W; l.ldw = ldw; l.w_trans = w_trans != 0;
+  GradArgs g;
+  g.G = G; g.ldg = ldg;
+  g.Z = Z; g.ldz = ldz;
+  g.act = act;
+  g.DX = DX; g.lddx = lddx;
+  g.DW = DW; g.lddw = lddw;
+  g.DB = DB;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-
-  if (m > 0 && thin_shape(n, k)) {
-    LayerArgs l;
-    l.type = type;
-    l.m = m; l.n = n; l.k = k;
-    l.X = X; l.ldx = ldx;
-    l.W = W; l.ldw = ldw; l.w_trans = w_trans != 0;
-    GradArgs g;
-    g.G = G; g.ldg = ldg;
-    g.Z = Z; g.ldz = ldz;
-    g.act = act;
-    g.DX = DX; g.lddx = lddx;
-    g.DW = DW; g.lddw = lddw;
-    g.DB = DB;
-    return run_thin_grad(l, g, *dev, st);
-  }
-  const bool products = n > 0 && (DX || DW) && m > 0 && k > 0;
-  SlopeArgs a;
-  a.type = type;
-  a.m = m; a.k = k;
-  a.G = G; a.ldg = ldg;
-  a.Z = Z; a.ldz = ldz;
-  a.act = act;
-  a.db = k > 0 ? DB : nullptr;
-  void* ws = nullptr;
-  // D is G itself where there is nothing to multiply and the products can read G where it lies
-  const bool as_is = act == FXTX_ACT_NONE && type != FXTX_F32 && ((uintptr_t)G & 15u) == 0 && ldg % 8 == 0;
-  const int64_t pitch = (k + 7) / 8 * 8, planes = type == FXTX_F32 ? 3 : 1;
-  const size_t d_bytes = products && !as_is ? ((size_t)planes * m * pitch * 2 + 255) / 256 * 256 : 0;
-  const size_t sum_bytes = a.db ? slope_ws_bytes(m, k, dev->sm_count) : 0;
-  s = alloc_pooled(&ws, d_bytes + sum_bytes, st);
-  if (s != FXTX_OK) return s;
-  a.ws = reinterpret_cast<float*>(static_cast<char*>(ws) + d_bytes);
-  if (d_bytes) {
-    a.D = ws;
-    a.ldd = pitch;
-    a.d_planes = m * pitch;
-  }
-  if (a.D || a.db) s = status_of(launch_slope(a, dev->sm_count, st));
-
-  Operand D;
-  D.p = a.D ? a.D : G;
-  D.ld = a.D ? a.ldd : ldg;
-  D.plane_stride = a.D && type == FXTX_F32 ? a.d_planes : 0;
-  if (s == FXTX_OK && DX && m > 0 && n > 0) {
-    Product p;
-    p.type = type;
-    p.M = m; p.N = n; p.K = k;
-    p.A = D;
-    p.B.p = W; p.B.ld = ldw; p.B.mn_major = w_trans;
-    p.e.out = DX; p.e.ldo = lddx;
-    s = run_product(p, *dev, st);
-  }
-  if (s == FXTX_OK && DW && n > 0 && k > 0) {
-    Operand x;
-    x.p = X; x.ld = ldx; x.mn_major = true;
-    D.mn_major = true;
-    Product p;
-    p.type = type;
-    p.M = w_trans ? k : n; p.N = w_trans ? n : k; p.K = m;
-    p.A = w_trans ? D : x;
-    p.B = w_trans ? x : D;
-    p.e.out = DW; p.e.ldo = lddw;
-    s = run_product(p, *dev, st);
-  }
-  if (ws) cudaFreeAsync(ws, st);
-  return s;
+  return m > 0 && thin_shape(n, k) ? run_thin_grad(l, g, *dev, st) : run_grad(l, g, *dev, st);
 }
 
 fxtx_status_t fxtx_adamw(int64_t count, const fxtx_adamw_tensor_t* tensors, fxtx_type_t p_type, fxtx_type_t g_type,

@@ -1,7 +1,7 @@
-// linear.cu — the product behind the linear layer and its gradient,
+// linear.cu — the linear layer and its gradient as products on the tensor cores,
 //     C_ij = sum_kk A(i, kk) B(j, kk),   out = act(C + bias_j) + R_ij:
-// its operands brought into the form that the tensor copies read, and its layout over the
-// tensor cores (plan_product).
+// operands brought into the form that the tensor copies read, where they are not in it, and
+// each product's layout over the tensor cores (plan_product).
 #include <algorithm>
 #include <cmath>
 
@@ -55,23 +55,58 @@ Planes planes_of(const Operand& o, fxtx_type_t type, int64_t mn, int64_t k, char
   return x;
 }
 
-fxtx_status_t pack(const Operand& o, fxtx_type_t type, const Planes& x, const DeviceInfo& dev, cudaStream_t st) {
-  PackArgs a;
-  a.type = type;
-  a.src = o.p;
-  a.rows = x.rows;
-  a.cols = x.cols;
-  a.ld = o.ld;
-  a.dst = const_cast<void*>(x.p);
-  a.pitch = x.pitch;
-  a.plane_stride = x.plane_stride;
-  return status_of(launch_pack(a, dev.sm_count, st));
+// Up to three operands and what has to be copied for them, in one workspace.
+struct Prepared {
+  fxtx_type_t type;
+  PackArgs packs[2];
+  int count = 0;
+  size_t bytes = 0;
+  size_t at[2];        // the copies' places in the workspace
+  Planes* of[2];       // and whose they are
+
+  Planes add(const Operand& o, int64_t mn, int64_t k, Planes* slot) {
+    size_t need = 0;
+    *slot = planes_of(o, type, mn, k, nullptr, &need);
+    if (need) {
+      PackArgs& a = packs[count];
+      a.src = o.p;
+      a.rows = slot->rows;
+      a.cols = slot->cols;
+      a.ld = o.ld;
+      a.pitch = slot->pitch;
+      a.plane_stride = slot->plane_stride;
+      at[count] = bytes;
+      of[count++] = slot;
+      bytes += need;
+    }
+    return *slot;
+  }
+  // once the workspace is there
+  void place(char* ws) {
+    for (int i = 0; i < count; ++i) of[i]->p = packs[i].dst = ws + at[i];
+  }
+};
+
+fxtx_status_t run_typed(fxtx_type_t type, const PlanesProduct& q, const DeviceInfo& dev, cudaStream_t st) {
+  switch (type) {
+    case FXTX_F32: return run_planes<float>(q, dev, st);
+    case FXTX_BF16: return run_planes<__nv_bfloat16>(q, dev, st);
+    default: return run_planes<__half>(q, dev, st);
+  }
 }
 
 template <typename T>
-fxtx_status_t run_empty(const Product& p, const DeviceInfo& dev, cudaStream_t st) {
-  const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 15) / 16) + 255) / 256, (int64_t)dev.sm_count * 8);
-  return status_of(launch_kernel(empty_sum_kernel<T>, dim3((unsigned)blocks), 256, 0, st, p.e, p.M, p.N));
+cudaError_t empty_t(const Epilogue& e, int64_t rows, int64_t cols, const DeviceInfo& dev, cudaStream_t st) {
+  const int64_t blocks = std::min<int64_t>((rows * ((cols + 15) / 16) + 255) / 256, (int64_t)dev.sm_count * 8);
+  return launch_kernel(empty_sum_kernel<T>, dim3((unsigned)blocks), 256, 0, st, e, rows, cols);
+}
+fxtx_status_t run_empty(fxtx_type_t type, const Epilogue& e, int64_t rows, int64_t cols, const DeviceInfo& dev,
+                        cudaStream_t st) {
+  switch (type) {
+    case FXTX_F32: return status_of(empty_t<float>(e, rows, cols, dev, st));
+    case FXTX_BF16: return status_of(empty_t<__nv_bfloat16>(e, rows, cols, dev, st));
+    default: return status_of(empty_t<__half>(e, rows, cols, dev, st));
+  }
 }
 
 }  // namespace
@@ -136,35 +171,106 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
   return best;
 }
 
-fxtx_status_t run_product(const Product& p, const DeviceInfo& dev, cudaStream_t st) {
-  if (p.K == 0) {
-    switch (p.type) {
-      case FXTX_F32: return run_empty<float>(p, dev, st);
-      case FXTX_BF16: return run_empty<__nv_bfloat16>(p, dev, st);
-      default: return run_empty<__half>(p, dev, st);
+fxtx_status_t run_linear(const LayerArgs& l, const DeviceInfo& dev, cudaStream_t st) {
+  if (l.n == 0) return run_empty(l.type, l.e, l.m, l.k, dev, st);
+  Operand x, w;
+  x.p = l.X; x.ld = l.ldx;
+  w.p = l.W; w.ld = l.ldw; w.mn_major = !l.w_trans;
+  PlanesProduct q;
+  q.M = l.m;
+  q.N = l.k;
+  q.K = l.n;
+  q.e = l.e;
+  Prepared p;
+  p.type = l.type;
+  p.add(x, l.m, l.n, &q.A);
+  p.add(w, l.k, l.n, &q.B);
+  char* ws = nullptr;
+  fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), p.bytes, st);
+  if (s != FXTX_OK) return s;
+  p.place(ws);
+  s = status_of(launch_prepare(l.type, nullptr, p.packs, p.count, dev.sm_count, st));
+  if (s == FXTX_OK) s = run_typed(l.type, q, dev, st);
+  if (ws) cudaFreeAsync(ws, st);
+  return s;
+}
+
+fxtx_status_t run_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& dev, cudaStream_t st) {
+  const bool dx = g.DX && l.m > 0 && l.n > 0, dw = g.DW && l.n > 0 && l.k > 0, f32 = l.type == FXTX_F32;
+  const bool sums = l.m > 0 && l.k > 0;  // a sum of no terms is zero
+  // D is G itself where there is nothing to multiply and the products can read G where it lies
+  Operand d;
+  d.p = g.G; d.ld = g.ldg;
+  const bool own = sums && (dx || dw) && (g.act != FXTX_ACT_NONE || f32 || !copyable(d));
+  SlopeArgs a;
+  a.m = l.m; a.k = l.k;
+  a.G = g.G; a.ldg = g.ldg;
+  a.Z = g.Z; a.ldz = g.ldz;
+  a.act = g.act;
+  a.db = l.k > 0 ? g.DB : nullptr;
+
+  Prepared p;
+  p.type = l.type;
+  PlanesProduct qx, qw;
+  if (sums && dx) {
+    Operand w;
+    w.p = l.W; w.ld = l.ldw; w.mn_major = l.w_trans;
+    qx.M = l.m; qx.N = l.n; qx.K = l.k;
+    p.add(w, l.n, l.k, &qx.B);
+  }
+  Planes xp;
+  if (sums && dw) {
+    Operand x;
+    x.p = l.X; x.ld = l.ldx; x.mn_major = true;
+    qw.M = l.w_trans ? l.k : l.n; qw.N = l.w_trans ? l.n : l.k; qw.K = l.m;
+    p.add(x, l.n, l.m, &xp);
+  }
+  const size_t d_at = p.bytes, pitch = (size_t)(l.k + 7) / 8 * 8;
+  const size_t d_bytes = own ? ((size_t)(f32 ? 3 : 1) * l.m * pitch * 2 + 255) / 256 * 256 : 0;
+  const size_t sum_bytes = a.db ? slope_ws_bytes(l.m, l.k, dev.sm_count) : 0;
+  char* ws = nullptr;
+  fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), d_at + d_bytes + sum_bytes, st);
+  if (s != FXTX_OK) return s;
+  p.place(ws);
+  a.ws = reinterpret_cast<float*>(ws + d_at + d_bytes);
+  if (own) {
+    a.D = ws + d_at;
+    a.ldd = (int64_t)pitch;
+    a.d_planes = l.m * (int64_t)pitch;
+    d.p = a.D;
+    d.ld = a.ldd;
+    d.plane_stride = f32 ? a.d_planes : 0;
+  }
+  s = status_of(launch_prepare(l.type, own || a.db ? &a : nullptr, p.packs, p.count, dev.sm_count, st));
+
+  size_t none = 0;
+  Epilogue e;
+  if (s == FXTX_OK && dx) {
+    e.out = g.DX;
+    e.ldo = g.lddx;
+    if (sums) {
+      qx.A = planes_of(d, l.type, l.m, l.k, nullptr, &none);
+      qx.e = e;
+      s = run_typed(l.type, qx, dev, st);
+    } else {
+      s = run_empty(l.type, e, l.m, l.n, dev, st);
     }
   }
-  PlanesProduct q;
-  q.M = p.M;
-  q.N = p.N;
-  q.K = p.K;
-  q.e = p.e;
-  size_t ab = 0, bb = 0;
-  planes_of(p.A, p.type, p.M, p.K, nullptr, &ab);
-  planes_of(p.B, p.type, p.N, p.K, nullptr, &bb);
-  char* ws = nullptr;
-  fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), ab + bb, st);
-  if (s != FXTX_OK) return s;
-  size_t used = 0;
-  q.A = planes_of(p.A, p.type, p.M, p.K, ws, &used);
-  q.B = planes_of(p.B, p.type, p.N, p.K, ws + ab, &used);
-  if (ab) s = pack(p.A, p.type, q.A, dev, st);
-  if (s == FXTX_OK && bb) s = pack(p.B, p.type, q.B, dev, st);
-  if (s == FXTX_OK) switch (p.type) {
-      case FXTX_F32: s = run_planes<float>(q, dev, st); break;
-      case FXTX_BF16: s = run_planes<__nv_bfloat16>(q, dev, st); break;
-      default: s = run_planes<__half>(q, dev, st); break;
+  if (s == FXTX_OK && dw) {
+    e.out = g.DW;
+    e.ldo = g.lddw;
+    const int64_t rows = l.w_trans ? l.k : l.n, cols = l.w_trans ? l.n : l.k;
+    if (sums) {
+      d.mn_major = true;
+      const Planes dp = planes_of(d, l.type, l.k, l.m, nullptr, &none);
+      qw.A = l.w_trans ? dp : xp;
+      qw.B = l.w_trans ? xp : dp;
+      qw.e = e;
+      s = run_typed(l.type, qw, dev, st);
+    } else {
+      s = run_empty(l.type, e, rows, cols, dev, st);
     }
+  }
   if (ws) cudaFreeAsync(ws, st);
   return s;
 }

@@ -31,15 +31,6 @@ struct Epilogue {
   int act = FXTX_ACT_NONE;
 };
 
-// C (M x N) = sum over kk < K of A(i, kk) B(j, kk), then the epilogue. Allocates its own workspace.
-struct Product {
-  fxtx_type_t type = FXTX_F32;
-  int64_t M = 0, N = 0, K = 0;
-  Operand A, B;
-  Epilogue e;
-};
-fxtx_status_t run_product(const Product& p, const DeviceInfo& dev, cudaStream_t st);
-
 // A 16-bit operand as the tensor copies read it: `planes` matrices of rows x cols in memory,
 // `pitch` elements from row to row and `plane_stride` from plane to plane, 16-byte aligned.
 // mn_major: the rows run over kk (entry (i, kk) at row kk, column i), else over i.
@@ -70,13 +61,11 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
 
 // A copy of a matrix with an aligned pitch: 16-bit as it is, float32 as three bfloat16 planes.
 struct PackArgs {
-  fxtx_type_t type = FXTX_F32;
   const void* src = nullptr;
   int64_t rows = 0, cols = 0, ld = 0;
   void* dst = nullptr;
   int64_t pitch = 0, plane_stride = 0;
 };
-cudaError_t launch_pack(const PackArgs& a, int sm_count, cudaStream_t st);
 
 // A layer's arguments, and its gradient's.
 struct LayerArgs {
@@ -102,6 +91,10 @@ struct GradArgs {
   void* DB = nullptr;
 };
 
+// The layer and its gradient as products on the tensor cores. Allocate their own workspace.
+fxtx_status_t run_linear(const LayerArgs& l, const DeviceInfo& dev, cudaStream_t st);
+fxtx_status_t run_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& dev, cudaStream_t st);
+
 // Layers of 1 to kThin features and outputs, on the CUDA cores.
 constexpr int kThin = 64;
 bool thin_shape(int64_t n, int64_t k);
@@ -111,7 +104,6 @@ fxtx_status_t run_thin_grad(const LayerArgs& l, const GradArgs& g, const DeviceI
 // D = G * act'(Z) and its column sums. D is written with row pitch ldd unless it is NULL (of
 // float32 as three bfloat16 planes, d_planes elements apart); db unless it is NULL.
 struct SlopeArgs {
-  fxtx_type_t type = FXTX_F32;
   int64_t m = 0, k = 0;
   const void* G = nullptr;
   int64_t ldg = 0;
@@ -124,6 +116,8 @@ struct SlopeArgs {
   float* ws = nullptr;  // slope_ws_bytes
 };
 size_t slope_ws_bytes(int64_t m, int64_t k, int sm_count);
-cudaError_t launch_slope(const SlopeArgs& a, int sm_count, cudaStream_t st);
+// One launch for a slope (or NULL) and up to two copies; a second one adds db's parts of many rows.
+cudaError_t launch_prepare(fxtx_type_t type, const SlopeArgs* slope, const PackArgs* packs, int count, int sm_count,
+                           cudaStream_t st);
 
 }  // namespace fxtx

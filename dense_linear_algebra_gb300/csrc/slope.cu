@@ -3,10 +3,12 @@
 //
 // Bound: HBM (G and Z read once, D written once). A thread takes 8 neighbouring columns, a
 // CTA 256 / CX rows at a time of CX such column groups; each CTA's column sums go to a
-// workspace and a second kernel adds them in order, so db is the same on every call. D is
+// workspace and a second kernel adds them in order, so db is the same on every call (few rows:
+// a CTA takes all of them and writes db itself). D is
 // rounded to the layer's type (the products that follow take it as an operand); db is summed
 // from the unrounded values. Of float32, D is written as the three bfloat16 planes that the
-// products take. The same stores serve a plain copy into an aligned pitch (launch_pack).
+// products take. The same stores copy a matrix into an aligned pitch, or split it into planes; a
+// gradient's slope and copies are one launch.
 #include <algorithm>
 #include <type_traits>
 
@@ -67,13 +69,17 @@ __host__ __device__ inline bool rows_aligned(const void* p, int64_t ld, int size
   return ((uintptr_t)p & 15u) == 0 && (ld * size) % 16 == 0;
 }
 
-// cx: column groups of 8 a CTA takes, a power of two up to 32
+struct SlopeGrid {
+  int cx;           // column groups of 8 a CTA takes, a power of two up to 32
+  int64_t gx, gy;   // CTAs over the columns and over the rows
+  int64_t rows;     // rows a CTA takes
+};
+
 template <typename T>
-__global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, const int cx, const int64_t rows_per_cta) {
-  after_previous();
-  const int gx = threadIdx.x & (cx - 1), gy = threadIdx.x / cx, step = 256 / cx;
-  const int64_t col = ((int64_t)blockIdx.x * cx + gx) * 8;
-  const int64_t r1 = min(a.m, (int64_t)(blockIdx.y + 1) * rows_per_cta);
+__device__ __forceinline__ void slope(const SlopeArgs& a, const SlopeGrid& grid, int64_t bx, int64_t by) {
+  const int cx = grid.cx, gx = threadIdx.x & (cx - 1), gy = threadIdx.x / cx, step = 256 / cx;
+  const int64_t col = (bx * cx + gx) * 8;
+  const int64_t r1 = min(a.m, (by + 1) * grid.rows);
   const int n = a.k - col >= 8 ? 8 : (a.k > col ? (int)(a.k - col) : 0);
   const bool wg = n == 8 && rows_aligned(a.G, a.ldg, sizeof(T));
   const bool wz = n == 8 && rows_aligned(a.Z, a.ldz, sizeof(T));
@@ -83,7 +89,7 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, const int
   if (n > 0)
     with_act(a.act, [&](auto act) {
       constexpr int ACT = decltype(act)::value;
-      for (int64_t r = (int64_t)blockIdx.y * rows_per_cta + gy; r < r1; r += step) {
+      for (int64_t r = by * grid.rows + gy; r < r1; r += step) {
         float g[8];
         load8(G + r * a.ldg, n, wg, g);
         if constexpr (ACT != FXTX_ACT_NONE) {
@@ -103,11 +109,45 @@ __global__ void __launch_bounds__(256) slope_kernel(const SlopeArgs a, const int
   for (int i = 0; i < 8; ++i) part[(gy * cx + gx) * 8 + i] = sum[i];
   __syncthreads();
   for (int c = threadIdx.x; c < cx * 8; c += 256) {
-    const int64_t j = (int64_t)blockIdx.x * cx * 8 + c;
+    const int64_t j = bx * cx * 8 + c;
     if (j >= a.k) continue;
     float s = 0.f;
     for (int y = 0; y < step; ++y) s += part[y * cx * 8 + c];
-    a.ws[(int64_t)blockIdx.y * a.k + j] = s;
+    if (grid.gy == 1) static_cast<T*>(a.db)[j] = from_f32<T>(s);
+    else a.ws[by * a.k + j] = s;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void pack(const PackArgs& a, int64_t b, int64_t ctas) {
+  const int64_t groups = (a.cols + 7) / 8, stride = ctas * 256;
+  const bool aligned = rows_aligned(a.src, a.ld, sizeof(T));
+  for (int64_t x = b * 256 + threadIdx.x; x < a.rows * groups; x += stride) {
+    const int64_t i = x / groups, j = x % groups * 8;
+    const int n = a.cols - j >= 8 ? 8 : (int)(a.cols - j);
+    float v[8];
+    load8(static_cast<const T*>(a.src) + i * a.ld + j, n, aligned && n == 8, v);
+    store8<T>(a.dst, i * a.pitch + j, a.plane_stride, n, n == 8, v);
+  }
+}
+
+struct PrepareArgs {
+  SlopeArgs slope;
+  SlopeGrid grid;
+  PackArgs pack[2];
+  int64_t ctas[3];  // the slope's, and each copy's
+};
+
+template <typename T>
+__global__ void __launch_bounds__(256) prepare_kernel(const __grid_constant__ PrepareArgs a) {
+  after_previous();
+  int64_t b = blockIdx.x;
+  if (b < a.ctas[0]) {
+    slope<T>(a.slope, a.grid, b % a.grid.gx, b / a.grid.gx);
+  } else if ((b -= a.ctas[0]) < a.ctas[1]) {
+    pack<T>(a.pack[0], b, a.ctas[1]);
+  } else {
+    pack<T>(a.pack[1], b - a.ctas[1], a.ctas[2]);
   }
 }
 
@@ -129,72 +169,62 @@ __global__ void __launch_bounds__(256) sums_kernel(const float* ws, int64_t part
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(const PackArgs a) {
-  const int64_t groups = (a.cols + 7) / 8, stride = (int64_t)gridDim.x * 256;
-  after_previous();
-  const bool aligned = rows_aligned(a.src, a.ld, sizeof(T));
-  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < a.rows * groups; x += stride) {
-    const int64_t i = x / groups, j = x % groups * 8;
-    const int n = a.cols - j >= 8 ? 8 : (int)(a.cols - j);
-    float v[8];
-    load8(static_cast<const T*>(a.src) + i * a.ld + j, n, aligned && n == 8, v);
-    store8<T>(a.dst, i * a.pitch + j, a.plane_stride, n, n == 8, v);
-  }
-}
-
-struct SlopeGrid {
-  int cx;
-  int64_t gx, gy, rows;
-};
 SlopeGrid slope_grid(int64_t m, int64_t k, int sm_count) {
   SlopeGrid g;
   const int64_t groups = (k + 7) / 8;
   g.cx = 1;
+  if (m <= 2048) {  // a CTA takes all rows, of as many columns as leave no SM without work
+    while (g.cx < 32 && g.cx < groups && (groups + 2 * g.cx - 1) / (2 * g.cx) >= sm_count) g.cx *= 2;
+    if (g.cx < 2 && groups > 1) g.cx = 2;  // whole 32-byte sectors
+    g.gx = (groups + g.cx - 1) / g.cx;
+    g.gy = 1;
+    g.rows = m;
+    return g;
+  }
   while (g.cx < 32 && g.cx < groups) g.cx *= 2;
   g.gx = (groups + g.cx - 1) / g.cx;
   // about 6 CTAs a SM, each of at least one step of rows
   const int64_t step = 256 / g.cx, want = std::max<int64_t>(1, (int64_t)sm_count * 6 / g.gx);
   const int64_t steps = (m + step - 1) / step, per = std::max<int64_t>(1, (steps + want - 1) / want);
   g.rows = per * step;
-  g.gy = std::max<int64_t>(1, (m + g.rows - 1) / g.rows);
-  // the grid's second dimension ends at 65,535
-  while (g.gy > 65535) {
-    g.rows *= 2;
-    g.gy = (m + g.rows - 1) / g.rows;
-  }
+  g.gy = (m + g.rows - 1) / g.rows;
   return g;
 }
 
 template <typename T>
-cudaError_t launch_t(const SlopeArgs& a, int sm_count, cudaStream_t st) {
-  const SlopeGrid g = slope_grid(a.m, a.k, sm_count);
-  const cudaError_t e = launch_kernel(slope_kernel<T>, dim3((unsigned)g.gx, (unsigned)g.gy), 256, 0, st, a, g.cx, g.rows);
-  if (e != cudaSuccess || a.db == nullptr) return e;
-  return launch_kernel(sums_kernel<T>, dim3((unsigned)((a.k + 31) / 32)), 256, 0, st, a.ws, g.gy, a.k, static_cast<T*>(a.db));
+cudaError_t launch_t(const SlopeArgs* s, const PackArgs* packs, int count, int sm_count, cudaStream_t st) {
+  PrepareArgs a;
+  a.ctas[0] = a.ctas[1] = a.ctas[2] = 0;
+  if (s) {
+    a.slope = *s;
+    a.grid = slope_grid(s->m, s->k, sm_count);
+    a.ctas[0] = a.grid.gx * a.grid.gy;
+  }
+  for (int i = 0; i < count; ++i) {
+    a.pack[i] = packs[i];
+    a.ctas[1 + i] = std::min<int64_t>((packs[i].rows * ((packs[i].cols + 7) / 8) + 255) / 256, (int64_t)sm_count * 16);
+  }
+  const int64_t ctas = a.ctas[0] + a.ctas[1] + a.ctas[2];
+  if (ctas == 0) return cudaSuccess;
+  const cudaError_t e = launch_kernel(prepare_kernel<T>, dim3((unsigned)ctas), 256, 0, st, a);
+  if (e != cudaSuccess || !s || s->db == nullptr || a.grid.gy == 1) return e;
+  return launch_kernel(sums_kernel<T>, dim3((unsigned)((s->k + 31) / 32)), 256, 0, st, s->ws, a.grid.gy, s->k,
+                       static_cast<T*>(s->db));
 }
 
 }  // namespace
 
-cudaError_t launch_pack(const PackArgs& a, int sm_count, cudaStream_t st) {
-  const int64_t blocks = std::min<int64_t>((a.rows * ((a.cols + 7) / 8) + 255) / 256, (int64_t)sm_count * 16);
-  if (blocks == 0) return cudaSuccess;
-  switch (a.type) {
-    case FXTX_F32: return launch_kernel(pack_kernel<float>, dim3((unsigned)blocks), 256, 0, st, a);
-    case FXTX_BF16: return launch_kernel(pack_kernel<__nv_bfloat16>, dim3((unsigned)blocks), 256, 0, st, a);
-    default: return launch_kernel(pack_kernel<__half>, dim3((unsigned)blocks), 256, 0, st, a);
-  }
-}
-
 size_t slope_ws_bytes(int64_t m, int64_t k, int sm_count) {
-  return (size_t)slope_grid(m, k, sm_count).gy * (size_t)k * 4;
+  const SlopeGrid g = slope_grid(m, k, sm_count);
+  return g.gy == 1 ? 0 : (size_t)g.gy * (size_t)k * 4;
 }
 
-cudaError_t launch_slope(const SlopeArgs& a, int sm_count, cudaStream_t st) {
-  switch (a.type) {
-    case FXTX_F32: return launch_t<float>(a, sm_count, st);
-    case FXTX_BF16: return launch_t<__nv_bfloat16>(a, sm_count, st);
-    default: return launch_t<__half>(a, sm_count, st);
+cudaError_t launch_prepare(fxtx_type_t type, const SlopeArgs* slope, const PackArgs* packs, int count, int sm_count,
+                           cudaStream_t st) {
+  switch (type) {
+    case FXTX_F32: return launch_t<float>(slope, packs, count, sm_count, st);
+    case FXTX_BF16: return launch_t<__nv_bfloat16>(slope, packs, count, sm_count, st);
+    default: return launch_t<__half>(slope, packs, count, sm_count, st);
   }
 }
 

@@ -4,6 +4,8 @@ The package only marshals arguments: every step runs in the kernels of ``libfuse
 """
 from __future__ import annotations
 
+from array import array
+
 import numpy as np
 import torch
 
@@ -36,10 +38,12 @@ def _act(act):
     return code
 
 
-def _matrix(t, dtype, m, n, name, index):
+def _pitch(t, dtype, m, n, name, index):
     """The row pitch of a row-major (m, n) CUDA tensor."""
     if t.dtype is not dtype or t.get_device() != index or t.shape != (m, n):
         raise ValueError(f"{name}: expected a {dtype} matrix of shape {(m, n)} on cuda:{index}")
+    if t.is_contiguous():
+        return n
     ld, unit = t.stride()
     if m <= 1:
         ld = n
@@ -61,21 +65,20 @@ def _weights(W, dtype, n, index):
     raise ValueError("W: expected unit stride along its rows or its columns")
 
 
-def _empty(shape, like, stream):
-    """A new tensor of the stream that writes it (the current one unless `stream` is given)."""
-    if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+def _features(X):
+    """The type code, dtype, device, rows, features and row pitch of X."""
+    index, dtype = X.get_device(), X.dtype
+    if index < 0 or X.dim() != 2:
+        raise ValueError("X: expected a 2-D CUDA tensor")
+    m, n = X.shape
+    return _type(X, "X"), dtype, index, m, n, _pitch(X, dtype, m, n, "X", index)
+
+
+def _on_stream(stream, index):
+    """The stream as a context that new tensors are made in, and as the C entries take it."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
-
-
-def _raw(stream, index):
-    """`stream`, or the current one, as the C entries take it."""
-    if stream is None:
-        return _current_stream(index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        stream = torch.cuda.ExternalStream(stream, device=index)
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
 def _call(fn, index, *args):
@@ -89,15 +92,6 @@ def _call(fn, index, *args):
         _check(rc, fn.__name__)
 
 
-def _features(X):
-    """The type code, device, rows, features and row pitch of X."""
-    index = X.get_device()
-    if index < 0 or X.dim() != 2:
-        raise ValueError("X: expected a 2-D CUDA tensor")
-    m, n = X.shape
-    return _type(X, "X"), index, m, n, _matrix(X, X.dtype, m, n, "X", index)
-
-
 def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=None):
     """act(X W + b) + residual in one pass: X (m, n), W (n, k), b (k), residual and the result (m, k).
 
@@ -107,8 +101,11 @@ def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=No
     returns Z = X W + b for ``linear_grad`` (or give the (m, k) tensor to keep it in). ``out`` may be ``residual``.
     Runs on the current stream, or on ``stream``, which then owns the new tensors.
     """
-    code, di, m, n, ldx = _features(X)
-    dt = X.dtype
+    if stream is not None:
+        context, stream = _on_stream(stream, X.get_device())
+        with context:
+            return linear(X, W, b, act, residual, pre, out)
+    code, dt, di, m, n, ldx = _features(X)
     k, ldw, trans = _weights(W, dt, n, di)
     pb = pr = pz = None
     ldr = ldz = 0
@@ -116,19 +113,20 @@ def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=No
         _lib._vec(b, dt, k, "b", di)
         pb = b.data_ptr()
     if residual is not None:
-        ldr, pr = _matrix(residual, dt, m, k, "residual", di), residual.data_ptr()
-    if pre is False:
-        pre = None
-    elif pre is True:
-        pre = _empty((m, k), X, stream)
-    if pre is not None:
-        ldz, pz = _matrix(pre, dt, m, k, "pre", di), pre.data_ptr()
-    if out is None:
-        out, ldo = _empty((m, k), X, stream), k
+        ldr, pr = _pitch(residual, dt, m, k, "residual", di), residual.data_ptr()
+    if pre is True:
+        pre, ldz = torch.empty((m, k), dtype=dt, device=X.device), k
+        pz = pre.data_ptr()
+    elif pre is not False and pre is not None:
+        ldz, pz = _pitch(pre, dt, m, k, "pre", di), pre.data_ptr()
     else:
-        ldo = _matrix(out, dt, m, k, "out", di)
+        pre = None
+    if out is None:
+        out, ldo = torch.empty((m, k), dtype=dt, device=X.device), k
+    else:
+        ldo = _pitch(out, dt, m, k, "out", di)
     _call(fxtx_linear, di, code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans, pb, _act(act), pr, ldr, pz, ldz,
-          out.data_ptr(), ldo, _raw(stream, di))
+          out.data_ptr(), ldo, _current_stream(di))
     return out if pre is None else (out, pre)
 
 
@@ -139,21 +137,33 @@ def linear_grad(G, X, W, pre=None, act=None, need=(True, True, True), stream=Non
     (not needed without an activation). ``need`` says which of the three are computed; the others come back as None.
     dW is stored as W is. Types, layouts and streams are those of ``linear``.
     """
-    code, di, m, n, ldx = _features(X)
-    dt, kind = X.dtype, _act(act)
+    if stream is not None:
+        context, stream = _on_stream(stream, X.get_device())
+        with context:
+            return linear_grad(G, X, W, pre, act, need)
+    code, dt, di, m, n, ldx = _features(X)
+    kind = _act(act)
     k, ldw, trans = _weights(W, dt, n, di)
-    ldg = _matrix(G, dt, m, k, "G", di)
-    if kind and pre is None:
-        raise ValueError("pre: the gradient of an activation needs the Z that linear kept")
-    ldz = _matrix(pre, dt, m, k, "pre", di) if kind else 0
-    dX = _empty((m, n), X, stream) if need[0] else None
-    dW = _empty((k, n) if trans else (n, k), X, stream) if need[1] else None
-    db = _empty((k,), X, stream) if need[2] else None
-    _call(fxtx_linear_grad, di, code, m, n, k, G.data_ptr(), ldg, X.data_ptr(), ldx, W.data_ptr(), ldw, trans,
-          pre.data_ptr() if kind else None, ldz, kind, None if dX is None else dX.data_ptr(), n,
-          None if dW is None else dW.data_ptr(), n if trans else k, None if db is None else db.data_ptr(),
-          _raw(stream, di))
-    return dX, dW.t() if dW is not None and trans else dW, db
+    ldg = _pitch(G, dt, m, k, "G", di)
+    pz, ldz = None, 0
+    if kind:
+        if pre is None:
+            raise ValueError("pre: the gradient of an activation needs the Z that linear kept")
+        ldz, pz = _pitch(pre, dt, m, k, "pre", di), pre.data_ptr()
+    device, (want_x, want_w, want_b) = X.device, need
+    dX = dW = db = px = pw = pb = None
+    if want_x:
+        dX = torch.empty((m, n), dtype=dt, device=device)
+        px = dX.data_ptr()
+    if want_w:
+        dW = torch.empty((k, n) if trans else (n, k), dtype=dt, device=device)
+        pw = dW.data_ptr()
+    if want_b:
+        db = torch.empty(k, dtype=dt, device=device)
+        pb = db.data_ptr()
+    _call(fxtx_linear_grad, di, code, m, n, k, G.data_ptr(), ldg, X.data_ptr(), ldx, W.data_ptr(), ldw, trans, pz, ldz,
+          kind, px, n, pw, n if trans else k, pb, _current_stream(di))
+    return dX, dW.t() if trans and want_w else dW, db
 
 
 class AdamW:
@@ -199,24 +209,39 @@ class AdamW:
         self.offsets = [int(b) * ADAMW_BLOCK for b in at[:-1]]
         blocks = int(at[-1])
         self._total = total = blocks * ADAMW_BLOCK
-        # the kernel's table (fxtx_adamw_tensor_t): n, p, g, m, v, m_scale, v_scale, copy
-        self._table = np.zeros((len(self._sizes), 8), dtype=np.int64)
-        self._table[:, 0] = self._sizes
         wide = state_bits == 32
-        self.exp_avg = torch.zeros(total, dtype=torch.float32 if wide else torch.int8, device=self._device)
-        self.exp_avg_sq = torch.zeros(total, dtype=torch.float32 if wide else torch.uint8, device=self._device)
-        self.exp_avg_scale = self.exp_avg_sq_scale = None
+        self._m = torch.zeros(total, dtype=torch.float32 if wide else torch.int8, device=self._device)
+        self._v = torch.zeros(total, dtype=torch.float32 if wide else torch.uint8, device=self._device)
+        self._ms = self._vs = None
+        # the kernel's table, one fxtx_adamw_tensor_t a tensor: n, p, g, m, v, m_scale, v_scale, copy
+        table = np.zeros((len(self._sizes), 8), dtype=np.int64)
         start = at[:-1] * ADAMW_BLOCK * (4 if wide else 1)
-        self._table[:, 3] = self.exp_avg.data_ptr() + start
-        self._table[:, 4] = self.exp_avg_sq.data_ptr() + start
+        table[:, 3] = self._m.data_ptr() + start
+        table[:, 4] = self._v.data_ptr() + start
         if not wide:
-            self.exp_avg_scale = torch.zeros(blocks, dtype=torch.float32, device=self._device)
-            self.exp_avg_sq_scale = torch.zeros(blocks, dtype=torch.float32, device=self._device)
-            self._table[:, 5] = self.exp_avg_scale.data_ptr() + at[:-1] * 4
-            self._table[:, 6] = self.exp_avg_sq_scale.data_ptr() + at[:-1] * 4
-        self._pointers(self.params, self._dtype, "params")
+            self._ms = torch.zeros(blocks, dtype=torch.float32, device=self._device)
+            self._vs = torch.zeros(blocks, dtype=torch.float32, device=self._device)
+            table[:, 5] = self._ms.data_ptr() + at[:-1] * 4
+            table[:, 6] = self._vs.data_ptr() + at[:-1] * 4
+        self._table = array("q", table.tobytes())
+        self._where = self._copy_where = None
+        self._hold()
+
+    exp_avg = property(lambda self: self._m)
+    exp_avg_sq = property(lambda self: self._v)
+    exp_avg_scale = property(lambda self: self._ms)
+    exp_avg_sq_scale = property(lambda self: self._vs)
+
+    def _hold(self):
+        """Takes the params' (and copies') addresses into the table, holding on to their memory: an address seen
+        again then stands for the same memory, and needs no other check."""
+        self._where = self._pointers(self.params, self._dtype, "params")
+        self._held = [p.detach() for p in self.params]
+        self._table[1::8] = array("q", self._where)
         if self.copies is not None:
-            self._pointers(self.copies, self._copy_dtype, "copies")
+            self._copy_where = self._pointers(self.copies, self._copy_dtype, "copies")
+            self._held += [c.detach() for c in self.copies]
+            self._table[7::8] = array("q", self._copy_where)
 
     def _pointers(self, tensors, dtype, name, optional=False):
         """The tensors' addresses (0 for a None where that is allowed), each checked against the size that the states
@@ -242,16 +267,17 @@ class AdamW:
         if kind is None:
             raise ValueError("grads: no gradient")
         g_type = _type(kind, "grads")
-        table = self._table
-        table[:, 1] = self._pointers(self.params, self._dtype, "params")
-        table[:, 2] = self._pointers(grads, kind.dtype, "grads", optional=True)
-        if self.copies is not None:
-            table[:, 7] = self._pointers(self.copies, self._copy_dtype, "copies")
+        if [p.data_ptr() for p in self.params] != self._where or (
+                self.copies is not None and [c.data_ptr() for c in self.copies] != self._copy_where):
+            self._hold()
+        table, where = self._table, self._pointers(grads, kind.dtype, "grads", optional=True)
+        table[2::8] = array("q", where)
         # an entry of no elements is left out
-        table[:, 0] = [0 if g is None else n for g, n in zip(grads, self._sizes)]
-        _call(fxtx_adamw, self._index, len(self._sizes), table.ctypes.data, self._type, g_type, self._copy_type,
+        table[0::8] = array("q", [n if g else 0 for g, n in zip(where, self._sizes)])
+        _call(fxtx_adamw, self._index, len(where), table.buffer_info()[0], self._type, g_type, self._copy_type,
               self.state_bits, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
-              _raw(stream, self._index))
+              _current_stream(self._index) if stream is None else
+              stream if isinstance(stream, int) else stream.cuda_stream)
         self.steps += 1
 
     def moments(self, stream=None):
@@ -259,11 +285,15 @@ class AdamW:
         bits, for 8 the values that they stand for."""
         if self.state_bits == 32:
             return self.exp_avg, self.exp_avg_sq
-        m = _empty((self._total,), self.exp_avg_scale, stream)
-        v = _empty((self._total,), self.exp_avg_scale, stream)
+        if stream is not None:
+            context, stream = _on_stream(stream, self._index)
+            with context:
+                return self.moments()
+        m = torch.empty(self._total, dtype=torch.float32, device=self._device)
+        v = torch.empty(self._total, dtype=torch.float32, device=self._device)
         _call(fxtx_adamw_moments, self._index, self._total, self.exp_avg.data_ptr(), self.exp_avg_scale.data_ptr(),
               self.exp_avg_sq.data_ptr(), self.exp_avg_sq_scale.data_ptr(), m.data_ptr(), v.data_ptr(),
-              _raw(stream, self._index))
+              _current_stream(self._index))
         return m, v
 
     def _state(self):
