@@ -21,7 +21,9 @@
 // Bound: HBM. Each of p, g and the states is read once and p and the states are written once.
 // One warp takes one block of 256 elements, 8 neighbouring elements a lane, so that every
 // array moves in 16-byte (32-bit and 16-bit types) or 8-byte (codes) accesses and the block's
-// maxima are one warp reduction. The tensor table travels as a kernel parameter (constant
+// maxima are one warp reduction. With 8-bit states the instructions bound it first (three
+// square roots and a division an element, each rounded as IEEE has it): products and sums go two
+// elements at a time, codes become numbers by one conversion and numbers codes by one addition. The tensor table travels as a kernel parameter (constant
 // bank): no copy and no workspace before the launch, at most 448 tensors a launch.
 #include <algorithm>
 
@@ -84,12 +86,55 @@ __device__ __forceinline__ void store_n(T* p, int n, const float* x) {
     if (i < n) p[i] = from_f32<T>(x[i]);
 }
 
+// Two products or sums in one instruction, each rounded on its own (the sum as a fused a * one + x,
+// with a 1 that the assembler does not know: it would merge a product with the sum that follows it, and round once).
+__device__ __forceinline__ void mul2(float& a, float& b, float x, float y) {
+  asm("{\n.reg .b64 u, v;\nmov.b64 u, {%0, %1};\nmov.b64 v, {%2, %3};\nmul.rn.f32x2 u, u, v;\nmov.b64 {%0, %1}, u;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y, float one) {
+  asm("{\n.reg .b64 u, v, w;\nmov.b64 u, {%0, %1};\nmov.b64 v, {%2, %3};\nmov.b64 w, {%4, %4};\nfma.rn.f32x2 u, u, w, v;\n"
+      "mov.b64 {%0, %1}, u;\n}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y), "f"(one));
+}
+
 // The largest |x| of a block, NaN if one is a NaN (magnitudes order as their bits do).
 __device__ __forceinline__ float block_max(const float* x) {
-  unsigned top = 0;
+  float top = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < PER; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  return __uint_as_float(__reduce_max_sync(FULL_MASK, top));
+  for (int i = 1; i < PER; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+  return __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(top) & 0x7fffffffu));
+}
+
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: a sum with it ends in the other term rounded to an integer
+
+// x_i becomes the integer rint(sqrt(x_i)), root and rounding as IEEE has them, for x_i up to 255.4^2. The
+// approximate root is off by less than 1e-4 and settles the code, unless it lies that close to the middle
+// of two: then the lane's roots are taken again.
+__device__ __forceinline__ void code_roots(float* x, float one) {
+  float off = 0.f, s[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i += 2) {
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s[i]) : "f"(x[i]));
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(s[i + 1]) : "f"(x[i + 1]));
+    float a = s[i], b = s[i + 1], u, v;
+    add2(a, b, kRound, kRound, one);
+    add2(a, b, -kRound, -kRound, one);
+    u = a;
+    v = b;
+    add2(a, b, -s[i], -s[i + 1], one);
+    off = fmaxf(off, fmaxf(fabsf(a), fabsf(b)));
+    s[i] = u;
+    s[i + 1] = v;
+  }
+  if (off > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) s[i] = __fsub_rn(__fadd_rn(__fsqrt_rn(x[i]), kRound), kRound);
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) x[i] = s[i];
 }
 
 // The scale of a block and the factor that takes its values to squares of codes; `square` is
@@ -164,22 +209,39 @@ __global__ void __launch_bounds__(WARPS * 32) adamw_kernel(const __grid_constant
       }
       const float ms = t.m_scale[blk], vs = t.v_scale[blk];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int a = mc[i], r = vc[i];
-        m[i] = __fmul_rn((float)(a * abs(a)), ms);
-        const float root = __fmul_rn((float)(r * r), vs);
-        v[i] = __fmul_rn(root, root);
+      for (int i = 0; i < PER; i += 2) {
+        m[i] = (float)mc[i];
+        m[i + 1] = (float)mc[i + 1];
+        mul2(m[i], m[i + 1], fabsf(m[i]), fabsf(m[i + 1]));  // exact
+        mul2(m[i], m[i + 1], ms, ms);
+        v[i] = (float)vc[i];
+        v[i + 1] = (float)vc[i + 1];
+        mul2(v[i], v[i + 1], v[i], v[i + 1]);  // exact
+        mul2(v[i], v[i + 1], vs, vs);
+        mul2(v[i], v[i + 1], v[i], v[i + 1]);
       }
     }
 
     float r[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      m[i] = __fadd_rn(__fmul_rn(m[i], c.b1), __fmul_rn(g[i], c.c1));
-      v[i] = __fadd_rn(__fmul_rn(v[i], c.b2), __fmul_rn(__fmul_rn(g[i], g[i]), c.c2));
-      r[i] = __fsqrt_rn(v[i]);
-      const float step = __fdiv_rn(m[i], __fadd_rn(__fmul_rn(r[i], c.root), c.eps));
-      p[i] = __fsub_rn(__fmul_rn(p[i], c.keep), __fmul_rn(step, c.rate));
+    for (int i = 0; i < PER; i += 2) {
+      float x = g[i], y = g[i + 1];
+      mul2(x, y, x, y);
+      mul2(x, y, c.c2, c.c2);
+      mul2(v[i], v[i + 1], c.b2, c.b2);
+      add2(v[i], v[i + 1], x, y, c.one);
+      mul2(g[i], g[i + 1], c.c1, c.c1);
+      mul2(m[i], m[i + 1], c.b1, c.b1);
+      add2(m[i], m[i + 1], g[i], g[i + 1], c.one);
+      x = r[i] = __fsqrt_rn(v[i]);
+      y = r[i + 1] = __fsqrt_rn(v[i + 1]);
+      mul2(x, y, c.root, c.root);
+      add2(x, y, c.eps, c.eps, c.one);
+      x = __fdiv_rn(m[i], x);
+      y = __fdiv_rn(m[i + 1], y);
+      mul2(x, y, -c.rate, -c.rate);
+      mul2(p[i], p[i + 1], c.keep, c.keep);
+      add2(p[i], p[i + 1], x, y, c.one);
     }
 
     if (wide) store8(pp, p);
@@ -214,12 +276,33 @@ __global__ void __launch_bounds__(WARPS * 32) adamw_kernel(const __grid_constant
       const float vs = block_scale(block_max(r), 65025.f, 1.f / 65025.f, vi);
       int8_t mc[PER];
       uint8_t vc[PER];
+      float x[PER];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int a = min(__float2int_rn(__fsqrt_rn(__fmul_rn(fabsf(m[i]), mi))), 127);
-        mc[i] = (int8_t)(m[i] < 0.f ? -a : a);
-        const int q = min(__float2int_rn(__fsqrt_rn(__fmul_rn(r[i], vi))), 255);
-        vc[i] = (uint8_t)max(q, r[i] > 0.f ? 1 : 0);
+      for (int i = 0; i < PER; i += 2) {
+        x[i] = fabsf(m[i]);
+        x[i + 1] = fabsf(m[i + 1]);
+        mul2(x[i], x[i + 1], mi, mi);
+      }
+      code_roots(x, c.one);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) mc[i] = (int8_t)(__float_as_int(copysignf(x[i], m[i]) + kRound));
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) {
+        x[i] = r[i];
+        x[i + 1] = r[i + 1];
+        mul2(x[i], x[i + 1], vi, vi);
+      }
+      code_roots(x, c.one);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) vc[i] = (uint8_t)(__float_as_int((r[i] > 0.f ? fmaxf(x[i], 1.f) : x[i]) + kRound));
+      // an infinity or a NaN in the block: nothing has a code, and all reads back by its scale
+      if (!(ms <= 3.4e38f)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mc[i] = 0;
+      }
+      if (!(vs <= 3.4e38f)) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) vc[i] = r[i] > 0.f ? 1 : 0;
       }
       int8_t* mp = static_cast<int8_t*>(t.m) + at;
       uint8_t* vp = static_cast<uint8_t*>(t.v) + at;
@@ -296,41 +379,42 @@ cudaError_t launch_param(int64_t count, const fxtx_adamw_tensor_t* t, int g_type
   }
 }
 
-// The values that 8-bit states stand for: 8 elements a thread.
+// The values that 8-bit states stand for: 4 elements a thread, so that a warp's stores are whole lines.
 __global__ void __launch_bounds__(256) moments_kernel(int64_t n, const int8_t* m, const float* ms, const uint8_t* r,
                                                       const float* rs, float* m_out, float* v_out) {
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * PER;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   after_previous();
   if (at >= n) return;
   const float a = ms[at / BLOCK], b = rs[at / BLOCK];
-  const bool wide = at + PER <= n && (((uintptr_t)m | (uintptr_t)r) & 7u) == 0 &&
+  const bool wide = at + 4 <= n && (((uintptr_t)m | (uintptr_t)r) & 3u) == 0 &&
                     (((uintptr_t)m_out | (uintptr_t)v_out) & 15u) == 0;
-  int8_t mc[PER];
-  uint8_t rc[PER];
+  int8_t mc[4];
+  uint8_t rc[4];
   if (wide) {
-    *reinterpret_cast<uint2*>(mc) = *reinterpret_cast<const uint2*>(m + at);
-    *reinterpret_cast<uint2*>(rc) = *reinterpret_cast<const uint2*>(r + at);
+    *reinterpret_cast<uint32_t*>(mc) = *reinterpret_cast<const uint32_t*>(m + at);
+    *reinterpret_cast<uint32_t*>(rc) = *reinterpret_cast<const uint32_t*>(r + at);
   } else {
-    for (int i = 0; i < PER; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mc[i] = at + i < n ? m[at + i] : (int8_t)0;
       rc[i] = at + i < n ? r[at + i] : (uint8_t)0;
     }
   }
-  float x[PER], y[PER];
+  float x[4], y[4];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int p = mc[i], q = rc[i];
-    x[i] = __fmul_rn((float)(p * abs(p)), a);
-    const float root = __fmul_rn((float)(q * q), b);
+  for (int i = 0; i < 4; ++i) {
+    const float p = (float)mc[i], q = (float)rc[i];
+    x[i] = __fmul_rn(p * fabsf(p), a);
+    const float root = __fmul_rn(q * q, b);
     y[i] = __fmul_rn(root, root);
   }
   if (wide) {
-    store8(m_out + at, x);
-    store8(v_out + at, y);
+    *reinterpret_cast<float4*>(m_out + at) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(v_out + at) = make_float4(y[0], y[1], y[2], y[3]);
   } else {
-    const int k = (int)min((int64_t)PER, n - at);
-    store_n(m_out + at, k, x);
-    store_n(v_out + at, k, y);
+    for (int i = 0; i < 4 && at + i < n; ++i) {
+      m_out[at + i] = x[i];
+      v_out[at + i] = y[i];
+    }
   }
 }
 
@@ -348,7 +432,7 @@ cudaError_t launch_adamw(int64_t count, const fxtx_adamw_tensor_t* t, int p_type
 cudaError_t launch_adamw_moments(int64_t n, const int8_t* m, const float* ms, const uint8_t* r, const float* rs,
                                  float* m_out, float* v_out, cudaStream_t st) {
   if (n <= 0) return cudaSuccess;
-  return launch_kernel(moments_kernel, dim3((unsigned)((n + 2047) / 2048)), 256, 0, st, n, m, ms, r, rs, m_out, v_out);
+  return launch_kernel(moments_kernel, dim3((unsigned)((n + 1023) / 1024)), 256, 0, st, n, m, ms, r, rs, m_out, v_out);
 }
 
 }  // namespace fxtx

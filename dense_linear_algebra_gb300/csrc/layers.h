@@ -61,6 +61,7 @@ struct AdamwConst {
   float eps;
   float keep;            // 1 - lr * weight_decay
   float rate;            // lr / (1 - beta1^t)
+  float one = 1.f;
 };
 cudaError_t launch_adamw(int64_t count, const fxtx_adamw_tensor_t* t, int p_type, int g_type, int copy_type, int bits,
                          const AdamwConst& c, int sm_count, cudaStream_t st);
