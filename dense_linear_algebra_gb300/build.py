@@ -19,7 +19,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfusedxtx.so")
 SOURCES = ["api.cu", "dense.cu", "csr.cu", "multi.cu", "multi_tc.cu", "split.cu", "plan.cpp", "tmap.cpp",
            "tune.cpp", "noalloc.cu", "layers_api.cu", "adamw.cu",
-           "linear.cu", "slope.cu", "product_tc.cu", "thin.cu"]
+           "linear.cu", "slope.cu", "product_tc.cu", "thin.cu", "few.cu"]
 HEADERS = ["act.cuh", "common.cuh", "host.h", "kernels.h", "layers.h", "linear.h", "multi.h", "plan.h", "product.cuh", "tc.cuh", "tmap.h",
            "tune.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

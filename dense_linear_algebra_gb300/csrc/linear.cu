@@ -171,8 +171,15 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
   return best;
 }
 
+// Whether a result of m rows is formed on the CUDA cores.
+bool few_rows(fxtx_type_t type, int64_t m, bool by_column) {
+  return type == FXTX_F32 && m <= (by_column ? kFewByColumn : kFewByRow);
+}
+
 fxtx_status_t run_linear(const LayerArgs& l, const DeviceInfo& dev, cudaStream_t st) {
   if (l.n == 0) return run_empty(l.type, l.e, l.m, l.k, dev, st);
+  if (few_rows(l.type, l.m, l.w_trans))
+    return run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, l.e, dev, st);
   Operand x, w;
   x.p = l.X; x.ld = l.ldx;
   w.p = l.W; w.ld = l.ldw; w.mn_major = !l.w_trans;
@@ -212,7 +219,8 @@ fxtx_status_t run_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& 
   Prepared p;
   p.type = l.type;
   PlanesProduct qx, qw;
-  if (sums && dx) {
+  const bool few = few_rows(l.type, l.m, !l.w_trans);  // dX = D W^T takes W in the other order
+  if (sums && dx && !few) {
     Operand w;
     w.p = l.W; w.ld = l.ldw; w.mn_major = l.w_trans;
     qx.M = l.m; qx.N = l.n; qx.K = l.k;
@@ -248,7 +256,9 @@ fxtx_status_t run_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& 
   if (s == FXTX_OK && dx) {
     e.out = g.DX;
     e.ldo = g.lddx;
-    if (sums) {
+    if (sums && few) {
+      s = run_few(l.m, l.k, l.n, d.p, d.ld, d.plane_stride, static_cast<const float*>(l.W), l.ldw, !l.w_trans, e, dev, st);
+    } else if (sums) {
       qx.A = planes_of(d, l.type, l.m, l.k, nullptr, &none);
       qx.e = e;
       s = run_typed(l.type, qx, dev, st);

@@ -101,6 +101,12 @@ bool thin_shape(int64_t n, int64_t k);
 fxtx_status_t run_thin_linear(const LayerArgs& l, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_thin_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& dev, cudaStream_t st);
 
+// float32 results of few rows on the CUDA cores: out = e(X W), W's entry (j, c) at W[j * ld + c] or by_column at
+// W[c * ld + j]; X as it is, or (x_planes > 0) as its three bfloat16 planes.
+constexpr int kFewByRow = 16, kFewByColumn = 8;  // rows at most
+fxtx_status_t run_few(int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, int64_t x_planes, const float* W,
+                      int64_t ld, bool by_column, const Epilogue& e, const DeviceInfo& dev, cudaStream_t st);
+
 // D = G * act'(Z) and its column sums. D is written with row pitch ldd unless it is NULL (of
 // float32 as three bfloat16 planes, d_planes elements apart); db unless it is NULL.
 struct SlopeArgs {

@@ -60,6 +60,16 @@ struct Finish {
     }
   }
 
+  // One entry.
+  __device__ __forceinline__ void one(int64_t i, int64_t j, float c) const {
+    if (i >= rows || j >= cols) return;
+    if (e.bias) c += to_f32(static_cast<const T*>(e.bias)[j]);
+    if (e.Z) static_cast<T*>(e.Z)[i * e.ldz + j] = from_f32<T>(c);
+    with_act(e.act, [&](auto act) { c = act_of<decltype(act)::value>(c); });
+    if (e.R) c += to_f32(static_cast<const T*>(e.R)[i * e.ldr + j]);
+    static_cast<T*>(e.out)[i * e.ldo + j] = from_f32<T>(c);
+  }
+
   // NV (4, 8 or 16) entries of row i from column j on, j a multiple of NV.
   template <int NV>
   __device__ __forceinline__ void row(int64_t i, int64_t j, const float* acc) const {

@@ -78,8 +78,9 @@ struct Cfg {
 template <int CG, int BN, int PL>
 struct TileCfg : Cfg<CG, BN, PL, PL == 3 ? 64 : 128, 192> {
   // Epilogue warps: few are slow to finish a tile, for the latencies of the exponentials and of the stores (a
-  // 128 x 128 tile with silu took 7,600 cycles with eight); 256 columns leave the memory for eight.
-  static constexpr int EPI = BN == 256 ? 8 : 16, THREADS = 32 * (4 + EPI);
+  // 128 x 128 tile with silu took 7,600 cycles with eight); 256 columns leave the memory for eight, the sums of
+  // float32 the registers.
+  static constexpr int EPI = BN == 256 || PL == 3 ? 8 : 16, THREADS = 32 * (4 + EPI);
   static constexpr int COLS = std::max(32, BN / (EPI / 4));  // columns a thread takes
   static constexpr size_t BYTES = TileCfg::Cfg::BYTES + EPI * Tile32<float>::BYTES;
   static_assert(BYTES + 2 * BN * 4 + 512 <= 227 * 1024, "shared memory");

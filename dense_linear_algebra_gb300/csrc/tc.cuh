@@ -157,7 +157,7 @@ struct Ring {
 
 // Waits for phase `parity` of `bar`; gives up when another role has given up (the CTA's abort
 // word) or after WAIT_LIMIT polls (raising FXTX_ERR_TIMEOUT and setting the word).
-__device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_word) {
+static __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, volatile int* abort_word) {
   for (uint32_t it = 0; it < WAIT_LIMIT; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 63u && *abort_word) return false;

@@ -114,6 +114,21 @@ def check_grad(m, n, k, dtype, act="none", w_t=False, pitch=0, offset=0, seed=0)
     assert dW.stride() == ((1, n) if w_t else (k, 1)) or 1 in (n, k)
 
 
+# around the kernels' borders: 64 features and outputs, 8 and 16 rows of float32, 128 rows, 256 x 256 tiles and more tiles
+# than SMs
+BORDERS = [(8, 300, 96), (9, 260, 200), (16, 100, 700), (17, 65, 300), (5, 2500, 70), (6, 70, 5000), (64, 64, 65), (64, 65, 64),
+           (129, 300, 160), (700, 200, 2600), (2304, 520, 2560), (5000, 136, 1000)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("w_t", [False, True])
+@pytest.mark.parametrize("shape", BORDERS, ids=str)
+def test_kernel_borders(shape, w_t, dtype):
+    check_linear(*shape, dtype, act=ACTS[sum(shape) % 6], w_t=w_t)
+    check_grad(*shape, dtype, act=ACTS[(sum(shape) + 1) % 6], w_t=w_t)
+
+
 SHAPES = [(1, 1, 1), (1, 64, 8), (2, 33, 17), (5, 128, 40), (16, 256, 136), (17, 1000, 24), (64, 96, 257), (65, 80, 64),
           (127, 129, 131), (128, 64, 256), (200, 520, 264), (300, 72, 1032), (1030, 48, 48), (4099, 32, 32)]
 
