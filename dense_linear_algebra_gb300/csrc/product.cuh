@@ -103,6 +103,7 @@ struct Finish {
 template <typename T>
 struct Tile32 {
   static constexpr int BYTES = 32 * 64;
+  // W: entries a row, at most one a lane
   static constexpr int W = 64 / sizeof(T), EPC = 16 / sizeof(T), CH = 4, ROWS = 8;  // entries a row and a chunk, chunks a row, rows an access
   __device__ __forceinline__ static uint4* at(unsigned char* buf, int r, int c) {
     return reinterpret_cast<uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
@@ -129,13 +130,22 @@ struct Tile32 {
       for (int q = 0; q < EPC; ++q) v[c * EPC + q] += to_f32(t[q]);
     }
   }
-  // what move<false> would bring, held by the lanes on its way (wide rows only), and put down
-  __device__ __forceinline__ static void fetch(uint4 (&v)[CH], const T* p, int64_t ld, int64_t i0, int64_t rows, int64_t j0) {
-    const int lane = threadIdx.x & 31, c = lane % CH;
+  // rows i0 .. i0 + 31 and columns j0 .. j0 + W - 1 of a matrix of rows x cols, held by the lanes on their way in
+  __device__ __forceinline__ static void fetch(uint4 (&v)[CH], const T* p, int64_t ld, bool wide, int64_t i0, int64_t rows,
+                                               int64_t j0, int64_t cols) {
+    const int lane = threadIdx.x & 31;
+    const int64_t j = j0 + lane % CH * EPC;
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-      const int64_t r = i0 + k * ROWS + lane / CH;
-      v[k] = r < rows ? *reinterpret_cast<const uint4*>(p + r * ld + j0 + c * EPC) : make_uint4(0, 0, 0, 0);
+      const int64_t i = i0 + k * ROWS + lane / CH;
+      const T* g = p + i * ld + j;
+      if (i < rows && wide && j + EPC <= cols) {
+        v[k] = *reinterpret_cast<const uint4*>(g);
+      } else {
+        T* t = reinterpret_cast<T*>(&v[k]);
+#pragma unroll
+        for (int q = 0; q < EPC; ++q) t[q] = i < rows && j + q < cols ? g[q] : from_f32<T>(0.f);
+      }
     }
   }
   __device__ __forceinline__ static void place(unsigned char* buf, const uint4 (&v)[CH]) {
@@ -143,30 +153,20 @@ struct Tile32 {
 #pragma unroll
     for (int k = 0; k < CH; ++k) *at(buf, k * ROWS + lane / CH, lane % CH) = v[k];
   }
-  // rows i0 .. i0 + 31 and columns j0 .. j0 + W - 1 of a matrix of rows x cols to memory, or from it
-  template <bool STORE>
-  __device__ __forceinline__ static void move(unsigned char* buf, T* p, int64_t ld, bool wide, int64_t i0, int64_t rows,
-                                              int64_t j0, int64_t cols) {
+  // the tile's part of such a matrix to memory
+  __device__ __forceinline__ static void drain(unsigned char* buf, T* p, int64_t ld, bool wide, int64_t i0, int64_t rows,
+                                               int64_t j0, int64_t cols) {
     const int lane = threadIdx.x & 31;
     if (wide && j0 + W <= cols) {
 #pragma unroll
       for (int k = 0; k < CH; ++k) {
         const int r = k * ROWS + lane / CH, c = lane % CH;
-        if (i0 + r < rows) {
-          uint4* g = reinterpret_cast<uint4*>(p + (i0 + r) * ld + j0 + c * EPC);
-          if constexpr (STORE) *g = *at(buf, r, c);
-          else *at(buf, r, c) = *g;
-        }
+        if (i0 + r < rows) *reinterpret_cast<uint4*>(p + (i0 + r) * ld + j0 + c * EPC) = *at(buf, r, c);
       }
     } else {
       const int n = cols - j0 < W ? (int)(cols - j0) : W, m = rows - i0 < 32 ? (int)(rows - i0) : 32;
       for (int r = 0; r < m; ++r)
-        for (int e = lane; e < n; e += 32) {
-          T* t = reinterpret_cast<T*>(at(buf, r, e / EPC)) + e % EPC;
-          T* g = p + (i0 + r) * ld + j0 + e;
-          if constexpr (STORE) *g = *t;
-          else *t = *g;
-        }
+        if (lane < n) p[(i0 + r) * ld + j0 + lane] = reinterpret_cast<const T*>(at(buf, r, lane / EPC))[lane % EPC];
     }
   }
 };

@@ -340,9 +340,8 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
       using Tile = Tile32<T>;
       const T* R = static_cast<const T*>(a.e.R);
       // the residual's first rows are on their way while the products run
-      const bool ahead = R != nullptr && !part && wide_r && j0 + C::COLS <= a.cols;
       uint4 next[Tile::CH];
-      if (ahead) Tile::fetch(next, R, a.e.ldr, i0, a.rows, j0);
+      if (R && !part) Tile::fetch(next, R, a.e.ldr, wide_r, i0, a.rows, j0, a.cols);
 
       uint32_t t = lane_base + (uint32_t)((acc & 1) * BN);
       if constexpr (PL == 1) {
@@ -383,7 +382,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           get(x, v);
           Tile32<float>::put(buf, 0, v);
           __syncwarp();
-          Tile32<float>::template move<true>(buf, part, a.cols, a.cols % 4 == 0, i0, a.rows, j0 + x, a.cols);
+          Tile32<float>::drain(buf, part, a.cols, a.cols % 4 == 0, i0, a.rows, j0 + x, a.cols);
           __syncwarp();
         }
         release();
@@ -399,16 +398,14 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
             Tile::put(buf, y, v);
           }
           __syncwarp();
-          Tile::template move<true>(buf, static_cast<T*>(a.e.Z), a.e.ldz, wide_z, i0, a.rows, j0 + x, a.cols);
+          Tile::drain(buf, static_cast<T*>(a.e.Z), a.e.ldz, wide_z, i0, a.rows, j0 + x, a.cols);
           __syncwarp();
         }
-        if (ahead) {
+        if (R) {
           Tile::place(buf, next);
-          if (x + Tile::W < C::COLS) Tile::fetch(next, R, a.e.ldr, i0, a.rows, j0 + x + Tile::W);
-        } else if (R) {
-          Tile::template move<false>(buf, const_cast<T*>(R), a.e.ldr, wide_r, i0, a.rows, j0 + x, a.cols);
+          if (x + Tile::W < C::COLS) Tile::fetch(next, R, a.e.ldr, wide_r, i0, a.rows, j0 + x + Tile::W, a.cols);
+          __syncwarp();
         }
-        if (R) __syncwarp();
 #pragma unroll 1
         for (int y = 0; y < Tile::W; y += 16) {
           float v[16];
@@ -421,7 +418,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           Tile::put(buf, y, v);
         }
         __syncwarp();
-        Tile::template move<true>(buf, static_cast<T*>(a.e.out), a.e.ldo, wide_out, i0, a.rows, j0 + x, a.cols);
+        Tile::drain(buf, static_cast<T*>(a.e.out), a.e.ldo, wide_out, i0, a.rows, j0 + x, a.cols);
         __syncwarp();
       }
       release();
