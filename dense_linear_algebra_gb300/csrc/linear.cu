@@ -114,7 +114,7 @@ fxtx_status_t run_empty(fxtx_type_t type, const Epilogue& e, int64_t rows, int64
 // The layout with the least estimated time, in cycles of an SM (figures measured on GB300). A stage
 // (64 of kk) takes its products (an M = 128, K = 16 product of a CTA holds the pipe for 64 cycles up
 // to N = 128) or its bytes, of which an SM gets about 55 a cycle from L2 with the deep pipelines of the
-// persistent kernel and a CTA of the split kernel about 32; no layout beats the operands' stream from
+// persistent kernel and a CTA of the split kernel 27 to 34; no layout beats the operands' stream from
 // HBM. A persistent CTA's tiles follow one another, each for as long as its products or its epilogue
 // take. On top come a fixed cost (launch, filling the pipeline, the last epilogue) and the exchange of
 // partial sums: between the CTAs of a cluster, or through memory and a second kernel.
@@ -132,16 +132,16 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
     const int64_t kb = std::max<int64_t>(1, (K + bk - 1) / bk);
     const double mma = bk / 16 * (planes == 3 ? 6 : 1) * std::max(64.0, bn / 2.0);
     const double bytes = planes * 2.0 * bk * (128.0 + bn / cg);
-    const double stage = std::max(mma, bytes / (cluster ? 32.0 : 55.0)), epilogue = 400.0 + 12.0 * bn;
+    const double stage = std::max(mma, bytes / (!cluster ? 55.0 : bn <= 64 ? 27.0 : 34.0)), epilogue = 400.0 + 12.0 * bn;
     auto price = [&](int64_t s) {
       const int64_t per = (kb + s - 1) / s;
       if (cluster && (s - 1) * per >= kb) return;  // a CTA without work
       const int64_t waves = (tiles * s + units - 1) / units;
       double t;
       if (cluster) {
-        t = std::max(floor, waves * (per * stage)) + waves * (3000.0 + 15.0 * bn) + (s > 1 ? 800.0 : 0.0);
+        t = std::max(floor, waves * (per * stage)) + waves * (3500.0 + 15.0 * bn) + (s > 1 ? 800.0 : 0.0);
       } else {
-        t = std::max(floor, waves * std::max(per * stage, epilogue)) + 4500.0 + epilogue;
+        t = std::max(floor, waves * std::max(per * stage, epilogue)) + 3000.0 + epilogue;
         if (s > 1) t += 4500.0 + (double)s * M * N * 8.0 / 3000.0;
       }
       if (t < best_t) {

@@ -14,7 +14,10 @@ textbook consumers of ``alpha * X^T (v * (X p)) + beta * z``:
   every Hessian-vector product ``X^T (D * (X p)) + lam p`` is ONE fused call with
   v = D = mu (1 - mu).
 
-X may be dense (a 2-D CUDA tensor) or CSR (a tuple ``(row_ptr, col_idx, vals, n)``).
+``mlp_adamw`` trains a network of more than one layer on the rows of X with the layer operators
+(``layers.linear``, ``layers.linear_grad``, ``layers.AdamW``).
+
+For the linear models X may be dense (a 2-D CUDA tensor) or CSR (a tuple ``(row_ptr, col_idx, vals, n)``).
 The few operations outside the pattern (``X^T b`` once, and per Newton step the
 margins ``X w`` and the gradient ``X^T (mu - b)``) are plain matrix-vector products
 done by torch (for CSR X on torch CSR copies built once per solve); vector updates on
@@ -220,3 +223,97 @@ def logistic_newton_cg(X, labels, lam: float, newton_steps: int = 20, tol: float
         info.newton_steps = step + 1
         info.cg_iterations += ci.iterations
     return w, info
+
+
+@dataclass
+class MLPInfo:
+    steps: int = 0
+    losses: list = field(default_factory=list)
+
+
+class MLP:
+    """A residual network on the rows of X: h = act(X W0 + b0), then h = h + act(h Wi + bi) for each hidden layer, and
+    the result h Wn + bn. Every layer is one fused call, forward and backward (``layers.linear``, ``layers.linear_grad``).
+
+    ``weights`` and ``biases`` are float32; ``dtype`` (bfloat16, float16 or float32) is what the layers compute in: the
+    working copies of 16-bit types are refreshed by the optimiser.
+    """
+
+    def __init__(self, features: int, hidden: int, outputs: int, layers: int = 1, act: str = "gelu",
+                 dtype=torch.float32, device="cuda", seed: int = 0):
+        gen = torch.Generator(device=device)
+        gen.manual_seed(seed)
+        sizes = [features] + [hidden] * (layers + 1) + [outputs]
+        self.act, self.dtype = act, dtype
+        self.weights = [torch.randn(a, b, generator=gen, device=device) / a ** 0.5 for a, b in zip(sizes, sizes[1:])]
+        self.biases = [torch.zeros(b, device=device) for b in sizes[1:]]
+        self.copies = None
+        if dtype != torch.float32:
+            self.copies = [p.to(dtype) for p in self.parameters()]
+
+    def parameters(self):
+        return self.weights + self.biases
+
+    def _working(self):
+        if self.copies is None:
+            return self.weights, self.biases
+        return self.copies[:len(self.weights)], self.copies[len(self.weights):]
+
+    def forward(self, X, keep: bool = False):
+        """The result for the rows of X; with ``keep`` also what ``backward`` needs."""
+        from . import layers
+
+        W, b = self._working()
+        last, saved, h = len(W) - 1, [], X
+        for i in range(last + 1):
+            residual = h if 0 < i < last else None
+            act = self.act if i < last else None
+            if keep and act:
+                out, pre = layers.linear(h, W[i], b[i], act=act, residual=residual, pre=True)
+            else:
+                out, pre = layers.linear(h, W[i], b[i], act=act, residual=residual), None
+            saved.append((h, pre))
+            h = out
+        return (h, saved) if keep else h
+
+    def backward(self, G, saved):
+        """The gradients of ``parameters()`` from the gradient at the result."""
+        from . import layers
+
+        W, _ = self._working()
+        last = len(W) - 1
+        dW, db = [None] * (last + 1), [None] * (last + 1)
+        for i in range(last, -1, -1):
+            h, pre = saved[i]
+            dh, dW[i], db[i] = layers.linear_grad(G, h, W[i], pre=pre, act=self.act if i < last else None,
+                                                  need=(i > 0, True, True))
+            # the residual passes the gradient on as it is
+            G = dh.add_(G) if 0 < i < last else dh
+        return dW + db
+
+
+def mlp_adamw(X, B, hidden: int, layers: int = 1, act: str = "gelu", steps: int = 100, batch: int = 0, lr: float = 1e-3,
+              weight_decay: float = 0.0, state_bits: int = 32, dtype=torch.float32, seed: int = 0):
+    """Least squares by a residual network (``MLP``) trained with AdamW: min mean((net(X) - B)^2).
+
+    X (m, n) and B (m, outputs) are float32 or ``dtype``; each step takes ``batch`` rows in turn (0: all of them).
+    Returns the network and the losses of the steps (left on the GPU until read).
+    """
+    from .layers import AdamW
+
+    X, B = X.to(dtype), B.to(dtype)
+    net = MLP(X.shape[1], hidden, B.shape[1], layers, act, dtype, X.device, seed)
+    opt = AdamW(net.parameters(), lr=lr, weight_decay=weight_decay, state_bits=state_bits, copies=net.copies)
+    info, m = MLPInfo(), X.shape[0]
+    batch = m if batch <= 0 else min(batch, m)
+    at = 0
+    for _ in range(steps):
+        if at + batch > m:
+            at = 0
+        out, saved = net.forward(X[at:at + batch], keep=True)
+        err = out.float() - B[at:at + batch].float()
+        info.losses.append(err.square().mean())
+        opt.step(net.backward((err * (2.0 / err.numel())).to(dtype), saved))
+        info.steps += 1
+        at += batch
+    return net, info
