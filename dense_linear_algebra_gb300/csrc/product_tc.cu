@@ -31,8 +31,10 @@
 //
 // float32 (PL = 3): each operand comes as three bfloat16 planes (x = hi + mid + lo, exactly),
 // and the six products of planes whose order is within 2^-18 of the first are summed; the rest
-// is at most 2^-26 of a term. The tensor cores' sums are taken out every 256 of kk and added in
-// fp32 registers, rounded to nearest, so that a long sum's error does not grow with its length.
+// is at most 2^-26 of a term. The tensor cores' sums are taken out every 128 of kk and added in
+// fp32 registers, rounded to nearest, so that a long sum's error does not grow with its length:
+// 2-norm error 6e-7 for 2048^3 normal inputs (8e-7 for fp32 multiply-adds in order), 1.5e-6 when taken out every 256
+// (5 % faster), 1.3e-7 every 64 (19 % slower).
 #include <cuda.h>
 
 #include <algorithm>
@@ -55,7 +57,7 @@ namespace {
 constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
 constexpr int SPLIT_EPI = 8;      // epilogue warps of the split kernel
 constexpr int SPLIT_THREADS = 32 * (4 + SPLIT_EPI);
-constexpr int CHUNK = 4;          // stages a sum stays in tensor memory (float32)
+constexpr int CHUNK = 2;          // stages a sum stays in tensor memory (float32)
 
 // BK: kk a stage; KB: kilobytes the stages may take.
 template <int CG, int BN, int PL, int BK_, int KB>
@@ -96,16 +98,18 @@ struct SplitCfg : Cfg<1, BN, PL, 64, PL == 3 ? 150 : (BN == 128 ? 128 : 80)> {
   static_assert(CTAS * (BYTES + 2048) <= 228 * 1024, "shared memory");
 };
 
-// A warp's 32 lanes of COLS tensor-memory columns added to `sum`.
+// A warp's 32 lanes of COLS tensor-memory columns added to `sum`, 32 on their way at a time.
 template <int COLS>
 __device__ __forceinline__ void add_columns(uint32_t t, float* sum) {
+  constexpr int STEP = COLS < 32 ? COLS : 32;
 #pragma unroll
-  for (int x = 0; x < COLS; x += 16) {
-    float r[16];
-    tc_load16(t + (uint32_t)x, r);
+  for (int x = 0; x < COLS; x += STEP) {
+    float r[STEP];
+#pragma unroll
+    for (int y = 0; y < STEP; y += 16) tc_load16(t + (uint32_t)(x + y), r + y);
     tc_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum[x + i] += r[i];
+    for (int i = 0; i < STEP; ++i) sum[x + i] += r[i];
   }
 }
 

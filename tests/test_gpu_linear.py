@@ -326,6 +326,19 @@ def test_graph_capture(dtype):
 
 
 @pytest.mark.gpu
+def test_no_workspace_is_reported(monkeypatch):
+    """float32 operands need a workspace: without one the call fails with its status, and the next one works."""
+    X, W = make((100, 300), torch.float32, 1), make((300, 200), torch.float32, 2)
+    want = fx.linear(X, W)
+    monkeypatch.setenv("FXTX_FAIL_ALLOC", "1")
+    with pytest.raises(fx.FxtxError) as e:
+        fx.linear(X, W)
+    assert e.value.status == fx.FXTX_ERR_ALLOC
+    monkeypatch.delenv("FXTX_FAIL_ALLOC")
+    assert torch.equal(fx.linear(X, W), want)
+
+
+@pytest.mark.gpu
 def test_python_refusals():
     X, W, b = make((6, 8), torch.float32, 1), make((8, 4), torch.float32, 2), make((1, 4), torch.float32, 3)[0]
     G = make((6, 4), torch.float32, 4)
