@@ -90,7 +90,7 @@ fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st) {
     props.allocType = cudaMemAllocationTypePinned;
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = d;
-    uint64_t keep = 256u << 20;
+    uint64_t keep = 1ull << 30;
     if (cudaMemPoolCreate(&pools[d], &props) != cudaSuccess) pools[d] = nullptr;
     else cudaMemPoolSetAttribute(pools[d], cudaMemPoolAttrReleaseThreshold, &keep);
     cudaGetLastError();

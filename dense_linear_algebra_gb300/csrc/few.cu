@@ -3,11 +3,11 @@
 //
 // Bound: HBM, the weights' stream (2 m operations for each entry of W: with 16 rows about 70 % of
 // the fp32 pipe). W is read once, where it lies, whatever its order, pitch and alignment; on the
-// tensor cores it is first split into three planes, four times the traffic. 4096 x 4096: one row 17 us
-// by rows and 14 us by columns (49 us on the tensor cores), 8 rows 27 and 40 us, 16 rows 33 us by rows (49),
-// 141 us by columns (50), whose lanes need all of X's rows for every feature; one row of 8192 x 8192 41 us
-// (6.5 TB/s). bfloat16 and float16 have no planes to make and stay on the tensor cores: 9.4 us for one to
-// 8 rows of 4096 x 4096.
+// tensor cores it is first split into three planes, four times the traffic. 4096 x 4096: one row 18 us
+// by rows and 14 us by columns (49 us on the tensor cores), 8 rows 25 and 38 us, 16 rows 29 us by rows (49);
+// by columns 16 rows took 141 us (50), since its lanes need all of X's rows for every feature. One row of
+// 8192 x 8192: 46 us (5.8 TB/s). bfloat16 and float16 have no planes to make and stay on the tensor cores: 8.1 us
+// for one row of 4096 x 4096.
 //
 // A cluster of R CTAs takes one block of columns, each CTA a part of the features; X's rows sit in
 // shared memory. W stored by rows: a lane takes 4 neighbouring columns of 4 features at a time, so

@@ -17,7 +17,7 @@ fxtx_status_t current_device(const DeviceInfo** out);
 // FXTX_ERR_ALLOC if it cannot be had, *p = nullptr for 0 bytes.
 fxtx_status_t alloc_ws(void** p, size_t bytes, cudaStream_t st);
 
-// The same from a pool of the library's own that keeps up to 256 MB between calls, so that a
+// The same from a pool of the library's own that keeps up to 1 GB between calls, so that a
 // call after a synchronisation does not map its workspace anew (a fifth of a millisecond).
 fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st);
 

@@ -142,7 +142,7 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
         t = std::max(floor, waves * (per * stage)) + waves * (3500.0 + 15.0 * bn) + (s > 1 ? 800.0 : 0.0);
       } else {
         t = std::max(floor, waves * std::max(per * stage, epilogue)) + 3000.0 + epilogue;
-        if (s > 1) t += 4500.0 + (double)s * M * N * 8.0 / 3000.0;
+        if (s > 1) t += 6500.0 + (double)s * M * N * 8.0 / 3000.0;
       }
       if (t < best_t) {
         best_t = t;

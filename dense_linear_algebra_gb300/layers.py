@@ -5,6 +5,7 @@ The package only marshals arguments: every step runs in the kernels of ``libfuse
 from __future__ import annotations
 
 from array import array
+from operator import attrgetter
 
 import numpy as np
 import torch
@@ -18,6 +19,9 @@ _current_stream = torch._C._cuda_getCurrentRawStream  # of a device, as the inte
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}  # fxtx_type_t
 
 ADAMW_BLOCK = 256  # FXTX_ADAMW_BLOCK
+
+_data_ptr, _numel, _get_device = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
+_is_contiguous, _dtype = torch.Tensor.is_contiguous, attrgetter("dtype")
 
 
 def _type(t, name):
@@ -110,7 +114,8 @@ def linear(X, W, b=None, act=None, residual=None, pre=False, out=None, stream=No
     pb = pr = pz = None
     ldr = ldz = 0
     if b is not None:
-        _lib._vec(b, dt, k, "b", di)
+        if b.dtype is not dt or b.get_device() != di or b.shape != (k,) or not b.is_contiguous():
+            raise ValueError(f"b: expected a contiguous {dt} vector of length {k} on cuda:{di}")
         pb = b.data_ptr()
     if residual is not None:
         ldr, pr = _pitch(residual, dt, m, k, "residual", di), residual.data_ptr()
@@ -246,6 +251,12 @@ class AdamW:
     def _pointers(self, tensors, dtype, name, optional=False):
         """The tensors' addresses (0 for a None where that is allowed), each checked against the size that the states
         were made for."""
+        try:  # one pass a property, none of it interpreted a tensor at a time
+            if (list(map(_numel, tensors)) == self._sizes and set(map(_dtype, tensors)) == {dtype}
+                    and set(map(_get_device, tensors)) == {self._index} and all(map(_is_contiguous, tensors))):
+                return list(map(_data_ptr, tensors))
+        except (TypeError, AttributeError):  # a None, or no tensor
+            pass
         if len(tensors) != len(self._sizes):
             raise ValueError(f"{name}: expected {len(self._sizes)} tensors, got {len(tensors)}")
         index, got = self._index, []
@@ -267,13 +278,13 @@ class AdamW:
         if kind is None:
             raise ValueError("grads: no gradient")
         g_type = _type(kind, "grads")
-        if [p.data_ptr() for p in self.params] != self._where or (
-                self.copies is not None and [c.data_ptr() for c in self.copies] != self._copy_where):
+        if list(map(_data_ptr, self.params)) != self._where or (
+                self.copies is not None and list(map(_data_ptr, self.copies)) != self._copy_where):
             self._hold()
         table, where = self._table, self._pointers(grads, kind.dtype, "grads", optional=True)
         table[2::8] = array("q", where)
         # an entry of no elements is left out
-        table[0::8] = array("q", [n if g else 0 for g, n in zip(where, self._sizes)])
+        table[0::8] = array("q", [n if g else 0 for g, n in zip(where, self._sizes)] if 0 in where else self._sizes)
         _call(fxtx_adamw, self._index, len(where), table.buffer_info()[0], self._type, g_type, self._copy_type,
               self.state_bits, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps, self.weight_decay,
               _current_stream(self._index) if stream is None else
