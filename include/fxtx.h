@@ -326,7 +326,10 @@ fxtx_status_t fxtx_multi_plan_describe(int is_f64, int64_t m, int64_t n, int64_t
  * The layer operators: a linear layer with its bias, activation and residual in one
  * pass, its gradient, and the AdamW step that uses it. Each takes the element type of
  * its tensors as an argument; sums are held in fp32 and results are rounded once, on
- * storing. Streams, ownership and errors are those of the entry points above.
+ * storing. Streams, ownership and errors are those of the entry points above, with two
+ * additions: workspace comes from a memory pool of the library's own, which keeps up to 1 GB
+ * between calls, and a call's kernels may be set up while the stream's previous kernel
+ * drains (they wait for its completion before they touch memory).
  */
 typedef enum { FXTX_F32 = 0, FXTX_BF16 = 1, FXTX_F16 = 2 } fxtx_type_t;
 
@@ -352,8 +355,14 @@ typedef enum {
  * OUT may equal R with ldo == ldr (in place); other overlaps of OUT or Z with anything
  * else are undefined. Any alignment and pitch is taken.
  *
- * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32. The result is
- * bitwise reproducible. FXTX_ERR_INVALID_ARG: an unknown type or activation, a size that is
+ * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32. FXTX_F32 operands
+ * of more than a few rows are split into three bfloat16 terms each (exactly) and six of
+ * their nine products formed, the rest being below 2^-26 of a term; they must be below
+ * 3.39e38 in magnitude, and an infinity or a NaN in a row of X or a column of W makes NaN
+ * of what it reaches. With at most 64 features and outputs, or few rows of FXTX_F32, the
+ * CUDA cores or 16-row products take the same terms. The result is bitwise
+ * reproducible. FXTX_ERR_ALLOC: no workspace (splitting operands, operands whose pitch or
+ * start is not a multiple of 16 bytes, long sums). FXTX_ERR_INVALID_ARG: an unknown type or activation, a size that is
  * negative or not below 2^31, a pitch below its row, a missing pointer.
  */
 fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
@@ -368,8 +377,8 @@ fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, con
  * and the gradient at R is G itself. Each of DX, DW, DB may be NULL (not computed; W is
  * read only for DX, X only for DW). DW is stored as W is (w_trans, pitch lddw). Z is
  * what fxtx_linear kept, and not read when act is FXTX_ACT_NONE. The slope of relu is
- * 0 at z <= 0. D is rounded to `type` before the products; DB is summed from the
- * unrounded values. m = 0 gives DW = 0 and DB = 0. Outputs must not overlap anything
+ * 0 at z <= 0. D of a 16-bit type is rounded to it before the products; DB is summed from
+ * the unrounded values. m = 0 gives DW = 0 and DB = 0. Outputs must not overlap anything
  * else. Types, layouts, precision and errors are those of fxtx_linear.
  */
 fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* G, int64_t ldg,
