@@ -356,13 +356,12 @@ typedef enum {
  * else are undefined. Any alignment and pitch is taken.
  *
  * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32. FXTX_F32 operands
- * of more than a few rows are split into three bfloat16 terms each (exactly) and six of
- * their nine products formed, the rest being below 2^-26 of a term; they must be below
- * 3.39e38 in magnitude, and an infinity or a NaN in a row of X or a column of W makes NaN
- * of what it reaches. With at most 64 features and outputs, or few rows of FXTX_F32, the
- * CUDA cores or 16-row products take the same terms. The result is bitwise
- * reproducible. FXTX_ERR_ALLOC: no workspace (splitting operands, operands whose pitch or
- * start is not a multiple of 16 bytes, long sums). FXTX_ERR_INVALID_ARG: an unknown type or activation, a size that is
+ * are split into three bfloat16 terms each and six of their nine products formed, each of
+ * the others being at most 2^-26 of the whole; they must be below 3.39e38 in magnitude,
+ * and an infinity gives NaN in what it reaches. (At most 16 rows, 8 with w_trans = 1, are
+ * plain fp32 multiply-adds.) The result is bitwise reproducible. Workspace is taken for
+ * the split, for 16-bit operands whose start or pitch is not a multiple of 16 bytes, and
+ * for some long sums; FXTX_ERR_ALLOC: none was left. FXTX_ERR_INVALID_ARG: an unknown type or activation, a size that is
  * negative or not below 2^31, a pitch below its row, a missing pointer.
  */
 fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
