@@ -296,8 +296,9 @@ def mlp_adamw(X, B, hidden: int, layers: int = 1, act: str = "gelu", steps: int 
               weight_decay: float = 0.0, state_bits: int = 32, dtype=torch.float32, seed: int = 0):
     """Least squares by a residual network (``MLP``) trained with AdamW: min mean((net(X) - B)^2).
 
-    X (m, n) and B (m, outputs) are float32 or ``dtype``; each step takes ``batch`` rows in turn (0: all of them).
-    Returns the network and the losses of the steps (left on the GPU until read).
+    X (m, n) and B (m, outputs) are float32 or ``dtype``; each step takes ``batch`` rows in turn (0: all of them), the
+    last step of a pass over X what is left of its rows. Returns the network and the losses of the steps (left on the
+    GPU until read).
     """
     from .layers import AdamW
 
@@ -308,12 +309,10 @@ def mlp_adamw(X, B, hidden: int, layers: int = 1, act: str = "gelu", steps: int 
     batch = m if batch <= 0 else min(batch, m)
     at = 0
     for _ in range(steps):
-        if at + batch > m:
-            at = 0
         out, saved = net.forward(X[at:at + batch], keep=True)
         err = out.float() - B[at:at + batch].float()
         info.losses.append(err.square().mean())
         opt.step(net.backward((err * (2.0 / err.numel())).to(dtype), saved))
         info.steps += 1
-        at += batch
+        at = at + batch if at + batch < m else 0
     return net, info
