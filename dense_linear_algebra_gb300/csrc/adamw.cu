@@ -297,14 +297,15 @@ __global__ void __launch_bounds__(WARPS * 32) adamw_kernel(const __grid_constant
       code_roots(x, c.one);
 #pragma unroll
       for (int i = 0; i < PER; ++i) vc[i] = (uint8_t)(__float_as_int((r[i] > 0.f ? fmaxf(x[i], 1.f) : x[i]) + kRound));
-      // an infinity or a NaN in the block: nothing has a code, and all reads back by its scale
+      // an infinity or a NaN in the block: nothing has a code, and all reads back as NaN by its scale (0 times an
+      // infinity, or a NaN; an infinite scale with codes above 0 would hold every weight of the block still for good)
       if (!(ms <= 3.4e38f)) {
 #pragma unroll
         for (int i = 0; i < PER; ++i) mc[i] = 0;
       }
       if (!(vs <= 3.4e38f)) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) vc[i] = r[i] > 0.f ? 1 : 0;
+        for (int i = 0; i < PER; ++i) vc[i] = 0;
       }
       int8_t* mp = static_cast<int8_t*>(t.m) + at;
       uint8_t* vp = static_cast<uint8_t*>(t.v) + at;

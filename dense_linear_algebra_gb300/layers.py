@@ -183,8 +183,9 @@ class AdamW:
 
     ``state_bits`` 32 holds both moments in fp32 (8 bytes an element). 8 holds each in one byte with an fp32 scale for
     every 256 elements of a tensor: the first moment as ``scale * c * |c|`` with int8 ``c``, the second as its root
-    ``scale * c * c`` with uint8 ``c``, rounded to nearest (a change smaller than half a step of the code is lost, and
-    an infinity or a NaN in a gradient makes its block's moments NaN).
+    ``scale * c * c`` with uint8 ``c``, rounded to nearest (a change smaller than half a step of the code is lost; an
+    infinity or a NaN in a gradient makes its block's moments NaN, and a gradient whose square is above fp32's range
+    its block's second moments: the block's params are NaN from the next step on).
 
     The states of all tensors lie one after the other in flat tensors, each starting at a multiple of 256 elements
     (``offsets``): ``exp_avg`` and ``exp_avg_sq``, and for 8 bits ``exp_avg_scale`` and ``exp_avg_sq_scale``.

@@ -401,8 +401,9 @@ fxtx_status_t fxtx_linear_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k
  * FXTX_ADAMW_BLOCK elements (the last one short) share a scale; m is int8_t codes with
  * value m_scale c |c|, v is uint8_t codes of its ROOT, v = (v_scale c^2)^2, and m_scale,
  * v_scale hold ceil(n / FXTX_ADAMW_BLOCK) floats. New codes are rounded to nearest; a
- * root above zero is held as 1 at least. A block with an infinity or a NaN in it reads
- * back as NaN. All-zero codes and scales are the initial state.
+ * root above zero is held as 1 at least. A moment's block with an infinity or a NaN in it
+ * reads back as NaN: m's where a gradient is one, v's also where a gradient's square is above
+ * fp32's range (from 1.8e19 on). All-zero codes and scales are the initial state.
  *
  * Any alignment is taken; 16-byte aligned arrays (8-byte for codes) move in wide
  * accesses. Tensors must not overlap. The call allocates nothing and launches one kernel
