@@ -35,6 +35,12 @@
 // fp32 registers, rounded to nearest, so that a long sum's error does not grow with its length:
 // 2-norm error 6e-7 for 2048^3 normal inputs (8e-7 for the vendor library's fp32 product, which has 1e-7 to 4e-7 where ours has 5e-7 to 6e-7 on some other sizes), 1.5e-6 when taken out every 256
 // (5 % faster), 1.3e-7 every 64 (19 % slower).
+//
+// 16 bits: the tensor cores' sums drop what lies below the accumulator's last bits, 6.3e-9 of a sum of terms of one
+// sign for each of kk (measured: 1.0e-4 after 16,384). A sum over more than FOLD of kk is therefore formed in pieces: the
+// first in one accumulator, the others in the second, which the epilogue warps add to the first in fp32 (rounded to
+// nearest). What is left is 5e-5, a tenth of float16's rounding; 300,000 rows in one piece were 2.7e-4 off. The products
+// wait for each addition: 1 to 3 % of sums of 16,384 to 65,536 (65,536 x 4096, 4096 outputs: dW 1,264 to 1,291 us).
 #include <cuda.h>
 
 #include <algorithm>
@@ -58,6 +64,7 @@ constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
 constexpr int SPLIT_EPI = 8;      // epilogue warps of the split kernel
 constexpr int SPLIT_THREADS = 32 * (4 + SPLIT_EPI);
 constexpr int CHUNK = 2;          // stages a sum stays in tensor memory (float32)
+constexpr int FOLD = 8192;        // of kk that a piece of a sum covers (16 bits)
 
 // BK: kk a stage; KB: kilobytes the stages may take.
 template <int CG, int BN, int PL, int BK_, int KB>
@@ -113,11 +120,35 @@ __device__ __forceinline__ void add_columns(uint32_t t, float* sum) {
   }
 }
 
+// A warp's 32 lanes of COLS tensor-memory columns at `from` added to those at `to`; `taken` is called once the last
+// of them have been read.
+template <int COLS, typename F>
+__device__ __forceinline__ void fold_columns(uint32_t from, uint32_t to, F taken) {
+  constexpr int STEP = COLS < 32 ? COLS : 32;
+#pragma unroll 1
+  for (int x = 0; x < COLS; x += STEP) {
+    float r[STEP], s[STEP];
+#pragma unroll
+    for (int y = 0; y < STEP; y += 16) {
+      tc_load16(from + (uint32_t)(x + y), r + y);
+      tc_load16(to + (uint32_t)(x + y), s + y);
+    }
+    tc_wait_ld();
+    if (x + STEP == COLS) taken();
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) s[i] += r[i];
+#pragma unroll
+    for (int y = 0; y < STEP; y += 16) tc_store16(to + (uint32_t)(x + y), s + y);
+  }
+  tc_wait_st();
+}
+
 struct TcArgs {
   int64_t rows = 0, cols = 0;   // the result's
   int tiles_l = 0, tiles_c = 0;  // tiles along the lanes (A) and the columns (B) of a tile
   int kblocks = 0, splits = 1, per_split = 0;  // stages of kk
   int ksteps = 0;                              // 16 of kk
+  int fold = 0;                                // stages a piece of a 16-bit sum covers
   bool a_mn = false, b_mn = false;
   uint32_t idesc = 0;
   Epilogue e;
@@ -183,30 +214,33 @@ __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* s
   const uint64_t ad0 = swizzled_desc(smem_addr(smem), C::BK * 128, 1024);
   const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * C::A_BYTES), C::BK * 128, 1024);
   Ring<C::S> ring;
-  Ring<2> acc;
+  // the accumulator in turn and the one that the sum began in; bit b: the parity of accumulator b's uses
+  uint32_t acc = 0, home = 0, uses = 0;
   bool ready = false;  // the stage in turn was seen full while the last one's products were issued
   int k0, k1;
   while (tile(k0, k1)) {
-    int left = 0;  // stages of the sum in hand
+    int left = 0;  // stages of the piece in hand
     for (int kb = k0; kb < k1; ++kb) {
       const bool fresh = left == 0;
       if (fresh) {
-        left = PL == 3 ? min(CHUNK, k1 - kb) : k1 - kb;
-        if (!tc_wait(&tempty[acc.s], acc.phase ^ 1u, abort_word)) return false;
+        left = min(PL == 3 ? CHUNK : a.fold, k1 - kb);
+        if (!tc_wait(&tempty[acc], (uses >> acc & 1u) ^ 1u, abort_word)) return false;
       }
       if (!tc_wait(&full[ring.s], ring.phase, abort_word, ready)) return false;
       const uint32_t s = ring.s;
       ring.next();
       ready = mbar_test(&full[ring.s], ring.phase);
       tc_fence_after();
-      mma_stage<CG, C, PL>(tmem + acc.s * bn, ad0 + s * (uint32_t)(C::STAGE >> 4), bd0 + s * (uint32_t)(C::STAGE >> 4), a,
+      mma_stage<CG, C, PL>(tmem + acc * bn, ad0 + s * (uint32_t)(C::STAGE >> 4), bd0 + s * (uint32_t)(C::STAGE >> 4), a,
                            fresh, a.ksteps - kb * (C::BK / 16));
       mma_commit<CG>(&empty[s]);
       if (--left == 0) {
-        mma_commit<CG>(&tfull[acc.s]);
-        acc.next();
+        mma_commit<CG>(&tfull[acc]);
+        uses ^= 1u << acc;
+        acc = PL == 3 ? acc ^ 1u : home ^ 1u;  // (float32 takes them in turn)
       }
     }
+    home = acc;
   }
   return true;
 }
@@ -306,10 +340,24 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(group * C::COLS);
     const uint32_t te0 = CG == 2 ? cluster_addr(&tempty[0], 0) : smem_addr(&tempty[0]);
     unsigned char* buf = smem + (size_t)C::S * C::STAGE + (warp - 4) * Tile32<T>::BYTES;
+    bool ok = true;
     const bool wide_out = Finish<T>::wide(a.e.out, a.e.ldo), wide_z = Finish<T>::wide(a.e.Z, a.e.ldz),
                wide_r = Finish<T>::wide(a.e.R, a.e.ldr);
-    int acc = 0, turn = 0;
-    bool ok = true;
+    int turn = 0;
+    uint32_t acc = 0, uses = 0;  // as the products take them
+    // whether the products of accumulator x are there
+    auto wait_full = [&](uint32_t x) {
+      if (!(ok = warp_wait(&tfull[x], uses >> x & 1u, abort_word))) return false;
+      uses ^= 1u << x;
+      tc_fence_after();
+      return true;
+    };
+    // accumulator x may be taken again
+    auto release = [&](uint32_t x) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(te0 + x * 8);
+    };
     // (after an abort a warp goes on to meet the others at each tile's barrier, and does nothing else)
     for (int w = first; w < work; w += step, ++turn) {
       int l, c, k0, k1;
@@ -326,40 +374,40 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * C::EPI) : "memory");
       if (!ok) continue;
       if (group * C::COLS >= BN) {  // a narrow tile's spare warps only give its accumulators back
-        for (int kb = k0; kb < k1; kb += PL == 3 ? CHUNK : k1 - k0) {
-          if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(te0 + (uint32_t)((acc & 1) * 8));
-          ++acc;
+        const uint32_t home = acc;
+        for (int kb = k0; kb < k1; kb += PL == 3 ? CHUNK : a.fold) {
+          if (!wait_full(acc)) break;
+          release(acc);
+          acc = PL == 3 ? acc ^ 1u : home ^ 1u;
         }
         continue;
       }
       bias += group * C::COLS;
-      auto release = [&]() {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(te0 + (uint32_t)((acc & 1) * 8));
-        ++acc;
-      };
       using Tile = Tile32<T>;
       const T* R = static_cast<const T*>(a.e.R);
       // the residual's first rows are on their way while the products run
       uint4 next[Tile::CH];
       if (R && !part) Tile::fetch(next, R, a.e.ldr, wide_r, i0, a.rows, j0, a.cols);
 
-      uint32_t t = lane_base + (uint32_t)((acc & 1) * BN);
+      uint32_t held = acc;  // the accumulator with the whole sum
+      uint32_t t = lane_base + held * BN;
       if constexpr (PL == 1) {
-        if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) continue;
-        tc_fence_after();
+        const uint32_t other = held ^ 1u;
+        if (!wait_full(held)) continue;
+        for (int kb = k0 + a.fold; kb < k1 && wait_full(other); kb += a.fold)
+          fold_columns<C::COLS>(lane_base + other * BN, t, [&] { release(other); });
+        if (!ok) continue;
+        acc = other;
       } else {
         float sum[C::COLS];
 #pragma unroll
         for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
         for (int kb = k0; kb < k1; kb += CHUNK) {
-          if (kb > k0) release();
-          t = lane_base + (uint32_t)((acc & 1) * BN);
-          if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
-          tc_fence_after();
+          if (kb > k0) release(held);
+          held = acc;
+          t = lane_base + held * BN;
+          if (!wait_full(held)) break;
+          acc ^= 1u;
           add_columns<C::COLS>(t, sum);
         }
         if (!ok) continue;
@@ -389,7 +437,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           Tile32<float>::drain(buf, part, a.cols, a.cols % 4 == 0, i0, a.rows, j0 + x, a.cols);
           __syncwarp();
         }
-        release();
+        release(held);
         continue;
       }
 #pragma unroll 1
@@ -425,7 +473,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
         Tile::drain(buf, static_cast<T*>(a.e.out), a.e.ldo, wide_out, i0, a.rows, j0 + x, a.cols);
         __syncwarp();
       }
-      release();
+      release(held);
     }
   }
 
@@ -541,6 +589,19 @@ __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
     } else {
       ok = warp_wait(&tfull[0], 0, abort_word);
       tc_fence_after();
+      const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
+      uint32_t phase = 0;
+      for (int kb = k0 + a.fold; kb < k1 && ok; kb += a.fold, phase ^= 1u) {
+        if (!(ok = warp_wait(&tfull[1], phase, abort_word))) break;
+        tc_fence_after();
+        auto taken = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(smem_addr(&tempty[1]));
+        };
+        if (mine) fold_columns<C::COLS>(t + (uint32_t)BN, t, taken);
+        else taken();
+      }
     }
   }
 
@@ -696,6 +757,7 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   a.ksteps = (int)((p.K + 15) / 16);
   a.per_split = (a.kblocks + plan.splits - 1) / plan.splits;
   a.splits = (a.kblocks + a.per_split - 1) / a.per_split;  // none of them empty
+  a.fold = FOLD / bk;
   // a cluster's CTAs share the tile's 128 lanes out evenly, and each has work
   if (plan.cluster && (a.splits != plan.splits || 128 % a.splits != 0 || a.splits > 8)) return FXTX_ERR_UNSUPPORTED;
   a.a_mn = A.mn_major;

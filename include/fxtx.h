@@ -355,7 +355,8 @@ typedef enum {
  * OUT may equal R with ldo == ldr (in place); other overlaps of OUT or Z with anything
  * else are undefined. Any alignment and pitch is taken.
  *
- * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32. FXTX_F32 operands
+ * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32 (on the tensor cores, which cut
+ * each sum off: sums of terms of one sign come out up to 5e-5 of themselves short, whatever their length). FXTX_F32 operands
  * are split into three bfloat16 terms each and six of their nine products formed, each of
  * the others being at most 2^-26 of the whole; they must be below 3.39e38 in magnitude,
  * and an infinity gives NaN in what it reaches. (At most 16 rows, 8 with w_trans = 1, are

@@ -1,0 +1,58 @@
+"""Layers at the ends of their ranges: sums over hundreds of thousands of terms of one sign."""
+import pytest
+import torch
+
+import dense_linear_algebra_gb300 as fx
+
+pytestmark = pytest.mark.gpu
+
+
+def _positive(shape, dtype, seed, scale=1.0, spread=None):
+    """Values of 1 to 2 times `scale`; `spread`: its rows (0) or columns (1) each times a factor of 1 to 2 of their own."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    x = (torch.rand(shape, generator=gen, device="cuda") + 1) * scale
+    if spread is not None:
+        f = torch.rand(shape[spread], generator=gen, device="cuda") + 1
+        x *= f[:, None] if spread == 0 else f
+    return x.to(dtype)
+
+
+def _bias(got, A, B, rows, cols):
+    """The mean relative error of entries (rows, cols) of A^T B, in 64 bits, A and B taken a piece of their rows at a time."""
+    want = torch.zeros(len(rows), len(cols), dtype=torch.float64, device="cuda")
+    for at in range(0, A.shape[0], 100_000):
+        want += A[at:at + 100_000][:, rows].double().t() @ B[at:at + 100_000][:, cols].double()
+    return float((got[rows][:, cols].double() / want - 1).mean())
+
+
+def _some(n):
+    return torch.linspace(0, n - 1, min(n, 64)).long().cuda()
+
+
+# Sums of positive terms: the tensor cores add 16 terms at a time to an accumulator, and drop what lies below its last
+# bit: at most 2^-23 of it. If at most 16,384 terms stay there, 1,024 such steps leave at most 1024 * 2^-23 of half the sum (it
+# grows evenly) on average, 2^-14, an eighth of float16's rounding. Roundings to the type average out over entries of 4,096 sizes:
+# w over the square root of 3 * 4096, 2^-14.8 for bfloat16.
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16], ids=str)
+@pytest.mark.parametrize("m,n,k", [(300_000, 4096, 2048), (400_001, 264, 200)])
+def test_long_gradient_sums(m, n, k, dtype):
+    X, G = _positive((m, n), dtype, 1, spread=1), _positive((m, k), dtype, 2, 1 / 128, spread=1)
+    W = torch.zeros(n, k, dtype=dtype, device="cuda")
+    _, dW, db = fx.linear_grad(G, X, W, need=(False, True, True))
+    assert fx.device_error() == fx.FXTX_OK
+    w = 2.0**-8 if dtype == torch.bfloat16 else 2.0**-11
+    assert abs(_bias(dW, X, G, _some(n), _some(k))) <= 2.0**-14 + w / 4096**0.5
+    assert float((db.double() / G.double().sum(0) - 1).abs().max()) <= 2.0**-14 + w
+
+
+@pytest.mark.parametrize("w_t", [False, True])
+@pytest.mark.parametrize("m,n,k", [(40, 1_000_000, 512), (1, 600_001, 96), (3000, 200_000, 2560)])
+def test_long_layer_sums(m, n, k, w_t):
+    dtype = torch.float16
+    X, W = _positive((m, n), dtype, 3, 1 / 512, 0), _positive((k, n) if w_t else (n, k), dtype, 4, spread=0 if w_t else 1)
+    W = W.t() if w_t else W
+    got, Z = fx.linear(X, W, pre=True)
+    assert fx.device_error() == fx.FXTX_OK
+    assert torch.equal(got, Z)
+    assert abs(_bias(got, X.t(), W, _some(m), _some(k))) <= 2.0**-14 + 2.0**-11 / (min(m, 64) * 64) ** 0.5
