@@ -24,6 +24,10 @@
 // (the rest is at most 2^-26 of a term); sums over rows leave the tensor cores after each 16 rows and
 // are added in fp32 registers. D stays in fp32 but for that split; of 16-bit types it is rounded
 // to the type, as the products take it.
+//
+// 16 bits: a warp's dW stays in the products' accumulators, which cut off 1e-7 of a sum of terms of one sign every
+// 16 rows. From 8,192 rows a warp on (20,000,000 in all) more CTAs than fit are launched instead, so
+// that 5e-5 is left at most, a tenth of float16's rounding; 200,000,000 rows on a grid that fits were 5.1e-4 off.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,6 +42,7 @@ namespace fxtx {
 namespace {
 
 constexpr int THREADS = 128, WARPS = THREADS / 32;
+constexpr int64_t MOST = 512;  // times 16 rows that a warp adds to its 16-bit dW
 
 struct ThinArgs {
   int64_t m;
@@ -525,7 +530,9 @@ cudaError_t launch_layer(const ThinArgs& a, int sm_count, cudaStream_t st) {
 
 template <typename T, int KN, int KC, bool DX, bool DW>
 fxtx_status_t launch_grad(ThinArgs a, int sm_count, cudaStream_t st) {
-  const unsigned ctas = grid_of<thin_grad_kernel<T, KN, KC, DX, DW>>(a.m, sm_count);
+  unsigned ctas = grid_of<thin_grad_kernel<T, KN, KC, DX, DW>>(a.m, sm_count);
+  if (DW && sizeof(T) == 2)
+    ctas = (unsigned)std::max<int64_t>(ctas, (a.m + 16 * WARPS * MOST - 1) / (16 * WARPS * MOST));
   constexpr int SIZE = KN * KC * 256 + 32 * 4 * KC;
   if (DW) {
     const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)ctas * SIZE * 4, st);

@@ -56,3 +56,17 @@ def test_long_layer_sums(m, n, k, w_t):
     assert fx.device_error() == fx.FXTX_OK
     assert torch.equal(got, Z)
     assert abs(_bias(got, X.t(), W, _some(m), _some(k))) <= 2.0**-14 + 2.0**-11 / (min(m, 64) * 64) ** 0.5
+
+
+@pytest.mark.parametrize("m,n,k", [(200_000_000, 8, 8), (40_000_000, 40, 60)])
+def test_long_thin_gradient_sums(m, n, k):
+    """The same for at most 64 features and outputs, where a warp adds 16 rows at a time: the same 2^-14, and the roundings of n k entries."""
+    X, G = _positive((m, n), torch.float16, 5, 2.0**-6, 1), _positive((m, k), torch.float16, 6, 2.0**-14, 1)
+    _, dW, db = fx.linear_grad(G, X, torch.zeros(n, k, dtype=torch.float16, device="cuda"), need=(False, True, True))
+    want, sums = torch.zeros(n, k, dtype=torch.float64, device="cuda"), torch.zeros(k, dtype=torch.float64, device="cuda")
+    for at in range(0, m, 4_000_000):
+        g = G[at:at + 4_000_000].double()
+        want += X[at:at + 4_000_000].double().t() @ g
+        sums += g.sum(0)
+    assert abs(float((dW.double() / want - 1).mean())) <= 2.0**-14 + 2.0**-11 / (n * k) ** 0.5
+    assert float((db.double() / sums - 1).abs().max()) <= 2.0**-14 + 2.0**-11
