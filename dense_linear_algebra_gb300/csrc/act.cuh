@@ -1,13 +1,16 @@
 // act.cuh — the activations and their slopes, in fp32.
 //
 // They are evaluated for every entry of a result, in epilogues that have few warps to hide
-// them, so the forms are the cheapest that keep fp32 accuracy: one ex2.approx (the exponential is
-// then off by about 1.2 |x| + 2 units in its last place), one rcp.approx (1 unit), both with
-// subnormal numbers taken as zero, and no difference of nearly equal terms. With expf, erff, tanhf
-// and IEEE division a tall layer (1,000,000 x 32, 32 outputs, silu) spent half of its time here.
-//   gelu       the complementary error function q of |z| / sqrt(2) by Abramowitz and Stegun 7.1.26
-//              (absolute error 1.5e-7): z (1 - q / 2) for z >= 0, z q / 2 below; its
-//              exponential exp(-z^2 / 2) is the slope's too
+// them: with expf, erff, tanhf and IEEE division a tall layer (1,000,000 x 32, 32 outputs, silu) spent half
+// of its time here. One exponential and one or two rcp.approx (1 unit in the last place, subnormal
+// results zero) each; the exponential is expf for float32 layers (gelu: ex2.approx of an exponent in two
+// parts), and plain ex2.approx, off by about 1.2 |x| + 2 units and zero where subnormal, for results that are
+// rounded to 16 bits.
+//   gelu       q = erfc(|z| / sqrt(2)) as exp(-z^2 / 2) times a polynomial in t = 1 / (1 + c |z| / sqrt(2)), the form of Abramowitz
+//              and Stegun 7.1.26 with the relative error made small instead of the absolute one, up to
+//              |z| = 13.5 (coefficients by iterated weighted least squares; c = 0.5: 4.3e-8, c = 0.3725 and two
+//              fewer of them for 16 bits: 5.7e-7): z (1 - q / 2) for z >= 0, z q / 2 below, so that the tail
+//              keeps its digits; the exponential is the slope's too
 //   gelu_tanh  z sigmoid(2 u), which is 0.5 z (1 + tanh(u)); with s = sigmoid(2 u) its slope is
 //              s + z s (1 - s) 2 u'
 #pragma once
@@ -23,7 +26,9 @@ constexpr float kRootTwoPi = 0.39894228040143267794f;  // 1 / sqrt(2 pi)
 constexpr float kTanh0 = 1.59576912160573071176f;      // 2 sqrt(2 / pi)
 constexpr float kTanh1 = 0.044715f;
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kHalfLog2e = -0.5f * kLog2e;  // and what a float of it leaves out
+constexpr float kHalfLog2eRest = (float)(-0.5 * 1.44269504088896340736 - (double)kHalfLog2e);
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -35,52 +40,81 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float sigmoid(float z) { return rcp(1.f + ex2(-kLog2e * z)); }
 
-// erfc(|z| / sqrt(2)) and exp(-z^2 / 2).
-__device__ __forceinline__ float erfc_half(float z, float& gauss) {
-  const float t = rcp(fmaf(0.3275911f * kRootHalf, fabsf(z), 1.f));
-  gauss = ex2(-0.5f * kLog2e * z * z);
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  return p * t * gauss;
+// The exponential for layers of type T.
+template <typename T>
+__device__ __forceinline__ float exp_of(float x) {
+  if constexpr (sizeof(T) == 4) return expf(x);
+  return ex2(kLog2e * x);
 }
 
-// A NaN stays a NaN in each.
-template <int ACT>
+template <typename T>
+__device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + exp_of<T>(-v)); }
+
+// A polynomial in t, its highest coefficient first.
+__device__ __forceinline__ float horner(float, float p) { return p; }
+template <typename... C>
+__device__ __forceinline__ float horner(float t, float p, float c, C... rest) {
+  return horner(t, fmaf(p, t, c), rest...);
+}
+
+// erfc(|z| / sqrt(2)) and exp(-z^2 / 2).
+template <typename T>
+__device__ __forceinline__ float erfc_half(float z, float& gauss) {
+  if constexpr (sizeof(T) == 4) {
+    // the exponent -z^2 log2(e) / 2 with what its roundings leave out (beyond 16 the exponential is zero)
+    const float a = fminf(fabsf(z), 16.f), h = a * a, x = kHalfLog2e * h;
+    float rest = fmaf(kHalfLog2e, h, -x);
+    rest = fmaf(kHalfLog2eRest, h, rest);
+    rest = fmaf(kHalfLog2e, fmaf(a, a, -h), rest);
+    gauss = ex2(x);
+    gauss = fmaf(gauss, kLn2 * rest, gauss);
+    const float t = rcp(fmaf(0.5f * kRootHalf, fabsf(z), 1.f));
+    return t * gauss *
+           horner(t, -0.05890960971f, 0.2837944093f, -0.4855764104f, 0.2762003024f, -0.0253320584f, 0.2021358148f,
+                  0.2432441336f, 0.282355836f, 0.2820875401f);
+  } else {
+    gauss = ex2(kHalfLog2e * z * z);
+    const float t = rcp(fmaf(0.3725f * kRootHalf, fabsf(z), 1.f));
+    return t * gauss *
+           horner(t, -0.1396021335f, 0.4141580827f, -0.161081597f, 0.3023959233f, 0.1588338403f, 0.2154489112f,
+                  0.2098469368f);
+  }
+}
+
+// A NaN stays a NaN in each. T: the layer's type.
+template <int ACT, typename T>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (ACT == FXTX_ACT_RELU) return z < 0.f ? 0.f : z;
   if constexpr (ACT == FXTX_ACT_GELU) {
     float gauss;
-    const float q = 0.5f * erfc_half(z, gauss);
+    const float q = 0.5f * erfc_half<T>(z, gauss);
     return z * (z < 0.f ? q : 1.f - q);
   }
-  if constexpr (ACT == FXTX_ACT_GELU_TANH) return z * sigmoid(kTanh0 * z * fmaf(kTanh1 * z, z, 1.f));
-  if constexpr (ACT == FXTX_ACT_SILU) return z * sigmoid(z);
-  if constexpr (ACT == FXTX_ACT_SIGMOID) return sigmoid(z);
+  if constexpr (ACT == FXTX_ACT_GELU_TANH) return z * sigmoid<T>(kTanh0 * z * fmaf(kTanh1 * z, z, 1.f));
+  if constexpr (ACT == FXTX_ACT_SILU) return z * sigmoid<T>(z);
+  if constexpr (ACT == FXTX_ACT_SIGMOID) return sigmoid<T>(z);
   return z;
 }
 
-template <int ACT>
+template <int ACT, typename T>
 __device__ __forceinline__ float slope_of(float z) {
   if constexpr (ACT == FXTX_ACT_RELU) return z <= 0.f ? 0.f : 1.f;
   if constexpr (ACT == FXTX_ACT_GELU) {
     float gauss;
-    const float q = 0.5f * erfc_half(z, gauss);
+    const float q = 0.5f * erfc_half<T>(z, gauss);
     return fmaf(z * kRootTwoPi, gauss, z < 0.f ? q : 1.f - q);
   }
   if constexpr (ACT == FXTX_ACT_GELU_TANH) {
-    const float z2 = kTanh1 * z * z, s = sigmoid(kTanh0 * z * (1.f + z2));
+    const float z2 = kTanh1 * z * z, s = sigmoid<T>(kTanh0 * z * (1.f + z2));
     return fmaf(z * s * (1.f - s) * kTanh0, fmaf(3.f, z2, 1.f), s);
   }
   if constexpr (ACT == FXTX_ACT_SILU) {
-    const float s = sigmoid(z);
+    const float s = sigmoid<T>(z);
     return s * fmaf(z, 1.f - s, 1.f);
   }
   if constexpr (ACT == FXTX_ACT_SIGMOID) {
-    const float s = sigmoid(z);
+    const float s = sigmoid<T>(z);
     return s * (1.f - s);
   }
   return 1.f;

@@ -65,7 +65,7 @@ struct Finish {
     if (i >= rows || j >= cols) return;
     if (e.bias) c += to_f32(static_cast<const T*>(e.bias)[j]);
     if (e.Z) static_cast<T*>(e.Z)[i * e.ldz + j] = from_f32<T>(c);
-    with_act(e.act, [&](auto act) { c = act_of<decltype(act)::value>(c); });
+    with_act(e.act, [&](auto act) { c = act_of<decltype(act)::value, T>(c); });
     if (e.R) c += to_f32(static_cast<const T*>(e.R)[i * e.ldr + j]);
     static_cast<T*>(e.out)[i * e.ldo + j] = from_f32<T>(c);
   }
@@ -86,7 +86,7 @@ struct Finish {
     if (e.Z) store<NV>(static_cast<T*>(e.Z) + i * e.ldz + j, n, wide_z, c);
     with_act(e.act, [&](auto act) {
 #pragma unroll
-      for (int q = 0; q < NV; ++q) c[q] = act_of<decltype(act)::value>(c[q]);
+      for (int q = 0; q < NV; ++q) c[q] = act_of<decltype(act)::value, T>(c[q]);
     });
     if (e.R) {
       load<NV>(static_cast<const T*>(e.R) + i * e.ldr + j, n, wide_r, x);

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           get(x + y, v);
           with_act(a.e.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = act_of<decltype(act)::value>(v[i]);
+            for (int i = 0; i < 16; ++i) v[i] = act_of<decltype(act)::value, T>(v[i]);
           });
           if (R) Tile::add(buf, y, v);
           Tile::put(buf, y, v);

@@ -96,7 +96,7 @@ __device__ __forceinline__ void slope(const SlopeArgs& a, const SlopeGrid& grid,
           float z[8];
           load8(Z + r * a.ldz, n, wz, z);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) g[i] *= slope_of<ACT>(z[i]);
+          for (int i = 0; i < 8; ++i) g[i] *= slope_of<ACT, T>(z[i]);
         }
         if (a.D != nullptr) store8<T>(a.D, r * a.ldd + col, a.d_planes, n, wd, g);
 #pragma unroll

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, (thin_ctas<T, KN, KC>())) thin_grad_k
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4 * KC; ++i) d[h][i] *= slope_of<ACT>(z[h][i]);
+          for (int i = 0; i < 4 * KC; ++i) d[h][i] *= slope_of<ACT, T>(z[h][i]);
       }
     });
     if constexpr (DX) {
