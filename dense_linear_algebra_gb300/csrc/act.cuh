@@ -5,14 +5,17 @@
 // of its time here. One exponential and one or two rcp.approx (1 unit in the last place, subnormal
 // results zero) each; the exponential is expf for float32 layers (gelu: ex2.approx of an exponent in two
 // parts), and plain ex2.approx, off by about 1.2 |x| + 2 units and zero where subnormal, for results that are
-// rounded to 16 bits.
+// rounded to 16 bits. With v the sigmoid's argument:
 //   gelu       q = erfc(|z| / sqrt(2)) as exp(-z^2 / 2) times a polynomial in t = 1 / (1 + c |z| / sqrt(2)), the form of Abramowitz
 //              and Stegun 7.1.26 with the relative error made small instead of the absolute one, up to
 //              |z| = 13.5 (coefficients by iterated weighted least squares; c = 0.5: 4.3e-8, c = 0.3725 and two
 //              fewer of them for 16 bits: 5.7e-7): z (1 - q / 2) for z >= 0, z q / 2 below, so that the tail
 //              keeps its digits; the exponential is the slope's too
-//   gelu_tanh  z sigmoid(2 u), which is 0.5 z (1 + tanh(u)); with s = sigmoid(2 u) its slope is
-//              s + z s (1 - s) 2 u'
+//   sigmoid    s and 1 - s both from e = exp(-|v|), as 1 / (1 + e) and e / (1 + e): the slopes use both,
+//              and 1 - s as a difference would leave nothing of a slope beyond v = 17
+//   gelu_tanh  z sigmoid(v), v = 2 u, which is 0.5 z (1 + tanh(u)); its slope is s + z s (1 - s) v'
+// The slopes of gelu, gelu_tanh and silu cross zero below z = 0, as a difference of two terms; they are accurate
+// to a few units of the larger one. The rounding of v itself leaves about 3 |v| units in gelu_tanh's tail.
 #pragma once
 
 #include <type_traits>
@@ -50,6 +53,14 @@ __device__ __forceinline__ float exp_of(float x) {
 
 template <typename T>
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.f + exp_of<T>(-v)); }
+
+// sigmoid(v), with 1 - sigmoid(v) beside it.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float v, float& rest) {
+  const float e = exp_of<T>(-fabsf(v)), r = rcp(1.f + e), x = e * r;
+  rest = v < 0.f ? r : x;
+  return v < 0.f ? x : r;
+}
 
 // A polynomial in t, its highest coefficient first.
 __device__ __forceinline__ float horner(float, float p) { return p; }
@@ -106,16 +117,20 @@ __device__ __forceinline__ float slope_of(float z) {
     return fmaf(z * kRootTwoPi, gauss, z < 0.f ? q : 1.f - q);
   }
   if constexpr (ACT == FXTX_ACT_GELU_TANH) {
-    const float z2 = kTanh1 * z * z, s = sigmoid<T>(kTanh0 * z * (1.f + z2));
-    return fmaf(z * s * (1.f - s) * kTanh0, fmaf(3.f, z2, 1.f), s);
+    const float z2 = kTanh1 * z * z;
+    float rest;
+    const float s = sigmoid<T>(kTanh0 * z * (1.f + z2), rest);
+    return fmaf(z * s * rest * kTanh0, fmaf(3.f, z2, 1.f), s);
   }
   if constexpr (ACT == FXTX_ACT_SILU) {
-    const float s = sigmoid<T>(z);
-    return s * fmaf(z, 1.f - s, 1.f);
+    float rest;
+    const float s = sigmoid<T>(z, rest);
+    return s * fmaf(z, rest, 1.f);
   }
   if constexpr (ACT == FXTX_ACT_SIGMOID) {
-    const float s = sigmoid<T>(z);
-    return s * (1.f - s);
+    float rest;
+    const float s = sigmoid<T>(z, rest);
+    return s * rest;
   }
   return 1.f;
 }

@@ -71,3 +71,13 @@ def test_gelu(dtype, span):
     a, size, s, x = values("gelu", z.double())
     check(act_of(z, "gelu"), a, tolerance("gelu", dtype, a.abs(), x), z)
     check(slope_of(z, "gelu"), s, tolerance("gelu", dtype, size, x), z)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("act,span", [("sigmoid", 80.0), ("sigmoid", 20.0), ("silu", 80.0), ("silu", 10.0),
+                                      ("gelu_tanh", 8.0), ("gelu_tanh", 3.0)])
+def test_sigmoid_forms(act, span, dtype):
+    z = points(dtype, span)
+    a, size, s, x = values(act, z.double())
+    check(act_of(z, act), a, tolerance(act, dtype, a.abs(), x), z)
+    check(slope_of(z, act), s, tolerance(act, dtype, size, x), z)
