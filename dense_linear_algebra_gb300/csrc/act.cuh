@@ -120,7 +120,9 @@ __device__ __forceinline__ float slope_of(float z) {
     const float z2 = kTanh1 * z * z;
     float rest;
     const float s = sigmoid<T>(kTanh0 * z * (1.f + z2), rest);
-    return fmaf(z * s * rest * kTanh0, fmaf(3.f, z2, 1.f), s);
+    const float slope = fmaf(z * s * rest * kTanh0, fmaf(3.f, z2, 1.f), s);
+    // s is 0 or 1 long before, and from 1e19 on z2 is an infinity
+    return fabsf(z) > 16.f ? (z < 0.f ? 0.f : 1.f) : slope;
   }
   if constexpr (ACT == FXTX_ACT_SILU) {
     float rest;

@@ -81,3 +81,20 @@ def test_sigmoid_forms(act, span, dtype):
     a, size, s, x = values(act, z.double())
     check(act_of(z, act), a, tolerance(act, dtype, a.abs(), x), z)
     check(slope_of(z, act), s, tolerance(act, dtype, size, x), z)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "sigmoid"])
+def test_far_out(act, dtype):
+    """Far out an activation is its argument or 0 (sigmoid: 1 or 0) and its slope 1 or 0 (sigmoid: 0); a NaN stays one."""
+    top = 6e4 if dtype == torch.float16 else 3e38
+    far = torch.tensor([200.0, 1e4, top] + ([] if dtype == torch.float16 else [1e10, 1e19, 1e20, 1e30])).to(dtype).cuda()
+    one = torch.ones_like(far)
+    assert torch.equal(act_of(far, act), one if act == "sigmoid" else far)
+    assert torch.equal(act_of(-far, act), torch.zeros_like(far))
+    assert torch.equal(slope_of(far, act), torch.zeros_like(far) if act == "sigmoid" else one)
+    assert torch.equal(slope_of(-far, act), torch.zeros_like(far))
+    nan = torch.full((3,), float("nan"), dtype=dtype, device="cuda")
+    assert torch.isnan(act_of(nan, act)).all()
+    if act != "relu":
+        assert torch.isnan(slope_of(nan, act)).all()
