@@ -44,7 +44,8 @@ struct FewArgs {
   const float* W;
   int64_t ld;
   Epilogue e;
-  int R, per;  // CTAs a cluster, features a CTA
+  int R;        // CTAs a cluster
+  int64_t per;  // features a CTA
   bool wide;   // W's rows (columns) are 16-byte aligned
 };
 
@@ -85,15 +86,16 @@ __global__ void __launch_bounds__(THREADS) few_kernel(const __grid_constant__ Fe
   const int R = a.R, rank = R > 1 ? (int)cluster_rank() : 0;
   const int c0 = (int)(blockIdx.x / (unsigned)R) * COLS;
   const int64_t i0 = (int64_t)blockIdx.y * MR;
-  const int j_begin = rank * a.per, j_end = min(a.n, j_begin + a.per);
+  // (64 bits: the last CTA's range, rounded up, and the slice after the last may begin beyond 2^31)
+  const int64_t j_begin = rank * a.per, j_end = min((int64_t)a.n, j_begin + a.per);
   const float* W = a.W;
   if (R > 1) cluster_arrive();  // waited for before the first store to another CTA
   after_previous();
 
   constexpr int AX = LC == 0 ? CC : VE;
   float acc[MR][AX] = {};
-  for (int j0 = j_begin; j0 < j_end; j0 += SLICE) {
-    const int len = min(SLICE, j_end - j0);
+  for (int64_t j0 = j_begin; j0 < j_end; j0 += SLICE) {
+    const int len = (int)min((int64_t)SLICE, j_end - j0);
     __syncthreads();
     // up to a whole step of the lanes; what lies beyond the features is zero
     const int padded = (len + 32 * VE - 1) / (32 * VE) * (32 * VE);
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(THREADS) few_kernel(const __grid_constant__ Fe
         float w[4][VE];
 #pragma unroll
         for (int s = 0; s < 4; ++s)
-          load_vec(W + (int64_t)(j0 + j + s) * a.ld + c, step, j + s < len ? a.k - c : 0, a.wide, w[s]);
+          load_vec(W + (j0 + j + s) * a.ld + c, step, j + s < len ? a.k - c : 0, a.wide, w[s]);
 #pragma unroll
         for (int i = 0; i < MR; ++i) {
           const float4 y = *reinterpret_cast<const float4*>(xs + i * SLICE + j);
@@ -203,7 +205,7 @@ cudaError_t launch(FewArgs a, int sm_count, cudaStream_t st) {
   // CTAs enough for two a SM, each with 64 features at least
   a.R = 1;
   while (a.R < 8 && blocks * chunks * a.R < 2 * sm_count && a.n >= 128 * a.R) a.R *= 2;
-  a.per = ((a.n + a.R - 1) / a.R + 31) / 32 * 32;
+  a.per = (((int64_t)a.n + a.R - 1) / a.R + 31) / 32 * 32;
   const void* k = (const void*)few_kernel<MR, LC>;
   cudaError_t e = ensure_smem(k, S::BYTES);
   if (e != cudaSuccess) return e;

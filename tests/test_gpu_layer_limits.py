@@ -1,4 +1,5 @@
-"""Layers at the ends of their ranges: sums over hundreds of thousands of terms of one sign."""
+"""Layers at the ends of their ranges: sums over hundreds of thousands of terms of one sign, and sums whose length comes close
+to 2^31."""
 import pytest
 import torch
 
@@ -70,3 +71,17 @@ def test_long_thin_gradient_sums(m, n, k):
         sums += g.sum(0)
     assert abs(float((dW.double() / want - 1).mean())) <= 2.0**-14 + 2.0**-11 / (n * k) ** 0.5
     assert float((db.double() / sums - 1).abs().max()) <= 2.0**-14 + 2.0**-11
+
+
+@pytest.mark.parametrize("w_t", [False, True])
+@pytest.mark.parametrize("n", [(1 << 31) - 1, (1 << 31) - 600])
+def test_few_rows_of_nearly_2_31_features(n, w_t):
+    """float32, one row: small whole numbers at both ends and in between, the sums exact."""
+    X = torch.zeros(1, n, device="cuda")
+    W = torch.zeros((2, n) if w_t else (n, 2), device="cuda")
+    W = W.t() if w_t else W
+    at = torch.cat([torch.arange(3), n // 8 * torch.arange(1, 8), torch.arange(n - 700, n, 7), torch.tensor([n - 1])]).cuda()
+    X[0, at] = torch.arange(1, at.numel() + 1, device="cuda").float() % 13
+    W[at, 0], W[at, 1] = 1.0, torch.arange(at.numel(), device="cuda").float() % 5
+    got = fx.linear(X, W)
+    assert torch.equal(got[0].double(), X[0, at].double() @ W[at].double())
