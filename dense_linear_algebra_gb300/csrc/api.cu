@@ -23,11 +23,14 @@ constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::once_flag g_dev_once[kMaxDevices];
 
-// Test hook: FXTX_FAIL_ALLOC=1 makes every workspace allocation fail (host side).
-bool fail_alloc() {
-  const char* s = getenv("FXTX_FAIL_ALLOC");
+// Test hooks: FXTX_FAIL_ALLOC=1 makes every workspace allocation fail, FXTX_FAIL_POOL=1 the
+// creation of the pool that some come from (host side).
+bool set_to_1(const char* name) {
+  const char* s = getenv(name);
   return s && s[0] == '1';
 }
+bool fail_alloc() { return set_to_1("FXTX_FAIL_ALLOC"); }
+bool fail_pool() { return set_to_1("FXTX_FAIL_POOL"); }
 
 }  // namespace
 
@@ -74,9 +77,32 @@ fxtx_status_t alloc_ws(void** p, size_t bytes, cudaStream_t st) {
   return FXTX_OK;
 }
 
-fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st) {
+namespace {
+
+// The library's pool on the current device d, made on first use; nullptr if it cannot be (the
+// next call tries again).
+cudaMemPool_t pool_of(int d) {
   static cudaMemPool_t pools[kMaxDevices];
-  static std::once_flag once[kMaxDevices];
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  if (pools[d] || fail_pool()) return pools[d];
+  cudaMemPoolProps props = {};
+  props.allocType = cudaMemAllocationTypePinned;
+  props.location.type = cudaMemLocationTypeDevice;
+  props.location.id = d;
+  cudaMemPool_t pool = nullptr;
+  uint64_t keep = 1ull << 30;
+  if (cudaMemPoolCreate(&pool, &props) == cudaSuccess) {
+    cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    pools[d] = pool;
+  }
+  cudaGetLastError();
+  return pools[d];
+}
+
+}  // namespace
+
+fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st) {
   *p = nullptr;
   if (bytes == 0) return FXTX_OK;
   if (fail_alloc()) return FXTX_ERR_ALLOC;
@@ -85,17 +111,8 @@ fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st) {
     cudaGetLastError();
     return FXTX_ERR_ALLOC;
   }
-  std::call_once(once[d], [d] {
-    cudaMemPoolProps props = {};
-    props.allocType = cudaMemAllocationTypePinned;
-    props.location.type = cudaMemLocationTypeDevice;
-    props.location.id = d;
-    uint64_t keep = 1ull << 30;
-    if (cudaMemPoolCreate(&pools[d], &props) != cudaSuccess) pools[d] = nullptr;
-    else cudaMemPoolSetAttribute(pools[d], cudaMemPoolAttrReleaseThreshold, &keep);
-    cudaGetLastError();
-  });
-  if (!pools[d] || cudaMallocFromPoolAsync(p, bytes, pools[d], st) != cudaSuccess) {
+  const cudaMemPool_t pool = pool_of(d);
+  if (!pool || cudaMallocFromPoolAsync(p, bytes, pool, st) != cudaSuccess) {
     cudaGetLastError();
     *p = nullptr;
     return FXTX_ERR_ALLOC;
