@@ -92,10 +92,15 @@ cudaMemPool_t pool_of(int d) {
   props.location.id = d;
   cudaMemPool_t pool = nullptr;
   uint64_t keep = 1ull << 30;
+  // creating a pool is no stream operation, but a capture under way (the process's first layer call may be in one) would
+  // be ended by it in the stricter modes
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  const bool exchanged = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
   if (cudaMemPoolCreate(&pool, &props) == cudaSuccess) {
     cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
     pools[d] = pool;
   }
+  if (exchanged) cudaThreadExchangeStreamCaptureMode(&mode);
   cudaGetLastError();
   return pools[d];
 }

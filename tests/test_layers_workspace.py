@@ -33,3 +33,22 @@ def test_a_pool_that_could_not_be_made_is_tried_again():
         del os.environ["FXTX_FAIL_POOL"]
         assert float((fx.linear(X, W) - X @ W).abs().max()) < 0.1
     """)
+
+
+@pytest.mark.gpu
+def test_first_call_in_a_capture():
+    """The first layer call of a process may be one that a graph captures."""
+    _child("""
+        import torch
+        import dense_linear_algebra_gb300 as fx
+        torch.manual_seed(0)
+        X, W = torch.randn(300, 200, device="cuda"), torch.randn(200, 136, device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = fx.linear(X, W)
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(got, fx.linear(X, W))
+        assert float((got - X @ W).abs().max()) < 0.1
+    """)
