@@ -87,11 +87,14 @@ def _on_stream(stream, index):
 
 def _call(fn, index, *args):
     """A C entry with the tensors' device current."""
-    if _current_device() == index:
-        rc = fn(*args)
-    else:
+    if _current_device() != index:
         with torch.cuda.device(index):
-            rc = fn(*args)
+            return _call(fn, index, *args)
+    rc = fn(*args)
+    if rc == _lib.FXTX_ERR_ALLOC and not torch.cuda.is_current_stream_capturing():
+        # no argument has been written over that a second call reads: once more, with what torch caches given back
+        torch.cuda.empty_cache()
+        rc = fn(*args)
     if rc:
         _check(rc, fn.__name__)
 
