@@ -316,15 +316,21 @@ class AdamW:
         return {name: getattr(self, name) for name in names}
 
     def state_dict(self) -> dict:
-        """The step count and copies of the held states (codes and scales for 8 bits)."""
-        return {"steps": self.steps} | {name: t.clone() for name, t in self._state().items()}
+        """The step count, the tensors' sizes and copies of the held states (codes and scales for 8 bits)."""
+        return {"steps": self.steps, "sizes": list(self._sizes)} | {name: t.clone() for name, t in self._state().items()}
 
     def load_state_dict(self, state: dict) -> None:
-        """Takes over what ``state_dict`` gave for tensors of the same sizes and the same ``state_bits``."""
+        """Takes over what ``state_dict`` gave for tensors of the same sizes and the same ``state_bits``. A state put together
+        by other means may leave ``sizes`` out: its tensors are then laid out by ``offsets``."""
         held = self._state()
         for name, t in held.items():
             if name not in state or state[name].dtype is not t.dtype or state[name].shape != t.shape:
                 raise ValueError(f"{name}: expected a {t.dtype} tensor of {t.numel()} elements")
+        if "sizes" in state and list(state["sizes"]) != self._sizes:
+            raise ValueError("sizes: the state is of other tensors, or of these in another order")
+        if "steps" not in state:
+            raise ValueError("steps: missing")
+        steps = int(state["steps"])
         for name, t in held.items():
             t.copy_(state[name])
-        self.steps = int(state["steps"])
+        self.steps = steps

@@ -1,4 +1,4 @@
-"""AdamW's held states where they go wrong quietly: blocks that are not finite."""
+"""AdamW's held states where they go wrong quietly: blocks that are not finite, and states of other tensors."""
 import pytest
 import torch
 
@@ -29,3 +29,30 @@ def test_8_bit_second_moment_of_a_block_that_is_not_finite(bad):
         if not abs(bad) < float("inf"):
             assert torch.isnan(m[:1000][block]).all()
     assert torch.isnan(p[block]).all() and torch.equal(p[~block], q[~block])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_states_of_other_tensors_are_refused(bits):
+    """The same number of elements in other tensors, in all or block by block, is not the same state; a state without its step count
+    is refused before anything is taken from it."""
+    def made(sizes):
+        return fx.AdamW([torch.zeros(n, device="cuda") for n in sizes], state_bits=bits)
+
+    a = made([256, 512])
+    a.step([torch.ones(256, device="cuda"), torch.ones(512, device="cuda")])
+    saved = a.state_dict()
+    for sizes in ([512, 256], [768], [255, 512], [256, 512, 0]):
+        b = made(sizes)
+        with pytest.raises(ValueError):
+            b.load_state_dict(saved)
+        assert b.steps == 0 and not b.exp_avg.any()
+    b = made([256, 512])
+    with pytest.raises(ValueError):
+        b.load_state_dict({k: v for k, v in saved.items() if k != "steps"})
+    assert b.steps == 0 and not b.exp_avg.any()
+    b.load_state_dict(saved)
+    assert b.steps == 1 and torch.equal(b.exp_avg, a.exp_avg)
+    # a state put together by hand may leave the sizes out
+    c = made([256, 512])
+    c.load_state_dict({k: v for k, v in saved.items() if k != "sizes"})
+    assert c.steps == 1 and torch.equal(c.exp_avg_sq, a.exp_avg_sq)
