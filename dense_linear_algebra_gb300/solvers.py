@@ -292,6 +292,19 @@ class MLP:
         return dW + db
 
 
+def _mean_square_gradients(net, err, saved):
+    """The gradients of mean(err^2) in the network's parameters."""
+    rate = 2.0 / err.numel()
+    if net.dtype != torch.float16:
+        return net.backward((err * rate).to(net.dtype), saved)
+    # float16 has nothing below 6e-8, where the gradient of a mean over millions of entries lies: it goes through the layers
+    # relative to the largest error, held down so that a sum over the rows stays below 4,096 times an entry of the layer's
+    # input, and gets its size in float32
+    top, part = err.abs().amax().clamp_min(1e-30), min(1.0, 4096 / err.shape[0])
+    grads = net.backward((err * (part / top)).to(net.dtype), saved)
+    return [g.float().mul_(top * (rate / part)) for g in grads]
+
+
 def mlp_adamw(X, B, hidden: int, layers: int = 1, act: str = "gelu", steps: int = 100, batch: int = 0, lr: float = 1e-3,
               weight_decay: float = 0.0, state_bits: int = 32, dtype=torch.float32, seed: int = 0):
     """Least squares by a residual network (``MLP``) trained with AdamW: min mean((net(X) - B)^2).
@@ -312,7 +325,7 @@ def mlp_adamw(X, B, hidden: int, layers: int = 1, act: str = "gelu", steps: int 
         out, saved = net.forward(X[at:at + batch], keep=True)
         err = out.float() - B[at:at + batch].float()
         info.losses.append(err.square().mean())
-        opt.step(net.backward((err * (2.0 / err.numel())).to(dtype), saved))
+        opt.step(_mean_square_gradients(net, err, saved))
         info.steps += 1
         at = at + batch if at + batch < m else 0
     return net, info
