@@ -355,15 +355,18 @@ typedef enum {
  * OUT may equal R with ldo == ldr (in place); other overlaps of OUT or Z with anything
  * else are undefined. Any alignment and pitch is taken.
  *
- * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32 (on the tensor cores, which cut
- * each sum off: sums of terms of one sign come out up to 5e-5 of themselves short, whatever their length). FXTX_F32 operands
- * are split into three bfloat16 terms each and six of their nine products formed, each of
- * the others being at most 2^-26 of the whole; they must be below 3.39e38 in magnitude,
- * and an infinity gives NaN in what it reaches. (At most 16 rows, 8 with w_trans = 1, are
- * plain fp32 multiply-adds.) The result is bitwise reproducible. Workspace is taken for
+ * Products of FXTX_BF16 and FXTX_F16 inputs are exact and summed in fp32 (on the tensor
+ * cores, which cut sums off: those of terms of one sign come out up to 5e-5 of themselves
+ * short, whatever their length). FXTX_F32 operands are split into three bfloat16 terms each
+ * and six of their nine products formed, each of the others being at most 2^-26 of the
+ * whole; they must be below 3.39e38 in magnitude, an infinity gives NaN in what it reaches,
+ * and each value is taken to within 2^-134 (a relative error from 2^-108 downwards). With
+ * more than 64 features or outputs, at most 16 rows (8 with w_trans = 1) are plain fp32
+ * multiply-adds instead. The result is bitwise reproducible. Workspace is taken for
  * the split, for 16-bit operands whose start or pitch is not a multiple of 16 bytes, and
- * for some long sums; FXTX_ERR_ALLOC: none was left. FXTX_ERR_INVALID_ARG: an unknown type or activation, a size that is
- * negative or not below 2^31, a pitch below its row, a missing pointer.
+ * for some long sums; FXTX_ERR_ALLOC: none was left. FXTX_ERR_INVALID_ARG: an unknown type
+ * or activation, a size that is negative or not below 2^31, a pitch below its row, a
+ * missing pointer.
  */
 fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
                           int64_t ldw, int w_trans, const void* b, fxtx_act_t act, const void* R, int64_t ldr, void* Z,
@@ -377,7 +380,8 @@ fxtx_status_t fxtx_linear(fxtx_type_t type, int64_t m, int64_t n, int64_t k, con
  * and the gradient at R is G itself. Each of DX, DW, DB may be NULL (not computed; W is
  * read only for DX, X only for DW). DW is stored as W is (w_trans, pitch lddw). Z is
  * what fxtx_linear kept, and not read when act is FXTX_ACT_NONE. The slope of relu is
- * 0 at z <= 0. D of a 16-bit type is rounded to it before the products; DB is summed from
+ * 0 at z <= 0. D of a 16-bit type is rounded to it before the products (float16: to 0
+ * below 3e-8, to an infinity from 65,520 on); DB is summed from
  * the unrounded values. m = 0 gives DW = 0 and DB = 0. Outputs must not overlap anything
  * else. Types, layouts, precision and errors are those of fxtx_linear.
  */

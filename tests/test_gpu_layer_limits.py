@@ -1,5 +1,5 @@
-"""Layers at the ends of their ranges: sums over hundreds of thousands of terms of one sign, and sums whose length comes close
-to 2^31."""
+"""Layers at the ends of their ranges: sums over hundreds of thousands of terms of one sign, sums whose length comes close
+to 2^31, float32 values that are not finite or tiny, and few float32 rows in slices."""
 import pytest
 import torch
 
@@ -85,3 +85,65 @@ def test_few_rows_of_nearly_2_31_features(n, w_t):
     W[at, 0], W[at, 1] = 1.0, torch.arange(at.numel(), device="cuda").float() % 5
     got = fx.linear(X, W)
     assert torch.equal(got[0].double(), X[0, at].double() @ W[at].double())
+
+
+@pytest.mark.parametrize("m,n,k", [(2, 200, 136), (6, 300, 200), (300, 200, 136), (300, 24, 40)])
+@pytest.mark.parametrize("w_t", [False, True])
+def test_float32_non_finite_stays_in_its_row(m, n, k, w_t):
+    """Where a row of float32 holds an infinity or a NaN, nothing finite comes out of it, and the other rows are what they were:
+    an infinity comes out as one or as a NaN (products of a value's three terms have no infinity)."""
+    X, W = _positive((m, n), torch.float32, 5), _positive((k, n) if w_t else (n, k), torch.float32, 6)
+    W = W.t() if w_t else W
+    want = fx.linear(X, W)
+    rest = [i for i in range(m) if i != 1]
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        Y = X.clone()
+        Y[1, 17] = bad
+        got = fx.linear(Y, W, act="relu" if bad != float("-inf") else None)
+        assert not torch.isfinite(got[1]).any()
+        assert torch.equal(got[rest], want[rest])
+        G = _positive((m, k), torch.float32, 7)
+        base = fx.linear_grad(G, X, W)
+        H = G.clone()
+        H[1, 3] = bad
+        dX, dW, db = fx.linear_grad(H, X, W)
+        assert not torch.isfinite(dX[1]).any() and torch.equal(dX[rest], base[0][rest])
+        cols = [j for j in range(k) if j != 3]
+        assert not torch.isfinite(dW[:, 3]).any() and torch.equal(dW[:, cols], base[1][:, cols])
+        assert not torch.isfinite(db[3]) and torch.equal(db[cols], base[2][cols])
+
+
+@pytest.mark.parametrize("w_t", [False, True])
+@pytest.mark.parametrize("m", [1, 5, 8, 16])
+@pytest.mark.parametrize("pitch", [3, 4])
+def test_few_rows_gradient_in_slices(m, pitch, w_t):
+    """float32 gradients of few rows from column slices (poisoned around them) are those of whole tensors, to fp32 rounding: 2 u S sqrt(K) of
+    two sums in orders of their own, 8 + 4 sqrt(K) taken."""
+    n, k = 272, 200
+    def cut(x):
+        wide = torch.full((x.shape[0], x.shape[1] + pitch), float("nan"), device="cuda")
+        wide[:, 1:1 + x.shape[1]] = x
+        return wide[:, 1:1 + x.shape[1]]
+    X, G, Z = (_positive(s, torch.float32, 8 + i) - 1.5 for i, s in enumerate([(m, n), (m, k), (m, k)]))
+    W = _positive((k, n) if w_t else (n, k), torch.float32, 11) - 1.5
+    turn = (lambda x: x.t()) if w_t else (lambda x: x)
+    got = fx.linear_grad(cut(G), cut(X), turn(cut(W)), pre=cut(Z), act="silu")
+    D = G.double() * torch.sigmoid(Z.double()) * (1 + Z.double() * torch.sigmoid(-Z.double()))
+    A, B = X.double(), turn(W).double()
+    for x, want, S, K in zip(got, (D @ B.t(), A.t() @ D, D.sum(0)),
+                             (D.abs() @ B.abs().t(), A.abs().t() @ D.abs(), D.abs().sum(0)), (k, m, m)):
+        # D itself to 32 u of its terms, as the slopes are
+        assert ((x.double() - want).abs() <= (8 + 4 * K**0.5 + 32) * 2.0**-24 * S + 2.0**-24 * want.abs() + 2.0**-20 * (S == 0)).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-34, 1e-36, 1e-38])
+@pytest.mark.parametrize("m,n,k", [(300, 200, 136), (300, 24, 40), (4, 200, 136)])
+def test_tiny_float32_values(m, n, k, size):
+    """float32 values so small that their terms end at bfloat16's smallest number, 2^-133: each is taken to within half of
+    that, on top of the usual (8 + 4 sqrt(K)) u S."""
+    X, W = (_positive(s, torch.float32, 12 + i) - 1.5 for i, s in enumerate([(m, n), (n, k)]))
+    X = X * size
+    got = fx.linear(X, W)
+    x, w = X.double(), W.double()
+    tol = (8 + 4 * n**0.5) * 2.0**-24 * (x.abs() @ w.abs()) + 2.0**-134 * w.abs().sum(0) + 2.0**-149
+    assert ((got.double() - x @ w).abs() <= tol).all()
