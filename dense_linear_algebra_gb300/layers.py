@@ -91,6 +91,8 @@ def _call(fn, index, *args):
         with torch.cuda.device(index):
             return _call(fn, index, *args)
     rc = fn(*args)
+    if not rc:
+        return
     if rc == _lib.FXTX_ERR_ALLOC and not torch.cuda.is_current_stream_capturing():
         # no argument has been written over that a second call reads: once more, with what torch caches given back
         torch.cuda.empty_cache()
