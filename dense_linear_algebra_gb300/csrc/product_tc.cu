@@ -41,6 +41,8 @@
 // first in one accumulator, the others in the second, which the epilogue warps add to the first in fp32 (rounded to
 // nearest). What is left is 5e-5, a tenth of float16's rounding; 300,000 rows in one piece were 2.7e-4 off. The products
 // wait for each addition: 1 to 3 % of sums of 16,384 to 65,536 (65,536 x 4096, 4096 outputs: dW 1,264 to 1,291 us).
+// Such sums have kernels of their own (LONG): the others' epilogue was slower for the code beside it (16384 x 256, 256
+// outputs: 8.6 us, 9.6).
 #include <cuda.h>
 
 #include <algorithm>
@@ -148,7 +150,7 @@ struct TcArgs {
   int tiles_l = 0, tiles_c = 0;  // tiles along the lanes (A) and the columns (B) of a tile
   int kblocks = 0, splits = 1, per_split = 0;  // stages of kk
   int ksteps = 0;                              // 16 of kk
-  int fold = 0;                                // stages a piece of a 16-bit sum covers
+  int fold = 0;                                // stages a piece of a long 16-bit sum covers; 0: sums in one piece
   bool a_mn = false, b_mn = false;
   uint32_t idesc = 0;
   Epilogue e;
@@ -205,17 +207,36 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, 
   else mma_steps<CG, C, PL, Q / 4>(d, ad, bd, a, fresh);
 }
 
+// The two accumulators as the products take them and the epilogue gives them back: in turn, or (HOME) the first piece of a
+// sum in one, the others in the second, and the next sum's first piece in the second too.
+template <bool HOME>
+struct Turns {
+  uint32_t s = 0, phase = 0;  // the accumulator in turn; its barriers' phase (HOME: both's, a bit each)
+  uint32_t home = 0;
+  __device__ __forceinline__ uint32_t parity() const { return HOME ? phase >> s & 1u : phase; }
+  // after a piece of a sum, the `last` or not
+  __device__ __forceinline__ void next(bool last) {
+    if constexpr (HOME) {
+      phase ^= 1u << s;
+      s = home ^ 1u;
+      if (last) home = s;
+    } else {
+      s ^= 1u;
+      if (s == 0) phase ^= 1u;
+    }
+  }
+};
+
 // The loop of a CTA's products over a ring of stages: one lane's. `tile(k0, k1)` gives the next range of
 // stages of kk, false after the last.
-template <int CG, class C, int PL, typename F>
+template <int CG, class C, int PL, bool LONG, typename F>
 __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* smem, uint64_t* full, uint64_t* empty,
                                                uint64_t* tfull, uint64_t* tempty, uint32_t tmem, int bn,
                                                volatile int* abort_word, F tile) {
   const uint64_t ad0 = swizzled_desc(smem_addr(smem), C::BK * 128, 1024);
   const uint64_t bd0 = swizzled_desc(smem_addr(smem + PL * C::A_BYTES), C::BK * 128, 1024);
   Ring<C::S> ring;
-  // the accumulator in turn and the one that the sum began in; bit b: the parity of accumulator b's uses
-  uint32_t acc = 0, home = 0, uses = 0;
+  Turns<PL == 3 || LONG> acc;
   bool ready = false;  // the stage in turn was seen full while the last one's products were issued
   int k0, k1;
   while (tile(k0, k1)) {
@@ -223,29 +244,27 @@ __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* s
     for (int kb = k0; kb < k1; ++kb) {
       const bool fresh = left == 0;
       if (fresh) {
-        left = min(PL == 3 ? CHUNK : a.fold, k1 - kb);
-        if (!tc_wait(&tempty[acc], (uses >> acc & 1u) ^ 1u, abort_word)) return false;
+        left = PL == 3 ? min(CHUNK, k1 - kb) : LONG ? min(a.fold, k1 - kb) : k1 - kb;
+        if (!tc_wait(&tempty[acc.s], acc.parity() ^ 1u, abort_word)) return false;
       }
       if (!tc_wait(&full[ring.s], ring.phase, abort_word, ready)) return false;
       const uint32_t s = ring.s;
       ring.next();
       ready = mbar_test(&full[ring.s], ring.phase);
       tc_fence_after();
-      mma_stage<CG, C, PL>(tmem + acc * bn, ad0 + s * (uint32_t)(C::STAGE >> 4), bd0 + s * (uint32_t)(C::STAGE >> 4), a,
+      mma_stage<CG, C, PL>(tmem + acc.s * bn, ad0 + s * (uint32_t)(C::STAGE >> 4), bd0 + s * (uint32_t)(C::STAGE >> 4), a,
                            fresh, a.ksteps - kb * (C::BK / 16));
       mma_commit<CG>(&empty[s]);
       if (--left == 0) {
-        mma_commit<CG>(&tfull[acc]);
-        uses ^= 1u << acc;
-        acc = PL == 3 ? acc ^ 1u : home ^ 1u;  // (float32 takes them in turn)
+        mma_commit<CG>(&tfull[acc.s]);
+        acc.next(PL == 3 || kb + 1 == k1);
       }
     }
-    home = acc;
   }
   return true;
 }
 
-template <typename T, int CG, int BN, int PL>
+template <typename T, int CG, int BN, int PL, bool LONG>
 __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                       const __grid_constant__ TcArgs a) {
@@ -324,7 +343,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
       int w = first;
-      issue_products<CG, C, PL>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
+      issue_products<CG, C, PL, LONG>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
         if (w >= work) return false;
         range(w, k0, k1);
         w += step;
@@ -344,11 +363,10 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
     const bool wide_out = Finish<T>::wide(a.e.out, a.e.ldo), wide_z = Finish<T>::wide(a.e.Z, a.e.ldz),
                wide_r = Finish<T>::wide(a.e.R, a.e.ldr);
     int turn = 0;
-    uint32_t acc = 0, uses = 0;  // as the products take them
-    // whether the products of accumulator x are there
-    auto wait_full = [&](uint32_t x) {
-      if (!(ok = warp_wait(&tfull[x], uses >> x & 1u, abort_word))) return false;
-      uses ^= 1u << x;
+    Turns<PL == 3 || LONG> acc;
+    // whether the products of the accumulator in turn are there
+    auto wait_full = [&]() {
+      if (!(ok = warp_wait(&tfull[acc.s], acc.parity(), abort_word))) return false;
       tc_fence_after();
       return true;
     };
@@ -374,11 +392,11 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
       asm volatile("bar.sync 1, %0;" ::"n"(32 * C::EPI) : "memory");
       if (!ok) continue;
       if (group * C::COLS >= BN) {  // a narrow tile's spare warps only give its accumulators back
-        const uint32_t home = acc;
-        for (int kb = k0; kb < k1; kb += PL == 3 ? CHUNK : a.fold) {
-          if (!wait_full(acc)) break;
-          release(acc);
-          acc = PL == 3 ? acc ^ 1u : home ^ 1u;
+        for (int kb = k0; kb < k1;) {
+          if (!wait_full()) break;
+          release(acc.s);
+          kb += PL == 3 ? CHUNK : LONG ? a.fold : k1 - k0;
+          acc.next(PL == 3 || kb >= k1);
         }
         continue;
       }
@@ -389,25 +407,30 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
       uint4 next[Tile::CH];
       if (R && !part) Tile::fetch(next, R, a.e.ldr, wide_r, i0, a.rows, j0, a.cols);
 
-      uint32_t held = acc;  // the accumulator with the whole sum
+      uint32_t held = acc.s;  // the accumulator with the whole sum
       uint32_t t = lane_base + held * BN;
       if constexpr (PL == 1) {
-        const uint32_t other = held ^ 1u;
-        if (!wait_full(held)) continue;
-        for (int kb = k0 + a.fold; kb < k1 && wait_full(other); kb += a.fold)
-          fold_columns<C::COLS>(lane_base + other * BN, t, [&] { release(other); });
-        if (!ok) continue;
-        acc = other;
+        if (!wait_full()) continue;
+        acc.next(!LONG || k0 + a.fold >= k1);
+        if constexpr (LONG) {
+          for (int kb = k0 + a.fold; kb < k1; kb += a.fold) {
+            if (!wait_full()) break;
+            const uint32_t x = acc.s;
+            fold_columns<C::COLS>(lane_base + x * BN, t, [&] { release(x); });
+            acc.next(kb + a.fold >= k1);
+          }
+          if (!ok) continue;
+        }
       } else {
         float sum[C::COLS];
 #pragma unroll
         for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
         for (int kb = k0; kb < k1; kb += CHUNK) {
           if (kb > k0) release(held);
-          held = acc;
+          held = acc.s;
           t = lane_base + held * BN;
-          if (!wait_full(held)) break;
-          acc ^= 1u;
+          if (!wait_full()) break;
+          acc.next(true);
           add_columns<C::COLS>(t, sum);
         }
         if (!ok) continue;
@@ -493,7 +516,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
 // One tile a cluster. The CTA of rank r of R finishes lanes r * 128 / R .. of the tile: every
 // CTA stores its partial sums of those lanes to r's shared memory (after the stages, which r
 // may still be reading), one cluster barrier, and r adds the R parts in order.
-template <typename T, int BN, int PL, bool SWAP>
+template <typename T, int BN, int PL, bool SWAP, bool LONG>
 __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
     product_split_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                          const __grid_constant__ TcArgs a) {
@@ -558,7 +581,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
   } else if (warp == 1) {
     if (elect_one()) {
       bool more = true;
-      ok = issue_products<1, C, PL>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
+      ok = issue_products<1, C, PL, LONG>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
         f0 = k0;
         f1 = k1;
         const bool m = more;
@@ -589,18 +612,20 @@ __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
     } else {
       ok = warp_wait(&tfull[0], 0, abort_word);
       tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
-      uint32_t phase = 0;
-      for (int kb = k0 + a.fold; kb < k1 && ok; kb += a.fold, phase ^= 1u) {
-        if (!(ok = warp_wait(&tfull[1], phase, abort_word))) break;
-        tc_fence_after();
-        auto taken = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(smem_addr(&tempty[1]));
-        };
-        if (mine) fold_columns<C::COLS>(t + (uint32_t)BN, t, taken);
-        else taken();
+      if constexpr (LONG) {
+        const uint32_t t = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * C::COLS);
+        uint32_t phase = 0;
+        for (int kb = k0 + a.fold; kb < k1 && ok; kb += a.fold, phase ^= 1u) {
+          if (!(ok = warp_wait(&tfull[1], phase, abort_word))) break;
+          tc_fence_after();
+          auto taken = [&] {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(smem_addr(&tempty[1]));
+          };
+          if (mine) fold_columns<C::COLS>(t + (uint32_t)BN, t, taken);
+          else taken();
+        }
       }
     }
   }
@@ -713,13 +738,17 @@ cudaError_t launch_clustered(const void* k, size_t smem, unsigned grid, int thre
 template <typename T, int CG, int BN, int PL>
 cudaError_t launch(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, int sm_count, cudaStream_t st) {
   const int64_t work = (int64_t)a.tiles_l * a.tiles_c * a.splits;
-  return launch_clustered((const void*)product_tc_kernel<T, CG, BN, PL>, TileCfg<CG, BN, PL>::BYTES,
+  const void* k = PL == 1 && a.fold ? (const void*)product_tc_kernel<T, CG, BN, PL, PL == 1>
+                                    : (const void*)product_tc_kernel<T, CG, BN, PL, false>;
+  return launch_clustered(k, TileCfg<CG, BN, PL>::BYTES,
                           (unsigned)(std::min<int64_t>(work, sm_count / CG) * CG), TileCfg<CG, BN, PL>::THREADS, CG, am, bm, a, st);
 }
 
 template <typename T, int BN, int PL, bool SWAP>
 cudaError_t launch_split(const CUtensorMap& am, const CUtensorMap& bm, const TcArgs& a, cudaStream_t st) {
-  return launch_clustered((const void*)product_split_kernel<T, BN, PL, SWAP>, SplitCfg<BN, PL>::BYTES,
+  const void* k = PL == 1 && a.fold ? (const void*)product_split_kernel<T, BN, PL, SWAP, PL == 1>
+                                    : (const void*)product_split_kernel<T, BN, PL, SWAP, false>;
+  return launch_clustered(k, SplitCfg<BN, PL>::BYTES,
                           (unsigned)(a.tiles_l * a.tiles_c * a.splits), SPLIT_THREADS, a.splits, am, bm, a, st);
 }
 
@@ -757,7 +786,7 @@ fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStre
   a.ksteps = (int)((p.K + 15) / 16);
   a.per_split = (a.kblocks + plan.splits - 1) / plan.splits;
   a.splits = (a.kblocks + a.per_split - 1) / a.per_split;  // none of them empty
-  a.fold = FOLD / bk;
+  if (PL == 1 && (int64_t)a.per_split * bk > FOLD) a.fold = FOLD / bk;
   // a cluster's CTAs share the tile's 128 lanes out evenly, and each has work
   if (plan.cluster && (a.splits != plan.splits || 128 % a.splits != 0 || a.splits > 8)) return FXTX_ERR_UNSUPPORTED;
   a.a_mn = A.mn_major;
