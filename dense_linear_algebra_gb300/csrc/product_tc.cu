@@ -41,8 +41,8 @@
 // first in one accumulator, the others in the second, which the epilogue warps add to the first in fp32 (rounded to
 // nearest). What is left is 5e-5, a tenth of float16's rounding; 300,000 rows in one piece were 2.7e-4 off. The products
 // wait for each addition: 1 to 3 % of sums of 16,384 to 65,536 (65,536 x 4096, 4096 outputs: dW 1,264 to 1,291 us).
-// Such sums have kernels of their own (LONG): the others' epilogue was slower for the code beside it (16384 x 256, 256
-// outputs: 8.6 us, 9.6).
+// Such sums have kernels of their own (LONG): beside that code the others took 1 to 2 % longer (512 x 4096, 4096
+// outputs: 17.9 us, 17.7).
 #include <cuda.h>
 
 #include <algorithm>
