@@ -55,7 +55,7 @@ Planes planes_of(const Operand& o, fxtx_type_t type, int64_t mn, int64_t k, char
   return x;
 }
 
-// Up to three operands and what has to be copied for them, in one workspace.
+// Up to two operands and what has to be copied for them, in one workspace.
 struct Prepared {
   fxtx_type_t type;
   PackArgs packs[2];
