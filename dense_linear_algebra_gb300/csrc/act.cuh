@@ -2,7 +2,7 @@
 //
 // They are evaluated for every entry of a result, in epilogues that have few warps to hide
 // them: with expf, erff, tanhf and IEEE division a tall layer (1,000,000 x 32, 32 outputs, silu) spent half
-// of its time here. One exponential and one or two rcp.approx (1 unit in the last place, subnormal
+// of its time here. One exponential and one rcp.approx (1 unit in the last place, subnormal
 // results zero) each; the exponential is expf for float32 layers (gelu: ex2.approx of an exponent in two
 // parts), and plain ex2.approx, off by about 1.2 |x| + 2 units and zero where subnormal, for results that are
 // rounded to 16 bits. With v the sigmoid's argument:

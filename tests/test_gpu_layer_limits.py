@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import dense_linear_algebra_gb300 as fx
+from test_gpu_linear import check_grad, check_linear
 
 pytestmark = pytest.mark.gpu
 
@@ -147,3 +148,20 @@ def test_tiny_float32_values(m, n, k, size):
     x, w = X.double(), W.double()
     tol = (8 + 4 * n**0.5) * 2.0**-24 * (x.abs() @ w.abs()) + 2.0**-134 * w.abs().sum(0) + 2.0**-149
     assert ((got.double() - x @ w).abs() <= tol).all()
+
+
+# Each way that a sum of more than 8,192 terms is laid over the tensor cores, entry by entry: narrow tiles by columns (16, 32 and
+# 64 rows), single CTAs and pairs with one tile or many in turn, and sums split through a workspace, some of them not into
+# equal pieces.
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("shape", [(10, 70_000, 20_000), (30, 20_000, 40_000), (60, 20_000, 40_000), (100, 20_000, 40_000),
+                                   (300, 20_000, 4096), (1000, 12_000, 4000), (5000, 8200, 5000), (40_000, 8300, 64),
+                                   (40_000, 8300, 100), (20_000, 33_000, 200), (1, 9000, 100_000), (300, 8193, 9728)], ids=str)
+def test_long_sums_entry_by_entry(shape, dtype):
+    check_linear(*shape, dtype, act="silu", w_t=shape[0] % 3 == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("shape", [(20_000, 300, 520), (9000, 4096, 264), (70_000, 72, 1000)], ids=str)
+def test_long_gradients_entry_by_entry(shape, dtype):
+    check_grad(*shape, dtype, act="gelu", w_t=shape[0] == 9000)
