@@ -20,6 +20,8 @@ The layer operators train and serve a model of more than one layer: ``linear`` i
 ``linear_grad`` its gradient, and ``AdamW`` updates a list of tensors in one launch,
 with its states in 32 bits or in 8.
 """
+import importlib
+
 from ._lib import (  # noqa: F401
     FXTX_ERR_ALLOC,
     FXTX_ERR_BAD_CSR,
@@ -69,8 +71,12 @@ from ._lib import (  # noqa: F401
     fxtx_dense_multi_f32,
     fxtx_dense_multi_f64,
     fxtx_device_error,
+    fxtx_embedding,
+    fxtx_embedding_grad,
     fxtx_epilogue_f32,
     fxtx_epilogue_f64,
+    fxtx_layer_norm,
+    fxtx_layer_norm_grad,
     fxtx_linear,
     fxtx_linear_grad,
     fxtx_multi_plan_describe,
@@ -82,11 +88,14 @@ from ._lib import (  # noqa: F401
 )
 
 
+_LAZY = dict.fromkeys(("AdamW", "linear", "linear_grad"), "layers") | dict.fromkeys(
+    ("layer_norm", "layer_norm_grad", "embedding", "embedding_grad"), "training")
+
+
 def __getattr__(name):
     """The layer operators need torch at import; the raw calls above do not."""
-    if name in ("AdamW", "linear", "linear_grad"):
-        from . import layers
-
-        value = globals()[name] = getattr(layers, name)
+    home = _LAZY.get(name)
+    if home is not None:
+        value = globals()[name] = getattr(importlib.import_module(f".{home}", __name__), name)
         return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

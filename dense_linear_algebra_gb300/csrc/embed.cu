@@ -1,0 +1,567 @@
+// embed.cu — the embedding lookup and its gradient:
+//     out_i = scale E[ids_i],   dE_v = scale * the sum of the rows of G with id v (zeros where there is none).
+//
+// Bound: HBM; the lookup reads each row once and writes it, the gradient reads G and writes dE once.
+//
+// The gradient sorts the ids, so that every row of dE is summed in registers, in the order of the positions, and
+// written once, with no atomic addition: the result is the same on every call. The sort is a stable radix sort of
+// (id, position), up to 9 bits a pass: each CTA counts its ids' digits, a second kernel turns the counts into places,
+// a third scatters, a warp ranking its 32 ids at a time by matching digits; up to 8,192 ids take one CTA and one
+// launch, in shared memory.
+//
+// The sorted positions are then cut into chunks. A worker (as many threads as a row has accesses of 16 bytes, up to
+// 256) adds a chunk's rows of G run by run. A run that begins and ends in the chunk is a row of dE; one that goes over
+// the chunk's ends becomes a partial sum in fp32, two a chunk at most, and the partial sums, sorted as they are, go
+// through the same kernel until one chunk holds them all. So a frequent id's thousands of rows are shared out evenly.
+// The rows of dE without an id are zeroed by further CTAs of the first of these launches, which look each row up
+// among the sorted ids.
+#include <algorithm>
+
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+#include "train.h"
+
+namespace fxtx {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int MAX_BITS = 9, RADIX = 1 << MAX_BITS;
+constexpr int ITEMS = 8, TILE = THREADS * ITEMS;        // ids a CTA of the sort takes
+constexpr int SMALL_THREADS = 1024, SMALL = SMALL_THREADS * ITEMS;
+constexpr int BATCH = 8;                                 // rows on their way at a time
+
+constexpr uint32_t NONE = 0xffffffffu, EMPTY = 0x80000000u;  // a partial sum's key: no run; a run's, with nothing to add
+
+// V neighbouring entries (of 16 bytes, or one; of float: V of them) from p on.
+template <typename S, int V>
+struct Piece {
+  static constexpr int B = V * sizeof(S);
+  uint4 v[B >= 16 ? B / 16 : 1];
+  __device__ __forceinline__ void load(const S* p) {
+    if constexpr (B >= 16) {
+#pragma unroll
+      for (int i = 0; i < B / 16; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+      static_assert(V == 1, "one entry");
+      *reinterpret_cast<S*>(&v[0]) = *p;
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (B >= 16 ? B / 16 : 1); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const S*>(v)[i]); }
+  __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<S*>(v)[i] = from_f32<S>(x); }
+  __device__ __forceinline__ void store(S* p) const {
+    if constexpr (B >= 16) {
+#pragma unroll
+      for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
+    } else {
+      *p = *reinterpret_cast<const S*>(&v[0]);
+    }
+  }
+};
+
+// The id at position i, `count` for one outside the table.
+__device__ __forceinline__ uint32_t id_at(const void* ids, bool wide, int64_t i, int64_t count) {
+  const int64_t v = wide ? static_cast<const int64_t*>(ids)[i] : (int64_t)static_cast<const int32_t*>(ids)[i];
+  return (uint32_t)(v < 0 || v >= count ? count : v);
+}
+
+// How the accesses of a row lie over threads: `tpr` threads a slab of the row, `groups` slabs a CTA in work.
+struct Shape {
+  int tpr = 1, groups = 1;
+  int64_t slabs = 1;
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) embed_kernel(const __grid_constant__ EmbedArgs a, const Shape s) {
+  constexpr int U = 4;
+  const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
+  const int64_t accesses = a.n / V, units = a.m * s.slabs;
+  after_previous();
+  for (int64_t w = (int64_t)blockIdx.x * s.groups + group; w < units; w += (int64_t)gridDim.x * s.groups) {
+    const int64_t i = w / s.slabs, first = (w - i * s.slabs) * s.tpr * U + t;
+    const uint32_t id = id_at(a.ids, a.ids64, i, a.count);
+    const bool in = id < a.count;
+    const T* p = static_cast<const T*>(a.src) + (int64_t)(in ? id : 0) * a.lds;
+    T* o = static_cast<T*>(a.out) + i * a.ldo;
+    Piece<T, V> x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = first + u * s.tpr;
+      if (in && c < accesses) x[u].load(p + c * V);
+      else x[u].zero();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t c = first + u * s.tpr;
+      if (c >= accesses) break;
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if (in) x[u].set(q, x[u].get(q) * a.scale);
+      x[u].store(o + c * V);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ the sort
+struct SortArgs {
+  const void* ids;
+  bool ids64;
+  int64_t m, count;
+  const uint2* from;  // (id, position); NULL: the ids themselves
+  uint2* to;
+  uint32_t *counts, *totals;  // [digit][CTA], [digit]
+  int64_t ctas;
+  int shift, bits;
+};
+
+__device__ __forceinline__ uint2 item(const SortArgs& a, int64_t i) {
+  if (i >= a.m) return make_uint2(NONE, 0);
+  return a.from ? a.from[i] : make_uint2(id_at(a.ids, a.ids64, i, a.count), (uint32_t)i);
+}
+__device__ __forceinline__ uint32_t digit_of(uint32_t key, int shift, int bits) { return (key >> shift) & ((1u << bits) - 1u); }
+
+// The warp's items (32 at a time, in order) ranked among its own of the same digit; `hist` counts them.
+__device__ __forceinline__ void rank_items(const uint2* x, int items, uint32_t* hist, int shift, int bits, uint32_t* rank) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    if (i >= items) break;
+    const bool in = x[i].x != NONE;
+    const uint32_t d = in ? digit_of(x[i].x, shift, bits) : NONE;
+    const uint32_t same = __match_any_sync(FULL_MASK, d), before = __popc(same & ((1u << lane) - 1u));
+    const uint32_t had = in ? hist[d] : 0;
+    __syncwarp();
+    if (in && before == 0) hist[d] = had + __popc(same);
+    __syncwarp();
+    rank[i] = had + before;
+  }
+}
+
+// An exclusive scan of v[0 .. n - 1] in shared memory by the whole CTA (n at most 2 RADIX); `warps` holds 32 words.
+__device__ __forceinline__ void scan(uint32_t* v, int n, uint32_t* warps) {
+  const int tid = threadIdx.x, lane = tid & 31, per = (n + (int)blockDim.x - 1) / (int)blockDim.x;
+  uint32_t own = 0;
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < n) own += v[tid * per + i];
+  uint32_t upto = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(FULL_MASK, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) warps[tid >> 5] = upto;
+  __syncthreads();
+  uint32_t at = upto - own;
+  for (int w = 0; w < tid >> 5; ++w) at += warps[w];
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < n) {
+      const uint32_t y = v[tid * per + i];
+      v[tid * per + i] = at;
+      at += y;
+    }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(THREADS) sort_count_kernel(const __grid_constant__ SortArgs a) {
+  __shared__ uint32_t hist[RADIX];
+  for (int d = threadIdx.x; d < 1 << a.bits; d += THREADS) hist[d] = 0;
+  __syncthreads();
+  after_previous();
+  const int64_t base = (int64_t)blockIdx.x * TILE;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const uint2 x = item(a, base + i * THREADS + threadIdx.x);
+    if (x.x != NONE) atomicAdd(&hist[digit_of(x.x, a.shift, a.bits)], 1u);
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < 1 << a.bits; d += THREADS) a.counts[d * a.ctas + blockIdx.x] = hist[d];
+}
+
+// counts: over the CTAs before, a warp a digit; totals: over all of them.
+__global__ void __launch_bounds__(THREADS) sort_places_kernel(const __grid_constant__ SortArgs a) {
+  const int lane = threadIdx.x & 31, d = (int)(blockIdx.x * (THREADS / 32)) + (int)(threadIdx.x >> 5);
+  after_previous();
+  if (d >= 1 << a.bits) return;
+  uint32_t* c = a.counts + d * a.ctas;
+  uint32_t sum = 0;
+  for (int64_t i = 0; i < a.ctas; i += 32) {
+    const uint32_t own = i + lane < a.ctas ? c[i + lane] : 0;
+    uint32_t upto = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(FULL_MASK, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (i + lane < a.ctas) c[i + lane] = sum + upto - own;
+    sum += __shfl_sync(FULL_MASK, upto, 31);
+  }
+  if (lane == 0) a.totals[d] = sum;
+}
+
+__global__ void __launch_bounds__(THREADS) sort_scatter_kernel(const __grid_constant__ SortArgs a) {
+  constexpr int WARPS = THREADS / 32;
+  __shared__ uint32_t hist[WARPS][RADIX], first[RADIX], warps[32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, digits = 1 << a.bits;
+  for (int d = tid; d < WARPS * RADIX; d += THREADS) (&hist[0][0])[d] = 0;
+  after_previous();
+  for (int d = tid; d < digits; d += THREADS) first[d] = a.totals[d];
+  uint2 x[ITEMS];
+  uint32_t rank[ITEMS];
+  const int64_t base = (int64_t)blockIdx.x * TILE + warp * 32 * ITEMS + lane;
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) x[i] = item(a, base + 32 * i);
+  __syncthreads();
+  rank_items(x, ITEMS, hist[warp], a.shift, a.bits, rank);
+  scan(first, digits, warps);
+  // where each warp's ids of a digit begin
+  for (int d = tid; d < digits; d += THREADS) {
+    uint32_t at = first[d] + a.counts[d * a.ctas + blockIdx.x];
+    for (int w = 0; w < WARPS; ++w) {
+      const uint32_t y = hist[w][d];
+      hist[w][d] = at;
+      at += y;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i)
+    if (x[i].x != NONE) a.to[hist[warp][digit_of(x[i].x, a.shift, a.bits)] + rank[i]] = x[i];
+}
+
+// All passes of up to SMALL ids, in one CTA: ids and positions in shared memory between passes.
+__global__ void __launch_bounds__(SMALL_THREADS) sort_small_kernel(const __grid_constant__ SortArgs a, int passes) {
+  extern __shared__ __align__(16) uint32_t shared[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps_n = (int)blockDim.x >> 5;
+  uint32_t *first = shared, *warps = first + RADIX, *hist = warps + 32;
+  uint2* held = reinterpret_cast<uint2*>(hist + warps_n * RADIX);
+  const int items = ((int)a.m + (int)blockDim.x - 1) / (int)blockDim.x, digits = 1 << a.bits;
+  const int base = warp * 32 * items + lane;
+  uint2 x[ITEMS];
+  uint32_t rank[ITEMS];
+  after_previous();
+  for (int p = 0; p < passes; ++p) {
+    const int shift = p * a.bits;
+    for (int d = tid; d < warps_n * RADIX; d += (int)blockDim.x) hist[d] = 0;
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (i >= items) break;
+      const int at = base + 32 * i;
+      x[i] = p == 0 ? item(a, at) : at < a.m ? held[at] : make_uint2(NONE, 0);
+    }
+    __syncthreads();
+    rank_items(x, items, hist + warp * RADIX, shift, a.bits, rank);
+    __syncthreads();
+    for (int d = tid; d < digits; d += (int)blockDim.x) {
+      uint32_t at = 0;
+      for (int w = 0; w < warps_n; ++w) {
+        const uint32_t y = hist[w * RADIX + d];
+        hist[w * RADIX + d] = at;
+        at += y;
+      }
+      first[d] = at;
+    }
+    __syncthreads();
+    scan(first, digits, warps);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (i >= items) break;
+      if (x[i].x == NONE) continue;
+      const uint32_t d = digit_of(x[i].x, shift, a.bits), at = first[d] + hist[warp * RADIX + d] + rank[i];
+      if (p + 1 < passes) held[at] = x[i];
+      else a.to[at] = x[i];
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------------------------------------ the sums
+struct ReduceArgs {
+  int64_t entries, n, count;
+  int chunk;              // entries a worker adds
+  const uint2* sorted;    // (id, row of src); NULL: partial sums, with their keys
+  const uint32_t* keys;
+  const void* src;
+  int64_t lds;
+  float scale;
+  void* out;
+  int64_t ldo;
+  float* part;            // [2 a chunk][n], and their keys; NULL where one chunk holds all
+  uint32_t* part_keys;
+  Shape shape;
+  int64_t sum_ctas;       // CTAs of sums; those beyond them zero `zero_rows` rows each
+  int zero_rows;
+};
+
+// Rows of dE without an id.
+template <typename T, int V>
+__device__ __forceinline__ void zero_rows(const ReduceArgs& a, int64_t row0) {
+  __shared__ uint32_t s_absent;
+  if (threadIdx.x < 32) {
+    const int64_t v = row0 + threadIdx.x;
+    const bool mine = (int)threadIdx.x < a.zero_rows && v < a.count;
+    // the first entry not below v
+    int64_t lo = 0, hi = mine ? a.entries : 0;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (a.sorted[mid].x < (uint32_t)v) lo = mid + 1;
+      else hi = mid;
+    }
+    const bool there = mine && lo < a.entries && a.sorted[lo].x == (uint32_t)v;
+    const uint32_t absent = __ballot_sync(FULL_MASK, mine && !there);
+    if (threadIdx.x == 0) s_absent = absent;
+  }
+  __syncthreads();
+  Piece<T, V> z;
+  z.zero();
+  const int64_t accesses = a.n / V;
+  for (uint32_t left = s_absent; left; left &= left - 1) {
+    T* p = static_cast<T*>(a.out) + (row0 + __ffs(left) - 1) * a.ldo;
+    for (int64_t c = threadIdx.x; c < accesses; c += blockDim.x) z.store(p + c * V);
+  }
+}
+
+template <typename S, typename T, int V>
+__global__ void __launch_bounds__(THREADS) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
+  after_previous();
+  if (blockIdx.x >= a.sum_ctas) {
+    zero_rows<T, V>(a, ((int64_t)blockIdx.x - a.sum_ctas) * a.zero_rows);
+    return;
+  }
+  const Shape& s = a.shape;
+  const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
+  const int64_t w = (int64_t)blockIdx.x * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t;
+  const int64_t e0 = chunk * a.chunk, e1 = min(a.entries, e0 + a.chunk);
+  if (group >= s.groups || e0 >= a.entries) return;
+  const bool mine = c < a.n / V, first_thread = c == 0;
+  auto key_at = [&](int64_t e) -> uint32_t { return a.sorted ? a.sorted[e].x : a.keys[e]; };
+  auto run_of = [](uint32_t key) { return key == NONE ? NONE : key & ~EMPTY; };
+  if (first_thread && a.part) a.part_keys[2 * chunk] = a.part_keys[2 * chunk + 1] = NONE;
+
+  float acc[V] = {};
+  uint32_t run = run_of(key_at(e0));
+  bool from_left = e0 > 0 && run_of(key_at(e0 - 1)) == run;
+  // the run in hand ends, in this chunk or beyond it
+  auto flush = [&](bool to_right) {
+    if (run < a.count) {
+      if (!from_left && !to_right) {
+        if (mine) {
+          Piece<T, V> o;
+#pragma unroll
+          for (int q = 0; q < V; ++q) o.set(q, acc[q] * a.scale);
+          o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
+        }
+      } else {
+        const int64_t slot = 2 * chunk + (from_left ? 0 : 1);
+        if (first_thread) {
+          a.part_keys[slot] = run;
+          if (from_left && to_right) a.part_keys[slot + 1] = run | EMPTY;  // a run's partial sums are neighbours
+        }
+        if (mine) {
+          Piece<float, V> o;
+#pragma unroll
+          for (int q = 0; q < V; ++q) o.set(q, acc[q]);
+          o.store(a.part + slot * a.n + c * V);
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) acc[q] = 0.f;
+    from_left = false;
+  };
+  for (int64_t e = e0; e < e1; e += BATCH) {
+    uint32_t key[BATCH];
+    Piece<S, V> x[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      key[i] = NONE;
+      int64_t row = e + i;
+      if (row < e1) {
+        if (a.sorted) {
+          const uint2 k = a.sorted[row];
+          key[i] = k.x;
+          row = k.y;
+        } else {
+          key[i] = a.keys[row];
+        }
+      }
+      // (an id outside the table is `count` and sorted last; NONE and EMPTY are above it)
+      if (mine && key[i] < a.count) x[i].load(static_cast<const S*>(a.src) + row * a.lds + c * V);
+      else x[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (e + i >= e1) break;
+      if (run_of(key[i]) != run) {
+        flush(false);
+        run = run_of(key[i]);
+      }
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[q] += x[i].get(q);
+    }
+  }
+  flush(e1 < a.entries && run_of(key_at(e1)) == run);
+}
+
+// ------------------------------------------------------------------------------------------------ on the host
+bool aligned(const void* p, int64_t ld, int size) { return ((uintptr_t)p & 15u) == 0 && ld * size % 16 == 0; }
+
+// `per` accesses a thread.
+Shape shape_of(int64_t accesses, int per) {
+  Shape s;
+  s.slabs = (accesses + (int64_t)THREADS * per - 1) / ((int64_t)THREADS * per);
+  const int64_t need = (accesses + s.slabs * per - 1) / (s.slabs * per);
+  if (need <= 32)
+    while (s.tpr < need) s.tpr *= 2;
+  else
+    s.tpr = (int)((need + 31) / 32 * 32);
+  s.groups = std::max(1, THREADS / s.tpr);
+  return s;
+}
+
+template <typename T, int V>
+cudaError_t lookup(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  const Shape s = shape_of(a.n / V, 4);
+  const int64_t ctas = std::min<int64_t>((a.m * s.slabs + s.groups - 1) / s.groups, (int64_t)dev.sm_count * 64);
+  return launch_kernel(embed_kernel<T, V>, dim3((unsigned)ctas), (unsigned)(s.tpr * s.groups), 0, st, a, s);
+}
+
+// The ids sorted into `to`, by way of `other`.
+cudaError_t sort_ids(const EmbedArgs& a, uint2* to, uint2* other, uint32_t* counts, int64_t ctas, cudaStream_t st) {
+  SortArgs s = {};
+  s.ids = a.ids;
+  s.ids64 = a.ids64;
+  s.m = a.m;
+  s.count = a.count;
+  s.counts = counts;
+  s.totals = counts + RADIX * ctas;
+  s.ctas = ctas;
+  int bits = 1;
+  while ((a.count >> bits) != 0) ++bits;  // of 0 .. count
+  const int passes = (bits + MAX_BITS - 1) / MAX_BITS;
+  s.bits = (bits + passes - 1) / passes;
+  if (a.m <= SMALL) {
+    s.to = to;
+    const int threads = (int)std::min<int64_t>(SMALL_THREADS, (a.m + 63) / 64 * 32);  // two ids a thread, up to 8
+    const size_t smem = ((size_t)RADIX + 32 + (size_t)threads / 32 * RADIX) * 4 + (size_t)a.m * 8;
+    const cudaError_t e = ensure_smem((const void*)sort_small_kernel, smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(sort_small_kernel, dim3(1), (unsigned)threads, smem, st, s, passes);
+  }
+  // the last pass ends in `to`
+  uint2* next = passes % 2 ? to : other;
+  for (int p = 0; p < passes; ++p) {
+    s.shift = p * s.bits;
+    s.to = next;
+    cudaError_t e = launch_kernel(sort_count_kernel, dim3((unsigned)ctas), THREADS, 0, st, s);
+    if (e == cudaSuccess)
+      e = launch_kernel(sort_places_kernel, dim3((unsigned)(((1 << s.bits) + THREADS / 32 - 1) / (THREADS / 32))), THREADS, 0, st, s);
+    if (e == cudaSuccess) e = launch_kernel(sort_scatter_kernel, dim3((unsigned)ctas), THREADS, 0, st, s);
+    if (e != cudaSuccess) return e;
+    s.from = next;
+    next = next == to ? other : to;
+  }
+  return cudaSuccess;
+}
+
+constexpr int CHUNK = 32;
+
+template <typename T, int V>
+fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  const int64_t tiles = (a.m + TILE - 1) / TILE, chunks = (a.m + CHUNK - 1) / CHUNK;
+  // the sorted ids, the counts, and two levels' partial sums, which take turns
+  auto up = [](int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); };
+  const int64_t deep = 2 * chunks, second = 2 * ((deep + CHUNK - 1) / CHUNK);
+  const size_t sort_bytes = up(a.m * 8), count_bytes = up((RADIX * tiles + RADIX) * 4);
+  const size_t part_bytes = chunks > 1 ? up(deep * a.n * 4) : 0, part2_bytes = chunks > 1 ? up(second * a.n * 4) : 0;
+  const size_t key_bytes = up(deep * 4);
+  char* ws = nullptr;
+  const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&ws), 2 * sort_bytes + count_bytes + part_bytes + part2_bytes + 2 * key_bytes, st);
+  if (r != FXTX_OK) return r;
+  char* at = ws;
+  auto take = [&](size_t bytes) {
+    char* p = at;
+    at += bytes;
+    return p;
+  };
+  uint2 *sorted = reinterpret_cast<uint2*>(take(sort_bytes)), *other = reinterpret_cast<uint2*>(take(sort_bytes));
+  uint32_t* counts = reinterpret_cast<uint32_t*>(take(count_bytes));
+  float* part[2] = {reinterpret_cast<float*>(take(part_bytes)), nullptr};
+  part[1] = reinterpret_cast<float*>(take(part2_bytes));
+  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(take(key_bytes)), nullptr};
+  keys[1] = reinterpret_cast<uint32_t*>(take(key_bytes));
+
+  cudaError_t e = a.m > 0 ? sort_ids(a, sorted, other, counts, tiles, st) : cudaSuccess;
+  ReduceArgs q = {};
+  q.entries = a.m;
+  q.n = a.n;
+  q.count = a.count;
+  q.chunk = CHUNK;
+  q.sorted = sorted;
+  q.src = a.src;
+  q.lds = a.lds;
+  q.scale = a.scale;
+  q.out = a.out;
+  q.ldo = a.ldo;
+  q.shape = shape_of(a.n / V, 1);
+  // CTAs that zero rows: 32 rows each, fewer where the table is small
+  q.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, a.count / (8 * (int64_t)dev.sm_count)));
+  int64_t zero_ctas = (a.count + q.zero_rows - 1) / q.zero_rows;
+  for (int level = 0; e == cudaSuccess; ++level) {
+    const int64_t c = (q.entries + q.chunk - 1) / q.chunk;
+    q.part = c > 1 ? part[level & 1] : nullptr;
+    q.part_keys = c > 1 ? keys[level & 1] : nullptr;
+    q.sum_ctas = (c * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
+    const dim3 grid((unsigned)(q.sum_ctas + zero_ctas));
+    const unsigned threads = (unsigned)(q.shape.tpr * q.shape.groups);
+    const unsigned block = (threads + 31) / 32 * 32;
+    e = level == 0 ? launch_kernel(embed_reduce_kernel<T, T, V>, grid, block, 0, st, q)
+                   : launch_kernel(embed_reduce_kernel<float, T, V>, grid, block, 0, st, q);
+    if (c <= 1) break;
+    zero_ctas = 0;
+    q.sorted = nullptr;
+    q.keys = keys[level & 1];
+    q.src = part[level & 1];
+    q.lds = a.n;
+    q.entries = 2 * c;
+    // (a level of at most 256 partial sums is the last)
+    q.chunk = q.entries <= 256 ? 256 : CHUNK;
+  }
+  cudaFreeAsync(ws, st);
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+template <typename T>
+fxtx_status_t run_t(const EmbedArgs& a, bool backward, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T), S = sizeof(T);
+  const bool wide = a.n % V == 0 && aligned(a.src, a.lds, S) && aligned(a.out, a.ldo, S);
+  if (backward) return wide ? gradient<T, V>(a, dev, st) : gradient<T, 1>(a, dev, st);
+  const cudaError_t e = wide ? lookup<T, V>(a, dev, st) : lookup<T, 1>(a, dev, st);
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+fxtx_status_t run(fxtx_type_t type, const EmbedArgs& a, bool backward, const DeviceInfo& dev, cudaStream_t st) {
+  switch (type) {
+    case FXTX_F32: return run_t<float>(a, backward, dev, st);
+    case FXTX_BF16: return run_t<__nv_bfloat16>(a, backward, dev, st);
+    default: return run_t<__half>(a, backward, dev, st);
+  }
+}
+
+}  // namespace
+
+fxtx_status_t run_embed(fxtx_type_t type, const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  return run(type, a, false, dev, st);
+}
+fxtx_status_t run_embed_grad(fxtx_type_t type, const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  return run(type, a, true, dev, st);
+}
+
+}  // namespace fxtx

@@ -5,6 +5,7 @@
 #include "host.h"
 #include "layers.h"
 #include "linear.h"
+#include "train.h"
 
 using namespace fxtx;
 
@@ -26,6 +27,8 @@ bool sizes_ok(int64_t m, int64_t n, int64_t k) {
   const int64_t top = (int64_t)1 << 31;
   return m >= 0 && n >= 0 && k >= 0 && m < top && n < top && k < top;
 }
+
+bool bits_ok(int bits) { return bits == 32 || bits == 64; }
 
 }  // namespace
 
@@ -130,6 +133,80 @@ fxtx_status_t fxtx_adamw_moments(int64_t n, const int8_t* m, const float* m_scal
   if (s != FXTX_OK) return s;
   return status_of(
       launch_adamw_moments(n, m, m_scale, v, v_scale, m_out, v_out, static_cast<cudaStream_t>(stream)));
+}
+
+fxtx_status_t fxtx_layer_norm(fxtx_type_t type, int64_t m, int64_t n, const void* X, int64_t ldx, const void* w, const void* b,
+                              double eps, void* OUT, int64_t ldo, float* MEAN, float* RSTD, void* stream) {
+  if (!type_ok(type) || !sizes_ok(m, n, 0) || n == 0 || !(eps >= 0.0) || !std::isfinite(eps)) return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(X, m, n, ldx) || !rows_ok(OUT, m, n, ldo)) return FXTX_ERR_INVALID_ARG;
+  if (m == 0) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  NormArgs a;
+  a.m = m; a.n = n;
+  a.X = X; a.ldx = ldx;
+  a.w = w; a.b = b;
+  a.eps = (float)eps;
+  a.out = OUT; a.ldo = ldo;
+  a.mean = MEAN; a.rstd = RSTD;
+  return run_norm(type, a, *dev, static_cast<cudaStream_t>(stream));
+}
+
+fxtx_status_t fxtx_layer_norm_grad(fxtx_type_t type, int64_t m, int64_t n, const void* G, int64_t ldg, const void* X, int64_t ldx,
+                                   const void* w, const float* mean, const float* rstd, const void* R, int64_t ldr, void* DX,
+                                   int64_t lddx, void* DW, void* DB, void* stream) {
+  if (!type_ok(type) || !sizes_ok(m, n, 0) || n == 0) return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(G, m, n, ldg) || !rows_ok(X, m, n, ldx) || (m > 0 && (!mean || !rstd))) return FXTX_ERR_INVALID_ARG;
+  if ((R != nullptr && ldr < n) || (DX != nullptr && lddx < n)) return FXTX_ERR_INVALID_ARG;
+  if (!DW && !DB && (!DX || m == 0)) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  NormArgs a;
+  a.m = m; a.n = n;
+  a.X = X; a.ldx = ldx;
+  a.w = w;
+  a.mean_in = mean; a.rstd_in = rstd;
+  a.G = G; a.ldg = ldg;
+  a.R = DX ? R : nullptr; a.ldr = ldr;
+  a.DX = DX; a.lddx = lddx;
+  a.DW = DW; a.DB = DB;
+  return run_norm_grad(type, a, *dev, static_cast<cudaStream_t>(stream));
+}
+
+fxtx_status_t fxtx_embedding(fxtx_type_t type, int64_t m, int64_t n, int64_t count, const void* ids, int id_bits, const void* E,
+                             int64_t lde, double scale, void* OUT, int64_t ldo, void* stream) {
+  if (!type_ok(type) || !sizes_ok(m, n, count) || !bits_ok(id_bits)) return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(E, count, n, lde) || !rows_ok(OUT, m, n, ldo) || (m > 0 && !ids)) return FXTX_ERR_INVALID_ARG;
+  if (m == 0 || n == 0) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  EmbedArgs a;
+  a.m = m; a.n = n; a.count = count;
+  a.ids = ids; a.ids64 = id_bits == 64;
+  a.scale = (float)scale;
+  a.src = E; a.lds = lde;
+  a.out = OUT; a.ldo = ldo;
+  return run_embed(type, a, *dev, static_cast<cudaStream_t>(stream));
+}
+
+fxtx_status_t fxtx_embedding_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t count, const void* G, int64_t ldg, const void* ids,
+                                  int id_bits, double scale, void* DE, int64_t ldde, void* stream) {
+  if (!type_ok(type) || !sizes_ok(m, n, count) || !bits_ok(id_bits)) return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(G, m, n, ldg) || !rows_ok(DE, count, n, ldde) || (m > 0 && !ids)) return FXTX_ERR_INVALID_ARG;
+  if (count == 0 || n == 0) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  EmbedArgs a;
+  a.m = m; a.n = n; a.count = count;
+  a.ids = ids; a.ids64 = id_bits == 64;
+  a.scale = (float)scale;
+  a.src = G; a.lds = ldg;
+  a.out = DE; a.ldo = ldde;
+  return run_embed_grad(type, a, *dev, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

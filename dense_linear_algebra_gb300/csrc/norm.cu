@@ -1,0 +1,625 @@
+// norm.cu — layer norm over the rows of X and its gradient:
+//     out = u w + b,  u = (x - mean) rstd,  rstd = (mean of (x - mean)^2 + eps)^-1/2
+//     h = g w:  dx = rstd (h - mean(h) - u mean(h u)) + r,  dw = sum over the rows of g u,  db = of g
+//
+// Bound: HBM; every matrix is read or written once. A row lies in the registers of `tpr` threads (1 to 32 neighbouring
+// lanes, or whole warps that meet at a named barrier), CH accesses of 16 bytes each, so that the variance is formed
+// from x - mean, in a second sum, without reading x again. A CTA has `groups` such rows in work at once and takes rows
+// in turn; the next row's loads are issued before the present one's sums. The columns of a thread stay the same from
+// row to row, so dw and db are summed in its registers, over the CTA's groups in shared memory, in turn, and over the
+// CTAs by a second kernel in order: the result is the same on every call.
+//
+// Rows beyond what the registers hold take more passes: the forward pass reads x three times (one CTA a row), the
+// gradient forms mean(h) and mean(h u) in one pass and dx and the column sums in another.
+//
+// Matrices whose start, pitch or width is no multiple of 16 bytes go entry by entry (V = 1), neighbouring threads
+// taking neighbouring entries.
+#include <algorithm>
+
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+#include "train.h"
+
+namespace fxtx {
+namespace {
+
+constexpr int FWD_THREADS = 256, GRAD_THREADS = 512, LONG_THREADS = 512;
+
+// V neighbouring entries as they are loaded.
+template <typename T, int V>
+struct Raw {
+  static_assert(V * sizeof(T) == 16, "16 bytes");
+  uint4 v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void values(float* x) const {
+    const T* t = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = to_f32(t[i]);
+  }
+  __device__ __forceinline__ static void store(T* p, const float* x) {
+    uint4 w;
+    T* t = reinterpret_cast<T*>(&w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = from_f32<T>(x[i]);
+    *reinterpret_cast<uint4*>(p) = w;
+  }
+};
+template <typename T>
+struct Raw<T, 1> {
+  T v;
+  __device__ __forceinline__ void load(const T* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = from_f32<T>(0.f); }
+  __device__ __forceinline__ void values(float* x) const { x[0] = to_f32(v); }
+  __device__ __forceinline__ static void store(T* p, const float* x) { *p = from_f32<T>(x[0]); }
+};
+
+// How rows lie over a CTA's threads.
+struct RowShape {
+  int tpr = 1, groups = 1;
+};
+
+// A row's accesses: thread t of its tpr takes accesses t, t + tpr, ...
+template <typename T, int V, int CH>
+struct RowOf {
+  const int t, tpr, count;
+  __device__ __forceinline__ RowOf(int t_, int tpr_, int64_t n) : t(t_), tpr(tpr_), count((int)(n / V)) {}
+  __device__ __forceinline__ bool has(int i) const { return t + i * tpr < count; }
+  __device__ __forceinline__ int64_t at(int i) const { return (int64_t)(t + i * tpr) * V; }
+  __device__ __forceinline__ void load(const void* base, int64_t row, int64_t rows, int64_t ld, Raw<T, V> (&x)[CH]) const {
+    const T* p = static_cast<const T*>(base) + row * ld;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (row < rows && has(i)) x[i].load(p + at(i));
+      else x[i].zero();
+    }
+  }
+};
+
+// Sums over a row's threads, the same in each of them. All threads of the CTA call it as often.
+template <bool BIG>
+struct RowSum {
+  float2 (*red)[32];  // [2][warps of the CTA]
+  int tpr, group, parity = 0;
+  __device__ __forceinline__ float2 operator()(float2 s) {
+    if constexpr (!BIG) {
+      for (int o = tpr >> 1; o > 0; o >>= 1) {
+        s.x += shfl_xor(s.x, o);
+        s.y += shfl_xor(s.y, o);
+      }
+      return s;
+    } else {
+      s.x = group_sum<32>(s.x);
+      s.y = group_sum<32>(s.y);
+      const int warp = threadIdx.x >> 5, w0 = group * (tpr >> 5), wn = tpr >> 5;
+      float2* buf = red[parity];
+      parity ^= 1;  // whoever writes this half again has passed the other half's barrier, which all readers of this one reach after
+      if ((threadIdx.x & 31) == 0) buf[warp] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+      s = make_float2(0.f, 0.f);
+      for (int w = 0; w < wn; ++w) {
+        const float2 v = buf[w0 + w];
+        s.x += v.x;
+        s.y += v.y;
+      }
+      return s;
+    }
+  }
+};
+
+template <typename T, int V, int CH, bool BIG>
+__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a, const RowShape shape) {
+  __shared__ float2 red[2][32];
+  const int tpr = shape.tpr, group = threadIdx.x / tpr;
+  const RowOf<T, V, CH> r((int)threadIdx.x % tpr, tpr, a.n);
+  RowSum<BIG> sum{red, tpr, group};
+  const float over = 1.f / (float)a.n;
+  const int64_t step = (int64_t)gridDim.x * shape.groups;
+  int64_t row = (int64_t)blockIdx.x * shape.groups + group;
+  after_previous();
+  Raw<T, V> next[CH];
+  r.load(a.X, row, a.m, a.ldx, next);
+  // (all threads go round as often as the CTA's first group, whose rows are the lowest)
+  for (int64_t first = (int64_t)blockIdx.x * shape.groups; first < a.m; first += step, row += step) {
+    float x[CH * V];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) next[i].values(x + i * V);
+    r.load(a.X, row + step, a.m, a.ldx, next);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH * V; ++i) s += x[i];
+    const float mean = sum(make_float2(s, 0.f)).x * over;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (r.has(i)) {
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          float& v = x[i * V + q];
+          v -= mean;
+          s = fmaf(v, v, s);
+        }
+      }
+    const float rstd = __frsqrt_rn(fmaf(sum(make_float2(s, 0.f)).x, over, a.eps));
+    if (row >= a.m) continue;
+    if (r.t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (!r.has(i)) continue;
+      float* v = x + i * V;
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] *= rstd;
+      Raw<T, V> c;
+      float y[V];
+      if (a.w) {
+        c.load(static_cast<const T*>(a.w) + r.at(i));
+        c.values(y);
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] *= y[q];
+      }
+      if (a.b) {
+        c.load(static_cast<const T*>(a.b) + r.at(i));
+        c.values(y);
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] += y[q];
+      }
+      Raw<T, V>::store(out + r.at(i), v);
+    }
+  }
+}
+
+// SUMS: dw and db too.
+template <typename T, int V, int CH, bool BIG, bool SUMS>
+__global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const __grid_constant__ NormArgs a, const RowShape shape) {
+  __shared__ float2 red[2][32];
+  constexpr int E = CH * V;
+  const int tpr = shape.tpr, group = threadIdx.x / tpr;
+  const RowOf<T, V, CH> r((int)threadIdx.x % tpr, tpr, a.n);
+  RowSum<BIG> sum{red, tpr, group};
+  const float over = 1.f / (float)a.n;
+  const int64_t step = (int64_t)gridDim.x * shape.groups;
+  int64_t row = (int64_t)blockIdx.x * shape.groups + group;
+  after_previous();
+  float dw[SUMS ? E : 1] = {}, db[SUMS ? E : 1] = {};
+  Raw<T, V> w[CH], xn[CH], gn[CH], rn[CH];
+  if (a.w) r.load(a.w, 0, 1, 0, w);
+  float mean_n = 0.f, rstd_n = 0.f;
+  auto fetch = [&](int64_t i) {
+    r.load(a.X, i, a.m, a.ldx, xn);
+    r.load(a.G, i, a.m, a.ldg, gn);
+    if (a.R) r.load(a.R, i, a.m, a.ldr, rn);
+    mean_n = i < a.m ? a.mean_in[i] : 0.f;
+    rstd_n = i < a.m ? a.rstd_in[i] : 0.f;
+  };
+  fetch(row);
+  for (int64_t first = (int64_t)blockIdx.x * shape.groups; first < a.m; first += step, row += step) {
+    float u[E], h[E];
+    Raw<T, V> res[CH];
+    const float mean = mean_n, rstd = rstd_n;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      xn[i].values(u + i * V);
+      gn[i].values(h + i * V);
+      if (a.R) res[i] = rn[i];
+    }
+    fetch(row + step);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float y[V];
+      w[i].values(y);
+      // (a thread beyond the row's end, or a row beyond the last, has zeros in G, but for u: those would be no
+      // numbers where mean or rstd is none)
+      const bool in = r.has(i) && row < a.m;
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        float &x = u[i * V + q], &g = h[i * V + q];
+        x = in ? (x - mean) * rstd : 0.f;
+        if constexpr (SUMS) {
+          dw[i * V + q] = fmaf(g, x, dw[i * V + q]);
+          db[i * V + q] += g;
+        }
+        if (a.w) g *= y[q];
+        s.x += g;
+        s.y = fmaf(g, x, s.y);
+      }
+    }
+    s = sum(s);
+    if (row >= a.m || !a.DX) continue;
+    const float c1 = s.x * over, c2 = s.y * over;
+    T* out = static_cast<T*>(a.DX) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (!r.has(i)) continue;
+      float v[V], y[V];
+      if (a.R) res[i].values(y);
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        v[q] = (h[i * V + q] - c1 - u[i * V + q] * c2) * rstd;
+        if (a.R) v[q] += y[q];
+      }
+      Raw<T, V>::store(out + r.at(i), v);
+    }
+  }
+  if constexpr (SUMS) {
+    // over the CTA's rows in work: a warp's by exchange, then group after group (or warp after warp) in shared memory
+    extern __shared__ __align__(16) float cols[];  // [2][E][tpr]
+    if constexpr (!BIG) {
+      for (int o = tpr; o < 32; o <<= 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          dw[e] += shfl_xor(dw[e], o);
+          db[e] += shfl_xor(db[e], o);
+        }
+      }
+    }
+    const int units = BIG ? shape.groups : (int)(blockDim.x >> 5), unit = BIG ? group : (int)(threadIdx.x >> 5);
+    const bool mine = BIG || (int)(threadIdx.x & 31) < tpr;
+    for (int y = 0; y < units; ++y) {
+      __syncthreads();
+      if (unit != y || !mine) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        float *p = cols + e * tpr + r.t, *q = p + E * tpr;
+        *p = y > 0 ? *p + dw[e] : dw[e];
+        *q = y > 0 ? *q + db[e] : db[e];
+      }
+    }
+    __syncthreads();
+    for (int64_t j = threadIdx.x; j < a.n; j += blockDim.x) {
+      const int c = (int)(j / V), e = c / tpr * V + (int)(j % V);
+      const float x = cols[e * tpr + c % tpr], y = cols[(E + e) * tpr + c % tpr];
+      if (gridDim.x == 1) {
+        if (a.DW) static_cast<T*>(a.DW)[j] = from_f32<T>(x);
+        if (a.DB) static_cast<T*>(a.DB)[j] = from_f32<T>(y);
+      } else {
+        float* p = a.part + (int64_t)blockIdx.x * 2 * a.n + j;
+        p[0] = x;
+        p[a.n] = y;
+      }
+    }
+  }
+}
+
+// dw and db from `parts` CTAs' sums, in order: 32 columns a CTA, 8 threads a column.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormArgs a, int64_t parts) {
+  __shared__ float part[8][32];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t j = (int64_t)blockIdx.x * 32 + x;
+  float s = 0.f;
+  after_previous();
+  if (j < 2 * a.n) {
+#pragma unroll 4
+    for (int64_t p = y; p < parts; p += 8) s += a.part[p * 2 * a.n + j];
+  }
+  part[y][x] = s;
+  __syncthreads();
+  if (y != 0 || j >= 2 * a.n) return;
+  for (int i = 1; i < 8; ++i) s += part[i][x];
+  T* to = static_cast<T*>(j < a.n ? a.DW : a.DB);
+  if (to) to[j < a.n ? j : j - a.n] = from_f32<T>(s);
+}
+
+// A CTA's sum of two doubles, the same in every thread.
+__device__ __forceinline__ double2 cta_sum(double x, double y, double2* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x += shfl_xor(x, o);
+    y += shfl_xor(y, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_double2(x, y);
+  __syncthreads();
+  double2 s = make_double2(0.0, 0.0);
+  for (int w = 0; w < LONG_THREADS / 32; ++w) {
+    s.x += red[w].x;
+    s.y += red[w].y;
+  }
+  return s;
+}
+
+// Rows of any length, one CTA a row at a time. A thread's sums leave fp32 after 16 accesses.
+template <typename T, int V>
+__global__ void __launch_bounds__(LONG_THREADS) norm_long_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ double2 red[LONG_THREADS / 32];
+  after_previous();
+  const int64_t accesses = a.n / V;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.X) + row * a.ldx;
+    auto total = [&](auto term) {
+      double s = 0.0;
+      for (int64_t c0 = threadIdx.x; c0 < accesses; c0 += 16 * LONG_THREADS) {
+        float p = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < 16; ++i) {
+          const int64_t c = c0 + (int64_t)i * LONG_THREADS;
+          if (c >= accesses) break;
+          Raw<T, V> raw;
+          float v[V];
+          raw.load(x + c * V);
+          raw.values(v);
+#pragma unroll
+          for (int q = 0; q < V; ++q) p += term(v[q]);
+        }
+        s += p;
+      }
+      return cta_sum(s, 0.0, red).x;
+    };
+    const float mean = (float)(total([](float v) { return v; }) / (double)a.n);
+    const float var = (float)(total([&](float v) { return (v - mean) * (v - mean); }) / (double)a.n);
+    const float rstd = __frsqrt_rn(var + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+    for (int64_t c = threadIdx.x; c < accesses; c += LONG_THREADS) {
+      Raw<T, V> raw;
+      float v[V], y[V];
+      raw.load(x + c * V);
+      raw.values(v);
+#pragma unroll
+      for (int q = 0; q < V; ++q) v[q] = (v[q] - mean) * rstd;
+      if (a.w) {
+        raw.load(static_cast<const T*>(a.w) + c * V);
+        raw.values(y);
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] *= y[q];
+      }
+      if (a.b) {
+        raw.load(static_cast<const T*>(a.b) + c * V);
+        raw.values(y);
+#pragma unroll
+        for (int q = 0; q < V; ++q) v[q] += y[q];
+      }
+      Raw<T, V>::store(out + c * V, v);
+    }
+  }
+}
+
+// The gradient of long rows, first pass: mean(h) and mean(h u) of each row.
+template <typename T, int V>
+__global__ void __launch_bounds__(LONG_THREADS) norm_long_means_kernel(const __grid_constant__ NormArgs a, float2* means) {
+  __shared__ double2 red[LONG_THREADS / 32];
+  after_previous();
+  const int64_t accesses = a.n / V;
+  for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
+    const T *x = static_cast<const T*>(a.X) + row * a.ldx, *g = static_cast<const T*>(a.G) + row * a.ldg;
+    const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+    double s = 0.0, t = 0.0;
+    for (int64_t c0 = threadIdx.x; c0 < accesses; c0 += 16 * LONG_THREADS) {
+      float p = 0.f, o = 0.f;
+#pragma unroll 2
+      for (int i = 0; i < 16; ++i) {
+        const int64_t c = c0 + (int64_t)i * LONG_THREADS;
+        if (c >= accesses) break;
+        Raw<T, V> raw;
+        float v[V], h[V], y[V];
+        raw.load(x + c * V);
+        raw.values(v);
+        raw.load(g + c * V);
+        raw.values(h);
+        if (a.w) {
+          raw.load(static_cast<const T*>(a.w) + c * V);
+          raw.values(y);
+        }
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          if (a.w) h[q] *= y[q];
+          p += h[q];
+          o = fmaf(h[q], (v[q] - mean) * rstd, o);
+        }
+      }
+      s += p;
+      t += o;
+    }
+    const double2 all = cta_sum(s, t, red);
+    if (threadIdx.x == 0) means[row] = make_float2((float)(all.x / (double)a.n), (float)(all.y / (double)a.n));
+  }
+}
+
+// Second pass: dx and the column sums; a thread keeps V columns and goes down `rows` rows.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) norm_long_grad_kernel(const __grid_constant__ NormArgs a, const float2* means, int64_t slabs,
+                                                             int64_t rows) {
+  const int64_t slab = blockIdx.x % slabs, part = blockIdx.x / slabs, j = (slab * 256 + threadIdx.x) * V;
+  after_previous();
+  if (j >= a.n) return;
+  Raw<T, V> raw;
+  float w[V], dw[V] = {}, db[V] = {};
+  if (a.w) {
+    raw.load(static_cast<const T*>(a.w) + j);
+    raw.values(w);
+  }
+  const int64_t end = min(a.m, (part + 1) * rows);
+#pragma unroll 2
+  for (int64_t row = part * rows; row < end; ++row) {
+    float u[V], g[V], y[V];
+    raw.load(static_cast<const T*>(a.X) + row * a.ldx + j);
+    raw.values(u);
+    raw.load(static_cast<const T*>(a.G) + row * a.ldg + j);
+    raw.values(g);
+    const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      u[q] = (u[q] - mean) * rstd;
+      dw[q] = fmaf(g[q], u[q], dw[q]);
+      db[q] += g[q];
+    }
+    if (!a.DX) continue;
+    const float2 c = means[row];
+    if (a.R) {
+      raw.load(static_cast<const T*>(a.R) + row * a.ldr + j);
+      raw.values(y);
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      if (a.w) g[q] *= w[q];
+      g[q] = (g[q] - c.x - u[q] * c.y) * rstd;
+      if (a.R) g[q] += y[q];
+    }
+    Raw<T, V>::store(static_cast<T*>(a.DX) + row * a.lddx + j, g);
+  }
+  if (a.part) {
+    float* p = a.part + part * 2 * a.n + j;
+#pragma unroll
+    for (int q = 0; q < V; ++q) {
+      p[q] = dw[q];
+      p[a.n + q] = db[q];
+    }
+  }
+}
+
+bool aligned(const void* p, int64_t ld, int size) { return p == nullptr || (((uintptr_t)p & 15u) == 0 && ld * size % 16 == 0); }
+
+// Threads a row takes and rows a CTA has in work: `per` accesses a thread at most.
+RowShape shape_of(int64_t accesses, int per, int threads) {
+  RowShape s;
+  const int64_t need = (accesses + per - 1) / per;
+  if (need <= 32)
+    while (s.tpr < need) s.tpr *= 2;
+  else
+    s.tpr = (int)((need + 31) / 32 * 32);
+  s.groups = std::max(1, threads / s.tpr);
+  return s;
+}
+
+template <typename... A>
+int ctas_per_sm(void (*kernel)(A...), int threads, size_t smem) {
+  int b = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, smem) != cudaSuccess) cudaGetLastError();
+  return std::max(b, 1);
+}
+
+template <typename T, int V, int CH, bool BIG>
+cudaError_t launch_forward(const NormArgs& a, const RowShape& s, const DeviceInfo& dev, cudaStream_t st) {
+  const int threads = (s.tpr * s.groups + 31) / 32 * 32;
+  const int64_t fit = (int64_t)ctas_per_sm(norm_kernel<T, V, CH, BIG>, threads, 0) * dev.sm_count;
+  const int64_t grid = std::min<int64_t>((a.m + s.groups - 1) / s.groups, fit);
+  return launch_kernel(norm_kernel<T, V, CH, BIG>, dim3((unsigned)grid), threads, 0, st, a, s);
+}
+
+template <typename T, int V, int CH>
+cudaError_t forward_ch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  const RowShape s = shape_of(a.n / V, CH, FWD_THREADS);
+  return s.tpr <= 32 ? launch_forward<T, V, CH, false>(a, s, dev, st) : launch_forward<T, V, CH, true>(a, s, dev, st);
+}
+
+template <typename T, int V>
+cudaError_t forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr int MOST = V == 1 ? 16 : 4;
+  const int64_t accesses = a.n / V;
+  if (accesses > (int64_t)MOST * 1024)
+    return launch_kernel(norm_long_kernel<T, V>, dim3((unsigned)std::min<int64_t>(a.m, (int64_t)dev.sm_count * 4)), LONG_THREADS, 0,
+                         st, a);
+  if (accesses <= 32) return forward_ch<T, V, 1>(a, dev, st);
+  return forward_ch<T, V, MOST>(a, dev, st);
+}
+
+template <typename T, int V, int CH, bool BIG, bool SUMS>
+fxtx_status_t launch_grad(NormArgs a, const RowShape& s, const DeviceInfo& dev, cudaStream_t st) {
+  const int threads = (s.tpr * s.groups + 31) / 32 * 32;
+  const size_t smem = SUMS ? (size_t)2 * CH * V * s.tpr * 4 : 0;
+  cudaError_t e = ensure_smem((const void*)norm_grad_kernel<T, V, CH, BIG, SUMS>, smem);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return FXTX_ERR_CUDA;
+  }
+  const int64_t fit = (int64_t)ctas_per_sm(norm_grad_kernel<T, V, CH, BIG, SUMS>, threads, smem) * dev.sm_count;
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((a.m + s.groups - 1) / s.groups, fit));  // (no rows: zero sums)
+  if (SUMS && grid > 1) {
+    const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)grid * 2 * a.n * 4, st);
+    if (r != FXTX_OK) return r;
+  }
+  e = launch_kernel(norm_grad_kernel<T, V, CH, BIG, SUMS>, dim3((unsigned)grid), threads, smem, st, a, s);
+  if (a.part) {
+    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 256, 0, st, a, grid);
+    cudaFreeAsync(a.part, st);
+  }
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+template <typename T, int V>
+fxtx_status_t long_grad(NormArgs a, const DeviceInfo& dev, cudaStream_t st) {
+  const bool sums = a.DW || a.DB;
+  const int64_t slabs = (a.n / V + 255) / 256;
+  const int64_t want = std::max<int64_t>(1, (int64_t)dev.sm_count * 4 / slabs);  // row ranges
+  const int64_t rows = std::max<int64_t>(1, (a.m + want - 1) / want), parts = std::max<int64_t>(1, (a.m + rows - 1) / rows);
+  const size_t mean_bytes = ((size_t)a.m * 8 + 255) / 256 * 256, part_bytes = sums ? (size_t)parts * 2 * a.n * 4 : 0;
+  char* ws = nullptr;
+  const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&ws), mean_bytes + part_bytes, st);
+  if (r != FXTX_OK) return r;
+  float2* means = reinterpret_cast<float2*>(ws);
+  a.part = sums ? reinterpret_cast<float*>(ws + mean_bytes) : nullptr;
+  cudaError_t e = cudaSuccess;
+  if (a.DX && a.m > 0)
+    e = launch_kernel(norm_long_means_kernel<T, V>, dim3((unsigned)std::min<int64_t>(a.m, (int64_t)dev.sm_count * 4)), LONG_THREADS, 0,
+                      st, a, means);
+  if (e == cudaSuccess)
+    e = launch_kernel(norm_long_grad_kernel<T, V>, dim3((unsigned)(slabs * parts)), 256, 0, st, a, (const float2*)means, slabs, rows);
+  if (e == cudaSuccess && sums) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 256, 0, st, a, parts);
+  cudaFreeAsync(ws, st);
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+template <typename T, int V, int CH>
+fxtx_status_t grad_ch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  const RowShape s = shape_of(a.n / V, CH, GRAD_THREADS);
+  const bool sums = a.DW || a.DB;
+  if (s.tpr <= 32)
+    return sums ? launch_grad<T, V, CH, false, true>(a, s, dev, st) : launch_grad<T, V, CH, false, false>(a, s, dev, st);
+  return sums ? launch_grad<T, V, CH, true, true>(a, s, dev, st) : launch_grad<T, V, CH, true, false>(a, s, dev, st);
+}
+
+template <typename T, int V>
+fxtx_status_t grad(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr int MOST = 16 / V;  // 16 entries a thread: with their sums, weights and the next row's they fill its registers
+  const int64_t accesses = a.n / V;
+  if (accesses > (int64_t)MOST * GRAD_THREADS) return long_grad<T, V>(a, dev, st);
+  if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
+  return grad_ch<T, V, MOST>(a, dev, st);
+}
+
+template <typename T>
+fxtx_status_t run_t(const NormArgs& a, bool backward, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T), S = sizeof(T);
+  bool wide = a.n % V == 0 && aligned(a.X, a.ldx, S) && aligned(a.w, 0, S);
+  if (backward) {
+    wide = wide && aligned(a.G, a.ldg, S) && aligned(a.R, a.ldr, S) && aligned(a.DX, a.lddx, S);
+    return wide ? grad<T, V>(a, dev, st) : grad<T, 1>(a, dev, st);
+  }
+  wide = wide && aligned(a.b, 0, S) && aligned(a.out, a.ldo, S);
+  const cudaError_t e = wide ? forward<T, V>(a, dev, st) : forward<T, 1>(a, dev, st);
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+fxtx_status_t run(fxtx_type_t type, const NormArgs& a, bool backward, const DeviceInfo& dev, cudaStream_t st) {
+  switch (type) {
+    case FXTX_F32: return run_t<float>(a, backward, dev, st);
+    case FXTX_BF16: return run_t<__nv_bfloat16>(a, backward, dev, st);
+    default: return run_t<__half>(a, backward, dev, st);
+  }
+}
+
+}  // namespace
+
+fxtx_status_t run_norm(fxtx_type_t type, const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  return run(type, a, false, dev, st);
+}
+fxtx_status_t run_norm_grad(fxtx_type_t type, const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  return run(type, a, true, dev, st);
+}
+
+}  // namespace fxtx

@@ -435,6 +435,47 @@ fxtx_status_t fxtx_adamw(int64_t count, const fxtx_adamw_tensor_t* tensors, fxtx
 fxtx_status_t fxtx_adamw_moments(int64_t n, const int8_t* m, const float* m_scale, const uint8_t* v,
                                  const float* v_scale, float* m_out, float* v_out, void* stream);
 
+/*
+ * What training a classifier takes besides its layers. Types, streams, ownership, workspace and errors are those of
+ * the layer operators; results are bitwise reproducible.
+ *
+ * Layer norm over the rows of X (m x n): with the row's mean and rstd = (the mean of (x - mean)^2 + eps)^-1/2,
+ *
+ *     OUT = (X - mean) rstd w + b
+ *
+ * w and b are n-vectors or NULL (ones, zeros). MEAN and RSTD (m fp32 values each, or NULL) receive the statistics, as
+ * the gradient takes them. OUT may equal X with ldo == ldx. eps >= 0. n = 0 is refused (a mean of no entries);
+ * m = 0 does nothing.
+ *
+ * The gradient: with u = (X - mean) rstd, h = G w and mean(.) over a row,
+ *
+ *     DX = rstd (h - mean(h) - u mean(h u)) + R      DW = the column sums of G u      DB = those of G
+ *
+ * R (m x n or NULL) is the gradient that reaches X on a residual path; it is read only for DX. Each of DX, DW, DB may
+ * be NULL (not computed). DX may equal G, R or X with the same pitch. m = 0 gives DW = 0 and DB = 0. Rows whose
+ * statistics are not finite give NaN in DX and DW, and in no other row of DX.
+ */
+fxtx_status_t fxtx_layer_norm(fxtx_type_t type, int64_t m, int64_t n, const void* X, int64_t ldx, const void* w, const void* b,
+                              double eps, void* OUT, int64_t ldo, float* MEAN, float* RSTD, void* stream);
+fxtx_status_t fxtx_layer_norm_grad(fxtx_type_t type, int64_t m, int64_t n, const void* G, int64_t ldg, const void* X, int64_t ldx,
+                                   const void* w, const float* mean, const float* rstd, const void* R, int64_t ldr, void* DX,
+                                   int64_t lddx, void* DW, void* DB, void* stream);
+
+/*
+ * The embedding lookup: row i of OUT (m x n) = scale * row ids[i] of the table E (count x n), and its gradient,
+ *
+ *     row v of DE (count x n) = scale * the sum of the rows i of G (m x n) with ids[i] = v
+ *
+ * (zeros where there is none; the sum is fp32, in the order of i, in pieces). ids: m integers of id_bits (32 or 64)
+ * bits. An id outside 0 .. count - 1 stands for no row: zeros come out and nothing goes back (-1 for padding). Every
+ * entry of OUT and DE is written. Outputs must not overlap anything else. Workspace is taken for the gradient: about
+ * 24 bytes an id, and an eighth of m x n fp32 values.
+ */
+fxtx_status_t fxtx_embedding(fxtx_type_t type, int64_t m, int64_t n, int64_t count, const void* ids, int id_bits, const void* E,
+                             int64_t lde, double scale, void* OUT, int64_t ldo, void* stream);
+fxtx_status_t fxtx_embedding_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t count, const void* G, int64_t ldg, const void* ids,
+                                  int id_bits, double scale, void* DE, int64_t ldde, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
