@@ -58,6 +58,8 @@ from ._lib import (  # noqa: F401
     fxtx_autotune_load,
     fxtx_autotune_save,
     fxtx_autotune_set,
+    fxtx_cross_entropy,
+    fxtx_cross_entropy_grad,
     fxtx_csr_analysis_clear,
     fxtx_csr_analyze,
     fxtx_csr_f32,
@@ -89,7 +91,7 @@ from ._lib import (  # noqa: F401
 
 
 _LAZY = dict.fromkeys(("AdamW", "linear", "linear_grad"), "layers") | dict.fromkeys(
-    ("layer_norm", "layer_norm_grad", "embedding", "embedding_grad"), "training")
+    ("layer_norm", "layer_norm_grad", "embedding", "embedding_grad", "cross_entropy", "cross_entropy_grad"), "training")
 
 
 def __getattr__(name):

@@ -66,6 +66,9 @@ def _load() -> ctypes.CDLL:
     lib.fxtx_layer_norm_grad.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp]
     lib.fxtx_embedding.argtypes = [i32, i64, i64, i64, vp, i32, vp, i64, f64, vp, i64, vp]
     lib.fxtx_embedding_grad.argtypes = [i32, i64, i64, i64, vp, i64, vp, i32, f64, vp, i64, vp]
+    lib.fxtx_cross_entropy.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, vp, i32, vp, vp, vp]
+    lib.fxtx_cross_entropy_grad.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, i32, vp, vp, i32, vp, vp, f64, vp, i64, vp, i64,
+                                            vp, vp]
     lib.fxtx_device_error.argtypes = [vp]
     lib.fxtx_status_string.argtypes = [i32]
     lib.fxtx_status_string.restype = ctypes.c_char_p
@@ -84,6 +87,7 @@ def _load() -> ctypes.CDLL:
                  "fxtx_epilogue_f32", "fxtx_epilogue_f64", "fxtx_csr_analyze", "fxtx_csr_analysis_clear",
                  "fxtx_csr_plan_describe_host", "fxtx_linear", "fxtx_linear_grad", "fxtx_adamw", "fxtx_adamw_moments",
                  "fxtx_layer_norm", "fxtx_layer_norm_grad", "fxtx_embedding", "fxtx_embedding_grad",
+                 "fxtx_cross_entropy", "fxtx_cross_entropy_grad",
                  "fxtx_plan_describe", "fxtx_multi_plan_describe", "fxtx_autotune_set", "fxtx_autotune_get",
                  "fxtx_autotune_clear", "fxtx_autotune_save", "fxtx_autotune_load", "fxtx_autotune_candidates"):
         getattr(lib, name).restype = i32
@@ -115,6 +119,8 @@ fxtx_layer_norm = _lib.fxtx_layer_norm
 fxtx_layer_norm_grad = _lib.fxtx_layer_norm_grad
 fxtx_embedding = _lib.fxtx_embedding
 fxtx_embedding_grad = _lib.fxtx_embedding_grad
+fxtx_cross_entropy = _lib.fxtx_cross_entropy
+fxtx_cross_entropy_grad = _lib.fxtx_cross_entropy_grad
 fxtx_device_error = _lib.fxtx_device_error
 fxtx_plan_describe = _lib.fxtx_plan_describe
 fxtx_multi_plan_describe = _lib.fxtx_multi_plan_describe

@@ -5,6 +5,7 @@
 #include "host.h"
 #include "layers.h"
 #include "linear.h"
+#include "loss.h"
 #include "train.h"
 
 using namespace fxtx;
@@ -207,6 +208,66 @@ fxtx_status_t fxtx_embedding_grad(fxtx_type_t type, int64_t m, int64_t n, int64_
   a.src = G; a.lds = ldg;
   a.out = DE; a.ldo = ldde;
   return run_embed_grad(type, a, *dev, static_cast<cudaStream_t>(stream));
+}
+
+fxtx_status_t fxtx_cross_entropy(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                                 int64_t ldw, int w_trans, const void* b, const void* labels, int label_bits, float* LOSS, float* LSE,
+                                 void* stream) {
+  if (!type_ok(type) || !sizes_ok(m, n, k) || n == 0 || k == 0 || (w_trans != 0 && w_trans != 1) || !bits_ok(label_bits))
+    return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(X, m, n, ldx) || !rows_ok(W, w_trans ? k : n, w_trans ? n : k, ldw) || (m > 0 && !labels)) return FXTX_ERR_INVALID_ARG;
+  if (m == 0 || (!LOSS && !LSE)) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  LayerArgs l;
+  l.type = type;
+  l.m = m; l.n = n; l.k = k;
+  l.X = X; l.ldx = ldx;
+  l.W = W; l.ldw = ldw; l.w_trans = w_trans != 0;
+  l.e.bias = b;
+  LossArgs a;
+  a.labels = labels; a.labels64 = label_bits == 64;
+  a.loss = LOSS; a.lse = LSE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return thin_shape(n, k) ? run_thin_loss(l, a, *dev, st) : run_loss(l, a, *dev, st);
+}
+
+fxtx_status_t fxtx_cross_entropy_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                                      int64_t ldw, int w_trans, const void* b, const void* labels, int label_bits, const float* LSE,
+                                      const float* G, double gain, void* DX, int64_t lddx, void* DW, int64_t lddw, void* DB,
+                                      void* stream) {
+  if (!type_ok(type) || !sizes_ok(m, n, k) || n == 0 || k == 0 || (w_trans != 0 && w_trans != 1) || !bits_ok(label_bits))
+    return FXTX_ERR_INVALID_ARG;
+  if (!rows_ok(X, m, n, ldx) || !rows_ok(W, w_trans ? k : n, w_trans ? n : k, ldw) || (m > 0 && (!labels || !LSE)))
+    return FXTX_ERR_INVALID_ARG;
+  if ((DX && lddx < n) || (DW && lddw < (w_trans ? n : k))) return FXTX_ERR_INVALID_ARG;
+  if (!DW && !DB && (!DX || m == 0)) return FXTX_OK;
+  const DeviceInfo* dev = nullptr;
+  const fxtx_status_t s = current_device(&dev);
+  if (s != FXTX_OK) return s;
+  LayerArgs l;
+  l.type = type;
+  l.m = m; l.n = n; l.k = k;
+  l.X = X; l.ldx = ldx;
+  l.W = W; l.ldw = ldw; l.w_trans = w_trans != 0;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (m == 0) {  // sums of no rows
+    GradArgs g;
+    g.ldg = k;
+    g.DW = DW; g.lddw = lddw;
+    g.DB = DB;
+    return run_grad(l, g, *dev, st);
+  }
+  l.e.bias = b;
+  LossArgs a;
+  a.labels = labels; a.labels64 = label_bits == 64;
+  a.lse_in = LSE;
+  a.g = G; a.gain = (float)gain;
+  a.DX = DX; a.lddx = lddx;
+  a.DW = DW; a.lddw = lddw;
+  a.DB = DB;
+  return thin_shape(n, k) ? run_thin_loss_grad(l, a, *dev, st) : run_loss_grad(l, a, *dev, st);
 }
 
 }  // extern "C"

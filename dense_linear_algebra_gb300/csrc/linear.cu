@@ -12,29 +12,9 @@
 #include "product.cuh"
 
 namespace fxtx {
-namespace {
 
-// A sum of no terms: out = act(bias_j) + R_ij.
-template <typename T>
-__global__ void __launch_bounds__(256) empty_sum_kernel(const Epilogue e, int64_t rows, int64_t cols) {
-  const Finish<T> fin(e, rows, cols);
-  const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
-  const float zero[16] = {};
-  after_previous();
-  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride)
-    fin.template row<16>(x / groups, x % groups * 16, zero);
-}
-
-fxtx_status_t status_of(cudaError_t e) {
-  if (e == cudaSuccess) return FXTX_OK;
-  cudaGetLastError();
-  return FXTX_ERR_CUDA;
-}
-
-// Whether the tensor copies can read a 16-bit operand where it lies.
 bool copyable(const Operand& o) { return ((uintptr_t)o.p & 15u) == 0 && o.ld % 8 == 0; }
 
-// The operand's planes (rows x cols in memory), where they will lie in `at` if it has to be packed.
 Planes planes_of(const Operand& o, fxtx_type_t type, int64_t mn, int64_t k, char* at, size_t* bytes) {
   Planes x;
   x.rows = o.mn_major ? k : mn;
@@ -53,6 +33,25 @@ Planes planes_of(const Operand& o, fxtx_type_t type, int64_t mn, int64_t k, char
     *bytes = ((size_t)x.planes * x.plane_stride * 2 + 255) / 256 * 256;
   }
   return x;
+}
+
+namespace {
+
+// A sum of no terms: out = act(bias_j) + R_ij.
+template <typename T>
+__global__ void __launch_bounds__(256) empty_sum_kernel(const Epilogue e, int64_t rows, int64_t cols) {
+  const Finish<T> fin(e, rows, cols);
+  const int64_t groups = (cols + 15) / 16, stride = (int64_t)gridDim.x * 256;
+  const float zero[16] = {};
+  after_previous();
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * groups; x += stride)
+    fin.template row<16>(x / groups, x % groups * 16, zero);
+}
+
+fxtx_status_t status_of(cudaError_t e) {
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
 }
 
 // Up to two operands and what has to be copied for them, in one workspace.
@@ -118,7 +117,8 @@ fxtx_status_t run_empty(fxtx_type_t type, const Epilogue& e, int64_t rows, int64
 // HBM. A persistent CTA's tiles follow one another, each for as long as its products or its epilogue
 // take. On top come a fixed cost (launch, filling the pipeline, the last epilogue) and the exchange of
 // partial sums: between the CTAs of a cluster, or through memory and a second kernel.
-TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count) {
+static TcPlan best_plan(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count, bool clusters,
+                        int64_t most) {
   TcPlan best;
   double best_t = 1e300;
   const double floor = planes * 2.0 * K * (double)(M + N) / 3400.0;
@@ -156,19 +156,28 @@ TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool
     if (cluster)
       for (int s = 1; s <= 8; s *= 2) price(s);
     else
-      for (int64_t s = 1; s <= std::min<int64_t>(kb, 4 * units); s = s < 8 ? s + 1 : s + s / 4) price(s);
+      for (int64_t s = 1; s <= std::min<int64_t>({kb, 4 * units, most}); s = s < 8 ? s + 1 : s + s / 4) price(s);
   };
   const int top = planes == 3 ? 64 : 128;  // the widest tile of the split kernel
-  if (M <= top)
-    for (int bn : {16, 32, 64, 128})
-      if (bn >= M && bn <= top) consider(true, true, 1, bn);
-  consider(false, true, 1, 64);
-  if (planes == 1) consider(false, true, 1, 128);
+  if (clusters) {
+    if (M <= top)
+      for (int bn : {16, 32, 64, 128})
+        if (bn >= M && bn <= top) consider(true, true, 1, bn);
+    consider(false, true, 1, 64);
+    if (planes == 1) consider(false, true, 1, 128);
+  }
   consider(false, false, 1, 64);
   consider(false, false, 1, 128);
   consider(false, false, 2, 128);
   if (planes == 1) consider(false, false, 2, 256);
   return best;
+}
+
+TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count) {
+  return best_plan(M, N, K, planes, a_mn, b_mn, sm_count, true, INT64_MAX);
+}
+TcPlan plan_persistent(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count, int64_t splits) {
+  return best_plan(M, N, K, planes, a_mn, b_mn, sm_count, false, splits);
 }
 
 // Whether a result of m rows is formed on the CUDA cores.

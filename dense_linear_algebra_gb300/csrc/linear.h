@@ -58,6 +58,13 @@ struct TcPlan {
   int cg = 1, bn = 128, splits = 1;
 };
 TcPlan plan_product(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count);
+// The same among the persistent kernel's layouts, with at most `splits` parts of kk.
+TcPlan plan_persistent(int64_t M, int64_t N, int64_t K, int planes, bool a_mn, bool b_mn, int sm_count, int64_t splits);
+
+// Whether the tensor copies can read a 16-bit operand where it lies.
+bool copyable(const Operand& o);
+// The operand's planes (rows x cols in memory), where they will lie in `at` if it has to be packed (`bytes` of it).
+Planes planes_of(const Operand& o, fxtx_type_t type, int64_t mn, int64_t k, char* at, size_t* bytes);
 
 // A copy of a matrix with an aligned pitch: 16-bit as it is, float32 as three bfloat16 planes.
 struct PackArgs {
@@ -101,6 +108,8 @@ bool thin_shape(int64_t n, int64_t k);
 fxtx_status_t run_thin_linear(const LayerArgs& l, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_thin_grad(const LayerArgs& l, const GradArgs& g, const DeviceInfo& dev, cudaStream_t st);
 
+// Whether a result of m rows is formed that way.
+bool few_rows(fxtx_type_t type, int64_t m, bool by_column);
 // float32 results of few rows on the CUDA cores: out = e(X W), W's entry (j, c) at W[j * ld + c] or by_column at
 // W[c * ld + j]; X as it is, or (x_planes > 0) as its three bfloat16 planes.
 constexpr int kFewByRow = 16, kFewByColumn = 8;  // rows at most

@@ -1,0 +1,507 @@
+// loss.cu — softmax cross entropy on a linear layer's outputs, and its gradient, without the outputs being kept:
+//     z = X W + b,  lse_i = log sum_j exp z_ij,  loss_i = lse_i - z_i,label
+//     D_ij = g_i (exp(z_ij - lse_i) - [j = label_i]),  dX = D W^T,  dW = X^T D,  db = the column sums of D
+//
+// Bound: the tensor cores, 2 m n k operations forward and 6 m n k backward (z is formed again), or with few rows the
+// stream of W.
+//
+// Forward: one product whose epilogue reduces each row of a tile to its largest entry and its sum of exponentials; a
+// second kernel joins a row's parts. Nothing of the size of z is written.
+//
+// Backward: W in pieces of the classes and X in slabs of rows, so that D of one piece and slab takes kCap bytes at most.
+// Per piece and slab three products: z again, whose epilogue writes D as an operand of the others (of the layer's type,
+// of float32 as three bfloat16 planes) and its column sums; D W^T, added up over the pieces in fp32; X^T D, over the slabs.
+//
+// float16 has nothing below 6e-8, where a mean's gradient over many classes lies: D is held multiplied by the power of
+// two that brings the largest |g| to 2^14 .. 2^15, which the last of the sums takes back. What is lost is below 2^-39 of
+// that |g| (below 2^-29 of it, digits are).
+//
+// At most 64 features and classes: thin_loss.cu. float32 of few rows: z in fp32 on the CUDA cores (few.cu), its statistics
+// or D by kernels of their own, and the layer's gradient from D.
+#include <algorithm>
+
+#include "act.cuh"
+#include "common.cuh"
+#include "host.h"
+#include "kernels.h"
+#include "loss.h"
+
+namespace fxtx {
+namespace {
+
+// Workspace for D, and for each other array that goes in pieces: the pool keeps 1 GB between calls.
+constexpr int64_t kCap = (int64_t)512 << 20, kSmallCap = (int64_t)256 << 20;
+constexpr int64_t kRows = 16384;  // of a slab, where the classes leave the choice
+
+fxtx_status_t status_of(cudaError_t e) {
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+// A row's statistics from its parts, and its loss: 32 rows a CTA, 8 threads a row.
+__global__ void __launch_bounds__(256) loss_join_kernel(const float2* stats, int64_t parts, int64_t rows, const float* target,
+                                                        const void* labels, bool labels64, int64_t count, float* loss, float* lse) {
+  __shared__ float2 part[8][32];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t i = (int64_t)blockIdx.x * 32 + x;
+  float top = -INFINITY, sum = 0.f;
+  auto add = [&](float2 s) {
+    const float most = fmaxf(top, s.x), from = most == -INFINITY ? 0.f : most;
+    sum = sum * expf(top - from) + s.y * expf(s.x - from);
+    top = most;
+  };
+  after_previous();
+  if (i < rows) {
+#pragma unroll 4
+    for (int64_t p = y; p < parts; p += 8) add(stats[p * rows + i]);
+  }
+  part[y][x] = make_float2(top, sum);
+  __syncthreads();
+  if (y != 0 || i >= rows) return;
+  for (int q = 1; q < 8; ++q) add(part[q][x]);
+  const float from = top == -INFINITY ? 0.f : top, rest = logf(sum);
+  if (lse) lse[i] = from + rest;
+  if (loss) loss[i] = label_at(labels, labels64, i, count) >= 0 ? (from - target[i]) + rest : 0.f;
+}
+
+constexpr int SEG = 4096;  // of a row that a CTA reduces
+
+// The statistics of rows of Z in memory: part s of row i is columns SEG s and on.
+__global__ void __launch_bounds__(256) row_stats_kernel(const float* Z, int64_t rows, int64_t k, int64_t segs, float2* stats,
+                                                        float* target, const void* labels, bool labels64) {
+  __shared__ float2 part[8];
+  const int64_t i = blockIdx.x / segs, s = blockIdx.x % segs, j0 = s * SEG, end = min(k, j0 + SEG);
+  after_previous();
+  float v[SEG / 256], top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int q = 0; q < SEG / 256; ++q) {
+    const int64_t j = j0 + q * 256 + threadIdx.x;
+    v[q] = j < end ? Z[i * k + j] : -INFINITY;
+    top = fmaxf(top, v[q]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, shfl_xor(top, o));
+  const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll
+  for (int q = 0; q < SEG / 256; ++q) sum += expf(v[q] - from);
+  sum = group_sum<32>(sum);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(top, sum);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float most = -INFINITY, all = 0.f;
+  for (int w = 0; w < 8; ++w) most = fmaxf(most, part[w].x);
+  const float base = most == -INFINITY ? 0.f : most;
+  for (int w = 0; w < 8; ++w) all += part[w].y * expf(part[w].x - base);
+  stats[s * rows + i] = make_float2(most, all);
+  const int64_t label = label_at(labels, labels64, i, k);
+  if (label >= j0 && label < end) target[i] = Z[i * k + label];
+}
+
+// Z to D, in place.
+__global__ void __launch_bounds__(256) row_slope_kernel(float* Z, int64_t rows, int64_t k, const void* labels, bool labels64,
+                                                        const float* lse, const float* g, float gain) {
+  after_previous();
+  const int64_t stride = (int64_t)gridDim.x * 256;
+  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * k; x += stride) {
+    const int64_t i = x / k, j = x - i * k, label = label_at(labels, labels64, i, k);
+    float d = 0.f;
+    if (label >= 0) {
+      const float w = g ? gain * g[i] : gain;
+      d = w * expf(Z[x] - lse[i]);
+      if (j == label) d -= w;
+    }
+    Z[x] = d;
+  }
+}
+
+__global__ void __launch_bounds__(1024) scales_kernel(const float* g, int64_t m, float gain, float* scales) {
+  __shared__ uint32_t warps[32];
+  after_previous();
+  // magnitudes as integers order as they are; a NaN is above all
+  uint32_t most = g ? 0u : __float_as_uint(1.f);
+  if (g) {
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < m; i += 1024) most = max(most, __float_as_uint(g[i]) & 0x7fffffffu);
+  }
+  most = __reduce_max_sync(FULL_MASK, most);
+  if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = most;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 32; ++w) most = max(most, warps[w]);
+  const float top = __uint_as_float(most) * fabsf(gain);
+  int e = 14;
+  if (top > 0.f && top <= 3.4e38f) e = min(max(ilogbf(top), -100), 120);
+  scales[0] = scalbnf(1.f, 14 - e);
+  scales[1] = scalbnf(1.f, e - 14);
+}
+
+// db from the column sums of D: 32 columns a CTA, 8 threads a column, in order; over the slabs through `keep`.
+template <typename T>
+__global__ void __launch_bounds__(256) db_join_kernel(const float* sums, int64_t parts, int64_t cols, const float* in, float* keep,
+                                                      const float* scales, T* db) {
+  __shared__ float part[8][32];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int64_t j = (int64_t)blockIdx.x * 32 + x;
+  float s = 0.f;
+  after_previous();
+  if (j < cols) {
+#pragma unroll 4
+    for (int64_t p = y; p < parts; p += 8) s += sums[p * cols + j];
+  }
+  part[y][x] = s;
+  __syncthreads();
+  if (y != 0 || j >= cols) return;
+  for (int i = 1; i < 8; ++i) s += part[i][x];
+  if (in) s += in[j];
+  if (keep) keep[j] = s;
+  else db[j] = from_f32<T>(scales ? s * scales[1] : s);
+}
+
+size_t up(int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); }
+int64_t floor256(int64_t x) { return std::max<int64_t>(256, x / 256 * 256); }
+
+// A workspace cut into arrays: sizes first, then addresses.
+struct Cut {
+  char* base = nullptr;
+  size_t bytes = 0;
+  char* take(int64_t n) {
+    char* p = base ? base + bytes : nullptr;
+    bytes += up(n);
+    return n ? p : nullptr;
+  }
+};
+
+// `rows` rows of a row-major matrix from row r on, `cols` columns from column c on, as an operand; packed to `at` if it must be.
+struct Part {
+  Operand o;
+  PackArgs pack;
+  bool packed = false;
+  Planes planes;
+};
+const char* entry(const void* p, int64_t ld, int64_t r, int64_t c, int size) { return static_cast<const char*>(p) + (r * ld + c) * size; }
+
+Part part_of(fxtx_type_t type, const void* p, int64_t ld, int64_t r, int64_t rows, int64_t c, int64_t cols, char* at) {
+  Part x;
+  x.o.p = entry(p, ld, r, c, type_size(type));
+  x.o.ld = ld;
+  size_t need = 0;
+  x.planes = planes_of(x.o, type, rows, cols, at, &need);  // (K-major: rows x cols in memory)
+  if (need) {
+    x.packed = true;
+    x.pack.src = x.o.p;
+    x.pack.rows = rows;
+    x.pack.cols = cols;
+    x.pack.ld = ld;
+    x.pack.dst = at;
+    x.pack.pitch = x.planes.pitch;
+    x.pack.plane_stride = x.planes.plane_stride;
+    x.o.p = at;
+    x.o.ld = x.planes.pitch;
+    x.o.plane_stride = type == FXTX_F32 ? x.planes.plane_stride : 0;
+  }
+  return x;
+}
+// The same matrix as an operand whose kk runs along its rows, or along its columns.
+Planes as(const Part& x, bool mn_major) {
+  Planes p = x.planes;
+  p.mn_major = mn_major;
+  return p;
+}
+
+// Of an operand that has to be packed (float32, or 16 bits that the tensor copies cannot read where they lie): the bytes
+// a row (or column) of it takes; else 0.
+int64_t packed_bytes(fxtx_type_t type, const void* p, int64_t ld, int64_t entries) {
+  Operand o;
+  o.p = p;
+  o.ld = ld;
+  if (type != FXTX_F32 && copyable(o)) return 0;
+  return (entries + 7) / 8 * 8 * (type == FXTX_F32 ? 6 : 2);
+}
+
+// The classes of W from c on: rows of a matrix stored by columns, else columns.
+Part classes_of(const LayerArgs& l, int64_t c, int64_t n, char* at) {
+  return l.w_trans ? part_of(l.type, l.W, l.ldw, c, n, 0, l.n, at) : part_of(l.type, l.W, l.ldw, 0, l.n, c, n, at);
+}
+
+// An even division into pieces of at most `most` (a multiple of 256).
+int64_t piece_of(int64_t n, int64_t most) {
+  if (n <= most) return n;
+  const int64_t pieces = (n + most - 1) / most;
+  return ((n + pieces - 1) / pieces + 255) / 256 * 256;
+}
+
+const void* bias_at(const LayerArgs& l, int64_t c) {
+  return l.e.bias ? static_cast<const char*>(l.e.bias) + c * type_size(l.type) : nullptr;
+}
+
+const void* labels_at(const LossArgs& a, int64_t r) { return static_cast<const char*>(a.labels) + r * (a.labels64 ? 8 : 4); }
+
+fxtx_status_t few_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  const int64_t segs = (l.k + SEG - 1) / SEG;
+  Cut c;
+  char* ws = nullptr;
+  float *z = nullptr, *target = nullptr;
+  float2* stats = nullptr;
+  for (int pass = 0; pass < 2; ++pass) {
+    z = reinterpret_cast<float*>(c.take(l.m * l.k * 4));
+    stats = reinterpret_cast<float2*>(c.take(segs * l.m * 8));
+    target = reinterpret_cast<float*>(c.take(l.m * 4));
+    if (pass == 0) {
+      const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), c.bytes, st);
+      if (s != FXTX_OK) return s;
+      c.base = ws;
+      c.bytes = 0;
+    }
+  }
+  Epilogue e;
+  e.bias = l.e.bias;
+  e.out = z;
+  e.ldo = l.k;
+  fxtx_status_t s = run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, e, dev, st);
+  if (s == FXTX_OK)
+    s = status_of(launch_kernel(row_stats_kernel, dim3((unsigned)(l.m * segs)), 256, 0, st, z, l.m, l.k, segs, stats, target, a.labels,
+                                a.labels64));
+  if (s == FXTX_OK)
+    s = status_of(launch_kernel(loss_join_kernel, dim3((unsigned)((l.m + 31) / 32)), 256, 0, st, stats, segs, l.m, target, a.labels,
+                                a.labels64, l.k, a.loss, a.lse));
+  cudaFreeAsync(ws, st);
+  return s;
+}
+
+fxtx_status_t few_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  float* z = nullptr;
+  fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&z), (size_t)(l.m * l.k * 4), st);
+  if (s != FXTX_OK) return s;
+  Epilogue e;
+  e.bias = l.e.bias;
+  e.out = z;
+  e.ldo = l.k;
+  s = run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, e, dev, st);
+  if (s == FXTX_OK) {
+    const int64_t ctas = std::min<int64_t>((l.m * l.k + 255) / 256, (int64_t)dev.sm_count * 8);
+    s = status_of(launch_kernel(row_slope_kernel, dim3((unsigned)ctas), 256, 0, st, z, l.m, l.k, a.labels, a.labels64, a.lse_in, a.g,
+                                a.gain));
+  }
+  if (s == FXTX_OK) {
+    GradArgs g;
+    g.G = z;
+    g.ldg = l.k;
+    g.DX = a.DX;
+    g.lddx = a.lddx;
+    g.DW = a.DW;
+    g.lddw = a.lddw;
+    g.DB = a.DB;
+    s = run_grad(l, g, dev, st);
+  }
+  cudaFreeAsync(z, st);
+  return s;
+}
+
+}  // namespace
+
+cudaError_t launch_scales(const float* g, int64_t m, float gain, float* scales, cudaStream_t st) {
+  return launch_kernel(scales_kernel, dim3(1), 1024, 0, st, g, m, gain, scales);
+}
+
+fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  if (few_rows(l.type, l.m, l.w_trans)) return few_loss(l, a, dev, st);
+  // W's classes go in pieces where they have to be packed, X's rows also where the parts' statistics would take more
+  const int64_t w_row = packed_bytes(l.type, l.W, l.ldw, l.n), x_row = packed_bytes(l.type, l.X, l.ldx, l.n);
+  const int64_t Vp = piece_of(l.k, w_row ? floor256(kSmallCap / w_row) : l.k), pieces = (l.k + Vp - 1) / Vp;
+  const int64_t parts_most = (Vp + 31) / 32 + 8;  // of a piece
+  int64_t most = floor256(kSmallCap / (8 * parts_most * pieces));
+  if (x_row) most = std::min(most, floor256(kSmallCap / x_row));
+  const int64_t mc = piece_of(l.m, most);
+
+  Cut c;
+  char *ws = nullptr, *w_at = nullptr, *x_at = nullptr;
+  float2* stats = nullptr;
+  float* target = nullptr;
+  for (int pass = 0; pass < 2; ++pass) {
+    // (the pitch of W stored by rows runs over the classes)
+    w_at = c.take(w_row ? (l.w_trans ? Vp * w_row : l.n * ((Vp + 7) / 8 * 8) * (l.type == FXTX_F32 ? 6 : 2)) : 0);
+    x_at = c.take(mc * x_row);
+    stats = reinterpret_cast<float2*>(c.take(parts_most * pieces * mc * 8));
+    target = reinterpret_cast<float*>(c.take(mc * 4));
+    if (pass == 0) {
+      const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), c.bytes, st);
+      if (s != FXTX_OK) return s;
+      c.base = ws;
+      c.bytes = 0;
+    }
+  }
+  fxtx_status_t s = FXTX_OK;
+  for (int64_t r = 0; r < l.m && s == FXTX_OK; r += mc) {
+    const int64_t rows = std::min(mc, l.m - r);
+    const Part x = part_of(l.type, l.X, l.ldx, r, rows, 0, l.n, x_at);
+    int64_t parts = 0;
+    for (int64_t v = 0; v < l.k && s == FXTX_OK; v += Vp) {
+      const int64_t n = std::min(Vp, l.k - v);
+      const Part w = classes_of(l, v, n, w_at);
+      PackArgs packs[2];
+      int count = 0;
+      if (x.packed && v == 0) packs[count++] = x.pack;
+      if (w.packed && (pieces > 1 || r == 0)) packs[count++] = w.pack;
+      if (count) s = status_of(launch_prepare(l.type, nullptr, packs, count, dev.sm_count, st));
+      PlanesProduct q;
+      q.M = rows;
+      q.N = n;
+      q.K = l.n;
+      q.A = as(x, false);
+      q.B = as(w, !l.w_trans);
+      q.e.bias = bias_at(l, v);
+      ModeArgs<1> m;
+      m.labels = labels_at(a, r);
+      m.labels64 = a.labels64;
+      m.count = l.k;
+      m.col0 = v;
+      m.stats = stats + parts * rows;
+      m.target = target;
+      if (s == FXTX_OK) s = run_stats(l.type, q, m, dev, st);
+      parts += stat_parts(l.type, q, dev);
+    }
+    if (s == FXTX_OK)
+      s = status_of(launch_kernel(loss_join_kernel, dim3((unsigned)((rows + 31) / 32)), 256, 0, st, stats, parts, rows, target,
+                                  labels_at(a, r), a.labels64, l.k, a.loss ? a.loss + r : nullptr, a.lse ? a.lse + r : nullptr));
+  }
+  cudaFreeAsync(ws, st);
+  return s;
+}
+
+fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  if (few_rows(l.type, l.m, l.w_trans)) return few_grad(l, a, dev, st);
+  const bool f32 = l.type == FXTX_F32;
+  const int size = type_size(l.type), d_size = f32 ? 6 : 2;
+  const int64_t w_row = packed_bytes(l.type, l.W, l.ldw, l.n), x_row = packed_bytes(l.type, l.X, l.ldx, l.n);
+  // slabs of rows and pieces of classes
+  int64_t mc = std::min(l.m, kRows);
+  int64_t v_most = floor256(kCap / (d_size * mc));
+  if (w_row) v_most = std::min(v_most, floor256(kSmallCap / w_row));
+  const int64_t Vp = piece_of(l.k, v_most);
+  int64_t m_most = floor256(kCap / (d_size * ((Vp + 7) / 8 * 8)));
+  if (x_row) m_most = std::min(m_most, floor256(kSmallCap / x_row));
+  mc = piece_of(l.m, m_most);
+  const int64_t pieces = (l.k + Vp - 1) / Vp, slabs = (l.m + mc - 1) / mc;
+  const int64_t pitch = (Vp + 7) / 8 * 8;
+
+  Cut c;
+  char *ws = nullptr, *w_at = nullptr, *x_at = nullptr, *d_at = nullptr;
+  float *dx_sum = nullptr, *dw_sum = nullptr, *db_parts = nullptr, *db_sum = nullptr, *scales = nullptr;
+  for (int pass = 0; pass < 2; ++pass) {
+    w_at = c.take(w_row ? (l.w_trans ? Vp * w_row : l.n * pitch * d_size) : 0);
+    x_at = c.take(mc * x_row);
+    d_at = c.take(mc * pitch * d_size);
+    dx_sum = reinterpret_cast<float*>(c.take(a.DX && pieces > 1 ? l.m * l.n * 4 : 0));
+    dw_sum = reinterpret_cast<float*>(c.take(a.DW && slabs > 1 ? Vp * l.n * 4 : 0));
+    db_parts = reinterpret_cast<float*>(c.take(a.DB ? (mc + 31) / 32 * Vp * 4 : 0));
+    db_sum = reinterpret_cast<float*>(c.take(a.DB && slabs > 1 ? Vp * 4 : 0));
+    scales = reinterpret_cast<float*>(c.take(l.type == FXTX_F16 ? 8 : 0));
+    if (pass == 0) {
+      const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), c.bytes, st);
+      if (s != FXTX_OK) return s;
+      c.base = ws;
+      c.bytes = 0;
+    }
+  }
+  fxtx_status_t s = FXTX_OK;
+  if (scales) s = status_of(launch_scales(a.g, l.m, a.gain, scales, st));
+  for (int64_t v = 0; v < l.k && s == FXTX_OK; v += Vp) {
+    const int64_t n = std::min(Vp, l.k - v);
+    const Part w = classes_of(l, v, n, w_at);
+    for (int64_t r = 0; r < l.m && s == FXTX_OK; r += mc) {
+      const int64_t rows = std::min(mc, l.m - r);
+      const Part x = part_of(l.type, l.X, l.ldx, r, rows, 0, l.n, x_at);
+      PackArgs packs[2];
+      int count = 0;
+      if (x.packed && (slabs > 1 || v == 0)) packs[count++] = x.pack;
+      if (w.packed && r == 0) packs[count++] = w.pack;
+      if (count) s = status_of(launch_prepare(l.type, nullptr, packs, count, dev.sm_count, st));
+      // D
+      PlanesProduct q;
+      q.M = rows;
+      q.N = n;
+      q.K = l.n;
+      q.A = as(x, false);
+      q.B = as(w, !l.w_trans);
+      q.e.bias = bias_at(l, v);
+      ModeArgs<2> d;
+      d.labels = labels_at(a, r);
+      d.labels64 = a.labels64;
+      d.count = l.k;
+      d.col0 = v;
+      d.lse = a.lse_in + r;
+      d.g = a.g ? a.g + r : nullptr;
+      d.gain = a.gain;
+      d.scales = scales;
+      d.D = d_at;
+      d.ldd = pitch;
+      d.d_planes = f32 ? rows * pitch : 0;
+      d.sums = db_parts;
+      d.sums_ld = n;
+      if (s == FXTX_OK) s = run_slope(l.type, q, d, dev, st);
+      if (s == FXTX_OK && a.DB) {
+        const float* in = r > 0 ? db_sum : nullptr;
+        float* keep = r + mc < l.m ? db_sum : nullptr;
+        const dim3 grid((unsigned)((n + 31) / 32));
+        char* db = static_cast<char*>(a.DB) + v * size;
+        const int64_t parts = (rows + 31) / 32;
+        switch (l.type) {
+          case FXTX_F32:
+            s = status_of(launch_kernel(db_join_kernel<float>, grid, 256, 0, st, db_parts, parts, n, in, keep, scales, reinterpret_cast<float*>(db)));
+            break;
+          case FXTX_BF16:
+            s = status_of(launch_kernel(db_join_kernel<__nv_bfloat16>, grid, 256, 0, st, db_parts, parts, n, in, keep, scales,
+                                        reinterpret_cast<__nv_bfloat16*>(db)));
+            break;
+          default:
+            s = status_of(launch_kernel(db_join_kernel<__half>, grid, 256, 0, st, db_parts, parts, n, in, keep, scales, reinterpret_cast<__half*>(db)));
+            break;
+        }
+      }
+      Planes dp;
+      dp.p = d_at;
+      dp.rows = rows;
+      dp.cols = n;
+      dp.pitch = pitch;
+      dp.planes = f32 ? 3 : 1;
+      dp.plane_stride = rows * pitch;
+      if (s == FXTX_OK && a.DX) {
+        PlanesProduct t;
+        t.M = rows;
+        t.N = l.n;
+        t.K = n;
+        t.A = dp;
+        t.B = as(w, l.w_trans);
+        t.e.out = static_cast<char*>(a.DX) + r * a.lddx * size;
+        t.e.ldo = a.lddx;
+        ModeArgs<3> m;
+        m.in = v > 0 ? dx_sum + r * l.n : nullptr;
+        m.keep = v + Vp < l.k ? dx_sum + r * l.n : nullptr;
+        m.scales = scales;
+        s = run_sum(l.type, t, m, dev, st);
+      }
+      if (s == FXTX_OK && a.DW) {
+        Planes dm = dp, xm = as(x, true);
+        dm.mn_major = true;
+        PlanesProduct t;
+        t.M = l.w_trans ? n : l.n;
+        t.N = l.w_trans ? l.n : n;
+        t.K = rows;
+        t.A = l.w_trans ? dm : xm;
+        t.B = l.w_trans ? xm : dm;
+        t.e.out = static_cast<char*>(a.DW) + (l.w_trans ? v * a.lddw : v) * size;
+        t.e.ldo = a.lddw;
+        ModeArgs<3> m;
+        m.in = r > 0 ? dw_sum : nullptr;
+        m.keep = r + mc < l.m ? dw_sum : nullptr;
+        m.scales = scales;
+        s = run_sum(l.type, t, m, dev, st);
+      }
+    }
+  }
+  cudaFreeAsync(ws, st);
+  return s;
+}
+
+}  // namespace fxtx

@@ -1,13 +1,14 @@
 """What training a classifier takes besides its layers, on CUDA tensors: layer norm (``layer_norm``), the embedding lookup
-(``embedding``), each with its gradient, over the C entries of the same names. The package only marshals
+(``embedding``) and softmax cross entropy on a linear layer (``cross_entropy``), each with its gradient, over the C entries of the same names. The package only marshals
 arguments: every step runs in the kernels of ``libfusedxtx.so``.
 """
 from __future__ import annotations
 
 import torch
 
-from ._lib import fxtx_embedding, fxtx_embedding_grad, fxtx_layer_norm, fxtx_layer_norm_grad
-from .layers import _call, _current_stream, _features, _on_stream, _pitch, _type
+from ._lib import (fxtx_cross_entropy, fxtx_cross_entropy_grad, fxtx_embedding, fxtx_embedding_grad, fxtx_layer_norm,
+                   fxtx_layer_norm_grad)
+from .layers import _call, _current_stream, _features, _on_stream, _pitch, _type, _weights
 
 _INT_BITS = {torch.int32: 32, torch.int64: 64}
 
@@ -138,3 +139,63 @@ def embedding_grad(G, ids, count: int, scale: float = 1.0, out=None, stream=None
     _call(fxtx_embedding_grad, index, code, m, n, count, G.data_ptr(), ldg, pi, bits, scale, out.data_ptr(), ldo,
           _current_stream(index))
     return out
+
+
+def cross_entropy(X, W, labels, b=None, stream=None):
+    """Softmax cross entropy on z = X W + b, without keeping z: (loss, lse), (m,) float32 tensors with lse_i = log sum_j exp z_ij
+    and loss_i = lse_i - z_i,labels[i].
+
+    X (m, n), W (n, k) and b (k,) have one dtype and are laid out as for ``linear``; n and k are at least 1. ``labels``:
+    (m,), int32 or int64; a row whose label lies outside 0 .. k - 1 is left out (loss 0, no gradient). A bias of -inf
+    takes a class out; a row without a class left has lse = -inf and a loss of NaN. Runs on the current stream, or on
+    ``stream``, which then owns the new tensors. Autograd records nothing: ``cross_entropy_grad`` takes lse.
+    """
+    if stream is not None:
+        context, stream = _on_stream(stream, X.get_device())
+        with context:
+            return cross_entropy(X, W, labels, b)
+    code, dt, di, m, n, ldx = _features(X)
+    k, ldw, trans = _weights(W, dt, n, di)
+    pb = _vector(b, dt, k, "b", di)
+    pl, bits = _integers(labels, m, "labels", di)
+    loss, lse = torch.empty((2, m), dtype=torch.float32, device=X.device).unbind()
+    _call(fxtx_cross_entropy, di, code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans, pb, pl, bits, loss.data_ptr(),
+          lse.data_ptr(), _current_stream(di))
+    return loss, lse
+
+
+def cross_entropy_grad(X, W, labels, lse, b=None, g=1.0, need=(True, True, True), stream=None):
+    """The gradient of ``cross_entropy``: with D_ij = g_i (exp(z_ij - lse_i) - [j = labels[i]]), (dX, dW, db) = (D W^T, X^T D, the
+    column sums of D).
+
+    ``g`` is the gradient at the losses: a number for all rows (1 / m for their mean), or an (m,) float32 tensor.
+    ``need`` says which of the three are computed; the others come back as None. z is formed again, in pieces of the
+    classes. D of a 16-bit type is rounded to it before the products; of float16 it is held multiplied by a power of two
+    that brings the largest |g_i| to 2^14 .. 2^15, so that what is below 2^-39 of that is lost. db is summed from the
+    unrounded values. dW is stored as W is: for W = P.t() it is the transposed view of a (k, n) tensor. Types, layouts,
+    labels and streams are those of ``cross_entropy``.
+    """
+    if stream is not None:
+        context, stream = _on_stream(stream, X.get_device())
+        with context:
+            return cross_entropy_grad(X, W, labels, lse, b, g, need)
+    code, dt, di, m, n, ldx = _features(X)
+    k, ldw, trans = _weights(W, dt, n, di)
+    pb = _vector(b, dt, k, "b", di)
+    pl, bits = _integers(labels, m, "labels", di)
+    ps = _vector(lse, torch.float32, m, "lse", di)
+    if ps is None:
+        raise ValueError("lse: the gradient needs what cross_entropy gave")
+    pg, gain = None, 1.0
+    if isinstance(g, torch.Tensor):
+        pg = _vector(g, torch.float32, m, "g", di)
+    else:
+        gain = float(g)
+    device, (want_x, want_w, want_b) = X.device, need
+    dX = torch.empty((m, n), dtype=dt, device=device) if want_x else None
+    dW = torch.empty((k, n) if trans else (n, k), dtype=dt, device=device) if want_w else None
+    db = torch.empty(k, dtype=dt, device=device) if want_b else None
+    _call(fxtx_cross_entropy_grad, di, code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans, pb, pl, bits, ps, pg, gain,
+          dX.data_ptr() if want_x else None, n, dW.data_ptr() if want_w else None, n if trans else k,
+          db.data_ptr() if want_b else None, _current_stream(di))
+    return dX, dW.t() if trans and want_w else dW, db

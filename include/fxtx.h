@@ -476,6 +476,34 @@ fxtx_status_t fxtx_embedding(fxtx_type_t type, int64_t m, int64_t n, int64_t cou
 fxtx_status_t fxtx_embedding_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t count, const void* G, int64_t ldg, const void* ids,
                                   int id_bits, double scale, void* DE, int64_t ldde, void* stream);
 
+/*
+ * Softmax cross entropy on a linear layer's outputs, which are not kept: with z = X W + b (m x k, the classes),
+ *
+ *     LSE_i = log sum_j exp z_ij      LOSS_i = LSE_i - z_i,labels[i]
+ *
+ * X, W, w_trans and b are those of fxtx_linear; n and k are at least 1. labels: m integers of label_bits (32 or 64)
+ * bits; a row whose label lies outside 0 .. k - 1 is left out: its loss is 0 and its gradient zero (-1, or -100, for
+ * rows to be ignored). LOSS and LSE: m fp32 values each, or NULL. A bias of -inf takes a class out; a row
+ * without a class left has LSE = -inf and a loss of NaN, and an infinite or NaN output makes its row NaN.
+ *
+ * The gradient, from the LSE that the forward call gave: with D_ij = gain G_i (exp(z_ij - LSE_i) - [j = labels[i]]),
+ *
+ *     DX = D W^T (m x n)      DW = X^T D (n x k)      DB = the column sums of D (k)
+ *
+ * G: m fp32 values, or NULL for ones (a mean's gain is 1 / m). Each of DX, DW, DB may be NULL (not computed). DW is
+ * stored as W is. z is formed again; D of a 16-bit type is rounded to it before the products (with more than 64
+ * features or classes held in pieces of up to 512 MB), float16 multiplied by a power of two that brings the largest
+ * |gain G_i| to 2^14 .. 2^15: what is below 2^-39 of that is lost. DB is summed from the unrounded values. m = 0 gives
+ * DW = 0 and DB = 0. Outputs must not overlap anything else. Precision and errors are those of fxtx_linear.
+ */
+fxtx_status_t fxtx_cross_entropy(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                                 int64_t ldw, int w_trans, const void* b, const void* labels, int label_bits, float* LOSS, float* LSE,
+                                 void* stream);
+fxtx_status_t fxtx_cross_entropy_grad(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
+                                      int64_t ldw, int w_trans, const void* b, const void* labels, int label_bits, const float* LSE,
+                                      const float* G, double gain, void* DX, int64_t lddx, void* DW, int64_t lddw, void* DB,
+                                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif
