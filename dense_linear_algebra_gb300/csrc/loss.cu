@@ -16,8 +16,8 @@
 // two that brings the largest |g| to 2^14 .. 2^15, which the last of the sums takes back. What is lost is below 2^-39 of
 // that |g| (below 2^-29 of it, digits are).
 //
-// At most 64 features and classes: thin_loss.cu. float32 of few rows: z in fp32 on the CUDA cores (few.cu), its statistics
-// or D by kernels of their own, and the layer's gradient from D.
+// At most 64 features and classes: thin_loss.cu. Few rows (float32: those of few.cu; 16 bits: up to 128): z is written out in
+// fp32, its statistics or D formed by kernels of their own, and the products are those of few rows.
 #include <algorithm>
 
 #include "act.cuh"
@@ -39,45 +39,88 @@ fxtx_status_t status_of(cudaError_t e) {
   return FXTX_ERR_CUDA;
 }
 
-// A row's statistics from its parts, and its loss: 32 rows a CTA, 8 threads a row.
+// A row's statistics from its parts, and its loss: RX rows a CTA, 256 / RX threads a row, 8 parts on their way at a time.
+template <int RX>
 __global__ void __launch_bounds__(256) loss_join_kernel(const float2* stats, int64_t parts, int64_t rows, const float* target,
                                                         const void* labels, bool labels64, int64_t count, float* loss, float* lse) {
-  __shared__ float2 part[8][32];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t i = (int64_t)blockIdx.x * 32 + x;
+  constexpr int RY = 256 / RX;
+  __shared__ float2 part[RY][RX];
+  const int x = threadIdx.x % RX, y = threadIdx.x / RX;
+  const int64_t i = (int64_t)blockIdx.x * RX + x;
   float top = -INFINITY, sum = 0.f;
-  auto add = [&](float2 s) {
-    const float most = fmaxf(top, s.x), from = most == -INFINITY ? 0.f : most;
-    sum = sum * expf(top - from) + s.y * expf(s.x - from);
+  auto add = [&](const float2* s, int n) {
+    float most = top;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) most = fmaxf(most, s[q].x);
+    const float from = most == -INFINITY ? 0.f : most;
+    sum *= expf(top - from);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) sum += s[q].y * expf(s[q].x - from);
     top = most;
   };
   after_previous();
   if (i < rows) {
-#pragma unroll 4
-    for (int64_t p = y; p < parts; p += 8) add(stats[p * rows + i]);
+    for (int64_t p = y; p < parts; p += 8 * RY) {
+      float2 s[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] = p + q * RY < parts ? stats[(p + q * RY) * rows + i] : make_float2(-INFINITY, 0.f);
+      add(s, 8);
+    }
   }
   part[y][x] = make_float2(top, sum);
-  __syncthreads();
+  // a row's threads two by two
+  for (int o = RY / 2; o > 0; o >>= 1) {
+    __syncthreads();
+    if (y >= o) continue;
+    add(&part[y + o][x], 1);
+    part[y][x] = make_float2(top, sum);
+  }
   if (y != 0 || i >= rows) return;
-  for (int q = 1; q < 8; ++q) add(part[q][x]);
   const float from = top == -INFINITY ? 0.f : top, rest = logf(sum);
   if (lse) lse[i] = from + rest;
   if (loss) loss[i] = label_at(labels, labels64, i, count) >= 0 ? (from - target[i]) + rest : 0.f;
 }
 
-constexpr int SEG = 4096;  // of a row that a CTA reduces
+cudaError_t launch_join(const float2* stats, int64_t parts, int64_t rows, const float* target, const void* labels, bool labels64,
+                        int64_t count, float* loss, float* lse, const DeviceInfo& dev, cudaStream_t st) {
+  // few rows: a CTA each
+  const int rx = rows < 8 * (int64_t)dev.sm_count ? 1 : 8;
+  const dim3 grid((unsigned)((rows + rx - 1) / rx));
+  return rx == 1 ? launch_kernel(loss_join_kernel<1>, grid, 256, 0, st, stats, parts, rows, target, labels, labels64, count, loss, lse)
+                 : launch_kernel(loss_join_kernel<8>, grid, 256, 0, st, stats, parts, rows, target, labels, labels64, count, loss, lse);
+}
 
-// The statistics of rows of Z in memory: part s of row i is columns SEG s and on.
-__global__ void __launch_bounds__(256) row_stats_kernel(const float* Z, int64_t rows, int64_t k, int64_t segs, float2* stats,
-                                                        float* target, const void* labels, bool labels64) {
+constexpr int SEG = 1024;  // of a row that a CTA reduces
+constexpr int kFewLogits = 128;  // rows whose logits are written out
+
+// Few rows' logits in memory: `parts` parts of X W to be added, [part][row][class], and the biases.
+struct FewLogits {
+  const float* z;
+  int64_t rows, k;
+  int parts;
+  const void* bias;
+};
+template <typename T>
+__device__ __forceinline__ float logit(const FewLogits& f, int64_t i, int64_t j) {
+  float z = 0.f;
+  for (int p = 0; p < f.parts; ++p) z += f.z[(p * f.rows + i) * f.k + j];
+  return f.bias ? z + to_f32(static_cast<const T*>(f.bias)[j]) : z;
+}
+
+// Their statistics: part s of row i is columns SEG s and on.
+template <typename T>
+__global__ void __launch_bounds__(256) row_stats_kernel(const FewLogits f, int64_t segs, float2* stats, float* target, const void* labels,
+                                                        bool labels64) {
   __shared__ float2 part[8];
-  const int64_t i = blockIdx.x / segs, s = blockIdx.x % segs, j0 = s * SEG, end = min(k, j0 + SEG);
+  const int64_t i = blockIdx.x / segs, s = blockIdx.x % segs, j0 = s * SEG, end = min(f.k, j0 + SEG);
   after_previous();
   float v[SEG / 256], top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int q = 0; q < SEG / 256; ++q) {
     const int64_t j = j0 + q * 256 + threadIdx.x;
-    v[q] = j < end ? Z[i * k + j] : -INFINITY;
+    v[q] = j < end ? logit<T>(f, i, j) : -INFINITY;
     top = fmaxf(top, v[q]);
   }
 #pragma unroll
@@ -93,26 +136,46 @@ __global__ void __launch_bounds__(256) row_stats_kernel(const float* Z, int64_t 
   for (int w = 0; w < 8; ++w) most = fmaxf(most, part[w].x);
   const float base = most == -INFINITY ? 0.f : most;
   for (int w = 0; w < 8; ++w) all += part[w].y * expf(part[w].x - base);
-  stats[s * rows + i] = make_float2(most, all);
-  const int64_t label = label_at(labels, labels64, i, k);
-  if (label >= j0 && label < end) target[i] = Z[i * k + label];
+  stats[s * f.rows + i] = make_float2(most, all);
+  const int64_t label = label_at(labels, labels64, i, f.k);
+  if (label >= j0 && label < end) target[i] = logit<T>(f, i, label);
 }
 
-// Z to D, in place.
-__global__ void __launch_bounds__(256) row_slope_kernel(float* Z, int64_t rows, int64_t k, const void* labels, bool labels64,
-                                                        const float* lse, const float* g, float gain) {
+// Their D and db: a thread takes a class and goes down the rows.
+template <typename T>
+__global__ void __launch_bounds__(256) row_slope_kernel(const FewLogits f, const void* labels, bool labels64, const float* lse, const float* g,
+                                                        float gain, const float* scales, T* D, int64_t ldd, T* db) {
+  struct Row {
+    float lse, g;
+    int64_t label;
+  };
+  __shared__ Row rows[kFewLogits];
   after_previous();
-  const int64_t stride = (int64_t)gridDim.x * 256;
-  for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < rows * k; x += stride) {
-    const int64_t i = x / k, j = x - i * k, label = label_at(labels, labels64, i, k);
-    float d = 0.f;
-    if (label >= 0) {
-      const float w = g ? gain * g[i] : gain;
-      d = w * expf(Z[x] - lse[i]);
-      if (j == label) d -= w;
-    }
-    Z[x] = d;
+  const float up = scales ? scales[0] : 1.f;
+  for (int i = threadIdx.x; i < f.rows; i += 256) {
+    Row r;
+    r.label = label_at(labels, labels64, i, f.k);
+    r.lse = lse[i];
+    r.g = g ? gain * g[i] : gain;
+    rows[i] = r;
   }
+  __syncthreads();
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= f.k) return;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < f.rows; ++i) {
+    const Row r = rows[i];
+    float d = 0.f;
+    if (r.label >= 0) {
+      const float w = r.g * up;
+      d = w * expf(logit<T>(f, i, j) - r.lse);
+      if (j == r.label) d -= w;
+    }
+    D[i * ldd + j] = from_f32<T>(d);
+    sum += d;
+  }
+  if (db) db[j] = from_f32<T>(scales ? sum * scales[1] : sum);
 }
 
 __global__ void __launch_bounds__(1024) scales_kernel(const float* g, int64_t m, float gain, float* scales) {
@@ -237,64 +300,133 @@ const void* bias_at(const LayerArgs& l, int64_t c) {
 
 const void* labels_at(const LossArgs& a, int64_t r) { return static_cast<const char*>(a.labels) + r * (a.labels64 ? 8 : 4); }
 
-fxtx_status_t few_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  const int64_t segs = (l.k + SEG - 1) / SEG;
-  Cut c;
-  char* ws = nullptr;
-  float *z = nullptr, *target = nullptr;
-  float2* stats = nullptr;
-  for (int pass = 0; pass < 2; ++pass) {
-    z = reinterpret_cast<float*>(c.take(l.m * l.k * 4));
-    stats = reinterpret_cast<float2*>(c.take(segs * l.m * 8));
-    target = reinterpret_cast<float*>(c.take(l.m * 4));
-    if (pass == 0) {
-      const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), c.bytes, st);
-      if (s != FXTX_OK) return s;
-      c.base = ws;
-      c.bytes = 0;
-    }
-  }
+// Whether a call's logits are written out, in fp32: float32 of few rows, on the CUDA cores, and 16-bit types of up to one
+// tile of rows, which the product kernels of few rows take (W is read once with no row of the tile wasted).
+bool few_logits(const LayerArgs& l) {
+  if (l.type == FXTX_F32) return few_rows(l.type, l.m, l.w_trans);
+  return l.m <= kFewLogits && packed_bytes(l.type, l.W, l.ldw, l.n) == 0;
+}
+
+// Few rows as an operand, in a workspace of its own where they have to be copied.
+struct FewRows {
+  Part x;
+  char* at = nullptr;
+};
+fxtx_status_t few_operand(const LayerArgs& l, FewRows* f, const DeviceInfo& dev, cudaStream_t st) {
+  const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&f->at), (size_t)(l.m * packed_bytes(l.type, l.X, l.ldx, l.n)), st);
+  if (s != FXTX_OK) return s;
+  f->x = part_of(l.type, l.X, l.ldx, 0, l.m, 0, l.n, f->at);
+  return f->x.packed ? status_of(launch_prepare(l.type, nullptr, &f->x.pack, 1, dev.sm_count, st)) : FXTX_OK;
+}
+
+PlanesProduct logits_product(const LayerArgs& l, const Part& x) {
+  const Part w = classes_of(l, 0, l.k, nullptr);
+  PlanesProduct q;
+  q.M = l.m;
+  q.N = l.k;
+  q.K = l.n;
+  q.A = as(x, false);
+  q.B = as(w, !l.w_trans);
+  return q;
+}
+
+// X W of few rows to z; its biases are left to the kernels that read it.
+fxtx_status_t run_logits(const LayerArgs& l, const Part& x, float* z, const DeviceInfo& dev, cudaStream_t st) {
+  if (l.type != FXTX_F32) return run_raw(l.type, logits_product(l, x), z, dev, st);
   Epilogue e;
-  e.bias = l.e.bias;
   e.out = z;
   e.ldo = l.k;
-  fxtx_status_t s = run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, e, dev, st);
+  return run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, e, dev, st);
+}
+
+template <typename T>
+fxtx_status_t few_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
+  FewRows x;
+  fxtx_status_t s = l.type == FXTX_F32 ? FXTX_OK : few_operand(l, &x, dev, st);
+  const int64_t segs = (l.k + SEG - 1) / SEG, parts = l.type == FXTX_F32 ? 1 : raw_parts(logits_product(l, x.x), dev);
+  const size_t z_bytes = up(parts * l.m * l.k * 4), stat_bytes = up(segs * l.m * 8);
+  char* ws = nullptr;
+  if (s == FXTX_OK) s = alloc_pooled(reinterpret_cast<void**>(&ws), z_bytes + stat_bytes + up(l.m * 4), st);
+  float *z = reinterpret_cast<float*>(ws), *target = reinterpret_cast<float*>(ws + z_bytes + stat_bytes);
+  float2* stats = reinterpret_cast<float2*>(ws + z_bytes);
+  if (s == FXTX_OK) s = run_logits(l, x.x, z, dev, st);
   if (s == FXTX_OK)
-    s = status_of(launch_kernel(row_stats_kernel, dim3((unsigned)(l.m * segs)), 256, 0, st, z, l.m, l.k, segs, stats, target, a.labels,
-                                a.labels64));
-  if (s == FXTX_OK)
-    s = status_of(launch_kernel(loss_join_kernel, dim3((unsigned)((l.m + 31) / 32)), 256, 0, st, stats, segs, l.m, target, a.labels,
-                                a.labels64, l.k, a.loss, a.lse));
-  cudaFreeAsync(ws, st);
+    s = status_of(launch_kernel(row_stats_kernel<T>, dim3((unsigned)(l.m * segs)), 256, 0, st, FewLogits{z, l.m, l.k, (int)parts, l.e.bias},
+                                segs, stats, target, a.labels, a.labels64));
+  if (s == FXTX_OK) s = status_of(launch_join(stats, segs, l.m, target, a.labels, a.labels64, l.k, a.loss, a.lse, dev, st));
+  if (ws) cudaFreeAsync(ws, st);
+  if (x.at) cudaFreeAsync(x.at, st);
   return s;
 }
 
+template <typename T>
 fxtx_status_t few_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  float* z = nullptr;
-  fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&z), (size_t)(l.m * l.k * 4), st);
-  if (s != FXTX_OK) return s;
-  Epilogue e;
-  e.bias = l.e.bias;
-  e.out = z;
-  e.ldo = l.k;
-  s = run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, e, dev, st);
-  if (s == FXTX_OK) {
-    const int64_t ctas = std::min<int64_t>((l.m * l.k + 255) / 256, (int64_t)dev.sm_count * 8);
-    s = status_of(launch_kernel(row_slope_kernel, dim3((unsigned)ctas), 256, 0, st, z, l.m, l.k, a.labels, a.labels64, a.lse_in, a.g,
-                                a.gain));
-  }
-  if (s == FXTX_OK) {
+  const bool f32 = l.type == FXTX_F32;
+  FewRows x;
+  fxtx_status_t s = f32 ? FXTX_OK : few_operand(l, &x, dev, st);
+  const int64_t parts = f32 ? 1 : raw_parts(logits_product(l, x.x), dev), pitch = (l.k + 7) / 8 * 8;
+  const size_t z_bytes = up(parts * l.m * l.k * 4), d_bytes = up(l.m * pitch * type_size(l.type));
+  char* ws = nullptr;
+  if (s == FXTX_OK) s = alloc_pooled(reinterpret_cast<void**>(&ws), z_bytes + d_bytes + 256, st);
+  float* z = reinterpret_cast<float*>(ws);
+  T* D = reinterpret_cast<T*>(ws + z_bytes);
+  float* scales = l.type == FXTX_F16 ? reinterpret_cast<float*>(ws + z_bytes + d_bytes) : nullptr;
+  if (s == FXTX_OK && scales) s = status_of(launch_scales(a.g, l.m, a.gain, scales, st));
+  if (s == FXTX_OK) s = run_logits(l, x.x, z, dev, st);
+  if (s == FXTX_OK)
+    s = status_of(launch_kernel(row_slope_kernel<T>, dim3((unsigned)((l.k + 255) / 256)), 256, 0, st,
+                                FewLogits{z, l.m, l.k, (int)parts, l.e.bias}, a.labels, a.labels64, a.lse_in, a.g, a.gain, scales, D, pitch,
+                                static_cast<T*>(a.DB)));
+  if (f32 && s == FXTX_OK && (a.DX || a.DW)) {
     GradArgs g;
-    g.G = z;
-    g.ldg = l.k;
+    g.G = D;
+    g.ldg = pitch;
     g.DX = a.DX;
     g.lddx = a.lddx;
     g.DW = a.DW;
     g.lddw = a.lddw;
-    g.DB = a.DB;
     s = run_grad(l, g, dev, st);
   }
-  cudaFreeAsync(z, st);
+  if (!f32) {
+    const Part w = classes_of(l, 0, l.k, nullptr);
+    Planes d;
+    d.p = D;
+    d.rows = l.m;
+    d.cols = l.k;
+    d.pitch = pitch;
+    d.plane_stride = l.m * pitch;
+    ModeArgs<3> m;
+    m.scales = scales;
+    if (s == FXTX_OK && a.DX) {
+      PlanesProduct t;
+      t.M = l.m;
+      t.N = l.n;
+      t.K = l.k;
+      t.A = d;
+      t.B = as(w, l.w_trans);
+      const int64_t dx_parts = raw_parts(t, dev);
+      float* sums = nullptr;
+      s = alloc_pooled(reinterpret_cast<void**>(&sums), (size_t)(dx_parts * l.m * l.n * 4), st);
+      if (s == FXTX_OK) s = run_raw(l.type, t, sums, dev, st);
+      if (s == FXTX_OK) s = join_sums(l.type, m, a.DX, a.lddx, l.m, l.n, dx_parts, sums, dev, st);
+      if (sums) cudaFreeAsync(sums, st);
+    }
+    if (s == FXTX_OK && a.DW) {
+      Planes dm = d, xm = as(x.x, true);
+      dm.mn_major = true;
+      PlanesProduct t;
+      t.M = l.w_trans ? l.k : l.n;
+      t.N = l.w_trans ? l.n : l.k;
+      t.K = l.m;
+      t.A = l.w_trans ? dm : xm;
+      t.B = l.w_trans ? xm : dm;
+      t.e.out = a.DW;
+      t.e.ldo = a.lddw;
+      s = run_sum(l.type, t, m, dev, st);
+    }
+  }
+  if (ws) cudaFreeAsync(ws, st);
+  if (x.at) cudaFreeAsync(x.at, st);
   return s;
 }
 
@@ -305,7 +437,11 @@ cudaError_t launch_scales(const float* g, int64_t m, float gain, float* scales, 
 }
 
 fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (few_rows(l.type, l.m, l.w_trans)) return few_loss(l, a, dev, st);
+  if (few_logits(l)) switch (l.type) {
+      case FXTX_F32: return few_loss<float>(l, a, dev, st);
+      case FXTX_BF16: return few_loss<__nv_bfloat16>(l, a, dev, st);
+      default: return few_loss<__half>(l, a, dev, st);
+    }
   // W's classes go in pieces where they have to be packed, X's rows also where the parts' statistics would take more
   const int64_t w_row = packed_bytes(l.type, l.W, l.ldw, l.n), x_row = packed_bytes(l.type, l.X, l.ldx, l.n);
   const int64_t Vp = piece_of(l.k, w_row ? floor256(kSmallCap / w_row) : l.k), pieces = (l.k + Vp - 1) / Vp;
@@ -362,15 +498,19 @@ fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& 
       parts += stat_parts(l.type, q, dev);
     }
     if (s == FXTX_OK)
-      s = status_of(launch_kernel(loss_join_kernel, dim3((unsigned)((rows + 31) / 32)), 256, 0, st, stats, parts, rows, target,
-                                  labels_at(a, r), a.labels64, l.k, a.loss ? a.loss + r : nullptr, a.lse ? a.lse + r : nullptr));
+      s = status_of(launch_join(stats, parts, rows, target, labels_at(a, r), a.labels64, l.k, a.loss ? a.loss + r : nullptr,
+                                a.lse ? a.lse + r : nullptr, dev, st));
   }
   cudaFreeAsync(ws, st);
   return s;
 }
 
 fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (few_rows(l.type, l.m, l.w_trans)) return few_grad(l, a, dev, st);
+  if (few_logits(l)) switch (l.type) {
+      case FXTX_F32: return few_grad<float>(l, a, dev, st);
+      case FXTX_BF16: return few_grad<__nv_bfloat16>(l, a, dev, st);
+      default: return few_grad<__half>(l, a, dev, st);
+    }
   const bool f32 = l.type == FXTX_F32;
   const int size = type_size(l.type), d_size = f32 ? 6 : 2;
   const int64_t w_row = packed_bytes(l.type, l.W, l.ldw, l.n), x_row = packed_bytes(l.type, l.X, l.ldx, l.n);

@@ -54,6 +54,13 @@ fxtx_status_t run_stats(fxtx_type_t type, const PlanesProduct& p, const ModeArgs
 fxtx_status_t run_slope(fxtx_type_t type, const PlanesProduct& p, const ModeArgs<2>& x, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_sum(fxtx_type_t type, const PlanesProduct& p, const ModeArgs<3>& x, const DeviceInfo& dev, cudaStream_t st);
 int64_t stat_parts(fxtx_type_t type, const PlanesProduct& p, const DeviceInfo& dev);
+// C in fp32, of 16-bit types: `raw_parts` parts of it, [part][row][column].
+fxtx_status_t run_raw(fxtx_type_t type, const PlanesProduct& p, float* out, const DeviceInfo& dev, cudaStream_t st);
+int64_t raw_parts(const PlanesProduct& p, const DeviceInfo& dev);
+// out = mode 3's result from such parts.
+fxtx_status_t join_sums(fxtx_type_t type, const ModeArgs<3>& x, void* out, int64_t ldo, int64_t rows, int64_t cols, int64_t parts,
+                        const float* part, const DeviceInfo& dev, cudaStream_t st);
+int take_raw_device_error();
 int take_stats_device_error();
 int take_slope_device_error();
 int take_sum_device_error();

@@ -39,6 +39,13 @@ __global__ void __launch_bounds__(256) sum_join_kernel(const __grid_constant__ M
 }
 
 template <typename T>
+cudaError_t join(const ModeArgs<3>& x, void* out, int64_t ldo, int64_t rows, int64_t cols, int64_t parts, const float* part,
+                 const DeviceInfo& dev, cudaStream_t st) {
+  const int64_t blocks = std::min<int64_t>((rows * ((cols + 3) / 4) + 255) / 256, (int64_t)dev.sm_count * 8);
+  return launch_kernel(sum_join_kernel<T>, dim3((unsigned)blocks), 256, 0, st, x, out, ldo, rows, cols, (int)parts, part);
+}
+
+template <typename T>
 fxtx_status_t run_t(const PlanesProduct& p, const ModeArgs<3>& x, const DeviceInfo& dev, cudaStream_t st) {
   const TcPlan plan =
       plan_persistent(p.M, p.N, p.K, std::is_same<T, float>::value ? 3 : 1, p.A.mn_major, p.B.mn_major, dev.sm_count, INT64_MAX);
@@ -52,11 +59,7 @@ fxtx_status_t run_t(const PlanesProduct& p, const ModeArgs<3>& x, const DeviceIn
   }
   cudaError_t e = launch_persistent<T, 3>(plan, am, bm, a, x, dev.sm_count, st);
   if (a.part) {
-    if (e == cudaSuccess) {
-      const int64_t blocks = std::min<int64_t>((p.M * ((p.N + 3) / 4) + 255) / 256, (int64_t)dev.sm_count * 8);
-      e = launch_kernel(sum_join_kernel<T>, dim3((unsigned)blocks), 256, 0, st, x, p.e.out, p.e.ldo, p.M, p.N, a.splits,
-                        (const float*)a.part);
-    }
+    if (e == cudaSuccess) e = join<T>(x, p.e.out, p.e.ldo, p.M, p.N, a.splits, a.part, dev, st);
     cudaFreeAsync(a.part, st);
   }
   if (e == cudaSuccess) return FXTX_OK;
@@ -67,6 +70,19 @@ fxtx_status_t run_t(const PlanesProduct& p, const ModeArgs<3>& x, const DeviceIn
 }  // namespace
 
 int take_sum_device_error() { return take_device_error(); }
+
+fxtx_status_t join_sums(fxtx_type_t type, const ModeArgs<3>& x, void* out, int64_t ldo, int64_t rows, int64_t cols, int64_t parts,
+                        const float* part, const DeviceInfo& dev, cudaStream_t st) {
+  cudaError_t e;
+  switch (type) {
+    case FXTX_F32: e = join<float>(x, out, ldo, rows, cols, parts, part, dev, st); break;
+    case FXTX_BF16: e = join<__nv_bfloat16>(x, out, ldo, rows, cols, parts, part, dev, st); break;
+    default: e = join<__half>(x, out, ldo, rows, cols, parts, part, dev, st); break;
+  }
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
 
 fxtx_status_t run_sum(fxtx_type_t type, const PlanesProduct& p, const ModeArgs<3>& x, const DeviceInfo& dev, cudaStream_t st) {
   switch (type) {

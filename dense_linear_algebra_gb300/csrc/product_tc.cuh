@@ -6,6 +6,7 @@
 //   2  the gradient of softmax cross entropy at C + bias: g_i (exp(C + bias_j - lse_i) - [j = label_i]), stored as an operand
 //      of the products that follow, and its column sums
 //   3  sums over pieces: out = scale (C + what earlier pieces left), or C + that kept in fp32 for the next piece
+//   4  C in fp32 (in any mode, the parts of split sums are stored so)
 // Each file that includes this has kernels of its own (internal linkage).
 #pragma once
 
@@ -109,7 +110,7 @@ struct TcArgs {
   bool a_mn = false, b_mn = false;
   uint32_t idesc = 0;
   Epilogue e;
-  float* part = nullptr;  // [splits][rows][cols] when splits > 1
+  float* part = nullptr;  // [splits][rows][cols] where the sums are split, or wanted as they are
 };
 
 // Tile `t`'s place: 8 tiles along the lanes at a time, then along the columns, so that the
@@ -160,6 +161,26 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, 
   if (steps > Q / 2) mma_steps<CG, C, PL, Q>(d, ad, bd, a, fresh);
   else if (steps > Q / 4) mma_steps<CG, C, PL, Q / 2>(d, ad, bd, a, fresh);
   else mma_steps<CG, C, PL, Q / 4>(d, ad, bd, a, fresh);
+}
+
+// The sums over a warp's lanes of N (16 or 32) values of each, column y's to p[y] for y < left: each step, a lane gives half of
+// its columns away, until one is left.
+template <int N>
+__device__ __forceinline__ void column_sums(const float* v, float* p, int64_t left, bool store) {
+  const int lane = threadIdx.x & 31;
+  float s[N];
+#pragma unroll
+  for (int y = 0; y < N; ++y) s[y] = v[y];
+#pragma unroll
+  for (int o = N / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int y = 0; y < o; ++y) {
+      const bool upper = lane & o;
+      const float give = upper ? s[y] : s[y + o];
+      s[y] = (upper ? s[y + o] : s[y]) + shfl_xor(give, o);
+    }
+  if constexpr (N == 16) s[0] += shfl_xor(s[0], 16);
+  if (store && lane < N && lane < left) p[lane] = s[0];
 }
 
 // The two accumulators as the products take them and the epilogue gives them back: in turn, or (HOME) the first piece of a
@@ -338,7 +359,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
       range(w, k0, k1);
       const int64_t i0 = (int64_t)l * 128 * CG + rank * 128 + 32 * q;  // the warp's first row of the result
       const int64_t j0 = (int64_t)c * BN + group * C::COLS;            // and its first column
-      float* part = a.splits > 1 ? a.part + (int64_t)(w % a.splits) * a.rows * a.cols : nullptr;
+      float* part = a.part ? a.part + (int64_t)(w % a.splits) * a.rows * a.cols : nullptr;
       // the tile's biases, read while its products run (the buffers alternate, and all epilogue warps
       // meet here once a tile)
       float* bias = s_bias[turn & 1];
@@ -480,9 +501,10 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           for (int y = 0; y < 16; ++y) s4[y & 3] += exp_of<T>(v[y] - from);
           sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
           if (at >= x && at < x + 16) {
+            float z = 0.f;  // (an index into v would put it into local memory)
 #pragma unroll
-            for (int y = 0; y < 16; ++y)
-              if (at - x == y) mode.target[i] = v[y];
+            for (int y = 0; y < 16; ++y) z = at - x == y ? v[y] : z;
+            mode.target[i] = z;
           }
         }
         if (i < a.rows) mode.stats[((int64_t)c * (BN / C::COLS) + group) * a.rows + i] = make_float2(top, sum);
@@ -498,48 +520,54 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
         if (on && mode.g) g *= mode.g[i];
         if (mode.scales) g *= mode.scales[0];
         const bool wide = Finish<S>::wide(mode.D, mode.ldd) && mode.d_planes % 8 == 0;
+        if constexpr (PL == 1) {
 #pragma unroll 1
-        for (int x = 0; x < C::COLS; x += 32) {
-          if (j0 + x >= a.cols) break;  // (the whole warp's)
-          float v[32];
+          for (int x = 0; x < C::COLS; x += 32) {
+            if (j0 + x >= a.cols) break;  // (the whole warp's)
+#pragma unroll 1
+            for (int y = 0; y < 32; y += 16) {
+              float v[16];
+              get(x + y, v);
 #pragma unroll
-          for (int y = 0; y < 32; y += 16) get(x + y, v + y);
+              for (int q = 0; q < 16; ++q) v[q] = on ? g * exp_of<T>(v[q] - lse) : 0.f;
+              if (__any_sync(FULL_MASK, at >= x + y && at < x + y + 16)) {
 #pragma unroll
-          for (int y = 0; y < 32; ++y) v[y] = on ? g * exp_of<T>(v[y] - lse) : 0.f;
-          if (at >= x && at < x + 32) {
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (at - x == y) v[y] -= g;
-          }
-          if (mode.sums) {
-            // lane l comes to hold column l's sum: each step, a lane gives half of its columns away
-            float s[32];
-#pragma unroll
-            for (int y = 0; y < 32; ++y) s[y] = v[y];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-              for (int y = 0; y < o; ++y) {
-                const bool upper = lane & o;
-                const float give = upper ? s[y] : s[y + o];
-                s[y] = (upper ? s[y + o] : s[y]) + shfl_xor(give, o);
+                for (int q = 0; q < 16; ++q) v[q] -= at - x - y == q ? g : 0.f;
               }
-            if (j0 + x + lane < a.cols && i0 < a.rows) mode.sums[i0 / 32 * mode.sums_ld + j0 + x + lane] = s[0];
+              Out::put(buf, y, v);
+              if (mode.sums) column_sums<16>(v, mode.sums + i0 / 32 * mode.sums_ld + j0 + x + y, a.cols - j0 - x - y, i0 < a.rows);
+            }
+            __syncwarp();
+            Out::drain(buf, static_cast<S*>(mode.D), mode.ldd, wide, i0, a.rows, j0 + x, a.cols);
+            __syncwarp();
           }
+        } else {
+#pragma unroll 1
+          for (int x = 0; x < C::COLS; x += 32) {
+            if (j0 + x >= a.cols) break;
+            float v[32];
 #pragma unroll
-          for (int p = 0; p < PL; ++p) {
+            for (int y = 0; y < 32; y += 16) get(x + y, v + y);
 #pragma unroll
-            for (int y = 0; y < 32; y += 16) Out::put(buf, y, v + y);
-            __syncwarp();
-            Out::drain(buf, static_cast<S*>(mode.D) + p * mode.d_planes, mode.ldd, wide, i0, a.rows, j0 + x, a.cols);
-            __syncwarp();
-            if (PL == 3) {
+            for (int y = 0; y < 32; ++y) v[y] = on ? g * exp_of<T>(v[y] - lse) : 0.f;
+            if (__any_sync(FULL_MASK, at >= x && at < x + 32)) {
+#pragma unroll
+              for (int y = 0; y < 32; ++y) v[y] -= at - x == y ? g : 0.f;
+            }
+            if (mode.sums) column_sums<32>(v, mode.sums + i0 / 32 * mode.sums_ld + j0 + x, a.cols - j0 - x, i0 < a.rows);
+#pragma unroll
+            for (int p = 0; p < PL; ++p) {
+#pragma unroll
+              for (int y = 0; y < 32; y += 16) Out::put(buf, y, v + y);
+              __syncwarp();
+              Out::drain(buf, static_cast<S*>(mode.D) + p * mode.d_planes, mode.ldd, wide, i0, a.rows, j0 + x, a.cols);
+              __syncwarp();
 #pragma unroll
               for (int y = 0; y < 32; ++y) v[y] -= to_f32(from_f32<S>(v[y]));  // exact
             }
           }
         }
-      } else {
+      } else if constexpr (MODE == 3) {
         const float down = mode.scales ? mode.scales[1] : 1.f;
         const bool wide_in = Finish<float>::wide(mode.in, a.cols), wide_keep = Finish<float>::wide(mode.keep, a.cols);
 #pragma unroll 1
