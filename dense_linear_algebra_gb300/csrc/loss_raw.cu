@@ -14,7 +14,7 @@ fxtx_status_t run_t(const PlanesProduct& p, float* out, const DeviceInfo& dev, c
   const TcPlan plan = plan_of(p, dev);
   TcArgs a;
   CUtensorMap am, bm;
-  const fxtx_status_t s = prepare_product<T>(p, plan, a, am, bm);
+  const fxtx_status_t s = prepare_product<T>(p, plan, a, am, bm, LOGIT_FOLD);
   if (s != FXTX_OK) return s;
   a.part = out;
   const cudaError_t e = plan.cluster ? launch_cluster<T, true>(plan, am, bm, a, st)

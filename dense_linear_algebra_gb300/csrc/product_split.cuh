@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
   } else if (warp == 1) {
     if (elect_one()) {
       bool more = true;
-      ok = issue_products<1, C, PL, LONG>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
+      ok = issue_products<1, C, PL, LONG, PL == 3>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
         f0 = k0;
         f1 = k1;
         const bool m = more;

@@ -33,6 +33,7 @@ namespace {
 constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
 constexpr int CHUNK = 2;          // stages a sum stays in tensor memory (float32)
 constexpr int FOLD = 8192;        // of kk that a piece of a sum covers (16 bits)
+constexpr int LOGIT_FOLD = 1024;  // of sums that are not rounded to 16 bits
 
 // BK: kk a stage; KB: kilobytes the stages may take.
 template <int CG, int BN, int PL, int BK_, int KB>
@@ -63,10 +64,11 @@ struct TileCfg : Cfg<CG, BN, PL, PL == 3 ? 64 : 128, 192> {
   static_assert(BYTES + 2 * BN * 4 + 512 <= 227 * 1024, "shared memory");
 };
 
-// A warp's 32 lanes of COLS tensor-memory columns added to `sum`, 32 on their way at a time.
+// A warp's 32 lanes of COLS tensor-memory columns added to `sum`, 32 on their way at a time (16 where the sums themselves fill
+// the registers).
 template <int COLS>
 __device__ __forceinline__ void add_columns(uint32_t t, float* sum) {
-  constexpr int STEP = COLS < 32 ? COLS : 32;
+  constexpr int STEP = COLS < 32 ? COLS : COLS > 64 ? 16 : 32;
 #pragma unroll
   for (int x = 0; x < COLS; x += STEP) {
     float r[STEP];
@@ -163,6 +165,12 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t ad, uint64_t bd, 
   else mma_steps<CG, C, PL, Q / 4>(d, ad, bd, a, fresh);
 }
 
+// z = v where `is` holds. (A chain of selections by an index is compiled into an array in local memory: D's epilogue took twice
+// its time with one.)
+__device__ __forceinline__ void take_if(float& z, float v, bool is) {
+  asm("{\n.reg .pred p;\nsetp.ne.b32 p, %2, 0;\n@p mov.f32 %0, %1;\n}" : "+f"(z) : "f"(v), "r"((int)is));
+}
+
 // The sums over a warp's lanes of N (16 or 32) values of each, column y's to p[y] for y < left: each step, a lane gives half of
 // its columns away, until one is left.
 template <int N>
@@ -205,7 +213,7 @@ struct Turns {
 
 // The loop of a CTA's products over a ring of stages: one lane's. `tile(k0, k1)` gives the next range of
 // stages of kk, false after the last.
-template <int CG, class C, int PL, bool LONG, typename F>
+template <int CG, class C, int PL, bool LONG, bool REGS, typename F>
 __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* smem, uint64_t* full, uint64_t* empty,
                                                uint64_t* tfull, uint64_t* tempty, uint32_t tmem, int bn,
                                                volatile int* abort_word, F tile) {
@@ -233,7 +241,7 @@ __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* s
       mma_commit<CG>(&empty[s]);
       if (--left == 0) {
         mma_commit<CG>(&tfull[acc.s]);
-        acc.next(PL == 3 || kb + 1 == k1);
+        acc.next(REGS || kb + 1 == k1);
       }
     }
   }
@@ -245,6 +253,8 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
     product_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                       const __grid_constant__ TcArgs a, const __grid_constant__ ModeArgs<MODE> mode) {
   using C = TileCfg<CG, BN, PL>;
+  // the pieces of a sum are added up in registers, each freeing its accumulator: float32, and logits, whose pieces are short
+  constexpr bool REGS = PL == 3 || (MODE == 1 && LONG);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
@@ -319,7 +329,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
       int w = first;
-      issue_products<CG, C, PL, LONG>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
+      issue_products<CG, C, PL, LONG, REGS>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
         if (w >= work) return false;
         range(w, k0, k1);
         w += step;
@@ -380,7 +390,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           if (!wait_full()) break;
           release(acc.s);
           kb += PL == 3 ? CHUNK : LONG ? a.fold : k1 - k0;
-          acc.next(PL == 3 || kb >= k1);
+          acc.next(REGS || kb >= k1);
         }
         continue;
       }
@@ -393,7 +403,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
 
       uint32_t held = acc.s;  // the accumulator with the whole sum
       uint32_t t = lane_base + held * BN;
-      if constexpr (PL == 1) {
+      if constexpr (!REGS) {
         if (!wait_full()) continue;
         acc.next(!LONG || k0 + a.fold >= k1);
         if constexpr (LONG) {
@@ -409,7 +419,8 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
         float sum[C::COLS];
 #pragma unroll
         for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
-        for (int kb = k0; kb < k1; kb += CHUNK) {
+        const int piece = PL == 3 ? CHUNK : a.fold;
+        for (int kb = k0; kb < k1; kb += piece) {
           if (kb > k0) release(held);
           held = acc.s;
           t = lane_base + held * BN;
@@ -500,11 +511,11 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
 #pragma unroll
           for (int y = 0; y < 16; ++y) s4[y & 3] += exp_of<T>(v[y] - from);
           sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
-          if (at >= x && at < x + 16) {
-            float z = 0.f;  // (an index into v would put it into local memory)
+          if (__any_sync(FULL_MASK, at >= x && at < x + 16)) {
+            float z = 0.f;
 #pragma unroll
-            for (int y = 0; y < 16; ++y) z = at - x == y ? v[y] : z;
-            mode.target[i] = z;
+            for (int y = 0; y < 16; ++y) take_if(z, v[y], at - x == y);
+            if (at >= x && at < x + 16) mode.target[i] = z;
           }
         }
         if (i < a.rows) mode.stats[((int64_t)c * (BN / C::COLS) + group) * a.rows + i] = make_float2(top, sum);
@@ -662,7 +673,8 @@ int stage_of(const TcPlan& plan, int planes) { return planes == 1 && !plan.clust
 
 // A product's arguments and its operands' maps.
 template <typename T>
-fxtx_status_t prepare_product(const PlanesProduct& p, const TcPlan& plan, TcArgs& a, CUtensorMap& am, CUtensorMap& bm) {
+fxtx_status_t prepare_product(const PlanesProduct& p, const TcPlan& plan, TcArgs& a, CUtensorMap& am, CUtensorMap& bm,
+                              int fold = FOLD) {
   constexpr int PL = std::is_same<T, float>::value ? 3 : 1;
   const bool bf16 = !std::is_same<T, __half>::value;
   if (log_enabled())
@@ -680,7 +692,7 @@ fxtx_status_t prepare_product(const PlanesProduct& p, const TcPlan& plan, TcArgs
   a.ksteps = (int)((p.K + 15) / 16);
   a.per_split = (a.kblocks + plan.splits - 1) / plan.splits;
   a.splits = (a.kblocks + a.per_split - 1) / a.per_split;  // none of them empty
-  if (PL == 1 && (int64_t)a.per_split * bk > FOLD) a.fold = FOLD / bk;
+  if (PL == 1 && (int64_t)a.per_split * bk > fold) a.fold = fold / bk;
   // a cluster's CTAs share the tile's 128 lanes out evenly, and each has work
   if (plan.cluster && (a.splits != plan.splits || 128 % a.splits != 0 || a.splits > 8)) return FXTX_ERR_UNSUPPORTED;
   a.a_mn = A.mn_major;
@@ -720,7 +732,7 @@ fxtx_status_t run_mode(const PlanesProduct& p, const ModeArgs<MODE>& mode, const
   const TcPlan plan = plan_persistent(p.M, p.N, p.K, std::is_same<T, float>::value ? 3 : 1, p.A.mn_major, p.B.mn_major, dev.sm_count, 1);
   TcArgs a;
   CUtensorMap am, bm;
-  const fxtx_status_t s = prepare_product<T>(p, plan, a, am, bm);
+  const fxtx_status_t s = prepare_product<T>(p, plan, a, am, bm, MODE == 1 ? LOGIT_FOLD : FOLD);
   if (s != FXTX_OK) return s;
   if (launch_persistent<T, MODE>(plan, am, bm, a, mode, dev.sm_count, st) == cudaSuccess) return FXTX_OK;
   cudaGetLastError();
