@@ -9,12 +9,11 @@
 // a third scatters, a warp ranking its 32 ids at a time by matching digits; up to 8,192 ids take one CTA and one
 // launch, in shared memory.
 //
-// The sorted positions are then cut into chunks. A worker (as many threads as a row has accesses of 16 bytes, up to
-// 256) adds a chunk's rows of G run by run. A run that begins and ends in the chunk is a row of dE; one that goes over
-// the chunk's ends becomes a partial sum in fp32, two a chunk at most, and the partial sums, sorted as they are, go
-// through the same kernel until one chunk holds them all. So a frequent id's thousands of rows are shared out evenly.
-// The rows of dE without an id are zeroed by further CTAs of the first of these launches, which look each row up
-// among the sorted ids.
+// The sorted positions are then cut into chunks of 32. A worker (as many threads as a row has accesses of 16 bytes, up to
+// 256) adds a chunk's rows of G run by run. A run that begins and ends in the chunk is a row of dE; of one that goes over
+// the chunk's ends the chunk's part is written out in fp32, two a chunk at most, and a second kernel adds each such run's
+// parts, so that a frequent id's thousands of rows are shared out evenly. The rows of dE without an id are zeroed by further
+// CTAs of the first of these launches, which look their rows up among the sorted ids.
 #include <algorithm>
 
 #include "common.cuh"
@@ -27,11 +26,12 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int MAX_BITS = 9, RADIX = 1 << MAX_BITS;
-constexpr int ITEMS = 8, TILE = THREADS * ITEMS;        // ids a CTA of the sort takes
-constexpr int SMALL_THREADS = 1024, SMALL = SMALL_THREADS * ITEMS;
+constexpr int ITEMS = 4, TILE = THREADS * ITEMS;         // ids a thread and a CTA of the sort take
+constexpr int SMALL_ITEMS = 8, SMALL_THREADS = 1024, SMALL = SMALL_THREADS * SMALL_ITEMS;
 constexpr int BATCH = 8;                                 // rows on their way at a time
+constexpr int CHUNK = 32;                                // sorted ids a worker adds
 
-constexpr uint32_t NONE = 0xffffffffu, EMPTY = 0x80000000u;  // a partial sum's key: no run; a run's, with nothing to add
+constexpr uint32_t NONE = 0xffffffffu;  // the key of no id
 
 // V neighbouring entries (of 16 bytes, or one; of float: V of them) from p on.
 template <typename S, int V>
@@ -125,6 +125,7 @@ __device__ __forceinline__ uint2 item(const SortArgs& a, int64_t i) {
 __device__ __forceinline__ uint32_t digit_of(uint32_t key, int shift, int bits) { return (key >> shift) & ((1u << bits) - 1u); }
 
 // The warp's items (32 at a time, in order) ranked among its own of the same digit; `hist` counts them.
+template <int ITEMS>
 __device__ __forceinline__ void rank_items(const uint2* x, int items, uint32_t* hist, int shift, int bits, uint32_t* rank) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -215,15 +216,17 @@ __global__ void __launch_bounds__(THREADS) sort_scatter_kernel(const __grid_cons
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) x[i] = item(a, base + 32 * i);
   __syncthreads();
-  rank_items(x, ITEMS, hist[warp], a.shift, a.bits, rank);
+  rank_items<ITEMS>(x, ITEMS, hist[warp], a.shift, a.bits, rank);
   scan(first, digits, warps);
   // where each warp's ids of a digit begin
   for (int d = tid; d < digits; d += THREADS) {
-    uint32_t at = first[d] + a.counts[d * a.ctas + blockIdx.x];
+    uint32_t at = first[d] + a.counts[d * a.ctas + blockIdx.x], y[WARPS];
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) y[w] = hist[w][d];
+#pragma unroll
     for (int w = 0; w < WARPS; ++w) {
-      const uint32_t y = hist[w][d];
       hist[w][d] = at;
-      at += y;
+      at += y[w];
     }
   }
   __syncthreads();
@@ -240,37 +243,42 @@ __global__ void __launch_bounds__(SMALL_THREADS) sort_small_kernel(const __grid_
   uint2* held = reinterpret_cast<uint2*>(hist + warps_n * RADIX);
   const int items = ((int)a.m + (int)blockDim.x - 1) / (int)blockDim.x, digits = 1 << a.bits;
   const int base = warp * 32 * items + lane;
-  uint2 x[ITEMS];
-  uint32_t rank[ITEMS];
+  uint2 x[SMALL_ITEMS];
+  uint32_t rank[SMALL_ITEMS];
   after_previous();
   for (int p = 0; p < passes; ++p) {
     const int shift = p * a.bits;
-    for (int d = tid; d < warps_n * RADIX; d += (int)blockDim.x) hist[d] = 0;
+    for (int d = tid; d < warps_n * digits; d += (int)blockDim.x) hist[d] = 0;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
+    for (int i = 0; i < SMALL_ITEMS; ++i) {
       if (i >= items) break;
       const int at = base + 32 * i;
       x[i] = p == 0 ? item(a, at) : at < a.m ? held[at] : make_uint2(NONE, 0);
     }
     __syncthreads();
-    rank_items(x, items, hist + warp * RADIX, shift, a.bits, rank);
+    rank_items<SMALL_ITEMS>(x, items, hist + warp * digits, shift, a.bits, rank);
     __syncthreads();
     for (int d = tid; d < digits; d += (int)blockDim.x) {
       uint32_t at = 0;
-      for (int w = 0; w < warps_n; ++w) {
-        const uint32_t y = hist[w * RADIX + d];
-        hist[w * RADIX + d] = at;
-        at += y;
+      for (int w = 0; w < warps_n; w += 8) {  // (eight reads on their way at a time)
+        uint32_t y[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[q] = w + q < warps_n ? hist[(w + q) * digits + d] : 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (w + q < warps_n) hist[(w + q) * digits + d] = at;
+          at += y[q];
+        }
       }
       first[d] = at;
     }
     __syncthreads();
     scan(first, digits, warps);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
+    for (int i = 0; i < SMALL_ITEMS; ++i) {
       if (i >= items) break;
       if (x[i].x == NONE) continue;
-      const uint32_t d = digit_of(x[i].x, shift, a.bits), at = first[d] + hist[warp * RADIX + d] + rank[i];
+      const uint32_t d = digit_of(x[i].x, shift, a.bits), at = first[d] + hist[warp * digits + d] + rank[i];
       if (p + 1 < passes) held[at] = x[i];
       else a.to[at] = x[i];
     }
@@ -280,21 +288,33 @@ __global__ void __launch_bounds__(SMALL_THREADS) sort_small_kernel(const __grid_
 
 // ------------------------------------------------------------------------------------------------ the sums
 struct ReduceArgs {
-  int64_t entries, n, count;
-  int chunk;              // entries a worker adds
-  const uint2* sorted;    // (id, row of src); NULL: partial sums, with their keys
-  const uint32_t* keys;
-  const void* src;
-  int64_t lds;
+  int64_t m, n, count;
+  const uint2* sorted;  // (id, row of G)
+  const void* G;
+  int64_t ldg;
   float scale;
   void* out;
   int64_t ldo;
-  float* part;            // [2 a chunk][n], and their keys; NULL where one chunk holds all
-  uint32_t* part_keys;
+  float* part;          // [2 a chunk][n]: what a chunk has of a run that began before it, and of one that it begins
   Shape shape;
-  int64_t sum_ctas;       // CTAs of sums; those beyond them zero `zero_rows` rows each
+  int64_t sum_ctas, ctas;  // CTAs of sums, spread among all; the others zero `zero_rows` rows each
   int zero_rows;
 };
+
+// How many of 0 .. n - 1 the predicate holds for, where it holds for the first ones and no others: a warp tries 32 at a time.
+template <typename F>
+__device__ __forceinline__ int64_t warp_bound(int64_t n, F holds) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0;
+  while (n > 0) {
+    const int64_t step = (n + 31) / 32, i = min(lo + n, lo + (lane + 1) * step) - 1;
+    const int yes = __popc(__ballot_sync(FULL_MASK, holds(i)));
+    if (yes == 32) return lo + n;
+    lo += yes * step;
+    n = min(n - yes * step, step) - 1;  // (the first that fails is known)
+  }
+  return lo;
+}
 
 // Rows of dE without an id.
 template <typename T, int V>
@@ -303,14 +323,16 @@ __device__ __forceinline__ void zero_rows(const ReduceArgs& a, int64_t row0) {
   if (threadIdx.x < 32) {
     const int64_t v = row0 + threadIdx.x;
     const bool mine = (int)threadIdx.x < a.zero_rows && v < a.count;
-    // the first entry not below v
-    int64_t lo = 0, hi = mine ? a.entries : 0;
+    // the entries of these rows, and in them the first one not below the lane's row
+    int64_t lo = warp_bound(a.m, [&](int64_t i) { return a.sorted[i].x < (uint32_t)row0; });
+    int64_t hi = lo + warp_bound(a.m - lo, [&](int64_t i) { return a.sorted[lo + i].x < (uint32_t)(row0 + a.zero_rows); });
+    const int64_t end = hi;
     while (lo < hi) {
       const int64_t mid = (lo + hi) >> 1;
       if (a.sorted[mid].x < (uint32_t)v) lo = mid + 1;
       else hi = mid;
     }
-    const bool there = mine && lo < a.entries && a.sorted[lo].x == (uint32_t)v;
+    const bool there = mine && lo < end && a.sorted[lo].x == (uint32_t)v;
     const uint32_t absent = __ballot_sync(FULL_MASK, mine && !there);
     if (threadIdx.x == 0) s_absent = absent;
   }
@@ -324,86 +346,126 @@ __device__ __forceinline__ void zero_rows(const ReduceArgs& a, int64_t row0) {
   }
 }
 
-template <typename S, typename T, int V>
+// WARPS: a worker is whole warps.
+template <typename T, int V, bool WARPS>
 __global__ void __launch_bounds__(THREADS) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
   after_previous();
-  if (blockIdx.x >= a.sum_ctas) {
-    zero_rows<T, V>(a, ((int64_t)blockIdx.x - a.sum_ctas) * a.zero_rows);
+  // the sums' CTAs lie among the others, so that reading and writing go on together
+  const int64_t b = blockIdx.x, before = b * a.sum_ctas / a.ctas;
+  if ((b + 1) * a.sum_ctas / a.ctas == before) {
+    zero_rows<T, V>(a, (b - before) * a.zero_rows);
     return;
   }
   const Shape& s = a.shape;
   const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
-  const int64_t w = (int64_t)blockIdx.x * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t;
-  const int64_t e0 = chunk * a.chunk, e1 = min(a.entries, e0 + a.chunk);
-  if (group >= s.groups || e0 >= a.entries) return;
-  const bool mine = c < a.n / V, first_thread = c == 0;
-  auto key_at = [&](int64_t e) -> uint32_t { return a.sorted ? a.sorted[e].x : a.keys[e]; };
-  auto run_of = [](uint32_t key) { return key == NONE ? NONE : key & ~EMPTY; };
-  if (first_thread && a.part) a.part_keys[2 * chunk] = a.part_keys[2 * chunk + 1] = NONE;
+  const int64_t w = before * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t;
+  const int64_t e0 = chunk * CHUNK, e1 = min(a.m, e0 + CHUNK);
+  if (group >= s.groups || e0 >= a.m) return;
+  const bool mine = c < a.n / V;
+  uint2 own = make_uint2(NONE, 0);  // a lane's entry of the chunk
+  if (WARPS && e0 + (threadIdx.x & 31) < e1) own = a.sorted[e0 + (threadIdx.x & 31)];
+  auto entry = [&](int64_t e) {
+    if constexpr (WARPS) {
+      const int i = (int)(e - e0);
+      return make_uint2(__shfl_sync(FULL_MASK, own.x, i), __shfl_sync(FULL_MASK, own.y, i));
+    } else {
+      return e < e1 ? a.sorted[e] : make_uint2(NONE, 0);
+    }
+  };
+  const uint32_t left = e0 > 0 ? a.sorted[e0 - 1].x : NONE, right = e1 < a.m ? a.sorted[e1].x : NONE;
 
   float acc[V] = {};
-  uint32_t run = run_of(key_at(e0));
-  bool from_left = e0 > 0 && run_of(key_at(e0 - 1)) == run;
+  uint32_t run = entry(e0).x;
+  bool from_left = left == run;
   // the run in hand ends, in this chunk or beyond it
   auto flush = [&](bool to_right) {
-    if (run < a.count) {
+    if (run < a.count && mine) {
       if (!from_left && !to_right) {
-        if (mine) {
-          Piece<T, V> o;
+        Piece<T, V> o;
 #pragma unroll
-          for (int q = 0; q < V; ++q) o.set(q, acc[q] * a.scale);
-          o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
-        }
+        for (int q = 0; q < V; ++q) o.set(q, acc[q] * a.scale);
+        o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
       } else {
-        const int64_t slot = 2 * chunk + (from_left ? 0 : 1);
-        if (first_thread) {
-          a.part_keys[slot] = run;
-          if (from_left && to_right) a.part_keys[slot + 1] = run | EMPTY;  // a run's partial sums are neighbours
-        }
-        if (mine) {
-          Piece<float, V> o;
+        Piece<float, V> o;
 #pragma unroll
-          for (int q = 0; q < V; ++q) o.set(q, acc[q]);
-          o.store(a.part + slot * a.n + c * V);
-        }
+        for (int q = 0; q < V; ++q) o.set(q, acc[q]);
+        o.store(a.part + (2 * chunk + (from_left ? 0 : 1)) * a.n + c * V);
       }
     }
 #pragma unroll
     for (int q = 0; q < V; ++q) acc[q] = 0.f;
     from_left = false;
   };
-  for (int64_t e = e0; e < e1; e += BATCH) {
+#pragma unroll 1
+  for (int64_t e = e0; e < e0 + CHUNK; e += BATCH) {
     uint32_t key[BATCH];
-    Piece<S, V> x[BATCH];
+    Piece<T, V> x[BATCH];
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      key[i] = NONE;
-      int64_t row = e + i;
-      if (row < e1) {
-        if (a.sorted) {
-          const uint2 k = a.sorted[row];
-          key[i] = k.x;
-          row = k.y;
-        } else {
-          key[i] = a.keys[row];
-        }
-      }
-      // (an id outside the table is `count` and sorted last; NONE and EMPTY are above it)
-      if (mine && key[i] < a.count) x[i].load(static_cast<const S*>(a.src) + row * a.lds + c * V);
+      const uint2 k = entry(e + i);
+      key[i] = k.x;
+      // (an id outside the table is `count`, sorted last; NONE is above it)
+      if (mine && k.x < a.count) x[i].load(static_cast<const T*>(a.G) + (int64_t)k.y * a.ldg + c * V);
       else x[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (e + i >= e1) break;
-      if (run_of(key[i]) != run) {
+      if (key[i] == NONE) break;
+      if (key[i] != run) {
         flush(false);
-        run = run_of(key[i]);
+        run = key[i];
       }
 #pragma unroll
       for (int q = 0; q < V; ++q) acc[q] += x[i].get(q);
     }
   }
-  flush(e1 < a.entries && run_of(key_at(e1)) == run);
+  flush(right == run);
+}
+
+// The rows of dE whose runs go over chunks, from the chunks' parts: a CTA for the run that a chunk begins and does not end,
+// TX accesses of the row wide, 256 / TX threads an access, whose sums are added in order.
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS) embed_join_kernel(const __grid_constant__ ReduceArgs a, int tx, int64_t slabs) {
+  __shared__ float sums[THREADS * V];
+  after_previous();
+  const int64_t chunk = blockIdx.x / slabs, slab = blockIdx.x % slabs, e1 = (chunk + 1) * CHUNK;
+  const uint32_t run = a.sorted[e1 - 1].x;  // (there is a chunk after this one)
+  if (run >= a.count || a.sorted[e1].x != run) return;
+  if (a.sorted[e1 - CHUNK].x == run && chunk > 0 && a.sorted[e1 - CHUNK - 1].x == run) return;  // begun before
+  // the chunks that end in the run, and the next where it begins with it
+  const int64_t chunks = (a.m + CHUNK - 1) / CHUNK, after = chunks - chunk - 1;
+  int64_t parts = warp_bound(after, [&](int64_t i) { return a.sorted[min(a.m, e1 + (i + 1) * CHUNK) - 1].x == run; });
+  if (parts < after && a.sorted[e1 + parts * CHUNK].x == run) ++parts;
+  ++parts;
+  const int x = threadIdx.x % tx, y = threadIdx.x / tx, ty = THREADS / tx;
+  const int64_t c = slab * tx + x;
+  const bool mine = c < a.n / V;
+  float acc[V] = {};
+  for (int64_t p = y; p < parts; p += BATCH * ty) {
+    Piece<float, V> v[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int64_t q = p + i * ty;
+      if (mine && q < parts) v[i].load(a.part + (2 * (chunk + q) + (q == 0 ? 1 : 0)) * a.n + c * V);
+      else v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[q] += v[i].get(q);
+  }
+#pragma unroll
+  for (int q = 0; q < V; ++q) sums[q * THREADS + threadIdx.x] = acc[q];
+  __syncthreads();
+  if (y != 0 || !mine) return;
+  Piece<T, V> o;
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    float s = acc[q];
+    for (int i = 1; i < ty; ++i) s += sums[q * THREADS + i * tx + x];
+    o.set(q, s * a.scale);
+  }
+  o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
 }
 
 // ------------------------------------------------------------------------------------------------ on the host
@@ -467,70 +529,46 @@ cudaError_t sort_ids(const EmbedArgs& a, uint2* to, uint2* other, uint32_t* coun
   return cudaSuccess;
 }
 
-constexpr int CHUNK = 32;
-
 template <typename T, int V>
 fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   const int64_t tiles = (a.m + TILE - 1) / TILE, chunks = (a.m + CHUNK - 1) / CHUNK;
-  // the sorted ids, the counts, and two levels' partial sums, which take turns
   auto up = [](int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); };
-  const int64_t deep = 2 * chunks, second = 2 * ((deep + CHUNK - 1) / CHUNK);
-  const size_t sort_bytes = up(a.m * 8), count_bytes = up((RADIX * tiles + RADIX) * 4);
-  const size_t part_bytes = chunks > 1 ? up(deep * a.n * 4) : 0, part2_bytes = chunks > 1 ? up(second * a.n * 4) : 0;
-  const size_t key_bytes = up(deep * 4);
+  const size_t sort_bytes = up(a.m * 8), count_bytes = up((RADIX * tiles + RADIX) * 4), part_bytes = chunks > 1 ? up(2 * chunks * a.n * 4) : 0;
   char* ws = nullptr;
-  const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&ws), 2 * sort_bytes + count_bytes + part_bytes + part2_bytes + 2 * key_bytes, st);
+  const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&ws), 2 * sort_bytes + count_bytes + part_bytes, st);
   if (r != FXTX_OK) return r;
-  char* at = ws;
-  auto take = [&](size_t bytes) {
-    char* p = at;
-    at += bytes;
-    return p;
-  };
-  uint2 *sorted = reinterpret_cast<uint2*>(take(sort_bytes)), *other = reinterpret_cast<uint2*>(take(sort_bytes));
-  uint32_t* counts = reinterpret_cast<uint32_t*>(take(count_bytes));
-  float* part[2] = {reinterpret_cast<float*>(take(part_bytes)), nullptr};
-  part[1] = reinterpret_cast<float*>(take(part2_bytes));
-  uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(take(key_bytes)), nullptr};
-  keys[1] = reinterpret_cast<uint32_t*>(take(key_bytes));
-
-  cudaError_t e = a.m > 0 ? sort_ids(a, sorted, other, counts, tiles, st) : cudaSuccess;
   ReduceArgs q = {};
-  q.entries = a.m;
+  uint2* sorted = reinterpret_cast<uint2*>(ws);
+  q.sorted = sorted;
+  q.part = reinterpret_cast<float*>(ws + 2 * sort_bytes + count_bytes);
+  cudaError_t e = cudaSuccess;
+  if (a.m > 0)
+    e = sort_ids(a, sorted, reinterpret_cast<uint2*>(ws + sort_bytes), reinterpret_cast<uint32_t*>(ws + 2 * sort_bytes), tiles, st);
+  q.m = a.m;
   q.n = a.n;
   q.count = a.count;
-  q.chunk = CHUNK;
-  q.sorted = sorted;
-  q.src = a.src;
-  q.lds = a.lds;
+  q.G = a.src;
+  q.ldg = a.lds;
   q.scale = a.scale;
   q.out = a.out;
   q.ldo = a.ldo;
   q.shape = shape_of(a.n / V, 1);
   // CTAs that zero rows: 32 rows each, fewer where the table is small
   q.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, a.count / (8 * (int64_t)dev.sm_count)));
-  int64_t zero_ctas = (a.count + q.zero_rows - 1) / q.zero_rows;
-  for (int level = 0; e == cudaSuccess; ++level) {
-    const int64_t c = (q.entries + q.chunk - 1) / q.chunk;
-    q.part = c > 1 ? part[level & 1] : nullptr;
-    q.part_keys = c > 1 ? keys[level & 1] : nullptr;
-    q.sum_ctas = (c * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
-    const dim3 grid((unsigned)(q.sum_ctas + zero_ctas));
-    const unsigned threads = (unsigned)(q.shape.tpr * q.shape.groups);
-    const unsigned block = (threads + 31) / 32 * 32;
-    e = level == 0 ? launch_kernel(embed_reduce_kernel<T, T, V>, grid, block, 0, st, q)
-                   : launch_kernel(embed_reduce_kernel<float, T, V>, grid, block, 0, st, q);
-    if (c <= 1) break;
-    zero_ctas = 0;
-    q.sorted = nullptr;
-    q.keys = keys[level & 1];
-    q.src = part[level & 1];
-    q.lds = a.n;
-    q.entries = 2 * c;
-    // (a level of at most 256 partial sums is the last)
-    q.chunk = q.entries <= 256 ? 256 : CHUNK;
+  q.sum_ctas = (chunks * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
+  q.ctas = q.sum_ctas + (a.count + q.zero_rows - 1) / q.zero_rows;
+  const unsigned threads = (unsigned)((q.shape.tpr * q.shape.groups + 31) / 32 * 32);
+  if (e == cudaSuccess)
+    e = q.shape.tpr >= 32 ? launch_kernel(embed_reduce_kernel<T, V, true>, dim3((unsigned)q.ctas), threads, 0, st, q)
+                          : launch_kernel(embed_reduce_kernel<T, V, false>, dim3((unsigned)q.ctas), threads, 0, st, q);
+  if (e == cudaSuccess && chunks > 1) {
+    const int64_t accesses = a.n / V;
+    int tx = 1;
+    while (tx < 64 && tx < accesses) tx *= 2;
+    const int64_t slabs = (accesses + tx - 1) / tx;
+    e = launch_kernel(embed_join_kernel<T, V>, dim3((unsigned)((chunks - 1) * slabs)), THREADS, 0, st, q, tx, slabs);
   }
-  cudaFreeAsync(ws, st);
+  if (ws) cudaFreeAsync(ws, st);
   if (e == cudaSuccess) return FXTX_OK;
   cudaGetLastError();
   return FXTX_ERR_CUDA;

@@ -15,6 +15,7 @@
 // Matrices whose start, pitch or width is no multiple of 16 bytes go entry by entry (V = 1), neighbouring threads
 // taking neighbouring entries.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "host.h"
@@ -490,17 +491,27 @@ RowShape shape_of(int64_t accesses, int per, int threads) {
   return s;
 }
 
-template <typename... A>
-int ctas_per_sm(void (*kernel)(A...), int threads, size_t smem) {
-  int b = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, threads, smem) != cudaSuccess) cudaGetLastError();
-  return std::max(b, 1);
+// CTAs of a kernel that fit an SM, asked once for each of the row shapes (threads and shared memory go by tpr).
+template <auto KERNEL>
+int ctas_per_sm(int tpr, int threads, size_t smem) {
+  static std::atomic<int> known[6 + 1024 / 32];
+  int x = 0;
+  if (tpr <= 32)
+    while ((1 << x) < tpr) ++x;
+  else
+    x = 5 + tpr / 32 - 1;
+  int b = known[x].load(std::memory_order_relaxed);
+  if (b > 0) return b;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, KERNEL, threads, smem) != cudaSuccess) cudaGetLastError();
+  b = std::max(b, 1);
+  known[x].store(b, std::memory_order_relaxed);
+  return b;
 }
 
 template <typename T, int V, int CH, bool BIG>
 cudaError_t launch_forward(const NormArgs& a, const RowShape& s, const DeviceInfo& dev, cudaStream_t st) {
   const int threads = (s.tpr * s.groups + 31) / 32 * 32;
-  const int64_t fit = (int64_t)ctas_per_sm(norm_kernel<T, V, CH, BIG>, threads, 0) * dev.sm_count;
+  const int64_t fit = (int64_t)ctas_per_sm<norm_kernel<T, V, CH, BIG>>(s.tpr, threads, 0) * dev.sm_count;
   const int64_t grid = std::min<int64_t>((a.m + s.groups - 1) / s.groups, fit);
   return launch_kernel(norm_kernel<T, V, CH, BIG>, dim3((unsigned)grid), threads, 0, st, a, s);
 }
@@ -531,7 +542,7 @@ fxtx_status_t launch_grad(NormArgs a, const RowShape& s, const DeviceInfo& dev, 
     cudaGetLastError();
     return FXTX_ERR_CUDA;
   }
-  const int64_t fit = (int64_t)ctas_per_sm(norm_grad_kernel<T, V, CH, BIG, SUMS>, threads, smem) * dev.sm_count;
+  const int64_t fit = (int64_t)ctas_per_sm<norm_grad_kernel<T, V, CH, BIG, SUMS>>(s.tpr, threads, smem) * dev.sm_count;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((a.m + s.groups - 1) / s.groups, fit));  // (no rows: zero sums)
   if (SUMS && grid > 1) {
     const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)grid * 2 * a.n * 4, st);

@@ -50,11 +50,11 @@ def layer_norm(X, weight=None, bias=None, eps: float = 1e-5, stats: bool = False
         out, ldo = torch.empty((m, n), dtype=dt, device=X.device), n
     else:
         ldo = _pitch(out, dt, m, n, "out", di)
-    mean = rstd = None
+    mean = rstd = pm = ps = None
     if stats:
-        mean, rstd = torch.empty((2, m), dtype=torch.float32, device=X.device).unbind()
-    _call(fxtx_layer_norm, di, code, m, n, X.data_ptr(), ldx, pw, pb, eps, out.data_ptr(), ldo,
-          mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, _current_stream(di))
+        mean, rstd = (torch.empty(m, dtype=torch.float32, device=X.device) for _ in range(2))
+        pm, ps = mean.data_ptr(), rstd.data_ptr()
+    _call(fxtx_layer_norm, di, code, m, n, X.data_ptr(), ldx, pw, pb, eps, out.data_ptr(), ldo, pm, ps, _current_stream(di))
     return (out, mean, rstd) if stats else out
 
 
@@ -158,7 +158,7 @@ def cross_entropy(X, W, labels, b=None, stream=None):
     k, ldw, trans = _weights(W, dt, n, di)
     pb = _vector(b, dt, k, "b", di)
     pl, bits = _integers(labels, m, "labels", di)
-    loss, lse = torch.empty((2, m), dtype=torch.float32, device=X.device).unbind()
+    loss, lse = (torch.empty(m, dtype=torch.float32, device=X.device) for _ in range(2))
     _call(fxtx_cross_entropy, di, code, m, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, trans, pb, pl, bits, loss.data_ptr(),
           lse.data_ptr(), _current_stream(di))
     return loss, lse
