@@ -9,11 +9,11 @@
 // a third scatters, a warp ranking its 32 ids at a time by matching digits; up to 8,192 ids take one CTA and one
 // launch, in shared memory.
 //
-// The sorted positions are then cut into chunks of 32. A worker (as many threads as a row has accesses of 16 bytes, up to
-// 256) adds a chunk's rows of G run by run. A run that begins and ends in the chunk is a row of dE; of one that goes over
-// the chunk's ends the chunk's part is written out in fp32, two a chunk at most, and a second kernel adds each such run's
-// parts, so that a frequent id's thousands of rows are shared out evenly. The rows of dE without an id are zeroed by further
-// CTAs of the first of these launches, which look their rows up among the sorted ids.
+// The sorted positions are then cut into chunks of 32. A worker adds a chunk's rows of G run by run; a run that goes over
+// into the next chunk and ends there is finished by the worker that began it. Of a longer one the chunks' parts are written
+// out in fp32, and a second kernel adds each such run's, so that a frequent id's thousands of rows are shared out evenly.
+// The rows of dE without an id are zeroed by further CTAs of the first of these launches, which look their rows up among
+// the sorted ids.
 #include <algorithm>
 
 #include "common.cuh"
@@ -22,6 +22,9 @@
 #include "train.h"
 
 namespace fxtx {
+
+int take_embed_device_error() { return take_device_error(); }
+
 namespace {
 
 constexpr int THREADS = 256;
@@ -114,6 +117,7 @@ struct SortArgs {
   const uint2* from;  // (id, position); NULL: the ids themselves
   uint2* to;
   uint32_t *counts, *totals;  // [digit][CTA], [digit]
+  uint32_t* clear;            // a word to be zeroed on the way
   int64_t ctas;
   int shift, bits;
 };
@@ -201,6 +205,7 @@ __global__ void __launch_bounds__(THREADS) sort_places_kernel(const __grid_const
     sum += __shfl_sync(FULL_MASK, upto, 31);
   }
   if (lane == 0) a.totals[d] = sum;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.clear = 0;
 }
 
 __global__ void __launch_bounds__(THREADS) sort_scatter_kernel(const __grid_constant__ SortArgs a) {
@@ -246,6 +251,7 @@ __global__ void __launch_bounds__(SMALL_THREADS) sort_small_kernel(const __grid_
   uint2 x[SMALL_ITEMS];
   uint32_t rank[SMALL_ITEMS];
   after_previous();
+  if (tid == 0) *a.clear = 0;
   for (int p = 0; p < passes; ++p) {
     const int shift = p * a.bits;
     for (int d = tid; d < warps_n * digits; d += (int)blockDim.x) hist[d] = 0;
@@ -295,7 +301,8 @@ struct ReduceArgs {
   float scale;
   void* out;
   int64_t ldo;
-  float* part;          // [2 a chunk][n]: what a chunk has of a run that began before it, and of one that it begins
+  float* part;          // [2 a chunk][n]: what a chunk has of a long run that began before it, and of one that it begins
+  uint32_t* longs;      // how many long runs there are, and the chunks that they begin in
   Shape shape;
   int64_t sum_ctas, ctas;  // CTAs of sums, spread among all; the others zero `zero_rows` rows each
   int zero_rows;
@@ -346,41 +353,54 @@ __device__ __forceinline__ void zero_rows(const ReduceArgs& a, int64_t row0) {
   }
 }
 
-// WARPS: a worker is whole warps.
-template <typename T, int V, bool WARPS>
-__global__ void __launch_bounds__(THREADS) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
-  after_previous();
-  // the sums' CTAs lie among the others, so that reading and writing go on together
-  const int64_t b = blockIdx.x, before = b * a.sum_ctas / a.ctas;
-  if ((b + 1) * a.sum_ctas / a.ctas == before) {
-    zero_rows<T, V>(a, (b - before) * a.zero_rows);
-    return;
+// A chunk of 32 sorted ids and the runs that go over its ends. A run that begins in one chunk and ends in the next is the
+// first one's as a whole; a longer one is cut at the chunks' ends, and its parts are added by the second kernel.
+struct Chunk {
+  int64_t e0, e1;
+  uint32_t left, right;     // the runs at the chunk's ends, NONE where none goes over them
+  bool skip, part_left;     // the left one is the chunk before's; is long
+  bool more, part_right;    // the right one goes on in the next chunk and ends there; is long
+  bool begins_long;         // the right one is long and begins here
+  __device__ __forceinline__ Chunk(const ReduceArgs& a, int64_t chunk) {
+    e0 = chunk * CHUNK;
+    e1 = min(a.m, e0 + CHUNK);
+    auto key = [&](int64_t e) { return e >= 0 && e < a.m ? a.sorted[e].x : NONE; };
+    const uint32_t m33 = key(e0 - CHUNK - 1), m32 = key(e0 - CHUNK), m1 = key(e0 - 1), k0 = key(e0), last = key(e1 - 1), next = key(e1),
+                   n31 = key(e1 + CHUNK - 1), n32 = key(e1 + CHUNK);
+    left = m1 == k0 ? k0 : NONE;
+    skip = left != NONE && !(m32 == left && m33 == left) && !(last == left && next == left);
+    part_left = left != NONE && !skip;
+    right = next == last ? last : NONE;
+    const bool begins = !(k0 == right && m1 == right), ends = !(n31 == right && n32 == right);
+    more = right != NONE && begins && ends;
+    part_right = right != NONE && !more;
+    begins_long = right != NONE && begins && !ends && right < a.count;
   }
-  const Shape& s = a.shape;
-  const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
-  const int64_t w = before * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t;
-  const int64_t e0 = chunk * CHUNK, e1 = min(a.m, e0 + CHUNK);
-  if (group >= s.groups || e0 >= a.m) return;
-  const bool mine = c < a.n / V;
-  uint2 own = make_uint2(NONE, 0);  // a lane's entry of the chunk
-  if (WARPS && e0 + (threadIdx.x & 31) < e1) own = a.sorted[e0 + (threadIdx.x & 31)];
-  auto entry = [&](int64_t e) {
-    if constexpr (WARPS) {
-      const int i = (int)(e - e0);
-      return make_uint2(__shfl_sync(FULL_MASK, own.x, i), __shfl_sync(FULL_MASK, own.y, i));
-    } else {
-      return e < e1 ? a.sorted[e] : make_uint2(NONE, 0);
-    }
-  };
-  const uint32_t left = e0 > 0 ? a.sorted[e0 - 1].x : NONE, right = e1 < a.m ? a.sorted[e1].x : NONE;
+};
 
+// One access of a row of dE: a chunk's sums, run by run.
+template <typename T, int V>
+struct RunSum {
+  const ReduceArgs& a;
+  const Chunk& k;
+  const int64_t chunk, c;
+  const bool mine;
   float acc[V] = {};
-  uint32_t run = entry(e0).x;
-  bool from_left = left == run;
-  // the run in hand ends, in this chunk or beyond it
-  auto flush = [&](bool to_right) {
+  uint32_t run = NONE;
+  __device__ __forceinline__ RunSum(const ReduceArgs& a_, const Chunk& k_, int64_t chunk_, int64_t c_, bool mine_)
+      : a(a_), k(k_), chunk(chunk_), c(c_), mine(mine_) {}
+  __device__ __forceinline__ void add(uint32_t key, const Piece<T, V>& x) {
+    if (key != run) {
+      flush(false);
+      run = key;
+    }
+#pragma unroll
+    for (int q = 0; q < V; ++q) acc[q] += x.get(q);
+  }
+  __device__ __forceinline__ void flush(bool part_right) {
     if (run < a.count && mine) {
-      if (!from_left && !to_right) {
+      const bool part_left = k.part_left && run == k.left;
+      if (!part_left && !part_right) {
         Piece<T, V> o;
 #pragma unroll
         for (int q = 0; q < V; ++q) o.set(q, acc[q] * a.scale);
@@ -389,83 +409,186 @@ __global__ void __launch_bounds__(THREADS) embed_reduce_kernel(const __grid_cons
         Piece<float, V> o;
 #pragma unroll
         for (int q = 0; q < V; ++q) o.set(q, acc[q]);
-        o.store(a.part + (2 * chunk + (from_left ? 0 : 1)) * a.n + c * V);
+        o.store(a.part + (2 * chunk + (part_left ? 0 : 1)) * a.n + c * V);
       }
     }
 #pragma unroll
     for (int q = 0; q < V; ++q) acc[q] = 0.f;
-    from_left = false;
-  };
+  }
+  // after the chunk's own entries: the rest of a run that ends in the next chunk
+  __device__ __forceinline__ void finish() {
+    if (run == NONE) return;
+    if (k.more)
 #pragma unroll 1
-  for (int64_t e = e0; e < e0 + CHUNK; e += BATCH) {
-    uint32_t key[BATCH];
+      for (int64_t e = k.e1; e < min(a.m, k.e1 + CHUNK); e += 4) {
+        Piece<T, V> x[4];
+        bool on[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint2 y = e + i < a.m ? a.sorted[e + i] : make_uint2(NONE, 0);
+          on[i] = y.x == k.right;
+          if (mine && on[i] && y.x < a.count) x[i].load(static_cast<const T*>(a.G) + (int64_t)y.y * a.ldg + c * V);
+          else x[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (on[i]) add(k.right, x[i]);
+        if (!on[3]) break;
+      }
+    flush(k.part_right);
+  }
+};
+
+// Whether the CTA sums (its place among those that do), else its place among those that zero rows: they lie among one
+// another, so that reading and writing go on together.
+__device__ __forceinline__ bool sums_here(const ReduceArgs& a, int64_t& at) {
+  const int64_t b = blockIdx.x, before = b * a.sum_ctas / a.ctas;
+  const bool is = (b + 1) * a.sum_ctas / a.ctas != before;
+  at = is ? before : b - before;
+  return is;
+}
+
+__device__ __forceinline__ void note_long(const ReduceArgs& a, const Chunk& k, int64_t chunk) {
+  if (k.begins_long) a.longs[1 + atomicAdd(a.longs, 1u)] = (uint32_t)chunk;  // (their order has no say in the result)
+}
+
+// Rows of at least 1 KB: a chunk's rows (2 KB of each) come by bulk copies to shared memory, all 32 on their way at once, a
+// lane each.
+constexpr int BULK_THREADS = 128, BULK_ROW = BULK_THREADS * 16;
+
+template <typename T>
+__global__ void __launch_bounds__(BULK_THREADS) embed_bulk_kernel(const __grid_constant__ ReduceArgs a) {
+  constexpr int V = 16 / sizeof(T), PER = 8, BARS = CHUNK / PER;  // rows a barrier
+  extern __shared__ __align__(128) unsigned char stage[];
+  __shared__ __align__(8) uint64_t full[BARS];
+  __shared__ uint32_t keys[CHUNK];
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < BARS; ++i) mbar_init(&full[i], PER);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  after_previous();
+  int64_t at;
+  if (!sums_here(a, at)) {
+    zero_rows<T, V>(a, at * a.zero_rows);
+    return;
+  }
+  const int64_t chunk = at / a.shape.slabs, slab = at % a.shape.slabs, accesses = a.n / V;
+  const int64_t c0 = slab * BULK_THREADS, c = c0 + threadIdx.x;
+  const uint32_t bytes = (uint32_t)min((int64_t)BULK_ROW, (accesses - c0) * 16);
+  const Chunk k(a, chunk);
+  if (threadIdx.x < CHUNK) {
+    const int lane = threadIdx.x;
+    uint2 own = k.e0 + lane < k.e1 ? a.sorted[k.e0 + lane] : make_uint2(NONE, 0);
+    if (k.skip && own.x == k.left) own.x = NONE;
+    keys[lane] = own.x;
+    const bool copy = own.x < a.count;
+    mbar_arrive_expect_tx(&full[lane / PER], copy ? bytes : 0);
+    if (copy)
+      bulk_g2s(stage + lane * BULK_ROW, static_cast<const T*>(a.G) + (int64_t)own.y * a.ldg + c0 * V, bytes, &full[lane / PER],
+               policy_evict_first());
+    if (lane == 0 && slab == 0) note_long(a, k, chunk);
+  }
+  __syncthreads();
+  RunSum<T, V> sum(a, k, chunk, c, c < accesses);
+  bool ok = true;
+#pragma unroll 1
+  for (int i = 0; i < CHUNK; ++i) {
+    if (i % PER == 0) ok = mbar_wait_bounded(&full[i / PER], 0) && ok;
+    const uint32_t key = keys[i];
+    if (key == NONE || !ok) continue;
+    Piece<T, V> x;
+    if (key < a.count) x.v[0] = *reinterpret_cast<const uint4*>(stage + i * BULK_ROW + threadIdx.x * 16);
+    else x.zero();
+    sum.add(key, x);
+  }
+  if (ok) sum.finish();
+}
+
+// Other rows: a worker is `tpr` threads, which hold 8 rows' accesses on their way.
+template <typename T, int V>
+__global__ void __launch_bounds__(THREADS, V == 1 ? 4 : 2) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
+  after_previous();
+  int64_t at;
+  if (!sums_here(a, at)) {
+    zero_rows<T, V>(a, at * a.zero_rows);
+    return;
+  }
+  const Shape& s = a.shape;
+  const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
+  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t;
+  if (group >= s.groups || chunk * CHUNK >= a.m) return;
+  const Chunk k(a, chunk);
+  if (c == 0) note_long(a, k, chunk);
+  RunSum<T, V> sum(a, k, chunk, c, c < a.n / V);
+#pragma unroll 1
+  for (int64_t e = k.e0; e < k.e1; e += BATCH) {
+    uint2 y[BATCH];
     Piece<T, V> x[BATCH];
 #pragma unroll
+    for (int i = 0; i < BATCH; ++i) y[i] = e + i < k.e1 ? a.sorted[e + i] : make_uint2(NONE, 0);
+#pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const uint2 k = entry(e + i);
-      key[i] = k.x;
+      if (k.skip && y[i].x == k.left) y[i].x = NONE;
       // (an id outside the table is `count`, sorted last; NONE is above it)
-      if (mine && k.x < a.count) x[i].load(static_cast<const T*>(a.G) + (int64_t)k.y * a.ldg + c * V);
+      if (sum.mine && y[i].x < a.count) x[i].load(static_cast<const T*>(a.G) + (int64_t)y[i].y * a.ldg + c * V);
       else x[i].zero();
     }
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (key[i] == NONE) break;
-      if (key[i] != run) {
-        flush(false);
-        run = key[i];
-      }
-#pragma unroll
-      for (int q = 0; q < V; ++q) acc[q] += x[i].get(q);
-    }
+    for (int i = 0; i < BATCH; ++i)
+      if (y[i].x != NONE) sum.add(y[i].x, x[i]);
   }
-  flush(right == run);
+  sum.finish();
 }
 
-// The rows of dE whose runs go over chunks, from the chunks' parts: a CTA for the run that a chunk begins and does not end,
-// TX accesses of the row wide, 256 / TX threads an access, whose sums are added in order.
+// The rows of dE of long runs, from the chunks' parts: TX accesses of a row a CTA, JOIN / TX threads an access, whose sums are
+// added in order.
+constexpr int JOIN = 512;
+
 template <typename T, int V>
-__global__ void __launch_bounds__(THREADS) embed_join_kernel(const __grid_constant__ ReduceArgs a, int tx, int64_t slabs) {
-  __shared__ float sums[THREADS * V];
+__global__ void __launch_bounds__(JOIN) embed_join_kernel(const __grid_constant__ ReduceArgs a, int tx, int64_t slabs) {
+  __shared__ float sums[JOIN * V];
   after_previous();
-  const int64_t chunk = blockIdx.x / slabs, slab = blockIdx.x % slabs, e1 = (chunk + 1) * CHUNK;
-  const uint32_t run = a.sorted[e1 - 1].x;  // (there is a chunk after this one)
-  if (run >= a.count || a.sorted[e1].x != run) return;
-  if (a.sorted[e1 - CHUNK].x == run && chunk > 0 && a.sorted[e1 - CHUNK - 1].x == run) return;  // begun before
-  // the chunks that end in the run, and the next where it begins with it
-  const int64_t chunks = (a.m + CHUNK - 1) / CHUNK, after = chunks - chunk - 1;
-  int64_t parts = warp_bound(after, [&](int64_t i) { return a.sorted[min(a.m, e1 + (i + 1) * CHUNK) - 1].x == run; });
-  if (parts < after && a.sorted[e1 + parts * CHUNK].x == run) ++parts;
-  ++parts;
-  const int x = threadIdx.x % tx, y = threadIdx.x / tx, ty = THREADS / tx;
-  const int64_t c = slab * tx + x;
-  const bool mine = c < a.n / V;
-  float acc[V] = {};
-  for (int64_t p = y; p < parts; p += BATCH * ty) {
-    Piece<float, V> v[BATCH];
+  const int64_t chunks = (a.m + CHUNK - 1) / CHUNK, units = (int64_t)a.longs[0] * slabs;
+  const int x = threadIdx.x % tx, y = threadIdx.x / tx, ty = JOIN / tx;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t chunk = a.longs[1 + u / slabs], e1 = (chunk + 1) * CHUNK, c = u % slabs * tx + x;
+    const uint32_t run = a.sorted[e1].x;
+    // the chunks that end in the run, and the next where it begins with it
+    const int64_t after = chunks - chunk - 1;
+    int64_t parts = warp_bound(after, [&](int64_t i) { return a.sorted[min(a.m, e1 + (i + 1) * CHUNK) - 1].x == run; });
+    if (parts < after && a.sorted[e1 + parts * CHUNK].x == run) ++parts;
+    ++parts;
+    const bool mine = c < a.n / V;
+    float acc[V] = {};
+    constexpr int U = 4;
+    for (int64_t p = y; p < parts; p += U * ty) {
+      Piece<float, V> v[U];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int64_t q = p + i * ty;
-      if (mine && q < parts) v[i].load(a.part + (2 * (chunk + q) + (q == 0 ? 1 : 0)) * a.n + c * V);
-      else v[i].zero();
+      for (int i = 0; i < U; ++i) {
+        const int64_t q = p + i * ty;
+        if (mine && q < parts) v[i].load(a.part + (2 * (chunk + q) + (q == 0 ? 1 : 0)) * a.n + c * V);
+        else v[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int q = 0; q < V; ++q) acc[q] += v[i].get(q);
     }
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i)
+    for (int q = 0; q < V; ++q) sums[q * JOIN + threadIdx.x] = acc[q];
+    __syncthreads();
+    if (y != 0 || !mine) continue;
+    Piece<T, V> o;
 #pragma unroll
-      for (int q = 0; q < V; ++q) acc[q] += v[i].get(q);
+    for (int q = 0; q < V; ++q) {
+      float s = acc[q];
+      for (int i = 1; i < ty; ++i) s += sums[q * JOIN + i * tx + x];
+      o.set(q, s * a.scale);
+    }
+    o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
   }
-#pragma unroll
-  for (int q = 0; q < V; ++q) sums[q * THREADS + threadIdx.x] = acc[q];
-  __syncthreads();
-  if (y != 0 || !mine) return;
-  Piece<T, V> o;
-#pragma unroll
-  for (int q = 0; q < V; ++q) {
-    float s = acc[q];
-    for (int i = 1; i < ty; ++i) s += sums[q * THREADS + i * tx + x];
-    o.set(q, s * a.scale);
-  }
-  o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
 }
 
 // ------------------------------------------------------------------------------------------------ on the host
@@ -492,13 +615,14 @@ cudaError_t lookup(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
 }
 
 // The ids sorted into `to`, by way of `other`.
-cudaError_t sort_ids(const EmbedArgs& a, uint2* to, uint2* other, uint32_t* counts, int64_t ctas, cudaStream_t st) {
+cudaError_t sort_ids(const EmbedArgs& a, uint2* to, uint2* other, uint32_t* counts, uint32_t* clear, int64_t ctas, cudaStream_t st) {
   SortArgs s = {};
   s.ids = a.ids;
   s.ids64 = a.ids64;
   s.m = a.m;
   s.count = a.count;
   s.counts = counts;
+  s.clear = clear;
   s.totals = counts + RADIX * ctas;
   s.ctas = ctas;
   int bits = 1;
@@ -531,19 +655,22 @@ cudaError_t sort_ids(const EmbedArgs& a, uint2* to, uint2* other, uint32_t* coun
 
 template <typename T, int V>
 fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  const int64_t tiles = (a.m + TILE - 1) / TILE, chunks = (a.m + CHUNK - 1) / CHUNK;
+  const int64_t tiles = (a.m + TILE - 1) / TILE, chunks = (a.m + CHUNK - 1) / CHUNK, accesses = a.n / V;
+  const bool longs = chunks > 2;  // there may be runs over three chunks
   auto up = [](int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); };
-  const size_t sort_bytes = up(a.m * 8), count_bytes = up((RADIX * tiles + RADIX) * 4), part_bytes = chunks > 1 ? up(2 * chunks * a.n * 4) : 0;
+  const size_t sort_bytes = up(a.m * 8), count_bytes = up((RADIX * tiles + RADIX) * 4), long_bytes = up((chunks + 1) * 4);
+  const size_t part_bytes = longs ? up(2 * chunks * a.n * 4) : 0;
   char* ws = nullptr;
-  const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&ws), 2 * sort_bytes + count_bytes + part_bytes, st);
+  const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&ws), 2 * sort_bytes + count_bytes + long_bytes + part_bytes, st);
   if (r != FXTX_OK) return r;
   ReduceArgs q = {};
   uint2* sorted = reinterpret_cast<uint2*>(ws);
   q.sorted = sorted;
-  q.part = reinterpret_cast<float*>(ws + 2 * sort_bytes + count_bytes);
+  q.longs = reinterpret_cast<uint32_t*>(ws + 2 * sort_bytes + count_bytes);
+  q.part = reinterpret_cast<float*>(ws + 2 * sort_bytes + count_bytes + long_bytes);
   cudaError_t e = cudaSuccess;
   if (a.m > 0)
-    e = sort_ids(a, sorted, reinterpret_cast<uint2*>(ws + sort_bytes), reinterpret_cast<uint32_t*>(ws + 2 * sort_bytes), tiles, st);
+    e = sort_ids(a, sorted, reinterpret_cast<uint2*>(ws + sort_bytes), reinterpret_cast<uint32_t*>(ws + 2 * sort_bytes), q.longs, tiles, st);
   q.m = a.m;
   q.n = a.n;
   q.count = a.count;
@@ -552,23 +679,32 @@ fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t s
   q.scale = a.scale;
   q.out = a.out;
   q.ldo = a.ldo;
-  q.shape = shape_of(a.n / V, 1);
   // CTAs that zero rows: 32 rows each, fewer where the table is small
   q.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, a.count / (8 * (int64_t)dev.sm_count)));
-  q.sum_ctas = (chunks * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
-  q.ctas = q.sum_ctas + (a.count + q.zero_rows - 1) / q.zero_rows;
-  const unsigned threads = (unsigned)((q.shape.tpr * q.shape.groups + 31) / 32 * 32);
-  if (e == cudaSuccess)
-    e = q.shape.tpr >= 32 ? launch_kernel(embed_reduce_kernel<T, V, true>, dim3((unsigned)q.ctas), threads, 0, st, q)
-                          : launch_kernel(embed_reduce_kernel<T, V, false>, dim3((unsigned)q.ctas), threads, 0, st, q);
-  if (e == cudaSuccess && chunks > 1) {
-    const int64_t accesses = a.n / V;
-    int tx = 1;
-    while (tx < 64 && tx < accesses) tx *= 2;
-    const int64_t slabs = (accesses + tx - 1) / tx;
-    e = launch_kernel(embed_join_kernel<T, V>, dim3((unsigned)((chunks - 1) * slabs)), THREADS, 0, st, q, tx, slabs);
+  const int64_t zero_ctas = (a.count + q.zero_rows - 1) / q.zero_rows;
+  if (V > 1 && accesses >= BULK_THREADS / 2) {
+    if constexpr (V > 1) {
+      q.shape.slabs = (accesses + BULK_THREADS - 1) / BULK_THREADS;
+      q.sum_ctas = chunks * q.shape.slabs;
+      q.ctas = q.sum_ctas + zero_ctas;
+      const size_t smem = CHUNK * BULK_ROW;
+      if (e == cudaSuccess) e = ensure_smem((const void*)embed_bulk_kernel<T>, smem);
+      if (e == cudaSuccess) e = launch_kernel(embed_bulk_kernel<T>, dim3((unsigned)q.ctas), BULK_THREADS, smem, st, q);
+    }
+  } else {
+    q.shape = shape_of(accesses, 1);
+    q.sum_ctas = (chunks * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
+    q.ctas = q.sum_ctas + zero_ctas;
+    const unsigned threads = (unsigned)((q.shape.tpr * q.shape.groups + 31) / 32 * 32);
+    if (e == cudaSuccess) e = launch_kernel(embed_reduce_kernel<T, V>, dim3((unsigned)q.ctas), threads, 0, st, q);
   }
-  if (ws) cudaFreeAsync(ws, st);
+  if (e == cudaSuccess && longs) {
+    int tx = 1;
+    while (tx < 32 && tx < accesses) tx *= 2;
+    const int64_t slabs = (accesses + tx - 1) / tx, most = (chunks - 2) * slabs;
+    e = launch_kernel(embed_join_kernel<T, V>, dim3((unsigned)std::min<int64_t>(most, (int64_t)dev.sm_count * 4)), JOIN, 0, st, q, tx, slabs);
+  }
+  cudaFreeAsync(ws, st);
   if (e == cudaSuccess) return FXTX_OK;
   cudaGetLastError();
   return FXTX_ERR_CUDA;

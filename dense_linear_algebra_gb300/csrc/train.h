@@ -46,6 +46,7 @@ struct EmbedArgs {
   int64_t ldo = 0;
 };
 fxtx_status_t run_embed(fxtx_type_t type, const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st);
+int take_embed_device_error();
 fxtx_status_t run_embed_grad(fxtx_type_t type, const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
 }  // namespace fxtx
