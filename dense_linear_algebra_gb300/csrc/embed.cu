@@ -6,8 +6,8 @@
 // The gradient sorts the ids, so that every row of dE is summed in registers, in the order of the positions, and
 // written once, with no atomic addition: the result is the same on every call. The sort is a stable radix sort of
 // (id, position), up to 9 bits a pass: each CTA counts its ids' digits, a second kernel turns the counts into places,
-// a third scatters, a warp ranking its 32 ids at a time by matching digits; up to 8,192 ids take one CTA and one
-// launch, in shared memory.
+// a third scatters, a warp ranking its 32 ids at a time by votes on the digits' bits; up to 16,384 ids take one launch of one
+// cluster, whose CTAs exchange their counts.
 //
 // The sorted positions are then cut into chunks of 32. A worker adds a chunk's rows of G run by run; a run that goes over
 // into the next chunk and ends there is finished by the worker that began it. Of a longer one the chunks' parts are written
@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
+#include "tc.cuh"
 #include "train.h"
 
 namespace fxtx {
@@ -30,8 +31,7 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int MAX_BITS = 9, RADIX = 1 << MAX_BITS;
 constexpr int ITEMS = 4, TILE = THREADS * ITEMS;         // ids a thread and a CTA of the sort take
-constexpr int SMALL_ITEMS = 8, SMALL_THREADS = 1024, SMALL = SMALL_THREADS * SMALL_ITEMS;
-constexpr int BATCH = 8;                                 // rows on their way at a time
+constexpr int CLUSTER_ITEMS = 2, CLUSTER_THREADS = 1024, CLUSTER = 8;  // the same of the sort in one cluster, and its CTAs at most
 constexpr int CHUNK = 32;                                // sorted ids a worker adds
 
 constexpr uint32_t NONE = 0xffffffffu;  // the key of no id
@@ -136,9 +136,15 @@ __device__ __forceinline__ void rank_items(const uint2* x, int items, uint32_t* 
   for (int i = 0; i < ITEMS; ++i) {
     if (i >= items) break;
     const bool in = x[i].x != NONE;
-    const uint32_t d = in ? digit_of(x[i].x, shift, bits) : NONE;
-    const uint32_t same = __match_any_sync(FULL_MASK, d), before = __popc(same & ((1u << lane) - 1u));
-    const uint32_t had = in ? hist[d] : 0;
+    const uint32_t d = in ? digit_of(x[i].x, shift, bits) : 0;
+    // the lanes with the same digit, by a vote a bit (match.any takes about 150 cycles where the digits differ)
+    uint32_t same = __ballot_sync(FULL_MASK, in);
+#pragma unroll
+    for (int q = 0; q < MAX_BITS; ++q) {
+      const uint32_t set = __ballot_sync(FULL_MASK, d >> q & 1u);
+      same &= d >> q & 1u ? set : ~set;
+    }
+    const uint32_t before = __popc(same & ((1u << lane) - 1u)), had = hist[d];
     __syncwarp();
     if (in && before == 0) hist[d] = had + __popc(same);
     __syncwarp();
@@ -240,55 +246,89 @@ __global__ void __launch_bounds__(THREADS) sort_scatter_kernel(const __grid_cons
     if (x[i].x != NONE) a.to[hist[warp][digit_of(x[i].x, a.shift, a.bits)] + rank[i]] = x[i];
 }
 
-// All passes of up to SMALL ids, in one CTA: ids and positions in shared memory between passes.
-__global__ void __launch_bounds__(SMALL_THREADS) sort_small_kernel(const __grid_constant__ SortArgs a, int passes) {
+// All passes in one cluster: each CTA takes `items` ids a thread, the CTAs' counts are exchanged through distributed shared
+// memory, and the cluster's barriers make the ids that one CTA has written seen by the others in the next pass.
+struct ClusterSort {
+  SortArgs s;
+  uint2* other;  // takes turns with s.to, which the last pass ends in
+  int passes, items;
+};
+
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(CLUSTER_THREADS) sort_cluster_kernel(const __grid_constant__ ClusterSort c) {
+  constexpr int WARPS = CLUSTER_THREADS / 32;
   extern __shared__ __align__(16) uint32_t shared[];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps_n = (int)blockDim.x >> 5;
-  uint32_t *first = shared, *warps = first + RADIX, *hist = warps + 32;
-  uint2* held = reinterpret_cast<uint2*>(hist + warps_n * RADIX);
-  const int items = ((int)a.m + (int)blockDim.x - 1) / (int)blockDim.x, digits = 1 << a.bits;
-  const int base = warp * 32 * items + lane;
-  uint2 x[SMALL_ITEMS];
-  uint32_t rank[SMALL_ITEMS];
+  __shared__ uint32_t total[RADIX], first[RADIX], before[RADIX], warps[32];
+  const SortArgs& a = c.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, digits = 1 << a.bits;
+  const int ctas = (int)gridDim.x, rank_here = (int)blockIdx.x;  // (one cluster)
+  uint32_t* hist = shared;  // [WARPS][digits]
+  const int64_t base = (int64_t)rank_here * CLUSTER_THREADS * c.items + warp * 32 * c.items + lane;
+  uint2 x[CLUSTER_ITEMS];
+  uint32_t rank[CLUSTER_ITEMS];
   after_previous();
-  if (tid == 0) *a.clear = 0;
-  for (int p = 0; p < passes; ++p) {
+  if (rank_here == 0 && tid == 0) *a.clear = 0;
+  const uint2* from = nullptr;
+  uint2* to = c.passes % 2 ? a.to : c.other;
+  for (int p = 0; p < c.passes; ++p) {
     const int shift = p * a.bits;
-    for (int d = tid; d < warps_n * digits; d += (int)blockDim.x) hist[d] = 0;
 #pragma unroll
-    for (int i = 0; i < SMALL_ITEMS; ++i) {
-      if (i >= items) break;
-      const int at = base + 32 * i;
-      x[i] = p == 0 ? item(a, at) : at < a.m ? held[at] : make_uint2(NONE, 0);
+    for (int i = 0; i < CLUSTER_ITEMS; ++i) {
+      if (i >= c.items) break;
+      const int64_t at = base + 32 * i;
+      x[i] = at >= a.m ? make_uint2(NONE, 0) : from ? from[at] : item(a, at);
     }
+    for (int d = tid; d < WARPS * digits; d += CLUSTER_THREADS) hist[d] = 0;
     __syncthreads();
-    rank_items<SMALL_ITEMS>(x, items, hist + warp * digits, shift, a.bits, rank);
+    rank_items<CLUSTER_ITEMS>(x, c.items, hist + warp * digits, shift, a.bits, rank);
     __syncthreads();
-    for (int d = tid; d < digits; d += (int)blockDim.x) {
+    // over the warps before, and over all of them
+    for (int d = tid; d < digits; d += CLUSTER_THREADS) {
       uint32_t at = 0;
-      for (int w = 0; w < warps_n; w += 8) {  // (eight reads on their way at a time)
+#pragma unroll 1
+      for (int w = 0; w < WARPS; w += 8) {
         uint32_t y[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] = w + q < warps_n ? hist[(w + q) * digits + d] : 0;
+        for (int q = 0; q < 8; ++q) y[q] = hist[(w + q) * digits + d];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          if (w + q < warps_n) hist[(w + q) * digits + d] = at;
+          hist[(w + q) * digits + d] = at;
           at += y[q];
         }
       }
-      first[d] = at;
+      total[d] = at;
+    }
+    // over the CTAs before, and over all of them
+    cluster_sync();
+    for (int d = tid; d < digits; d += CLUSTER_THREADS) {
+      uint32_t mine = 0, all = 0;
+#pragma unroll 4
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t v = ld_cluster(cluster_addr(total + d, (uint32_t)r));
+        all += v;
+        mine += r < rank_here ? v : 0;
+      }
+      first[d] = all;
+      before[d] = mine;
     }
     __syncthreads();
     scan(first, digits, warps);
 #pragma unroll
-    for (int i = 0; i < SMALL_ITEMS; ++i) {
-      if (i >= items) break;
+    for (int i = 0; i < CLUSTER_ITEMS; ++i) {
+      if (i >= c.items) break;
       if (x[i].x == NONE) continue;
-      const uint32_t d = digit_of(x[i].x, shift, a.bits), at = first[d] + hist[warp * digits + d] + rank[i];
-      if (p + 1 < passes) held[at] = x[i];
-      else a.to[at] = x[i];
+      const uint32_t d = digit_of(x[i].x, shift, a.bits);
+      to[first[d] + before[d] + hist[warp * digits + d] + rank[i]] = x[i];
     }
-    __syncthreads();
+    // (the other CTAs have read this one's totals, and this pass's ids are seen by all)
+    cluster_sync();
+    from = to;
+    to = to == a.to ? c.other : a.to;
   }
 }
 
@@ -323,50 +363,72 @@ __device__ __forceinline__ int64_t warp_bound(int64_t n, F holds) {
   return lo;
 }
 
+// `bytes` from p on to zero, by the whole CTA: 16 at a time between the first and the last multiple of that. p and bytes are
+// multiples of 2.
+__device__ __forceinline__ void zero_bytes(void* p, int64_t bytes) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const int64_t head = min(bytes, (int64_t)(-at & 15u)), words = (bytes - head) / 16, tail = bytes - head - words * 16;
+  char* base = static_cast<char*>(p);
+  for (int64_t i = threadIdx.x; i < words; i += blockDim.x) reinterpret_cast<uint4*>(base + head)[i] = make_uint4(0, 0, 0, 0);
+  const int i = (int)threadIdx.x;
+  if (2 * i < head) *reinterpret_cast<uint16_t*>(base + 2 * i) = 0;
+  if (2 * i < tail) *reinterpret_cast<uint16_t*>(base + head + words * 16 + 2 * i) = 0;
+}
+
 // Rows of dE without an id.
-template <typename T, int V>
+template <typename T>
 __device__ __forceinline__ void zero_rows(const ReduceArgs& a, int64_t row0) {
   __shared__ uint32_t s_absent;
   if (threadIdx.x < 32) {
     const int64_t v = row0 + threadIdx.x;
     const bool mine = (int)threadIdx.x < a.zero_rows && v < a.count;
-    // the entries of these rows, and in them the first one not below the lane's row
+    // the first entry not below these rows; those from there on show which rows are there
     int64_t lo = warp_bound(a.m, [&](int64_t i) { return a.sorted[i].x < (uint32_t)row0; });
-    int64_t hi = lo + warp_bound(a.m - lo, [&](int64_t i) { return a.sorted[lo + i].x < (uint32_t)(row0 + a.zero_rows); });
-    const int64_t end = hi;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (a.sorted[mid].x < (uint32_t)v) lo = mid + 1;
-      else hi = mid;
+    uint32_t there = 0;
+    bool all = false;
+    for (int i = 0; i < 4 && !all; ++i) {
+      const int64_t e = lo + 32 * i + threadIdx.x;
+      const uint32_t at = (e < a.m ? a.sorted[e].x : NONE) - (uint32_t)row0;
+      const bool in = at < (uint32_t)a.zero_rows;
+      there |= __reduce_or_sync(FULL_MASK, in ? 1u << at : 0u);
+      all = !__all_sync(FULL_MASK, in);
     }
-    const bool there = mine && lo < end && a.sorted[lo].x == (uint32_t)v;
-    const uint32_t absent = __ballot_sync(FULL_MASK, mine && !there);
+    if (!all) {  // many entries to a row: a search a row
+      int64_t hi = mine ? a.m : lo;
+      while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (a.sorted[mid].x < (uint32_t)v) lo = mid + 1;
+        else hi = mid;
+      }
+      there = __ballot_sync(FULL_MASK, mine && lo < a.m && a.sorted[lo].x == (uint32_t)v);
+    }
+    const uint32_t absent = __ballot_sync(FULL_MASK, mine) & ~there;
     if (threadIdx.x == 0) s_absent = absent;
   }
   __syncthreads();
-  Piece<T, V> z;
-  z.zero();
-  const int64_t accesses = a.n / V;
-  for (uint32_t left = s_absent; left; left &= left - 1) {
-    T* p = static_cast<T*>(a.out) + (row0 + __ffs(left) - 1) * a.ldo;
-    for (int64_t c = threadIdx.x; c < accesses; c += blockDim.x) z.store(p + c * V);
+  // neighbouring rows without a gap between them as one range
+  const int64_t bytes = a.n * (int64_t)sizeof(T);
+  for (uint32_t left = s_absent; left;) {
+    const int first = __ffs(left) - 1, rows = a.ldo == a.n ? __ffs(~(left >> first)) - 1 : 1;  // (32 rows: ~ has no bit, 0 - 1)
+    const int some = rows < 0 ? 32 : rows;
+    zero_bytes(static_cast<T*>(a.out) + (row0 + first) * a.ldo, some * bytes);
+    left = first + some < 32 ? left >> (first + some) << (first + some) : 0;
   }
 }
 
 // A chunk of 32 sorted ids and the runs that go over its ends. A run that begins in one chunk and ends in the next is the
 // first one's as a whole; a longer one is cut at the chunks' ends, and its parts are added by the second kernel.
 struct Chunk {
-  int64_t e0, e1;
+  int n;                    // its ids
   uint32_t left, right;     // the runs at the chunk's ends, NONE where none goes over them
   bool skip, part_left;     // the left one is the chunk before's; is long
   bool more, part_right;    // the right one goes on in the next chunk and ends there; is long
   bool begins_long;         // the right one is long and begins here
-  __device__ __forceinline__ Chunk(const ReduceArgs& a, int64_t chunk) {
-    e0 = chunk * CHUNK;
-    e1 = min(a.m, e0 + CHUNK);
-    auto key = [&](int64_t e) { return e >= 0 && e < a.m ? a.sorted[e].x : NONE; };
-    const uint32_t m33 = key(e0 - CHUNK - 1), m32 = key(e0 - CHUNK), m1 = key(e0 - 1), k0 = key(e0), last = key(e1 - 1), next = key(e1),
-                   n31 = key(e1 + CHUNK - 1), n32 = key(e1 + CHUNK);
+  // `k`: the sorted ids from the chunk's first on, those of BEFORE entries before it and of the next chunk among them
+  __device__ __forceinline__ Chunk(const ReduceArgs& a, int64_t chunk, const uint2* k) {
+    n = (int)min((int64_t)CHUNK, a.m - chunk * CHUNK);
+    const uint32_t m33 = k[-CHUNK - 1].x, m32 = k[-CHUNK].x, m1 = k[-1].x, k0 = k[0].x, last = k[n - 1].x, next = k[n].x,
+                   n31 = k[2 * CHUNK - 1].x, n32 = k[2 * CHUNK].x;
     left = m1 == k0 ? k0 : NONE;
     skip = left != NONE && !(m32 == left && m33 == left) && !(last == left && next == left);
     part_left = left != NONE && !skip;
@@ -377,6 +439,17 @@ struct Chunk {
     begins_long = right != NONE && begins && !ends && right < a.count;
   }
 };
+constexpr int BEFORE = CHUNK + 1;
+
+// The sorted ids of `chunks` chunks from one on, with those before and after them, to shared memory (NONE beyond the ends), by
+// the whole CTA. Gives the place of the first chunk's.
+__device__ __forceinline__ const uint2* load_ids(const ReduceArgs& a, int64_t chunk, int chunks, uint2* s) {
+  const int64_t first = chunk * CHUNK - BEFORE;
+  const int n = BEFORE + chunks * CHUNK + CHUNK + 1;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) s[i] = first + i >= 0 && first + i < a.m ? a.sorted[first + i] : make_uint2(NONE, 0);
+  __syncthreads();
+  return s + BEFORE;
+}
 
 // One access of a row of dE: a chunk's sums, run by run.
 template <typename T, int V>
@@ -415,26 +488,31 @@ struct RunSum {
 #pragma unroll
     for (int q = 0; q < V; ++q) acc[q] = 0.f;
   }
+  // the rows of the first `n` of N ids, those other than `only` left out unless it is NONE
+  template <int N>
+  __device__ __forceinline__ void add_rows(const uint2* ids, int n, uint32_t only) {
+    Piece<T, V> x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint2 y = ids[i < n ? i : 0];
+      // (an id outside the table is `count`, sorted last; NONE is above it)
+      if (mine && i < n && y.x < a.count && (only == NONE || y.x == only)) x[i].load(static_cast<const T*>(a.G) + (int64_t)y.y * a.ldg + c * V);
+      else x[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i >= n) break;
+      const uint32_t key = ids[i].x;
+      if (only == NONE || key == only) add(key, x[i]);
+    }
+  }
   // after the chunk's own entries: the rest of a run that ends in the next chunk
-  __device__ __forceinline__ void finish() {
+  template <int N>
+  __device__ __forceinline__ void finish(const uint2* ids) {
     if (run == NONE) return;
     if (k.more)
 #pragma unroll 1
-      for (int64_t e = k.e1; e < min(a.m, k.e1 + CHUNK); e += 4) {
-        Piece<T, V> x[4];
-        bool on[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint2 y = e + i < a.m ? a.sorted[e + i] : make_uint2(NONE, 0);
-          on[i] = y.x == k.right;
-          if (mine && on[i] && y.x < a.count) x[i].load(static_cast<const T*>(a.G) + (int64_t)y.y * a.ldg + c * V);
-          else x[i].zero();
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (on[i]) add(k.right, x[i]);
-        if (!on[3]) break;
-      }
+      for (int i = CHUNK; i < 2 * CHUNK && ids[i].x == k.right; i += N) add_rows<N>(ids + i, 2 * CHUNK - i, k.right);
     flush(k.part_right);
   }
 };
@@ -454,14 +532,14 @@ __device__ __forceinline__ void note_long(const ReduceArgs& a, const Chunk& k, i
 
 // Rows of at least 1 KB: a chunk's rows (2 KB of each) come by bulk copies to shared memory, all 32 on their way at once, a
 // lane each.
-constexpr int BULK_THREADS = 128, BULK_ROW = BULK_THREADS * 16;
+constexpr int BULK_THREADS = 64, BULK_ROW = BULK_THREADS * 16;
 
 template <typename T>
 __global__ void __launch_bounds__(BULK_THREADS) embed_bulk_kernel(const __grid_constant__ ReduceArgs a) {
   constexpr int V = 16 / sizeof(T), PER = 8, BARS = CHUNK / PER;  // rows a barrier
   extern __shared__ __align__(128) unsigned char stage[];
   __shared__ __align__(8) uint64_t full[BARS];
-  __shared__ uint32_t keys[CHUNK];
+  __shared__ uint2 s_ids[BEFORE + 2 * CHUNK + 1];
   if (threadIdx.x == 0) {
     for (int i = 0; i < BARS; ++i) mbar_init(&full[i], PER);
     fence_mbar_init();
@@ -470,80 +548,73 @@ __global__ void __launch_bounds__(BULK_THREADS) embed_bulk_kernel(const __grid_c
   after_previous();
   int64_t at;
   if (!sums_here(a, at)) {
-    zero_rows<T, V>(a, at * a.zero_rows);
+    zero_rows<T>(a, at * a.zero_rows);
     return;
   }
   const int64_t chunk = at / a.shape.slabs, slab = at % a.shape.slabs, accesses = a.n / V;
   const int64_t c0 = slab * BULK_THREADS, c = c0 + threadIdx.x;
   const uint32_t bytes = (uint32_t)min((int64_t)BULK_ROW, (accesses - c0) * 16);
-  const Chunk k(a, chunk);
+  const uint2* ids = load_ids(a, chunk, 1, s_ids);
+  const Chunk k(a, chunk, ids);
+  // an id of the chunk's own, NONE where it is the chunk before's
+  auto own = [&](int i) { return i >= k.n || (k.skip && ids[i].x == k.left) ? NONE : ids[i].x; };
   if (threadIdx.x < CHUNK) {
     const int lane = threadIdx.x;
-    uint2 own = k.e0 + lane < k.e1 ? a.sorted[k.e0 + lane] : make_uint2(NONE, 0);
-    if (k.skip && own.x == k.left) own.x = NONE;
-    keys[lane] = own.x;
-    const bool copy = own.x < a.count;
+    const bool copy = own(lane) < a.count;
     mbar_arrive_expect_tx(&full[lane / PER], copy ? bytes : 0);
     if (copy)
-      bulk_g2s(stage + lane * BULK_ROW, static_cast<const T*>(a.G) + (int64_t)own.y * a.ldg + c0 * V, bytes, &full[lane / PER],
+      bulk_g2s(stage + lane * BULK_ROW, static_cast<const T*>(a.G) + (int64_t)ids[lane].y * a.ldg + c0 * V, bytes, &full[lane / PER],
                policy_evict_first());
     if (lane == 0 && slab == 0) note_long(a, k, chunk);
   }
-  __syncthreads();
   RunSum<T, V> sum(a, k, chunk, c, c < accesses);
   bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < CHUNK; ++i) {
     if (i % PER == 0) ok = mbar_wait_bounded(&full[i / PER], 0) && ok;
-    const uint32_t key = keys[i];
+    const uint32_t key = own(i);
     if (key == NONE || !ok) continue;
     Piece<T, V> x;
     if (key < a.count) x.v[0] = *reinterpret_cast<const uint4*>(stage + i * BULK_ROW + threadIdx.x * 16);
     else x.zero();
     sum.add(key, x);
   }
-  if (ok) sum.finish();
+  if (ok) sum.template finish<4>(ids);
 }
 
-// Other rows: a worker is `tpr` threads, which hold 8 rows' accesses on their way.
+// Other rows: a worker is `tpr` threads, which hold several rows' accesses on their way.
+constexpr int GROUPS = 16;  // workers a CTA has at most
+
 template <typename T, int V>
 __global__ void __launch_bounds__(THREADS, V == 1 ? 4 : 2) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
+  __shared__ uint2 s_ids[BEFORE + (GROUPS + 1) * CHUNK + 1];
   after_previous();
   int64_t at;
   if (!sums_here(a, at)) {
-    zero_rows<T, V>(a, at * a.zero_rows);
+    zero_rows<T>(a, at * a.zero_rows);
     return;
   }
+  constexpr int N = V == 1 ? 16 : 8;
   const Shape& s = a.shape;
   const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
-  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t;
+  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t, first = at * s.groups / s.slabs;
+  const uint2* ids = load_ids(a, first, s.groups, s_ids);
   if (group >= s.groups || chunk * CHUNK >= a.m) return;
-  const Chunk k(a, chunk);
+  ids += (chunk - first) * CHUNK;
+  const Chunk k(a, chunk, ids);
   if (c == 0) note_long(a, k, chunk);
   RunSum<T, V> sum(a, k, chunk, c, c < a.n / V);
+  int i = 0;
+  if (k.skip)
+    while (ids[i].x == k.left) ++i;
 #pragma unroll 1
-  for (int64_t e = k.e0; e < k.e1; e += BATCH) {
-    uint2 y[BATCH];
-    Piece<T, V> x[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) y[i] = e + i < k.e1 ? a.sorted[e + i] : make_uint2(NONE, 0);
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      if (k.skip && y[i].x == k.left) y[i].x = NONE;
-      // (an id outside the table is `count`, sorted last; NONE is above it)
-      if (sum.mine && y[i].x < a.count) x[i].load(static_cast<const T*>(a.G) + (int64_t)y[i].y * a.ldg + c * V);
-      else x[i].zero();
-    }
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (y[i].x != NONE) sum.add(y[i].x, x[i]);
-  }
-  sum.finish();
+  for (; i < k.n; i += N) sum.template add_rows<N>(ids + i, k.n - i, NONE);
+  sum.template finish<N>(ids);
 }
 
 // The rows of dE of long runs, from the chunks' parts: TX accesses of a row a CTA, JOIN / TX threads an access, whose sums are
 // added in order.
-constexpr int JOIN = 512;
+constexpr int JOIN = 256;
 
 template <typename T, int V>
 __global__ void __launch_bounds__(JOIN) embed_join_kernel(const __grid_constant__ ReduceArgs a, int tx, int64_t slabs) {
@@ -629,13 +700,32 @@ cudaError_t sort_ids(const EmbedArgs& a, uint2* to, uint2* other, uint32_t* coun
   while ((a.count >> bits) != 0) ++bits;  // of 0 .. count
   const int passes = (bits + MAX_BITS - 1) / MAX_BITS;
   s.bits = (bits + passes - 1) / passes;
-  if (a.m <= SMALL) {
-    s.to = to;
-    const int threads = (int)std::min<int64_t>(SMALL_THREADS, (a.m + 63) / 64 * 32);  // two ids a thread, up to 8
-    const size_t smem = ((size_t)RADIX + 32 + (size_t)threads / 32 * RADIX) * 4 + (size_t)a.m * 8;
-    const cudaError_t e = ensure_smem((const void*)sort_small_kernel, smem);
+  if (a.m <= (int64_t)CLUSTER * CLUSTER_THREADS * CLUSTER_ITEMS) {
+    ClusterSort c;
+    c.s = s;
+    c.s.to = to;
+    c.other = other;
+    c.passes = passes;
+    int ctas = 1;
+    while (ctas < CLUSTER && a.m > (int64_t)ctas * CLUSTER_THREADS) ctas *= 2;
+    c.items = (int)((a.m + (int64_t)ctas * CLUSTER_THREADS - 1) / (ctas * CLUSTER_THREADS));
+    const size_t smem = (size_t)CLUSTER_THREADS / 32 * ((size_t)1 << s.bits) * 4;
+    const cudaError_t e = ensure_smem((const void*)sort_cluster_kernel, smem);
     if (e != cudaSuccess) return e;
-    return launch_kernel(sort_small_kernel, dim3(1), (unsigned)threads, smem, st, s, passes);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(CLUSTER_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (see after_previous)
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, sort_cluster_kernel, c);
   }
   // the last pass ends in `to`
   uint2* next = passes % 2 ? to : other;
@@ -682,7 +772,7 @@ fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t s
   // CTAs that zero rows: 32 rows each, fewer where the table is small
   q.zero_rows = (int)std::max<int64_t>(1, std::min<int64_t>(32, a.count / (8 * (int64_t)dev.sm_count)));
   const int64_t zero_ctas = (a.count + q.zero_rows - 1) / q.zero_rows;
-  if (V > 1 && accesses >= BULK_THREADS / 2) {
+  if (V > 1 && accesses >= BULK_THREADS) {
     if constexpr (V > 1) {
       q.shape.slabs = (accesses + BULK_THREADS - 1) / BULK_THREADS;
       q.sum_ctas = chunks * q.shape.slabs;
@@ -693,6 +783,7 @@ fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t s
     }
   } else {
     q.shape = shape_of(accesses, 1);
+    q.shape.groups = std::min(q.shape.groups, GROUPS);
     q.sum_ctas = (chunks * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
     q.ctas = q.sum_ctas + zero_ctas;
     const unsigned threads = (unsigned)((q.shape.tpr * q.shape.groups + 31) / 32 * 32);
@@ -702,7 +793,7 @@ fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t s
     int tx = 1;
     while (tx < 32 && tx < accesses) tx *= 2;
     const int64_t slabs = (accesses + tx - 1) / tx, most = (chunks - 2) * slabs;
-    e = launch_kernel(embed_join_kernel<T, V>, dim3((unsigned)std::min<int64_t>(most, (int64_t)dev.sm_count * 4)), JOIN, 0, st, q, tx, slabs);
+    e = launch_kernel(embed_join_kernel<T, V>, dim3((unsigned)std::min<int64_t>(most, (int64_t)dev.sm_count * 8)), JOIN, 0, st, q, tx, slabs);
   }
   cudaFreeAsync(ws, st);
   if (e == cudaSuccess) return FXTX_OK;
