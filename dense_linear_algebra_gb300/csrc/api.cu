@@ -638,12 +638,12 @@ fxtx_status_t fxtx_device_error(void* stream) {
   const int c = take_multi_device_error();
   const int d = take_product_device_error();
   const int e = take_stats_device_error(), f = take_slope_device_error(), g = take_sum_device_error(), h = take_raw_device_error();
-  const int i = take_embed_device_error();
-  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0 || g < 0 || h < 0 || i < 0) {
+  const int i = take_embed_device_error(), j = take_norm_device_error();
+  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0 || g < 0 || h < 0 || i < 0 || j < 0) {
     cudaGetLastError();
     return FXTX_ERR_CUDA;
   }
-  return (a || b || c || d || e || f || g || h || i) ? FXTX_ERR_TIMEOUT : FXTX_OK;
+  return (a || b || c || d || e || f || g || h || i || j) ? FXTX_ERR_TIMEOUT : FXTX_OK;
 }
 
 const char* fxtx_status_string(fxtx_status_t status) {

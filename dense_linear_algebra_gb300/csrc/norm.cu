@@ -23,9 +23,51 @@
 #include "train.h"
 
 namespace fxtx {
+
+int take_norm_device_error() { return take_device_error(); }
+
 namespace {
 
 constexpr int FWD_THREADS = 256, GRAD_THREADS = 512, LONG_THREADS = 512;
+
+__device__ __forceinline__ uint32_t pair(__nv_bfloat16, float x, float y) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ uint32_t pair(__half, float x, float y) {
+  const __half2 p = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ float2 unpair(__nv_bfloat16, uint32_t v) { return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)); }
+__device__ __forceinline__ float2 unpair(__half, uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// Two values in one register pair, and their operations, an instruction for both.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // V neighbouring entries as they are loaded.
 template <typename T, int V>
@@ -35,15 +77,41 @@ struct Raw {
   __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void values(float* x) const {
-    const T* t = reinterpret_cast<const T*>(&v);
+    const uint32_t t[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = to_f32(t[i]);
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (V == 4) {
+        x[i] = __uint_as_float(t[i]);
+      } else {
+        const float2 y = unpair(T{}, t[i]);
+        x[2 * i] = y.x;
+        x[2 * i + 1] = y.y;
+      }
+    }
+  }
+  __device__ __forceinline__ void pairs(f2* x) const {
+    float y[V];
+    values(y);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) x[i] = pack2(y[2 * i], y[2 * i + 1]);
+  }
+  __device__ __forceinline__ static void store_pairs(T* p, const f2* x) {
+    float y[V];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const float2 v = unpack2(x[i]);
+      y[2 * i] = v.x;
+      y[2 * i + 1] = v.y;
+    }
+    store(p, y);
   }
   __device__ __forceinline__ static void store(T* p, const float* x) {
     uint4 w;
-    T* t = reinterpret_cast<T*>(&w);
-#pragma unroll
-    for (int i = 0; i < V; ++i) t[i] = from_f32<T>(x[i]);
+    if constexpr (V == 4) {
+      w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    } else {  // two at a time, an instruction each
+      w = make_uint4(pair(T{}, x[0], x[1]), pair(T{}, x[2], x[3]), pair(T{}, x[4], x[5]), pair(T{}, x[6], x[7]));
+    }
     *reinterpret_cast<uint4*>(p) = w;
   }
 };
@@ -287,6 +355,282 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) norm_grad_kernel(const __grid
   }
 }
 
+// ------------------------------------------------------------------------------------------------ rows by bulk copies
+// Many rows of several warps each: a group's next rows come to a ring in shared memory, several on their way at a time (held
+// in registers, one: 8192 rows a group in turn left the memory waiting for the sums).
+
+constexpr int RING_THREADS = 512, RING_BYTES = 200 * 1024, MOST_STAGES = 8, MOST_GROUPS = 8;
+
+__device__ __forceinline__ void copy_row(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_addr(dst)), "l"(src),
+               "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// A group's ring: MATS rows (of as many matrices) a stage.
+template <typename T, int MATS>
+struct RowRing {
+  unsigned char* at;   // the group's stages
+  uint64_t* full;
+  uint32_t bytes;      // of a row
+  int stages, mats, s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  __device__ __forceinline__ RowRing(unsigned char* smem, uint64_t* bars, int group, int stages_, int mats_, int64_t n)
+      : bytes((uint32_t)(n * sizeof(T))), stages(stages_), mats(mats_) {
+    at = smem + (size_t)group * stages * mats * bytes;
+    full = bars + group * MOST_STAGES;
+  }
+  __device__ __forceinline__ const T* row(int mat) const { return reinterpret_cast<const T*>(at + (size_t)(s * mats + mat) * bytes); }
+  // one thread's: the rows at p[0 .. mats - 1] to stage x
+  __device__ __forceinline__ void fill(int x, const void* const (&p)[MATS]) {
+    mbar_arrive_expect_tx(&full[x], bytes * (uint32_t)mats);
+#pragma unroll
+    for (int i = 0; i < MATS; ++i)
+      if (i < mats) copy_row(at + (size_t)(x * mats + i) * bytes, p[i], bytes, &full[x]);
+  }
+  __device__ __forceinline__ void wait() { ok = ok && mbar_wait_bounded(&full[s], phase); }
+  __device__ __forceinline__ void next() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// A thread's accesses of a row in shared memory, and of w or b (`none` where there is no such vector).
+template <typename T, int V, int CH>
+__device__ __forceinline__ void load_pairs(const RowOf<T, V, CH>& r, const T* row, f2* x) {
+  Raw<T, V> raw[CH];
+  r.load(row, 0, 1, 0, raw);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) raw[i].pairs(x + i * V / 2);
+}
+template <typename T, int V, int CH>
+__device__ __forceinline__ void load_vector(const RowOf<T, V, CH>& r, const void* p, float none, f2* x) {
+  if (p) {
+    load_pairs<T, V, CH>(r, static_cast<const T*>(p), x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH * V / 2; ++i) x[i] = pack2(none, none);
+  }
+}
+
+template <typename T, int CH>
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid_constant__ NormArgs a, const RowShape shape, int stages) {
+  constexpr int V = 16 / sizeof(T);
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t full[MOST_GROUPS * MOST_STAGES];
+  __shared__ float2 red[2][32];
+  __shared__ float s_n[32];
+  const int tpr = shape.tpr, group = threadIdx.x / tpr;
+  const RowOf<T, V, CH> r((int)threadIdx.x % tpr, tpr, a.n);
+  RowRing<T, 1> ring(smem, full, group, stages, 1, a.n);
+  // entries of the thread, of warp y of the row, and of the thread's warp
+  const int accesses = (int)(a.n / V);
+  auto n_of = [&](int y) {  // whole accesses of 32 threads, and a last one of fewer
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) n += min(32, max(0, accesses - y * 32 - i * tpr));
+    return (float)(n * V);
+  };
+  float n_own = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) n_own += r.has(i) ? (float)V : 0.f;
+  const float over_own = n_own > 0.f ? 1.f / n_own : 0.f, n_warp = n_of(r.t >> 5), over_warp = n_warp > 0.f ? 1.f / n_warp : 0.f;
+  if ((threadIdx.x & 31) == 0) s_n[threadIdx.x >> 5] = n_warp;
+  int parity = 0;
+  if (r.t == 0) {
+    for (int x = 0; x < stages; ++x) mbar_init(&ring.full[x], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const float over = 1.f / (float)a.n;
+  const int64_t step = (int64_t)gridDim.x * shape.groups;
+  int64_t row = (int64_t)blockIdx.x * shape.groups + group;
+  after_previous();
+  auto fill = [&](int x, int64_t i) {
+    const void* p[1] = {static_cast<const T*>(a.X) + i * a.ldx};
+    if (i < a.m) ring.fill(x, p);
+  };
+  if (r.t == 0)
+    for (int x = 0; x < stages; ++x) fill(x, row + x * step);
+  constexpr int P = CH * V / 2;  // pairs
+  f2 w[P], b[P];
+  load_vector<T, V, CH>(r, a.w, 1.f, w);
+  load_vector<T, V, CH>(r, a.b, 0.f, b);
+  for (; row < a.m; row += step) {
+    ring.wait();
+    f2 x[P];
+    load_pairs<T, V, CH>(r, ring.row(0), x);
+    // the thread's own mean and squares about it, the warp's from those, the row's from the warps' (one barrier a row)
+    f2 sum = 0, squares = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum = add2(sum, x[i]);
+    const float own = (unpack2(sum).x + unpack2(sum).y) * over_own;
+    const f2 off = pack2(-own, -own);
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (r.has(i)) {
+#pragma unroll
+        for (int q = 0; q < V / 2; ++q) {
+          const f2 v = add2(x[i * V / 2 + q], off);
+          squares = fma2(v, v, squares);
+        }
+      }
+    const float warp_mean = group_sum<32>(own * n_own) * over_warp, d = own - warp_mean;
+    const float warp_square = group_sum<32>(fmaf(n_own * d, d, unpack2(squares).x + unpack2(squares).y));
+    float2* buf = red[parity];
+    parity ^= 1;
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(warp_mean, warp_square);
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+    // (every thread of the group has read the row)
+    if (r.t == 0) fill(ring.s, row + stages * step);
+    ring.next();
+    const int w0 = group * (tpr >> 5), wn = tpr >> 5;
+    float mean = 0.f, square = 0.f;
+    for (int y = 0; y < wn; ++y) mean = fmaf(buf[w0 + y].x, s_n[w0 + y], mean);
+    mean *= over;
+    for (int y = 0; y < wn; ++y) {
+      const float2 z = buf[w0 + y];
+      square += fmaf(s_n[w0 + y] * (z.x - mean), z.x - mean, z.y);
+    }
+    const float rstd = __frsqrt_rn(fmaf(square, over, a.eps));
+    if (!ring.ok) continue;  // FXTX_ERR_TIMEOUT is raised
+    if (r.t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+    const f2 minus = pack2(-mean, -mean), scale = pack2(rstd, rstd);
+#pragma unroll
+    for (int i = 0; i < P; ++i) x[i] = fma2(mul2(add2(x[i], minus), scale), w[i], b[i]);
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (r.has(i)) Raw<T, V>::store_pairs(out + r.at(i), x + i * V / 2);
+  }
+}
+
+// A thread's column sums, over the groups in turn, to the CTA's part (or dw and db, of one CTA).
+template <typename T, int V, int CH>
+__device__ __forceinline__ void store_columns(const NormArgs& a, const RowOf<T, V, CH>& r, int group, int groups, const float* dw,
+                                              const float* db, float* cols) {
+  constexpr int E = CH * V;
+  for (int y = 0; y < groups; ++y) {
+    __syncthreads();
+    if (group != y) continue;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float *p = cols + e * r.tpr + r.t, *q = p + E * r.tpr;
+      *p = y > 0 ? *p + dw[e] : dw[e];
+      *q = y > 0 ? *q + db[e] : db[e];
+    }
+  }
+  __syncthreads();
+  for (int64_t j = threadIdx.x; j < a.n; j += blockDim.x) {
+    const int c = (int)(j / V), e = c / r.tpr * V + (int)(j % V);
+    const float x = cols[e * r.tpr + c % r.tpr], y = cols[(E + e) * r.tpr + c % r.tpr];
+    if (gridDim.x == 1) {
+      if (a.DW) static_cast<T*>(a.DW)[j] = from_f32<T>(x);
+      if (a.DB) static_cast<T*>(a.DB)[j] = from_f32<T>(y);
+    } else {
+      float* p = a.part + (int64_t)blockIdx.x * 2 * a.n + j;
+      p[0] = x;
+      p[a.n] = y;
+    }
+  }
+}
+
+template <typename T, int CH, bool SUMS>
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const __grid_constant__ NormArgs a, const RowShape shape, int stages) {
+  constexpr int V = 16 / sizeof(T), E = CH * V;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t full[MOST_GROUPS * MOST_STAGES];
+  __shared__ float2 red[2][32];
+  const int tpr = shape.tpr, group = threadIdx.x / tpr;
+  const RowOf<T, V, CH> r((int)threadIdx.x % tpr, tpr, a.n);
+  RowSum<true> sum{red, tpr, group};
+  RowRing<T, 3> ring(smem, full, group, stages, a.R ? 3 : 2, a.n);
+  if (r.t == 0) {
+    for (int x = 0; x < stages; ++x) mbar_init(&ring.full[x], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const float over = 1.f / (float)a.n;
+  const int64_t step = (int64_t)gridDim.x * shape.groups;
+  int64_t row = (int64_t)blockIdx.x * shape.groups + group;
+  after_previous();
+  auto fill = [&](int x, int64_t i) {
+    const void* p[3] = {static_cast<const T*>(a.X) + i * a.ldx, static_cast<const T*>(a.G) + i * a.ldg, static_cast<const T*>(a.R) + i * a.ldr};
+    if (i < a.m) ring.fill(x, p);
+  };
+  if (r.t == 0)
+    for (int x = 0; x < stages; ++x) fill(x, row + x * step);
+  constexpr int P = E / 2;  // pairs
+  f2 dw[SUMS ? P : 1] = {}, db[SUMS ? P : 1] = {}, w[P];
+  load_vector<T, V, CH>(r, a.w, 1.f, w);
+  float mean_n = row < a.m ? a.mean_in[row] : 0.f, rstd_n = row < a.m ? a.rstd_in[row] : 0.f;
+  for (; row < a.m; row += step) {
+    const float mean = mean_n, rstd = rstd_n;
+    if (row + step < a.m) {
+      mean_n = a.mean_in[row + step];
+      rstd_n = a.rstd_in[row + step];
+    }
+    ring.wait();
+    f2 u[P], h[P];
+    Raw<T, V> res[CH];
+    load_pairs<T, V, CH>(r, ring.row(0), u);
+    load_pairs<T, V, CH>(r, ring.row(1), h);
+    if (a.R) r.load(ring.row(2), 0, 1, 0, res);
+    const f2 minus = pack2(-mean, -mean), scale = pack2(rstd, rstd);
+    f2 s1 = 0, s2 = 0;
+    // (beyond the row's end g is zero, and u counts for nothing unless the whole row is no number)
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      u[i] = mul2(add2(u[i], minus), scale);
+      if constexpr (SUMS) {
+        dw[i] = fma2(h[i], u[i], dw[i]);
+        db[i] = add2(db[i], h[i]);
+      }
+      h[i] = mul2(h[i], w[i]);
+      s1 = add2(s1, h[i]);
+      s2 = fma2(h[i], u[i], s2);
+    }
+    const float2 s = sum(make_float2(unpack2(s1).x + unpack2(s1).y, unpack2(s2).x + unpack2(s2).y));
+    if (r.t == 0) fill(ring.s, row + stages * step);
+    ring.next();
+    if (!ring.ok || !a.DX) continue;
+    const float c1 = -s.x * over, c2 = -s.y * over;
+    const f2 d1 = pack2(c1, c1), d2 = pack2(c2, c2);
+    T* out = static_cast<T*>(a.DX) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (!r.has(i)) continue;
+      f2 v[V / 2], y[V / 2];
+      if (a.R) {
+        res[i].pairs(y);
+      } else {
+#pragma unroll
+        for (int q = 0; q < V / 2; ++q) y[q] = 0;
+      }
+#pragma unroll
+      for (int q = 0; q < V / 2; ++q) v[q] = fma2(fma2(u[i * V / 2 + q], d2, add2(h[i * V / 2 + q], d1)), scale, y[q]);
+      Raw<T, V>::store_pairs(out + r.at(i), v);
+    }
+  }
+  if constexpr (SUMS) {
+    float x[E], y[E];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      x[2 * i] = unpack2(dw[i]).x;
+      x[2 * i + 1] = unpack2(dw[i]).y;
+      y[2 * i] = unpack2(db[i]).x;
+      y[2 * i + 1] = unpack2(db[i]).y;
+    }
+    store_columns<T, V, CH>(a, r, group, shape.groups, x, y, reinterpret_cast<float*>(smem));
+  }
+}
+
 // dw and db from `parts` CTAs' sums, in order: 32 columns a CTA, 8 threads a column.
 template <typename T>
 __global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormArgs a, int64_t parts) {
@@ -522,6 +866,23 @@ cudaError_t forward_ch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st
   return s.tpr <= 32 ? launch_forward<T, V, CH, false>(a, s, dev, st) : launch_forward<T, V, CH, true>(a, s, dev, st);
 }
 
+// A ring's stages for rows of `bytes` and `mats` matrices; fewer than two: rows do not go that way.
+int stages_of(const RowShape& s, int64_t bytes, int mats) {
+  return (int)std::min<int64_t>(MOST_STAGES, RING_BYTES / (s.groups * mats * bytes));
+}
+// Rows of several warps, enough of them to keep the rings of all SMs full.
+bool ring_rows(const RowShape& s, int64_t m, const DeviceInfo& dev) {
+  return s.tpr > 32 && s.groups <= MOST_GROUPS && s.tpr <= RING_THREADS && m >= 4 * (int64_t)dev.sm_count * s.groups;
+}
+
+template <typename T, int CH>
+cudaError_t launch_ring(const NormArgs& a, const RowShape& s, int stages, const DeviceInfo& dev, cudaStream_t st) {
+  const size_t smem = (size_t)s.groups * stages * a.n * sizeof(T);
+  const cudaError_t e = ensure_smem((const void*)norm_ring_kernel<T, CH>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(norm_ring_kernel<T, CH>, dim3((unsigned)dev.sm_count), (unsigned)(s.tpr * s.groups), smem, st, a, s, stages);
+}
+
 template <typename T, int V>
 cudaError_t forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   constexpr int MOST = V == 1 ? 16 : 4;
@@ -530,6 +891,11 @@ cudaError_t forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
     return launch_kernel(norm_long_kernel<T, V>, dim3((unsigned)std::min<int64_t>(a.m, (int64_t)dev.sm_count * 4)), LONG_THREADS, 0,
                          st, a);
   if (accesses <= 32) return forward_ch<T, V, 1>(a, dev, st);
+  if constexpr (V > 1) {
+    const RowShape s = shape_of(accesses, MOST, RING_THREADS);
+    const int stages = stages_of(s, a.n * (int64_t)sizeof(T), 1);
+    if (stages >= 2 && ring_rows(s, a.m, dev)) return launch_ring<T, MOST>(a, s, stages, dev, st);
+  }
   return forward_ch<T, V, MOST>(a, dev, st);
 }
 
@@ -583,6 +949,27 @@ fxtx_status_t long_grad(NormArgs a, const DeviceInfo& dev, cudaStream_t st) {
   return FXTX_ERR_CUDA;
 }
 
+template <typename T, int CH, bool SUMS>
+fxtx_status_t launch_grad_ring(NormArgs a, const RowShape& s, int stages, const DeviceInfo& dev, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  const size_t sums = SUMS ? (size_t)2 * CH * V * s.tpr * 4 : 0;
+  const size_t smem = std::max((size_t)s.groups * stages * (a.R ? 3 : 2) * a.n * sizeof(T), sums);
+  cudaError_t e = ensure_smem((const void*)norm_grad_ring_kernel<T, CH, SUMS>, smem);
+  if (SUMS && e == cudaSuccess) {
+    const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)dev.sm_count * 2 * a.n * 4, st);
+    if (r != FXTX_OK) return r;
+  }
+  if (e == cudaSuccess)
+    e = launch_kernel(norm_grad_ring_kernel<T, CH, SUMS>, dim3((unsigned)dev.sm_count), (unsigned)(s.tpr * s.groups), smem, st, a, s, stages);
+  if (a.part) {
+    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 256, 0, st, a, (int64_t)dev.sm_count);
+    cudaFreeAsync(a.part, st);
+  }
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
 template <typename T, int V, int CH>
 fxtx_status_t grad_ch(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   const RowShape s = shape_of(a.n / V, CH, GRAD_THREADS);
@@ -598,6 +985,12 @@ fxtx_status_t grad(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   const int64_t accesses = a.n / V;
   if (accesses > (int64_t)MOST * GRAD_THREADS) return long_grad<T, V>(a, dev, st);
   if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
+  if constexpr (V > 1) {
+    const RowShape s = shape_of(accesses, MOST, RING_THREADS);
+    const int stages = stages_of(s, a.n * (int64_t)sizeof(T), a.R ? 3 : 2);
+    if (stages >= 2 && ring_rows(s, a.m, dev))
+      return a.DW || a.DB ? launch_grad_ring<T, MOST, true>(a, s, stages, dev, st) : launch_grad_ring<T, MOST, false>(a, s, stages, dev, st);
+  }
   return grad_ch<T, V, MOST>(a, dev, st);
 }
 

@@ -30,6 +30,7 @@ struct NormArgs {
   void *DW = nullptr, *DB = nullptr;
   float* part = nullptr;  // [CTAs][2][n] column sums
 };
+int take_norm_device_error();
 fxtx_status_t run_norm(fxtx_type_t type, const NormArgs& a, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_norm_grad(fxtx_type_t type, const NormArgs& a, const DeviceInfo& dev, cudaStream_t st);
 

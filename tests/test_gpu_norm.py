@@ -140,11 +140,19 @@ def test_rows(m, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n", [(5001, 1160), (6000, 2056), (3000, 4096), (1300, 5000), (1300, 8192), (700, 16384), (2500, 4104)])
+def test_many_long_rows(m, n, dtype):
+    """Rows that come by bulk copies."""
+    check_forward(m, n, dtype, shift=3.0)
+    check_grad(m, n, dtype, residual=n % 16 == 0, need=(True, n != 2056, n != 2056))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("pad,offset", [(8, 0), (16, 8), (1, 0), (5, 3)])
-@pytest.mark.parametrize("n", [32, 301, 1024, 20_000])
-def test_column_slices(n, pad, offset, dtype):
-    check_forward(9, n, dtype, pad=pad, offset=offset)
-    check_grad(9, n, dtype, pad=pad, offset=offset)
+@pytest.mark.parametrize("m,n", [(9, 32), (9, 301), (9, 1024), (9, 20_000), (3000, 2048)])
+def test_column_slices(m, n, pad, offset, dtype):
+    check_forward(m, n, dtype, pad=pad, offset=offset)
+    check_grad(m, n, dtype, pad=pad, offset=offset)
 
 
 @pytest.mark.parametrize("dtype", TYPES)
