@@ -631,24 +631,200 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
   }
 }
 
-// dw and db from `parts` CTAs' sums, in order: 32 columns a CTA, 8 threads a column.
+// Rows of at most 32 accesses of 16 bytes, without gaps between them: a row lies over `tpr` neighbouring lanes, an access
+// each, and each warp has a ring of its own, of tiles of about 2 KB a matrix, several on their way at a time (with a row ahead in
+// registers 1,000,000 x 32 float32 took 90 us).
+constexpr int SHORT_THREADS = 512, SHORT_TILE = 2048, SHORT_BYTES = 192 * 1024;  // of a tile at most, of all rings
+
+template <typename T, bool SUMS>
+__global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const __grid_constant__ NormArgs a, const int tpr, const int rows,
+                                                                          const int slot, const int stages) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, WARPS = SHORT_THREADS / 32;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t s_full[WARPS][MOST_STAGES];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / tpr, t = lane % tpr, groups = 32 / tpr, accesses = (int)(a.n / V);
+  const bool has = t < accesses;
+  const int mats = a.R ? 3 : 2;
+  const float over = 1.f / (float)a.n;
+  unsigned char* at = smem + (size_t)warp * stages * mats * slot;
+  uint64_t* full = s_full[warp];
+  if (lane == 0) {
+    for (int x = 0; x < stages; ++x) mbar_init(&full[x], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  after_previous();
+  const int64_t tiles = (a.m + rows - 1) / rows, step = (int64_t)gridDim.x * WARPS;
+  int64_t tile = (int64_t)blockIdx.x * WARPS + warp;
+  auto fill = [&](int x, int64_t i) {
+    if (i >= tiles) return;
+    const int64_t first = i * rows * a.n;
+    const uint32_t bytes = (uint32_t)(min((int64_t)rows, a.m - i * rows) * accesses * 16);
+    unsigned char* to = at + (size_t)x * mats * slot;
+    mbar_arrive_expect_tx(&full[x], bytes * (uint32_t)mats);
+    copy_row(to, static_cast<const T*>(a.X) + first, bytes, &full[x]);
+    copy_row(to + slot, static_cast<const T*>(a.G) + first, bytes, &full[x]);
+    if (a.R) copy_row(to + 2 * slot, static_cast<const T*>(a.R) + first, bytes, &full[x]);
+  };
+  if (lane == 0)
+    for (int x = 0; x < stages; ++x) fill(x, tile + x * step);
+  f2 dw[SUMS ? P : 1] = {}, db[SUMS ? P : 1] = {}, w[P];
+  {
+    Raw<T, V> raw;
+    raw.zero();
+    if (a.w && has) raw.load(static_cast<const T*>(a.w) + t * V);
+    raw.pairs(w);
+    if (!a.w) {
+#pragma unroll
+      for (int q = 0; q < P; ++q) w[q] = pack2(1.f, 1.f);
+    }
+  }
+  bool ok = true;
+  int s = 0;
+  uint32_t phase = 0;
+  // the statistics of a tile's rows (32 at most), a row a lane, a tile ahead
+  float mean_n = 0.f, rstd_n = 0.f;
+  auto fetch = [&](int64_t i) {
+    const int64_t r = i * rows + lane;
+    const bool in = lane < rows && r < a.m;
+    mean_n = in ? a.mean_in[r] : 0.f;
+    rstd_n = in ? a.rstd_in[r] : 0.f;
+  };
+  fetch(tile);
+  for (; tile < tiles; tile += step) {
+    const int64_t row0 = tile * rows;
+    const float mean_t = mean_n, rstd_t = rstd_n;
+    fetch(tile + step);
+    const int here = (int)min((int64_t)rows, a.m - row0);  // the tile's rows
+    ok = __all_sync(FULL_MASK, ok && mbar_wait_bounded(&full[s], phase));
+    if (!ok) break;  // FXTX_ERR_TIMEOUT is raised
+    const unsigned char* x_at = at + (size_t)s * mats * slot + t * 16;
+#pragma unroll 1
+    for (int r0 = 0; r0 < here; r0 += 2 * groups) {
+      f2 u[2][P], h[2][P], y[2][P];
+      float scale[2], s1[2], s2[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + i * groups + group;
+        const bool in = r < here;
+        Raw<T, V> x, g, res;
+        x.zero();
+        g.zero();
+        res.zero();
+        const float mean = __shfl_sync(FULL_MASK, mean_t, r & 31);
+        scale[i] = __shfl_sync(FULL_MASK, rstd_t, r & 31);
+        if (in && has) {
+          const unsigned char* p = x_at + r * accesses * 16;
+          x.load(reinterpret_cast<const T*>(p));
+          g.load(reinterpret_cast<const T*>(p + slot));
+          if (a.R) res.load(reinterpret_cast<const T*>(p + 2 * slot));
+        }
+        x.pairs(u[i]);
+        g.pairs(h[i]);
+        res.pairs(y[i]);
+        const f2 minus = pack2(-mean, -mean), sc = pack2(scale[i], scale[i]);
+        f2 p1 = 0, p2 = 0;
+        // (beyond the row's end g is zero, and u counts for nothing unless the whole row is no number)
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+          u[i][q] = mul2(add2(u[i][q], minus), sc);
+          if constexpr (SUMS) {
+            dw[q] = fma2(h[i][q], u[i][q], dw[q]);
+            db[q] = add2(db[q], h[i][q]);
+          }
+          h[i][q] = mul2(h[i][q], w[q]);
+          p1 = add2(p1, h[i][q]);
+          p2 = fma2(h[i][q], u[i][q], p2);
+        }
+        s1[i] = unpack2(p1).x + unpack2(p1).y;
+        s2[i] = unpack2(p2).x + unpack2(p2).y;
+      }
+      if (!a.DX) continue;
+      for (int o = tpr >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s1[i] += shfl_xor(s1[i], o);
+          s2[i] += shfl_xor(s2[i], o);
+        }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = r0 + i * groups + group;
+        if (r >= here || !has) continue;
+        const float c1 = -s1[i] * over, c2 = -s2[i] * over;
+        const f2 d1 = pack2(c1, c1), d2 = pack2(c2, c2), sc = pack2(scale[i], scale[i]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) y[i][q] = fma2(fma2(u[i][q], d2, add2(h[i][q], d1)), sc, y[i][q]);
+        Raw<T, V>::store_pairs(static_cast<T*>(a.DX) + (row0 + r) * a.lddx + t * V, y[i]);
+      }
+    }
+    __syncwarp();  // the tile has been read
+    if (lane == 0) fill(s, tile + stages * step);
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  if constexpr (SUMS) {
+    // a warp's by exchange, then warp after warp in shared memory: [2][V][tpr]
+    __shared__ float cols[2 * V * 32];
+    float x[V], y[V];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      x[2 * q] = unpack2(dw[q]).x;
+      x[2 * q + 1] = unpack2(dw[q]).y;
+      y[2 * q] = unpack2(db[q]).x;
+      y[2 * q + 1] = unpack2(db[q]).y;
+    }
+    for (int o = tpr; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x[e] += shfl_xor(x[e], o);
+        y[e] += shfl_xor(y[e], o);
+      }
+    for (int z = 0; z < SHORT_THREADS / 32; ++z) {
+      __syncthreads();
+      if ((int)(threadIdx.x >> 5) != z || (int)(threadIdx.x & 31) >= tpr) continue;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float *p = cols + e * tpr + t, *q = p + V * tpr;
+        *p = z > 0 ? *p + x[e] : x[e];
+        *q = z > 0 ? *q + y[e] : y[e];
+      }
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < a.n; j += SHORT_THREADS) {
+      const float p = cols[j % V * tpr + j / V], q = cols[(V + j % V) * tpr + j / V];
+      if (gridDim.x == 1) {
+        if (a.DW) static_cast<T*>(a.DW)[j] = from_f32<T>(p);
+        if (a.DB) static_cast<T*>(a.DB)[j] = from_f32<T>(q);
+      } else {
+        a.part[((int64_t)blockIdx.x * 2) * a.n + j] = p;
+        a.part[((int64_t)blockIdx.x * 2 + 1) * a.n + j] = q;
+      }
+    }
+  }
+}
+
+// dw and db from `parts` CTAs' sums, in order: 32 columns a CTA, 32 threads a column.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_join_kernel(const __grid_constant__ NormArgs a, int64_t parts) {
-  __shared__ float part[8][32];
+__global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__ NormArgs a, int64_t parts) {
+  __shared__ float part[32][33];
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int64_t j = (int64_t)blockIdx.x * 32 + x;
   float s = 0.f;
   after_previous();
   if (j < 2 * a.n) {
 #pragma unroll 4
-    for (int64_t p = y; p < parts; p += 8) s += a.part[p * 2 * a.n + j];
+    for (int64_t p = y; p < parts; p += 32) s += a.part[p * 2 * a.n + j];
   }
   part[y][x] = s;
   __syncthreads();
-  if (y != 0 || j >= 2 * a.n) return;
-  for (int i = 1; i < 8; ++i) s += part[i][x];
-  T* to = static_cast<T*>(j < a.n ? a.DW : a.DB);
-  if (to) to[j < a.n ? j : j - a.n] = from_f32<T>(s);
+  // a warp a column
+  s = group_sum<32>(part[x][y]);
+  const int64_t c = (int64_t)blockIdx.x * 32 + y;
+  if (x != 0 || c >= 2 * a.n) return;
+  T* to = static_cast<T*>(c < a.n ? a.DW : a.DB);
+  if (to) to[c < a.n ? c : c - a.n] = from_f32<T>(s);
 }
 
 // A CTA's sum of two doubles, the same in every thread.
@@ -916,7 +1092,7 @@ fxtx_status_t launch_grad(NormArgs a, const RowShape& s, const DeviceInfo& dev, 
   }
   e = launch_kernel(norm_grad_kernel<T, V, CH, BIG, SUMS>, dim3((unsigned)grid), threads, smem, st, a, s);
   if (a.part) {
-    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 256, 0, st, a, grid);
+    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 1024, 0, st, a, grid);
     cudaFreeAsync(a.part, st);
   }
   if (e == cudaSuccess) return FXTX_OK;
@@ -942,7 +1118,7 @@ fxtx_status_t long_grad(NormArgs a, const DeviceInfo& dev, cudaStream_t st) {
                       st, a, means);
   if (e == cudaSuccess)
     e = launch_kernel(norm_long_grad_kernel<T, V>, dim3((unsigned)(slabs * parts)), 256, 0, st, a, (const float2*)means, slabs, rows);
-  if (e == cudaSuccess && sums) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 256, 0, st, a, parts);
+  if (e == cudaSuccess && sums) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 1024, 0, st, a, parts);
   cudaFreeAsync(ws, st);
   if (e == cudaSuccess) return FXTX_OK;
   cudaGetLastError();
@@ -962,7 +1138,31 @@ fxtx_status_t launch_grad_ring(NormArgs a, const RowShape& s, int stages, const 
   if (e == cudaSuccess)
     e = launch_kernel(norm_grad_ring_kernel<T, CH, SUMS>, dim3((unsigned)dev.sm_count), (unsigned)(s.tpr * s.groups), smem, st, a, s, stages);
   if (a.part) {
-    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 256, 0, st, a, (int64_t)dev.sm_count);
+    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 1024, 0, st, a, (int64_t)dev.sm_count);
+    cudaFreeAsync(a.part, st);
+  }
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+
+template <typename T, bool SUMS>
+fxtx_status_t launch_short(NormArgs a, const DeviceInfo& dev, cudaStream_t st) {
+  const int accesses = (int)(a.n / (16 / (int)sizeof(T)));
+  const RowShape s = shape_of(accesses, 1, 32);
+  const int groups = 32 / s.tpr, rows = std::min(32, std::max(groups, SHORT_TILE / (accesses * 16) / groups * groups));
+  const int slot = (rows * accesses * 16 + 127) / 128 * 128, each = SHORT_THREADS / 32 * (a.R ? 3 : 2) * slot;
+  const int stages = std::min(MOST_STAGES, SHORT_BYTES / each);
+  const size_t smem = (size_t)each * stages;
+  cudaError_t e = ensure_smem((const void*)norm_grad_short_kernel<T, SUMS>, smem);
+  const int64_t tiles = (a.m + rows - 1) / rows, grid = std::min<int64_t>((tiles + SHORT_THREADS / 32 - 1) / (SHORT_THREADS / 32), dev.sm_count);
+  if (SUMS && e == cudaSuccess && grid > 1) {
+    const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)grid * 2 * a.n * 4, st);
+    if (r != FXTX_OK) return r;
+  }
+  if (e == cudaSuccess) e = launch_kernel(norm_grad_short_kernel<T, SUMS>, dim3((unsigned)grid), SHORT_THREADS, smem, st, a, s.tpr, rows, slot, stages);
+  if (a.part) {
+    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 1024, 0, st, a, grid);
     cudaFreeAsync(a.part, st);
   }
   if (e == cudaSuccess) return FXTX_OK;
@@ -984,12 +1184,17 @@ fxtx_status_t grad(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   constexpr int MOST = 16 / V;  // 16 entries a thread: with their sums, weights and the next row's they fill its registers
   const int64_t accesses = a.n / V;
   if (accesses > (int64_t)MOST * GRAD_THREADS) return long_grad<T, V>(a, dev, st);
-  if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
   if constexpr (V > 1) {
+    // (of fewer rows no warp has a second tile)
+    if (accesses <= 32 && a.m * accesses >= (int64_t)dev.sm_count * SHORT_THREADS * 4 && a.ldx == a.n && a.ldg == a.n && (!a.R || a.ldr == a.n))
+      return a.DW || a.DB ? launch_short<T, true>(a, dev, st) : launch_short<T, false>(a, dev, st);
+    if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
     const RowShape s = shape_of(accesses, MOST, RING_THREADS);
     const int stages = stages_of(s, a.n * (int64_t)sizeof(T), a.R ? 3 : 2);
     if (stages >= 2 && ring_rows(s, a.m, dev))
       return a.DW || a.DB ? launch_grad_ring<T, MOST, true>(a, s, stages, dev, st) : launch_grad_ring<T, MOST, false>(a, s, stages, dev, st);
+  } else {
+    if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
   }
   return grad_ch<T, V, MOST>(a, dev, st);
 }

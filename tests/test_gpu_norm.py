@@ -140,6 +140,13 @@ def test_rows(m, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n", [(400_001, 8), (200_003, 16), (100_001, 40), (100_003, 64), (50_001, 104), (30_011, 128), (20_003, 232)])
+def test_many_short_rows(m, n, dtype):
+    """Tiles of rows that come by bulk copies, the last one short."""
+    check_grad(m, n, dtype, residual=m % 4 == 3, affine=n != 64, need=(True, n != 40, n != 40))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m,n", [(5001, 1160), (6000, 2056), (3000, 4096), (1300, 5000), (1300, 8192), (700, 16384), (2500, 4104)])
 def test_many_long_rows(m, n, dtype):
     """Rows that come by bulk copies."""
