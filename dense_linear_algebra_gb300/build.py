@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libfusedxtx.so")
 SOURCES = ["api.cu", "dense.cu", "csr.cu", "multi.cu", "multi_tc.cu", "split.cu", "plan.cpp", "tmap.cpp",
            "tune.cpp", "noalloc.cu", "layers_api.cu", "adamw.cu",
            "linear.cu", "slope.cu", "product_tc.cu", "thin.cu", "few.cu", "norm.cu", "embed.cu",
-           "loss.cu", "loss_raw.cu", "loss_stats.cu", "loss_slope.cu", "loss_sum.cu", "thin_loss.cu"]
+           "loss.cu", "loss_raw.cu", "loss_stats.cu", "loss_slope.cu", "loss_sum.cu", "thin_loss.cu", "thin_loss_f32.cu"]
 HEADERS = ["act.cuh", "common.cuh", "host.h", "kernels.h", "layers.h", "linear.h", "loss.h", "multi.h", "plan.h",
            "product.cuh", "product_split.cuh", "product_tc.cuh", "tc.cuh", "thin.cuh", "tmap.h",
            "train.h", "tune.h"]

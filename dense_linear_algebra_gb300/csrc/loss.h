@@ -83,6 +83,11 @@ fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceI
 fxtx_status_t run_thin_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_thin_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
+// float32 of at most 16 classes and 64 features, on the CUDA cores.
+bool tall_loss_shape(const LayerArgs& l);
+fxtx_status_t run_tall_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
+fxtx_status_t run_tall_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
+
 // scales[0] = a power of two that brings |gain| max |g| to 2^14 .. 2^15, scales[1] its inverse (1 and 1 where that is zero
 // or not finite).
 cudaError_t launch_scales(const float* g, int64_t m, float gain, float* scales, cudaStream_t st);
