@@ -1079,7 +1079,8 @@ template <typename T, int V, int CH, bool BIG, bool SUMS>
 fxtx_status_t launch_grad(NormArgs a, const RowShape& s, const DeviceInfo& dev, cudaStream_t st) {
   const int threads = (s.tpr * s.groups + 31) / 32 * 32;
   const size_t smem = SUMS ? (size_t)2 * CH * V * s.tpr * 4 : 0;
-  cudaError_t e = ensure_smem((const void*)norm_grad_kernel<T, V, CH, BIG, SUMS>, smem);
+  // (its static shared memory counts too: 48 KB of dynamic alone do not fit without the attribute)
+  cudaError_t e = ensure_smem((const void*)norm_grad_kernel<T, V, CH, BIG, SUMS>, smem + 1024);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return FXTX_ERR_CUDA;

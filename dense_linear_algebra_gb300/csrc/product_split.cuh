@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
   } else if (warp == 1) {
     if (elect_one()) {
       bool more = true;
-      ok = issue_products<1, C, PL, LONG, PL == 3>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
+      ok = issue_products<1, C, PL, LONG, PL == 3, CHUNK<0>>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& f0, int& f1) {
         f0 = k0;
         f1 = k1;
         const bool m = more;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(SPLIT_THREADS, SplitCfg<BN, PL>::CTAS)
 #pragma unroll
       for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
       int acc = 0;
-      for (int kb = k0; kb < k1; kb += CHUNK, ++acc) {
+      for (int kb = k0; kb < k1; kb += CHUNK<0>, ++acc) {
         if (!(ok = warp_wait(&tfull[acc & 1], (uint32_t)((acc >> 1) & 1), abort_word))) break;
         tc_fence_after();
         if (mine) add_columns<C::COLS>(t + (uint32_t)((acc & 1) * BN), sum);

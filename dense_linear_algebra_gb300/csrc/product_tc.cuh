@@ -31,7 +31,10 @@ namespace fxtx {
 namespace {
 
 constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
-constexpr int CHUNK = 2;          // stages a sum stays in tensor memory (float32)
+// Stages of 64 of kk that a float32 sum stays in tensor memory: two, one for logits, whose error is that of their exponentials
+// (2-norm error of 2048^3: 6e-7, 1.3e-7 and 19 % more time).
+template <int MODE>
+constexpr int CHUNK = MODE == 1 || MODE == 2 ? 1 : 2;
 constexpr int FOLD = 8192;        // of kk that a piece of a sum covers (16 bits)
 constexpr int LOGIT_FOLD = 1024;  // of sums that are not rounded to 16 bits
 
@@ -213,7 +216,7 @@ struct Turns {
 
 // The loop of a CTA's products over a ring of stages: one lane's. `tile(k0, k1)` gives the next range of
 // stages of kk, false after the last.
-template <int CG, class C, int PL, bool LONG, bool REGS, typename F>
+template <int CG, class C, int PL, bool LONG, bool REGS, int PIECE, typename F>
 __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* smem, uint64_t* full, uint64_t* empty,
                                                uint64_t* tfull, uint64_t* tempty, uint32_t tmem, int bn,
                                                volatile int* abort_word, F tile) {
@@ -228,7 +231,7 @@ __device__ __forceinline__ bool issue_products(const TcArgs& a, unsigned char* s
     for (int kb = k0; kb < k1; ++kb) {
       const bool fresh = left == 0;
       if (fresh) {
-        left = PL == 3 ? min(CHUNK, k1 - kb) : LONG ? min(a.fold, k1 - kb) : k1 - kb;
+        left = PL == 3 ? min(PIECE, k1 - kb) : LONG ? min(a.fold, k1 - kb) : k1 - kb;
         if (!tc_wait(&tempty[acc.s], acc.parity() ^ 1u, abort_word)) return false;
       }
       if (!tc_wait(&full[ring.s], ring.phase, abort_word, ready)) return false;
@@ -329,7 +332,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
       int w = first;
-      issue_products<CG, C, PL, LONG, REGS>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
+      issue_products<CG, C, PL, LONG, REGS, CHUNK<MODE>>(a, smem, full, empty, tfull, tempty, tmem, BN, abort_word, [&](int& k0, int& k1) {
         if (w >= work) return false;
         range(w, k0, k1);
         w += step;
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
         for (int kb = k0; kb < k1;) {
           if (!wait_full()) break;
           release(acc.s);
-          kb += PL == 3 ? CHUNK : LONG ? a.fold : k1 - k0;
+          kb += PL == 3 ? CHUNK<MODE> : LONG ? a.fold : k1 - k0;
           acc.next(REGS || kb >= k1);
         }
         continue;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
         float sum[C::COLS];
 #pragma unroll
         for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
-        const int piece = PL == 3 ? CHUNK : a.fold;
+        const int piece = PL == 3 ? CHUNK<MODE> : a.fold;
         for (int kb = k0; kb < k1; kb += piece) {
           if (kb > k0) release(held);
           held = acc.s;

@@ -329,3 +329,141 @@ def mlp_adamw(X, B, hidden: int, layers: int = 1, act: str = "gelu", steps: int 
         info.steps += 1
         at = at + batch if at + batch < m else 0
     return net, info
+
+
+class Classifier:
+    """A residual network with layer norms and a softmax over classes, on rows of features or of ids.
+
+    With ``tokens`` = 0 the rows of X (m, features) go in as they are. Else they are ids (m, slots), each looked up in a
+    (tokens, width) table: a row is its slots' rows side by side (features = slots * width; an id outside the table is
+    padding and gives zeros). Then h = act(x W0 + b0), h = h + act(norm(h) Wi + bi) for each hidden layer, and the
+    classes' logits norm(h) P^T + c, which only ``logits`` writes out: the loss and its gradient do without
+    (``training.cross_entropy``). ``params`` are float32; ``dtype`` is what the layers compute in, as for ``MLP``.
+    """
+
+    def __init__(self, features: int, hidden: int, classes: int, layers: int = 1, tokens: int = 0, width: int = 0, act: str = "gelu",
+                 dtype=torch.float32, device="cuda", seed: int = 0):
+        gen = torch.Generator(device=device)
+        gen.manual_seed(seed)
+
+        def normal(a, b, scale):
+            return torch.randn(a, b, generator=gen, device=device) * scale
+
+        self.act, self.dtype, self.layers, self.tokens, self.width = act, dtype, layers, tokens, width
+        self.params = {}
+        if tokens:
+            self.params["table"] = normal(tokens, width, width**-0.5)
+        for i in range(layers + 1):
+            n = hidden if i else features
+            self.params[f"W{i}"], self.params[f"b{i}"] = normal(n, hidden, n**-0.5), torch.zeros(hidden, device=device)
+            # the norm before layer i + 1, the last one before the classes
+            self.params[f"g{i}"], self.params[f"s{i}"] = torch.ones(hidden, device=device), torch.zeros(hidden, device=device)
+        self.params["P"], self.params["c"] = normal(classes, hidden, hidden**-0.5), torch.zeros(classes, device=device)
+        self.copies = None if dtype == torch.float32 else {name: p.to(dtype) for name, p in self.params.items()}
+
+    def parameters(self):
+        return list(self.params.values())
+
+    def working(self):
+        """The parameters that the layers compute with."""
+        return self.params if self.copies is None else self.copies
+
+    def forward(self, X, keep: bool = False):
+        """norm(h) of the rows of X before the classes; with ``keep`` also what ``backward`` needs."""
+        from . import layers, training
+
+        p, saved = self.working(), []
+        if self.tokens:
+            rows = training.embedding(X.reshape(-1), p["table"], scale=self.width**0.5)
+            x = rows.view(X.shape[0], -1)
+        else:
+            x = X
+        v, h = x, None
+        for i in range(self.layers + 1):
+            entry, pre = h, None
+            out = layers.linear(v, p[f"W{i}"], p[f"b{i}"], act=self.act, residual=h, pre=keep)
+            h, pre = out if keep else (out, None)
+            saved.append((entry, v, pre))
+            v, mean, rstd = training.layer_norm(h, p[f"g{i}"], p[f"s{i}"], stats=True)
+            saved[-1] += (h, mean, rstd)
+        return (v, saved) if keep else v
+
+    def logits(self, X):
+        """The logits of the rows of X."""
+        from . import layers
+
+        p = self.working()
+        return layers.linear(self.forward(X), p["P"].t(), p["c"])
+
+    def loss(self, X, labels):
+        """The rows' losses and what ``backward`` needs. A label outside the classes leaves its row out."""
+        from . import training
+
+        p = self.working()
+        v, saved = self.forward(X, keep=True)
+        loss, lse = training.cross_entropy(v, p["P"].t(), labels, p["c"])
+        return loss, (X, labels, v, lse, saved)
+
+    def backward(self, g, kept):
+        """The gradients of ``parameters()`` from the gradient ``g`` at the losses (a number, or a float32 tensor of the rows)."""
+        from . import layers, training
+
+        p, grads = self.working(), {}
+        X, labels, v, lse, saved = kept
+        dv, dP, grads["c"] = training.cross_entropy_grad(v, p["P"].t(), labels, lse, p["c"], g=g)
+        grads["P"], dh = dP.t(), None
+        for i in range(self.layers, -1, -1):
+            _, v, pre, h, mean, rstd = saved[i]
+            # what reaches h through the norm, and past it
+            dh, grads[f"g{i}"], grads[f"s{i}"] = training.layer_norm_grad(dv, h, p[f"g{i}"], mean, rstd, residual=dh)
+            dv, grads[f"W{i}"], grads[f"b{i}"] = layers.linear_grad(dh, v, p[f"W{i}"], pre=pre, act=self.act,
+                                                                    need=(i > 0 or self.tokens > 0, True, True))
+        if self.tokens:
+            grads["table"] = training.embedding_grad(dv.view(-1, self.width), X.reshape(-1), self.tokens, scale=self.width**0.5)
+        return [grads[name] for name in self.params]
+
+
+def _mean_loss_gradients(net, labels, kept):
+    """The gradients of the mean loss of the rows that have a label, in the network's parameters."""
+    classes = net.params["P"].shape[0]
+    rate = 1.0 / ((labels >= 0) & (labels < classes)).sum().clamp_min(1).float()
+    if net.dtype != torch.float16:
+        return net.backward(rate.expand(labels.shape[0]).contiguous(), kept)
+    # float16 has nothing below 6e-8, where the gradient of a mean over millions of rows lies: it goes through the layers at a
+    # size that a sum over the rows leaves below 4,096 times an entry of the layer's input, and gets its own in float32
+    part = min(1.0, 4096 / labels.shape[0])
+    return [g.float().mul_(rate / part) for g in net.backward(part, kept)]
+
+
+def classify_adamw(X, labels, classes: int, hidden: int, layers: int = 1, tokens: int = 0, width: int = 0, act: str = "gelu",
+                   steps: int = 100, batch: int = 0, lr: float = 1e-3, weight_decay: float = 0.0, state_bits: int = 32,
+                   dtype=torch.float32, seed: int = 0):
+    """Classification by a residual network (``Classifier``) trained with AdamW: min mean cross entropy of softmax(net(X)).
+
+    X is (m, n) features, or with ``tokens`` > 0 (m, slots) ids, int32 or int64, into a table of ``tokens`` rows of ``width``.
+    ``labels`` (m,) are int32 or int64; rows with a label outside 0 .. classes - 1 are left out. Each step takes ``batch``
+    rows in turn (0: all of them), the last step of a pass over X what is left of its rows. Returns the network and the
+    steps' mean losses (left on the GPU until read).
+    """
+    from .layers import AdamW
+
+    m, features = X.shape
+    if tokens:
+        features *= width
+    else:
+        X = X.to(dtype)
+    net = Classifier(features, hidden, classes, layers, tokens, width, act, dtype, X.device, seed)
+    opt = AdamW(net.parameters(), lr=lr, weight_decay=weight_decay, state_bits=state_bits,
+                copies=None if net.copies is None else list(net.copies.values()))
+    info = MLPInfo()
+    batch = m if batch <= 0 else min(batch, m)
+    at = 0
+    for _ in range(steps):
+        y = labels[at:at + batch]
+        loss, kept = net.loss(X[at:at + batch], y)
+        inside = ((y >= 0) & (y < classes)).sum().clamp_min(1)
+        info.losses.append(loss.sum() / inside)
+        opt.step(_mean_loss_gradients(net, y, kept))
+        info.steps += 1
+        at = at + batch if at + batch < m else 0
+    return net, info

@@ -115,8 +115,8 @@ def check_grad(m, n, dtype, affine=True, residual=True, scale=1.0, shift=0.0, pa
 
 # one access a thread, several lanes, a warp, several warps, the most that registers hold and one more, by 16 bytes and by
 # entries
-LENGTHS = [1, 2, 3, 7, 8, 16, 31, 32, 33, 64, 100, 127, 128, 129, 256, 264, 301, 512, 513, 1000, 1001, 1024, 2056, 4096, 4104, 5000,
-           8192, 8200, 8193, 16384, 16392, 32768, 32776]
+LENGTHS = [1, 2, 3, 7, 8, 16, 31, 32, 33, 64, 100, 127, 128, 129, 256, 264, 301, 512, 513, 1000, 1001, 1024, 2056, 4096, 4104, 5000, 5912,
+           6144, 8192, 8200, 8193, 16384, 16392, 32768, 32776]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
