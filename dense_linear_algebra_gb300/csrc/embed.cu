@@ -451,53 +451,66 @@ __device__ __forceinline__ const uint2* load_ids(const ReduceArgs& a, int64_t ch
   return s + BEFORE;
 }
 
-// One access of a row of dE: a chunk's sums, run by run.
-template <typename T, int V>
+// CH accesses of a row of dE, `step` apart: a chunk's sums, run by run.
+template <typename T, int V, int CH>
 struct RunSum {
   const ReduceArgs& a;
   const Chunk& k;
-  const int64_t chunk, c;
-  const bool mine;
-  float acc[V] = {};
+  const int64_t chunk, c, accesses;
+  const int step;
+  float acc[CH * V] = {};
   uint32_t run = NONE;
-  __device__ __forceinline__ RunSum(const ReduceArgs& a_, const Chunk& k_, int64_t chunk_, int64_t c_, bool mine_)
-      : a(a_), k(k_), chunk(chunk_), c(c_), mine(mine_) {}
-  __device__ __forceinline__ void add(uint32_t key, const Piece<T, V>& x) {
+  __device__ __forceinline__ RunSum(const ReduceArgs& a_, const Chunk& k_, int64_t chunk_, int64_t c_, int step_)
+      : a(a_), k(k_), chunk(chunk_), c(c_), accesses(a_.n / V), step(step_) {}
+  __device__ __forceinline__ bool has(int h) const { return c + h * step < accesses; }
+  __device__ __forceinline__ int64_t at(int h) const { return (c + h * step) * V; }
+  __device__ __forceinline__ void add(uint32_t key, const Piece<T, V> (&x)[CH]) {
     if (key != run) {
       flush(false);
       run = key;
     }
 #pragma unroll
-    for (int q = 0; q < V; ++q) acc[q] += x.get(q);
+    for (int h = 0; h < CH; ++h)
+#pragma unroll
+      for (int q = 0; q < V; ++q) acc[h * V + q] += x[h].get(q);
   }
   __device__ __forceinline__ void flush(bool part_right) {
-    if (run < a.count && mine) {
+    if (run < a.count) {
       const bool part_left = k.part_left && run == k.left;
-      if (!part_left && !part_right) {
-        Piece<T, V> o;
 #pragma unroll
-        for (int q = 0; q < V; ++q) o.set(q, acc[q] * a.scale);
-        o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + c * V);
-      } else {
-        Piece<float, V> o;
+      for (int h = 0; h < CH; ++h) {
+        if (!has(h)) continue;
+        if (!part_left && !part_right) {
+          Piece<T, V> o;
 #pragma unroll
-        for (int q = 0; q < V; ++q) o.set(q, acc[q]);
-        o.store(a.part + (2 * chunk + (part_left ? 0 : 1)) * a.n + c * V);
+          for (int q = 0; q < V; ++q) o.set(q, acc[h * V + q] * a.scale);
+          o.store(static_cast<T*>(a.out) + (int64_t)run * a.ldo + at(h));
+        } else {
+          Piece<float, V> o;
+#pragma unroll
+          for (int q = 0; q < V; ++q) o.set(q, acc[h * V + q]);
+          o.store(a.part + (2 * chunk + (part_left ? 0 : 1)) * a.n + at(h));
+        }
       }
     }
 #pragma unroll
-    for (int q = 0; q < V; ++q) acc[q] = 0.f;
+    for (int q = 0; q < CH * V; ++q) acc[q] = 0.f;
   }
   // the rows of the first `n` of N ids, those other than `only` left out unless it is NONE
   template <int N>
   __device__ __forceinline__ void add_rows(const uint2* ids, int n, uint32_t only) {
-    Piece<T, V> x[N];
+    Piece<T, V> x[N][CH];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint2 y = ids[i < n ? i : 0];
       // (an id outside the table is `count`, sorted last; NONE is above it)
-      if (mine && i < n && y.x < a.count && (only == NONE || y.x == only)) x[i].load(static_cast<const T*>(a.G) + (int64_t)y.y * a.ldg + c * V);
-      else x[i].zero();
+      const bool take = i < n && y.x < a.count && (only == NONE || y.x == only);
+      const T* row = static_cast<const T*>(a.G) + (int64_t)y.y * a.ldg;
+#pragma unroll
+      for (int h = 0; h < CH; ++h) {
+        if (take && has(h)) x[i][h].load(row + at(h));
+        else x[i][h].zero();
+      }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -567,23 +580,26 @@ __global__ void __launch_bounds__(BULK_THREADS) embed_bulk_kernel(const __grid_c
                policy_evict_first());
     if (lane == 0 && slab == 0) note_long(a, k, chunk);
   }
-  RunSum<T, V> sum(a, k, chunk, c, c < accesses);
+  RunSum<T, V, 1> sum(a, k, chunk, c, 0);
   bool ok = true;
 #pragma unroll 1
   for (int i = 0; i < CHUNK; ++i) {
     if (i % PER == 0) ok = mbar_wait_bounded(&full[i / PER], 0) && ok;
     const uint32_t key = own(i);
     if (key == NONE || !ok) continue;
-    Piece<T, V> x;
-    if (key < a.count) x.v[0] = *reinterpret_cast<const uint4*>(stage + i * BULK_ROW + threadIdx.x * 16);
-    else x.zero();
+    Piece<T, V> x[1];
+    if (key < a.count) x[0].v[0] = *reinterpret_cast<const uint4*>(stage + i * BULK_ROW + threadIdx.x * 16);
+    else x[0].zero();
     sum.add(key, x);
   }
   if (ok) sum.template finish<4>(ids);
 }
 
-// Other rows: a worker is `tpr` threads, which hold several rows' accesses on their way.
+// Other rows: a worker is `tpr` threads, which hold several rows' accesses on their way. Rows that go entry by entry (no 16-byte
+// accesses) have 4 entries a thread, `tpr` apart: one left 33,468 rows of 3,485 bfloat16 at 480 us.
 constexpr int GROUPS = 16;  // workers a CTA has at most
+template <int V>
+constexpr int EACH = V == 1 ? 4 : 1;  // accesses a thread has
 
 template <typename T, int V>
 __global__ void __launch_bounds__(THREADS, V == 1 ? 4 : 2) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
@@ -594,16 +610,16 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 4 : 2) embed_reduce_kernel(c
     zero_rows<T>(a, at * a.zero_rows);
     return;
   }
-  constexpr int N = V == 1 ? 16 : 8;
+  constexpr int N = 8;
   const Shape& s = a.shape;
   const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
-  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr + t, first = at * s.groups / s.slabs;
+  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr * EACH<V> + t, first = at * s.groups / s.slabs;
   const uint2* ids = load_ids(a, first, s.groups, s_ids);
   if (group >= s.groups || chunk * CHUNK >= a.m) return;
   ids += (chunk - first) * CHUNK;
   const Chunk k(a, chunk, ids);
   if (c == 0) note_long(a, k, chunk);
-  RunSum<T, V> sum(a, k, chunk, c, c < a.n / V);
+  RunSum<T, V, EACH<V>> sum(a, k, chunk, c, s.tpr);
   int i = 0;
   if (k.skip)
     while (ids[i].x == k.left) ++i;
@@ -782,7 +798,7 @@ fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t s
       if (e == cudaSuccess) e = launch_kernel(embed_bulk_kernel<T>, dim3((unsigned)q.ctas), BULK_THREADS, smem, st, q);
     }
   } else {
-    q.shape = shape_of(accesses, 1);
+    q.shape = shape_of(accesses, EACH<V>);
     q.shape.groups = std::min(q.shape.groups, GROUPS);
     q.sum_ctas = (chunks * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
     q.ctas = q.sum_ctas + zero_ctas;

@@ -16,8 +16,8 @@
 // two that brings the largest |g| to 2^14 .. 2^15, which the last of the sums takes back. What is lost is below 2^-39 of
 // that |g| (below 2^-29 of it, digits are).
 //
-// At most 64 features and classes: thin_loss.cu. Few rows (float32: those of few.cu; 16 bits: up to 128): z is written out in
-// fp32, its statistics or D formed by kernels of their own, and the products are those of few rows.
+// At most 64 features and classes: thin_loss.cu, and thin_loss_f32.cu. Few rows: z is written out in fp32, its statistics or D
+// formed by kernels of their own, and the products are those of few rows.
 #include <algorithm>
 
 #include "act.cuh"
@@ -93,7 +93,9 @@ cudaError_t launch_join(const float2* stats, int64_t parts, int64_t rows, const 
 }
 
 constexpr int SEG = 1024;  // of a row that a CTA reduces
-constexpr int kFewLogits = 128;  // rows whose logits are written out
+// Rows whose logits are written out, at most: of 16 bits forward (2048 x 32,000: 36 us at 1 to 16 rows and 44 at 64; in tiles 47 at
+// 1, 49 at 16, 38 at 64) and for the gradient (130 us at 1 row and 144 at 16, in tiles 144 and 135), and of float32 forward.
+constexpr int kFewLogits = 16, kFewLogitsGrad = 4, kFewLogitsF32 = 128;
 
 // Few rows' logits in memory: `parts` parts of X W to be added, [part][row][class], and the biases.
 struct FewLogits {
@@ -300,11 +302,12 @@ const void* bias_at(const LayerArgs& l, int64_t c) {
 
 const void* labels_at(const LossArgs& a, int64_t r) { return static_cast<const char*>(a.labels) + r * (a.labels64 ? 8 : 4); }
 
-// Whether a call's logits are written out, in fp32: float32 of few rows, on the CUDA cores, and 16-bit types of up to one
-// tile of rows, which the product kernels of few rows take (W is read once with no row of the tile wasted).
-bool few_logits(const LayerArgs& l) {
-  if (l.type == FXTX_F32) return few_rows(l.type, l.m, l.w_trans);
-  return l.m <= kFewLogits && packed_bytes(l.type, l.W, l.ldw, l.n) == 0;
+// Whether a call's logits are written out, in fp32: few rows', which the product kernels of few rows take (W is read once with
+// no row of the tile wasted), or for float32 the CUDA cores. The gradient of float32 rows that those do not take forms
+// W's planes once for all of its products instead.
+bool few_logits(const LayerArgs& l, bool grad) {
+  if (l.type == FXTX_F32) return grad ? few_rows(l.type, l.m, l.w_trans) : l.m <= kFewLogitsF32;
+  return l.m <= (grad ? kFewLogitsGrad : kFewLogits) && packed_bytes(l.type, l.W, l.ldw, l.n) == 0;
 }
 
 // Few rows as an operand, in a workspace of its own where they have to be copied.
@@ -333,10 +336,11 @@ PlanesProduct logits_product(const LayerArgs& l, const Part& x) {
 // X W of few rows to z; its biases are left to the kernels that read it.
 fxtx_status_t run_logits(const LayerArgs& l, const Part& x, float* z, const DeviceInfo& dev, cudaStream_t st) {
   if (l.type != FXTX_F32) return run_raw(l.type, logits_product(l, x), z, dev, st);
-  Epilogue e;
-  e.out = z;
-  e.ldo = l.k;
-  return run_few(l.m, l.n, l.k, l.X, l.ldx, 0, static_cast<const float*>(l.W), l.ldw, l.w_trans, e, dev, st);
+  LayerArgs z_of = l;
+  z_of.e = Epilogue{};
+  z_of.e.out = z;
+  z_of.e.ldo = l.k;
+  return run_linear(z_of, dev, st);
 }
 
 template <typename T>
@@ -437,7 +441,7 @@ cudaError_t launch_scales(const float* g, int64_t m, float gain, float* scales, 
 }
 
 fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (few_logits(l)) switch (l.type) {
+  if (few_logits(l, false)) switch (l.type) {
       case FXTX_F32: return few_loss<float>(l, a, dev, st);
       case FXTX_BF16: return few_loss<__nv_bfloat16>(l, a, dev, st);
       default: return few_loss<__half>(l, a, dev, st);
@@ -506,7 +510,7 @@ fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& 
 }
 
 fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (few_logits(l)) switch (l.type) {
+  if (few_logits(l, true)) switch (l.type) {
       case FXTX_F32: return few_grad<float>(l, a, dev, st);
       case FXTX_BF16: return few_grad<__nv_bfloat16>(l, a, dev, st);
       default: return few_grad<__half>(l, a, dev, st);

@@ -16,6 +16,7 @@
 // taking neighbouring entries.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "host.h"
@@ -631,6 +632,195 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
   }
 }
 
+// ------------------------------------------------------------------------------------------------ rows of any width by bulk copies
+// Many rows whose pitch or width is no multiple of 16 bytes, from 16-byte aligned matrices: a row comes with what of its first
+// and last 16 bytes belongs to its neighbours (of the last row the end is read where it lies), and threads take its entries
+// from shared memory, neighbours neighbouring ones (entry by entry from memory, 30,001 x 2047 bfloat16 took 218 us, its
+// gradient 564).
+
+template <typename T, int MATS>
+struct OddRing {
+  unsigned char* at;
+  uint64_t* full;
+  int slot, stages, mats, s = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  __device__ __forceinline__ OddRing(unsigned char* smem, uint64_t* bars, int group, int slot_, int stages_, int mats_)
+      : slot(slot_), stages(stages_), mats(mats_) {
+    at = smem + (size_t)group * stages * mats * slot;
+    full = bars + group * MOST_STAGES;
+  }
+  // where a row's copy begins, and its bytes
+  __device__ __forceinline__ static uint32_t head(const T* p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u); }
+  __device__ __forceinline__ static uint32_t copied(const T* p, int64_t n, bool last) {
+    const uint32_t bytes = head(p) + (uint32_t)(n * sizeof(T));
+    return last ? bytes / 16 * 16 : (bytes + 15) / 16 * 16;
+  }
+  __device__ __forceinline__ void fill(int x, const T* const (&p)[MATS], int64_t n, bool last) {
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < MATS; ++i)
+      if (i < mats) all += copied(p[i], n, last);
+    mbar_arrive_expect_tx(&full[x], all);
+#pragma unroll
+    for (int i = 0; i < MATS; ++i)
+      if (i < mats) {
+        const uint32_t bytes = copied(p[i], n, last);
+        if (bytes) copy_row(at + (size_t)(x * mats + i) * slot, reinterpret_cast<const unsigned char*>(p[i]) - head(p[i]), bytes, &full[x]);
+      }
+  }
+  __device__ __forceinline__ void wait() { ok = ok && mbar_wait_bounded(&full[s], phase); }
+  __device__ __forceinline__ void next() {
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  // the thread's entries of the row at p
+  template <int CH>
+  __device__ __forceinline__ void load(int mat, const T* p, int t, int tpr, int64_t n, bool last, float (&x)[CH]) const {
+    const T* row = reinterpret_cast<const T*>(at + (size_t)(s * mats + mat) * slot + head(p));
+    const int there = last ? (int)((copied(p, n, true) - min(copied(p, n, true), head(p))) / sizeof(T)) : (int)n;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int j = t + i * tpr;
+      x[i] = j < there ? to_f32(row[j]) : j < n ? to_f32(p[j]) : 0.f;
+    }
+  }
+};
+
+template <typename T, int CH>
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_constant__ NormArgs a, const RowShape shape, int slot, int stages) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t full[MOST_GROUPS * MOST_STAGES];
+  __shared__ float2 red[2][32];
+  const int tpr = shape.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, n = (int)a.n;
+  RowSum<true> sum{red, tpr, group};
+  OddRing<T, 1> ring(smem, full, group, slot, stages, 1);
+  if (t == 0) {
+    for (int x = 0; x < stages; ++x) mbar_init(&ring.full[x], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const float over = 1.f / (float)n;
+  const int64_t step = (int64_t)gridDim.x * shape.groups;
+  int64_t row = (int64_t)blockIdx.x * shape.groups + group;
+  after_previous();
+  auto at = [&](int64_t i) { return static_cast<const T*>(a.X) + i * a.ldx; };
+  auto fill = [&](int x, int64_t i) {
+    const T* p[1] = {at(i)};
+    if (i < a.m) ring.fill(x, p, n, i + 1 == a.m);
+  };
+  if (t == 0)
+    for (int x = 0; x < stages; ++x) fill(x, row + x * step);
+  float w[CH], b[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int j = t + i * tpr;
+    w[i] = a.w && j < n ? to_f32(static_cast<const T*>(a.w)[j]) : 1.f;
+    b[i] = a.b && j < n ? to_f32(static_cast<const T*>(a.b)[j]) : 0.f;
+  }
+  for (; row < a.m; row += step) {
+    ring.wait();
+    float x[CH];
+    ring.load(0, at(row), t, tpr, n, row + 1 == a.m, x);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) s += x[i];
+    const float mean = sum(make_float2(s, 0.f)).x * over;
+    // (every thread of the group has read the row)
+    if (t == 0) fill(ring.s, row + stages * step);
+    ring.next();
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      x[i] = t + i * tpr < n ? x[i] - mean : 0.f;
+      s = fmaf(x[i], x[i], s);
+    }
+    const float rstd = __frsqrt_rn(fmaf(sum(make_float2(s, 0.f)).x, over, a.eps));
+    if (!ring.ok) continue;  // FXTX_ERR_TIMEOUT is raised
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (t + i * tpr < n) out[t + i * tpr] = from_f32<T>(fmaf(x[i] * rstd, w[i], b[i]));
+  }
+}
+
+template <typename T, int CH, bool SUMS>
+__global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_odd_kernel(const __grid_constant__ NormArgs a, const RowShape shape, int slot,
+                                                                       int stages) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ __align__(8) uint64_t full[MOST_GROUPS * MOST_STAGES];
+  __shared__ float2 red[2][32];
+  const int tpr = shape.tpr, group = threadIdx.x / tpr, t = threadIdx.x % tpr, n = (int)a.n;
+  RowSum<true> sum{red, tpr, group};
+  OddRing<T, 3> ring(smem, full, group, slot, stages, a.R ? 3 : 2);
+  if (t == 0) {
+    for (int x = 0; x < stages; ++x) mbar_init(&ring.full[x], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  const float over = 1.f / (float)n;
+  const int64_t step = (int64_t)gridDim.x * shape.groups;
+  int64_t row = (int64_t)blockIdx.x * shape.groups + group;
+  after_previous();
+  auto x_at = [&](int64_t i) { return static_cast<const T*>(a.X) + i * a.ldx; };
+  auto g_at = [&](int64_t i) { return static_cast<const T*>(a.G) + i * a.ldg; };
+  auto r_at = [&](int64_t i) { return static_cast<const T*>(a.R) + i * a.ldr; };
+  auto fill = [&](int x, int64_t i) {
+    if (i >= a.m) return;
+    const T* p[3] = {x_at(i), g_at(i), a.R ? r_at(i) : nullptr};
+    ring.fill(x, p, n, i + 1 == a.m);
+  };
+  if (t == 0)
+    for (int x = 0; x < stages; ++x) fill(x, row + x * step);
+  float w[CH], dw[SUMS ? CH : 1] = {}, db[SUMS ? CH : 1] = {};
+#pragma unroll
+  for (int i = 0; i < CH; ++i) w[i] = a.w && t + i * tpr < n ? to_f32(static_cast<const T*>(a.w)[t + i * tpr]) : 1.f;
+  float mean_n = row < a.m ? a.mean_in[row] : 0.f, rstd_n = row < a.m ? a.rstd_in[row] : 0.f;
+  for (; row < a.m; row += step) {
+    const float mean = mean_n, rstd = rstd_n;
+    const bool last = row + 1 == a.m;
+    if (row + step < a.m) {
+      mean_n = a.mean_in[row + step];
+      rstd_n = a.rstd_in[row + step];
+    }
+    ring.wait();
+    float u[CH], h[CH], res[CH];
+    ring.load(0, x_at(row), t, tpr, n, last, u);
+    ring.load(1, g_at(row), t, tpr, n, last, h);
+    if (a.R) ring.load(2, r_at(row), t, tpr, n, last, res);
+    float2 s = make_float2(0.f, 0.f);
+    // (beyond the row's end g is zero, and u counts for nothing unless the whole row is no number)
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      u[i] = (u[i] - mean) * rstd;
+      if constexpr (SUMS) {
+        dw[i] = fmaf(h[i], u[i], dw[i]);
+        db[i] += h[i];
+      }
+      h[i] *= w[i];
+      s.x += h[i];
+      s.y = fmaf(h[i], u[i], s.y);
+    }
+    s = sum(s);
+    if (t == 0) fill(ring.s, row + stages * step);
+    ring.next();
+    if (!ring.ok || !a.DX) continue;
+    const float c1 = s.x * over, c2 = s.y * over;
+    T* out = static_cast<T*>(a.DX) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+      if (t + i * tpr < n) out[t + i * tpr] = from_f32<T>(fmaf(fmaf(-u[i], c2, h[i] - c1), rstd, a.R ? res[i] : 0.f));
+  }
+  if constexpr (SUMS)
+    store_columns<T, 1, CH>(a, RowOf<T, 1, CH>(t, tpr, a.n), group, shape.groups, dw, db, reinterpret_cast<float*>(smem));
+}
+
 // Rows of at most 32 accesses of 16 bytes, without gaps between them: a row lies over `tpr` neighbouring lanes, an access
 // each, and each warp has a ring of its own, of tiles of about 2 KB a matrix, several on their way at a time (with a row ahead in
 // registers 1,000,000 x 32 float32 took 90 us).
@@ -1059,6 +1249,30 @@ cudaError_t launch_ring(const NormArgs& a, const RowShape& s, int stages, const 
   return launch_kernel(norm_ring_kernel<T, CH>, dim3((unsigned)dev.sm_count), (unsigned)(s.tpr * s.groups), smem, st, a, s, stages);
 }
 
+// The shape of rows that come so: at most CH entries a thread, 64 threads at least; their slot in shared memory.
+struct OddShape {
+  RowShape s;
+  int slot = 0, stages = 0;
+};
+bool odd_rows(const NormArgs& a, int size, int mats, const DeviceInfo& dev, OddShape& o) {
+  if (a.n <= 128 || a.n > 16 * RING_THREADS) return false;
+  for (const void* p : {a.X, a.G, a.R})
+    if ((uintptr_t)p & 15u) return false;
+  o.s.tpr = (int)std::max<int64_t>(64, ((a.n + 15) / 16 + 31) / 32 * 32);
+  o.s.groups = RING_THREADS / o.s.tpr;
+  o.slot = (int)((a.n * size + 15) / 16 * 16 + 32);
+  o.stages = stages_of(o.s, o.slot, mats);
+  return o.stages >= 2 && ring_rows(o.s, a.m, dev);
+}
+
+template <typename T, int CH>
+cudaError_t launch_odd(const NormArgs& a, const OddShape& o, const DeviceInfo& dev, cudaStream_t st) {
+  const size_t smem = (size_t)o.s.groups * o.stages * o.slot;
+  const cudaError_t e = ensure_smem((const void*)norm_odd_kernel<T, CH>, smem + 1024);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(norm_odd_kernel<T, CH>, dim3((unsigned)dev.sm_count), (unsigned)(o.s.tpr * o.s.groups), smem, st, a, o.s, o.slot, o.stages);
+}
+
 template <typename T, int V>
 cudaError_t forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   constexpr int MOST = V == 1 ? 16 : 4;
@@ -1071,6 +1285,10 @@ cudaError_t forward(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
     const RowShape s = shape_of(accesses, MOST, RING_THREADS);
     const int stages = stages_of(s, a.n * (int64_t)sizeof(T), 1);
     if (stages >= 2 && ring_rows(s, a.m, dev)) return launch_ring<T, MOST>(a, s, stages, dev, st);
+  } else {
+    OddShape o;
+    if (odd_rows(a, sizeof(T), 1, dev, o))
+      return a.n <= 256 ? launch_odd<T, 4>(a, o, dev, st) : a.n <= 512 ? launch_odd<T, 8>(a, o, dev, st) : launch_odd<T, 16>(a, o, dev, st);
   }
   return forward_ch<T, V, MOST>(a, dev, st);
 }
@@ -1147,6 +1365,33 @@ fxtx_status_t launch_grad_ring(NormArgs a, const RowShape& s, int stages, const 
   return FXTX_ERR_CUDA;
 }
 
+template <typename T, int CH, bool SUMS>
+fxtx_status_t launch_grad_odd(NormArgs a, const OddShape& o, const DeviceInfo& dev, cudaStream_t st) {
+  const size_t sums = SUMS ? (size_t)2 * CH * o.s.tpr * 4 : 0;
+  const size_t smem = std::max((size_t)o.s.groups * o.stages * (a.R ? 3 : 2) * o.slot, sums);
+  cudaError_t e = ensure_smem((const void*)norm_grad_odd_kernel<T, CH, SUMS>, smem + 1024);
+  if (SUMS && e == cudaSuccess) {
+    const fxtx_status_t r = alloc_pooled(reinterpret_cast<void**>(&a.part), (size_t)dev.sm_count * 2 * a.n * 4, st);
+    if (r != FXTX_OK) return r;
+  }
+  if (e == cudaSuccess)
+    e = launch_kernel(norm_grad_odd_kernel<T, CH, SUMS>, dim3((unsigned)dev.sm_count), (unsigned)(o.s.tpr * o.s.groups), smem, st, a, o.s,
+                      o.slot, o.stages);
+  if (a.part) {
+    if (e == cudaSuccess) e = launch_kernel(norm_join_kernel<T>, dim3((unsigned)((2 * a.n + 31) / 32)), 1024, 0, st, a, (int64_t)dev.sm_count);
+    cudaFreeAsync(a.part, st);
+  }
+  if (e == cudaSuccess) return FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
+}
+template <typename T, bool SUMS>
+fxtx_status_t grad_odd(const NormArgs& a, const OddShape& o, const DeviceInfo& dev, cudaStream_t st) {
+  return a.n <= 256   ? launch_grad_odd<T, 4, SUMS>(a, o, dev, st)
+         : a.n <= 512 ? launch_grad_odd<T, 8, SUMS>(a, o, dev, st)
+                      : launch_grad_odd<T, 16, SUMS>(a, o, dev, st);
+}
+
 template <typename T, bool SUMS>
 fxtx_status_t launch_short(NormArgs a, const DeviceInfo& dev, cudaStream_t st) {
   const int accesses = (int)(a.n / (16 / (int)sizeof(T)));
@@ -1190,12 +1435,20 @@ fxtx_status_t grad(const NormArgs& a, const DeviceInfo& dev, cudaStream_t st) {
     if (accesses <= 32 && a.m * accesses >= (int64_t)dev.sm_count * SHORT_THREADS * 4 && a.ldx == a.n && a.ldg == a.n && (!a.R || a.ldr == a.n))
       return a.DW || a.DB ? launch_short<T, true>(a, dev, st) : launch_short<T, false>(a, dev, st);
     if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
-    const RowShape s = shape_of(accesses, MOST, RING_THREADS);
-    const int stages = stages_of(s, a.n * (int64_t)sizeof(T), a.R ? 3 : 2);
-    if (stages >= 2 && ring_rows(s, a.m, dev))
-      return a.DW || a.DB ? launch_grad_ring<T, MOST, true>(a, s, stages, dev, st) : launch_grad_ring<T, MOST, false>(a, s, stages, dev, st);
+    auto ring = [&](auto ch, fxtx_status_t& r) {
+      constexpr int CH = decltype(ch)::value;
+      const RowShape s = shape_of(accesses, CH, RING_THREADS);
+      const int stages = stages_of(s, a.n * (int64_t)sizeof(T), a.R ? 3 : 2);
+      if (stages < 2 || !ring_rows(s, a.m, dev)) return false;
+      r = a.DW || a.DB ? launch_grad_ring<T, CH, true>(a, s, stages, dev, st) : launch_grad_ring<T, CH, false>(a, s, stages, dev, st);
+      return true;
+    };
+    fxtx_status_t r;
+    if (accesses <= 64 ? ring(std::integral_constant<int, 1>{}, r) : ring(std::integral_constant<int, MOST>{}, r)) return r;
   } else {
     if (accesses <= 32) return grad_ch<T, V, 1>(a, dev, st);
+    OddShape o;
+    if (odd_rows(a, sizeof(T), a.R ? 3 : 2, dev, o)) return a.DW || a.DB ? grad_odd<T, true>(a, o, dev, st) : grad_odd<T, false>(a, o, dev, st);
   }
   return grad_ch<T, V, MOST>(a, dev, st);
 }

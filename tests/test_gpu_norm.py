@@ -140,6 +140,14 @@ def test_rows(m, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("m,n", [(8001, 129), (8000, 250), (8003, 257), (6001, 511), (6000, 1001), (3001, 2047), (1500, 4099), (900, 8191), (9000, 130)])
+def test_many_rows_of_odd_widths(m, n, dtype):
+    """Rows that come by bulk copies from where they lie, whole 16 bytes around them; the last one's end is read apart."""
+    check_forward(m, n, dtype, affine=n != 257, shift=1.0)
+    check_grad(m, n, dtype, residual=m % 2 == 1, affine=n != 511, need=(True, n != 1001, n != 1001))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("m,n", [(400_001, 8), (200_003, 16), (100_001, 40), (100_003, 64), (50_001, 104), (30_011, 128), (20_003, 232)])
 def test_many_short_rows(m, n, dtype):
     """Tiles of rows that come by bulk copies, the last one short."""
@@ -156,7 +164,7 @@ def test_many_long_rows(m, n, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("pad,offset", [(8, 0), (16, 8), (1, 0), (5, 3)])
-@pytest.mark.parametrize("m,n", [(9, 32), (9, 301), (9, 1024), (9, 20_000), (3000, 2048)])
+@pytest.mark.parametrize("m,n", [(9, 32), (9, 301), (9, 1024), (9, 20_000), (3000, 2048), (5000, 700)])
 def test_column_slices(m, n, pad, offset, dtype):
     check_forward(m, n, dtype, pad=pad, offset=offset)
     check_grad(m, n, dtype, pad=pad, offset=offset)
