@@ -678,13 +678,24 @@ struct OddRing {
   }
   // the thread's entries of the row at p
   template <int CH>
-  __device__ __forceinline__ void load(int mat, const T* p, int t, int tpr, int64_t n, bool last, float (&x)[CH]) const {
+  __device__ __forceinline__ void load(int mat, const T* p, int t, int tpr, int n, bool last, float (&x)[CH]) const {
     const T* row = reinterpret_cast<const T*>(at + (size_t)(s * mats + mat) * slot + head(p));
-    const int there = last ? (int)((copied(p, n, true) - min(copied(p, n, true), head(p))) / sizeof(T)) : (int)n;
+    if (!last) {
 #pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int j = t + i * tpr;
+        x[i] = to_f32(row[j < n ? j : 0]);
+        if (j >= n) x[i] = 0.f;
+      }
+      return;
+    }
+    const int there = (int)((max(copied(p, n, true), head(p)) - head(p)) / sizeof(T));
+#pragma unroll 1
     for (int i = 0; i < CH; ++i) {
       const int j = t + i * tpr;
-      x[i] = j < there ? to_f32(row[j]) : j < n ? to_f32(p[j]) : 0.f;
+      const float v = j < there ? to_f32(row[j]) : j < n ? to_f32(p[j]) : 0.f;
+#pragma unroll
+      for (int q = 0; q < CH; ++q) x[q] = q == i ? v : x[q];
     }
   }
 };
