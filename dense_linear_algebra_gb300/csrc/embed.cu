@@ -40,30 +40,31 @@ constexpr uint32_t NONE = 0xffffffffu;  // the key of no id
 template <typename S, int V>
 struct Piece {
   static constexpr int B = V * sizeof(S);
-  uint4 v[B >= 16 ? B / 16 : 1];
+  static_assert(B % 16 == 0, "16 bytes");
+  uint4 v[B / 16];
   __device__ __forceinline__ void load(const S* p) {
-    if constexpr (B >= 16) {
 #pragma unroll
-      for (int i = 0; i < B / 16; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-    } else {
-      static_assert(V == 1, "one entry");
-      *reinterpret_cast<S*>(&v[0]) = *p;
-    }
+    for (int i = 0; i < B / 16; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < (B >= 16 ? B / 16 : 1); ++i) v[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < B / 16; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const S*>(v)[i]); }
   __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<S*>(v)[i] = from_f32<S>(x); }
   __device__ __forceinline__ void store(S* p) const {
-    if constexpr (B >= 16) {
 #pragma unroll
-      for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
-    } else {
-      *p = *reinterpret_cast<const S*>(&v[0]);
-    }
+    for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
   }
+};
+template <typename S>
+struct Piece<S, 1> {
+  S v;
+  __device__ __forceinline__ void load(const S* p) { v = *p; }
+  __device__ __forceinline__ void zero() { v = from_f32<S>(0.f); }
+  __device__ __forceinline__ float get(int) const { return to_f32(v); }
+  __device__ __forceinline__ void set(int, float x) { v = from_f32<S>(x); }
+  __device__ __forceinline__ void store(S* p) const { *p = v; }
 };
 
 // The id at position i, `count` for one outside the table.
@@ -588,20 +589,19 @@ __global__ void __launch_bounds__(BULK_THREADS) embed_bulk_kernel(const __grid_c
     const uint32_t key = own(i);
     if (key == NONE || !ok) continue;
     Piece<T, V> x[1];
-    if (key < a.count) x[0].v[0] = *reinterpret_cast<const uint4*>(stage + i * BULK_ROW + threadIdx.x * 16);
+    if (key < a.count) x[0].load(reinterpret_cast<const T*>(stage + i * BULK_ROW + threadIdx.x * 16));
     else x[0].zero();
     sum.add(key, x);
   }
   if (ok) sum.template finish<4>(ids);
 }
 
-// Other rows: a worker is `tpr` threads, which hold several rows' accesses on their way. Rows that go entry by entry (no 16-byte
-// accesses) have 4 entries a thread, `tpr` apart: one left 33,468 rows of 3,485 bfloat16 at 480 us.
+// Other rows: a worker is `tpr` threads, which hold several rows' accesses on their way. Many rows that go entry by entry (no 16-byte
+// accesses) have 4 entries a thread, `tpr` apart.
 constexpr int GROUPS = 16;  // workers a CTA has at most
-template <int V>
-constexpr int EACH = V == 1 ? 4 : 1;  // accesses a thread has
 
-template <typename T, int V>
+// EACH: accesses a thread has.
+template <typename T, int V, int EACH>
 __global__ void __launch_bounds__(THREADS, V == 1 ? 4 : 2) embed_reduce_kernel(const __grid_constant__ ReduceArgs a) {
   __shared__ uint2 s_ids[BEFORE + (GROUPS + 1) * CHUNK + 1];
   after_previous();
@@ -610,16 +610,16 @@ __global__ void __launch_bounds__(THREADS, V == 1 ? 4 : 2) embed_reduce_kernel(c
     zero_rows<T>(a, at * a.zero_rows);
     return;
   }
-  constexpr int N = 8;
+  constexpr int N = V == 1 && EACH == 1 ? 16 : 8;
   const Shape& s = a.shape;
   const int group = threadIdx.x / s.tpr, t = threadIdx.x % s.tpr;
-  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr * EACH<V> + t, first = at * s.groups / s.slabs;
+  const int64_t w = at * s.groups + group, chunk = w / s.slabs, c = (w - chunk * s.slabs) * s.tpr * EACH + t, first = at * s.groups / s.slabs;
   const uint2* ids = load_ids(a, first, s.groups, s_ids);
   if (group >= s.groups || chunk * CHUNK >= a.m) return;
   ids += (chunk - first) * CHUNK;
   const Chunk k(a, chunk, ids);
   if (c == 0) note_long(a, k, chunk);
-  RunSum<T, V, EACH<V>> sum(a, k, chunk, c, s.tpr);
+  RunSum<T, V, EACH> sum(a, k, chunk, c, s.tpr);
   int i = 0;
   if (k.skip)
     while (ids[i].x == k.left) ++i;
@@ -798,12 +798,17 @@ fxtx_status_t gradient(const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t s
       if (e == cudaSuccess) e = launch_kernel(embed_bulk_kernel<T>, dim3((unsigned)q.ctas), BULK_THREADS, smem, st, q);
     }
   } else {
-    q.shape = shape_of(accesses, EACH<V>);
+    // (entry by entry, four a thread where each SM has several CTAs all the same)
+    const bool four = V == 1 && chunks * accesses >= (int64_t)dev.sm_count * THREADS * 4 * 8;
+    q.shape = shape_of(accesses, four ? 4 : 1);
     q.shape.groups = std::min(q.shape.groups, GROUPS);
     q.sum_ctas = (chunks * q.shape.slabs + q.shape.groups - 1) / q.shape.groups;
     q.ctas = q.sum_ctas + zero_ctas;
     const unsigned threads = (unsigned)((q.shape.tpr * q.shape.groups + 31) / 32 * 32);
-    if (e == cudaSuccess) e = launch_kernel(embed_reduce_kernel<T, V>, dim3((unsigned)q.ctas), threads, 0, st, q);
+    if (e == cudaSuccess && !four) e = launch_kernel(embed_reduce_kernel<T, V, 1>, dim3((unsigned)q.ctas), threads, 0, st, q);
+    if constexpr (V == 1) {
+      if (e == cudaSuccess && four) e = launch_kernel(embed_reduce_kernel<T, V, 4>, dim3((unsigned)q.ctas), threads, 0, st, q);
+    }
   }
   if (e == cudaSuccess && longs) {
     int tx = 1;

@@ -391,6 +391,10 @@ struct RowRing {
       if (i < mats) copy_row(at + (size_t)(x * mats + i) * bytes, p[i], bytes, &full[x]);
   }
   __device__ __forceinline__ void wait() { ok = ok && mbar_wait_bounded(&full[s], phase); }
+  // after a timeout: one thread waits, each time with a limit, for the copies in flight
+  __device__ __forceinline__ void drain() {
+    for (int x = 0; x < stages; ++x) mbar_wait_bounded(&full[x], x < s ? phase ^ 1u : phase);
+  }
   __device__ __forceinline__ void next() {
     if (++s == stages) {
       s = 0;
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(warp_mean, warp_square);
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
     // (every thread of the group has read the row)
-    if (r.t == 0) fill(ring.s, row + stages * step);
+    if (r.t == 0 && ring.ok) fill(ring.s, row + stages * step);
     ring.next();
     const int w0 = group * (tpr >> 5), wn = tpr >> 5;
     float mean = 0.f, square = 0.f;
@@ -510,6 +514,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid
     for (int i = 0; i < CH; ++i)
       if (r.has(i)) Raw<T, V>::store_pairs(out + r.at(i), x + i * V / 2);
   }
+  if (!ring.ok && r.t == 0) ring.drain();
 }
 
 // A thread's column sums, over the groups in turn, to the CTA's part (or dw and db, of one CTA).
@@ -598,7 +603,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
       s2 = fma2(h[i], u[i], s2);
     }
     const float2 s = sum(make_float2(unpack2(s1).x + unpack2(s1).y, unpack2(s2).x + unpack2(s2).y));
-    if (r.t == 0) fill(ring.s, row + stages * step);
+    if (r.t == 0 && ring.ok) fill(ring.s, row + stages * step);
     ring.next();
     if (!ring.ok || !a.DX) continue;
     const float c1 = -s.x * over, c2 = -s.y * over;
@@ -619,6 +624,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
       Raw<T, V>::store_pairs(out + r.at(i), v);
     }
   }
+  if (!ring.ok && r.t == 0) ring.drain();
   if constexpr (SUMS) {
     float x[E], y[E];
 #pragma unroll
@@ -670,6 +676,10 @@ struct OddRing {
       }
   }
   __device__ __forceinline__ void wait() { ok = ok && mbar_wait_bounded(&full[s], phase); }
+  // after a timeout: one thread waits, each time with a limit, for the copies in flight
+  __device__ __forceinline__ void drain() {
+    for (int x = 0; x < stages; ++x) mbar_wait_bounded(&full[x], x < s ? phase ^ 1u : phase);
+  }
   __device__ __forceinline__ void next() {
     if (++s == stages) {
       s = 0;
@@ -740,7 +750,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_
     for (int i = 0; i < CH; ++i) s += x[i];
     const float mean = sum(make_float2(s, 0.f)).x * over;
     // (every thread of the group has read the row)
-    if (t == 0) fill(ring.s, row + stages * step);
+    if (t == 0 && ring.ok) fill(ring.s, row + stages * step);
     ring.next();
     s = 0.f;
 #pragma unroll
@@ -759,6 +769,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_
     for (int i = 0; i < CH; ++i)
       if (t + i * tpr < n) out[t + i * tpr] = from_f32<T>(fmaf(x[i] * rstd, w[i], b[i]));
   }
+  if (!ring.ok && t == 0) ring.drain();
 }
 
 template <typename T, int CH, bool SUMS>
@@ -819,7 +830,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_odd_kernel(const __
       s.y = fmaf(h[i], u[i], s.y);
     }
     s = sum(s);
-    if (t == 0) fill(ring.s, row + stages * step);
+    if (t == 0 && ring.ok) fill(ring.s, row + stages * step);
     ring.next();
     if (!ring.ok || !a.DX) continue;
     const float c1 = s.x * over, c2 = s.y * over;
@@ -828,6 +839,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_odd_kernel(const __
     for (int i = 0; i < CH; ++i)
       if (t + i * tpr < n) out[t + i * tpr] = from_f32<T>(fmaf(fmaf(-u[i], c2, h[i] - c1), rstd, a.R ? res[i] : 0.f));
   }
+  if (!ring.ok && t == 0) ring.drain();
   if constexpr (SUMS)
     store_columns<T, 1, CH>(a, RowOf<T, 1, CH>(t, tpr, a.n), group, shape.groups, dw, db, reinterpret_cast<float*>(smem));
 }
@@ -898,7 +910,11 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
     fetch(tile + step);
     const int here = (int)min((int64_t)rows, a.m - row0);  // the tile's rows
     ok = __all_sync(FULL_MASK, ok && mbar_wait_bounded(&full[s], phase));
-    if (!ok) break;  // FXTX_ERR_TIMEOUT is raised
+    if (!ok) {  // FXTX_ERR_TIMEOUT is raised; the other copies in flight land before the CTA leaves
+      if (lane == 0)
+        for (int x = 0; x < stages; ++x) mbar_wait_bounded(&full[x], x < s ? phase ^ 1u : phase);
+      break;
+    }
     const unsigned char* x_at = at + (size_t)s * mats * slot + t * 16;
 #pragma unroll 1
     for (int r0 = 0; r0 < here; r0 += 2 * groups) {
