@@ -54,7 +54,8 @@ def test_gradients_against_autograd(m, classes, hidden, layers, tokens, slots, n
     got, kept = net.loss(X, labels)
     inside = (labels >= 0) & (labels < classes)
     assert not got[~inside].any()
-    assert abs(float(got.double().sum() / inside.sum()) - float(loss)) <= tol * abs(float(loss))
+    loss = float(loss.detach())
+    assert abs(float(got.double().sum() / inside.sum()) - loss) <= tol * abs(loss)
     assert float((net.logits(X).double() - logits.detach()).norm() / logits.detach().norm()) <= tol
     grads = solvers._mean_loss_gradients(net, labels, kept)
     for name, a, b in zip(net.params, grads, want):
