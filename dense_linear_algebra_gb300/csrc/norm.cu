@@ -4,16 +4,22 @@
 //
 // Bound: HBM; every matrix is read or written once. A row lies in the registers of `tpr` threads (1 to 32 neighbouring
 // lanes, or whole warps that meet at a named barrier), CH accesses of 16 bytes each, so that the variance is formed
-// from x - mean, in a second sum, without reading x again. A CTA has `groups` such rows in work at once and takes rows
-// in turn; the next row's loads are issued before the present one's sums. The columns of a thread stay the same from
-// row to row, so dw and db are summed in its registers, over the CTA's groups in shared memory, in turn, and over the
-// CTAs by a second kernel in order: the result is the same on every call.
+// from x - mean without reading x again. A CTA has `groups` such rows in work at once and takes rows in turn. The columns of a
+// thread stay the same from row to row, so dw and db are summed in its registers, over the CTA's groups in shared memory, in
+// turn, and over the CTAs by a second kernel in order: the result is the same on every call.
 //
-// Rows beyond what the registers hold take more passes: the forward pass reads x three times (one CTA a row), the
-// gradient forms mean(h) and mean(h u) in one pass and dx and the column sums in another.
-//
-// Matrices whose start, pitch or width is no multiple of 16 bytes go entry by entry (V = 1), neighbouring threads
-// taking neighbouring entries.
+// Which kernel, by the rows' number, width and alignment (bytes in all: 16384 x 4096 bfloat16 268 MB forward, 537 MB backward with
+// the residual path; 1,000,000 x 32 float32 384 MB backward):
+//   norm_ring_kernel, norm_grad_ring_kernel   many rows of more than a warp's accesses: bulk copies bring a group's next rows into a
+//              ring; 51 us (5.3 TB/s: the instructions of 16 warps a SM) and 85 us (6.3 TB/s); the register kernels 57 and 138 us
+//   norm_grad_short_kernel   many rows of at most 32 accesses: a ring of tiles a warp; 68 us (5.6 TB/s), in registers 90
+//   norm_odd_kernel, norm_grad_odd_kernel   many rows whose pitch or width is no multiple of 16 bytes, of 129 to 8,192 entries;
+//              30,001 x 2047 bfloat16 109 and 174 us, entry by entry from memory 218 and 564
+//   norm_kernel, norm_grad_kernel   the others: rows loaded into registers, the next one ahead; one row of 4096 3.3 us
+//   norm_long_kernel and norm_long_means_kernel, norm_long_grad_kernel   rows beyond what the registers hold (16 bits: 32,768
+//              forward, 8,192 backward; float32 half and the same): x read three times, one CTA a row; backward the two means in
+//              one pass, dx and the column sums in another
+// Rows that go entry by entry (V = 1) have neighbouring threads take neighbouring entries.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
