@@ -307,6 +307,7 @@ const void* labels_at(const LossArgs& a, int64_t r) { return static_cast<const c
 // no row of the tile wasted), or for float32 the CUDA cores. The gradient of float32 rows that those do not take forms
 // W's planes once for all of its products instead.
 bool few_logits(const LayerArgs& l, bool grad) {
+  if (l.m * l.k * 4 > kSmallCap) return false;
   if (l.type == FXTX_F32) return grad ? few_rows(l.type, l.m, l.w_trans) : l.m <= kFewLogitsF32;
   return l.m <= (grad ? kFewLogitsGrad : kFewLogits) && packed_bytes(l.type, l.W, l.ldw, l.n) == 0;
 }

@@ -1050,17 +1050,15 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(const __grid_constant__
   if (to) to[c < a.n ? c : c - a.n] = from_f32<T>(s);
 }
 
-// A CTA's sum of two doubles, the same in every thread.
-__device__ __forceinline__ double2 cta_sum(double x, double y, double2* red) {
+// A CTA's sums of two values, the same in every thread. (In doubles this took 5 us a row: two of them a cycle and SM.)
+__device__ __forceinline__ float2 cta_sum(float x, float y, float2* red) {
+  x = group_sum<32>(x);
+  y = group_sum<32>(y);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(x, y);
+  __syncthreads();
+  float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x += shfl_xor(x, o);
-    y += shfl_xor(y, o);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_double2(x, y);
-  __syncthreads();
-  double2 s = make_double2(0.0, 0.0);
   for (int w = 0; w < LONG_THREADS / 32; ++w) {
     s.x += red[w].x;
     s.y += red[w].y;
@@ -1071,7 +1069,7 @@ __device__ __forceinline__ double2 cta_sum(double x, double y, double2* red) {
 // Rows of any length, one CTA a row at a time. A thread's sums leave fp32 after 16 accesses.
 template <typename T, int V>
 __global__ void __launch_bounds__(LONG_THREADS) norm_long_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ double2 red[LONG_THREADS / 32];
+  __shared__ float2 red[LONG_THREADS / 32];
   after_previous();
   const int64_t accesses = a.n / V;
   for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
@@ -1093,10 +1091,10 @@ __global__ void __launch_bounds__(LONG_THREADS) norm_long_kernel(const __grid_co
         }
         s += p;
       }
-      return cta_sum(s, 0.0, red).x;
+      return cta_sum((float)s, 0.f, red).x;
     };
-    const float mean = (float)(total([](float v) { return v; }) / (double)a.n);
-    const float var = (float)(total([&](float v) { return (v - mean) * (v - mean); }) / (double)a.n);
+    const float mean = total([](float v) { return v; }) / (float)a.n;
+    const float var = total([&](float v) { return (v - mean) * (v - mean); }) / (float)a.n;
     const float rstd = __frsqrt_rn(var + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
@@ -1130,32 +1128,44 @@ __global__ void __launch_bounds__(LONG_THREADS) norm_long_kernel(const __grid_co
 // The gradient of long rows, first pass: mean(h) and mean(h u) of each row.
 template <typename T, int V>
 __global__ void __launch_bounds__(LONG_THREADS) norm_long_means_kernel(const __grid_constant__ NormArgs a, float2* means) {
-  __shared__ double2 red[LONG_THREADS / 32];
+  __shared__ float2 red[LONG_THREADS / 32];
   after_previous();
   const int64_t accesses = a.n / V;
   for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x) {
     const T *x = static_cast<const T*>(a.X) + row * a.ldx, *g = static_cast<const T*>(a.G) + row * a.ldg;
     const float mean = a.mean_in[row], rstd = a.rstd_in[row];
     double s = 0.0, t = 0.0;
-    for (int64_t c0 = threadIdx.x; c0 < accesses; c0 += 16 * LONG_THREADS) {
-      float p = 0.f, o = 0.f;
-#pragma unroll 2
-      for (int i = 0; i < 16; ++i) {
+    // four accesses of each on their way at a time
+    constexpr int U = 4;
+    for (int64_t c0 = threadIdx.x; c0 < accesses; c0 += U * LONG_THREADS) {
+      Raw<T, V> xr[U], gr[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
         const int64_t c = c0 + (int64_t)i * LONG_THREADS;
-        if (c >= accesses) break;
-        Raw<T, V> raw;
+        xr[i].zero();
+        gr[i].zero();
+        if (c < accesses) {
+          xr[i].load(x + c * V);
+          gr[i].load(g + c * V);
+        }
+      }
+      float p = 0.f, o = 0.f;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t c = c0 + (int64_t)i * LONG_THREADS;
         float v[V], h[V], y[V];
-        raw.load(x + c * V);
-        raw.values(v);
-        raw.load(g + c * V);
-        raw.values(h);
-        if (a.w) {
+        xr[i].values(v);
+        gr[i].values(h);
+        if (a.w && c < accesses) {
+          Raw<T, V> raw;
           raw.load(static_cast<const T*>(a.w) + c * V);
           raw.values(y);
+#pragma unroll
+          for (int q = 0; q < V; ++q) h[q] *= y[q];
         }
+        // (beyond the row's end h is zero)
 #pragma unroll
         for (int q = 0; q < V; ++q) {
-          if (a.w) h[q] *= y[q];
           p += h[q];
           o = fmaf(h[q], (v[q] - mean) * rstd, o);
         }
@@ -1163,8 +1173,8 @@ __global__ void __launch_bounds__(LONG_THREADS) norm_long_means_kernel(const __g
       s += p;
       t += o;
     }
-    const double2 all = cta_sum(s, t, red);
-    if (threadIdx.x == 0) means[row] = make_float2((float)(all.x / (double)a.n), (float)(all.y / (double)a.n));
+    const float2 all = cta_sum((float)s, (float)t, red);
+    if (threadIdx.x == 0) means[row] = make_float2(all.x / (float)a.n, all.y / (float)a.n);
   }
 }
 
@@ -1182,7 +1192,7 @@ __global__ void __launch_bounds__(256) norm_long_grad_kernel(const __grid_consta
     raw.values(w);
   }
   const int64_t end = min(a.m, (part + 1) * rows);
-#pragma unroll 2
+#pragma unroll 4
   for (int64_t row = part * rows; row < end; ++row) {
     float u[V], g[V], y[V];
     raw.load(static_cast<const T*>(a.X) + row * a.ldx + j);
