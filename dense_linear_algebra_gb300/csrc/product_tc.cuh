@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
                       const __grid_constant__ TcArgs a, const __grid_constant__ ModeArgs<MODE> mode) {
   using C = TileCfg<CG, BN, PL>;
   // the pieces of a sum are added up in registers, each freeing its accumulator: float32, and logits, whose pieces are short
-  constexpr bool REGS = PL == 3 || (MODE == 1 && LONG);
+  constexpr bool REGS = PL == 3 || ((MODE == 1 || MODE == 2) && LONG);
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
@@ -729,13 +729,16 @@ cudaError_t launch_persistent(const TcPlan& plan, const CUtensorMap& am, const C
   return cudaErrorInvalidConfiguration;
 }
 
-// A product of one of the modes above 0 whose sums are in one piece.
+// A product of logits (modes 1 and 2), whose kk is not split. Both modes take the same sums, since the gradient's exponentials are
+// divided by the sum that the loss had of them: with pieces of FOLD in mode 2 alone, logits of 8,192 positive terms around 400 gave
+// probabilities 1.2 (bfloat16) and 2.1 % (float16) too small. What it costs mode 2, whose epilogue holds one accumulator for longer:
+// 8192 x 2048, 32,768 classes 580 to 635 us.
 template <typename T, int MODE>
 fxtx_status_t run_mode(const PlanesProduct& p, const ModeArgs<MODE>& mode, const DeviceInfo& dev, cudaStream_t st) {
   const TcPlan plan = plan_persistent(p.M, p.N, p.K, std::is_same<T, float>::value ? 3 : 1, p.A.mn_major, p.B.mn_major, dev.sm_count, 1);
   TcArgs a;
   CUtensorMap am, bm;
-  const fxtx_status_t s = prepare_product<T>(p, plan, a, am, bm, MODE == 1 ? LOGIT_FOLD : FOLD);
+  const fxtx_status_t s = prepare_product<T>(p, plan, a, am, bm, LOGIT_FOLD);
   if (s != FXTX_OK) return s;
   if (launch_persistent<T, MODE>(plan, am, bm, a, mode, dev.sm_count, st) == cudaSuccess) return FXTX_OK;
   cudaGetLastError();
