@@ -14,8 +14,8 @@
 // of float32 as three bfloat16 planes) and its column sums; D W^T, added up over the pieces in fp32; X^T D, over the slabs.
 //
 // float16 has nothing below 6e-8, where a mean's gradient over many classes lies: D is held multiplied by the power of
-// two that brings the largest |g| to 2^14 .. 2^15, which the last of the sums takes back. What is lost is below 2^-39 of
-// that |g| (below 2^-29 of it, digits are).
+// two that brings the largest |g| of a row with a label to 2^14 .. 2^15, which the last of the sums takes back. What is lost is below
+// 2^-39 of that |g| (below 2^-29 of it, digits are).
 //
 // At most 64 features and classes: thin_loss.cu, and thin_loss_f32.cu. Few rows: z is written out in fp32, its statistics or D
 // formed by kernels of their own, and the products are those of few rows.
@@ -181,25 +181,44 @@ __global__ void __launch_bounds__(256) row_slope_kernel(const FewLogits f, const
   if (db) db[j] = from_f32<T>(scales ? sum * scales[1] : sum);
 }
 
-__global__ void __launch_bounds__(1024) scales_kernel(const float* g, int64_t m, float gain, float* scales) {
+// The powers of two that float16's D is held at, from the largest |g| of a row that has a label (as its bits: magnitudes order as
+// integers do, a NaN above all).
+__device__ __forceinline__ void set_scales(uint32_t most, float gain, float* scales) {
+  const float top = __uint_as_float(most) * fabsf(gain);
+  int e = 14;
+  if (top > 0.f && top <= 3.4e38f) e = min(max(ilogbf(top), -100), 120);
+  scales[0] = scalbnf(1.f, 14 - e);
+  scales[1] = scalbnf(1.f, e - 14);
+}
+
+// A CTA's part of the rows; a single one's is all. (1,000,000 x 32, 10 classes: 54 us in all; one CTA for all weights 116.)
+__global__ void __launch_bounds__(1024) largest_kernel(const void* labels, bool labels64, int64_t count, const float* g, int64_t m,
+                                                       float gain, float* scales) {
   __shared__ uint32_t warps[32];
   after_previous();
-  // magnitudes as integers order as they are; a NaN is above all
-  uint32_t most = g ? 0u : __float_as_uint(1.f);
-  if (g) {
+  uint32_t most = 0;
+  const int64_t step = (int64_t)gridDim.x * 1024;
 #pragma unroll 4
-    for (int64_t i = threadIdx.x; i < m; i += 1024) most = max(most, __float_as_uint(g[i]) & 0x7fffffffu);
+  for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < m; i += step) {
+    const uint32_t bits = __float_as_uint(g[i]) & 0x7fffffffu;
+    most = max(most, label_at(labels, labels64, i, count) >= 0 ? bits : 0u);
   }
   most = __reduce_max_sync(FULL_MASK, most);
   if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = most;
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int w = 1; w < 32; ++w) most = max(most, warps[w]);
-  const float top = __uint_as_float(most) * fabsf(gain);
-  int e = 14;
-  if (top > 0.f && top <= 3.4e38f) e = min(max(ilogbf(top), -100), 120);
-  scales[0] = scalbnf(1.f, 14 - e);
-  scales[1] = scalbnf(1.f, e - 14);
+  if (gridDim.x == 1) set_scales(most, gain, scales);
+  else reinterpret_cast<uint32_t*>(scales)[2 + blockIdx.x] = most;
+}
+
+// The same from `parts` CTAs' parts; without any (no weights) from 1.
+__global__ void __launch_bounds__(32) scales_kernel(int parts, float gain, float* scales) {
+  after_previous();
+  uint32_t most = parts ? 0u : __float_as_uint(1.f);
+  for (int i = threadIdx.x; i < parts; i += 32) most = max(most, reinterpret_cast<const uint32_t*>(scales)[2 + i]);
+  most = __reduce_max_sync(FULL_MASK, most);
+  if (threadIdx.x == 0) set_scales(most, gain, scales);
 }
 
 // db from the column sums of D: 32 columns a CTA, 8 threads a column, in order; over the slabs through `keep`.
@@ -373,11 +392,11 @@ fxtx_status_t few_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& 
   const int64_t parts = f32 ? 1 : raw_parts(logits_product(l, x.x), dev), pitch = (l.k + 7) / 8 * 8;
   const size_t z_bytes = up(parts * l.m * l.k * 4), d_bytes = up(l.m * pitch * type_size(l.type));
   char* ws = nullptr;
-  if (s == FXTX_OK) s = alloc_pooled(reinterpret_cast<void**>(&ws), z_bytes + d_bytes + 256, st);
+  if (s == FXTX_OK) s = alloc_pooled(reinterpret_cast<void**>(&ws), z_bytes + d_bytes + kScaleBytes, st);
   float* z = reinterpret_cast<float*>(ws);
   T* D = reinterpret_cast<T*>(ws + z_bytes);
   float* scales = l.type == FXTX_F16 ? reinterpret_cast<float*>(ws + z_bytes + d_bytes) : nullptr;
-  if (s == FXTX_OK && scales) s = status_of(launch_scales(a.g, l.m, a.gain, scales, st));
+  if (s == FXTX_OK && scales) s = status_of(launch_scales(a, l.m, l.k, scales, st));
   if (s == FXTX_OK) s = run_logits(l, x.x, z, dev, st);
   if (s == FXTX_OK)
     s = status_of(launch_kernel(row_slope_kernel<T>, dim3((unsigned)((l.k + 255) / 256)), 256, 0, st,
@@ -438,8 +457,14 @@ fxtx_status_t few_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& 
 
 }  // namespace
 
-cudaError_t launch_scales(const float* g, int64_t m, float gain, float* scales, cudaStream_t st) {
-  return launch_kernel(scales_kernel, dim3(1), 1024, 0, st, g, m, gain, scales);
+cudaError_t launch_scales(const LossArgs& a, int64_t m, int64_t k, float* scales, cudaStream_t st) {
+  int parts = 0;
+  if (a.g) {
+    parts = (int)std::min<int64_t>(kScaleParts, (m + 8191) / 8192);  // (of 8 rows a thread)
+    const cudaError_t e = launch_kernel(largest_kernel, dim3((unsigned)parts), 1024, 0, st, a.labels, a.labels64, k, a.g, m, a.gain, scales);
+    if (e != cudaSuccess || parts == 1) return e;
+  }
+  return launch_kernel(scales_kernel, dim3(1), 32, 0, st, parts, a.gain, scales);
 }
 
 fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
@@ -542,7 +567,7 @@ fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceI
     dw_sum = reinterpret_cast<float*>(c.take(a.DW && slabs > 1 ? Vp * l.n * 4 : 0));
     db_parts = reinterpret_cast<float*>(c.take(a.DB ? (mc + 31) / 32 * Vp * 4 : 0));
     db_sum = reinterpret_cast<float*>(c.take(a.DB && slabs > 1 ? Vp * 4 : 0));
-    scales = reinterpret_cast<float*>(c.take(l.type == FXTX_F16 ? 8 : 0));
+    scales = reinterpret_cast<float*>(c.take(l.type == FXTX_F16 ? kScaleBytes : 0));
     if (pass == 0) {
       const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&ws), c.bytes, st);
       if (s != FXTX_OK) return s;
@@ -551,7 +576,7 @@ fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceI
     }
   }
   fxtx_status_t s = FXTX_OK;
-  if (scales) s = status_of(launch_scales(a.g, l.m, a.gain, scales, st));
+  if (scales) s = status_of(launch_scales(a, l.m, l.k, scales, st));
   for (int64_t v = 0; v < l.k && s == FXTX_OK; v += Vp) {
     const int64_t n = std::min(Vp, l.k - v);
     const Part w = classes_of(l, v, n, w_at);

@@ -88,8 +88,10 @@ bool tall_loss_shape(const LayerArgs& l);
 fxtx_status_t run_tall_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_tall_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
-// scales[0] = a power of two that brings |gain| max |g| to 2^14 .. 2^15, scales[1] its inverse (1 and 1 where that is zero
-// or not finite).
-cudaError_t launch_scales(const float* g, int64_t m, float gain, float* scales, cudaStream_t st);
+// scales[0] = a power of two that brings |gain| max |g| over the rows with a label to 2^14 .. 2^15, scales[1] its inverse (1 and 1 where
+// that is zero or not finite). What a row that is left out has for g does not count. `scales` has kScaleBytes.
+constexpr int kScaleParts = 128;
+constexpr int64_t kScaleBytes = (2 + kScaleParts) * 4;
+cudaError_t launch_scales(const LossArgs& a, int64_t m, int64_t k, float* scales, cudaStream_t st);
 
 }  // namespace fxtx

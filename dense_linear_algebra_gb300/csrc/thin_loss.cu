@@ -110,9 +110,9 @@ fxtx_status_t run_thin_loss_grad(const LayerArgs& l, const LossArgs& q, const De
   a.DB = q.DB;
   float* scales = nullptr;
   if (l.type == FXTX_F16) {
-    const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&scales), 8, st);
+    const fxtx_status_t s = alloc_pooled(reinterpret_cast<void**>(&scales), kScaleBytes, st);
     if (s != FXTX_OK) return s;
-    if (launch_scales(q.g, l.m, q.gain, scales, st) != cudaSuccess) {
+    if (launch_scales(q, l.m, l.k, scales, st) != cudaSuccess) {
       cudaGetLastError();
       cudaFreeAsync(scales, st);
       return FXTX_ERR_CUDA;

@@ -171,9 +171,9 @@ def cross_entropy_grad(X, W, labels, lse, b=None, g=1.0, need=(True, True, True)
     ``g`` is the gradient at the losses: a number for all rows (1 / m for their mean), or an (m,) float32 tensor.
     ``need`` says which of the three are computed; the others come back as None. z is formed again, in pieces of the
     classes. D of a 16-bit type is rounded to it before the products; of float16 it is held multiplied by a power of two
-    that brings the largest |g_i| to 2^14 .. 2^15, so that what is below 2^-39 of that is lost. db is summed from the
-    unrounded values. dW is stored as W is: for W = P.t() it is the transposed view of a (k, n) tensor. Types, layouts,
-    labels and streams are those of ``cross_entropy``.
+    that brings the largest |g_i| of a row with a label to 2^14 .. 2^15, so that what is below 2^-39 of that is lost. db is
+    summed from the unrounded values. dW is stored as W is: for W = P.t() it is the transposed view of a (k, n) tensor.
+    Types, layouts, labels and streams are those of ``cross_entropy``.
     """
     if stream is not None:
         context, stream = _on_stream(stream, X.get_device())

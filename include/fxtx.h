@@ -493,9 +493,9 @@ fxtx_status_t fxtx_embedding_grad(fxtx_type_t type, int64_t m, int64_t n, int64_
  * G: m fp32 values, or NULL for ones (a mean's gain is 1 / m). Each of DX, DW, DB may be NULL (not computed). DW is
  * stored as W is. z is formed again; D of a 16-bit type is rounded to it before the products (with more than 64
  * features or classes held in pieces of up to 512 MB), float16 multiplied by a power of two that brings the largest
- * |gain G_i| to 2^14 .. 2^15: what is below 2^-39 of that is lost. DB is summed from the unrounded values. m = 0 gives
- * DW = 0 and DB = 0. DW takes every row of X: what is not finite there reaches it, although the row is left out. Outputs must
- * not overlap anything else. Precision and errors are those of fxtx_linear, but for 16-bit logits, whose sums leave the tensor
+ * |gain G_i| of a row with a label to 2^14 .. 2^15: what is below 2^-39 of that is lost. DB is summed from the unrounded
+ * values. m = 0 gives DW = 0 and DB = 0. DW takes every row of X: what is not finite there reaches it, although the row is
+ * left out; G and LSE of such a row have no say. Outputs must not overlap anything else. Precision and errors are those of fxtx_linear, but for 16-bit logits, whose sums leave the tensor
  * cores every 1,024 features (z is short by up to 6e-6 of the sum of its terms).
  */
 fxtx_status_t fxtx_cross_entropy(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,

@@ -1,5 +1,5 @@
 """Layer norm, the embedding lookup, cross entropy and their gradients where one of them was wrong or took too much: long logits of
-terms of one sign."""
+terms of one sign, weights of rows that are left out."""
 import pytest
 import torch
 
@@ -48,3 +48,39 @@ def test_logits_of_terms_of_one_sign(m, k, n, dtype):
     total = float(D.sum()) / 64
     slack = m * ((2 * float((lse[:, None] - z).max()) + 8 + 8 + 4 * k**0.5 + 40) * U + 2 * U * S) + W_OF[dtype] * float(D.abs().sum()) / 64
     assert abs(total) <= slack, (total, slack)
+
+
+@pytest.mark.parametrize("m,n,k", [(200, 40, 20), (3, 100, 300), (200, 100, 300), (8193, 24, 10), (40_000, 72, 70)])
+@pytest.mark.parametrize("weight", [1e20, float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_weights_of_rows_without_a_label(m, n, k, weight, dtype):
+    """They have no say, in the power of two that float16's D is held at neither.
+
+    db is D's sum: of each entry z and lse are off by at most 2.5e-5 (48 u S, S below 9), the exponential by 2e-6, the sum by 5e-5
+    ((8 + 4 sqrt(m)) u): 1e-4 of the magnitudes' sum.
+    """
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(m)
+    X = torch.randn(m, n, generator=gen, device="cuda").to(dtype)
+    W = (torch.randn(k, n, generator=gen, device="cuda") / n**0.5).to(dtype).t()
+    labels = torch.randint(0, k, (m,), generator=gen, device="cuda")
+    out = torch.arange(m, device="cuda") % 3 == 1
+    labels[out] = torch.where(torch.arange(int(out.sum()), device="cuda") % 2 == 0, -1, k)
+    _, lse = fx.cross_entropy(X, W, labels)
+    # the largest weight stands in the last row that has a label, behind many others
+    g = torch.full((m,), 1e-3, device="cuda")
+    g[int((~out).nonzero()[-1])] = 3e-2
+    g[out] = 0
+    want = fx.cross_entropy_grad(X, W, labels, lse, g=g)
+    g[out] = weight
+    got = fx.cross_entropy_grad(X, W, labels, lse, g=g)
+    assert all(torch.equal(a, b) and torch.isfinite(a).all() for a, b in zip(got, want))
+    z = X.double() @ W.double()
+    D = torch.exp(z - torch.logsumexp(z, 1, keepdim=True))
+    D[torch.arange(m, device="cuda"), torch.where(out, 0, labels)] -= 1
+    D *= torch.where(out, 0.0, g.double())[:, None]
+    tol = (W_OF[dtype] * D.sum(0).abs() + 1e-4 * D.abs().sum(0)) + (2.0**-25 if dtype is torch.float16 else 0)
+    assert bool(((got[2].double() - D.sum(0)).abs() <= tol).all())
+    # all rows left out: nothing
+    none = fx.cross_entropy_grad(X, W, torch.full_like(labels, -1), lse, g=torch.full((m,), weight, device="cuda"))
+    assert not any(t.any() for t in none)
