@@ -596,10 +596,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
     if (a.R) r.load(ring.row(2), 0, 1, 0, res);
     const f2 minus = pack2(-mean, -mean), scale = pack2(rstd, rstd);
     f2 s1 = 0, s2 = 0;
-    // (beyond the row's end g is zero, and u counts for nothing unless the whole row is no number)
+    // (beyond the row's end x and g are zero, and mean is taken as zero there: -mean rstd may be beyond fp32 where u is not)
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      u[i] = mul2(add2(u[i], minus), scale);
+      u[i] = mul2(add2(u[i], r.has(i / (V / 2)) ? minus : 0), scale);
       if constexpr (SUMS) {
         dw[i] = fma2(h[i], u[i], dw[i]);
         db[i] = add2(db[i], h[i]);
@@ -693,15 +693,16 @@ struct OddRing {
     }
   }
   // the thread's entries of the row at p
+  // (`beyond` for what lies beyond its end)
   template <int CH>
-  __device__ __forceinline__ void load(int mat, const T* p, int t, int tpr, int n, bool last, float (&x)[CH]) const {
+  __device__ __forceinline__ void load(int mat, const T* p, int t, int tpr, int n, bool last, float (&x)[CH], float beyond = 0.f) const {
     const T* row = reinterpret_cast<const T*>(at + (size_t)(s * mats + mat) * slot + head(p));
     if (!last) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
         const int j = t + i * tpr;
         x[i] = to_f32(row[j < n ? j : 0]);
-        if (j >= n) x[i] = 0.f;
+        if (j >= n) x[i] = beyond;
       }
       return;
     }
@@ -709,7 +710,7 @@ struct OddRing {
 #pragma unroll 1
     for (int i = 0; i < CH; ++i) {
       const int j = t + i * tpr;
-      const float v = j < there ? to_f32(row[j]) : j < n ? to_f32(p[j]) : 0.f;
+      const float v = j < there ? to_f32(row[j]) : j < n ? to_f32(p[j]) : beyond;
 #pragma unroll
       for (int q = 0; q < CH; ++q) x[q] = q == i ? v : x[q];
     }
@@ -819,11 +820,11 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_odd_kernel(const __
     }
     ring.wait();
     float u[CH], h[CH], res[CH];
-    ring.load(0, x_at(row), t, tpr, n, last, u);
+    ring.load(0, x_at(row), t, tpr, n, last, u, mean);
     ring.load(1, g_at(row), t, tpr, n, last, h);
     if (a.R) ring.load(2, r_at(row), t, tpr, n, last, res);
     float2 s = make_float2(0.f, 0.f);
-    // (beyond the row's end g is zero, and u counts for nothing unless the whole row is no number)
+    // (beyond the row's end g is zero, and x mean: -mean rstd may be beyond fp32 where u is not)
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       u[i] = (u[i] - mean) * rstd;
@@ -945,9 +946,9 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
         x.pairs(u[i]);
         g.pairs(h[i]);
         res.pairs(y[i]);
-        const f2 minus = pack2(-mean, -mean), sc = pack2(scale[i], scale[i]);
+        const f2 minus = in && has ? pack2(-mean, -mean) : 0, sc = pack2(scale[i], scale[i]);
         f2 p1 = 0, p2 = 0;
-        // (beyond the row's end g is zero, and u counts for nothing unless the whole row is no number)
+        // (beyond the row's end x and g are zero, and mean is taken as zero there: -mean rstd may be beyond fp32 where u is not)
 #pragma unroll
         for (int q = 0; q < P; ++q) {
           u[i][q] = mul2(add2(u[i][q], minus), sc);
@@ -1163,7 +1164,7 @@ __global__ void __launch_bounds__(LONG_THREADS) norm_long_means_kernel(const __g
 #pragma unroll
           for (int q = 0; q < V; ++q) h[q] *= y[q];
         }
-        // (beyond the row's end h is zero)
+        if (c >= accesses) continue;  // (-mean rstd may be beyond fp32 where u is not)
 #pragma unroll
         for (int q = 0; q < V; ++q) {
           p += h[q];

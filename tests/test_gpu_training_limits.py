@@ -1,5 +1,5 @@
 """Layer norm, the embedding lookup, cross entropy and their gradients where one of them was wrong or took too much: long logits of
-terms of one sign, weights of rows that are left out."""
+terms of one sign, weights of rows that are left out, rows around a large mean."""
 import pytest
 import torch
 
@@ -84,3 +84,27 @@ def test_weights_of_rows_without_a_label(m, n, k, weight, dtype):
     # all rows left out: nothing
     none = fx.cross_entropy_grad(X, W, torch.full_like(labels, -1), lse, g=torch.full((m,), weight, device="cuda"))
     assert not any(t.any() for t in none)
+
+
+# a register, a ring, a short, an odd and a long row's kernel, each with threads beyond the row's end
+@pytest.mark.parametrize("m,n,dtype", [(9, 301, torch.float32), (9, 280, torch.bfloat16), (3100, 1160, torch.float32), (5000, 280, torch.bfloat16),
+                                       (62_300, 20, torch.float32), (120_000, 24, torch.bfloat16), (5000, 301, torch.float32), (3001, 2047, torch.bfloat16),
+                                       (5, 10_000, torch.float32), (5, 9001, torch.bfloat16)])
+def test_norm_of_rows_around_a_large_mean(m, n, dtype):
+    """mean rstd is beyond fp32 (1e39), x - mean is zero: u is zero, and dX = rstd (g - avg g) + r.
+
+    avg g is off by C = 80 roundings of avg |g|, as in the norm's other tests, the rest by three of each term.
+    """
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n)
+    X = torch.full((m, n), 1e36, device="cuda").to(dtype)
+    G, R = (torch.randn(m, n, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    mean, rstd = X[:, 0].float().contiguous(), torch.full((m,), 1e3, device="cuda")
+    dX, dw, db = fx.layer_norm_grad(G, X, None, mean, rstd, residual=R)
+    g, r = G.double(), R.double()
+    c = g.mean(1, keepdim=True)
+    want = 1e3 * (g - c) + r
+    tol = 1e3 * (80 * U * g.abs().mean(1, keepdim=True) + 4 * U * (g.abs() + c.abs())) + 2 * U * r.abs()
+    err = (dX.double() - want).abs()
+    assert bool((err <= tol + W_OF[dtype] * (want.abs() + tol)).all())
+    assert not dw.any() and bool(((db.double() - g.sum(0)).abs() <= (8 + 4 * m**0.5) * U * g.abs().sum(0) + W_OF[dtype] * g.sum(0).abs() * 1.001).all())
