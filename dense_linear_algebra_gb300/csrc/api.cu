@@ -25,13 +25,16 @@ constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 std::once_flag g_dev_once[kMaxDevices];
 
-// Test hooks: FXTX_FAIL_ALLOC=1 makes every workspace allocation fail, FXTX_FAIL_POOL=1 the
-// creation of the pool that some come from (host side).
+// Test hooks: FXTX_FAIL_ALLOC=1 makes every workspace allocation fail, FXTX_FAIL_ALLOC_ABOVE=<bytes> those of more,
+// FXTX_FAIL_POOL=1 the creation of the pool that some come from (host side).
 bool set_to_1(const char* name) {
   const char* s = getenv(name);
   return s && s[0] == '1';
 }
-bool fail_alloc() { return set_to_1("FXTX_FAIL_ALLOC"); }
+bool fail_alloc(size_t bytes) {
+  const char* most = getenv("FXTX_FAIL_ALLOC_ABOVE");
+  return set_to_1("FXTX_FAIL_ALLOC") || (most && most[0] && bytes > strtoull(most, nullptr, 10));
+}
 bool fail_pool() { return set_to_1("FXTX_FAIL_POOL"); }
 
 }  // namespace
@@ -70,7 +73,7 @@ bool log_enabled() {
 fxtx_status_t alloc_ws(void** p, size_t bytes, cudaStream_t st) {
   *p = nullptr;
   if (bytes == 0) return FXTX_OK;
-  if (fail_alloc()) return FXTX_ERR_ALLOC;
+  if (fail_alloc(bytes)) return FXTX_ERR_ALLOC;
   if (cudaMallocAsync(p, bytes, st) != cudaSuccess) {
     cudaGetLastError();
     *p = nullptr;
@@ -112,7 +115,7 @@ cudaMemPool_t pool_of(int d) {
 fxtx_status_t alloc_pooled(void** p, size_t bytes, cudaStream_t st) {
   *p = nullptr;
   if (bytes == 0) return FXTX_OK;
-  if (fail_alloc()) return FXTX_ERR_ALLOC;
+  if (fail_alloc(bytes)) return FXTX_ERR_ALLOC;
   int d = -1;
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) {
     cudaGetLastError();

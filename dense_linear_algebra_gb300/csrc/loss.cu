@@ -30,7 +30,7 @@
 namespace fxtx {
 namespace {
 
-// Workspace for D, and for each other array that goes in pieces: the pool keeps 1 GB between calls.
+// Workspace for D (or few float32 rows' planes of W), and for each other array that goes in pieces: the pool keeps 1 GB between calls.
 constexpr int64_t kCap = (int64_t)512 << 20, kSmallCap = (int64_t)256 << 20;
 constexpr int64_t kRows = 16384;  // of a slab, where the classes leave the choice
 
@@ -322,13 +322,17 @@ const void* bias_at(const LayerArgs& l, int64_t c) {
 
 const void* labels_at(const LossArgs& a, int64_t r) { return static_cast<const char*>(a.labels) + r * (a.labels64 ? 8 : 4); }
 
+// W's planes as the linear layer takes them, all of float32's classes at once.
+int64_t planes_bytes(const LayerArgs& l) { return 6 * l.k * ((l.n + 7) / 8 * 8); }
+
 // Whether a call's logits are written out, in fp32: few rows', which the product kernels of few rows take (W is read once with
 // no row of the tile wasted), or for float32 the CUDA cores. The gradient of float32 rows that those do not take forms
-// W's planes once for all of its products instead.
-bool few_logits(const LayerArgs& l, bool grad) {
+// W's planes once for all of its products instead, and so does that of rows whose dX needs planes that go in pieces only.
+bool few_logits(const LayerArgs& l, const LossArgs* grad) {
   if (l.m * l.k * 4 > kSmallCap) return false;
-  if (l.type == FXTX_F32) return grad ? few_rows(l.type, l.m, l.w_trans) : l.m <= kFewLogitsF32;
-  return l.m <= (grad ? kFewLogitsGrad : kFewLogits) && packed_bytes(l.type, l.W, l.ldw, l.n) == 0;
+  if (l.type != FXTX_F32) return l.m <= (grad ? kFewLogitsGrad : kFewLogits) && packed_bytes(l.type, l.W, l.ldw, l.n) == 0;
+  if (!grad) return l.m <= kFewLogitsF32;
+  return few_rows(l.type, l.m, l.w_trans) && (!grad->DX || few_rows(l.type, l.m, !l.w_trans) || planes_bytes(l) <= kCap);
 }
 
 // Few rows as an operand, in a workspace of its own where they have to be copied.
@@ -354,14 +358,23 @@ PlanesProduct logits_product(const LayerArgs& l, const Part& x) {
   return q;
 }
 
-// X W of few rows to z; its biases are left to the kernels that read it.
+// X W of few rows to z; its biases are left to the kernels that read it. Of float32 W goes in pieces of the classes where its planes
+// would take more than kCap (128 x 4096, 131,072 classes: 3.2 GB at once 1,664 us, in pieces 1,556).
 fxtx_status_t run_logits(const LayerArgs& l, const Part& x, float* z, const DeviceInfo& dev, cudaStream_t st) {
   if (l.type != FXTX_F32) return run_raw(l.type, logits_product(l, x), z, dev, st);
+  const int64_t row = (l.n + 7) / 8 * 8 * 6, most = few_rows(l.type, l.m, l.w_trans) ? l.k : floor256(kCap / row);
+  const int64_t Vp = piece_of(l.k, most);
   LayerArgs z_of = l;
   z_of.e = Epilogue{};
-  z_of.e.out = z;
   z_of.e.ldo = l.k;
-  return run_linear(z_of, dev, st);
+  fxtx_status_t s = FXTX_OK;
+  for (int64_t v = 0; v < l.k && s == FXTX_OK; v += Vp) {
+    z_of.k = std::min(Vp, l.k - v);
+    z_of.W = l.w_trans ? entry(l.W, l.ldw, v, 0, 4) : entry(l.W, l.ldw, 0, v, 4);
+    z_of.e.out = z + v;
+    s = run_linear(z_of, dev, st);
+  }
+  return s;
 }
 
 template <typename T>
@@ -468,7 +481,7 @@ cudaError_t launch_scales(const LossArgs& a, int64_t m, int64_t k, float* scales
 }
 
 fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (few_logits(l, false)) switch (l.type) {
+  if (few_logits(l, nullptr)) switch (l.type) {
       case FXTX_F32: return few_loss<float>(l, a, dev, st);
       case FXTX_BF16: return few_loss<__nv_bfloat16>(l, a, dev, st);
       default: return few_loss<__half>(l, a, dev, st);
@@ -537,7 +550,7 @@ fxtx_status_t run_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& 
 }
 
 fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
-  if (few_logits(l, true)) switch (l.type) {
+  if (few_logits(l, &a)) switch (l.type) {
       case FXTX_F32: return few_grad<float>(l, a, dev, st);
       case FXTX_BF16: return few_grad<__nv_bfloat16>(l, a, dev, st);
       default: return few_grad<__half>(l, a, dev, st);

@@ -1,9 +1,10 @@
 """Layer norm, the embedding lookup, cross entropy and their gradients where one of them was wrong or took too much: long logits of
-terms of one sign, weights of rows that are left out, rows around a large mean."""
+terms of one sign, weights of rows that are left out, rows around a large mean, workspace."""
 import pytest
 import torch
 
 import dense_linear_algebra_gb300 as fx
+from test_gpu_cross_entropy import check
 
 pytestmark = pytest.mark.gpu
 
@@ -108,3 +109,12 @@ def test_norm_of_rows_around_a_large_mean(m, n, dtype):
     err = (dX.double() - want).abs()
     assert bool((err <= tol + W_OF[dtype] * (want.abs() + tol)).all())
     assert not dw.any() and bool(((db.double() - g.sum(0)).abs() <= (8 + 4 * m**0.5) * U * g.abs().sum(0) + W_OF[dtype] * g.sum(0).abs() * 1.001).all())
+
+
+@pytest.mark.parametrize("w_t", [False, True])
+@pytest.mark.parametrize("m", [5, 9, 12, 16, 17, 128, 129])
+def test_workspace_of_a_few_float32_rows(m, w_t, monkeypatch):
+    """W's planes (600 MB for all classes) go in pieces of up to 512 MB whatever the rows' number; the other arrays of an allocation are
+    below 64 MB."""
+    monkeypatch.setenv("FXTX_FAIL_ALLOC_ABOVE", str(576_000_000))
+    check(m, 1000, 100_001, torch.float32, w_t=w_t)
