@@ -22,7 +22,7 @@ SOURCES = ["api.cu", "dense.cu", "csr.cu", "multi.cu", "multi_tc.cu", "split.cu"
            "linear.cu", "slope.cu", "product_tc.cu", "thin.cu", "few.cu", "norm.cu", "embed.cu",
            "loss.cu", "loss_raw.cu", "loss_stats.cu", "loss_slope.cu", "loss_sum.cu", "thin_loss.cu", "thin_loss_f32.cu"]
 HEADERS = ["act.cuh", "common.cuh", "host.h", "kernels.h", "layers.h", "linear.h", "loss.h", "multi.h", "plan.h",
-           "product.cuh", "product_split.cuh", "product_tc.cuh", "tc.cuh", "thin.cuh", "tmap.h",
+           "product.cuh", "product_split.cuh", "product_tc.cuh", "ring.h", "tc.cuh", "thin.cuh", "tmap.h",
            "train.h", "tune.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -27,6 +27,7 @@
 #include "common.cuh"
 #include "host.h"
 #include "kernels.h"
+#include "ring.h"
 #include "train.h"
 
 namespace fxtx {
@@ -153,6 +154,9 @@ struct RowOf {
   }
 };
 
+// A row's whole warps meet.
+__device__ __forceinline__ void group_barrier(int group, int tpr) { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory"); }
+
 // Sums over a row's threads, the same in each of them. All threads of the CTA call it as often.
 template <bool BIG>
 struct RowSum {
@@ -172,7 +176,7 @@ struct RowSum {
       float2* buf = red[parity];
       parity ^= 1;  // whoever writes this half again has passed the other half's barrier, which all readers of this one reach after
       if ((threadIdx.x & 31) == 0) buf[warp] = s;
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+      group_barrier(group, tpr);
       s = make_float2(0.f, 0.f);
       for (int w = 0; w < wn; ++w) {
         const float2 v = buf[w0 + w];
@@ -374,21 +378,38 @@ __device__ __forceinline__ void copy_row(void* dst, const void* src, uint32_t by
                : "memory");
 }
 
+// A warp's wait that gave up (FXTX_ERR_TIMEOUT is raised) ends its rows: nothing more is read, copied or stored. The copying thread
+// then waits, each time with a limit, for the copies under way, before anything else is done with their memory,
+template <typename I>
+__device__ __forceinline__ void drain(uint64_t* full, const RingTurn& turn, I item, I items, I step) {
+#pragma unroll 1
+  for (int x = 0; x < turn.stages; ++x)
+    if (turn.asked(x, item, items, step)) mbar_wait_bounded(&full[x], turn.parity(x));
+}
+// and the warp meets its group's others at the barriers of the rows that are left.
+template <int BARRIERS, typename Ring>
+__device__ __forceinline__ void leave_rows(const Ring& ring, bool copies, int group, int tpr, int64_t row, int64_t rows, int64_t step) {
+  if (copies) drain(ring.full, ring.turn, row, rows, step);
+  __syncwarp();
+#pragma unroll 1
+  for (; row < rows; row += step)
+    for (int i = 0; i < BARRIERS; ++i) group_barrier(group, tpr);
+}
+
 // A group's ring: MATS rows (of as many matrices) a stage.
 template <typename T, int MATS>
 struct RowRing {
   unsigned char* at;   // the group's stages
   uint64_t* full;
   uint32_t bytes;      // of a row
-  int stages, mats, s = 0;
-  uint32_t phase = 0;
-  bool ok = true;
+  int mats;
+  RingTurn turn;
   __device__ __forceinline__ RowRing(unsigned char* smem, uint64_t* bars, int group, int stages_, int mats_, int64_t n)
-      : bytes((uint32_t)(n * sizeof(T))), stages(stages_), mats(mats_) {
-    at = smem + (size_t)group * stages * mats * bytes;
+      : bytes((uint32_t)(n * sizeof(T))), mats(mats_), turn(stages_) {
+    at = smem + (size_t)group * stages_ * mats * bytes;
     full = bars + group * MOST_STAGES;
   }
-  __device__ __forceinline__ const T* row(int mat) const { return reinterpret_cast<const T*>(at + (size_t)(s * mats + mat) * bytes); }
+  __device__ __forceinline__ const T* row(int mat) const { return reinterpret_cast<const T*>(at + (size_t)(turn.s * mats + mat) * bytes); }
   // one thread's: the rows at p[0 .. mats - 1] to stage x
   __device__ __forceinline__ void fill(int x, const void* const (&p)[MATS]) {
     mbar_arrive_expect_tx(&full[x], bytes * (uint32_t)mats);
@@ -396,17 +417,8 @@ struct RowRing {
     for (int i = 0; i < MATS; ++i)
       if (i < mats) copy_row(at + (size_t)(x * mats + i) * bytes, p[i], bytes, &full[x]);
   }
-  __device__ __forceinline__ void wait() { ok = ok && mbar_wait_bounded(&full[s], phase); }
-  // after a timeout: one thread waits, each time with a limit, for the copies in flight
-  __device__ __forceinline__ void drain() {
-    for (int x = 0; x < stages; ++x) mbar_wait_bounded(&full[x], x < s ? phase ^ 1u : phase);
-  }
-  __device__ __forceinline__ void next() {
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1u;
-    }
-  }
+  // this turn's copies; false (the whole warp's) after a timeout
+  __device__ __forceinline__ bool wait() { return __all_sync(FULL_MASK, mbar_wait_bounded(&full[turn.s], turn.phase)); }
 };
 
 // A thread's accesses of a row in shared memory, and of w or b (`none` where there is no such vector).
@@ -471,7 +483,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid
   load_vector<T, V, CH>(r, a.w, 1.f, w);
   load_vector<T, V, CH>(r, a.b, 0.f, b);
   for (; row < a.m; row += step) {
-    ring.wait();
+    if (!ring.wait()) break;
     f2 x[P];
     load_pairs<T, V, CH>(r, ring.row(0), x);
     // the thread's own mean and squares about it, the warp's from those, the row's from the warps' (one barrier a row)
@@ -494,10 +506,10 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid
     float2* buf = red[parity];
     parity ^= 1;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(warp_mean, warp_square);
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+    group_barrier(group, tpr);
     // (every thread of the group has read the row)
-    if (r.t == 0 && ring.ok) fill(ring.s, row + stages * step);
-    ring.next();
+    if (r.t == 0) fill(ring.turn.s, row + stages * step);
+    ring.turn.next();
     const int w0 = group * (tpr >> 5), wn = tpr >> 5;
     float mean = 0.f, square = 0.f;
     for (int y = 0; y < wn; ++y) mean = fmaf(buf[w0 + y].x, s_n[w0 + y], mean);
@@ -507,7 +519,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid
       square += fmaf(s_n[w0 + y] * (z.x - mean), z.x - mean, z.y);
     }
     const float rstd = __frsqrt_rn(fmaf(square, over, a.eps));
-    if (!ring.ok) continue;  // FXTX_ERR_TIMEOUT is raised
     if (r.t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_ring_kernel(const __grid
     for (int i = 0; i < CH; ++i)
       if (r.has(i)) Raw<T, V>::store_pairs(out + r.at(i), x + i * V / 2);
   }
-  if (!ring.ok && r.t == 0) ring.drain();
+  leave_rows<1>(ring, r.t == 0, group, tpr, row, a.m, step);
 }
 
 // A thread's column sums, over the groups in turn, to the CTA's part (or dw and db, of one CTA).
@@ -588,7 +599,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
       mean_n = a.mean_in[row + step];
       rstd_n = a.rstd_in[row + step];
     }
-    ring.wait();
+    if (!ring.wait()) break;
     f2 u[P], h[P];
     Raw<T, V> res[CH];
     load_pairs<T, V, CH>(r, ring.row(0), u);
@@ -609,9 +620,9 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
       s2 = fma2(h[i], u[i], s2);
     }
     const float2 s = sum(make_float2(unpack2(s1).x + unpack2(s1).y, unpack2(s2).x + unpack2(s2).y));
-    if (r.t == 0 && ring.ok) fill(ring.s, row + stages * step);
-    ring.next();
-    if (!ring.ok || !a.DX) continue;
+    if (r.t == 0) fill(ring.turn.s, row + stages * step);
+    ring.turn.next();
+    if (!a.DX) continue;
     const float c1 = -s.x * over, c2 = -s.y * over;
     const f2 d1 = pack2(c1, c1), d2 = pack2(c2, c2);
     T* out = static_cast<T*>(a.DX) + row * a.lddx;
@@ -630,7 +641,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_ring_kernel(const _
       Raw<T, V>::store_pairs(out + r.at(i), v);
     }
   }
-  if (!ring.ok && r.t == 0) ring.drain();
+  leave_rows<1>(ring, r.t == 0, group, tpr, row, a.m, step);
   if constexpr (SUMS) {
     float x[E], y[E];
 #pragma unroll
@@ -654,12 +665,11 @@ template <typename T, int MATS>
 struct OddRing {
   unsigned char* at;
   uint64_t* full;
-  int slot, stages, mats, s = 0;
-  uint32_t phase = 0;
-  bool ok = true;
+  int slot, mats;
+  RingTurn turn;
   __device__ __forceinline__ OddRing(unsigned char* smem, uint64_t* bars, int group, int slot_, int stages_, int mats_)
-      : slot(slot_), stages(stages_), mats(mats_) {
-    at = smem + (size_t)group * stages * mats * slot;
+      : slot(slot_), mats(mats_), turn(stages_) {
+    at = smem + (size_t)group * stages_ * mats * slot;
     full = bars + group * MOST_STAGES;
   }
   // where a row's copy begins, and its bytes
@@ -681,22 +691,13 @@ struct OddRing {
         if (bytes) copy_row(at + (size_t)(x * mats + i) * slot, reinterpret_cast<const unsigned char*>(p[i]) - head(p[i]), bytes, &full[x]);
       }
   }
-  __device__ __forceinline__ void wait() { ok = ok && mbar_wait_bounded(&full[s], phase); }
-  // after a timeout: one thread waits, each time with a limit, for the copies in flight
-  __device__ __forceinline__ void drain() {
-    for (int x = 0; x < stages; ++x) mbar_wait_bounded(&full[x], x < s ? phase ^ 1u : phase);
-  }
-  __device__ __forceinline__ void next() {
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1u;
-    }
-  }
+  // this turn's copies; false (the whole warp's) after a timeout
+  __device__ __forceinline__ bool wait() { return __all_sync(FULL_MASK, mbar_wait_bounded(&full[turn.s], turn.phase)); }
   // the thread's entries of the row at p
   // (`beyond` for what lies beyond its end)
   template <int CH>
   __device__ __forceinline__ void load(int mat, const T* p, int t, int tpr, int n, bool last, float (&x)[CH], float beyond = 0.f) const {
-    const T* row = reinterpret_cast<const T*>(at + (size_t)(s * mats + mat) * slot + head(p));
+    const T* row = reinterpret_cast<const T*>(at + (size_t)(turn.s * mats + mat) * slot + head(p));
     if (!last) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -749,7 +750,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_
     b[i] = a.b && j < n ? to_f32(static_cast<const T*>(a.b)[j]) : 0.f;
   }
   for (; row < a.m; row += step) {
-    ring.wait();
+    if (!ring.wait()) break;
     float x[CH];
     ring.load(0, at(row), t, tpr, n, row + 1 == a.m, x);
     float s = 0.f;
@@ -757,8 +758,8 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_
     for (int i = 0; i < CH; ++i) s += x[i];
     const float mean = sum(make_float2(s, 0.f)).x * over;
     // (every thread of the group has read the row)
-    if (t == 0 && ring.ok) fill(ring.s, row + stages * step);
-    ring.next();
+    if (t == 0) fill(ring.turn.s, row + stages * step);
+    ring.turn.next();
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
@@ -766,7 +767,6 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_
       s = fmaf(x[i], x[i], s);
     }
     const float rstd = __frsqrt_rn(fmaf(sum(make_float2(s, 0.f)).x, over, a.eps));
-    if (!ring.ok) continue;  // FXTX_ERR_TIMEOUT is raised
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_odd_kernel(const __grid_
     for (int i = 0; i < CH; ++i)
       if (t + i * tpr < n) out[t + i * tpr] = from_f32<T>(fmaf(x[i] * rstd, w[i], b[i]));
   }
-  if (!ring.ok && t == 0) ring.drain();
+  leave_rows<2>(ring, t == 0, group, tpr, row, a.m, step);
 }
 
 template <typename T, int CH, bool SUMS>
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_odd_kernel(const __
       mean_n = a.mean_in[row + step];
       rstd_n = a.rstd_in[row + step];
     }
-    ring.wait();
+    if (!ring.wait()) break;
     float u[CH], h[CH], res[CH];
     ring.load(0, x_at(row), t, tpr, n, last, u, mean);
     ring.load(1, g_at(row), t, tpr, n, last, h);
@@ -837,16 +837,16 @@ __global__ void __launch_bounds__(RING_THREADS, 1) norm_grad_odd_kernel(const __
       s.y = fmaf(h[i], u[i], s.y);
     }
     s = sum(s);
-    if (t == 0 && ring.ok) fill(ring.s, row + stages * step);
-    ring.next();
-    if (!ring.ok || !a.DX) continue;
+    if (t == 0) fill(ring.turn.s, row + stages * step);
+    ring.turn.next();
+    if (!a.DX) continue;
     const float c1 = s.x * over, c2 = s.y * over;
     T* out = static_cast<T*>(a.DX) + row * a.lddx;
 #pragma unroll
     for (int i = 0; i < CH; ++i)
       if (t + i * tpr < n) out[t + i * tpr] = from_f32<T>(fmaf(fmaf(-u[i], c2, h[i] - c1), rstd, a.R ? res[i] : 0.f));
   }
-  if (!ring.ok && t == 0) ring.drain();
+  leave_rows<1>(ring, t == 0, group, tpr, row, a.m, step);
   if constexpr (SUMS)
     store_columns<T, 1, CH>(a, RowOf<T, 1, CH>(t, tpr, a.n), group, shape.groups, dw, db, reinterpret_cast<float*>(smem));
 }
@@ -874,12 +874,12 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
   }
   __syncwarp();
   after_previous();
-  const int64_t tiles = (a.m + rows - 1) / rows, step = (int64_t)gridDim.x * WARPS;
-  int64_t tile = (int64_t)blockIdx.x * WARPS + warp;
-  auto fill = [&](int x, int64_t i) {
+  const int tiles = (int)((a.m + rows - 1) / rows), step = (int)gridDim.x * WARPS;  // (a tile has four rows at least)
+  int tile = (int)blockIdx.x * WARPS + warp;
+  auto fill = [&](int x, int i) {
     if (i >= tiles) return;
-    const int64_t first = i * rows * a.n;
-    const uint32_t bytes = (uint32_t)(min((int64_t)rows, a.m - i * rows) * accesses * 16);
+    const int64_t first = (int64_t)i * rows * a.n;
+    const uint32_t bytes = (uint32_t)(min((int64_t)rows, a.m - (int64_t)i * rows) * accesses * 16);
     unsigned char* to = at + (size_t)x * mats * slot;
     mbar_arrive_expect_tx(&full[x], bytes * (uint32_t)mats);
     copy_row(to, static_cast<const T*>(a.X) + first, bytes, &full[x]);
@@ -899,30 +899,28 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
       for (int q = 0; q < P; ++q) w[q] = pack2(1.f, 1.f);
     }
   }
+  RingTurn turn(stages);
   bool ok = true;
-  int s = 0;
-  uint32_t phase = 0;
   // the statistics of a tile's rows (32 at most), a row a lane, a tile ahead
   float mean_n = 0.f, rstd_n = 0.f;
-  auto fetch = [&](int64_t i) {
-    const int64_t r = i * rows + lane;
+  auto fetch = [&](int i) {
+    const int64_t r = (int64_t)i * rows + lane;
     const bool in = lane < rows && r < a.m;
     mean_n = in ? a.mean_in[r] : 0.f;
     rstd_n = in ? a.rstd_in[r] : 0.f;
   };
   fetch(tile);
   for (; tile < tiles; tile += step) {
-    const int64_t row0 = tile * rows;
+    const int64_t row0 = (int64_t)tile * rows;
     const float mean_t = mean_n, rstd_t = rstd_n;
     fetch(tile + step);
     const int here = (int)min((int64_t)rows, a.m - row0);  // the tile's rows
-    ok = __all_sync(FULL_MASK, ok && mbar_wait_bounded(&full[s], phase));
-    if (!ok) {  // FXTX_ERR_TIMEOUT is raised; the other copies in flight land before the CTA leaves
-      if (lane == 0)
-        for (int x = 0; x < stages; ++x) mbar_wait_bounded(&full[x], x < s ? phase ^ 1u : phase);
+    ok = __all_sync(FULL_MASK, ok && mbar_wait_bounded(&full[turn.s], turn.phase));
+    if (!ok) {  // FXTX_ERR_TIMEOUT is raised
+      if (lane == 0) drain(full, turn, tile, tiles, step);
       break;
     }
-    const unsigned char* x_at = at + (size_t)s * mats * slot + t * 16;
+    const unsigned char* x_at = at + (size_t)turn.s * mats * slot + t * 16;
 #pragma unroll 1
     for (int r0 = 0; r0 < here; r0 += 2 * groups) {
       f2 u[2][P], h[2][P], y[2][P];
@@ -935,8 +933,9 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
         x.zero();
         g.zero();
         res.zero();
-        const float mean = __shfl_sync(FULL_MASK, mean_t, r & 31);
+        float mean = __shfl_sync(FULL_MASK, mean_t, r & 31);
         scale[i] = __shfl_sync(FULL_MASK, rstd_t, r & 31);
+        mean = in && has ? mean : 0.f;  // (beyond the row's end x and g are zero; -mean rstd may be beyond fp32 where u is not)
         if (in && has) {
           const unsigned char* p = x_at + r * accesses * 16;
           x.load(reinterpret_cast<const T*>(p));
@@ -946,9 +945,8 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
         x.pairs(u[i]);
         g.pairs(h[i]);
         res.pairs(y[i]);
-        const f2 minus = in && has ? pack2(-mean, -mean) : 0, sc = pack2(scale[i], scale[i]);
+        const f2 minus = pack2(-mean, -mean), sc = pack2(scale[i], scale[i]);
         f2 p1 = 0, p2 = 0;
-        // (beyond the row's end x and g are zero, and mean is taken as zero there: -mean rstd may be beyond fp32 where u is not)
 #pragma unroll
         for (int q = 0; q < P; ++q) {
           u[i][q] = mul2(add2(u[i][q], minus), sc);
@@ -982,11 +980,8 @@ __global__ void __launch_bounds__(SHORT_THREADS, 1) norm_grad_short_kernel(const
       }
     }
     __syncwarp();  // the tile has been read
-    if (lane == 0) fill(s, tile + stages * step);
-    if (++s == stages) {
-      s = 0;
-      phase ^= 1u;
-    }
+    if (lane == 0) fill(turn.s, tile + stages * step);
+    turn.next();
   }
   if constexpr (SUMS) {
     // a warp's by exchange, then warp after warp in shared memory: [2][V][tpr]
