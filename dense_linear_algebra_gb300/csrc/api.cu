@@ -496,6 +496,39 @@ const DeviceInfo* device_or_fallback(DeviceInfo* fallback) {
 }
 
 }  // namespace
+namespace {
+
+// The kernel files' error words, read and cleared in one launch and one copy (a copy a word took 9 us each).
+constexpr int kErrorWords = 10;
+struct ErrorWords {
+  int* p[kErrorWords];
+};
+__device__ int g_any_error;
+__global__ void take_errors_kernel(const ErrorWords w) {
+  const int v = threadIdx.x < kErrorWords ? atomicExch(w.p[threadIdx.x], 0) : 0;
+  const bool any = __any_sync(0xffffffffu, v != 0);
+  if (threadIdx.x == 0) g_any_error = any;
+}
+
+// Whether any word is set (on the legacy stream, which waits for the blocking ones); false if they cannot be read.
+bool take_errors(int* any) {
+  static std::mutex mu;  // (one result)
+  std::lock_guard<std::mutex> lock(mu);
+  const ErrorWords w = {{dense_error_word(), csr_error_word(), multi_error_word(), product_error_word(), stats_error_word(),
+                         slope_error_word(), sum_error_word(), raw_error_word(), embed_error_word(), norm_error_word()}};
+  for (int* p : w.p)
+    if (!p) return false;
+  // test hook: FXTX_PLANT_ERROR=<i> sets word i, as a wait that ran out would
+  if (const char* plant = getenv("FXTX_PLANT_ERROR")) {
+    const int i = atoi(plant), timeout = FXTX_ERR_TIMEOUT;
+    if (i >= 0 && i < kErrorWords && cudaMemcpy(w.p[i], &timeout, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return false;
+  }
+  take_errors_kernel<<<1, 32>>>(w);
+  return cudaGetLastError() == cudaSuccess && cudaMemcpyFromSymbol(any, g_any_error, sizeof(int)) == cudaSuccess;
+}
+
+}  // namespace
+
 }  // namespace fxtx
 
 using namespace fxtx;
@@ -632,21 +665,10 @@ fxtx_status_t fxtx_csr_plan_describe_host(int is_f64, int64_t m, int64_t n, int6
 }
 
 fxtx_status_t fxtx_device_error(void* stream) {
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) {
-    cudaGetLastError();
-    return FXTX_ERR_CUDA;
-  }
-  const int a = take_dense_device_error();
-  const int b = take_csr_device_error();
-  const int c = take_multi_device_error();
-  const int d = take_product_device_error();
-  const int e = take_stats_device_error(), f = take_slope_device_error(), g = take_sum_device_error(), h = take_raw_device_error();
-  const int i = take_embed_device_error(), j = take_norm_device_error();
-  if (a < 0 || b < 0 || c < 0 || d < 0 || e < 0 || f < 0 || g < 0 || h < 0 || i < 0 || j < 0) {
-    cudaGetLastError();
-    return FXTX_ERR_CUDA;
-  }
-  return (a || b || c || d || e || f || g || h || i || j) ? FXTX_ERR_TIMEOUT : FXTX_OK;
+  int any = 0;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) == cudaSuccess && take_errors(&any)) return any ? FXTX_ERR_TIMEOUT : FXTX_OK;
+  cudaGetLastError();
+  return FXTX_ERR_CUDA;
 }
 
 const char* fxtx_status_string(fxtx_status_t status) {

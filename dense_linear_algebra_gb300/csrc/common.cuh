@@ -18,8 +18,8 @@ constexpr unsigned FULL_MASK = 0xffffffffu;
 constexpr uint32_t WAIT_LIMIT = 1u << 22;
 
 // Sticky device-side error word (FXTX_OK or FXTX_ERR_TIMEOUT). Each translation
-// unit has its own copy (internal linkage, no relocatable device code); its
-// host-side reader is take_device_error() below, which every kernel file
+// unit has its own copy (internal linkage, no relocatable device code); where it
+// lies is device_error_word() below, which every kernel file that waits
 // exports under its own name for fxtx_device_error.
 static __device__ int g_device_error = 0;
 
@@ -231,12 +231,10 @@ struct OuterAcc<double> {
   using type = AccF64;
 };
 
-// Reads and clears this translation unit's error word (synchronous).
-static inline int take_device_error() {
-  int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return -1;
-  if (v != 0 && cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return -1;
-  return v;
+// This translation unit's error word on the current device, nullptr if it cannot be had.
+static inline int* device_error_word() {
+  void* p = nullptr;
+  return cudaGetSymbolAddress(&p, g_device_error) == cudaSuccess ? static_cast<int*>(p) : nullptr;
 }
 
 template <typename T>

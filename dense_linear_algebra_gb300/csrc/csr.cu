@@ -151,7 +151,7 @@ __device__ __forceinline__ void defer_row(const CsrArgs<T>& a, int64_t r, int64_
 
 }  // namespace
 
-int take_csr_device_error() { return take_device_error(); }
+int* csr_error_word() { return device_error_word(); }
 
 size_t csr_rows_smem(int64_t win_len, int64_t ylen, int elem) {
   return window_bytes(win_len, elem) + window_bytes(ylen, elem) + 32 * WARP_SCRATCH;

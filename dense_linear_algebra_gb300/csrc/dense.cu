@@ -30,7 +30,7 @@
 
 namespace fxtx {
 
-int take_dense_device_error() { return take_device_error(); }
+int* dense_error_word() { return device_error_word(); }
 
 __host__ __device__ constexpr size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -26,7 +26,7 @@
 
 namespace fxtx {
 
-int take_embed_device_error() { return take_device_error(); }
+int* embed_error_word() { return device_error_word(); }
 
 namespace {
 

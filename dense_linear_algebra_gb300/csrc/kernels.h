@@ -75,8 +75,8 @@ cudaError_t launch_epilogue(int64_t n, const T* w, double alpha, double beta, co
 
 // Read and clear the device-side error word of each kernel file (synchronous;
 // -1 if the read itself failed).
-int take_dense_device_error();
-int take_csr_device_error();
+int* dense_error_word();
+int* csr_error_word();
 
 // Ensures a kernel may use `bytes` of dynamic shared memory on the current device.
 cudaError_t ensure_smem(const void* kernel, size_t bytes);

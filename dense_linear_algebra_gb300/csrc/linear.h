@@ -49,7 +49,7 @@ struct PlanesProduct {
 };
 template <typename T>
 fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStream_t st);
-int take_product_device_error();
+int* product_error_word();
 
 // How a product is laid over the tensor cores.
 struct TcPlan {

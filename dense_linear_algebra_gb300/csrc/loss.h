@@ -60,10 +60,10 @@ int64_t raw_parts(const PlanesProduct& p, const DeviceInfo& dev);
 // out = mode 3's result from such parts.
 fxtx_status_t join_sums(fxtx_type_t type, const ModeArgs<3>& x, void* out, int64_t ldo, int64_t rows, int64_t cols, int64_t parts,
                         const float* part, const DeviceInfo& dev, cudaStream_t st);
-int take_raw_device_error();
-int take_stats_device_error();
-int take_slope_device_error();
-int take_sum_device_error();
+int* raw_error_word();
+int* stats_error_word();
+int* slope_error_word();
+int* sum_error_word();
 
 // The loss and its gradient.
 struct LossArgs {

@@ -26,7 +26,7 @@ fxtx_status_t run_t(const PlanesProduct& p, float* out, const DeviceInfo& dev, c
 
 }  // namespace
 
-int take_raw_device_error() { return take_device_error(); }
+int* raw_error_word() { return device_error_word(); }
 
 int64_t raw_parts(const PlanesProduct& p, const DeviceInfo& dev) {
   const TcPlan plan = plan_of(p, dev);

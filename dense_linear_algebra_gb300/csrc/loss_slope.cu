@@ -3,7 +3,7 @@
 
 namespace fxtx {
 
-int take_slope_device_error() { return take_device_error(); }
+int* slope_error_word() { return device_error_word(); }
 
 fxtx_status_t run_slope(fxtx_type_t type, const PlanesProduct& p, const ModeArgs<2>& x, const DeviceInfo& dev, cudaStream_t st) {
   switch (type) {

@@ -3,7 +3,7 @@
 
 namespace fxtx {
 
-int take_stats_device_error() { return take_device_error(); }
+int* stats_error_word() { return device_error_word(); }
 
 fxtx_status_t run_stats(fxtx_type_t type, const PlanesProduct& p, const ModeArgs<1>& x, const DeviceInfo& dev, cudaStream_t st) {
   switch (type) {

@@ -69,7 +69,7 @@ fxtx_status_t run_t(const PlanesProduct& p, const ModeArgs<3>& x, const DeviceIn
 
 }  // namespace
 
-int take_sum_device_error() { return take_device_error(); }
+int* sum_error_word() { return device_error_word(); }
 
 fxtx_status_t join_sums(fxtx_type_t type, const ModeArgs<3>& x, void* out, int64_t ldo, int64_t rows, int64_t cols, int64_t parts,
                         const float* part, const DeviceInfo& dev, cudaStream_t st) {

@@ -511,7 +511,7 @@ int describe_multi(const MultiPlan& p, char* buf, size_t cap) {
                   p.ctas, p.smem, p.ws_bytes, p.est_us);
 }
 
-int take_multi_device_error() { return take_device_error(); }
+int* multi_error_word() { return device_error_word(); }
 
 template <typename T, int NB, int KB>
 static cudaError_t launch_kb(const MultiPlan& p, const MultiArgs<T>& a0, int vmode, cudaStream_t st) {

@@ -75,6 +75,6 @@ cudaError_t launch_multi_tc(const MultiPlan& p, const MultiArgs<float>& a, cudaS
 int describe_multi(const MultiPlan& p, char* buf, size_t cap);
 
 // Reads and clears the device-side error word of the multi-vector kernels (synchronous).
-int take_multi_device_error();
+int* multi_error_word();
 
 }  // namespace fxtx

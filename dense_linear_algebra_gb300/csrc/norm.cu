@@ -32,7 +32,7 @@
 
 namespace fxtx {
 
-int take_norm_device_error() { return take_device_error(); }
+int* norm_error_word() { return device_error_word(); }
 
 namespace {
 

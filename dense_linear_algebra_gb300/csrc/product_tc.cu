@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Epilogue e, int64_t row
 
 }  // namespace
 
-int take_product_device_error() { return take_device_error(); }
+int* product_error_word() { return device_error_word(); }
 
 template <typename T>
 fxtx_status_t run_planes(const PlanesProduct& p, const DeviceInfo& dev, cudaStream_t st) {

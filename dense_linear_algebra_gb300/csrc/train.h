@@ -30,7 +30,7 @@ struct NormArgs {
   void *DW = nullptr, *DB = nullptr;
   float* part = nullptr;  // [CTAs][2][n] column sums
 };
-int take_norm_device_error();
+int* norm_error_word();
 fxtx_status_t run_norm(fxtx_type_t type, const NormArgs& a, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_norm_grad(fxtx_type_t type, const NormArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
@@ -47,7 +47,7 @@ struct EmbedArgs {
   int64_t ldo = 0;
 };
 fxtx_status_t run_embed(fxtx_type_t type, const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st);
-int take_embed_device_error();
+int* embed_error_word();
 fxtx_status_t run_embed_grad(fxtx_type_t type, const EmbedArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
 }  // namespace fxtx
