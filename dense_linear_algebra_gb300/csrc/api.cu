@@ -499,7 +499,7 @@ const DeviceInfo* device_or_fallback(DeviceInfo* fallback) {
 namespace {
 
 // The kernel files' error words, read and cleared in one launch and one copy (a copy a word took 9 us each).
-constexpr int kErrorWords = 10;
+constexpr int kErrorWords = 11;
 struct ErrorWords {
   int* p[kErrorWords];
 };
@@ -514,8 +514,8 @@ __global__ void take_errors_kernel(const ErrorWords w) {
 bool take_errors(int* any) {
   static std::mutex mu;  // (one result)
   std::lock_guard<std::mutex> lock(mu);
-  const ErrorWords w = {{dense_error_word(), csr_error_word(), multi_error_word(), product_error_word(), stats_error_word(),
-                         slope_error_word(), sum_error_word(), raw_error_word(), embed_error_word(), norm_error_word()}};
+  const ErrorWords w = {{dense_error_word(), csr_error_word(), multi_error_word(), multi_tc_error_word(), product_error_word(),
+                         stats_error_word(), slope_error_word(), sum_error_word(), raw_error_word(), embed_error_word(), norm_error_word()}};
   for (int* p : w.p)
     if (!p) return false;
   // test hook: FXTX_PLANT_ERROR=<i> sets word i, as a wait that ran out would

@@ -76,5 +76,6 @@ int describe_multi(const MultiPlan& p, char* buf, size_t cap);
 
 // Reads and clears the device-side error word of the multi-vector kernels (synchronous).
 int* multi_error_word();
+int* multi_tc_error_word();
 
 }  // namespace fxtx

@@ -574,6 +574,8 @@ cudaError_t launch_tc_kb(const MultiPlan& p, const MultiArgs<float>& a, int vmod
 
 }  // namespace
 
+int* multi_tc_error_word() { return device_error_word(); }
+
 size_t multi_tc_smem(int kb) {
   switch (kb) {
     case 8: return TcCfg<8>::BYTES;

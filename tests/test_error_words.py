@@ -30,6 +30,14 @@ def test_the_words_of_the_files():
     assert sorted(exported) == sorted(names)
 
 
+def test_each_file_that_waits_has_its_word():
+    """A file has a word of its own: one that waits, by itself or by the kernels of a header, has to give it out."""
+    waits = re.compile(r"mbar_wait_bounded\(|tc_wait\(|warp_wait\(|raise_error\(|#include \"product_(tc|split)\.cuh\"")
+    for f in sorted(os.listdir(CSRC)):
+        if f.endswith(".cu") and waits.search(source(f)):
+            assert "_error_word() { return device_error_word(); }" in source(f), f
+
+
 @pytest.mark.gpu
 def test_each_word_is_read_and_cleared(monkeypatch):
     assert fx.device_error() == fx.FXTX_OK
