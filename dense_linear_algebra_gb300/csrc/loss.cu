@@ -97,6 +97,8 @@ constexpr int SEG = 1024;  // of a row that a CTA reduces
 // Rows whose logits are written out, at most: of 16 bits forward (2048 x 32,000: 36 us at 1 to 16 rows and 44 at 64; in tiles 47 at
 // 1, 49 at 16, 38 at 64) and for the gradient (130 us at 1 row and 144 at 16, in tiles 144 and 135), and of float32 forward.
 constexpr int kFewLogits = 16, kFewLogitsGrad = 4, kFewLogitsF32 = 128;
+// The rows that few_logits leaves to the gradient's way, at most: float32's are those of the CUDA cores.
+constexpr int kSlopeRows = std::max({kFewLogitsGrad, kFewByRow, kFewByColumn});
 
 // Few rows' logits in memory: `parts` parts of X W to be added, [part][row][class], and the biases.
 struct FewLogits {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(256) row_slope_kernel(const FewLogits f, const
     float lse, g;
     int64_t label;
   };
-  __shared__ Row rows[kFewLogits];
+  __shared__ Row rows[kSlopeRows];
   after_previous();
   const float up = scales ? scales[0] : 1.f;
   for (int i = threadIdx.x; i < f.rows; i += 256) {
