@@ -375,7 +375,7 @@ class Classifier:
         p, saved = self.working(), []
         if self.tokens:
             rows = training.embedding(X.reshape(-1), p["table"], scale=self.width**0.5)
-            x = rows.view(X.shape[0], -1)
+            x = rows.view(X.shape[0], X.shape[1] * self.width)
         else:
             x = X
         v, h = x, None
@@ -431,7 +431,7 @@ def _mean_loss_gradients(net, labels, kept):
         return net.backward(rate.expand(labels.shape[0]).contiguous(), kept)
     # float16 has nothing below 6e-8, where the gradient of a mean over millions of rows lies: it goes through the layers at a
     # size that a sum over the rows leaves below 4,096 times an entry of the layer's input, and gets its own in float32
-    part = min(1.0, 4096 / labels.shape[0])
+    part = min(1.0, 4096 / max(labels.shape[0], 1))
     return [g.float().mul_(rate / part) for g in net.backward(part, kept)]
 
 

@@ -1,9 +1,10 @@
 """Layer norm, the embedding lookup, cross entropy and their gradients where one of them was wrong or took too much: long logits of
-terms of one sign, weights of rows that are left out, rows around a large mean, workspace."""
+terms of one sign, weights of rows that are left out, rows around a large mean, workspace, a classifier of no rows."""
 import pytest
 import torch
 
 import dense_linear_algebra_gb300 as fx
+from dense_linear_algebra_gb300 import solvers
 from test_gpu_cross_entropy import check
 
 pytestmark = pytest.mark.gpu
@@ -118,3 +119,16 @@ def test_workspace_of_a_few_float32_rows(m, w_t, monkeypatch):
     below 64 MB."""
     monkeypatch.setenv("FXTX_FAIL_ALLOC_ABOVE", str(576_000_000))
     check(m, 1000, 100_001, torch.float32, w_t=w_t)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens", [0, 50])
+def test_a_classifier_of_no_rows(tokens, dtype):
+    """Nothing to classify, and nothing to learn from."""
+    X = torch.empty((0, 3), dtype=torch.int64, device="cuda") if tokens else torch.empty((0, 20), device="cuda")
+    labels = torch.empty(0, dtype=torch.int64, device="cuda")
+    net, info = solvers.classify_adamw(X, labels, 7, hidden=72, layers=1, tokens=tokens, width=16, steps=2, dtype=dtype)
+    assert info.steps == 2 and not torch.stack(info.losses).any()
+    fresh = solvers.Classifier(3 * 16 if tokens else 20, 72, 7, 1, tokens, 16, dtype=dtype)
+    assert all(torch.equal(a, b) for a, b in zip(net.parameters(), fresh.parameters()))
+    assert net.logits(X if tokens else X.to(dtype)).shape == (0, 7)
