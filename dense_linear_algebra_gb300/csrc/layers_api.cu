@@ -230,7 +230,7 @@ fxtx_status_t fxtx_cross_entropy(fxtx_type_t type, int64_t m, int64_t n, int64_t
   a.labels = labels; a.labels64 = label_bits == 64;
   a.loss = LOSS; a.lse = LSE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (tall_loss_shape(l)) return run_tall_loss(l, a, *dev, st);
+  if (tall_loss_shape(l, false)) return run_tall_loss(l, a, *dev, st);
   return thin_shape(n, k) ? run_thin_loss(l, a, *dev, st) : run_loss(l, a, *dev, st);
 }
 
@@ -268,7 +268,7 @@ fxtx_status_t fxtx_cross_entropy_grad(fxtx_type_t type, int64_t m, int64_t n, in
   a.DX = DX; a.lddx = lddx;
   a.DW = DW; a.lddw = lddw;
   a.DB = DB;
-  if (tall_loss_shape(l)) return run_tall_loss_grad(l, a, *dev, st);
+  if (tall_loss_shape(l, true)) return run_tall_loss_grad(l, a, *dev, st);
   return thin_shape(n, k) ? run_thin_loss_grad(l, a, *dev, st) : run_loss_grad(l, a, *dev, st);
 }
 

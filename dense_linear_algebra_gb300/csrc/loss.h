@@ -83,8 +83,8 @@ fxtx_status_t run_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceI
 fxtx_status_t run_thin_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_thin_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 
-// float32 of at most 16 classes and 64 features, on the CUDA cores.
-bool tall_loss_shape(const LayerArgs& l);
+// Many float32 rows of few classes and features, on the CUDA cores.
+bool tall_loss_shape(const LayerArgs& l, bool grad);
 fxtx_status_t run_tall_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 fxtx_status_t run_tall_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st);
 

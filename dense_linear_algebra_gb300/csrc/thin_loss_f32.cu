@@ -1,15 +1,15 @@
-// thin_loss_f32.cu — softmax cross entropy of float32 rows on at most 16 classes and 64 features, and its gradient, on the CUDA
-// cores: plain fp32 multiply-adds, two an instruction.
+// thin_loss_f32.cu — softmax cross entropy of many float32 rows on at most 16 classes (the gradient 12) and 64 features, and its
+// gradient, on the CUDA cores: plain fp32 multiply-adds, two an instruction.
 //
 // Bound: HBM (X read once) and the multiply-adds, n k a row for z and as many for dW (1,000,000 x 32, 10 classes: 21 us and 17 us).
 // On the tensor cores float32 takes six products of bfloat16 terms, and half of a fragment is padding at 10 classes: that
-// form of the gradient took 64 us.
+// form of the gradient takes 60 us.
 //
 // A warp takes tiles of 64 rows, which come by asynchronous copies into shared memory (while the other warps work: a second
 // buffer would leave 10 warps a SM), with a pitch that keeps both ways of reading free of bank conflicts: a lane two rows for z,
 // the softmax and D; then a lane two features for dW, whose sums stay in its registers, the rows shared out among the
 // lanes that are left. D goes through shared memory in between. What it waits for is shared memory: with a row a lane W is
-// read twice as often (51 us). The warps' sums are added in turn, the CTAs' by a second kernel in order.
+// read twice as often (52 us, two rows 48). The warps' sums are added in turn, the CTAs' by a second kernel in order.
 #include <algorithm>
 
 #include "act.cuh"
@@ -20,6 +20,8 @@
 
 namespace fxtx {
 namespace {
+
+constexpr int MOST_CLASSES = 16, MOST_GRAD_CLASSES = 12;
 
 struct TallArgs {
   int64_t m;
@@ -378,17 +380,19 @@ fxtx_status_t launch(TallArgs a, const DeviceInfo& dev, cudaStream_t st) {
 }
 template <int N, int KP>
 fxtx_status_t launch_mode(const TallArgs& a, int mode, const DeviceInfo& dev, cudaStream_t st) {
-  return mode == 0 ? launch<N, KP, 0>(a, dev, st) : mode == 1 ? launch<N, KP, 1>(a, dev, st) : launch<N, KP, 2>(a, dev, st);
+  if constexpr (2 * KP <= MOST_GRAD_CLASSES) {
+    if (mode > 0) return mode == 1 ? launch<N, KP, 1>(a, dev, st) : launch<N, KP, 2>(a, dev, st);
+  }
+  return launch<N, KP, 0>(a, dev, st);
 }
-template <int N>
+// Pairs of classes as many as there are (padded to the next even number of pairs, the gradient of 1,000,000 x 32 takes 44 us for 6
+// classes, as they are 37; its loss 40 for 14 classes, as they are 37).
+template <int N, int KP = 1>
 fxtx_status_t launch_classes(const TallArgs& a, int mode, const DeviceInfo& dev, cudaStream_t st) {
-  const int kp = (a.k + 1) / 2;
-  return kp <= 1   ? launch_mode<N, 1>(a, mode, dev, st)
-         : kp <= 2 ? launch_mode<N, 2>(a, mode, dev, st)
-         : kp <= 4 ? launch_mode<N, 4>(a, mode, dev, st)
-         : kp == 5 ? launch_mode<N, 5>(a, mode, dev, st)
-         : kp == 6 ? launch_mode<N, 6>(a, mode, dev, st)
-                   : launch_mode<N, 8>(a, mode, dev, st);
+  if constexpr (KP < MOST_CLASSES / 2) {
+    if (a.k > 2 * KP) return launch_classes<N, KP + 1>(a, mode, dev, st);
+  }
+  return launch_mode<N, KP>(a, mode, dev, st);
 }
 
 fxtx_status_t run(const LayerArgs& l, const LossArgs& q, int mode, const DeviceInfo& dev, cudaStream_t st) {
@@ -412,7 +416,17 @@ fxtx_status_t run(const LayerArgs& l, const LossArgs& q, int mode, const DeviceI
 
 }  // namespace
 
-bool tall_loss_shape(const LayerArgs& l) { return l.type == FXTX_F32 && l.k <= 16 && l.n <= 64; }
+// Where this way is the faster one (us, here and on the tensor cores, of the loss / dW and db / dX too):
+//   1,000,000 x 32   6 classes 26 / 37 / 59 and 41 / 60 / 92, 12 classes 32 / 53 / 81 and 41 / 60 / 92, 14 classes 37 / 72 / 116, 16
+//                    classes 40 / 91 / 136; x 24, 13 classes 35 / 68 / 112 and 47 / 80 / 109
+//   500,000 x 64     8 classes 30 / 47 / 75 and 33 / 56 / 91, 10 classes 34 / 57 / 90, 12 classes 37 / 61 / 98 and 33 / 56 / 91
+//   rows of 32       2 classes, 20,000 rows 4.2 / 6.7 / 9.5 and 3.8 / 8.8 / 9.8; 10 classes, 20,000 6.0 / 10.7 / 14.7 and 4.1 / 9.2 / 9.7,
+//                    50,000 6.0 / 11.2 / 15.3 and 4.9 / 11.9 / 13.1, 100,000 6.0 / 12.0 / 16.1 and 7.0 / 14.0 / 16.1 (a warp takes 64
+//                    rows at a time: few rows leave SMs without, for longer the more classes there are)
+bool tall_loss_shape(const LayerArgs& l, bool grad) {
+  return l.type == FXTX_F32 && l.n <= 64 && l.k <= (grad ? MOST_GRAD_CLASSES : MOST_CLASSES) && l.n * l.k <= 512 &&
+         l.m >= (grad ? 5000 : 8000) * l.k;
+}
 fxtx_status_t run_tall_loss(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) { return run(l, a, 0, dev, st); }
 fxtx_status_t run_tall_loss_grad(const LayerArgs& l, const LossArgs& a, const DeviceInfo& dev, cudaStream_t st) {
   return run(l, a, a.DX ? 2 : 1, dev, st);

@@ -132,3 +132,11 @@ def test_a_classifier_of_no_rows(tokens, dtype):
     fresh = solvers.Classifier(3 * 16 if tokens else 20, 72, 7, 1, tokens, 16, dtype=dtype)
     assert all(torch.equal(a, b) for a, b in zip(net.parameters(), fresh.parameters()))
     assert net.logits(X if tokens else X.to(dtype)).shape == (0, 7)
+
+
+@pytest.mark.parametrize("k", range(1, 18))
+@pytest.mark.parametrize("n", [3, 16, 24, 32, 61, 64])
+def test_every_number_of_few_classes(n, k):
+    """Float32 rows of few features and classes, whose kernels hold the classes in pairs; one row too few for those kernels too."""
+    for m in (5000 * k - 1, 8000 * k + 1):
+        check(m, n, k, torch.float32, bias=k % 2 == 0, w_t=n % 2 == 0, need=(k % 3 != 0, True, True))
