@@ -94,8 +94,13 @@ cudaError_t launch_join(const float2* stats, int64_t parts, int64_t rows, const 
 }
 
 constexpr int SEG = 1024;  // of a row that a CTA reduces
-// Rows whose logits are written out, at most: of 16 bits forward (2048 x 32,000: 36 us at 1 to 16 rows and 44 at 64; in tiles 47 at
-// 1, 49 at 16, 38 at 64) and for the gradient (130 us at 1 row and 144 at 16, in tiles 144 and 135), and of float32 forward.
+// Rows whose logits are written out, at most. Of 16 bits (us, written out and in tiles; bfloat16):
+//   loss       2048 x 32,000  1 row 32 and 45, 16 rows 33 and 46, 32 rows 36 and 35, 64 rows 41 and 36; 8192 x 4000  1 row 15 and 47, 64 rows 18
+//              and 30; 1024 x 8000  16 rows 12 and 13, 32 rows 13 and 13; 512 x 50,000  1 row 23 and 20; 4096 x 131,072  1 row 263 and 245
+//   gradient   2048 x 32,000  1 row 126 and 135, 4 rows 127 and 130, 16 rows 132 and 130; 8192 x 4000  4 rows 65 and 113, 16 rows 72 and 89;
+//              512 x 50,000  4 rows 79 and 77, 16 rows 88 and 77
+// and the loss of float32: 2048 x 32,000  24 rows 199 and 211, 128 rows 212 and 214, 256 rows 290 and 289; 8192 x 4000  128 rows 113 and 208;
+// 512 x 50,000  24 rows 89 and 92, 128 rows 108 and 92.
 constexpr int kFewLogits = 16, kFewLogitsGrad = 4, kFewLogitsF32 = 128;
 // The rows that few_logits leaves to the gradient's way, at most: float32's are those of the CUDA cores.
 constexpr int kSlopeRows = std::max({kFewLogitsGrad, kFewByRow, kFewByColumn});

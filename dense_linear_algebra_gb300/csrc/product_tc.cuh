@@ -258,6 +258,9 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
   using C = TileCfg<CG, BN, PL>;
   // the pieces of a sum are added up in registers, each freeing its accumulator: float32, and logits, whose pieces are short
   constexpr bool REGS = PL == 3 || ((MODE == 1 || MODE == 2) && LONG);
+  // and taken from there too: D's epilogue is as long as the products of a piece, which wait for an accumulator that it holds (D of
+  // 8192 x 2048, 32,768 classes 648 us so; of the loss, whose epilogue is shorter, no difference)
+  constexpr bool FROM_REGS = MODE == 2 && PL == 1 && LONG;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::S], empty[C::S], tfull[2], tempty[2], fin_bar;
@@ -404,6 +407,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
       uint4 next[Tile::CH];
       if (MODE == 0 && R && !part) Tile::fetch(next, R, a.e.ldr, wide_r, i0, a.rows, j0, a.cols);
 
+      float sum[REGS ? C::COLS : 1];
       uint32_t held = acc.s;  // the accumulator with the whole sum
       uint32_t t = lane_base + held * BN;
       if constexpr (!REGS) {
@@ -419,7 +423,6 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           if (!ok) continue;
         }
       } else {
-        float sum[C::COLS];
 #pragma unroll
         for (int x = 0; x < C::COLS; ++x) sum[x] = 0.f;
         const int piece = PL == 3 ? CHUNK<MODE> : a.fold;
@@ -432,34 +435,45 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           add_columns<C::COLS>(t, sum);
         }
         if (!ok) continue;
-        // the sums go back to where the last of them came from: what follows reads them 16 columns at a time
-        // in a loop (unrolled over registers its code would not fit the instruction cache)
+        if constexpr (FROM_REGS) {
+          release(held);
+        } else {
+          // the sums go back to where the last of them came from: what follows reads them 16 columns at a time
+          // in a loop (unrolled over registers its code would not fit the instruction cache)
 #pragma unroll
-        for (int x = 0; x < C::COLS; x += 16) tc_store16(t + (uint32_t)x, sum + x);
-        tc_wait_st();
+          for (int x = 0; x < C::COLS; x += 16) tc_store16(t + (uint32_t)x, sum + x);
+          tc_wait_st();
+        }
       }
       // 16 sums of the lane's row from column x on, with their biases
       auto get = [&](int x, float* v) {
-        tc_load16(t + (uint32_t)x, v);
-        tc_wait_ld();
+        if constexpr (FROM_REGS) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = sum[x + i];
+        } else {
+          tc_load16(t + (uint32_t)x, v);
+          tc_wait_ld();
+        }
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 b = *reinterpret_cast<const float4*>(bias + x + i);
           v[i] += b.x; v[i + 1] += b.y; v[i + 2] += b.z; v[i + 3] += b.w;
         }
       };
-      if (part) {
+      if constexpr (!FROM_REGS) {  // (such sums are not split)
+        if (part) {
 #pragma unroll 1
-        for (int x = 0; x < C::COLS; x += 16) {
-          float v[16];
-          get(x, v);
-          Tile32<float>::put(buf, 0, v);
-          __syncwarp();
-          Tile32<float>::drain(buf, part, a.cols, a.cols % 4 == 0, i0, a.rows, j0 + x, a.cols);
-          __syncwarp();
+          for (int x = 0; x < C::COLS; x += 16) {
+            float v[16];
+            get(x, v);
+            Tile32<float>::put(buf, 0, v);
+            __syncwarp();
+            Tile32<float>::drain(buf, part, a.cols, a.cols % 4 == 0, i0, a.rows, j0 + x, a.cols);
+            __syncwarp();
+          }
+          release(held);
+          continue;
         }
-        release(held);
-        continue;
       }
       if constexpr (MODE == 0) {
 #pragma unroll 1
@@ -535,11 +549,8 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
         if (mode.scales) g *= mode.scales[0];
         const bool wide = Finish<S>::wide(mode.D, mode.ldd) && mode.d_planes % 8 == 0;
         if constexpr (PL == 1) {
-#pragma unroll 1
-          for (int x = 0; x < C::COLS; x += 32) {
-            if (j0 + x >= a.cols) break;  // (the whole warp's)
-#pragma unroll 1
-            for (int y = 0; y < 32; y += 16) {
+          auto columns = [&](int x) {  // 32
+            auto half = [&](int y) {
               float v[16];
               get(x + y, v);
 #pragma unroll
@@ -550,10 +561,26 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
               }
               Out::put(buf, y, v);
               if (mode.sums) column_sums<16>(v, mode.sums + i0 / 32 * mode.sums_ld + j0 + x + y, a.cols - j0 - x - y, i0 < a.rows);
+            };
+            if constexpr (FROM_REGS) {
+              half(0);
+              half(16);
+            } else {
+#pragma unroll 1
+              for (int y = 0; y < 32; y += 16) half(y);
             }
             __syncwarp();
             Out::drain(buf, static_cast<S*>(mode.D), mode.ldd, wide, i0, a.rows, j0 + x, a.cols);
             __syncwarp();
+          };
+          // (columns beyond the last: the whole warp's)
+          if constexpr (FROM_REGS) {
+#pragma unroll
+            for (int x = 0; x < C::COLS; x += 32)
+              if (j0 + x < a.cols) columns(x);
+          } else {
+#pragma unroll 1
+            for (int x = 0; x < C::COLS && j0 + x < a.cols; x += 32) columns(x);
           }
         } else {
 #pragma unroll 1
@@ -617,7 +644,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
           __syncwarp();
         }
       }
-      release(held);
+      if constexpr (!FROM_REGS) release(held);
     }
   }
 
@@ -731,8 +758,7 @@ cudaError_t launch_persistent(const TcPlan& plan, const CUtensorMap& am, const C
 
 // A product of logits (modes 1 and 2), whose kk is not split. Both modes take the same sums, since the gradient's exponentials are
 // divided by the sum that the loss had of them: with pieces of FOLD in mode 2 alone, logits of 8,192 positive terms around 400 gave
-// probabilities 1.2 (bfloat16) and 2.1 % (float16) too small. What it costs mode 2, whose epilogue holds one accumulator for longer:
-// 8192 x 2048, 32,768 classes 580 to 635 us.
+// probabilities 1.2 (bfloat16) and 2.1 % (float16) too small. The gradient of 8192 x 2048, 65,536 classes takes 0.5 % longer for it.
 template <typename T, int MODE>
 fxtx_status_t run_mode(const PlanesProduct& p, const ModeArgs<MODE>& mode, const DeviceInfo& dev, cudaStream_t st) {
   const TcPlan plan = plan_persistent(p.M, p.N, p.K, std::is_same<T, float>::value ? 3 : 1, p.A.mn_major, p.B.mn_major, dev.sm_count, 1);
