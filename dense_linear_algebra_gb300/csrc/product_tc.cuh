@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
   using C = TileCfg<CG, BN, PL>;
   // the pieces of a sum are added up in registers, each freeing its accumulator: float32, and logits, whose pieces are short
   constexpr bool REGS = PL == 3 || ((MODE == 1 || MODE == 2) && LONG);
-  // and taken from there too: D's epilogue is as long as the products of a piece, which wait for an accumulator that it holds (D of
-  // 8192 x 2048, 32,768 classes 648 us so; of the loss, whose epilogue is shorter, no difference)
+  // and taken from there too: D's epilogue is as long as the products of a piece, which waited for the accumulator that it held (D of
+  // 8192 x 2048, 32,768 classes 648 us; from registers DTIME)
   constexpr bool FROM_REGS = MODE == 2 && PL == 1 && LONG;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

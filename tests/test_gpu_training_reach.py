@@ -1,5 +1,5 @@
 """Layer norm, the embedding lookup, cross entropy and their gradients on the kernels that large and odd sizes take: in place, rows
-that are not finite, long runs of one id, ids of 28 bits, few rows against many classes and features, calls without workspace."""
+that are not finite, long runs of one id, ids of 28 bits, few rows against many classes and features, calls without workspace, offsets beyond 32 bits."""
 import pytest
 import torch
 
@@ -130,3 +130,59 @@ def test_which_calls_take_workspace(size, takes, monkeypatch):
             assert all(torch.equal(a, b) for a, b in zip(call(), want))
         monkeypatch.delenv("FXTX_FAIL_ALLOC")
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
+
+
+@pytest.fixture
+def wide():
+    """A matrix of 2.4 billion entries: offsets beyond 32 bits."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    yield torch.randn(300_000, 8192, generator=gen, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.empty_cache()
+
+
+def test_norm_beyond_32_bits(wide):
+    """Rows at the end as a call on them alone has them. The kernels differ, so fp32 results do by at most 1e-6 of a row's entries
+    (below 6); rounded to bfloat16, half a step each, two such results are up to one step of bfloat16 apart: 2^-7 of their size.
+    """
+    end = wide[-50:].clone()
+    want, mean, rstd = fx.layer_norm(end, stats=True)
+    got, mean2, rstd2 = fx.layer_norm(wide, stats=True)
+    G = torch.full((50, 8192), 0.5, dtype=torch.bfloat16, device="cuda") + end
+    grad = fx.layer_norm_grad(G, end, None, mean, rstd, need=(True, False, False))[0]
+    for a, b in ((got[-50:], want), (mean2[-50:], mean), (rstd2[-50:], rstd)):
+        assert bool(((a.double() - b.double()).abs() <= 2.0**-7 * b.double().abs() + 1e-6).all())
+    del got
+    G2 = wide.clone()
+    G2[-50:] = G
+    dX = fx.layer_norm_grad(G2, wide, None, mean2, rstd2, need=(True, False, False))[0]
+    assert bool(((dX[-50:].double() - grad.double()).abs() <= 2.0**-7 * grad.double().abs() + 2e-6).all())
+
+
+def test_lookup_beyond_32_bits(wide):
+    ids = torch.tensor([299_999, 0, 262_143, 299_999, -1], device="cuda")
+    rows = fx.embedding(ids, wide)
+    assert torch.equal(rows[:4], wide[ids[:4]]) and not rows[4].any()
+    ids = torch.full((300_000,), -1, device="cuda")
+    ids[-3:] = torch.tensor([7, 5, 7], device="cuda")
+    dE = fx.embedding_grad(wide, ids, 9)
+    assert torch.equal(dE[5], wide[-2]) and torch.equal(dE[7], (wide[-3].float() + wide[-1].float()).bfloat16())
+    assert not dE[:5].any() and not dE[6].any() and not dE[8:].any()
+    G = wide[:3].clone()
+    dE = fx.embedding_grad(G, torch.tensor([299_999, 1, 299_998], device="cuda"), 300_000, out=wide)
+    assert dE is wide and torch.equal(dE[[299_999, 1, 299_998]], G) and not dE[2:299_998].any() and not dE[0].any()
+
+
+def test_loss_beyond_32_bits(wide):
+    """The last rows' losses and gradients as calls on them alone have them, within the roundings of z (n = 8192: its sums are those of
+    tiles in both) and of bfloat16."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(6)
+    W = (torch.randn(70, 8192, generator=gen, device="cuda") / 90).bfloat16().t()
+    labels = torch.randint(-1, 71, (300_000,), generator=gen, device="cuda")
+    loss, lse = fx.cross_entropy(wide, W, labels)
+    want, lse_end = fx.cross_entropy(wide[-200:], W, labels[-200:])
+    assert bool(((loss[-200:] - want).abs() <= 1e-5).all()) and bool(((lse[-200:] - lse_end).abs() <= 1e-5).all())
+    dX, _, _ = fx.cross_entropy_grad(wide, W, labels, lse, need=(True, False, False))
+    end, _, _ = fx.cross_entropy_grad(wide[-200:], W, labels[-200:], lse_end, need=(True, False, False))
+    assert float((dX[-200:].double() - end.double()).norm()) <= 2.0**-7 * float(end.double().norm())
