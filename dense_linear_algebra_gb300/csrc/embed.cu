@@ -546,7 +546,7 @@ __device__ __forceinline__ void note_long(const ReduceArgs& a, const Chunk& k, i
   if (k.begins_long) a.longs[1 + atomicAdd(a.longs, 1u)] = (uint32_t)chunk;  // (their order has no say in the result)
 }
 
-// Rows of at least 1 KB: a chunk's rows (2 KB of each) come by bulk copies to shared memory, all 32 on their way at once, a
+// Rows of at least 1 KB: a chunk's rows (1 KB of each) come by bulk copies to shared memory, all 32 on their way at once, a
 // lane each.
 constexpr int BULK_THREADS = 64, BULK_ROW = BULK_THREADS * 16;
 

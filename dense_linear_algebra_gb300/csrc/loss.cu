@@ -3,8 +3,8 @@
 //     D_ij = g_i (exp(z_ij - lse_i) - [j = label_i]),  dX = D W^T,  dW = X^T D,  db = the column sums of D
 //
 // Bound: the tensor cores, 2 m n k operations forward and 6 m n k backward (z is formed again), or with few rows the
-// stream of W. 8192 x 2048, 65,536 classes in bfloat16: 1.10 ms (2,000 TFLOP/s) and 3.60 ms (1,835; at the power limit 1.29 and
-// 4.1 ms); one row of 4096, 32,000 classes 52 us (5.0 TB/s).
+// stream of W. 8192 x 2048, 65,536 classes in bfloat16: 1.10 ms (2,000 TFLOP/s) and 3.64 ms (1,815; at the power limit 1.29 and
+// 4.1 ms); one row of 4096, 32,000 classes 53 us (5.0 TB/s).
 //
 // Forward: one product whose epilogue reduces each row of a tile to its largest entry and its sum of exponentials; a
 // second kernel joins a row's parts. Nothing of the size of z is written.
@@ -12,6 +12,9 @@
 // Backward: W in pieces of the classes and X in slabs of rows, so that D of one piece and slab takes kCap bytes at most.
 // Per piece and slab three products: z again, whose epilogue writes D as an operand of the others (of the layer's type,
 // of float32 as three bfloat16 planes) and its column sums; D W^T, added up over the pieces in fp32; X^T D, over the slabs.
+//
+// D of a 16-bit type is rounded to it, as linear_grad's is: dX and dW are then 2.4e-3 off in bfloat16 (2-norm, relative; 1.7e-3, the
+// result's own rounding, with D in fp32). As the sum of two 16-bit terms it would take dX and dW twice, 1.2 of 3.64 ms more.
 //
 // float16 has nothing below 6e-8, where a mean's gradient over many classes lies: D is held multiplied by the power of
 // two that brings the largest |g| of a row with a label to 2^14 .. 2^15, which the last of the sums takes back. What is lost is below

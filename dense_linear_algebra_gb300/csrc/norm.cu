@@ -11,10 +11,10 @@
 // Which kernel, by the rows' number, width and alignment (bytes in all: 16384 x 4096 bfloat16 268 MB forward, 537 MB backward with
 // the residual path; 1,000,000 x 32 float32 384 MB backward):
 //   norm_ring_kernel, norm_grad_ring_kernel   many rows of more than a warp's accesses: bulk copies bring a group's next rows into a
-//              ring; 51 us (5.3 TB/s: the instructions of 16 warps a SM) and 85 us (6.3 TB/s); the register kernels 57 and 138 us
+//              ring; 48 us (5.6 TB/s: the instructions of 16 warps a SM) and 85 us (6.3 TB/s); the register kernels 57 and 138 us
 //   norm_grad_short_kernel   many rows of at most 32 accesses: a ring of tiles a warp; 68 us (5.6 TB/s), in registers 90
 //   norm_odd_kernel, norm_grad_odd_kernel   many rows whose pitch or width is no multiple of 16 bytes, of 129 to 8,192 entries;
-//              30,001 x 2047 bfloat16 109 and 174 us, entry by entry from memory 218 and 564
+//              30,001 x 2047 bfloat16 108 and 152 us (177 with the residual path), entry by entry from memory 218 and 564
 //   norm_kernel, norm_grad_kernel   the others: rows loaded into registers, the next one ahead; one row of 4096 3.3 us
 //   norm_long_kernel and norm_long_means_kernel, norm_long_grad_kernel   rows beyond what the registers hold (16 bits: 32,768
 //              forward, 8,192 backward; float32 half and the same): x read three times, one CTA a row; backward the two means in

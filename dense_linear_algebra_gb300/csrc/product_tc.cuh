@@ -31,12 +31,13 @@ namespace fxtx {
 namespace {
 
 constexpr int BX = 64;            // kk of a box of a K-major operand: 128 bytes
-// Stages of 64 of kk that a float32 sum stays in tensor memory: two, one for logits, whose error is that of their exponentials
-// (2-norm error of 2048^3: 6e-7, 1.3e-7 and 19 % more time).
+// Stages of 64 of kk that a float32 sum stays in tensor memory: two, one for logits that an epilogue takes, whose error is that of
+// their exponentials (2-norm error of 2048^3: 6e-7, 1.3e-7 and 19 % more time). The logits of few rows that are written out are a
+// layer's: two.
 template <int MODE>
 constexpr int CHUNK = MODE == 1 || MODE == 2 ? 1 : 2;
 constexpr int FOLD = 8192;        // of kk that a piece of a sum covers (16 bits)
-constexpr int LOGIT_FOLD = 1024;  // of sums that are not rounded to 16 bits
+constexpr int LOGIT_FOLD = 1024;  // of logits, which are not rounded to 16 bits
 
 // BK: kk a stage; KB: kilobytes the stages may take.
 template <int CG, int BN, int PL, int BK_, int KB>
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(TileCfg<CG, BN, PL>::THREADS, 1)
   // the pieces of a sum are added up in registers, each freeing its accumulator: float32, and logits, whose pieces are short
   constexpr bool REGS = PL == 3 || ((MODE == 1 || MODE == 2) && LONG);
   // and taken from there too: D's epilogue is as long as the products of a piece, which waited for the accumulator that it held (D of
-  // 8192 x 2048, 32,768 classes 648 us; from registers DTIME)
+  // 8192 x 2048, 32,768 classes 648 us; from registers 593, in pieces of 8,192 features 579)
   constexpr bool FROM_REGS = MODE == 2 && PL == 1 && LONG;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));

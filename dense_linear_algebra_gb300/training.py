@@ -1,6 +1,6 @@
 """What training a classifier takes besides its layers, on CUDA tensors: layer norm (``layer_norm``), the embedding lookup
-(``embedding``) and softmax cross entropy on a linear layer (``cross_entropy``), each with its gradient, over the C entries of the same names. The package only marshals
-arguments: every step runs in the kernels of ``libfusedxtx.so``.
+(``embedding``) and softmax cross entropy on a linear layer (``cross_entropy``), each with its gradient, over the C entries of the
+same names. The package only marshals arguments: every step runs in the kernels of ``libfusedxtx.so``.
 """
 from __future__ import annotations
 

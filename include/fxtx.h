@@ -469,7 +469,7 @@ fxtx_status_t fxtx_layer_norm_grad(fxtx_type_t type, int64_t m, int64_t n, const
  * (zeros where there is none; the sum is fp32, in the order of i, in pieces). ids: m integers of id_bits (32 or 64)
  * bits. An id outside 0 .. count - 1 stands for no row: zeros come out and nothing goes back (-1 for padding). Every
  * entry of OUT and DE is written. Outputs must not overlap anything else. Workspace is taken for the gradient: about
- * 24 bytes an id, and an eighth of m x n fp32 values.
+ * 18 bytes an id, and a sixteenth of m x n fp32 values.
  */
 fxtx_status_t fxtx_embedding(fxtx_type_t type, int64_t m, int64_t n, int64_t count, const void* ids, int id_bits, const void* E,
                              int64_t lde, double scale, void* OUT, int64_t ldo, void* stream);
@@ -495,8 +495,9 @@ fxtx_status_t fxtx_embedding_grad(fxtx_type_t type, int64_t m, int64_t n, int64_
  * features or classes held in pieces of up to 512 MB), float16 multiplied by a power of two that brings the largest
  * |gain G_i| of a row with a label to 2^14 .. 2^15: what is below 2^-39 of that is lost. DB is summed from the unrounded
  * values. m = 0 gives DW = 0 and DB = 0. DW takes every row of X: what is not finite there reaches it, although the row is
- * left out; G and LSE of such a row have no say. Outputs must not overlap anything else. Precision and errors are those of fxtx_linear, but for 16-bit logits, whose sums leave the tensor
- * cores every 1,024 features (z is short by up to 6e-6 of the sum of its terms).
+ * left out; G and LSE of such a row have no say. Outputs must not overlap anything else. Precision and errors are those of
+ * fxtx_linear, but for 16-bit logits, whose sums leave the tensor cores every 1,024 features in both calls (z is short by up to
+ * 6e-6 of the sum of its terms).
  */
 fxtx_status_t fxtx_cross_entropy(fxtx_type_t type, int64_t m, int64_t n, int64_t k, const void* X, int64_t ldx, const void* W,
                                  int64_t ldw, int w_trans, const void* b, const void* labels, int label_bits, float* LOSS, float* LSE,
