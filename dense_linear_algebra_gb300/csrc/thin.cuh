@@ -300,8 +300,9 @@ __device__ __forceinline__ void softmax_slope(const ThinArgs& a, const float* bi
     const int64_t label = r < a.m ? label_at(a.loss.labels, a.loss.labels64, r, a.k) : -1;
     const bool on = label >= 0;
     const float lse = on ? a.loss.lse_in[r] : 0.f;
-    float g = on ? a.loss.gain * up : 0.f;
+    float g = on ? a.loss.gain : 0.f;
     if (on && a.loss.g) g *= a.loss.g[r];
+    g *= up;  // (last: gain up alone may be beyond fp32)
     const int at = (int)label - 4 * KC * t;
 #pragma unroll
     for (int i = 0; i < 4 * KC; ++i) {

@@ -1,5 +1,7 @@
 """Layer norm, the embedding lookup, cross entropy and their gradients where one of them was wrong or took too much: long logits of
-terms of one sign, weights of rows that are left out, rows around a large mean, workspace, a classifier of no rows."""
+terms of one sign, weights of rows that are left out, rows around a large mean, workspace, a classifier of no rows, a gain beside the weights."""
+import math
+
 import pytest
 import torch
 
@@ -140,3 +142,26 @@ def test_every_number_of_few_classes(n, k):
     """Float32 rows of few features and classes, whose kernels hold the classes in pairs; one row too few for those kernels too."""
     for m in (5000 * k - 1, 8000 * k + 1):
         check(m, n, k, torch.float32, bias=k % 2 == 0, w_t=n % 2 == 0, need=(k % 3 != 0, True, True))
+
+
+@pytest.mark.parametrize("dtype,code", [(torch.float32, 0), (torch.bfloat16, 1), (torch.float16, 2)])
+@pytest.mark.parametrize("m,n,k", [(200, 40, 20), (3, 100, 300), (200, 100, 300), (70_000, 32, 10)])
+@pytest.mark.parametrize("gain", [1e-30, 2.0**120])
+def test_a_gain_beside_the_weights(m, n, k, gain, dtype, code):
+    """gain G is what counts, whatever the size of each: a power of two in one and its inverse in the other changes no bit."""
+    gain = 2.0 ** round(math.log2(gain))
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(m)
+    X = torch.randn(m, n, generator=gen, device="cuda").to(dtype)
+    P = (torch.randn(k, n, generator=gen, device="cuda") / n**0.5).to(dtype)
+    labels = torch.randint(-1, k, (m,), generator=gen, device="cuda")
+    g = torch.rand(m, generator=gen, device="cuda") + 0.5
+    _, lse = fx.cross_entropy(X, P.t(), labels)
+    want = fx.cross_entropy_grad(X, P.t(), labels, lse, g=g)
+    dX, dP, db = torch.empty_like(X), torch.empty_like(P), torch.empty(k, dtype=dtype, device="cuda")
+    weights = g / gain
+    rc = fx.fxtx_cross_entropy_grad(code, m, n, k, X.data_ptr(), n, P.data_ptr(), n, 1, None, labels.data_ptr(), 64, lse.data_ptr(),
+                                    weights.data_ptr(), gain, dX.data_ptr(), n, dP.data_ptr(), n, db.data_ptr(),
+                                    torch.cuda.current_stream().cuda_stream)
+    assert rc == fx.FXTX_OK
+    assert torch.equal(dX, want[0]) and torch.equal(dP.t(), want[1]) and torch.equal(db, want[2])
