@@ -44,7 +44,8 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
-// The exponential for layers of type T.
+// The exponential for layers of type T. Of 16 bits in two instructions: off by 2^-22 of itself and (the argument's rounding) 1.5 |x| 2^-24,
+// below the types' 2^-8 and 2^-11; a loss in fp32 of such a layer carries logits that are off by more.
 template <typename T>
 __device__ __forceinline__ float exp_of(float x) {
   if constexpr (sizeof(T) == 4) return expf(x);
